@@ -350,6 +350,220 @@ int w4a16_gemm_plan_tail(int64_t M, int64_t N, int64_t K, int *tail_rows, int *t
 int w4a16_gemm_ex_plan(int64_t M, int64_t N, int64_t K, int32_t group, int32_t zero_points,
                        int32_t alpha, int *path, int *splits, int *ctas, int *rows_per_cta);
 
+/* ------------------------------------------------------------------------
+ * Serving operators: the paged key-value cache between the quantized linear
+ * layers, the attention of a new token over it, the care of its pages, and
+ * the scores of sampled tokens.
+ *
+ * The conventions above hold, with these differences.  Tensors may be
+ * strided where a stride is an argument (in elements, or in bytes where the
+ * argument says so); the innermost dimension is always dense.  Integer
+ * tensors (int32) need 4-byte alignment only.  What an integer tensor holds
+ * is device data that the call cannot see: kernels check every page and row
+ * number against its range before they use it, and what each does with one
+ * that is outside is said below.
+ * ------------------------------------------------------------------------ */
+
+/* Element types. */
+enum { W4A16_F16 = 0, W4A16_BF16 = 1, W4A16_F32 = 2 };
+
+/*
+ * A cache: two pools of `pages` pages of `page_size` positions, and `batch`
+ * rows of page numbers.  Position p of row b lies in page
+ * tables[b * table_stride + p / page_size] at slot p % page_size; its head h
+ * starts at page * page_stride + slot * slot_stride + h * head_stride
+ * elements from the pool's start, head_dim elements long.  Both pools have
+ * the same strides, so token-major, head-major and interleaved pools are all
+ * of this form.
+ *   pages >= 1; page_size 1 .. 65536; kv_heads 1 .. 1024; head_dim 8 .. 256,
+ *   a multiple of 8; type W4A16_F16 or W4A16_BF16; the three strides
+ *   multiples of 8 elements and >= 0; batch 1 .. 65535; table_width 1 .. 2^24,
+ *   table_width * page_size < 2^31; pages < 2^31.
+ */
+typedef struct w4a16_cache_shape {
+    int64_t pages, page_size, kv_heads, head_dim, type;
+    int64_t page_stride, slot_stride, head_stride;
+    int64_t batch, table_width, table_stride;
+} w4a16_cache_shape;
+
+/*
+ * w4a16_paged_append -- new tokens' keys and values into their pages.
+ *   token t of row b (offsets[b] <= t < offsets[b + 1]; one token a row,
+ *   t = b, when offsets is NULL) goes to position starts[b] + t - offsets[b].
+ *
+ *   k, v       [tokens, kv_heads, head_dim]; strides in elements, multiples
+ *              of 8 (a slice of a wider product is such a tensor).
+ *   tables     [batch, table_width] int32; starts [batch]; offsets
+ *              [batch + 1], not descending, or NULL.
+ * A token whose position is negative or past table_width * page_size, or
+ * whose page number is outside [0, pages), and one that no row claims, is
+ * left out.
+ * Errors: NULL -> W4A16_ERR_NULL; a size or stride outside the ranges above,
+ * tokens < 0, or offsets NULL with tokens != batch -> W4A16_ERR_SHAPE; k, v
+ * or a pool not 16-byte aligned -> W4A16_ERR_ALIGN.
+ */
+int w4a16_paged_append(const void *k, const void *v, void *k_pool, void *v_pool,
+                       const int32_t *tables, const int32_t *starts, const int32_t *offsets,
+                       const w4a16_cache_shape *cache, int64_t tokens, int64_t k_token_stride,
+                       int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                       void *stream);
+
+/* The queries and outputs of w4a16_paged_attention: q_heads a multiple of
+ * kv_heads (at most 1024); strides in elements, multiples of 8. */
+typedef struct w4a16_query_shape {
+    int64_t q_heads;
+    int64_t q_row_stride, q_head_stride, out_row_stride, out_head_stride;
+    double scale;
+} w4a16_query_shape;
+
+/*
+ * w4a16_paged_attention -- one new token's attention over a paged cache:
+ *   out[b, h] = sum_p w[p] V[b, p, h / g],  w = softmax_p(scale * q[b, h] . K[b, p, h / g])
+ * over positions p < lengths[b], g = q_heads / kv_heads.  Scores, statistics
+ * and sums are held in FP32; out is rounded once.
+ *
+ *   q          [batch, q_heads, head_dim] of the cache's type.
+ *   lengths    [batch] int32; a length below 0 counts as 0, one past
+ *              table_width * page_size as that.
+ *   out        [batch, q_heads, head_dim], written.  A row of length 0 gets
+ *              zeros.
+ *   lse        NULL, or [batch, q_heads] float, written: the natural
+ *              logarithm of sum_p exp(scale * q . K), -infinity for a row of
+ *              length 0.
+ *   workspace  w4a16_paged_attention_workspace(cache, q_heads) bytes, 16-byte
+ *              aligned, of any content; not read after the call's work is
+ *              done, and not to be shared by calls that may run at once.
+ * Positions whose page number is outside [0, pages) are left out, as if
+ * masked.  The result does not depend on how the work was split beyond the
+ * order of its FP32 sums; two calls on the same inputs give the same bits.
+ * Errors: NULL -> W4A16_ERR_NULL; sizes outside the ranges above ->
+ * W4A16_ERR_SHAPE; q, out, a pool or the workspace not 16-byte aligned ->
+ * W4A16_ERR_ALIGN.
+ */
+int w4a16_paged_attention(const void *q, const void *k_pool, const void *v_pool,
+                          const int32_t *tables, const int32_t *lengths, void *out, float *lse,
+                          void *workspace, const w4a16_cache_shape *cache,
+                          const w4a16_query_shape *query, void *stream);
+
+/* Bytes of workspace of w4a16_paged_attention on the current device (-1 on
+ * a bad shape or device). */
+int64_t w4a16_paged_attention_workspace(const w4a16_cache_shape *cache, int64_t q_heads);
+
+/*
+ * The books of a cache's pages: how many rows hold each page (`refs`, <= 0 is
+ * free), each row's page numbers (`tables`, -1 past its pages) and each row's
+ * positions (`lengths`).  Row r of length n holds ceil(n / page_size) pages.
+ *   pages 1 .. 2^31 - 1; rows 1 .. 2^24; width 1 .. 2^24, rows * width <
+ *   2^40; strides in elements.  Every call reads the `in` books and writes
+ *   the `out` ones whole; each `out` tensor is its `in` tensor (with the same
+ *   stride) or overlaps none.
+ */
+typedef struct w4a16_books_shape {
+    int64_t pages, rows, width, in_stride, out_stride, page_size;
+} w4a16_books_shape;
+
+/* The pages themselves: `planes` pools (keys and values of every layer),
+ * page p of plane l at l * plane_stride + p * page_stride bytes, page_bytes
+ * long, all three multiples of 16. */
+typedef struct w4a16_pool_shape {
+    int64_t planes, plane_stride, page_stride, page_bytes;
+} w4a16_pool_shape;
+
+/* Bytes of workspace of w4a16_pages_extend, _fork and _compact for `count`
+ * requests (0 for compact); 16-byte aligned, of any content, as the
+ * attention's. */
+int64_t w4a16_pages_workspace(const w4a16_books_shape *books, int64_t count);
+
+/*
+ * w4a16_pages_free -- gives back every page of the `count` rows listed: one
+ * holder fewer for each, the row's page numbers -1 and its length 0.  A row
+ * listed twice is given back once; one outside [0, rows) is passed over.
+ */
+int w4a16_pages_free(const int32_t *refs_in, const int32_t *tables_in, const int32_t *lengths_in,
+                     const int32_t *listed, int64_t count, int32_t *refs_out, int32_t *tables_out,
+                     int32_t *lengths_out, const w4a16_books_shape *books, void *stream);
+
+/*
+ * w4a16_pages_extend -- makes row listed[i] longer by counts[i] positions,
+ * giving it the free pages it then needs: the lowest numbers first, in the
+ * order of the list.  done[i] is 1, or 0 with the row unchanged: the row is
+ * outside [0, rows) or was listed before, the count is negative, the row
+ * would pass width * page_size, or it or one listed before it would need
+ * more free pages than there are.
+ */
+int w4a16_pages_extend(const int32_t *refs_in, const int32_t *tables_in,
+                       const int32_t *lengths_in, const int32_t *listed, const int32_t *counts,
+                       int64_t count, int32_t *refs_out, int32_t *tables_out,
+                       int32_t *lengths_out, int32_t *done, void *workspace,
+                       const w4a16_books_shape *books, void *stream);
+
+/*
+ * w4a16_pages_fork -- makes the empty row children[i] a copy of row
+ * parents[i]: full pages are shared (one holder more), a last page that is
+ * partly filled is copied in every plane to the lowest free page, in the
+ * order of the list.  done[i] is 1, or 0 with the child unchanged: a row is
+ * outside [0, rows), the child's length is not 0 or it was listed before, the
+ * parent's last page is none, or this child or one listed before it would
+ * need more free pages than there are.
+ */
+int w4a16_pages_fork(void *pool, const int32_t *refs_in, const int32_t *tables_in,
+                     const int32_t *lengths_in, const int32_t *parents, const int32_t *children,
+                     int64_t count, int32_t *refs_out, int32_t *tables_out, int32_t *lengths_out,
+                     int32_t *done, void *workspace, const w4a16_books_shape *books,
+                     const w4a16_pool_shape *shape, void *stream);
+
+/*
+ * w4a16_pages_compact -- moves the pages that are held to the lowest
+ * numbers: with n held pages in all, those numbered n or above move, in
+ * ascending order, to the free ones below n, in ascending order.  Their
+ * numbers in the tables follow.  used[0] = n.  Pages left behind keep their
+ * old content.
+ */
+int w4a16_pages_compact(void *pool, const int32_t *refs_in, const int32_t *tables_in,
+                        int32_t *refs_out, int32_t *tables_out, int32_t *used, void *workspace,
+                        const w4a16_books_shape *books, const w4a16_pool_shape *shape,
+                        void *stream);
+
+/*
+ * w4a16_pages_copy -- page from[i] to page to[i] in every plane, for i <
+ * count.  A pair with a number outside [0, pages) is passed over.  No page
+ * may be the target of two pairs, or both a target and a source.
+ *
+ * Errors of the w4a16_pages_* calls: NULL -> W4A16_ERR_NULL; sizes outside
+ * the ranges above or count < 0 (count > 2^24) -> W4A16_ERR_SHAPE; pool or
+ * workspace not 16-byte aligned -> W4A16_ERR_ALIGN.
+ */
+int w4a16_pages_copy(void *pool, const int32_t *from, const int32_t *to, int64_t count,
+                     int64_t pages, const w4a16_pool_shape *shape, void *stream);
+
+/* Most alternatives w4a16_token_logprobs gives. */
+#define W4A16_MAX_TOP 32
+
+/*
+ * w4a16_token_logprobs -- the scores of given tokens under rows of logits:
+ *   lse = ln sum_j exp(x[j]),  logprob = x[token] - lse,
+ *   entropy = lse - sum_j p[j] x[j] with p[j] = exp(x[j] - lse) (p x = 0 where p = 0),
+ *   and the `top` largest x[j], of equal ones the lowest j first, with x[j] - lse.
+ * Statistics are held in FP32.
+ *
+ *   logits     [rows, vocabulary] of `type` (W4A16_F16, _BF16, _F32), rows
+ *              row_stride elements apart, aligned to their element only.
+ *   tokens     [rows], int64 (wide = 1) or int32 (wide = 0).  A token outside
+ *              [0, vocabulary) has the logprob NaN.
+ *   logprob, entropy  [rows] float; top_ids [rows, top] int32, top_logprobs
+ *              [rows, top] float (both may be NULL when top = 0).
+ *   rows       1 .. 2^24; vocabulary 1 .. 2^30; top 0 .. min(32, vocabulary).
+ * -infinity masks a logit.  A row with nothing but -infinity has lse =
+ * -infinity, every logprob -infinity and the entropy 0.  A row with a NaN or
+ * +infinity has NaN for every number; its ids count NaN as the largest.
+ * Errors: NULL -> W4A16_ERR_NULL; sizes or type outside the ranges above ->
+ * W4A16_ERR_SHAPE; logits not aligned to their element -> W4A16_ERR_ALIGN.
+ */
+int w4a16_token_logprobs(const void *logits, const void *tokens, float *logprob, float *entropy,
+                         int32_t *top_ids, float *top_logprobs, int64_t rows, int64_t vocabulary,
+                         int64_t row_stride, int32_t type, int32_t wide, int32_t top,
+                         void *stream);
+
 /*
  * w4a16_device_status -- synchronises the current device, returns in
  * *status the OR of the W4A16_ERR_* conditions recorded by kernels since

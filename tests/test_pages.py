@@ -1,0 +1,312 @@
+"""The books of a paged cache and its page copies against list definitions:
+whole numbers, equal in every place."""
+from __future__ import annotations
+
+import random
+
+import pytest
+import torch
+
+import paged_reference as ref
+import w4a16_weight_only_gemm_gb300 as w4
+
+pytestmark = pytest.mark.gpu
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def make(pages, rows, width, ps, used, seed=0):
+    """Books with `used` pages held, some by several rows, and the rest free."""
+    rng = random.Random(seed)
+    held = rng.sample(range(pages), used)
+    refs, tables, lengths, at = [0] * pages, [], [], 0
+    for r in range(rows):
+        n = rng.randint(0, width - 1) if rng.random() < 0.8 else 0
+        n = min(n, used - at)
+        row, at = held[at:at + n], at + n
+        if tables and rng.random() < 0.3:      # a prefix shared with an earlier row
+            other = rng.choice(tables)
+            row = ([p for p in other if p >= 0][:rng.randint(0, 3)] + row)[:width - 1]
+        for p in row:
+            refs[p] += 1
+        lengths.append(max(0, len(row) * ps - rng.randrange(ps)) if row else 0)
+        tables.append(row + [-1] * (width - len(row)))
+    return refs, tables, lengths
+
+
+def same(got, want):
+    for g, w in zip(got, want):
+        assert torch.equal(g.cpu(), torch.tensor(w, dtype=torch.int32).view(g.shape))
+
+
+def books(b, in_place, wide=False):
+    """Input tensors of the books (tables a slice of a wider tensor when asked) and `out`."""
+    refs, tables, lengths = (ints(t) for t in b)
+    if wide:
+        big = torch.full((tables.shape[0], tables.shape[1] + 5), -3, dtype=torch.int32,
+                         device="cuda")
+        big[:, :tables.shape[1]] = tables
+        tables = big[:, :tables.shape[1]]
+    ins = refs, tables, lengths
+    return ins, (ins if in_place else None)
+
+
+SIZES = [(1, 1, 2, 1), (40, 6, 5, 16), (511, 40, 12, 16), (512, 33, 20, 4), (2000, 64, 70, 16),
+         (16384, 100, 130, 1), (16385, 300, 33, 32), (140000, 50, 999, 16)]
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("pages, rows, width, ps", SIZES)
+def test_free(w4lib, pages, rows, width, ps, in_place):
+    b = make(pages, rows, width, ps, pages * 3 // 4, seed=pages)
+    rng = random.Random(1)
+    listed = [rng.randrange(rows) for _ in range(rows // 2 + 1)] + [-1, rows, 2 ** 31 - 1]
+    ins, out = books(b, in_place, wide=True)
+    got = w4.pages_free(*ins, ints(listed), out=out)
+    same(got, ref.free(*b, listed))
+    if not in_place:
+        same(ins, b)
+
+
+def test_free_of_foreign_numbers_and_nothing(w4lib):
+    b = [1, 2, 1], [[0, -1, 7, 2 ** 31 - 1], [1, -5, 1, -1]], [4, 2]
+    ins, _ = books(b, False)
+    same(w4.pages_free(*ins, ints([0, 1])), ref.free(*b, [0, 1]))
+    same(w4.pages_free(*ins, ints([])), b)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("pages, rows, width, ps", SIZES)
+def test_extend(w4lib, pages, rows, width, ps, in_place):
+    b = make(pages, rows, width, ps, pages // 2, seed=pages + 1)
+    rng = random.Random(2)
+    n = min(rows, 2500)
+    listed = rng.sample(range(rows), n) + [rng.randrange(rows), -1, rows, 0]
+    counts = [rng.choice((0, 1, 2, ps, 3 * ps, rng.randrange(width * ps + 2))) for _ in range(n)]
+    counts += [1, 1, 1, -4]
+    ins, out = books(b, in_place, wide=True)
+    got = w4.pages_extend(*ins, ints(listed), ints(counts), ps, out=out)
+    same(got, ref.extend(*b, listed, counts, ps))
+
+
+def test_extend_until_none_is_left(w4lib):
+    b = [0, 1, 0, 0], [[1, -1, -1], [-1] * 3, [-1] * 3], [3, 0, 0]
+    for listed, counts in (([1, 2, 0], [8, 5, 1]), ([2, 0, 1], [12, 1, 1]), ([0], [9]), ([], [])):
+        ins, _ = books(b, False)
+        got = w4.pages_extend(*ins, ints(listed), ints(counts), 4)
+        same(got, ref.extend(*b, listed, counts, 4))
+
+
+def test_extend_long_lists(w4lib):
+    """More requests than a block has threads."""
+    rows = 3000
+    b = [0] * 4000, [[-1] * 3 for _ in range(rows)], [0] * rows
+    listed = list(range(rows))
+    counts = [(i * 7) % 9 for i in listed]
+    ins, out = books(b, True)
+    same(w4.pages_extend(*ins, ints(listed), ints(counts), 4, out=out),
+         ref.extend(*b, listed, counts, 4))
+
+
+def fill(planes, pages, shape, dtype, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(planes, pages, *shape, generator=g, device="cuda").to(dtype)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("pages, rows, width, ps", SIZES)
+def test_fork(w4lib, pages, rows, width, ps, in_place):
+    b = make(pages, rows, width, ps, pages // 2, seed=pages + 2)
+    rng = random.Random(3)
+    empty = [r for r, n in enumerate(b[2]) if n == 0]
+    children = empty + empty[:2] + [0, rows - 1, -1, rows]
+    rng.shuffle(children)
+    parents = [rng.randrange(rows) for _ in children]
+    parents[0] = rows
+    pool = fill(2, pages, (8,), torch.float16)
+    want = pool.clone()
+    ins, out = books(b, in_place, wide=True)
+    got = w4.pages_fork(pool, *ins, ints(parents), ints(children), ps, out=out)
+    *books_want, copies = ref.fork(*b, parents, children, ps)
+    same(got, books_want)
+    for a, z in copies:
+        want[:, z] = want[:, a]
+    assert torch.equal(pool, want)
+
+
+def test_fork_exhausts_and_chains(w4lib):
+    """Too few pages for all; a child that is also listed as an (empty) parent."""
+    b = [1, 1, 0, 0], [[0, 1, -1]] + [[-1] * 3 for _ in range(5)], [6, 0, 0, 0, 0, 0]
+    for parents, children in (([0, 0, 0, 0], [1, 2, 3, 4]), ([0, 1, 2], [1, 2, 3]),
+                              ([5, 0], [1, 5]), ([0], [0]), ([], [])):
+        for in_place in (False, True):
+            pool = fill(3, 4, (4, 2, 8), torch.bfloat16, seed=4)
+            want = pool.clone()
+            ins, out = books(b, in_place)
+            got = w4.pages_fork(pool, *ins, ints(parents), ints(children), 4, out=out)
+            *books_want, copies = ref.fork(*b, parents, children, 4)
+            same(got, books_want)
+            for a, z in copies:
+                want[:, z] = want[:, a]
+            assert torch.equal(pool, want)
+
+
+def test_fork_whose_parent_lacks_its_last_page(w4lib):
+    b = [1, 0, 0], [[0, -1], [7, 0], [-1, -1], [-1, -1]], [6, 3, 0, 0]
+    pool = fill(1, 3, (8,), torch.float16)
+    before = pool.clone()
+    ins, _ = books(b, False)
+    got = w4.pages_fork(pool, *ins, ints([0, 1]), ints([2, 3]), 4)
+    same(got, ref.fork(*b, [0, 1], [2, 3], 4)[:4])
+    assert got[3].tolist() == [0, 0] and torch.equal(pool, before)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("used", [0.0, 0.3, 0.7, 1.0])
+@pytest.mark.parametrize("pages, rows, width, ps", SIZES)
+def test_compact(w4lib, pages, rows, width, ps, used, in_place):
+    b = make(pages, rows, width, ps, int(pages * used), seed=pages + 3)
+    pool = fill(3, pages, (8,), torch.float16)
+    want = pool.clone()
+    ins, out = books(b, in_place, wide=True)
+    got = w4.pages_compact(pool, *ins[:2], out=out[:2] if out else None)
+    *books_want, copies = ref.compact(*b[:2])
+    same(got, books_want)
+    for a, z in copies:
+        want[:, z] = want[:, a]
+    assert torch.equal(pool, want)
+
+
+def test_compact_passes_over_numbers_that_nothing_holds(w4lib):
+    b = [0, 1, 0, 0, 2, 1], [[4, 5, 3, -1], [4, 1, 9, -8]]
+    pool = fill(2, 6, (8,), torch.float16)
+    want = pool.clone()
+    got = w4.pages_compact(pool, ints(b[0]), ints(b[1]))
+    *books_want, copies = ref.compact(*b)
+    same(got, books_want)
+    for a, z in copies:
+        want[:, z] = want[:, a]
+    assert torch.equal(pool, want)
+
+
+@pytest.mark.parametrize("values", [8, 24, 1000, 16384, 40008])
+def test_page_sizes_of_a_copy(w4lib, values):
+    """Pages of 16 bytes to many pieces, in planes and pages with gaps between."""
+    wide = fill(5, 9, (values + 8,), torch.float16)
+    pool = wide[1:4, :, :values]
+    want = wide.clone()
+    sources, targets = [0, 3, -1, 5, 9, 2], [1, 8, 4, 6, 7, 12]
+    for a, z in ((0, 1), (3, 8), (5, 6)):
+        want[1:4, z, :values] = want[1:4, a, :values]
+    w4.pages_copy(pool, ints(sources), ints(targets))
+    torch.cuda.synchronize()
+    assert torch.equal(wide, want)
+    w4.pages_copy(pool, ints([]), ints([]))
+    assert torch.equal(wide, want)
+
+
+def test_copy_many_pages(w4lib):
+    pool = fill(7, 600, (2, 16, 40), torch.bfloat16)
+    want = pool.clone()
+    order = random.Random(5).sample(range(600), 600)
+    sources, targets = order[:300], order[300:]
+    want[:, targets] = want[:, sources]
+    w4.pages_copy(pool, ints(sources), ints(targets))
+    assert torch.equal(pool, want)
+
+
+def test_copy_past_32_bit_offsets(w4lib):
+    pool = torch.zeros(2, 1200, 1 << 20, dtype=torch.float16, device="cuda")  # 2.5 G values
+    pool[:, 1199, -5:] = 3.0
+    w4.pages_copy(pool, ints([1199]), ints([1]))
+    assert (pool[:, 1, -5:] == 3).all() and (pool[:, 1, :-5] == 0).all()
+
+
+def test_life_of_a_cache(w4lib):
+    """Random lives of rows through PagedCache, its books checked at every step."""
+    rng = random.Random(6)
+    ps, rows, pages, layers = 4, 12, 64, 2
+    cache = w4.PagedCache(layers, rows, pages, 2, 16, page_size=ps, max_length=60)
+    b = [0] * pages, [[-1] * 15 for _ in range(rows)], [0] * rows
+    content = [[] for _ in range(rows)]        # the value of each position of each row
+    stamp = 0
+    for step in range(120):
+        what = rng.choice(("extend", "extend", "fork", "free", "compact"))
+        if what == "extend":
+            listed = rng.sample(range(rows), rng.randint(1, rows))
+            counts = [rng.randint(0, 9) for _ in listed]
+            starts = [b[2][r] for r in listed]
+            done = cache.extend(ints(listed), ints(counts))
+            *b, want = ref.extend(*b, listed, counts, ps)
+            assert done.tolist() == want
+            counts = [c if d else 0 for c, d in zip(counts, want)]
+            new = [list(range(stamp + 1 + sum(counts[:i]), stamp + 1 + sum(counts[:i + 1])))
+                   for i in range(len(listed))]
+            stamp += sum(counts)
+            for r, x in zip(listed, new):
+                content[r] = content[r] + x
+            flat = torch.tensor([y % 2000 for x in new for y in x], device="cuda").half()
+            k = flat.view(-1, 1, 1).expand(-1, 2, 16).contiguous()
+            offsets = [sum(counts[:i]) for i in range(len(counts) + 1)]
+            for layer in range(layers):
+                cache.append(layer, k + layer, k - layer, ints(starts), ints(offsets),
+                             rows=ints(listed))
+        elif what == "fork":
+            children = rng.sample(range(rows), 4)
+            parents = [rng.randrange(rows) for _ in children]
+            done = cache.fork(ints(parents), ints(children))
+            old = [list(c) for c in content]
+            *b, want, _ = ref.fork(*b, parents, children, ps)
+            assert done.tolist() == want
+            for a, c, d in zip(parents, children, want):
+                if d:
+                    content[c] = old[a]
+        elif what == "free":
+            listed = rng.sample(range(rows), rng.randint(1, 4))
+            cache.free(ints(listed))
+            b = ref.free(*b, listed)
+            for r in listed:
+                content[r] = []
+        else:
+            used = cache.compact()
+            refs, tables, want, _ = ref.compact(b[0], b[1])
+            b = refs, tables, b[2]
+            assert used.item() == want
+        same((cache.refs, cache.tables, cache.lengths), b)
+        for r in range(rows):
+            assert b[2][r] == len(content[r])
+            for layer in range(layers):
+                pages_of = [p for p in b[1][r] if p >= 0]
+                got = cache.pool[2 * layer][pages_of].flatten(0, 1)[:b[2][r], 1, 3]
+                assert got.tolist() == [x % 2000 + layer for x in content[r]]
+
+
+def test_refusals(w4lib):
+    b = make(8, 4, 3, 4, 4)
+    (refs, tables, lengths), _ = books(b, False)
+    pool = fill(2, 8, (8,), torch.float16)
+    one = ints([1])
+    with pytest.raises(ValueError):
+        w4.pages_free(refs.long(), tables, lengths, one)
+    with pytest.raises(ValueError):
+        w4.pages_free(refs, tables, lengths[:2], one)
+    with pytest.raises(ValueError):
+        w4.pages_free(refs, tables, lengths, one.long())
+    with pytest.raises(ValueError):
+        w4.pages_free(refs, tables, lengths, one, out=(refs, tables))
+    with pytest.raises(ValueError):
+        w4.pages_extend(refs, tables, lengths, one, ints([1, 2]), 4)
+    with pytest.raises(w4._native.W4A16Error):
+        w4.pages_extend(refs, tables, lengths, one, one, 0)
+    with pytest.raises(ValueError):
+        w4.pages_fork(pool[:, :5], refs, tables, lengths, one, one, 4)
+    with pytest.raises(ValueError):
+        w4.pages_fork(pool.cpu(), refs, tables, lengths, one, one, 4)
+    with pytest.raises(ValueError):
+        w4.pages_compact(fill(2, 8, (4, 8), torch.float16).transpose(2, 3), refs, tables)
+    with pytest.raises(w4._native.W4A16Error):
+        w4.pages_compact(fill(2, 8, (7,), torch.float16), refs, tables)     # 14-byte pages
+    with pytest.raises(ValueError):
+        w4.pages_copy(pool, one, ints([1, 2]))

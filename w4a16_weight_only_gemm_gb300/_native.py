@@ -23,6 +23,7 @@ STATUS_NAMES = {
 
 # name -> (restype, argtypes); mirrors include/w4a16.h
 _P, _I64, _I32, _U64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_uint64
+_S = ctypes.c_char_p  # a shape struct, passed as its packed bytes
 SIGNATURES = {
     "w4a16_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "w4a16_version": (ctypes.c_int, []),
@@ -41,6 +42,16 @@ SIGNATURES = {
     "w4a16_gemm_plan_tail": (ctypes.c_int, [_I64, _I64, _I64] + [ctypes.POINTER(ctypes.c_int)] * 2),
     "w4a16_gemm_ex_plan": (ctypes.c_int, [_I64, _I64, _I64, ctypes.c_int32, ctypes.c_int32,
                                           ctypes.c_int32] + [ctypes.POINTER(ctypes.c_int)] * 4),
+    "w4a16_paged_append": (ctypes.c_int, [_P] * 7 + [_S] + [_I64] * 5 + [_P]),
+    "w4a16_paged_attention": (ctypes.c_int, [_P] * 8 + [_S] * 2 + [_P]),
+    "w4a16_paged_attention_workspace": (_I64, [_S, _I64]),
+    "w4a16_pages_workspace": (_I64, [_S, _I64]),
+    "w4a16_pages_free": (ctypes.c_int, [_P] * 4 + [_I64] + [_P] * 3 + [_S, _P]),
+    "w4a16_pages_extend": (ctypes.c_int, [_P] * 5 + [_I64] + [_P] * 5 + [_S, _P]),
+    "w4a16_pages_fork": (ctypes.c_int, [_P] * 6 + [_I64] + [_P] * 5 + [_S, _S, _P]),
+    "w4a16_pages_compact": (ctypes.c_int, [_P] * 7 + [_S, _S, _P]),
+    "w4a16_pages_copy": (ctypes.c_int, [_P] * 3 + [_I64] * 2 + [_S, _P]),
+    "w4a16_token_logprobs": (ctypes.c_int, [_P] * 6 + [_I64] * 3 + [_I32] * 3 + [_P]),
     "w4a16_device_status": (ctypes.c_int, [ctypes.POINTER(ctypes.c_int)]),
     "w4a16_set_wait_timeout_ns": (None, [_U64]),
     "w4a16_selftest_wait_timeout": (ctypes.c_int, [_U64, _P]),

@@ -58,6 +58,35 @@ bool good_nk(int64_t N, int64_t K) {
            K <= (int64_t)1 << 20 && N * K <= (int64_t)1 << 40;
 }
 
+// The serving operators' shapes, within the ranges the header gives.
+bool good_cache(const w4a16_cache_shape& c) {
+    const auto stride = [](int64_t s) { return s >= 0 && s % 8 == 0 && s <= (int64_t)1 << 40; };
+    return c.pages >= 1 && c.pages < (int64_t)1 << 31 && c.page_size >= 1 && c.page_size <= 65536 &&
+           c.kv_heads >= 1 && c.kv_heads <= 1024 && c.head_dim >= 8 && c.head_dim <= 256 &&
+           c.head_dim % 8 == 0 && (c.type == W4A16_F16 || c.type == W4A16_BF16) &&
+           stride(c.page_stride) && stride(c.slot_stride) && stride(c.head_stride) && c.batch >= 1 &&
+           c.batch <= 65535 && c.table_width >= 1 && c.table_width <= (int64_t)1 << 24 &&
+           c.table_width * c.page_size < (int64_t)1 << 31 && c.table_stride >= 0 &&
+           c.table_stride <= (int64_t)1 << 40;
+}
+
+bool good_books(const w4a16_books_shape& b) {
+    return b.pages >= 1 && b.pages < (int64_t)1 << 31 && b.rows >= 1 && b.rows <= (int64_t)1 << 24 &&
+           b.width >= 1 && b.width <= (int64_t)1 << 24 && b.rows * b.width <= (int64_t)1 << 40 &&
+           b.in_stride >= 0 && b.in_stride <= (int64_t)1 << 40 && b.out_stride >= b.width &&
+           b.out_stride <= (int64_t)1 << 40 && b.page_size >= 1 && b.page_size <= 65536 &&
+           b.width * b.page_size < (int64_t)1 << 31;
+}
+
+bool good_pool(const w4a16_pool_shape& p) {
+    const auto whole = [](int64_t s) { return s >= 0 && s % 16 == 0 && s <= (int64_t)1 << 42; };
+    return p.planes >= 1 && p.planes <= (int64_t)1 << 20 && whole(p.plane_stride) &&
+           whole(p.page_stride) && whole(p.page_bytes) && p.page_bytes >= 16 &&
+           p.page_bytes <= (int64_t)1 << 36;
+}
+
+bool good_count(int64_t count) { return count >= 0 && count <= (int64_t)1 << 24; }
+
 // Launchers report an unsupported configuration (no shared-memory layout
 // fits) as cudaErrorInvalidValue before launching anything.
 int from_cuda(cudaError_t e) {
@@ -322,6 +351,158 @@ int w4a16_gemm_ex_plan(int64_t M, int64_t N, int64_t K, int32_t group, int32_t z
     if (*splits == 0) return W4A16_ERR_CUDA;
     *rows_per_cta = 128;
     return W4A16_OK;
+}
+
+int w4a16_paged_append(const void* k, const void* v, void* k_pool, void* v_pool,
+                       const int32_t* tables, const int32_t* starts, const int32_t* offsets,
+                       const w4a16_cache_shape* cache, int64_t tokens, int64_t k_token_stride,
+                       int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                       void* stream) {
+    if (!cache) return W4A16_ERR_NULL;
+    if (!good_cache(*cache) || tokens < 0 || tokens > (int64_t)1 << 31 ||
+        (!offsets && tokens != cache->batch))
+        return W4A16_ERR_SHAPE;
+    for (int64_t s : {k_token_stride, k_head_stride, v_token_stride, v_head_stride})
+        if (s < 0 || s % 8 != 0 || s > (int64_t)1 << 40) return W4A16_ERR_SHAPE;
+    if (tokens == 0) return W4A16_OK;
+    if (!k || !v || !k_pool || !v_pool || !tables || !starts) return W4A16_ERR_NULL;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_pool) || !aligned16(v_pool))
+        return W4A16_ERR_ALIGN;
+    DeviceCtx ctx;
+    if (int rc = device_ctx(&ctx)) return rc;
+    return from_cuda(launch_paged_append(k, v, k_pool, v_pool, tables, starts, offsets, *cache,
+                                         tokens, k_token_stride, k_head_stride, v_token_stride,
+                                         v_head_stride, static_cast<cudaStream_t>(stream), ctx));
+}
+
+int64_t w4a16_paged_attention_workspace(const w4a16_cache_shape* cache, int64_t q_heads) {
+    if (!cache || !good_cache(*cache) || q_heads < 1 || q_heads > 1024 ||
+        q_heads % cache->kv_heads != 0)
+        return -1;
+    DeviceCtx ctx;
+    if (device_ctx(&ctx)) return -1;
+    return paged_attention_workspace(*cache, q_heads, ctx);
+}
+
+int w4a16_paged_attention(const void* q, const void* k_pool, const void* v_pool,
+                          const int32_t* tables, const int32_t* lengths, void* out, float* lse,
+                          void* workspace, const w4a16_cache_shape* cache,
+                          const w4a16_query_shape* query, void* stream) {
+    if (!q || !k_pool || !v_pool || !tables || !lengths || !out || !workspace || !cache || !query)
+        return W4A16_ERR_NULL;
+    if (!good_cache(*cache) || query->q_heads < 1 || query->q_heads > 1024 ||
+        query->q_heads % cache->kv_heads != 0 || !(query->scale == query->scale))
+        return W4A16_ERR_SHAPE;
+    for (int64_t s : {query->q_row_stride, query->q_head_stride, query->out_row_stride,
+                      query->out_head_stride})
+        if (s < 0 || s % 8 != 0 || s > (int64_t)1 << 40) return W4A16_ERR_SHAPE;
+    if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out) ||
+        !aligned16(workspace))
+        return W4A16_ERR_ALIGN;
+    DeviceCtx ctx;
+    if (int rc = device_ctx(&ctx)) return rc;
+    return from_cuda(launch_paged_attention(q, k_pool, v_pool, tables, lengths, out, lse, workspace,
+                                            *cache, *query, static_cast<cudaStream_t>(stream),
+                                            ctx));
+}
+
+int64_t w4a16_pages_workspace(const w4a16_books_shape* books, int64_t count) {
+    return books && good_books(*books) && good_count(count) ? pages_workspace(*books, count) : -1;
+}
+
+int w4a16_pages_free(const int32_t* refs_in, const int32_t* tables_in, const int32_t* lengths_in,
+                     const int32_t* listed, int64_t count, int32_t* refs_out, int32_t* tables_out,
+                     int32_t* lengths_out, const w4a16_books_shape* books, void* stream) {
+    if (!refs_in || !tables_in || !lengths_in || (!listed && count) || !refs_out || !tables_out ||
+        !lengths_out || !books)
+        return W4A16_ERR_NULL;
+    if (!good_books(*books) || !good_count(count)) return W4A16_ERR_SHAPE;
+    DeviceCtx ctx;
+    if (int rc = device_ctx(&ctx)) return rc;
+    return from_cuda(launch_pages_free(
+        {refs_in, tables_in, lengths_in, refs_out, tables_out, lengths_out, *books}, listed, count,
+        static_cast<cudaStream_t>(stream)));
+}
+
+int w4a16_pages_extend(const int32_t* refs_in, const int32_t* tables_in,
+                       const int32_t* lengths_in, const int32_t* listed, const int32_t* counts,
+                       int64_t count, int32_t* refs_out, int32_t* tables_out,
+                       int32_t* lengths_out, int32_t* done, void* workspace,
+                       const w4a16_books_shape* books, void* stream) {
+    if (!refs_in || !tables_in || !lengths_in || !refs_out || !tables_out || !lengths_out ||
+        !workspace || !books || (count && (!listed || !counts || !done)))
+        return W4A16_ERR_NULL;
+    if (!good_books(*books) || !good_count(count)) return W4A16_ERR_SHAPE;
+    if (!aligned16(workspace)) return W4A16_ERR_ALIGN;
+    DeviceCtx ctx;
+    if (int rc = device_ctx(&ctx)) return rc;
+    return from_cuda(launch_pages_extend(
+        {refs_in, tables_in, lengths_in, refs_out, tables_out, lengths_out, *books}, listed, counts,
+        count, done, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+int w4a16_pages_fork(void* pool, const int32_t* refs_in, const int32_t* tables_in,
+                     const int32_t* lengths_in, const int32_t* parents, const int32_t* children,
+                     int64_t count, int32_t* refs_out, int32_t* tables_out, int32_t* lengths_out,
+                     int32_t* done, void* workspace, const w4a16_books_shape* books,
+                     const w4a16_pool_shape* shape, void* stream) {
+    if (!pool || !refs_in || !tables_in || !lengths_in || !refs_out || !tables_out ||
+        !lengths_out || !workspace || !books || !shape ||
+        (count && (!parents || !children || !done)))
+        return W4A16_ERR_NULL;
+    if (!good_books(*books) || !good_pool(*shape) || !good_count(count)) return W4A16_ERR_SHAPE;
+    if (!aligned16(pool) || !aligned16(workspace)) return W4A16_ERR_ALIGN;
+    DeviceCtx ctx;
+    if (int rc = device_ctx(&ctx)) return rc;
+    return from_cuda(launch_pages_fork(
+        pool, {refs_in, tables_in, lengths_in, refs_out, tables_out, lengths_out, *books}, parents,
+        children, count, done, workspace, *shape, static_cast<cudaStream_t>(stream), ctx));
+}
+
+int w4a16_pages_compact(void* pool, const int32_t* refs_in, const int32_t* tables_in,
+                        int32_t* refs_out, int32_t* tables_out, int32_t* used, void* workspace,
+                        const w4a16_books_shape* books, const w4a16_pool_shape* shape,
+                        void* stream) {
+    if (!pool || !refs_in || !tables_in || !refs_out || !tables_out || !used || !workspace ||
+        !books || !shape)
+        return W4A16_ERR_NULL;
+    if (!good_books(*books) || !good_pool(*shape)) return W4A16_ERR_SHAPE;
+    if (!aligned16(pool) || !aligned16(workspace)) return W4A16_ERR_ALIGN;
+    DeviceCtx ctx;
+    if (int rc = device_ctx(&ctx)) return rc;
+    return from_cuda(launch_pages_compact(
+        pool, {refs_in, tables_in, nullptr, refs_out, tables_out, nullptr, *books}, used, workspace,
+        *shape, static_cast<cudaStream_t>(stream), ctx));
+}
+
+int w4a16_pages_copy(void* pool, const int32_t* from, const int32_t* to, int64_t count,
+                     int64_t pages, const w4a16_pool_shape* shape, void* stream) {
+    if (!pool || !shape || (count && (!from || !to))) return W4A16_ERR_NULL;
+    if (!good_pool(*shape) || !good_count(count) || pages < 1 || pages >= (int64_t)1 << 31)
+        return W4A16_ERR_SHAPE;
+    if (!aligned16(pool)) return W4A16_ERR_ALIGN;
+    DeviceCtx ctx;
+    if (int rc = device_ctx(&ctx)) return rc;
+    return from_cuda(launch_pages_copy(pool, from, to, count, pages, *shape,
+                                       static_cast<cudaStream_t>(stream), ctx));
+}
+
+int w4a16_token_logprobs(const void* logits, const void* tokens, float* logprob, float* entropy,
+                         int32_t* top_ids, float* top_logprobs, int64_t rows, int64_t vocabulary,
+                         int64_t row_stride, int32_t type, int32_t wide, int32_t top,
+                         void* stream) {
+    if (!logits || !tokens || !logprob || !entropy || (top && (!top_ids || !top_logprobs)))
+        return W4A16_ERR_NULL;
+    if (rows < 1 || rows > (int64_t)1 << 24 || vocabulary < 1 || vocabulary > (int64_t)1 << 30 ||
+        row_stride < 0 || row_stride > (int64_t)1 << 40 || top < 0 || top > W4A16_MAX_TOP ||
+        top > vocabulary || type < W4A16_F16 || type > W4A16_F32 || (wide != 0 && wide != 1))
+        return W4A16_ERR_SHAPE;
+    if (reinterpret_cast<uintptr_t>(logits) % (type == W4A16_F32 ? 4 : 2)) return W4A16_ERR_ALIGN;
+    DeviceCtx ctx;
+    if (int rc = device_ctx(&ctx)) return rc;
+    return from_cuda(launch_token_logprobs(logits, tokens, logprob, entropy, top_ids, top_logprobs,
+                                           rows, vocabulary, row_stride, type, wide, top,
+                                           static_cast<cudaStream_t>(stream), ctx));
 }
 
 int w4a16_device_status(int* status) {

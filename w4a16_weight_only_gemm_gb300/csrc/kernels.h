@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "../../include/w4a16.h"
+
 namespace w4a16 {
 
 // Per-device facts and the device status word, resolved once per device.
@@ -85,6 +87,45 @@ void gemm_tc_plan_info(int64_t M, int64_t N, int64_t K, const DeviceCtx& ctx, in
 cudaError_t launch_gemm_tc(const void* x, const void* repacked, const void* scales, void* y,
                            int64_t M, int64_t N, int64_t K, cudaStream_t stream,
                            const DeviceCtx& ctx);
+// The serving operators (arguments as in the C ABI, checked there).
+cudaError_t launch_paged_append(const void* k, const void* v, void* k_pool, void* v_pool,
+                                const int32_t* tables, const int32_t* starts,
+                                const int32_t* offsets, const w4a16_cache_shape& cache,
+                                int64_t tokens, int64_t k_token, int64_t k_head, int64_t v_token,
+                                int64_t v_head, cudaStream_t stream, const DeviceCtx& ctx);
+int64_t paged_attention_workspace(const w4a16_cache_shape& cache, int64_t q_heads,
+                                  const DeviceCtx& ctx);
+cudaError_t launch_paged_attention(const void* q, const void* k_pool, const void* v_pool,
+                                   const int32_t* tables, const int32_t* lengths, void* out,
+                                   float* lse, void* workspace, const w4a16_cache_shape& cache,
+                                   const w4a16_query_shape& query, cudaStream_t stream,
+                                   const DeviceCtx& ctx);
+// The books that a page call reads and writes.
+struct PageBooks {
+    const int32_t *refs_in, *tables_in, *lengths_in;
+    int32_t *refs_out, *tables_out, *lengths_out;
+    w4a16_books_shape shape;
+};
+int64_t pages_workspace(const w4a16_books_shape& books, int64_t count);
+cudaError_t launch_pages_free(const PageBooks& books, const int32_t* listed, int64_t count,
+                              cudaStream_t stream);
+cudaError_t launch_pages_extend(const PageBooks& books, const int32_t* listed,
+                                const int32_t* counts, int64_t count, int32_t* done,
+                                void* workspace, cudaStream_t stream);
+cudaError_t launch_pages_fork(void* pool, const PageBooks& books, const int32_t* parents,
+                              const int32_t* children, int64_t count, int32_t* done,
+                              void* workspace, const w4a16_pool_shape& shape, cudaStream_t stream,
+                              const DeviceCtx& ctx);
+cudaError_t launch_pages_compact(void* pool, const PageBooks& books, int32_t* used,
+                                 void* workspace, const w4a16_pool_shape& shape,
+                                 cudaStream_t stream, const DeviceCtx& ctx);
+cudaError_t launch_pages_copy(void* pool, const int32_t* from, const int32_t* to, int64_t count,
+                              int64_t pages, const w4a16_pool_shape& shape, cudaStream_t stream,
+                              const DeviceCtx& ctx);
+cudaError_t launch_token_logprobs(const void* logits, const void* tokens, float* logprob,
+                                  float* entropy, int32_t* top_ids, float* top_logprobs,
+                                  int64_t rows, int64_t vocabulary, int64_t row_stride, int type,
+                                  int wide, int top, cudaStream_t stream, const DeviceCtx& ctx);
 cudaError_t launch_selftest_wait(uint64_t timeout_ns, cudaStream_t stream, const DeviceCtx& ctx);
 
 }  // namespace w4a16

@@ -1,0 +1,546 @@
+// pages.cu -- the books of a paged cache: freeing, extending, forking and
+// compacting rows, and the page copies these need.
+//
+// The books are small (a few int32 per page and per row) and every decision
+// in them is a prefix sum: the k-th free page in ascending order, the pages
+// wanted before request i.  One thread-block cluster does them: its barrier is
+// cheaper than a second launch, and its shared memory carries the sums.  What
+// moves whole pages runs over all SMs in a second launch that reads the list
+// of copies from the workspace, so nothing waits for the host.
+#include "common.cuh"
+#include "kernels.h"
+
+namespace w4a16 {
+namespace {
+
+constexpr int kBookThreads = 1024;
+constexpr int kBookWarps = kBookThreads / 32;
+constexpr int kPagesPerLane = 16;                          // pages a lane looks at per sweep
+constexpr int kPagesPerWarp = 32 * kPagesPerLane;          // consecutive ones of a warp
+
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t n;
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+    return n;
+}
+
+__device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// Every thread of the cluster; orders global and shared memory within it.
+__device__ __forceinline__ void books_sync(uint32_t ctas) {
+    if (ctas == 1)
+        __syncthreads();
+    else
+        cluster_sync_all();
+}
+
+struct ScanShared {
+    int warp_total[kBookWarps];
+    int cta_total;
+};
+
+// Sum of `count` (the same in all lanes of a warp) over the warps before this
+// one, in the order of (CTA rank, warp); *total: over all warps of the cluster.
+__device__ int scan_warps(int count, ScanShared& sh, uint32_t rank, uint32_t ctas, int* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (lane == 0) sh.warp_total[warp] = count;
+    __syncthreads();
+    int v = sh.warp_total[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int o = __shfl_up_sync(~0u, v, d);
+        if (lane >= d) v += o;
+    }
+    int before = __shfl_sync(~0u, v, warp) - count;
+    int sum = __shfl_sync(~0u, v, 31);
+    if (ctas > 1) {
+        if (threadIdx.x == 0) sh.cta_total = sum;
+        cluster_sync_all();
+        int t = lane < (int)ctas ? ld_cluster_s32(map_to_cta(smem_u32(&sh.cta_total), lane)) : 0;
+        int lower = lane < (int)rank ? t : 0;
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) {
+            t += __shfl_xor_sync(~0u, t, d);
+            lower += __shfl_xor_sync(~0u, lower, d);
+        }
+        before += lower;
+        sum = t;
+    }
+    books_sync(ctas);  // the totals may be overwritten by the next scan
+    *total = sum;
+    return before;
+}
+
+// Calls visit(page, ordinal, is_member) for every page in [0, pages), ordinal
+// being the number of members (pages with in(refs[page])) before it; returns
+// the number of members.  Called by all threads of the cluster.
+template <typename In, typename Visit>
+__device__ int sweep_pages(const int32_t* refs, int64_t pages, ScanShared& sh, uint32_t rank,
+                           uint32_t ctas, In in, Visit visit) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t sweep = (int64_t)ctas * kBookWarps * kPagesPerWarp;
+    int carry = 0;
+    for (int64_t base = 0; base < pages; base += sweep) {
+        const int64_t first = base + ((int64_t)rank * kBookWarps + warp) * kPagesPerWarp;
+        uint32_t mask[kPagesPerLane];
+        int count = 0;
+#pragma unroll
+        for (int k = 0; k < kPagesPerLane; ++k) {
+            const int64_t p = first + 32 * k + lane;
+            mask[k] = __ballot_sync(~0u, p < pages && in(refs[p < pages ? p : 0]));
+            count += __popc(mask[k]);
+        }
+        int total;
+        int at = carry + scan_warps(count, sh, rank, ctas, &total);
+        carry += total;
+#pragma unroll
+        for (int k = 0; k < kPagesPerLane; ++k) {
+            const int64_t p = first + 32 * k + lane;
+            const int mine = at + __popc(mask[k] & ((1u << lane) - 1));
+            if (p < pages) visit(p, mine, (mask[k] >> lane) & 1u);
+            at += __popc(mask[k]);
+        }
+    }
+    return carry;
+}
+
+struct Books {
+    const int32_t *refs_in, *tables_in, *lengths_in;
+    int32_t *refs_out, *tables_out, *lengths_out;
+    int64_t pages, rows, width, in_stride, out_stride, page_size;
+};
+
+// The `in` books into the `out` ones where these are other tensors.
+__device__ void copy_books(const Books& b, int64_t thread, int64_t threads) {
+    if (b.refs_in != b.refs_out)
+        for (int64_t p = thread; p < b.pages; p += threads) b.refs_out[p] = b.refs_in[p];
+    if (b.lengths_in != b.lengths_out)
+        for (int64_t r = thread; r < b.rows; r += threads) b.lengths_out[r] = b.lengths_in[r];
+    if (b.tables_in != b.tables_out)
+        for (int64_t r = thread / 32; r < b.rows; r += threads / 32)
+            for (int64_t j = thread % 32; j < b.width; j += 32)
+                b.tables_out[r * b.out_stride + j] = b.tables_in[r * b.in_stride + j];
+}
+
+__global__ void __launch_bounds__(kBookThreads) free_kernel(Books b, const int32_t* listed,
+                                                            int64_t count) {
+    const uint32_t ctas = cluster_size();
+    const int64_t threads = (int64_t)ctas * kBookThreads;
+    const int64_t thread = (int64_t)cluster_cta_rank() * kBookThreads + threadIdx.x;
+    copy_books(b, thread, threads);
+    books_sync(ctas);
+    for (int64_t i = thread / 32; i < count; i += threads / 32) {
+        const int64_t r = listed[i];
+        if (r < 0 || r >= b.rows) continue;
+        int32_t* row = b.tables_out + r * b.out_stride;
+        for (int64_t j = thread % 32; j < b.width; j += 32) {
+            if (row[j] == -1) continue;
+            // the exchange gives each page back once, however often its row is listed
+            const int32_t p = atomicExch(&row[j], -1);
+            if (p >= 0 && p < b.pages) atomicSub(&b.refs_out[p], 1);
+        }
+        if (thread % 32 == 0) b.lengths_out[r] = 0;
+    }
+}
+
+// Workspace of extend, fork and compact: one int32 array after another.
+struct Space {
+    int32_t* claim;  // [rows]    first request that names the row
+    int32_t* order;  // [count]   first of the request's pages in `free`, -1: refused
+    int32_t* from;   // [count]   fork: page to copy, -1: none
+    int32_t* to;     // [count]
+    int32_t* length; // [count]   fork: the child's length
+    int32_t* free;   // [pages]   free pages, ascending; compact: holes
+    int32_t* high;   // [pages]   compact: held pages from the top
+    int32_t* place;  // [pages]   compact: place of a page in `high`
+    int32_t* copies; // [1]       page copies listed
+};
+
+Space split_space(void* workspace, int64_t rows, int64_t pages, int64_t count) {
+    Space s;
+    int32_t* w = static_cast<int32_t*>(workspace);
+    s.copies = w, w += 4;
+    s.claim = w, w += rows;
+    s.order = w, w += count;
+    s.from = w, w += count;
+    s.to = w, w += count;
+    s.length = w, w += count;
+    s.free = w, w += pages;
+    s.high = w, w += pages;
+    s.place = w;
+    return s;
+}
+
+// Gives every in-range row of the list its first request's number.
+__device__ void claim_rows(const Space& s, const int32_t* listed, int64_t count, int64_t rows,
+                           uint32_t ctas, int64_t thread, int64_t threads) {
+    for (int64_t r = thread; r < rows; r += threads) s.claim[r] = 0x7FFFFFFF;
+    books_sync(ctas);
+    for (int64_t i = thread; i < count; i += threads)
+        if (listed[i] >= 0 && listed[i] < rows) atomicMin(&s.claim[listed[i]], (int)i);
+}
+
+// One CTA: runs want(i) -> pages wanted (-1: refused) over the list in order and
+// calls grant(i, first, wanted): first of the pages in the free list, or -1.
+template <typename Want, typename Grant>
+__device__ void serve_in_order(int64_t count, int64_t n_free, Want want, Grant grant) {
+    __shared__ int64_t warp_total[kBookWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t carry = 0;
+    for (int64_t base = 0; base < count; base += kBookThreads) {
+        const int64_t i = base + threadIdx.x;
+        const int64_t w = i < count ? want(i) : -1;
+        int64_t v = w > 0 ? w : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int64_t o = __shfl_up_sync(~0u, v, d);
+            if (lane >= d) v += o;
+        }
+        if (lane == 31) warp_total[warp] = v;
+        __syncthreads();
+        int64_t t = warp_total[lane];
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int64_t o = __shfl_up_sync(~0u, t, d);
+            if (lane >= d) t += o;
+        }
+        const int64_t own = __shfl_sync(~0u, t, warp) - __shfl_sync(~0u, v, 31);
+        const int64_t upto = carry + own + v;
+        if (i < count) grant(i, w >= 0 && upto <= n_free ? upto - w : -1, w);
+        carry += __shfl_sync(~0u, t, 31);
+        __syncthreads();
+    }
+}
+
+__device__ __forceinline__ int64_t pages_of(int64_t length, int64_t page_size) {
+    return (length + page_size - 1) / page_size;
+}
+
+__global__ void __launch_bounds__(kBookThreads)
+    extend_kernel(Books b, const int32_t* listed, const int32_t* counts, int64_t count,
+                  int32_t* done, Space s) {
+    __shared__ ScanShared sh;
+    const uint32_t ctas = cluster_size(), rank = cluster_cta_rank();
+    const int64_t threads = (int64_t)ctas * kBookThreads;
+    const int64_t thread = (int64_t)rank * kBookThreads + threadIdx.x;
+    const int64_t n_free = sweep_pages(
+        b.refs_in, b.pages, sh, rank, ctas, [](int32_t r) { return r <= 0; },
+        [&](int64_t p, int k, bool member) {
+            if (member) s.free[k] = (int32_t)p;
+        });
+    copy_books(b, thread, threads);
+    claim_rows(s, listed, count, b.rows, ctas, thread, threads);
+    books_sync(ctas);
+    if (rank == 0)
+        serve_in_order(
+            count, n_free,
+            [&](int64_t i) -> int64_t {
+                const int64_t r = listed[i], more = counts[i];
+                if (r < 0 || r >= b.rows || s.claim[r] != i || more < 0) return -1;
+                const int64_t n = max(b.lengths_out[r], 0);
+                if (n + more > b.width * b.page_size) return -1;
+                return pages_of(n + more, b.page_size) - pages_of(n, b.page_size);
+            },
+            [&](int64_t i, int64_t first, int64_t) {
+                s.order[i] = (int32_t)first;
+                done[i] = first >= 0;
+                if (first >= 0)
+                    b.lengths_out[listed[i]] = max(b.lengths_out[listed[i]], 0) + counts[i];
+            });
+    books_sync(ctas);
+    for (int64_t i = thread / 32; i < count; i += threads / 32) {
+        const int64_t first = s.order[i];
+        if (first < 0) continue;
+        const int64_t r = listed[i], n = b.lengths_out[r];
+        const int64_t had = pages_of(n - counts[i], b.page_size), has = pages_of(n, b.page_size);
+        for (int64_t j = had + thread % 32; j < has; j += 32) {
+            const int32_t p = s.free[first + j - had];
+            b.tables_out[r * b.out_stride + j] = p;
+            b.refs_out[p] = 1;
+        }
+    }
+}
+
+// What forking decides; the tables and the pages follow in fork_apply_kernel.
+__global__ void __launch_bounds__(kBookThreads)
+    fork_plan_kernel(Books b, const int32_t* parents, const int32_t* children, int64_t count,
+                     int32_t* done, Space s) {
+    __shared__ ScanShared sh;
+    const uint32_t ctas = cluster_size(), rank = cluster_cta_rank();
+    const int64_t threads = (int64_t)ctas * kBookThreads;
+    const int64_t thread = (int64_t)rank * kBookThreads + threadIdx.x;
+    const int64_t n_free = sweep_pages(
+        b.refs_in, b.pages, sh, rank, ctas, [](int32_t r) { return r <= 0; },
+        [&](int64_t p, int k, bool member) {
+            if (member && k < count) s.free[k] = (int32_t)p;  // one page a child at most
+            if (b.refs_in != b.refs_out) b.refs_out[p] = b.refs_in[p];
+        });
+    claim_rows(s, children, count, b.rows, ctas, thread, threads);
+    books_sync(ctas);
+    if (rank == 0)
+        serve_in_order(
+            count, n_free,
+            [&](int64_t i) -> int64_t {
+                const int64_t from = parents[i], to = children[i];
+                s.from[i] = s.to[i] = -1;
+                if (from < 0 || from >= b.rows || to < 0 || to >= b.rows) return -1;
+                if (s.claim[to] != i || b.lengths_in[to] != 0) return -1;
+                const int64_t n = min((int64_t)max(b.lengths_in[from], 0), b.width * b.page_size);
+                s.length[i] = (int32_t)n;
+                if (n % b.page_size == 0) return 0;
+                const int32_t last = b.tables_in[from * b.in_stride + n / b.page_size];
+                if (last < 0 || last >= b.pages) return -1;
+                s.from[i] = last;
+                return 1;
+            },
+            [&](int64_t i, int64_t first, int64_t wanted) {
+                s.order[i] = (int32_t)first;
+                done[i] = first >= 0;
+                if (first >= 0 && wanted > 0) {
+                    s.to[i] = s.free[first];
+                    b.refs_out[s.free[first]] = 1;
+                }
+            });
+    if (rank == 0 && threadIdx.x == 0) *s.copies = (int32_t)count;
+}
+
+// Copies the listed pages, thread blocks taking 16 KB pieces in turn.
+constexpr int kCopyThreads = 256;
+constexpr int kCopyUnroll = 4;
+constexpr int64_t kPiece = (int64_t)kCopyThreads * kCopyUnroll * 16;
+
+struct Pool {
+    char* base;
+    int64_t planes, plane_stride, page_stride, page_bytes;
+};
+
+template <typename From, typename To>
+__device__ void copy_pages(const Pool& pool, int64_t copies, int64_t pages, From from, To to) {
+    const int64_t pieces = (pool.page_bytes + kPiece - 1) / kPiece;
+    const int64_t units = copies * pool.planes * pieces;
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const int64_t piece = u % pieces, plane = u / pieces % pool.planes;
+        const int64_t i = u / pieces / pool.planes;
+        const int64_t src = from(i), dst = to(i);
+        if (src < 0 || src >= pages || dst < 0 || dst >= pages) continue;
+        const char* a = pool.base + plane * pool.plane_stride + src * pool.page_stride;
+        char* z = pool.base + plane * pool.plane_stride + dst * pool.page_stride;
+        uint4 v[kCopyUnroll];
+#pragma unroll
+        for (int k = 0; k < kCopyUnroll; ++k) {
+            const int64_t at = piece * kPiece + (k * kCopyThreads + threadIdx.x) * 16;
+            if (at < pool.page_bytes) v[k] = *reinterpret_cast<const uint4*>(a + at);
+        }
+#pragma unroll
+        for (int k = 0; k < kCopyUnroll; ++k) {
+            const int64_t at = piece * kPiece + (k * kCopyThreads + threadIdx.x) * 16;
+            if (at < pool.page_bytes) *reinterpret_cast<uint4*>(z + at) = v[k];
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kCopyThreads)
+    fork_apply_kernel(Books b, const int32_t* parents, const int32_t* children, int64_t count,
+                      Space s, Pool pool) {
+    grid_dependency_wait();
+    const int64_t thread = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x;
+    const int64_t threads = (int64_t)gridDim.x * kCopyThreads;
+    const int lane = threadIdx.x & 31;
+    for (int64_t r = thread / 32; r < b.rows; r += threads / 32) {
+        const int32_t i = s.claim[r];
+        const bool forked = i < count && s.order[i] >= 0;
+        const int64_t from = forked ? parents[i] : r;
+        if (!forked && b.tables_in == b.tables_out && b.lengths_in == b.lengths_out) continue;
+        const int32_t* in = b.tables_in + from * b.in_stride;
+        int32_t* out = b.tables_out + r * b.out_stride;
+        if (!forked) {
+            if (in != out)
+                for (int64_t j = lane; j < b.width; j += 32) out[j] = in[j];
+            if (lane == 0) b.lengths_out[r] = b.lengths_in[r];
+            continue;
+        }
+        // not from the books: where `out` is `in`, the parent may be a child written just now
+        // (it was empty then, so none of its page numbers are read here)
+        const int64_t n = s.length[i];
+        const int64_t full = n / b.page_size;
+        const int32_t last = s.to[i];
+        for (int64_t j = lane; j < b.width; j += 32) {
+            int32_t p = -1;
+            if (j < full) {
+                p = in[j];
+                if (p >= 0 && p < b.pages) atomicAdd(&b.refs_out[p], 1);
+            } else if (j == full) {
+                p = last;
+            }
+            out[j] = p;
+        }
+        if (lane == 0) b.lengths_out[r] = (int32_t)n;
+    }
+    copy_pages(pool, count, b.pages, [&](int64_t i) { return s.from[i]; },
+               [&](int64_t i) { return s.to[i]; });
+}
+
+// The holes below the number of held pages, ascending, and the held pages from the top.
+__global__ void __launch_bounds__(kBookThreads)
+    compact_plan_kernel(Books b, int32_t* used, Space s) {
+    __shared__ ScanShared sh;
+    const uint32_t ctas = cluster_size(), rank = cluster_cta_rank();
+    const auto held = [](int32_t r) { return r > 0; };
+    int n = 0, unused;
+    {
+        const int64_t threads = (int64_t)ctas * kBookThreads;
+        for (int64_t p = (int64_t)rank * kBookThreads + threadIdx.x; p < b.pages; p += threads)
+            n += held(b.refs_in[p]);
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) n += __shfl_xor_sync(~0u, n, d);
+        (void)scan_warps(n, sh, rank, ctas, &unused);
+        n = unused;
+    }
+    // page p is the k-th held one: the k before it leave p - k holes below it, n - 1 - k come after
+    sweep_pages(b.refs_in, b.pages, sh, rank, ctas, held, [&](int64_t p, int k, bool member) {
+        if (p < n && !member) s.free[p - k] = (int32_t)p;
+        if (p >= n && member) {
+            s.high[n - 1 - k] = (int32_t)p;
+            s.place[p] = n - 1 - k;
+        }
+        if (p == n - 1) *s.copies = (int32_t)(p + 1 - k - (member ? 1 : 0));
+    });
+    if (rank == 0 && threadIdx.x == 0) {
+        used[0] = n;
+        if (n == 0) *s.copies = 0;
+    }
+}
+
+__global__ void __launch_bounds__(kCopyThreads)
+    compact_apply_kernel(Books b, const int32_t* used, Space s, Pool pool) {
+    grid_dependency_wait();
+    const int64_t thread = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x;
+    const int64_t threads = (int64_t)gridDim.x * kCopyThreads;
+    const int64_t copies = *s.copies, n = used[0];
+    // a pair's two counts belong to one thread, so `out` may be `in`
+    for (int64_t i = thread; i < copies; i += threads) {
+        const int32_t src = s.high[copies - 1 - i], dst = s.free[i];
+        const int32_t held = b.refs_in[src];
+        b.refs_out[dst] = held;
+        b.refs_out[src] = 0;
+    }
+    if (b.refs_in != b.refs_out)
+        for (int64_t p = thread; p < b.pages; p += threads)
+            if ((b.refs_in[p] > 0) == (p < n)) b.refs_out[p] = b.refs_in[p];
+    for (int64_t r = thread / 32; r < b.rows; r += threads / 32)
+        for (int64_t j = thread % 32; j < b.width; j += 32) {
+            int32_t p = b.tables_in[r * b.in_stride + j];
+            // a number n or above that no count holds is left as it is
+            if (p >= n && p < b.pages) {
+                const int32_t k = s.place[p];
+                if (k >= 0 && k < copies && s.high[k] == p) p = s.free[copies - 1 - k];
+            }
+            b.tables_out[r * b.out_stride + j] = p;
+        }
+    copy_pages(pool, copies, b.pages, [&](int64_t i) { return s.high[copies - 1 - i]; },
+               [&](int64_t i) { return s.free[i]; });
+}
+
+__global__ void __launch_bounds__(kCopyThreads)
+    copy_kernel(Pool pool, const int32_t* from, const int32_t* to, int64_t count, int64_t pages) {
+    copy_pages(pool, count, pages, [&](int64_t i) { return from[i]; },
+               [&](int64_t i) { return to[i]; });
+}
+
+// The cluster of a books kernel: one CTA up to a sweep of pages, else eight.
+template <typename... P, typename... A>
+cudaError_t launch_books(void (*kernel)(P...), int64_t pages, cudaStream_t stream, A... args) {
+    const unsigned ctas = pages <= kBookWarps * kPagesPerWarp ? 1 : 8;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kBookThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_apply(void (*kernel)(P...), unsigned ctas, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kCopyThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
+Books books_of(const PageBooks& b) {
+    return {b.refs_in,     b.tables_in,  b.lengths_in, b.refs_out,        b.tables_out,
+            b.lengths_out, b.shape.pages, b.shape.rows, b.shape.width,     b.shape.in_stride,
+            b.shape.out_stride, b.shape.page_size};
+}
+
+Pool pool_of(void* pool, const w4a16_pool_shape& s) {
+    return {static_cast<char*>(pool), s.planes, s.plane_stride, s.page_stride, s.page_bytes};
+}
+
+unsigned copy_ctas(const DeviceCtx& ctx) { return 8u * (unsigned)ctx.num_sms; }
+
+}  // namespace
+
+int64_t pages_workspace(const w4a16_books_shape& b, int64_t count) {
+    return 4 * (4 + b.rows + 4 * count + 3 * b.pages);
+}
+
+cudaError_t launch_pages_free(const PageBooks& b, const int32_t* listed, int64_t count,
+                              cudaStream_t stream) {
+    return launch_books(free_kernel, b.shape.pages, stream, books_of(b), listed, count);
+}
+
+cudaError_t launch_pages_extend(const PageBooks& b, const int32_t* listed, const int32_t* counts,
+                                int64_t count, int32_t* done, void* workspace,
+                                cudaStream_t stream) {
+    return launch_books(extend_kernel, b.shape.pages, stream, books_of(b), listed, counts, count,
+                        done, split_space(workspace, b.shape.rows, b.shape.pages, count));
+}
+
+cudaError_t launch_pages_fork(void* pool, const PageBooks& b, const int32_t* parents,
+                              const int32_t* children, int64_t count, int32_t* done,
+                              void* workspace, const w4a16_pool_shape& shape, cudaStream_t stream,
+                              const DeviceCtx& ctx) {
+    const Space s = split_space(workspace, b.shape.rows, b.shape.pages, count);
+    cudaError_t e = launch_books(fork_plan_kernel, b.shape.pages, stream, books_of(b), parents,
+                                 children, count, done, s);
+    if (e != cudaSuccess) return e;
+    return launch_apply(fork_apply_kernel, copy_ctas(ctx), stream, books_of(b), parents, children,
+                        count, s, pool_of(pool, shape));
+}
+
+cudaError_t launch_pages_compact(void* pool, const PageBooks& b, int32_t* used, void* workspace,
+                                 const w4a16_pool_shape& shape, cudaStream_t stream,
+                                 const DeviceCtx& ctx) {
+    const Space s = split_space(workspace, b.shape.rows, b.shape.pages, 0);
+    cudaError_t e = launch_books(compact_plan_kernel, b.shape.pages, stream, books_of(b), used, s);
+    if (e != cudaSuccess) return e;
+    return launch_apply(compact_apply_kernel, copy_ctas(ctx), stream, books_of(b),
+                        (const int32_t*)used, s, pool_of(pool, shape));
+}
+
+cudaError_t launch_pages_copy(void* pool, const int32_t* from, const int32_t* to, int64_t count,
+                              int64_t pages, const w4a16_pool_shape& shape, cudaStream_t stream,
+                              const DeviceCtx& ctx) {
+    if (count == 0) return cudaSuccess;
+    copy_kernel<<<copy_ctas(ctx), kCopyThreads, 0, stream>>>(pool_of(pool, shape), from, to, count,
+                                                             pages);
+    return cudaGetLastError();
+}
+
+}  // namespace w4a16
