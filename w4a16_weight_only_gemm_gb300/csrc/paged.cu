@@ -2,6 +2,9 @@
 // attention of one new token over them.
 #include <cuda_bf16.h>
 
+#include <atomic>
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -70,114 +73,598 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
 
 // ---------------------------------------------------------------------------
 // Attention
+//
+// A step is 64 positions of one item (a row's key-value head with up to 16 of
+// its query heads); the items' steps, one item after the other, form one line
+// that the blocks cut into equal parts, so rows of any lengths load every SM
+// alike and one long row is split over all of them.  A block that has all of
+// an item writes its output; the others leave (max, sum, unnormalised output)
+// in the workspace, and join_kernel adds those up.
+//
+// Bound by HBM: each key and value is read once and meets 2 * group FLOPs a
+// byte, so what counts is bytes in flight.  Each lane has a ring of its own in
+// shared memory: it copies (cp.async) exactly the 16-byte pieces that it reads
+// back as MMA operands, so the ring needs no barrier and has no bank conflict.
+// Scores are taken transposed, S^T = K Q^T: 16 positions are the rows of an
+// MMA and 8 query heads its columns, with the dimension permuted alike in K
+// and Q so that a lane's operands are 16 consecutive bytes.  P^T becomes the
+// right operand of O^T = V^T P^T by an 8x8 transposition between lanes; V's
+// pairs of positions are put together from two of the lane's own pieces.
+// P is split in two 16-bit parts, its value and what rounding that left over,
+// so that the probabilities keep 22 (fp16) or 16 (bf16) bits: the MMAs are
+// far from the bound, and the output is then rounded only once.
 // ---------------------------------------------------------------------------
-template <typename T>
-__device__ __forceinline__ float to_float(T v);
-template <>
-__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
-template <>
-__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <typename T>
-__device__ __forceinline__ T from_float(float v);
-template <>
-__device__ __forceinline__ __half from_float(float v) { return __float2half_rn(v); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_float(float v) { return __float2bfloat16_rn(v); }
-
 constexpr int kAttendWarps = 4;
-constexpr int kMaxDim = 256;
+constexpr int kAttendThreads = 32 * kAttendWarps;
+constexpr int kTile = 16;                       // positions of a warp in a step
+constexpr int kStep = kTile * kAttendWarps;     // positions of a step
+constexpr float kLn2 = 0.6931471805599453f;
 
-template <typename T>
-struct AttendArgs {
-    const T *q, *k_pool, *v_pool;
-    const int32_t *tables, *lengths;
-    T* out;
-    float* lse;
-    int q_heads, group;
-    int64_t q_row, q_head, out_row, out_head;
-    float scale;
-    Cache c;
+// What a block leaves for the join: the item that begins in it and is ended
+// by the `count` blocks after it (count 0: none).
+struct Joint {
+    int row, item, count, unused;
 };
 
-// One block a (row, query head); a warp takes every fourth position, a lane
-// every 32nd element, with a running maximum and sum; the warps join at the end.
+struct AttendArgs {
+    const uint16_t *q, *k_pool, *v_pool;
+    const int32_t *tables, *lengths;
+    uint16_t* out;
+    float* lse;
+    float* partial;     // [blocks][2][heads of an item][padded dim]
+    float2* partial_ml; // [blocks][2][heads of an item]
+    Joint* joints;      // [blocks]
+    int q_heads, group;
+    int items;          // of a row: kv_heads * blocks of heads
+    int head_blocks;    // per key-value head
+    int block_heads;    // query heads of an item (the last block may have fewer)
+    int64_t q_row, q_head, out_row, out_head;
+    float scale_log2;
+    Cache c;
+
+    __device__ int length(int row) const {
+        return min(max(lengths[row], 0), c.width * c.page_size);
+    }
+    __device__ int first_head(int item) const {
+        return item / head_blocks * group + item % head_blocks * block_heads;
+    }
+    __device__ int heads_of(int item) const {
+        return min(block_heads, group - item % head_blocks * block_heads);
+    }
+};
+
 template <typename T>
-__global__ void __launch_bounds__(32 * kAttendWarps) attend_kernel(AttendArgs<T> a) {
-    __shared__ float part[kAttendWarps][kMaxDim], top[kAttendWarps], total[kAttendWarps];
-    const int h = blockIdx.x, b = blockIdx.y, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int d = a.c.head_dim;
-    const int64_t most = (int64_t)a.c.width * a.c.page_size;
-    const int64_t n = min((int64_t)max(a.lengths[b], 0), most);
-    float q[kMaxDim / 32], o[kMaxDim / 32], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int i = 0; i < kMaxDim / 32; ++i) {
-        const int x = 32 * i + lane;
-        q[i] = x < d ? to_float(a.q[b * a.q_row + h * a.q_head + x]) * a.scale : 0.f;
-        o[i] = 0.f;
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t v);
+template <>
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t v) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t v) {
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
+}
+
+// c += A(16x16) * B(16x8)
+template <typename T>
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1) {
+    if constexpr (std::is_same<T, __half>::value)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+            "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+            "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+// 16 bytes to shared memory, or 16 zero bytes when `there` is false.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(there ? 16 : 0)
+                 : "memory");
+}
+
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <int DP>
+struct AttendShape {
+    static constexpr int kPieces = DP / 8;              // 16-byte pieces of a lane in a tile
+    static constexpr int kTileBytes = kPieces * 512;    // a warp's keys and values of 16 positions
+    static constexpr int kStageBytes = kTileBytes * kAttendWarps;
+    static constexpr int kBlocksPerSm = DP <= 128 ? 2 : 1;
+    static constexpr int kStages = DP == 64 ? 6 : 3;    // 96 KB a block, or 192 KB
+    static constexpr int kSmem = kStages * kStageBytes;
+};
+
+// A place on the line of steps.
+struct Place {
+    int row, item, tile, steps, length;
+};
+
+__device__ __forceinline__ int steps_of(int length) { return (length + kStep - 1) / kStep; }
+
+__device__ __forceinline__ void advance(const AttendArgs& a, Place& p) {
+    if (++p.tile < p.steps) return;
+    p.tile = 0;
+    if (++p.item < a.items) return;
+    p.item = 0;
+    p.steps = 0;
+    while (++p.row < a.c.batch) {
+        p.length = a.length(p.row);
+        p.steps = steps_of(p.length);
+        if (p.steps) return;
     }
-    for (int64_t p = warp; p < n; p += kAttendWarps) {
-        const int64_t page = a.tables[b * a.c.table_stride + p / a.c.page_size];
-        if (page < 0 || page >= a.c.pages) continue;
-        const int64_t at = page * a.c.page_stride + p % a.c.page_size * a.c.slot_stride +
-                           h / a.group * a.c.head_stride;
-        float s = 0.f;
+}
+
+// The part [lo, hi) of the line that block `index` of `blocks` takes.
+__device__ __forceinline__ int64_t cut(int64_t total, int64_t index, int64_t blocks) {
+    return total * index / blocks;
+}
+
+template <typename T, int DP, int NT, bool kTilePage>
+__global__ void __launch_bounds__(kAttendThreads, AttendShape<DP>::kBlocksPerSm)
+    attend_kernel(AttendArgs a) {
+    using S = AttendShape<DP>;
+    constexpr int kHeads = 8 * NT;
+    extern __shared__ __align__(16) unsigned char ring[];
+    __shared__ int64_t scan[kAttendWarps];
+    __shared__ Place begin;
+    __shared__ float2 warp_ml[kAttendWarps][kHeads];
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
+    const int dim = a.c.head_dim;
+
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    // The line: its length, and where this block's part begins.
+    const int per = (a.c.batch + kAttendThreads - 1) / kAttendThreads;
+    const int r0 = min(tid * per, a.c.batch), r1 = min(r0 + per, a.c.batch);
+    int64_t mine = 0;
+    for (int r = r0; r < r1; ++r) mine += steps_of(a.length(r));
+    int64_t upto = mine;
 #pragma unroll
-        for (int i = 0; i < kMaxDim / 32; ++i)
-            if (32 * i + lane < d) s += q[i] * to_float(a.k_pool[at + 32 * i + lane]);
-#pragma unroll
-        for (int x = 16; x > 0; x /= 2) s += __shfl_xor_sync(~0u, s, x);
-        const float higher = fmaxf(m, s);
-        if (higher == -INFINITY) continue;
-        const float keep = __expf(m - higher), w = __expf(s - higher);
-        l = l * keep + w;
-        m = higher;
-#pragma unroll
-        for (int i = 0; i < kMaxDim / 32; ++i)
-            if (32 * i + lane < d)
-                o[i] = o[i] * keep + w * to_float(a.v_pool[at + 32 * i + lane]);
+    for (int d = 1; d < 32; d *= 2) {
+        const int64_t o = __shfl_up_sync(~0u, upto, d);
+        if (lane >= d) upto += o;
     }
-#pragma unroll
-    for (int i = 0; i < kMaxDim / 32; ++i) part[warp][32 * i + lane] = o[i];
-    if (lane == 0) top[warp] = m, total[warp] = l;
+    if (lane == 31) scan[warp] = upto;
     __syncthreads();
-    m = -INFINITY, l = 0.f;
-    for (int w = 0; w < kAttendWarps; ++w) m = fmaxf(m, top[w]);
-    float keep[kAttendWarps];
+    int64_t total = 0;
+#pragma unroll
     for (int w = 0; w < kAttendWarps; ++w) {
-        keep[w] = top[w] == -INFINITY ? 0.f : __expf(top[w] - m);
-        l += total[w] * keep[w];
+        if (w < warp) upto += scan[w];
+        total += scan[w];
     }
-    for (int x = threadIdx.x; x < d; x += 32 * kAttendWarps) {
-        float v = 0.f;
-        for (int w = 0; w < kAttendWarps; ++w) v += part[w][x] * keep[w];
-        a.out[b * a.out_row + h * a.out_head + x] = from_float<T>(l > 0.f ? v / l : 0.f);
+    total *= a.items;
+    const int64_t blocks = min((int64_t)gridDim.x, total);
+    const bool idle = blockIdx.x >= blocks;
+    const int64_t lo = idle ? total : cut(total, blockIdx.x, blocks);
+    const int64_t hi = idle ? total : cut(total, blockIdx.x + 1, blocks);
+    if (!idle && (upto - mine) * a.items <= lo && lo < upto * a.items) {
+        int r = r0;
+        int64_t at = (upto - mine) * a.items;
+        int n = steps_of(a.length(r));
+        while (at + (int64_t)n * a.items <= lo) at += (int64_t)n * a.items, n = steps_of(a.length(++r));
+        begin = {r, (int)((lo - at) / n), (int)((lo - at) % n), n, a.length(r)};
     }
-    if (a.lse && threadIdx.x == 0) a.lse[(int64_t)b * a.q_heads + h] = l > 0.f ? m + logf(l) : -INFINITY;
+    if (tid == 0) a.joints[blockIdx.x] = {0, 0, 0, 0};
+    // rows without a position
+    for (int r = blockIdx.x; r < a.c.batch; r += gridDim.x) {
+        if (a.length(r) != 0) continue;
+        for (int h = warp; h < a.q_heads; h += kAttendWarps) {
+            for (int x = lane * 8; x < dim; x += 256)
+                *reinterpret_cast<uint4*>(a.out + r * a.out_row + h * a.out_head + x) =
+                    make_uint4(0, 0, 0, 0);
+            if (a.lse && lane == 0) a.lse[(int64_t)r * a.q_heads + h] = -INFINITY;
+        }
+    }
+    if (idle) return;
+    __syncthreads();
+
+    Place ahead = begin, here = begin;
+    const uint32_t my_ring = smem_u32(ring) + warp * S::kTileBytes + lane * 16;
+    uint32_t flags = 0;      // two bits a tile in flight: whether the lane's two positions count
+    int64_t left = hi - lo;  // steps to issue
+    int next_page = -1;      // of the tile to issue next: the warp's, or of position `lane`
+
+    const auto load_page = [&]() {
+        const int p = ahead.tile * kStep + warp * kTile + (kTilePage ? 0 : lane % kTile);
+        next_page = -1;
+        if (p < ahead.length)
+            next_page = a.tables[ahead.row * a.c.table_stride + p / a.c.page_size];
+    };
+    const auto issue = [&](int stage) {
+        flags <<= 2;
+        if (left > 0) {
+            --left;
+            const int first = ahead.tile * kStep + warp * kTile;
+            const int64_t head = (int64_t)(ahead.item / a.head_blocks) * a.c.head_stride;
+            const bool there = (uint32_t)next_page < (uint32_t)a.c.pages;
+            int64_t at;      // where the tile's first position starts, or position `lane`
+            if (kTilePage)
+                at = next_page * a.c.page_stride + first % a.c.page_size * a.c.slot_stride + head;
+            else
+                at = there ? next_page * a.c.page_stride +
+                                 (first + lane % kTile) % a.c.page_size * a.c.slot_stride + head
+                           : -1;
+            const auto place = [&](int x, bool& in) -> int64_t {
+                if (kTilePage) {
+                    in = there && first + x < ahead.length;
+                    return in ? at + x * a.c.slot_stride : 0;
+                }
+                const int64_t o = __shfl_sync(~0u, at, x);
+                in = o >= 0;  // a page number is looked up only below the length
+                return in ? o : 0;
+            };
+            const uint32_t dst = my_ring + stage * S::kStageBytes;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                bool in;
+                const uint16_t* src = a.k_pool + place(g + 8 * r, in) + 8 * t;
+                flags |= (uint32_t)in << r;
+#pragma unroll
+                for (int j = 0; j < DP / 32; ++j)
+                    copy16(dst + (r * (DP / 32) + j) * 512, src + 32 * j,
+                           in && 32 * j + 8 * t < dim);
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                bool in;
+                const uint16_t* src = a.v_pool + place(2 * t + (x & 1) + 8 * (x >> 1), in) + 8 * g;
+#pragma unroll
+                for (int j = 0; j < DP / 64; ++j)
+                    copy16(dst + (DP / 16 + x * (DP / 64) + j) * 512, src + 64 * j,
+                           in && 64 * j + 8 * g < dim);
+            }
+            advance(a, ahead);
+            if (left > 0) load_page();
+        }
+        copy_commit();
+    };
+
+    load_page();
+#pragma unroll 1
+    for (int s = 0; s < S::kStages; ++s) issue(s);
+
+    uint4 q[NT][DP / 32];
+    float o[NT][DP / 16][4], top[NT][2], sum[NT][2];
+    bool fresh = true;
+    int first_tile = 0, stage = 0;
+#pragma unroll 1
+    for (int64_t step = lo; step < hi; ++step) {
+        if (fresh) {
+            fresh = false;
+            first_tile = here.tile;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int h = 8 * n + g;
+                const bool in = h < a.heads_of(here.item);
+                const uint16_t* src =
+                    a.q + here.row * a.q_row + (a.first_head(here.item) + (in ? h : 0)) * a.q_head + 8 * t;
+#pragma unroll
+                for (int j = 0; j < DP / 32; ++j)
+                    q[n][j] = in && 32 * j + 8 * t < dim ? *reinterpret_cast<const uint4*>(src + 32 * j)
+                                                         : make_uint4(0, 0, 0, 0);
+                top[n][0] = top[n][1] = -INFINITY;
+                sum[n][0] = sum[n][1] = 0.f;
+#pragma unroll
+                for (int i = 0; i < DP / 16; ++i)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) o[n][i][x] = 0.f;
+            }
+        }
+        copy_wait<S::kStages - 1>();
+        const uint32_t src = my_ring + stage * S::kStageBytes;
+        float c[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
+#pragma unroll
+        for (int j = 0; j < DP / 32; ++j) {
+            const uint4 k0 = lds128(src + j * 512), k1 = lds128(src + (DP / 32 + j) * 512);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                mma<T>(c[n], k0.x, k1.x, k0.y, k1.y, q[n][j].x, q[n][j].y);
+                mma<T>(c[n], k0.z, k1.z, k0.w, k1.w, q[n][j].z, q[n][j].w);
+            }
+        }
+        const uint32_t bits = flags >> (2 * (S::kStages - 1));
+        uint32_t p_hi[NT][2], p_lo[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float keep[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {  // heads 2t and 2t + 1
+                const float s0 = bits & 1 ? c[n][x] * a.scale_log2 : -INFINITY;
+                const float s1 = bits & 2 ? c[n][x + 2] * a.scale_log2 : -INFINITY;
+                float m = fmaxf(s0, s1);
+                m = fmaxf(m, __shfl_xor_sync(~0u, m, 4));
+                m = fmaxf(m, __shfl_xor_sync(~0u, m, 8));
+                m = fmaxf(m, __shfl_xor_sync(~0u, m, 16));
+                m = fmaxf(m, top[n][x]);
+                const float base = m == -INFINITY ? 0.f : m;  // nothing yet: every weight is 0
+                keep[x] = exp2_fast(top[n][x] - base);
+                top[n][x] = m;
+                c[n][x] = exp2_fast(s0 - base);
+                c[n][x + 2] = exp2_fast(s1 - base);
+                sum[n][x] = sum[n][x] * keep[x] + (c[n][x] + c[n][x + 2]);
+            }
+            if (__any_sync(~0u, keep[0] != 1.f || keep[1] != 1.f)) {
+#pragma unroll
+                for (int i = 0; i < DP / 16; ++i) {
+                    o[n][i][0] *= keep[0], o[n][i][1] *= keep[1];
+                    o[n][i][2] *= keep[0], o[n][i][3] *= keep[1];
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {  // positions g and g + 8
+                const uint32_t hi16 = pack2<T>(c[n][2 * r], c[n][2 * r + 1]);
+                const float2 back = unpack2<T>(hi16);
+                p_hi[n][r] = transpose8x8(hi16);
+                p_lo[n][r] = transpose8x8(pack2<T>(c[n][2 * r] - back.x, c[n][2 * r + 1] - back.y));
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < DP / 64; ++j) {
+            uint32_t v[4][4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const uint4 w = lds128(src + (DP / 16 + x * (DP / 64) + j) * 512);
+                v[x][0] = w.x, v[x][1] = w.y, v[x][2] = w.z, v[x][3] = w.w;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {  // rows g and g + 8: dims 64j + 8g + 2i and one more
+                const uint32_t a0 = __byte_perm(v[0][i], v[1][i], 0x5410);
+                const uint32_t a1 = __byte_perm(v[0][i], v[1][i], 0x7632);
+                const uint32_t a2 = __byte_perm(v[2][i], v[3][i], 0x5410);
+                const uint32_t a3 = __byte_perm(v[2][i], v[3][i], 0x7632);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    mma<T>(o[n][4 * j + i], a0, a1, a2, a3, p_hi[n][0], p_hi[n][1]);
+                    mma<T>(o[n][4 * j + i], a0, a1, a2, a3, p_lo[n][0], p_lo[n][1]);
+                }
+            }
+        }
+
+        const bool ends = here.tile == here.steps - 1;
+        if (ends || step == hi - 1) {
+            // The warps' parts meet in the slots of the tiles just read.
+            float* mine_out = reinterpret_cast<float*>(ring + stage * S::kStageBytes +
+                                                       warp * S::kTileBytes);
+            __syncwarp();
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float l = sum[n][x];
+                    l += __shfl_xor_sync(~0u, l, 4);
+                    l += __shfl_xor_sync(~0u, l, 8);
+                    l += __shfl_xor_sync(~0u, l, 16);
+                    const int h = 8 * n + 2 * t + x;
+                    if (g == 0) warp_ml[warp][h] = make_float2(top[n][x], l);
+#pragma unroll
+                    for (int i = 0; i < DP / 16; ++i)
+                        *reinterpret_cast<float2*>(mine_out + h * DP + 64 * (i / 4) + 8 * g +
+                                                   2 * (i % 4)) =
+                            make_float2(o[n][i][x], o[n][i][x + 2]);
+                }
+            }
+            __syncthreads();
+            const bool whole = ends && first_tile == 0;
+            const int heads = a.heads_of(here.item), side = first_tile == 0 ? 1 : 0;
+            const float* parts = reinterpret_cast<const float*>(ring + stage * S::kStageBytes);
+            for (int i = tid; i < heads * (DP / 4); i += kAttendThreads) {
+                const int h = i / (DP / 4), x = i % (DP / 4) * 4;
+                float m = -INFINITY, l = 0.f;
+#pragma unroll
+                for (int w = 0; w < kAttendWarps; ++w) m = fmaxf(m, warp_ml[w][h].x);
+                const float base = m == -INFINITY ? 0.f : m;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < kAttendWarps; ++w) {
+                    const float e = exp2_fast(warp_ml[w][h].x - base);
+                    const float4 u = *reinterpret_cast<const float4*>(
+                        parts + w * (S::kTileBytes / 4) + h * DP + x);
+                    l += e * warp_ml[w][h].y;
+                    v.x += e * u.x, v.y += e * u.y, v.z += e * u.z, v.w += e * u.w;
+                }
+                if (whole) {
+                    const int head = a.first_head(here.item) + h;
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
+                    if (x < dim)
+                        *reinterpret_cast<uint2*>(a.out + here.row * a.out_row + head * a.out_head + x) =
+                            make_uint2(pack2<T>(v.x * inv, v.y * inv), pack2<T>(v.z * inv, v.w * inv));
+                    if (x == 0 && a.lse)
+                        a.lse[(int64_t)here.row * a.q_heads + head] =
+                            l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+                } else {
+                    const int64_t slot = ((int64_t)blockIdx.x * 2 + side) * kHeads + h;
+                    *reinterpret_cast<float4*>(a.partial + slot * DP + x) = v;
+                    if (x == 0) a.partial_ml[slot] = make_float2(m, l);
+                }
+            }
+            if (!ends && side == 1 && tid == 0) {
+                const int64_t last = step + (here.steps - 1 - here.tile);  // the item's last step
+                int64_t owner = last * blocks / total;
+                while (cut(total, owner + 1, blocks) <= last) ++owner;
+                while (cut(total, owner, blocks) > last) --owner;
+                a.joints[blockIdx.x] = {here.row, here.item, (int)(owner - blockIdx.x), 0};
+            }
+            __syncthreads();
+            fresh = true;
+        }
+        advance(a, here);
+        issue(stage);
+        stage = stage + 1 == S::kStages ? 0 : stage + 1;
+    }
+    copy_wait<0>();
+}
+
+// Adds up an item's parts: block (x, y) has head y of the item that begins in
+// block x of attend_kernel.  Four groups of threads take the parts in turn.
+constexpr int kJoinGroups = 4;
+template <typename T, int DP>
+__global__ void __launch_bounds__(DP / 4 * kJoinGroups) join_kernel(AttendArgs a, int heads_padded) {
+    __shared__ float4 part[kJoinGroups][DP / 4];
+    __shared__ float2 part_ml[kJoinGroups];
+    const int h = blockIdx.y, x = threadIdx.x % (DP / 4), group = threadIdx.x / (DP / 4);
+    grid_dependency_wait();
+    const Joint joint = a.joints[blockIdx.x];
+    if (joint.count == 0 || h >= a.heads_of(joint.item)) return;
+    float m = -INFINITY, l = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = group; i <= joint.count; i += kJoinGroups) {
+        const int64_t slot = ((int64_t)(blockIdx.x + i) * 2 + (i == 0)) * heads_padded + h;
+        const float2 ml = a.partial_ml[slot];
+        const float4 u = *reinterpret_cast<const float4*>(a.partial + slot * DP + 4 * x);
+        const float higher = fmaxf(m, ml.x), base = higher == -INFINITY ? 0.f : higher;
+        const float keep = exp2_fast(m - base), e = exp2_fast(ml.x - base);
+        m = higher;
+        l = l * keep + e * ml.y;
+        v.x = v.x * keep + e * u.x, v.y = v.y * keep + e * u.y;
+        v.z = v.z * keep + e * u.z, v.w = v.w * keep + e * u.w;
+    }
+    part[group][x] = v;
+    if (x == 0) part_ml[group] = make_float2(m, l);
+    __syncthreads();
+    if (group) return;
+    m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int i = 0; i < kJoinGroups; ++i) m = fmaxf(m, part_ml[i].x);
+    const float base = m == -INFINITY ? 0.f : m;
+    v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kJoinGroups; ++i) {
+        const float e = exp2_fast(part_ml[i].x - base);
+        const float4 u = part[i][x];
+        l += e * part_ml[i].y;
+        v.x += e * u.x, v.y += e * u.y, v.z += e * u.z, v.w += e * u.w;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int head = a.first_head(joint.item) + h;
+    if (4 * x < a.c.head_dim)
+        *reinterpret_cast<uint2*>(a.out + joint.row * a.out_row + head * a.out_head + 4 * x) =
+            make_uint2(pack2<T>(v.x * inv, v.y * inv), pack2<T>(v.z * inv, v.w * inv));
+    if (x == 0 && a.lse)
+        a.lse[(int64_t)joint.row * a.q_heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// Query heads of an item and their tiles of 8: one tile up to 8 heads to a
+// key-value head, else two; more than 16 are dealt out evenly over blocks.
+struct HeadPlan {
+    int tiles, blocks, heads;
+};
+HeadPlan plan_heads(int64_t group) {
+    HeadPlan p;
+    p.tiles = group <= 8 ? 1 : 2;
+    p.blocks = (int)((group + 8 * p.tiles - 1) / (8 * p.tiles));
+    p.heads = (int)((group + p.blocks - 1) / p.blocks);
+    return p;
+}
+
+int padded_dim(int64_t dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
+
+int attend_blocks(int64_t dim, const DeviceCtx& ctx) { return ctx.num_sms * (dim <= 128 ? 2 : 1); }
+
+// The workspace: partial outputs, their maxima and sums, the joints.
+struct Workspace {
+    int64_t partial, ml, joints, bytes;
+};
+Workspace plan_workspace(int64_t dim, int64_t group, const DeviceCtx& ctx) {
+    const int64_t blocks = attend_blocks(dim, ctx), slots = 2 * blocks * 8 * plan_heads(group).tiles;
+    Workspace w;
+    w.partial = 0;
+    w.ml = slots * padded_dim(dim) * 4;
+    w.joints = w.ml + slots * 8;
+    w.bytes = w.joints + blocks * (int64_t)sizeof(Joint);
+    return w;
+}
+
+template <typename T, int DP, int NT, bool kTilePage>
+cudaError_t attend(const AttendArgs& a, cudaStream_t stream, const DeviceCtx& ctx) {
+    using S = AttendShape<DP>;
+    static std::atomic<bool> ready[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(attend_kernel<T, DP, NT, kTilePage>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) ready[dev].store(true, std::memory_order_release);
+    }
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    const unsigned blocks = (unsigned)attend_blocks(DP, ctx);
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kAttendThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, attend_kernel<T, DP, NT, kTilePage>, a);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(blocks, (unsigned)a.block_heads);
+    cfg.blockDim = dim3(DP / 4 * kJoinGroups);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, join_kernel<T, DP>, a, 8 * NT);
+}
+
+// Tiles of 16 positions lie within a page where the page size is a multiple of
+// 16: one page number a tile then, else one a position.
+template <typename T, int DP, int NT>
+cudaError_t attend(const AttendArgs& a, cudaStream_t stream, const DeviceCtx& ctx) {
+    return a.c.page_size % kTile == 0 ? attend<T, DP, NT, true>(a, stream, ctx)
+                                      : attend<T, DP, NT, false>(a, stream, ctx);
+}
+
+template <typename T, int DP>
+cudaError_t attend(const AttendArgs& a, int tiles, cudaStream_t stream, const DeviceCtx& ctx) {
+    return tiles == 1 ? attend<T, DP, 1>(a, stream, ctx) : attend<T, DP, 2>(a, stream, ctx);
 }
 
 template <typename T>
-cudaError_t attend(const void* q, const void* k_pool, const void* v_pool, const int32_t* tables,
-                   const int32_t* lengths, void* out, float* lse, const w4a16_cache_shape& cache,
-                   const w4a16_query_shape& query, cudaStream_t stream) {
-    AttendArgs<T> a;
-    a.q = static_cast<const T*>(q);
-    a.k_pool = static_cast<const T*>(k_pool);
-    a.v_pool = static_cast<const T*>(v_pool);
-    a.tables = tables;
-    a.lengths = lengths;
-    a.out = static_cast<T*>(out);
-    a.lse = lse;
-    a.q_heads = (int)query.q_heads;
-    a.group = (int)(query.q_heads / cache.kv_heads);
-    a.q_row = query.q_row_stride;
-    a.q_head = query.q_head_stride;
-    a.out_row = query.out_row_stride;
-    a.out_head = query.out_head_stride;
-    a.scale = (float)query.scale;
-    a.c = cache_of(cache);
-    attend_kernel<T><<<dim3((unsigned)query.q_heads, (unsigned)cache.batch), 32 * kAttendWarps, 0,
-                       stream>>>(a);
-    return cudaGetLastError();
+cudaError_t attend(const AttendArgs& a, int tiles, cudaStream_t stream, const DeviceCtx& ctx) {
+    switch (padded_dim(a.c.head_dim)) {
+        case 64: return attend<T, 64>(a, tiles, stream, ctx);
+        case 128: return attend<T, 128>(a, tiles, stream, ctx);
+        default: return attend<T, 256>(a, tiles, stream, ctx);
+    }
 }
 
 }  // namespace
@@ -199,8 +686,7 @@ cudaError_t launch_paged_append(const void* k, const void* v, void* k_pool, void
 
 int64_t paged_attention_workspace(const w4a16_cache_shape& cache, int64_t q_heads,
                                   const DeviceCtx& ctx) {
-    (void)cache, (void)q_heads, (void)ctx;
-    return 16;
+    return plan_workspace(cache.head_dim, q_heads / cache.kv_heads, ctx).bytes;
 }
 
 cudaError_t launch_paged_attention(const void* q, const void* k_pool, const void* v_pool,
@@ -208,10 +694,33 @@ cudaError_t launch_paged_attention(const void* q, const void* k_pool, const void
                                    float* lse, void* workspace, const w4a16_cache_shape& cache,
                                    const w4a16_query_shape& query, cudaStream_t stream,
                                    const DeviceCtx& ctx) {
-    (void)workspace, (void)ctx;
-    return cache.type == W4A16_BF16
-               ? attend<__nv_bfloat16>(q, k_pool, v_pool, tables, lengths, out, lse, cache, query, stream)
-               : attend<__half>(q, k_pool, v_pool, tables, lengths, out, lse, cache, query, stream);
+    AttendArgs a;
+    a.q = static_cast<const uint16_t*>(q);
+    a.k_pool = static_cast<const uint16_t*>(k_pool);
+    a.v_pool = static_cast<const uint16_t*>(v_pool);
+    a.tables = tables;
+    a.lengths = lengths;
+    a.out = static_cast<uint16_t*>(out);
+    a.lse = lse;
+    a.q_heads = (int)query.q_heads;
+    a.group = (int)(query.q_heads / cache.kv_heads);
+    const HeadPlan heads = plan_heads(a.group);
+    a.head_blocks = heads.blocks;
+    a.block_heads = heads.heads;
+    a.items = (int)cache.kv_heads * heads.blocks;
+    const Workspace w = plan_workspace(cache.head_dim, a.group, ctx);
+    char* base = static_cast<char*>(workspace);
+    a.partial = reinterpret_cast<float*>(base + w.partial);
+    a.partial_ml = reinterpret_cast<float2*>(base + w.ml);
+    a.joints = reinterpret_cast<Joint*>(base + w.joints);
+    a.q_row = query.q_row_stride;
+    a.q_head = query.q_head_stride;
+    a.out_row = query.out_row_stride;
+    a.out_head = query.out_head_stride;
+    a.scale_log2 = (float)(query.scale * 1.4426950408889634);
+    a.c = cache_of(cache);
+    return cache.type == W4A16_BF16 ? attend<__nv_bfloat16>(a, heads.tiles, stream, ctx)
+                                    : attend<__half>(a, heads.tiles, stream, ctx);
 }
 
 }  // namespace w4a16
