@@ -15,12 +15,23 @@ namespace {
 struct Cache {
     int64_t pages, page_stride, slot_stride, head_stride, table_stride;
     int page_size, kv_heads, head_dim, batch, width;
+    uint32_t div_mul, div_shift;
+
+    // position / page_size for 0 <= position < 2^31: with l = ceil(log2 page_size) and
+    // m = floor(2^(31 + l) / page_size) + 1, m * page_size exceeds 2^(31 + l) by at most
+    // page_size <= 2^l, so position * m / 2^(31 + l) is off by less than 1 / page_size.
+    __device__ __forceinline__ int page_of(int position) const {
+        return (int)(((uint64_t)(uint32_t)position * div_mul) >> div_shift);
+    }
 };
 
 Cache cache_of(const w4a16_cache_shape& c) {
-    return {c.pages,          c.page_stride,    c.slot_stride, c.head_stride,
+    uint32_t l = 0;
+    while (((int64_t)1 << l) < c.page_size) ++l;
+    return {c.pages,          c.page_stride,    c.slot_stride,   c.head_stride,
             c.table_stride,   (int)c.page_size, (int)c.kv_heads, (int)c.head_dim,
-            (int)c.batch,     (int)c.table_width};
+            (int)c.batch,     (int)c.table_width,
+            (uint32_t)(((uint64_t)1 << (31 + l)) / (uint64_t)c.page_size + 1), 31 + l};
 }
 
 // ---------------------------------------------------------------------------
@@ -82,14 +93,17 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
 // in the workspace, and join_kernel adds those up.
 //
 // Bound by HBM: each key and value is read once and meets 2 * group FLOPs a
-// byte, so what counts is bytes in flight.  Each lane has a ring of its own in
-// shared memory: it copies (cp.async) exactly the 16-byte pieces that it reads
-// back as MMA operands, so the ring needs no barrier and has no bank conflict.
-// Scores are taken transposed, S^T = K Q^T: 16 positions are the rows of an
-// MMA and 8 query heads its columns, with the dimension permuted alike in K
-// and Q so that a lane's operands are 16 consecutive bytes.  P^T becomes the
-// right operand of O^T = V^T P^T by an 8x8 transposition between lanes; V's
-// pairs of positions are put together from two of the lane's own pieces.
+// byte, so what counts is bytes in flight and few instructions a tile.  Each
+// warp has a ring of its own in shared memory, filled by cp.async with whole
+// 128-byte lines by eight lanes (lines cut in halves cost 1.5 times the traffic
+// between L2 and the SM), so it waits for its own copies only and the block
+// meets at the end of an item.  Scores are taken transposed, S^T = K Q^T: 16
+// positions are the rows of an MMA and 8 query heads its columns, with the
+// dimension permuted alike in K and Q so that a lane's operands are 16
+// consecutive bytes.  P^T becomes the right operand of O^T = V^T P^T by an 8x8
+// transposition between lanes; V^T comes from transposing matrix loads.  The
+// 16-byte pieces of a row are swizzled against bank conflicts, K's for the
+// lanes' 16-byte reads and V's for the matrix loads.
 // P is split in two 16-bit parts, its value and what rounding that left over,
 // so that the probabilities keep 22 (fp16) or 16 (bf16) bits: the MMAs are
 // far from the bound, and the output is then rounded only once.
@@ -161,13 +175,13 @@ template <typename T>
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                     uint32_t a3, uint32_t b0, uint32_t b1) {
     if constexpr (std::is_same<T, __half>::value)
-        asm volatile(
+        asm(
             "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
             "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
     else
-        asm volatile(
+        asm(
             "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
             "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -176,8 +190,20 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
+}
+
+// Four 8x8 matrices, transposed; lane i names row i % 8 of matrix i / 8.
+__device__ __forceinline__ void load_transposed(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
 // 16 bytes to shared memory, or 16 zero bytes when `there` is false.
@@ -199,13 +225,15 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-template <int DP>
+template <int DP, int NT>
 struct AttendShape {
-    static constexpr int kPieces = DP / 8;              // 16-byte pieces of a lane in a tile
-    static constexpr int kTileBytes = kPieces * 512;    // a warp's keys and values of 16 positions
+    static constexpr int kRowBytes = 2 * DP;
+    static constexpr int kHalf = kTile * kRowBytes;     // a warp's keys of 16 positions
+    static constexpr int kTileBytes = 2 * kHalf;        // and values
     static constexpr int kStageBytes = kTileBytes * kAttendWarps;
-    static constexpr int kBlocksPerSm = DP <= 128 ? 2 : 1;
-    static constexpr int kStages = DP == 64 ? 6 : 3;    // 96 KB a block, or 192 KB
+    // 192 KB of ring an SM: as many blocks as registers allow
+    static constexpr int kBlocksPerSm = DP == 64 ? (NT == 1 ? 4 : 3) : DP == 128 ? (NT == 1 ? 3 : 2) : 1;
+    static constexpr int kStages = 192 * 1024 / kBlocksPerSm / kStageBytes;
     static constexpr int kSmem = kStages * kStageBytes;
 };
 
@@ -235,9 +263,9 @@ __device__ __forceinline__ int64_t cut(int64_t total, int64_t index, int64_t blo
 }
 
 template <typename T, int DP, int NT, bool kTilePage>
-__global__ void __launch_bounds__(kAttendThreads, AttendShape<DP>::kBlocksPerSm)
+__global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPerSm)
     attend_kernel(AttendArgs a) {
-    using S = AttendShape<DP>;
+    using S = AttendShape<DP, NT>;
     constexpr int kHeads = 8 * NT;
     extern __shared__ __align__(16) unsigned char ring[];
     __shared__ int64_t scan[kAttendWarps];
@@ -295,17 +323,20 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP>::kBlocksPerSm)
     __syncthreads();
 
     Place ahead = begin, here = begin;
-    const uint32_t my_ring = smem_u32(ring) + warp * S::kTileBytes + lane * 16;
-    uint32_t flags = 0;      // two bits a tile in flight: whether the lane's two positions count
+    const uint32_t warp_ring = smem_u32(ring) + warp * S::kTileBytes;
+    uint32_t flags = 0;      // two bits a tile in flight: whether positions g and g + 8 count
     int64_t left = hi - lo;  // steps to issue
     int next_page = -1;      // of the tile to issue next: the warp's, or of position `lane`
 
     const auto load_page = [&]() {
         const int p = ahead.tile * kStep + warp * kTile + (kTilePage ? 0 : lane % kTile);
         next_page = -1;
-        if (p < ahead.length)
-            next_page = a.tables[ahead.row * a.c.table_stride + p / a.c.page_size];
+        if (p < ahead.length) next_page = a.tables[ahead.row * a.c.table_stride + a.c.page_of(p)];
     };
+    // Copies: lane's piece `piece` of rows row0, row0 + kRows, ...
+    constexpr int kPieces = DP / 8, kRows = 32 / kPieces;
+    const int piece = lane % kPieces, row0 = lane / kPieces;
+    const bool in_dim = piece * 8 < dim;
     const auto issue = [&](int stage) {
         flags <<= 2;
         if (left > 0) {
@@ -313,47 +344,63 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP>::kBlocksPerSm)
             const int first = ahead.tile * kStep + warp * kTile;
             const int64_t head = (int64_t)(ahead.item / a.head_blocks) * a.c.head_stride;
             const bool there = (uint32_t)next_page < (uint32_t)a.c.pages;
-            int64_t at;      // where the tile's first position starts, or position `lane`
-            if (kTilePage)
-                at = next_page * a.c.page_stride + first % a.c.page_size * a.c.slot_stride + head;
-            else
-                at = there ? next_page * a.c.page_stride +
-                                 (first + lane % kTile) % a.c.page_size * a.c.slot_stride + head
-                           : -1;
-            const auto place = [&](int x, bool& in) -> int64_t {
-                if (kTilePage) {
-                    in = there && first + x < ahead.length;
-                    return in ? at + x * a.c.slot_stride : 0;
-                }
-                const int64_t o = __shfl_sync(~0u, at, x);
-                in = o >= 0;  // a page number is looked up only below the length
-                return in ? o : 0;
+            const uint32_t dst = warp_ring + stage * S::kStageBytes + row0 * S::kRowBytes;
+            // the swizzle of row r: K's pieces meet 4 to a row in a read, V's 8 to a row
+            const auto k_at = [&](int r) {
+                const int y = row0 + r;
+                return dst + r * S::kRowBytes + ((piece ^ ((y & 1) << 2 | (y >> 1 & 3))) << 4);
             };
-            const uint32_t dst = my_ring + stage * S::kStageBytes;
+            const auto v_at = [&](int r) {
+                return dst + S::kHalf + r * S::kRowBytes + ((piece ^ (row0 + r & 7)) << 4);
+            };
+            if (kTilePage) {
+                const int slot = first - a.c.page_of(first) * a.c.page_size;
+                const int64_t at =
+                    next_page * a.c.page_stride + (slot + row0) * a.c.slot_stride + head + 8 * piece;
+                const int n = there ? ahead.length - first : 0;  // positions that count
+                const uint16_t *k = a.k_pool + at, *v = a.v_pool + at;
+                const int64_t next = kRows * a.c.slot_stride;
+                flags |= (uint32_t)(g < n) | (uint32_t)(g + 8 < n) << 1;
+                if (n >= kTile && dim == DP) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                bool in;
-                const uint16_t* src = a.k_pool + place(g + 8 * r, in) + 8 * t;
-                flags |= (uint32_t)in << r;
+                    for (int r = 0; r < kTile; r += kRows, k += next, v += next)
+                        copy16(k_at(r), k), copy16(v_at(r), v);
+                } else {
 #pragma unroll
-                for (int j = 0; j < DP / 32; ++j)
-                    copy16(dst + (r * (DP / 32) + j) * 512, src + 32 * j,
-                           in && 32 * j + 8 * t < dim);
-            }
+                    for (int r = 0; r < kTile; r += kRows, k += next, v += next) {
+                        const bool in = row0 + r < n && in_dim;
+                        copy16(k_at(r), in ? k : a.k_pool, in);
+                        copy16(v_at(r), in ? v : a.v_pool, in);
+                    }
+                }
+            } else {
+                // where position `lane` starts; a page number is looked up below the length only
+                const int p = first + lane % kTile;
+                const int64_t at = there ? next_page * a.c.page_stride +
+                                               (p - a.c.page_of(p) * a.c.page_size) * a.c.slot_stride +
+                                               head
+                                         : -1;
+                flags |= (uint32_t)(__shfl_sync(~0u, at, g) >= 0) |
+                         (uint32_t)(__shfl_sync(~0u, at, g + 8) >= 0) << 1;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                bool in;
-                const uint16_t* src = a.v_pool + place(2 * t + (x & 1) + 8 * (x >> 1), in) + 8 * g;
-#pragma unroll
-                for (int j = 0; j < DP / 64; ++j)
-                    copy16(dst + (DP / 16 + x * (DP / 64) + j) * 512, src + 64 * j,
-                           in && 64 * j + 8 * g < dim);
+                for (int r = 0; r < kTile; r += kRows) {
+                    const int64_t o = __shfl_sync(~0u, at, row0 + r);
+                    const bool in = o >= 0 && in_dim;
+                    copy16(k_at(r), a.k_pool + (in ? o + 8 * piece : 0), in);
+                    copy16(v_at(r), a.v_pool + (in ? o + 8 * piece : 0), in);
+                }
             }
             advance(a, ahead);
             if (left > 0) load_page();
         }
         copy_commit();
     };
+    // Reads: K's row g (and g + 8, alike in the swizzle), pieces 4j + t; V's transposed matrices.
+    const int k_swizzle = (g & 1) << 2 | (g >> 1 & 3);
+    const uint32_t k_lane = warp_ring + g * S::kRowBytes, k_xor = (t ^ k_swizzle) << 4;
+    const uint32_t v_lane =
+        warp_ring + S::kHalf + ((lane >> 4) * 8 + lane % 8) * S::kRowBytes;
+    const uint32_t v_xor = ((lane >> 3 & 1) ^ lane % 8) << 4;
 
     load_page();
 #pragma unroll 1
@@ -387,19 +434,27 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP>::kBlocksPerSm)
             }
         }
         copy_wait<S::kStages - 1>();
-        const uint32_t src = my_ring + stage * S::kStageBytes;
-        float c[NT][4];
+        __syncwarp();
+        const uint32_t at = stage * S::kStageBytes;
+        float c[NT][4], c2[NT][4];  // two chains
 #pragma unroll
-        for (int n = 0; n < NT; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) c[n][x] = c2[n][x] = 0.f;
 #pragma unroll
         for (int j = 0; j < DP / 32; ++j) {
-            const uint4 k0 = lds128(src + j * 512), k1 = lds128(src + (DP / 32 + j) * 512);
+            const uint32_t row = at + k_lane + (k_xor ^ (64 * j));
+            const uint4 k0 = lds128(row), k1 = lds128(row + 8 * S::kRowBytes);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 mma<T>(c[n], k0.x, k1.x, k0.y, k1.y, q[n][j].x, q[n][j].y);
-                mma<T>(c[n], k0.z, k1.z, k0.w, k1.w, q[n][j].z, q[n][j].w);
+                mma<T>(c2[n], k0.z, k1.z, k0.w, k1.w, q[n][j].z, q[n][j].w);
             }
         }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) c[n][x] += c2[n][x];
         const uint32_t bits = flags >> (2 * (S::kStages - 1));
         uint32_t p_hi[NT][2], p_lo[NT][2];
 #pragma unroll
@@ -437,33 +492,23 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP>::kBlocksPerSm)
             }
         }
 #pragma unroll
-        for (int j = 0; j < DP / 64; ++j) {
-            uint32_t v[4][4];
+        for (int i = 0; i < DP / 16; ++i) {
+            uint32_t v[4];
+            load_transposed(v, at + v_lane + (v_xor ^ (32 * i)));
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const uint4 w = lds128(src + (DP / 16 + x * (DP / 64) + j) * 512);
-                v[x][0] = w.x, v[x][1] = w.y, v[x][2] = w.z, v[x][3] = w.w;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {  // rows g and g + 8: dims 64j + 8g + 2i and one more
-                const uint32_t a0 = __byte_perm(v[0][i], v[1][i], 0x5410);
-                const uint32_t a1 = __byte_perm(v[0][i], v[1][i], 0x7632);
-                const uint32_t a2 = __byte_perm(v[2][i], v[3][i], 0x5410);
-                const uint32_t a3 = __byte_perm(v[2][i], v[3][i], 0x7632);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    mma<T>(o[n][4 * j + i], a0, a1, a2, a3, p_hi[n][0], p_hi[n][1]);
-                    mma<T>(o[n][4 * j + i], a0, a1, a2, a3, p_lo[n][0], p_lo[n][1]);
-                }
+            for (int n = 0; n < NT; ++n) {
+                mma<T>(o[n][i], v[0], v[1], v[2], v[3], p_hi[n][0], p_hi[n][1]);
+                mma<T>(o[n][i], v[0], v[1], v[2], v[3], p_lo[n][0], p_lo[n][1]);
             }
         }
+        __syncwarp();  // the tile is read: its slot may be filled again
 
         const bool ends = here.tile == here.steps - 1;
         if (ends || step == hi - 1) {
             // The warps' parts meet in the slots of the tiles just read.
+            // (dims 16i + g and 16i + g + 8 of heads 2t, 2t + 1; swizzled by the head)
             float* mine_out = reinterpret_cast<float*>(ring + stage * S::kStageBytes +
                                                        warp * S::kTileBytes);
-            __syncwarp();
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -475,10 +520,10 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP>::kBlocksPerSm)
                     const int h = 8 * n + 2 * t + x;
                     if (g == 0) warp_ml[warp][h] = make_float2(top[n][x], l);
 #pragma unroll
-                    for (int i = 0; i < DP / 16; ++i)
-                        *reinterpret_cast<float2*>(mine_out + h * DP + 64 * (i / 4) + 8 * g +
-                                                   2 * (i % 4)) =
-                            make_float2(o[n][i][x], o[n][i][x + 2]);
+                    for (int i = 0; i < DP / 16; ++i) {
+                        mine_out[h * DP + ((16 * i + g) ^ 8 * t)] = o[n][i][x];
+                        mine_out[h * DP + ((16 * i + g + 8) ^ 8 * t)] = o[n][i][x + 2];
+                    }
                 }
             }
             __syncthreads();
@@ -496,7 +541,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP>::kBlocksPerSm)
                 for (int w = 0; w < kAttendWarps; ++w) {
                     const float e = exp2_fast(warp_ml[w][h].x - base);
                     const float4 u = *reinterpret_cast<const float4*>(
-                        parts + w * (S::kTileBytes / 4) + h * DP + x);
+                        parts + w * (S::kTileBytes / 4) + h * DP + (x ^ 8 * (h / 2 % 4)));
                     l += e * warp_ml[w][h].y;
                     v.x += e * u.x, v.y += e * u.y, v.z += e * u.z, v.w += e * u.w;
                 }
@@ -597,14 +642,20 @@ HeadPlan plan_heads(int64_t group) {
 
 int padded_dim(int64_t dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
-int attend_blocks(int64_t dim, const DeviceCtx& ctx) { return ctx.num_sms * (dim <= 128 ? 2 : 1); }
+int attend_blocks(int64_t dim, int tiles, const DeviceCtx& ctx) {
+    const int per_sm[3][2] = {{AttendShape<64, 1>::kBlocksPerSm, AttendShape<64, 2>::kBlocksPerSm},
+                              {AttendShape<128, 1>::kBlocksPerSm, AttendShape<128, 2>::kBlocksPerSm},
+                              {AttendShape<256, 1>::kBlocksPerSm, AttendShape<256, 2>::kBlocksPerSm}};
+    return ctx.num_sms * per_sm[dim <= 64 ? 0 : dim <= 128 ? 1 : 2][tiles - 1];
+}
 
 // The workspace: partial outputs, their maxima and sums, the joints.
 struct Workspace {
     int64_t partial, ml, joints, bytes;
 };
 Workspace plan_workspace(int64_t dim, int64_t group, const DeviceCtx& ctx) {
-    const int64_t blocks = attend_blocks(dim, ctx), slots = 2 * blocks * 8 * plan_heads(group).tiles;
+    const int tiles = plan_heads(group).tiles;
+    const int64_t blocks = attend_blocks(dim, tiles, ctx), slots = 2 * blocks * 8 * tiles;
     Workspace w;
     w.partial = 0;
     w.ml = slots * padded_dim(dim) * 4;
@@ -615,7 +666,7 @@ Workspace plan_workspace(int64_t dim, int64_t group, const DeviceCtx& ctx) {
 
 template <typename T, int DP, int NT, bool kTilePage>
 cudaError_t attend(const AttendArgs& a, cudaStream_t stream, const DeviceCtx& ctx) {
-    using S = AttendShape<DP>;
+    using S = AttendShape<DP, NT>;
     static std::atomic<bool> ready[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -630,7 +681,7 @@ cudaError_t attend(const AttendArgs& a, cudaStream_t stream, const DeviceCtx& ct
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    const unsigned blocks = (unsigned)attend_blocks(DP, ctx);
+    const unsigned blocks = (unsigned)attend_blocks(DP, NT, ctx);
     cfg.gridDim = dim3(blocks);
     cfg.blockDim = dim3(kAttendThreads);
     cfg.dynamicSmemBytes = S::kSmem;
