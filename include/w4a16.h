@@ -357,7 +357,8 @@ int w4a16_gemm_ex_plan(int64_t M, int64_t N, int64_t K, int32_t group, int32_t z
  *
  * The conventions above hold, with these differences.  Tensors may be
  * strided where a stride is an argument (in elements, or in bytes where the
- * argument says so); the innermost dimension is always dense.  Integer
+ * argument says so); the innermost dimension is always dense, and the stride
+ * of a dimension of size 1 is not looked at.  Integer
  * tensors (int32) need 4-byte alignment only.  What an integer tensor holds
  * is device data that the call cannot see: kernels check every page and row
  * number against its range before they use it, and what each does with one

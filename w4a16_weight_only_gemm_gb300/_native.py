@@ -71,6 +71,8 @@ def library_path() -> str:
 def lib():
     """The loaded library (loaded once; raises if it has not been built)."""
     global _LIB
+    if _LIB is not None:
+        return _LIB
     with _LOCK:
         if _LIB is None:
             path = library_path()

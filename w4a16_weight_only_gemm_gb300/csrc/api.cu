@@ -59,30 +59,34 @@ bool good_nk(int64_t N, int64_t K) {
 }
 
 // The serving operators' shapes, within the ranges the header gives.
+bool good_stride(int64_t size, int64_t stride) {
+    return size == 1 || (stride >= 0 && stride % 8 == 0 && stride <= (int64_t)1 << 40);
+}
+
 bool good_cache(const w4a16_cache_shape& c) {
-    const auto stride = [](int64_t s) { return s >= 0 && s % 8 == 0 && s <= (int64_t)1 << 40; };
     return c.pages >= 1 && c.pages < (int64_t)1 << 31 && c.page_size >= 1 && c.page_size <= 65536 &&
            c.kv_heads >= 1 && c.kv_heads <= 1024 && c.head_dim >= 8 && c.head_dim <= 256 &&
            c.head_dim % 8 == 0 && (c.type == W4A16_F16 || c.type == W4A16_BF16) &&
-           stride(c.page_stride) && stride(c.slot_stride) && stride(c.head_stride) && c.batch >= 1 &&
-           c.batch <= 65535 && c.table_width >= 1 && c.table_width <= (int64_t)1 << 24 &&
-           c.table_width * c.page_size < (int64_t)1 << 31 && c.table_stride >= 0 &&
-           c.table_stride <= (int64_t)1 << 40;
+           good_stride(c.pages, c.page_stride) && good_stride(c.page_size, c.slot_stride) &&
+           good_stride(c.kv_heads, c.head_stride) && c.batch >= 1 && c.batch <= 65535 && c.table_width >= 1 && c.table_width <= (int64_t)1 << 24 &&
+           c.table_width * c.page_size < (int64_t)1 << 31 &&
+           (c.batch == 1 || (c.table_stride >= 0 && c.table_stride <= (int64_t)1 << 40));
 }
 
 bool good_books(const w4a16_books_shape& b) {
     return b.pages >= 1 && b.pages < (int64_t)1 << 31 && b.rows >= 1 && b.rows <= (int64_t)1 << 24 &&
            b.width >= 1 && b.width <= (int64_t)1 << 24 && b.rows * b.width <= (int64_t)1 << 40 &&
-           b.in_stride >= 0 && b.in_stride <= (int64_t)1 << 40 && b.out_stride >= b.width &&
-           b.out_stride <= (int64_t)1 << 40 && b.page_size >= 1 && b.page_size <= 65536 &&
+           (b.rows == 1 || (b.in_stride >= 0 && b.in_stride <= (int64_t)1 << 40 &&
+                            b.out_stride >= b.width && b.out_stride <= (int64_t)1 << 40)) &&
+           b.page_size >= 1 && b.page_size <= 65536 &&
            b.width * b.page_size < (int64_t)1 << 31;
 }
 
 bool good_pool(const w4a16_pool_shape& p) {
     const auto whole = [](int64_t s) { return s >= 0 && s % 16 == 0 && s <= (int64_t)1 << 42; };
-    return p.planes >= 1 && p.planes <= (int64_t)1 << 20 && whole(p.plane_stride) &&
-           whole(p.page_stride) && whole(p.page_bytes) && p.page_bytes >= 16 &&
-           p.page_bytes <= (int64_t)1 << 36;
+    return p.planes >= 1 && p.planes <= (int64_t)1 << 20 &&
+           (p.planes == 1 || whole(p.plane_stride)) && whole(p.page_stride) &&
+           whole(p.page_bytes) && p.page_bytes >= 16 && p.page_bytes <= (int64_t)1 << 36;
 }
 
 bool good_count(int64_t count) { return count >= 0 && count <= (int64_t)1 << 24; }
@@ -362,9 +366,10 @@ int w4a16_paged_append(const void* k, const void* v, void* k_pool, void* v_pool,
     if (!good_cache(*cache) || tokens < 0 || tokens > (int64_t)1 << 31 ||
         (!offsets && tokens != cache->batch))
         return W4A16_ERR_SHAPE;
-    for (int64_t s : {k_token_stride, k_head_stride, v_token_stride, v_head_stride})
-        if (s < 0 || s % 8 != 0 || s > (int64_t)1 << 40) return W4A16_ERR_SHAPE;
     if (tokens == 0) return W4A16_OK;
+    if (!good_stride(tokens, k_token_stride) || !good_stride(cache->kv_heads, k_head_stride) ||
+        !good_stride(tokens, v_token_stride) || !good_stride(cache->kv_heads, v_head_stride))
+        return W4A16_ERR_SHAPE;
     if (!k || !v || !k_pool || !v_pool || !tables || !starts) return W4A16_ERR_NULL;
     if (!aligned16(k) || !aligned16(v) || !aligned16(k_pool) || !aligned16(v_pool))
         return W4A16_ERR_ALIGN;
@@ -393,9 +398,11 @@ int w4a16_paged_attention(const void* q, const void* k_pool, const void* v_pool,
     if (!good_cache(*cache) || query->q_heads < 1 || query->q_heads > 1024 ||
         query->q_heads % cache->kv_heads != 0 || !(query->scale == query->scale))
         return W4A16_ERR_SHAPE;
-    for (int64_t s : {query->q_row_stride, query->q_head_stride, query->out_row_stride,
-                      query->out_head_stride})
-        if (s < 0 || s % 8 != 0 || s > (int64_t)1 << 40) return W4A16_ERR_SHAPE;
+    if (!good_stride(cache->batch, query->q_row_stride) ||
+        !good_stride(query->q_heads, query->q_head_stride) ||
+        !good_stride(cache->batch, query->out_row_stride) ||
+        !good_stride(query->q_heads, query->out_head_stride))
+        return W4A16_ERR_SHAPE;
     if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out) ||
         !aligned16(workspace))
         return W4A16_ERR_ALIGN;
@@ -494,7 +501,7 @@ int w4a16_token_logprobs(const void* logits, const void* tokens, float* logprob,
     if (!logits || !tokens || !logprob || !entropy || (top && (!top_ids || !top_logprobs)))
         return W4A16_ERR_NULL;
     if (rows < 1 || rows > (int64_t)1 << 24 || vocabulary < 1 || vocabulary > (int64_t)1 << 30 ||
-        row_stride < 0 || row_stride > (int64_t)1 << 40 || top < 0 || top > W4A16_MAX_TOP ||
+        (rows > 1 && (row_stride < 0 || row_stride > (int64_t)1 << 40)) || top < 0 || top > W4A16_MAX_TOP ||
         top > vocabulary || type < W4A16_F16 || type > W4A16_F32 || (wide != 0 && wide != 1))
         return W4A16_ERR_SHAPE;
     if (reinterpret_cast<uintptr_t>(logits) % (type == W4A16_F32 ? 4 : 2)) return W4A16_ERR_ALIGN;

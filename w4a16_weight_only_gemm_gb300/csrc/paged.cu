@@ -2,6 +2,7 @@
 // attention of one new token over them.
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <atomic>
 #include <type_traits>
 
@@ -578,45 +579,77 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
 }
 
 // Adds up an item's parts: block (x, y) has head y of the item that begins in
-// block x of attend_kernel.  Four groups of threads take the parts in turn.
-constexpr int kJoinGroups = 4;
+// block x of attend_kernel.  A row split over the whole GPU has some sixty
+// parts a head: a thread group's first eight are read before the weights are
+// settled, and no part waits for another.  (One part at a time with running
+// maxima in between took 13 us of a 131071-position call.)
+constexpr int kJoinThreads = 256;
+constexpr int kMaxParts = 1024;  // blocks of attend_kernel: num_sms * kBlocksPerSm at most
 template <typename T, int DP>
-__global__ void __launch_bounds__(DP / 4 * kJoinGroups) join_kernel(AttendArgs a, int heads_padded) {
-    __shared__ float4 part[kJoinGroups][DP / 4];
-    __shared__ float2 part_ml[kJoinGroups];
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs a, int heads_padded) {
+    constexpr int kGroups = kJoinThreads / (DP / 4);
+    __shared__ float weight[kMaxParts + 1];
+    __shared__ float4 part[kGroups][DP / 4];
+    __shared__ float2 warp_ml[kJoinThreads / 32];
     const int h = blockIdx.y, x = threadIdx.x % (DP / 4), group = threadIdx.x / (DP / 4);
     grid_dependency_wait();
     const Joint joint = a.joints[blockIdx.x];
     if (joint.count == 0 || h >= a.heads_of(joint.item)) return;
-    float m = -INFINITY, l = 0.f;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = group; i <= joint.count; i += kJoinGroups) {
-        const int64_t slot = ((int64_t)(blockIdx.x + i) * 2 + (i == 0)) * heads_padded + h;
-        const float2 ml = a.partial_ml[slot];
-        const float4 u = *reinterpret_cast<const float4*>(a.partial + slot * DP + 4 * x);
-        const float higher = fmaxf(m, ml.x), base = higher == -INFINITY ? 0.f : higher;
-        const float keep = exp2_fast(m - base), e = exp2_fast(ml.x - base);
-        m = higher;
-        l = l * keep + e * ml.y;
-        v.x = v.x * keep + e * u.x, v.y = v.y * keep + e * u.y;
-        v.z = v.z * keep + e * u.z, v.w = v.w * keep + e * u.w;
+    // part i: the first block's second slot, then the first slots of the blocks after it
+    const auto slot = [&](int i) {
+        return ((int64_t)(blockIdx.x + i) * 2 + (i == 0)) * heads_padded + h;
+    };
+    constexpr int kAhead = 8;
+    float4 u[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+        const int i = group + k * kGroups;
+        if (i <= joint.count)
+            u[k] = *reinterpret_cast<const float4*>(a.partial + slot(i) * DP + 4 * x);
     }
-    part[group][x] = v;
-    if (x == 0) part_ml[group] = make_float2(m, l);
+    float m = -INFINITY, l = 0.f;
+    for (int i = threadIdx.x; i <= joint.count; i += kJoinThreads) {
+        const float2 ml = a.partial_ml[slot(i)];
+        const float higher = fmaxf(m, ml.x), base = higher == -INFINITY ? 0.f : higher;
+        l = l * exp2_fast(m - base) + ml.y * exp2_fast(ml.x - base);
+        m = higher;
+        weight[i] = ml.x;
+    }
+    const float own = m;
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+    l *= exp2_fast(own - (m == -INFINITY ? 0.f : m));
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) l += __shfl_xor_sync(~0u, l, d);
+    if (threadIdx.x % 32 == 0) warp_ml[threadIdx.x / 32] = make_float2(m, l);
     __syncthreads();
-    if (group) return;
     m = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int i = 0; i < kJoinGroups; ++i) m = fmaxf(m, part_ml[i].x);
+    for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, warp_ml[w].x);
     const float base = m == -INFINITY ? 0.f : m;
-    v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < kJoinGroups; ++i) {
-        const float e = exp2_fast(part_ml[i].x - base);
+    for (int w = 0; w < kJoinThreads / 32; ++w) l += warp_ml[w].y * exp2_fast(warp_ml[w].x - base);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+        const int i = group + k * kGroups;
+        if (i > joint.count) break;
+        const float e = exp2_fast(weight[i] - base);
+        v.x += e * u[k].x, v.y += e * u[k].y, v.z += e * u[k].z, v.w += e * u[k].w;
+    }
+#pragma unroll 4
+    for (int i = group + kAhead * kGroups; i <= joint.count; i += kGroups) {
+        const float e = exp2_fast(weight[i] - base);
+        const float4 w = *reinterpret_cast<const float4*>(a.partial + slot(i) * DP + 4 * x);
+        v.x += e * w.x, v.y += e * w.y, v.z += e * w.z, v.w += e * w.w;
+    }
+    part[group][x] = v;
+    __syncthreads();
+    if (group) return;
+#pragma unroll
+    for (int i = 1; i < kGroups; ++i) {
         const float4 u = part[i][x];
-        l += e * part_ml[i].y;
-        v.x += e * u.x, v.y += e * u.y, v.z += e * u.z, v.w += e * u.w;
+        v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const int head = a.first_head(joint.item) + h;
@@ -646,7 +679,7 @@ int attend_blocks(int64_t dim, int tiles, const DeviceCtx& ctx) {
     const int per_sm[3][2] = {{AttendShape<64, 1>::kBlocksPerSm, AttendShape<64, 2>::kBlocksPerSm},
                               {AttendShape<128, 1>::kBlocksPerSm, AttendShape<128, 2>::kBlocksPerSm},
                               {AttendShape<256, 1>::kBlocksPerSm, AttendShape<256, 2>::kBlocksPerSm}};
-    return ctx.num_sms * per_sm[dim <= 64 ? 0 : dim <= 128 ? 1 : 2][tiles - 1];
+    return std::min(kMaxParts, ctx.num_sms * per_sm[dim <= 64 ? 0 : dim <= 128 ? 1 : 2][tiles - 1]);
 }
 
 // The workspace: partial outputs, their maxima and sums, the joints.
@@ -691,7 +724,7 @@ cudaError_t attend(const AttendArgs& a, cudaStream_t stream, const DeviceCtx& ct
     e = cudaLaunchKernelEx(&cfg, attend_kernel<T, DP, NT, kTilePage>, a);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(blocks, (unsigned)a.block_heads);
-    cfg.blockDim = dim3(DP / 4 * kJoinGroups);
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, join_kernel<T, DP>, a, 8 * NT);
 }

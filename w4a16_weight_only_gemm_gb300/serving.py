@@ -14,64 +14,95 @@ import struct
 import torch
 
 from . import _native
-from .ops import _call, _device_of, _stream_ptr
+from .ops import _call, _device_of, _raw_stream, _stream_ptr
 
 MAX_TOP = 32
 
 _TYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
-_CACHE_SHAPE = struct.Struct("11q")
-_QUERY_SHAPE = struct.Struct("5qd")
-_BOOKS_SHAPE = struct.Struct("6q")
-_POOL_SHAPE = struct.Struct("4q")
+_CACHE_SHAPE = struct.Struct("11q").pack
+_QUERY_SHAPE = struct.Struct("5qd").pack
+_BOOKS_SHAPE = struct.Struct("6q").pack
+_POOL_SHAPE = struct.Struct("4q").pack
+
+# A decode step makes these calls once a layer, and their kernels take a few
+# microseconds: each check below is one pass over plain attributes, and what
+# was wrong is looked for only when something was.
 
 
-def _empty(shape, dtype, dev, stream) -> torch.Tensor:
-    """A new tensor whose memory belongs to the stream the call runs on."""
+def _run(dev: int, stream, name: str, *args) -> None:
+    """Calls the library's entry point on device `dev` and the given or current stream."""
+    fn = getattr(_native.lib(), name)
+    if stream is None and _raw_stream is not None and dev == torch.cuda.current_device():
+        rc = fn(*args, _raw_stream(dev))
+    else:
+        device = torch.device("cuda", dev)
+        rc = _call(device, fn, *args, _stream_ptr(stream, device))
+    if rc:
+        _native.check(rc, name)
+
+
+def _empty(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
+    """A new tensor on `like`'s device whose memory belongs to the stream the call runs on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _device(stream, **named) -> int:
+    """The index of the one CUDA device of the named tensors (None passed over)."""
+    _device_of(stream, *named.items())
+    for name, t in named.items():
+        if t is not None and not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+    raise AssertionError("unreachable")
 
 
 def _ints(t: torch.Tensor, name: str, shape: tuple) -> None:
-    """A dense int32 CUDA tensor of `shape` (None: any size)."""
-    if t.dtype != torch.int32 or not t.is_cuda:
-        raise ValueError(f"{name} must be an int32 CUDA tensor, got {t.dtype} on {t.device}")
+    """Refuses what is not a dense int32 tensor of `shape` (None: any size)."""
+    if t.dtype is not torch.int32:
+        raise ValueError(f"{name} must be an int32 tensor, got {t.dtype}")
     if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must be dense in its last dimension")
 
 
-def _stride(t: torch.Tensor, dim: int) -> int:
-    return t.stride(dim) if t.shape[dim] > 1 else 0
+def _row(t: torch.Tensor, n: int, name: str) -> None:
+    """Refuses what is not a dense int32 tensor [n]."""
+    if t.dtype is not torch.int32 or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+        _ints(t, name, (n,))
 
 
-def _heads(t: torch.Tensor, name: str, dtype, shape: tuple) -> None:
-    """A CUDA tensor [rows, heads, head_dim], dense in its last dimension."""
-    if t.dtype != dtype or not t.is_cuda:
-        raise ValueError(f"{name} must be a {dtype} CUDA tensor, got {t.dtype} on {t.device}")
+def _heads(t: torch.Tensor, name: str, dtype, shape: tuple) -> tuple:
+    """The strides of a [rows, heads, head_dim] tensor, dense in its last dimension."""
+    strides = t.stride()
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be a {dtype} tensor, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.stride(2) != 1:
+    if strides[2] != 1:
         raise ValueError(f"{name} must be dense in its last dimension")
+    return strides
 
 
 def _cache_shape(k_pool: torch.Tensor, v_pool: torch.Tensor, tables: torch.Tensor) -> bytes:
     """The cache's geometry, packed for the library."""
-    shape, strides = k_pool.shape, k_pool.stride()
+    shape, strides, dtype = k_pool.shape, k_pool.stride(), k_pool.dtype
     if len(shape) != 4 or v_pool.shape != shape:
         raise ValueError("k_pool and v_pool must be [pages, page_size, kv_heads, head_dim], "
                          f"got {list(shape)} and {list(v_pool.shape)}")
-    if k_pool.dtype not in (torch.float16, torch.bfloat16) or v_pool.dtype != k_pool.dtype:
+    if v_pool.dtype is not dtype or dtype not in (torch.float16, torch.bfloat16):
         raise ValueError("k_pool and v_pool must be both float16 or both bfloat16, got "
-                         f"{k_pool.dtype} and {v_pool.dtype}")
-    if not k_pool.is_cuda or v_pool.stride() != strides or strides[3] != 1:
-        raise ValueError("k_pool and v_pool must be CUDA tensors of the same strides, dense in "
-                         "their last dimension")
-    _ints(tables, "tables", (None, None))
-    return _CACHE_SHAPE.pack(*shape, _TYPES[k_pool.dtype], _stride(k_pool, 0), _stride(k_pool, 1),
-                             _stride(k_pool, 2), *tables.shape, _stride(tables, 0))
+                         f"{dtype} and {v_pool.dtype}")
+    if v_pool.stride() != strides or strides[3] != 1:
+        raise ValueError("k_pool and v_pool must have the same strides, dense in their last "
+                         "dimension")
+    rows = tables.stride()
+    if tables.dtype is not torch.int32 or len(rows) != 2 or rows[1] != 1:
+        _ints(tables, "tables", (None, None))
+    return _CACHE_SHAPE(*shape, _TYPES[dtype], strides[0], strides[1], strides[2], *tables.shape,
+                        rows[0])
 
 
 def paged_append(k: torch.Tensor, v: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
@@ -86,28 +117,31 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, k_pool: torch.Tensor, v_pool:
     go to positions starts[b], starts[b] + 1, ...  Tokens without a valid page
     are left out."""
     cache = _cache_shape(k_pool, v_pool, tables)
-    rows, tokens = tables.shape[0], k.shape[0]
+    rows, tokens, dtype = tables.shape[0], k.shape[0], k_pool.dtype
     heads = (tokens, k_pool.shape[2], k_pool.shape[3])
-    _heads(k, "k", k_pool.dtype, heads)
-    _heads(v, "v", k_pool.dtype, heads)
-    _ints(starts, "starts", (rows,))
+    ks, vs = _heads(k, "k", dtype, heads), _heads(v, "v", dtype, heads)
+    _row(starts, rows, "starts")
+    dev = k.get_device()
+    if (dev < 0 or v.get_device() != dev or k_pool.get_device() != dev
+            or v_pool.get_device() != dev or tables.get_device() != dev
+            or starts.get_device() != dev or offsets is not None and offsets.get_device() != dev
+            or stream is not None and stream.device.index != dev):
+        _device(stream, k=k, v=v, k_pool=k_pool, v_pool=v_pool, tables=tables, starts=starts,
+                offsets=offsets)
     if offsets is not None:
-        _ints(offsets, "offsets", (rows + 1,))
-    dev = _device_of(stream, ("k", k), ("v", v), ("k_pool", k_pool), ("v_pool", v_pool),
-                     ("tables", tables), ("starts", starts), ("offsets", offsets))
+        _row(offsets, rows + 1, "offsets")
+        offsets = offsets.data_ptr()
     if not rows:
         return
-    rc = _call(dev, _native.lib().w4a16_paged_append, k.data_ptr(), v.data_ptr(),
-               k_pool.data_ptr(), v_pool.data_ptr(), tables.data_ptr(), starts.data_ptr(),
-               offsets.data_ptr() if offsets is not None else None, cache, tokens, _stride(k, 0),
-               _stride(k, 1), _stride(v, 0), _stride(v, 1), _stream_ptr(stream, dev))
-    if rc:
-        _native.check(rc, "w4a16_paged_append")
+    _run(dev, stream, "w4a16_paged_append", k.data_ptr(), v.data_ptr(), k_pool.data_ptr(),
+         v_pool.data_ptr(), tables.data_ptr(), starts.data_ptr(), offsets, cache, tokens, ks[0],
+         ks[1], vs[0], vs[1])
 
 
 @functools.lru_cache(maxsize=1024)
-def _attention_workspace(cache: bytes, q_heads: int, device: int | None) -> int:
-    n = _native.lib().w4a16_paged_attention_workspace(cache, q_heads)
+def _attention_workspace(cache: bytes, q_heads: int, dev: int) -> int:
+    with torch.cuda.device(dev):
+        n = _native.lib().w4a16_paged_attention_workspace(cache, q_heads)
     if n < 0:
         _native.check(2, "w4a16_paged_attention_workspace")
     return n
@@ -123,74 +157,85 @@ def paged_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
     length 0), and with return_lse also the logarithm of each head's sum of
     exponentials, fp32 [rows, q_heads] (-inf for a row of length 0)."""
     cache = _cache_shape(k_pool, v_pool, tables)
-    if q.dim() != 3:
-        raise ValueError(f"q must be [rows, q_heads, head_dim], got {list(q.shape)}")
-    rows, q_heads, dim = tables.shape[0], q.shape[1], k_pool.shape[3]
-    _heads(q, "q", k_pool.dtype, (rows, q_heads, dim))
-    _ints(lengths, "lengths", (rows,))
-    dev = _device_of(stream, ("q", q), ("k_pool", k_pool), ("v_pool", v_pool), ("tables", tables),
-                     ("lengths", lengths), ("out", out))
+    shape, dtype = q.shape, k_pool.dtype
+    if len(shape) != 3:
+        raise ValueError(f"q must be [rows, q_heads, head_dim], got {list(shape)}")
+    rows, q_heads, dim = tables.shape[0], shape[1], k_pool.shape[3]
+    qs = _heads(q, "q", dtype, (rows, q_heads, dim))
+    _row(lengths, rows, "lengths")
+    dev = q.get_device()
+    if (dev < 0 or k_pool.get_device() != dev or v_pool.get_device() != dev
+            or tables.get_device() != dev or lengths.get_device() != dev
+            or out is not None and out.get_device() != dev
+            or stream is not None and stream.device.index != dev):
+        _device(stream, q=q, k_pool=k_pool, v_pool=v_pool, tables=tables, lengths=lengths, out=out)
     if out is None:
-        out = _empty((rows, q_heads, dim), q.dtype, dev, stream)
-    else:
-        _heads(out, "out", q.dtype, (rows, q_heads, dim))
-    lse = _empty((rows, q_heads), torch.float32, dev, stream) if return_lse else None
-    if not rows:
-        return (out, lse) if return_lse else out
-    size = _call(dev, _attention_workspace, cache, q_heads, dev.index)
-    workspace = _empty(size, torch.uint8, dev, stream)
-    query = _QUERY_SHAPE.pack(q_heads, _stride(q, 0), _stride(q, 1), _stride(out, 0),
-                              _stride(out, 1), dim ** -0.5 if scale is None else scale)
-    rc = _call(dev, _native.lib().w4a16_paged_attention, q.data_ptr(), k_pool.data_ptr(),
-               v_pool.data_ptr(), tables.data_ptr(), lengths.data_ptr(), out.data_ptr(),
-               lse.data_ptr() if return_lse else None, workspace.data_ptr(), cache, query,
-               _stream_ptr(stream, dev))
-    if rc:
-        _native.check(rc, "w4a16_paged_attention")
+        out = _empty(q, shape, dtype, stream)
+    os = _heads(out, "out", dtype, shape)
+    lse = _empty(q, (rows, q_heads), torch.float32, stream) if return_lse else None
+    if rows:
+        workspace = _empty(q, _attention_workspace(cache, q_heads, dev), torch.uint8, stream)
+        _run(dev, stream, "w4a16_paged_attention", q.data_ptr(), k_pool.data_ptr(),
+             v_pool.data_ptr(), tables.data_ptr(), lengths.data_ptr(), out.data_ptr(),
+             lse.data_ptr() if return_lse else None, workspace.data_ptr(), cache,
+             _QUERY_SHAPE(q_heads, qs[0], qs[1], os[0], os[1],
+                          dim ** -0.5 if scale is None else scale))
     return (out, lse) if return_lse else out
 
 
-def _books(refs, tables, lengths, out, page_size: int, stream):
-    """The checked books, their outputs (new ones, or `out`) and the packed shape."""
-    _ints(refs, "refs", (None,))
-    _ints(tables, "tables", (None, None))
+def _books(refs, tables, lengths, out, page_size: int, stream, **others):
+    """The books' device, their addresses, their outputs (new ones, or `out`), the outputs'
+    addresses and the packed shape; the tensors in `others` share the device."""
+    pages, shape, strides = refs.shape[0], tables.shape, tables.stride()
+    _row(refs, pages, "refs")
+    if tables.dtype is not torch.int32 or len(strides) != 2 or strides[1] != 1:
+        _ints(tables, "tables", (None, None))
+    ins = (refs, tables)
     if lengths is not None:
-        _ints(lengths, "lengths", (tables.shape[0],))
-    ins = (refs, tables) if lengths is None else (refs, tables, lengths)
+        _row(lengths, shape[0], "lengths")
+        ins = (refs, tables, lengths)
     if out is None:
-        outs = tuple(_empty(t.shape, torch.int32, refs.device, stream) for t in ins)
+        outs = [_empty(refs, t.shape, torch.int32, stream) for t in ins]
     else:
-        outs = tuple(out)
+        outs = list(out)
         if len(outs) != len(ins):
             raise ValueError(f"out must be {len(ins)} tensors")
         for t, o in zip(ins, outs):
             _ints(o, "out", tuple(t.shape))
             if o.data_ptr() == t.data_ptr() and o.stride() != t.stride():
                 raise ValueError("an out tensor that is its input must have its strides")
-    rows, width = tables.shape
-    shape = _BOOKS_SHAPE.pack(refs.shape[0], rows, width, _stride(tables, 0),
-                              outs[1].stride(0) if rows > 1 else width, page_size)
-    return ins, outs, shape
+    dev = refs.get_device()
+    if (dev < 0 or stream is not None and stream.device.index != dev
+            or any(t.get_device() != dev for t in (*ins, *outs, *others.values()))):
+        _device(stream, refs=refs, tables=tables, lengths=lengths, **others,
+                **{f"out[{i}]": o for i, o in enumerate(outs)})
+    rows, width = shape
+    row = outs[1].stride(0) if rows > 1 else width
+    return (dev, [t.data_ptr() for t in ins], outs, [t.data_ptr() for t in outs],
+            _BOOKS_SHAPE(pages, rows, width, strides[0], row, page_size))
 
 
 def _pool_shape(pool: torch.Tensor, pages: int | None) -> bytes:
     """`pool` [planes, pages, ...] with dense pages, packed for the library."""
-    if not pool.is_cuda or pool.dim() < 3:
-        raise ValueError("pool must be a CUDA tensor [planes, pages, ...]")
-    if pages is not None and pool.shape[1] != pages:
-        raise ValueError(f"pool has {pool.shape[1]} pages, the books {pages}")
-    if not pool[0, 0].is_contiguous():
-        raise ValueError("pool must be dense within a page")
-    size = pool.element_size()
-    return _POOL_SHAPE.pack(pool.shape[0], _stride(pool, 0) * size, _stride(pool, 1) * size,
-                            pool[0, 0].numel() * size)
+    shape, strides, size = pool.shape, pool.stride(), pool.element_size()
+    if len(shape) < 3:
+        raise ValueError(f"pool must be [planes, pages, ...], got {list(shape)}")
+    if pages is not None and shape[1] != pages:
+        raise ValueError(f"pool has {shape[1]} pages, the books {pages}")
+    page = size
+    for n, s in zip(shape[:1:-1], strides[:1:-1]):
+        if n > 1 and s * size != page:
+            raise ValueError("pool must be dense within a page")
+        page *= n
+    return _POOL_SHAPE(shape[0], strides[0] * size, strides[1] * size, page)
 
 
-def _space(books: bytes, count: int, dev, stream) -> torch.Tensor:
+@functools.lru_cache(maxsize=1024)
+def _pages_workspace(books: bytes, count: int) -> int:
     n = _native.lib().w4a16_pages_workspace(books, count)
     if n < 0:
         _native.check(2, "w4a16_pages_workspace")
-    return _empty(n, torch.uint8, dev, stream)
+    return n
 
 
 def pages_free(refs: torch.Tensor, tables: torch.Tensor, lengths: torch.Tensor,
@@ -198,15 +243,11 @@ def pages_free(refs: torch.Tensor, tables: torch.Tensor, lengths: torch.Tensor,
     """Gives back the pages of the listed rows (int32): one holder fewer in
     refs [pages], page numbers -1 in tables [rows, width], length 0.  Returns
     (refs, tables, lengths), new tensors or `out` (which may be the inputs)."""
-    ins, outs, shape = _books(refs, tables, lengths, out, 1, stream)
-    _ints(rows, "rows", (None,))
-    dev = _device_of(stream, ("refs", refs), ("tables", tables), ("lengths", lengths),
-                     ("rows", rows), *(("out", o) for o in outs))
-    rc = _call(dev, _native.lib().w4a16_pages_free, *(t.data_ptr() for t in ins), rows.data_ptr(),
-               rows.shape[0], *(t.data_ptr() for t in outs), shape, _stream_ptr(stream, dev))
-    if rc:
-        _native.check(rc, "w4a16_pages_free")
-    return outs
+    count = rows.shape[0]
+    _row(rows, count, "rows")
+    dev, ins, outs, to, shape = _books(refs, tables, lengths, out, 1, stream, rows=rows)
+    _run(dev, stream, "w4a16_pages_free", *ins, rows.data_ptr(), count, *to, shape)
+    return tuple(outs)
 
 
 def pages_extend(refs: torch.Tensor, tables: torch.Tensor, lengths: torch.Tensor,
@@ -215,18 +256,15 @@ def pages_extend(refs: torch.Tensor, tables: torch.Tensor, lengths: torch.Tensor
     pages it then needs, in the order of the list.  Returns (refs, tables,
     lengths, done); done[i] = 0 where the row is left as it was: too few free
     pages, a row too long, out of range or listed before."""
-    ins, outs, shape = _books(refs, tables, lengths, out, page_size, stream)
-    _ints(rows, "rows", (None,))
-    _ints(counts, "counts", (rows.shape[0],))
-    dev = _device_of(stream, ("refs", refs), ("tables", tables), ("lengths", lengths),
-                     ("rows", rows), ("counts", counts), *(("out", o) for o in outs))
-    done = _empty(rows.shape, torch.int32, dev, stream)
-    space = _space(shape, rows.shape[0], dev, stream)
-    rc = _call(dev, _native.lib().w4a16_pages_extend, *(t.data_ptr() for t in ins),
-               rows.data_ptr(), counts.data_ptr(), rows.shape[0], *(t.data_ptr() for t in outs),
-               done.data_ptr(), space.data_ptr(), shape, _stream_ptr(stream, dev))
-    if rc:
-        _native.check(rc, "w4a16_pages_extend")
+    count = rows.shape[0]
+    _row(rows, count, "rows")
+    _row(counts, count, "counts")
+    dev, ins, outs, to, shape = _books(refs, tables, lengths, out, page_size, stream, rows=rows,
+                                       counts=counts)
+    done = _empty(refs, count, torch.int32, stream)
+    space = _empty(refs, _pages_workspace(shape, count), torch.uint8, stream)
+    _run(dev, stream, "w4a16_pages_extend", *ins, rows.data_ptr(), counts.data_ptr(), count, *to,
+         done.data_ptr(), space.data_ptr(), shape)
     return *outs, done
 
 
@@ -238,21 +276,15 @@ def pages_fork(pool: torch.Tensor, refs: torch.Tensor, tables: torch.Tensor,
     [planes, pages, ...] to the lowest free page.  Returns (refs, tables,
     lengths, done); done[i] = 0 where the child is left as it was: too few free
     pages, a child not empty, a row out of range or a child listed before."""
-    ins, outs, shape = _books(refs, tables, lengths, out, page_size, stream)
-    planes = _pool_shape(pool, refs.shape[0])
-    _ints(parents, "parents", (None,))
-    _ints(children, "children", (parents.shape[0],))
-    dev = _device_of(stream, ("pool", pool), ("refs", refs), ("tables", tables),
-                     ("lengths", lengths), ("parents", parents), ("children", children),
-                     *(("out", o) for o in outs))
-    done = _empty(parents.shape, torch.int32, dev, stream)
-    space = _space(shape, parents.shape[0], dev, stream)
-    rc = _call(dev, _native.lib().w4a16_pages_fork, pool.data_ptr(),
-               *(t.data_ptr() for t in ins), parents.data_ptr(), children.data_ptr(),
-               parents.shape[0], *(t.data_ptr() for t in outs), done.data_ptr(), space.data_ptr(),
-               shape, planes, _stream_ptr(stream, dev))
-    if rc:
-        _native.check(rc, "w4a16_pages_fork")
+    planes, count = _pool_shape(pool, refs.shape[0]), parents.shape[0]
+    _row(parents, count, "parents")
+    _row(children, count, "children")
+    dev, ins, outs, to, shape = _books(refs, tables, lengths, out, page_size, stream, pool=pool,
+                                       parents=parents, children=children)
+    done = _empty(refs, count, torch.int32, stream)
+    space = _empty(refs, _pages_workspace(shape, count), torch.uint8, stream)
+    _run(dev, stream, "w4a16_pages_fork", pool.data_ptr(), *ins, parents.data_ptr(),
+         children.data_ptr(), count, *to, done.data_ptr(), space.data_ptr(), shape, planes)
     return *outs, done
 
 
@@ -261,17 +293,12 @@ def pages_compact(pool: torch.Tensor, refs: torch.Tensor, tables: torch.Tensor, 
     """Moves the n held pages to the numbers below n: those at n and above go,
     in ascending order, to the free ones below, in every plane of pool
     [planes, pages, ...].  Returns (refs, tables, used) with used = [n]."""
-    ins, outs, shape = _books(refs, tables, None, out, 1, stream)
     planes = _pool_shape(pool, refs.shape[0])
-    dev = _device_of(stream, ("pool", pool), ("refs", refs), ("tables", tables),
-                     *(("out", o) for o in outs))
-    used = _empty((1,), torch.int32, dev, stream)
-    space = _space(shape, 0, dev, stream)
-    rc = _call(dev, _native.lib().w4a16_pages_compact, pool.data_ptr(),
-               *(t.data_ptr() for t in ins), *(t.data_ptr() for t in outs), used.data_ptr(),
-               space.data_ptr(), shape, planes, _stream_ptr(stream, dev))
-    if rc:
-        _native.check(rc, "w4a16_pages_compact")
+    dev, ins, outs, to, shape = _books(refs, tables, None, out, 1, stream, pool=pool)
+    used = _empty(refs, 1, torch.int32, stream)
+    space = _empty(refs, _pages_workspace(shape, 0), torch.uint8, stream)
+    _run(dev, stream, "w4a16_pages_compact", pool.data_ptr(), *ins, *to, used.data_ptr(),
+         space.data_ptr(), shape, planes)
     return *outs, used
 
 
@@ -279,15 +306,14 @@ def pages_copy(pool: torch.Tensor, sources: torch.Tensor, targets: torch.Tensor,
                stream=None) -> None:
     """Copies page sources[i] to page targets[i] (int32) in every plane of pool
     [planes, pages, ...]; pairs out of range are passed over."""
-    planes = _pool_shape(pool, None)
-    _ints(sources, "sources", (None,))
-    _ints(targets, "targets", (sources.shape[0],))
-    dev = _device_of(stream, ("pool", pool), ("sources", sources), ("targets", targets))
-    rc = _call(dev, _native.lib().w4a16_pages_copy, pool.data_ptr(), sources.data_ptr(),
-               targets.data_ptr(), sources.shape[0], pool.shape[1], planes,
-               _stream_ptr(stream, dev))
-    if rc:
-        _native.check(rc, "w4a16_pages_copy")
+    planes, count, dev = _pool_shape(pool, None), sources.shape[0], pool.get_device()
+    _row(sources, count, "sources")
+    _row(targets, count, "targets")
+    if (dev < 0 or sources.get_device() != dev or targets.get_device() != dev
+            or stream is not None and stream.device.index != dev):
+        _device(stream, pool=pool, sources=sources, targets=targets)
+    _run(dev, stream, "w4a16_pages_copy", pool.data_ptr(), sources.data_ptr(), targets.data_ptr(),
+         count, pool.shape[1], planes)
 
 
 def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0, stream=None):
@@ -297,30 +323,31 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0, str
     fp32 [rows, top]; the `top` (at most 32) largest logits come first, of equal
     ones the lowest index.  -inf masks a logit; a token outside the vocabulary
     has the log probability NaN."""
-    if logits.dim() != 2 or logits.dtype not in _TYPES or not logits.is_cuda:
-        raise ValueError("logits must be a float16, bfloat16 or float32 CUDA tensor "
+    strides, kind = logits.stride(), _TYPES.get(logits.dtype)
+    if kind is None or len(strides) != 2:
+        raise ValueError("logits must be a float16, bfloat16 or float32 tensor "
                          f"[rows, vocabulary], got {logits.dtype} {list(logits.shape)}")
     rows, vocabulary = logits.shape
-    if vocabulary > 1 and logits.stride(1) != 1:
+    if strides[1] != 1 and vocabulary > 1:
         raise ValueError("logits must be dense in their last dimension")
-    if tokens.dtype not in (torch.int64, torch.int32) or tokens.shape != (rows,) \
-            or not tokens.is_contiguous():
+    wide = tokens.dtype is torch.int64
+    if (not wide and tokens.dtype is not torch.int32 or tokens.shape != (rows,)
+            or not tokens.is_contiguous()):
         raise ValueError(f"tokens must be a dense int64 or int32 tensor [{rows}]")
-    if not 0 <= top <= min(MAX_TOP, vocabulary):
+    if not 0 <= top <= MAX_TOP or top > vocabulary:
         raise ValueError(f"top must be 0 .. {min(MAX_TOP, vocabulary)}, got {top}")
-    dev = _device_of(stream, ("logits", logits), ("tokens", tokens))
-    logprobs = _empty(rows, torch.float32, dev, stream)
-    entropies = _empty(rows, torch.float32, dev, stream)
-    ids = _empty((rows, top), torch.int32, dev, stream)
-    likeliest = _empty((rows, top), torch.float32, dev, stream)
+    dev = logits.get_device()
+    if (dev < 0 or tokens.get_device() != dev
+            or stream is not None and stream.device.index != dev):
+        _device(stream, logits=logits, tokens=tokens)
+    logprobs = _empty(logits, rows, torch.float32, stream)
+    entropies = _empty(logits, rows, torch.float32, stream)
+    ids = _empty(logits, (rows, top), torch.int32, stream)
+    likeliest = _empty(logits, (rows, top), torch.float32, stream)
     if rows:
-        rc = _call(dev, _native.lib().w4a16_token_logprobs, logits.data_ptr(), tokens.data_ptr(),
-                   logprobs.data_ptr(), entropies.data_ptr(), ids.data_ptr(),
-                   likeliest.data_ptr(), rows, vocabulary, _stride(logits, 0),
-                   _TYPES[logits.dtype], tokens.dtype == torch.int64, top,
-                   _stream_ptr(stream, dev))
-        if rc:
-            _native.check(rc, "w4a16_token_logprobs")
+        _run(dev, stream, "w4a16_token_logprobs", logits.data_ptr(), tokens.data_ptr(),
+             logprobs.data_ptr(), entropies.data_ptr(), ids.data_ptr(), likeliest.data_ptr(), rows,
+             vocabulary, strides[0], kind, wide, top)
     return logprobs, entropies, ids, likeliest
 
 
