@@ -1,6 +1,30 @@
 // logprobs.cu -- the scores of given tokens under rows of logits: log
 // probability, entropy and the likeliest alternatives.
+//
+// With m the row's maximum, s = sum e^(x - m) and t = sum e^(x - m) (x - m):
+//   logprob = x[token] - m - ln s,   entropy = ln s - t / s,
+// so one pass over the logits gives everything but the alternatives.  Each
+// thread keeps (m, s, t) of its own 16-byte pieces and takes a new maximum
+// once a batch of them; parts with other maxima are added up as
+//   s = sum s_i e^(m_i - m),   t = sum e^(m_i - m) (t_i + s_i (m_i - m)).
+//
+// The alternatives come from the maxima that the pass leaves anyway.  The
+// k-th largest of the maxima of 64 groups of threads is at most the k-th
+// largest logit, and few logits are above it (k = 20: 24 of 128256 independent
+// ones); only the threads whose maximum reaches it read their pieces again,
+// from L2, and the few logits found are ranked by counting.  Where they are
+// not few (masks leave fewer than k logits, so the cut is the mask's value),
+// those above the cut are kept and the lowest indices at it added in order.
+//
+// Bound by HBM for many rows: about seven instructions and one exponential a
+// logit are 0.6 and 0.7 of the time its two bytes take.  A row is a block's,
+// or, for few rows, a cluster's, whose first block joins the others' sums and
+// alternatives through shared memory: no workspace, one launch.
 #include <cuda_bf16.h>
+
+#include <stddef.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -8,12 +32,14 @@
 namespace w4a16 {
 namespace {
 
-constexpr int kScoreThreads = 512;
+constexpr int kScoreThreads = 256;
 constexpr int kScoreWarps = kScoreThreads / 32;
-
-__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
-__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_float(float v) { return v; }
+constexpr int kScoreBlocksPerSm = 5;
+constexpr int kGroups = kScoreThreads / 4;  // of threads, for the first cut of the alternatives
+constexpr int kBatch = 4;                   // 16-byte pieces a thread has in flight
+constexpr int kCandidates = 1024;
+constexpr int kMaxCluster = 8;
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct ScoreArgs {
     const void *logits, *tokens;
@@ -23,80 +49,409 @@ struct ScoreArgs {
     int wide, top;
 };
 
-// Whole numbers in the order of the values, NaN above all, -0 equal to 0, and
-// of equal values the lower index above the higher.
-__device__ __forceinline__ uint64_t rank_of(float x, int index) {
-    int bits = __float_as_int(x + 0.f);
-    if (x != x) bits = 0x7FFFFFFF;
-    const uint32_t ordered = (uint32_t)(bits ^ ((bits >> 31) & 0x7FFFFFFF)) ^ 0x80000000u;
-    return ((uint64_t)ordered << 32) | (uint32_t)~index;
+__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_float(float v) { return v; }
+
+// The larger, NaN if one is: of a word's values at once.
+__device__ __forceinline__ uint32_t max_words(uint32_t a, uint32_t b, __half) {
+    uint32_t r;
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t max_words(uint32_t a, uint32_t b, __nv_bfloat16) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t max_words(uint32_t a, uint32_t b, float) {
+    return __float_as_uint(max_nan(__uint_as_float(a), __uint_as_float(b)));
 }
 
-__device__ uint64_t block_max(uint64_t v, uint64_t* shared) {
-#pragma unroll
-    for (int d = 16; d > 0; d /= 2) v = max(v, __shfl_xor_sync(~0u, v, d));
-    if (threadIdx.x % 32 == 0) shared[threadIdx.x / 32] = v;
-    __syncthreads();
-    v = shared[threadIdx.x % kScoreWarps];
-#pragma unroll
-    for (int d = 16; d > 0; d /= 2) v = max(v, __shfl_xor_sync(~0u, v, d));
-    __syncthreads();
-    return v;
+// A 32-bit word's values.
+__device__ __forceinline__ void word_values(uint32_t w, float (&v)[2], __half) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    v[0] = f.x, v[1] = f.y;
+}
+__device__ __forceinline__ void word_values(uint32_t w, float (&v)[2], __nv_bfloat16) {
+    v[0] = __uint_as_float(w << 16), v[1] = __uint_as_float(w & 0xFFFF0000u);
+}
+__device__ __forceinline__ void word_values(uint32_t w, float (&v)[1], float) {
+    v[0] = __uint_as_float(w);
 }
 
-__device__ float block_sum(float v, float* shared) {
-#pragma unroll
-    for (int d = 16; d > 0; d /= 2) v += __shfl_xor_sync(~0u, v, d);
-    if (threadIdx.x % 32 == 0) shared[threadIdx.x / 32] = v;
-    __syncthreads();
-    v = 0.f;
-    for (int i = 0; i < kScoreWarps; ++i) v += shared[i];
-    __syncthreads();
-    return v;
-}
-
-// One block a row: the maximum, the two sums under it, then one sweep for each alternative.
 template <typename T>
-__global__ void __launch_bounds__(kScoreThreads) score_kernel(ScoreArgs a) {
-    __shared__ uint64_t shared_rank[kScoreWarps];
-    __shared__ float shared_sum[kScoreWarps];
-    const int64_t row = blockIdx.x;
+__device__ __forceinline__ uint32_t lowest_word() {  // -infinity
+    return sizeof(T) == 4 ? 0xFF800000u : std::is_same<T, __half>::value ? 0xFC00FC00u : 0xFF80FF80u;
+}
+
+__device__ __forceinline__ float exp_fast(float x) {  // x <= 0
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * kLog2e));
+    return y;
+}
+
+// Whole numbers in the order of the values, NaN above all, -0 equal to 0; none is 0.
+__device__ __forceinline__ uint32_t key_of(float x) {
+    const int bits = __float_as_int(x + 0.f);
+    const uint32_t key = (uint32_t)(bits ^ ((bits >> 31) & 0x7FFFFFFF)) ^ 0x80000000u;
+    return x != x ? 0xFFFFFFFFu : key;
+}
+__device__ __forceinline__ float value_of(uint32_t key) {
+    const int bits = (int)(key ^ 0x80000000u);
+    return __int_as_float(bits ^ ((bits >> 31) & 0x7FFFFFFF));  // all ones gives a NaN
+}
+// The same with the index: of equal values the lower index first.
+__device__ __forceinline__ uint64_t rank_of(uint32_t key, int index) {
+    return (uint64_t)key << 32 | (uint32_t)~index;
+}
+
+// Part of a row's sums.  worst: the key of a NaN or +infinity seen, else 0.
+struct Sums {
+    float m, s, t;
+    uint32_t worst;
+};
+
+__device__ __forceinline__ Sums add(const Sums& a, const Sums& b) {
+    Sums r;
+    r.m = fmaxf(a.m, b.m);
+    r.worst = max(a.worst, b.worst);
+    const float da = a.m == -INFINITY ? 0.f : a.m - r.m, db = b.m == -INFINITY ? 0.f : b.m - r.m;
+    const float ea = exp_fast(da), eb = exp_fast(db);  // s = t = 0 where m is -infinity
+    // far below, e is 0 and e * d is not to be 0 * infinity
+    r.s = a.s * ea + b.s * eb;
+    r.t = (ea > 0.f ? ea * (a.t + a.s * da) : 0.f) + (eb > 0.f ? eb * (b.t + b.s * db) : 0.f);
+    return r;
+}
+
+struct ScoreShared {
+    Sums part[kScoreWarps];
+    Sums sums;                      // of the block
+    uint32_t group_key[kGroups];
+    uint32_t cut;
+    int listed, found;
+    uint16_t list[kScoreThreads];   // threads whose maximum reaches the cut
+    uint64_t best[W4A16_MAX_TOP];   // the block's alternatives, in order
+    int bests;
+    uint64_t candidate[kCandidates];
+    uint64_t warp_best[kScoreWarps];
+    int equal[kScoreWarps];
+};
+
+__device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t addr) {
+    uint64_t v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kScoreThreads, kScoreBlocksPerSm)
+    score_kernel(ScoreArgs a, int blocks) {
+    constexpr int kPer = 16 / sizeof(T), kWord = 4 / sizeof(T);
+    __shared__ ScoreShared sh;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int64_t row = blockIdx.x / blocks;
+    const int rank = (int)(blockIdx.x % blocks);
     const T* x = static_cast<const T*>(a.logits) + row * a.row_stride;
     const int n = (int)a.vocabulary;
-    uint64_t best = 0;
-    for (int i = threadIdx.x; i < n; i += kScoreThreads) best = max(best, rank_of(to_float(x[i]), i));
-    best = block_max(best, shared_rank);
-    const float m = to_float(x[(int)~(uint32_t)best]);
-    const bool nothing = m == -INFINITY;
-    float s = 0.f, t = 0.f;
-    for (int i = threadIdx.x; i < n && !nothing; i += kScoreThreads) {
-        const float d = to_float(x[i]) - m, e = expf(d);
-        s += e;
-        t += e > 0.f ? e * d : (e == 0.f ? 0.f : e);
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    // The row: values before the first 16-byte boundary, pieces, values after the last.
+    const int head = min(n, (int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) % 16 / sizeof(T)));
+    const int pieces = (n - head) / kPer;
+    const int loose = rank == 0 ? n - pieces * kPer : 0;  // < 2 * kPer, one a thread
+    const int loose_at = tid < head ? tid : tid + pieces * kPer;
+    const int first = (int)((int64_t)pieces * rank / blocks);
+    const int count = (int)((int64_t)pieces * (rank + 1) / blocks) - first;
+    const uint4* piece = reinterpret_cast<const uint4*>(x + head) + first;
+
+    int64_t token = -1;
+    float token_logit = 0.f;
+    if (rank == 0 && tid == 0) {
+        token = a.wide ? static_cast<const int64_t*>(a.tokens)[row]
+                       : static_cast<const int32_t*>(a.tokens)[row];
+        if (token >= 0 && token < n) token_logit = to_float(x[token]);
+        sh.listed = sh.found = 0;
+    } else if (tid == 0) {
+        sh.listed = sh.found = 0;
     }
-    s = block_sum(s, shared_sum);
-    t = block_sum(t, shared_sum);
-    const float ln = logf(s);
-    if (threadIdx.x == 0) {
-        const int64_t token = a.wide ? static_cast<const int64_t*>(a.tokens)[row]
-                                     : static_cast<const int32_t*>(a.tokens)[row];
-        const bool inside = token >= 0 && token < n;
-        a.logprob[row] = !inside ? NAN : nothing ? -INFINITY : to_float(x[token]) - m - ln;
-        a.entropy[row] = nothing ? 0.f : ln - t / s;
+
+    Sums own{-INFINITY, 0.f, 0.f, 0u};
+    const bool some = tid < loose || tid < count;
+    if (tid < loose) {
+        const float v = to_float(x[loose_at]);
+        if (!(v < INFINITY))
+            own.worst = key_of(v);
+        else if (v > -INFINITY)
+            own = {v, 1.f, 0.f, 0u};
     }
-    for (int k = 0; k < a.top; ++k) {
-        if (threadIdx.x == 0) {
-            const int id = (int)~(uint32_t)best;
-            a.top_ids[row * a.top + k] = id;
-            a.top_logprobs[row * a.top + k] = nothing ? -INFINITY : to_float(x[id]) - m - ln;
+    for (int j = tid; j < count; j += kBatch * kScoreThreads) {
+        uint4 v[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int at = j + b * kScoreThreads;
+            v[b] = make_uint4(lowest_word<T>(), lowest_word<T>(), lowest_word<T>(), lowest_word<T>());
+            if (at < count) v[b] = __ldg(piece + at);
         }
-        uint64_t next = 0;
-        for (int i = threadIdx.x; i < n; i += kScoreThreads) {
-            const uint64_t r = rank_of(to_float(x[i]), i);
-            if (r < best) next = max(next, r);
+        uint32_t top = v[0].x;
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            top = max_words(top, v[b].x, T());
+            top = max_words(top, v[b].y, T());
+            top = max_words(top, v[b].z, T());
+            top = max_words(top, v[b].w, T());
         }
-        best = block_max(next, shared_rank);
+        float f[kWord];
+        word_values(top, f, T());
+        const float higher = kWord == 2 ? max_nan(f[0], f[kWord - 1]) : f[0];
+        if (!(higher <= own.m)) {  // a new maximum, or no number
+            if (higher < INFINITY) {
+                const float d = own.m - higher;  // -infinity at first, with s = t = 0
+                const float e = exp_fast(d);
+                own.t = e > 0.f ? e * (own.t + own.s * d) : 0.f;
+                own.s *= e;
+                own.m = higher;
+            } else {
+                own.worst = max(own.worst, key_of(higher));
+            }
+        }
+        float s = 0.f, t = 0.f;
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const uint32_t w[4] = {v[b].x, v[b].y, v[b].z, v[b].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                word_values(w[i], f, T());
+#pragma unroll
+                for (int k = 0; k < kWord; ++k) {
+                    // at least -100, where e is 0: so a masked logit adds 0 and not 0 * infinity,
+                    // and so does one under a maximum of -infinity
+                    const float d = fmaxf(f[k] - own.m, -100.f);
+                    const float e = exp_fast(d);
+                    s += e;
+                    t = fmaf(e, d, t);
+                }
+            }
+        }
+        own.s += s;
+        own.t += t;
     }
+    const uint32_t own_key = some ? max(key_of(own.m), own.worst) : 0u;
+
+    // The block's sums, and the maxima of its groups of four threads.
+    uint32_t key = max(own_key, __shfl_xor_sync(~0u, own_key, 1));
+    key = max(key, __shfl_xor_sync(~0u, key, 2));
+    if (lane % 4 == 0) sh.group_key[tid / 4] = key;
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) {
+        const Sums o{__shfl_xor_sync(~0u, own.m, d), __shfl_xor_sync(~0u, own.s, d),
+                     __shfl_xor_sync(~0u, own.t, d), __shfl_xor_sync(~0u, own.worst, d)};
+        own = add(own, o);
+    }
+    if (lane == 0) sh.part[warp] = own;
+    __syncthreads();
+    if (warp == kScoreWarps - 1) {
+        Sums p = lane < kScoreWarps ? sh.part[lane] : Sums{-INFINITY, 0.f, 0.f, 0u};
+#pragma unroll
+        for (int d = kScoreWarps / 2; d > 0; d /= 2) {
+            const Sums o{__shfl_xor_sync(~0u, p.m, d), __shfl_xor_sync(~0u, p.s, d),
+                         __shfl_xor_sync(~0u, p.t, d), __shfl_xor_sync(~0u, p.worst, d)};
+            p = add(p, o);
+        }
+        if (lane == 0) sh.sums = p;
+    }
+    if (a.top > 0) {
+        // the cut: the group maximum with top - 1 others before it
+        if (tid < kGroups) {
+            const uint32_t mine = sh.group_key[tid];
+            int before = 0;
+#pragma unroll 16
+            for (int i = 0; i < kGroups; ++i)
+                before += sh.group_key[i] > mine || (sh.group_key[i] == mine && i < tid);
+            if (before == a.top - 1) sh.cut = mine;
+        }
+        __syncthreads();
+        const uint32_t cut = sh.cut;
+        if (own_key != 0u && own_key >= cut) sh.list[atomicAdd(&sh.listed, 1)] = (uint16_t)tid;
+        __syncthreads();
+        // the listed threads' logits with a key of at least `least`
+        const auto collect = [&](uint32_t least) {
+            const auto offer = [&](float v, int index) {
+                const uint32_t k = key_of(v);
+                if (k < least) return;
+                const int at = atomicAdd(&sh.found, 1);
+                if (at < kCandidates) sh.candidate[at] = rank_of(k, index);
+            };
+            const int listed = sh.listed, turns = (count + kScoreThreads - 1) / kScoreThreads;
+            for (int u = tid; u < listed * turns; u += kScoreThreads) {
+                const int at = u / listed * kScoreThreads + sh.list[u % listed];
+                if (at >= count) continue;
+                const uint4 v = __ldg(piece + at);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                const int index = head + (first + at) * kPer;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float f[kWord];
+                    word_values(w[i], f, T());
+#pragma unroll
+                    for (int k = 0; k < kWord; ++k) offer(f[k], index + i * kWord + k);
+                }
+            }
+            if (tid < loose) offer(to_float(x[loose_at]), loose_at);
+            __syncthreads();
+            return sh.found;
+        };
+        // logit e of the block's part, in ascending order
+        const int before_pieces = rank == 0 ? head : 0, in_pieces = count * kPer;
+        const int part = loose + in_pieces;
+        const auto index_of = [&](int e) {
+            return e < before_pieces               ? e
+                   : e < before_pieces + in_pieces ? head + first * kPer + e - before_pieces
+                                                   : head + pieces * kPer + e - before_pieces - in_pieces;
+        };
+        int found = collect(cut);
+        if (found > kCandidates) {
+            __syncthreads();
+            if (tid == 0) sh.found = 0;
+            __syncthreads();
+            found = cut == 0xFFFFFFFFu ? 0 : collect(cut + 1);
+            for (int base = 0; found < a.top && base < part; base += kScoreThreads) {
+                const int index = index_of(min(base + tid, part - 1));
+                const bool equal = base + tid < part && key_of(to_float(x[index])) == cut;
+                const uint32_t mask = __ballot_sync(~0u, equal);
+                if (lane == 0) sh.equal[warp] = __popc(mask);
+                __syncthreads();
+                int at = found + __popc(mask & ((1u << lane) - 1));
+                for (int w = 0; w < kScoreWarps; ++w) {
+                    if (w < warp) at += sh.equal[w];
+                    found += sh.equal[w];
+                }
+                if (equal && at < a.top) sh.candidate[at] = rank_of(cut, index);
+                __syncthreads();
+                found = min(found, a.top);
+            }
+        }
+        if (found <= kCandidates) {
+            for (int i = tid; i < found; i += kScoreThreads) {
+                const uint64_t mine = sh.candidate[i];
+                int before = 0;
+                for (int j = 0; j < found; ++j) before += sh.candidate[j] > mine;
+                if (before < a.top) sh.best[before] = mine;
+            }
+            if (tid == 0) sh.bests = min(found, a.top);
+        } else {
+            // A thousand logits above the cut, in the pieces of few threads: a sweep of the
+            // block's part for each alternative.
+            uint64_t last = ~0ull;
+            for (int k = 0; k < a.top; ++k) {
+                uint64_t next = 0;
+                for (int e = tid; e < part; e += kScoreThreads) {
+                    const int index = index_of(e);
+                    const uint64_t r = rank_of(key_of(to_float(x[index])), index);
+                    if (r < last) next = max(next, r);
+                }
+#pragma unroll
+                for (int d = 16; d > 0; d /= 2) next = max(next, __shfl_xor_sync(~0u, next, d));
+                if (lane == 0) sh.warp_best[warp] = next;
+                __syncthreads();
+                for (int w = 0; w < kScoreWarps; ++w) next = max(next, sh.warp_best[w]);
+                last = next;
+                if (tid == 0) sh.best[k] = next;
+                __syncthreads();
+            }
+            if (tid == 0) sh.bests = a.top;
+        }
+    }
+    __syncthreads();
+
+    // The first block joins the cluster's parts.
+    Sums all = sh.sums;
+    if (blocks > 1) {
+        cluster_sync_all();
+        if (rank == 0) {
+            const uint32_t here = smem_u32(&sh);
+            for (int r = 1; r < blocks; ++r) {
+                const uint32_t there = map_to_cta(here, r) + (uint32_t)offsetof(ScoreShared, sums);
+                const Sums o{__uint_as_float(ld_cluster_u32(there)),
+                             __uint_as_float(ld_cluster_u32(there + 4)),
+                             __uint_as_float(ld_cluster_u32(there + 8)), ld_cluster_u32(there + 12)};
+                all = add(all, o);
+            }
+            if (a.top > 0) {
+                // thread (r, k) has alternative k of block r
+                const int r = tid / W4A16_MAX_TOP, k = tid % W4A16_MAX_TOP;
+                uint64_t mine = 0;
+                if (r < blocks) {
+                    const uint32_t there = map_to_cta(here, r);
+                    const int held = (int)ld_cluster_u32(there + (uint32_t)offsetof(ScoreShared, bests));
+                    if (k < held)
+                        mine = ld_cluster_u64(there + (uint32_t)offsetof(ScoreShared, best) + 8 * k);
+                }
+                sh.candidate[tid] = mine;  // 0: none, below all
+                __syncthreads();
+                int before = 0;
+                for (int j = 0; j < blocks * W4A16_MAX_TOP; ++j) before += sh.candidate[j] > mine;
+                __syncthreads();
+                if (mine != 0 && before < a.top) sh.best[before] = mine;
+                __syncthreads();
+            }
+        }
+        cluster_sync_all();  // the other blocks' shared memory has been read
+        if (rank != 0) return;
+    }
+    const bool nothing = all.worst == 0 && all.m == -INFINITY;
+    const float ln = logf(all.s);
+    const auto score = [&](float v) {
+        return all.worst ? NAN : nothing ? -INFINITY : v - all.m - ln;
+    };
+    if (tid == 0) {
+        a.logprob[row] = token >= 0 && token < n ? score(token_logit) : NAN;
+        a.entropy[row] = all.worst ? NAN : nothing ? 0.f : ln - all.t / all.s;
+    }
+    if (tid < a.top) {
+        const uint64_t best = sh.best[tid];
+        a.top_ids[row * a.top + tid] = (int)~(uint32_t)best;
+        a.top_logprobs[row * a.top + tid] = score(value_of((uint32_t)(best >> 32)));
+    }
+}
+
+// Blocks to a row: one where the rows alone fill the SMs, else up to eight (a
+// portable cluster), as many as keep a piece of the row for every thread.
+int score_blocks(int64_t rows, int64_t vocabulary, int size, const DeviceCtx& ctx) {
+    int blocks = 1;
+    while (blocks < kMaxCluster && rows * blocks * 2 <= 8 * ctx.num_sms &&
+           vocabulary * size / 16 >= (int64_t)blocks * 2 * kScoreThreads)
+        blocks *= 2;
+    return blocks;
+}
+
+template <typename T>
+cudaError_t score(const ScoreArgs& a, cudaStream_t stream, const DeviceCtx& ctx) {
+    const int blocks = score_blocks(a.rows, a.vocabulary, sizeof(T), ctx);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.rows * blocks));
+    cfg.blockDim = dim3(kScoreThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)blocks;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = blocks > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, score_kernel<T>, a, blocks);
 }
 
 }  // namespace
@@ -105,17 +460,11 @@ cudaError_t launch_token_logprobs(const void* logits, const void* tokens, float*
                                   float* entropy, int32_t* top_ids, float* top_logprobs,
                                   int64_t rows, int64_t vocabulary, int64_t row_stride, int type,
                                   int wide, int top, cudaStream_t stream, const DeviceCtx& ctx) {
-    (void)ctx;
-    ScoreArgs a{logits, tokens, logprob, entropy, top_logprobs, top_ids,
-                rows, vocabulary, row_stride, wide, top};
-    const unsigned grid = (unsigned)rows;
-    if (type == W4A16_F16)
-        score_kernel<__half><<<grid, kScoreThreads, 0, stream>>>(a);
-    else if (type == W4A16_BF16)
-        score_kernel<__nv_bfloat16><<<grid, kScoreThreads, 0, stream>>>(a);
-    else
-        score_kernel<float><<<grid, kScoreThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    const ScoreArgs a{logits, tokens, logprob, entropy, top_logprobs, top_ids,
+                      rows, vocabulary, row_stride, wide, top};
+    return type == W4A16_F16    ? score<__half>(a, stream, ctx)
+           : type == W4A16_BF16 ? score<__nv_bfloat16>(a, stream, ctx)
+                                : score<float>(a, stream, ctx);
 }
 
 }  // namespace w4a16
