@@ -12,33 +12,49 @@
 namespace w4a16 {
 namespace {
 
+// x / divisor for 0 <= x < 2^31: with l = ceil(log2 divisor) and
+// m = floor(2^(31 + l) / divisor) + 1, m * divisor exceeds 2^(31 + l) by at most
+// divisor <= 2^l, so x * m / 2^(31 + l) is off by less than 1 / divisor.
+struct Divisor {
+    int value;
+    uint32_t mul, shift;
+
+    explicit Divisor(int64_t divisor = 1) : value((int)divisor) {
+        uint32_t l = 0;
+        while (((int64_t)1 << l) < divisor) ++l;
+        shift = 31 + l;
+        mul = (uint32_t)(((uint64_t)1 << shift) / (uint64_t)divisor + 1);
+    }
+    __device__ __forceinline__ int quotient(int x) const {
+        return (int)(((uint64_t)(uint32_t)x * mul) >> shift);
+    }
+    __device__ __forceinline__ int remainder(int x) const { return x - quotient(x) * value; }
+};
+
 // A cache's geometry; strides in elements (2 bytes).
 struct Cache {
     int64_t pages, page_stride, slot_stride, head_stride, table_stride;
-    int page_size, kv_heads, head_dim, batch, width;
-    uint32_t div_mul, div_shift;
-
-    // position / page_size for 0 <= position < 2^31: with l = ceil(log2 page_size) and
-    // m = floor(2^(31 + l) / page_size) + 1, m * page_size exceeds 2^(31 + l) by at most
-    // page_size <= 2^l, so position * m / 2^(31 + l) is off by less than 1 / page_size.
-    __device__ __forceinline__ int page_of(int position) const {
-        return (int)(((uint64_t)(uint32_t)position * div_mul) >> div_shift);
-    }
+    int kv_heads, head_dim, batch, width;
+    Divisor page_size;
 };
 
 Cache cache_of(const w4a16_cache_shape& c) {
-    uint32_t l = 0;
-    while (((int64_t)1 << l) < c.page_size) ++l;
-    return {c.pages,          c.page_stride,    c.slot_stride,   c.head_stride,
-            c.table_stride,   (int)c.page_size, (int)c.kv_heads, (int)c.head_dim,
-            (int)c.batch,     (int)c.table_width,
-            (uint32_t)(((uint64_t)1 << (31 + l)) / (uint64_t)c.page_size + 1), 31 + l};
+    return {c.pages,         c.page_stride,    c.slot_stride,    c.head_stride,
+            c.table_stride,  (int)c.kv_heads,  (int)c.head_dim,  (int)c.batch,
+            (int)c.table_width, Divisor(c.page_size)};
 }
 
 // ---------------------------------------------------------------------------
 // Append
+//
+// A copy, bound by HBM.  A block first finds the places of up to 16 tokens, a
+// warp each in turn (the row by a 32-way search of the offsets, then its
+// start, then its page: three loads that depend on one another), and then
+// copies their 16-byte pieces, four of a thread in flight.
 // ---------------------------------------------------------------------------
 constexpr int kAppendThreads = 256;
+constexpr int kAppendTokens = 16;  // of a block at most
+constexpr int kAppendUnroll = 4;
 
 struct AppendArgs {
     const uint16_t *k, *v;
@@ -46,40 +62,68 @@ struct AppendArgs {
     const int32_t *tables, *starts, *offsets;
     int64_t tokens, k_token, k_head, v_token, v_head;
     Cache c;
+    int block_tokens;
+    Divisor token_pieces, head_pieces;  // 16-byte pieces of a token's keys, of a head
 };
 
-// The row whose [offsets[b], offsets[b + 1]) holds the token; -1: none does.
+// The row with offsets[b] <= token < offsets[b + 1], -1 if none; by a whole warp.
 __device__ int row_of(const AppendArgs& a, int64_t token) {
     if (!a.offsets) return (int)token;
-    int lo = 0, hi = a.c.batch;  // the last row that starts at or before the token
-    while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (a.offsets[mid] <= token)
-            lo = mid + 1;
-        else
-            hi = mid;
-    }
-    return lo - 1 >= 0 && token < a.offsets[lo] ? lo - 1 : -1;
+    const int lane = threadIdx.x % 32;
+    int lo = 0, step = a.c.batch;  // rows before lo end at or before the token
+    do {
+        step = (step + 31) / 32;
+        const int last = lo + (lane + 1) * step - 1;  // of the lane's part
+        const bool before = last < a.c.batch && a.offsets[last + 1] <= token;
+        lo += __popc(__ballot_sync(~0u, before)) * step;
+    } while (step > 1 && lo < a.c.batch);
+    return lo < a.c.batch && a.offsets[lo] <= token && token < a.offsets[lo + 1] ? lo : -1;
 }
 
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
-    const int vectors = a.c.head_dim / 8, per = a.c.kv_heads * vectors;
-    for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+    __shared__ int64_t place[kAppendTokens];  // where a token's heads start in the pools, -1: nowhere
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int64_t first = (int64_t)blockIdx.x * a.block_tokens;
+    const int tokens = (int)min((int64_t)a.block_tokens, a.tokens - first);
+    for (int i = threadIdx.x / 32; i < tokens; i += kAppendThreads / 32) {
+        const int64_t t = first + i;
         const int b = row_of(a, t);
-        if (b < 0) continue;
-        const int64_t p = (int64_t)a.starts[b] + t - (a.offsets ? a.offsets[b] : t);
-        if (p < 0 || p >= (int64_t)a.c.width * a.c.page_size) continue;
-        const int64_t page = a.tables[b * a.c.table_stride + p / a.c.page_size];
-        if (page < 0 || page >= a.c.pages) continue;
-        const int64_t to = page * a.c.page_stride + p % a.c.page_size * a.c.slot_stride;
-        for (int i = threadIdx.x; i < 2 * per; i += kAppendThreads) {
-            const bool value = i >= per;
-            const int h = i % per / vectors, x = i % per % vectors * 8;
-            const uint16_t* from = value ? a.v + t * a.v_token + h * a.v_head
-                                         : a.k + t * a.k_token + h * a.k_head;
-            uint16_t* dst = (value ? a.v_pool : a.k_pool) + to + h * a.c.head_stride;
-            *reinterpret_cast<uint4*>(dst + x) = *reinterpret_cast<const uint4*>(from + x);
+        int64_t at = -1;
+        if (b >= 0) {
+            const int64_t p = (int64_t)a.starts[b] + t - (a.offsets ? a.offsets[b] : t);
+            if (p >= 0 && p < (int64_t)a.c.width * a.c.page_size.value) {
+                const int j = a.c.page_size.quotient((int)p);
+                const int64_t page = a.tables[b * a.c.table_stride + j];
+                if (page >= 0 && page < a.c.pages)
+                    at = page * a.c.page_stride + (p - j * a.c.page_size.value) * a.c.slot_stride;
+            }
         }
+        if (threadIdx.x % 32 == 0) place[i] = at;
+    }
+    __syncthreads();
+    const int units = tokens * a.token_pieces.value;  // of keys, and as many of values
+    for (int u = threadIdx.x; u < 2 * units; u += kAppendUnroll * kAppendThreads) {
+        uint4 data[kAppendUnroll];
+        uint16_t* to[kAppendUnroll];
+#pragma unroll
+        for (int k = 0; k < kAppendUnroll; ++k) {
+            const int w = u + k * kAppendThreads;
+            const bool value = w >= units;
+            const int x = value ? w - units : w;
+            const int i = a.token_pieces.quotient(x), y = x - i * a.token_pieces.value;
+            const int h = a.head_pieces.quotient(y), d = (y - h * a.head_pieces.value) * 8;
+            const int64_t at = w < 2 * units ? place[i] : -1;
+            to[k] = nullptr;
+            if (at < 0) continue;
+            data[k] = *reinterpret_cast<const uint4*>(
+                value ? a.v + (first + i) * a.v_token + h * a.v_head + d
+                      : a.k + (first + i) * a.k_token + h * a.k_head + d);
+            to[k] = (value ? a.v_pool : a.k_pool) + at + h * a.c.head_stride + d;
+        }
+#pragma unroll
+        for (int k = 0; k < kAppendUnroll; ++k)
+            if (to[k]) *reinterpret_cast<uint4*>(to[k]) = data[k];
     }
 }
 
@@ -138,7 +182,7 @@ struct AttendArgs {
     Cache c;
 
     __device__ int length(int row) const {
-        return min(max(lengths[row], 0), c.width * c.page_size);
+        return min(max(lengths[row], 0), c.width * c.page_size.value);
     }
     __device__ int first_head(int item) const {
         return item / head_blocks * group + item % head_blocks * block_heads;
@@ -332,7 +376,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
     const auto load_page = [&]() {
         const int p = ahead.tile * kStep + warp * kTile + (kTilePage ? 0 : lane % kTile);
         next_page = -1;
-        if (p < ahead.length) next_page = a.tables[ahead.row * a.c.table_stride + a.c.page_of(p)];
+        if (p < ahead.length) next_page = a.tables[ahead.row * a.c.table_stride + a.c.page_size.quotient(p)];
     };
     // Copies: lane's piece `piece` of rows row0, row0 + kRows, ...
     constexpr int kPieces = DP / 8, kRows = 32 / kPieces;
@@ -355,7 +399,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
                 return dst + S::kHalf + r * S::kRowBytes + ((piece ^ (row0 + r & 7)) << 4);
             };
             if (kTilePage) {
-                const int slot = first - a.c.page_of(first) * a.c.page_size;
+                const int slot = a.c.page_size.remainder(first);
                 const int64_t at =
                     next_page * a.c.page_stride + (slot + row0) * a.c.slot_stride + head + 8 * piece;
                 const int n = there ? ahead.length - first : 0;  // positions that count
@@ -378,7 +422,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
                 // where position `lane` starts; a page number is looked up below the length only
                 const int p = first + lane % kTile;
                 const int64_t at = there ? next_page * a.c.page_stride +
-                                               (p - a.c.page_of(p) * a.c.page_size) * a.c.slot_stride +
+                                               a.c.page_size.remainder(p) * a.c.slot_stride +
                                                head
                                          : -1;
                 flags |= (uint32_t)(__shfl_sync(~0u, at, g) >= 0) |
@@ -733,7 +777,7 @@ cudaError_t attend(const AttendArgs& a, cudaStream_t stream, const DeviceCtx& ct
 // 16: one page number a tile then, else one a position.
 template <typename T, int DP, int NT>
 cudaError_t attend(const AttendArgs& a, cudaStream_t stream, const DeviceCtx& ctx) {
-    return a.c.page_size % kTile == 0 ? attend<T, DP, NT, true>(a, stream, ctx)
+    return a.c.page_size.value % kTile == 0 ? attend<T, DP, NT, true>(a, stream, ctx)
                                       : attend<T, DP, NT, false>(a, stream, ctx);
 }
 
@@ -758,14 +802,27 @@ cudaError_t launch_paged_append(const void* k, const void* v, void* k_pool, void
                                 const int32_t* offsets, const w4a16_cache_shape& cache,
                                 int64_t tokens, int64_t k_token, int64_t k_head, int64_t v_token,
                                 int64_t v_head, cudaStream_t stream, const DeviceCtx& ctx) {
-    if (tokens == 0) return cudaSuccess;
-    AppendArgs a{static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
-                 static_cast<uint16_t*>(k_pool),  static_cast<uint16_t*>(v_pool),
-                 tables, starts, offsets, tokens, k_token, k_head, v_token, v_head,
-                 cache_of(cache)};
-    const int64_t ctas = min(tokens, (int64_t)8 * ctx.num_sms);
-    append_kernel<<<(unsigned)ctas, kAppendThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    const int64_t pieces = cache.head_dim / 8;
+    // up to 16 tokens a block while that leaves four blocks an SM
+    const int64_t block = std::max<int64_t>(
+        1, std::min<int64_t>(kAppendTokens, tokens / (4 * ctx.num_sms)));
+    const AppendArgs a{static_cast<const uint16_t*>(k),
+                       static_cast<const uint16_t*>(v),
+                       static_cast<uint16_t*>(k_pool),
+                       static_cast<uint16_t*>(v_pool),
+                       tables, starts, offsets, tokens, k_token, k_head, v_token, v_head,
+                       cache_of(cache), (int)block, Divisor(cache.kv_heads * pieces),
+                       Divisor(pieces)};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((tokens + block - 1) / block));
+    cfg.blockDim = dim3(kAppendThreads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, append_kernel, a);
 }
 
 int64_t paged_attention_workspace(const w4a16_cache_shape& cache, int64_t q_heads,

@@ -44,9 +44,9 @@ def _run(dev: int, stream, name: str, *args) -> None:
 def _empty(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
     """A new tensor on `like`'s device whose memory belongs to the stream the call runs on."""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _device(stream, **named) -> int:
