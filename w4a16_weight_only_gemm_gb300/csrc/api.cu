@@ -491,7 +491,7 @@ int w4a16_pages_copy(void* pool, const int32_t* from, const int32_t* to, int64_t
     DeviceCtx ctx;
     if (int rc = device_ctx(&ctx)) return rc;
     return from_cuda(launch_pages_copy(pool, from, to, count, pages, *shape,
-                                       static_cast<cudaStream_t>(stream), ctx));
+                                       static_cast<cudaStream_t>(stream)));
 }
 
 int w4a16_token_logprobs(const void* logits, const void* tokens, float* logprob, float* entropy,

@@ -120,8 +120,8 @@ cudaError_t launch_pages_compact(void* pool, const PageBooks& books, int32_t* us
                                  void* workspace, const w4a16_pool_shape& shape,
                                  cudaStream_t stream, const DeviceCtx& ctx);
 cudaError_t launch_pages_copy(void* pool, const int32_t* from, const int32_t* to, int64_t count,
-                              int64_t pages, const w4a16_pool_shape& shape, cudaStream_t stream,
-                              const DeviceCtx& ctx);
+                              int64_t pages, const w4a16_pool_shape& shape,
+                              cudaStream_t stream);
 cudaError_t launch_token_logprobs(const void* logits, const void* tokens, float* logprob,
                                   float* entropy, int32_t* top_ids, float* top_logprobs,
                                   int64_t rows, int64_t vocabulary, int64_t row_stride, int type,

@@ -7,6 +7,8 @@
 // cheaper than a second launch, and its shared memory carries the sums.  What
 // moves whole pages runs over all SMs in a second launch that reads the list
 // of copies from the workspace, so nothing waits for the host.
+#include <algorithm>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -131,6 +133,8 @@ __global__ void __launch_bounds__(kBookThreads) free_kernel(Books b, const int32
     const uint32_t ctas = cluster_size();
     const int64_t threads = (int64_t)ctas * kBookThreads;
     const int64_t thread = (int64_t)cluster_cta_rank() * kBookThreads + threadIdx.x;
+    grid_dependency_wait();
+    grid_launch_dependents();
     copy_books(b, thread, threads);
     books_sync(ctas);
     for (int64_t i = thread / 32; i < count; i += threads / 32) {
@@ -158,12 +162,15 @@ struct Space {
     int32_t* high;   // [pages]   compact: held pages from the top
     int32_t* place;  // [pages]   compact: place of a page in `high`
     int32_t* copies; // [1]       page copies listed
+    unsigned long long* next;  // [1]  the piece to copy next
 };
 
 Space split_space(void* workspace, int64_t rows, int64_t pages, int64_t count) {
     Space s;
     int32_t* w = static_cast<int32_t*>(workspace);
-    s.copies = w, w += 4;
+    s.copies = w;
+    s.next = reinterpret_cast<unsigned long long*>(w + 2);
+    w += 4;
     s.claim = w, w += rows;
     s.order = w, w += count;
     s.from = w, w += count;
@@ -227,6 +234,8 @@ __global__ void __launch_bounds__(kBookThreads)
     const uint32_t ctas = cluster_size(), rank = cluster_cta_rank();
     const int64_t threads = (int64_t)ctas * kBookThreads;
     const int64_t thread = (int64_t)rank * kBookThreads + threadIdx.x;
+    grid_dependency_wait();
+    grid_launch_dependents();
     const int64_t n_free = sweep_pages(
         b.refs_in, b.pages, sh, rank, ctas, [](int32_t r) { return r <= 0; },
         [&](int64_t p, int k, bool member) {
@@ -273,6 +282,8 @@ __global__ void __launch_bounds__(kBookThreads)
     const uint32_t ctas = cluster_size(), rank = cluster_cta_rank();
     const int64_t threads = (int64_t)ctas * kBookThreads;
     const int64_t thread = (int64_t)rank * kBookThreads + threadIdx.x;
+    grid_dependency_wait();
+    grid_launch_dependents();
     const int64_t n_free = sweep_pages(
         b.refs_in, b.pages, sh, rank, ctas, [](int32_t r) { return r <= 0; },
         [&](int64_t p, int k, bool member) {
@@ -305,41 +316,61 @@ __global__ void __launch_bounds__(kBookThreads)
                     b.refs_out[s.free[first]] = 1;
                 }
             });
-    if (rank == 0 && threadIdx.x == 0) *s.copies = (int32_t)count;
+    if (rank == 0 && threadIdx.x == 0) *s.next = 0;
 }
 
-// Copies the listed pages, thread blocks taking 16 KB pieces in turn.
+// Page copies, in pieces of 16 KB.  Pieces are handed out as blocks become
+// free: shared out beforehand, the blocks that sit further from their pages'
+// memory end last (992 MB in and out: 321 us, handed out 292 us, 6.8 TB/s).
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnroll = 4;
+constexpr int kCopyBlocksPerSm = 6;
 constexpr int64_t kPiece = (int64_t)kCopyThreads * kCopyUnroll * 16;
 
 struct Pool {
     char* base;
-    int64_t planes, plane_stride, page_stride, page_bytes;
+    int64_t planes, plane_stride, page_stride, page_bytes, pages;
+
+    __device__ int64_t pieces() const { return (page_bytes + kPiece - 1) / kPiece; }
 };
 
+// Piece `unit` of the copies from(i) -> to(i).
 template <typename From, typename To>
-__device__ void copy_pages(const Pool& pool, int64_t copies, int64_t pages, From from, To to) {
-    const int64_t pieces = (pool.page_bytes + kPiece - 1) / kPiece;
-    const int64_t units = copies * pool.planes * pieces;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int64_t piece = u % pieces, plane = u / pieces % pool.planes;
-        const int64_t i = u / pieces / pool.planes;
-        const int64_t src = from(i), dst = to(i);
-        if (src < 0 || src >= pages || dst < 0 || dst >= pages) continue;
-        const char* a = pool.base + plane * pool.plane_stride + src * pool.page_stride;
-        char* z = pool.base + plane * pool.plane_stride + dst * pool.page_stride;
-        uint4 v[kCopyUnroll];
+__device__ __forceinline__ void copy_piece(const Pool& pool, int64_t unit, From from, To to) {
+    const int64_t pieces = pool.pieces();
+    const int64_t piece = unit % pieces, plane = unit / pieces % pool.planes;
+    const int64_t i = unit / pieces / pool.planes;
+    const int64_t src = from(i), dst = to(i);
+    if (src < 0 || src >= pool.pages || dst < 0 || dst >= pool.pages) return;
+    const char* a = pool.base + plane * pool.plane_stride + src * pool.page_stride;
+    char* z = pool.base + plane * pool.plane_stride + dst * pool.page_stride;
+    uint4 v[kCopyUnroll];
 #pragma unroll
-        for (int k = 0; k < kCopyUnroll; ++k) {
-            const int64_t at = piece * kPiece + (k * kCopyThreads + threadIdx.x) * 16;
-            if (at < pool.page_bytes) v[k] = *reinterpret_cast<const uint4*>(a + at);
-        }
+    for (int k = 0; k < kCopyUnroll; ++k) {
+        const int64_t at = piece * kPiece + (k * kCopyThreads + threadIdx.x) * 16;
+        if (at < pool.page_bytes) v[k] = *reinterpret_cast<const uint4*>(a + at);
+    }
 #pragma unroll
-        for (int k = 0; k < kCopyUnroll; ++k) {
-            const int64_t at = piece * kPiece + (k * kCopyThreads + threadIdx.x) * 16;
-            if (at < pool.page_bytes) *reinterpret_cast<uint4*>(z + at) = v[k];
-        }
+    for (int k = 0; k < kCopyUnroll; ++k) {
+        const int64_t at = piece * kPiece + (k * kCopyThreads + threadIdx.x) * 16;
+        if (at < pool.page_bytes) *reinterpret_cast<uint4*>(z + at) = v[k];
+    }
+}
+
+// All pieces of `copies` copies; *next is 0 at first.
+template <typename From, typename To>
+__device__ void copy_pages(const Pool& pool, int64_t copies, unsigned long long* next, From from,
+                           To to) {
+    __shared__ unsigned long long turn[2];  // this piece, and the one asked for while it is copied
+    const unsigned long long units = copies * pool.planes * pool.pieces();
+    if (threadIdx.x == 0) turn[0] = units ? atomicAdd(next, 1ull) : 0;
+    __syncthreads();
+    int which = 0;
+    for (unsigned long long u = turn[0]; u < units; u = turn[which]) {
+        which ^= 1;
+        if (threadIdx.x == 0) turn[which] = atomicAdd(next, 1ull);
+        copy_piece(pool, (int64_t)u, from, to);
+        __syncthreads();
     }
 }
 
@@ -380,7 +411,7 @@ __global__ void __launch_bounds__(kCopyThreads)
         }
         if (lane == 0) b.lengths_out[r] = (int32_t)n;
     }
-    copy_pages(pool, count, b.pages, [&](int64_t i) { return s.from[i]; },
+    copy_pages(pool, count, s.next, [&](int64_t i) { return s.from[i]; },
                [&](int64_t i) { return s.to[i]; });
 }
 
@@ -390,6 +421,8 @@ __global__ void __launch_bounds__(kBookThreads)
     __shared__ ScanShared sh;
     const uint32_t ctas = cluster_size(), rank = cluster_cta_rank();
     const auto held = [](int32_t r) { return r > 0; };
+    grid_dependency_wait();
+    grid_launch_dependents();
     int n = 0, unused;
     {
         const int64_t threads = (int64_t)ctas * kBookThreads;
@@ -411,6 +444,7 @@ __global__ void __launch_bounds__(kBookThreads)
     });
     if (rank == 0 && threadIdx.x == 0) {
         used[0] = n;
+        *s.next = 0;
         if (n == 0) *s.copies = 0;
     }
 }
@@ -441,14 +475,16 @@ __global__ void __launch_bounds__(kCopyThreads)
             }
             b.tables_out[r * b.out_stride + j] = p;
         }
-    copy_pages(pool, copies, b.pages, [&](int64_t i) { return s.high[copies - 1 - i]; },
+    copy_pages(pool, copies, s.next, [&](int64_t i) { return s.high[copies - 1 - i]; },
                [&](int64_t i) { return s.free[i]; });
 }
 
 __global__ void __launch_bounds__(kCopyThreads)
-    copy_kernel(Pool pool, const int32_t* from, const int32_t* to, int64_t count, int64_t pages) {
-    copy_pages(pool, count, pages, [&](int64_t i) { return from[i]; },
-               [&](int64_t i) { return to[i]; });
+    copy_kernel(Pool pool, const int32_t* from, const int32_t* to, int64_t units) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x)
+        copy_piece(pool, u, [&](int64_t i) { return from[i]; }, [&](int64_t i) { return to[i]; });
 }
 
 // The cluster of a books kernel: one CTA up to a sweep of pages, else eight.
@@ -459,12 +495,14 @@ cudaError_t launch_books(void (*kernel)(P...), int64_t pages, cudaStream_t strea
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kBookThreads);
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ctas;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 
@@ -488,11 +526,11 @@ Books books_of(const PageBooks& b) {
             b.shape.out_stride, b.shape.page_size};
 }
 
-Pool pool_of(void* pool, const w4a16_pool_shape& s) {
-    return {static_cast<char*>(pool), s.planes, s.plane_stride, s.page_stride, s.page_bytes};
+Pool pool_of(void* pool, const w4a16_pool_shape& s, int64_t pages) {
+    return {static_cast<char*>(pool), s.planes, s.plane_stride, s.page_stride, s.page_bytes, pages};
 }
 
-unsigned copy_ctas(const DeviceCtx& ctx) { return 8u * (unsigned)ctx.num_sms; }
+unsigned copy_ctas(const DeviceCtx& ctx) { return (unsigned)(kCopyBlocksPerSm * ctx.num_sms); }
 
 }  // namespace
 
@@ -521,7 +559,7 @@ cudaError_t launch_pages_fork(void* pool, const PageBooks& b, const int32_t* par
                                  children, count, done, s);
     if (e != cudaSuccess) return e;
     return launch_apply(fork_apply_kernel, copy_ctas(ctx), stream, books_of(b), parents, children,
-                        count, s, pool_of(pool, shape));
+                        count, s, pool_of(pool, shape, b.shape.pages));
 }
 
 cudaError_t launch_pages_compact(void* pool, const PageBooks& b, int32_t* used, void* workspace,
@@ -531,16 +569,17 @@ cudaError_t launch_pages_compact(void* pool, const PageBooks& b, int32_t* used, 
     cudaError_t e = launch_books(compact_plan_kernel, b.shape.pages, stream, books_of(b), used, s);
     if (e != cudaSuccess) return e;
     return launch_apply(compact_apply_kernel, copy_ctas(ctx), stream, books_of(b),
-                        (const int32_t*)used, s, pool_of(pool, shape));
+                        (const int32_t*)used, s, pool_of(pool, shape, b.shape.pages));
 }
 
 cudaError_t launch_pages_copy(void* pool, const int32_t* from, const int32_t* to, int64_t count,
-                              int64_t pages, const w4a16_pool_shape& shape, cudaStream_t stream,
-                              const DeviceCtx& ctx) {
+                              int64_t pages, const w4a16_pool_shape& shape,
+                              cudaStream_t stream) {
     if (count == 0) return cudaSuccess;
-    copy_kernel<<<copy_ctas(ctx), kCopyThreads, 0, stream>>>(pool_of(pool, shape), from, to, count,
-                                                             pages);
-    return cudaGetLastError();
+    // a piece a block: the scheduler hands them out
+    const int64_t units = count * shape.planes * ((shape.page_bytes + kPiece - 1) / kPiece);
+    return launch_apply(copy_kernel, (unsigned)std::min<int64_t>(units, 1 << 30), stream,
+                        pool_of(pool, shape, pages), from, to, units);
 }
 
 }  // namespace w4a16

@@ -183,19 +183,30 @@ def paged_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
     return (out, lse) if return_lse else out
 
 
+def _like(t: torch.Tensor, stream) -> torch.Tensor:
+    """A new tensor of t's shape and type, dense in its last dimension as t is."""
+    if stream is None:
+        return torch.empty_like(t)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t)
+
+
 def _books(refs, tables, lengths, out, page_size: int, stream, **others):
     """The books' device, their addresses, their outputs (new ones, or `out`), the outputs'
-    addresses and the packed shape; the tensors in `others` share the device."""
-    pages, shape, strides = refs.shape[0], tables.shape, tables.stride()
+    addresses and the packed shape; the tensors in `others` share the device.  lengths may be
+    None: neither read nor written."""
+    pages, (rows, width), strides = refs.shape[0], tables.shape, tables.stride()
     _row(refs, pages, "refs")
-    if tables.dtype is not torch.int32 or len(strides) != 2 or strides[1] != 1:
+    if tables.dtype is not torch.int32 or strides[1] != 1:
         _ints(tables, "tables", (None, None))
     ins = (refs, tables)
     if lengths is not None:
-        _row(lengths, shape[0], "lengths")
+        _row(lengths, rows, "lengths")
         ins = (refs, tables, lengths)
+    dev = refs.get_device()
+    same = dev >= 0 and (stream is None or stream.device.index == dev)
     if out is None:
-        outs = [_empty(refs, t.shape, torch.int32, stream) for t in ins]
+        outs = [_like(t, stream) for t in ins] if dev >= 0 else ins
     else:
         outs = list(out)
         if len(outs) != len(ins):
@@ -204,15 +215,17 @@ def _books(refs, tables, lengths, out, page_size: int, stream, **others):
             _ints(o, "out", tuple(t.shape))
             if o.data_ptr() == t.data_ptr() and o.stride() != t.stride():
                 raise ValueError("an out tensor that is its input must have its strides")
-    dev = refs.get_device()
-    if (dev < 0 or stream is not None and stream.device.index != dev
-            or any(t.get_device() != dev for t in (*ins, *outs, *others.values()))):
+            same = same and o.get_device() == dev
+    for t in ins[1:]:
+        same = same and t.get_device() == dev
+    for t in others.values():
+        same = same and t.get_device() == dev
+    if not same:
         _device(stream, refs=refs, tables=tables, lengths=lengths, **others,
                 **{f"out[{i}]": o for i, o in enumerate(outs)})
-    rows, width = shape
-    row = outs[1].stride(0) if rows > 1 else width
     return (dev, [t.data_ptr() for t in ins], outs, [t.data_ptr() for t in outs],
-            _BOOKS_SHAPE(pages, rows, width, strides[0], row, page_size))
+            _BOOKS_SHAPE(pages, rows, width, strides[0], outs[1].stride(0) if rows > 1 else width,
+                         page_size))
 
 
 def _pool_shape(pool: torch.Tensor, pages: int | None) -> bytes:
@@ -223,10 +236,10 @@ def _pool_shape(pool: torch.Tensor, pages: int | None) -> bytes:
     if pages is not None and shape[1] != pages:
         raise ValueError(f"pool has {shape[1]} pages, the books {pages}")
     page = size
-    for n, s in zip(shape[:1:-1], strides[:1:-1]):
-        if n > 1 and s * size != page:
+    for i in range(len(shape) - 1, 1, -1):
+        if strides[i] * size != page and shape[i] > 1:
             raise ValueError("pool must be dense within a page")
-        page *= n
+        page *= shape[i]
     return _POOL_SHAPE(shape[0], strides[0] * size, strides[1] * size, page)
 
 
