@@ -8,18 +8,19 @@
 // once a batch of them; parts with other maxima are added up as
 //   s = sum s_i e^(m_i - m),   t = sum e^(m_i - m) (t_i + s_i (m_i - m)).
 //
+// The sums run in pairs (f32x2) with y = (x - m) log2(e), t in units of ln 2.
+//
 // The alternatives come from the maxima that the pass leaves anyway.  The
 // k-th largest of the maxima of 64 groups of threads is at most the k-th
 // largest logit, and few logits are above it (k = 20: 24 of 128256 independent
-// ones); only the threads whose maximum reaches it read their pieces again,
-// from L2, and the few logits found are ranked by counting.  Where they are
-// not few (masks leave fewer than k logits, so the cut is the mask's value),
-// those above the cut are kept and the lowest indices at it added in order.
+// ones); only the batches of pieces whose maximum reaches it are read again,
+// and the few logits found are ranked by counting.  Where they are not few
+// (masks leave fewer than k logits, so the cut is the mask's value), those
+// above the cut are kept and the lowest indices at it added in order.
 //
-// Bound by HBM for many rows: about seven instructions and one exponential a
-// logit are 0.6 and 0.7 of the time its two bytes take.  A row is a block's,
-// or, for few rows, a cluster's, whose first block joins the others' sums and
-// alternatives through shared memory: no workspace, one launch.
+// Bound by HBM for many rows.  A row is a block's, or, for few rows, a
+// cluster's, whose first block joins the others' sums and alternatives through
+// shared memory: no workspace, one launch.
 #include <cuda_bf16.h>
 
 #include <stddef.h>
@@ -39,7 +40,9 @@ constexpr int kGroups = kScoreThreads / 4;  // of threads, for the first cut of 
 constexpr int kBatch = 4;                   // 16-byte pieces a thread has in flight
 constexpr int kCandidates = 1024;
 constexpr int kMaxCluster = 8;
+constexpr int kKept = 32;                   // batches of a thread whose maxima are kept
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 struct ScoreArgs {
     const void *logits, *tokens;
@@ -52,6 +55,42 @@ struct ScoreArgs {
 __device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_float(float v) { return v; }
+
+__device__ __forceinline__ __half from_float(float v, __half) { return __float2half_rn(v); }
+__device__ __forceinline__ __nv_bfloat16 from_float(float v, __nv_bfloat16) {
+    return __float2bfloat16_rn(v);
+}
+__device__ __forceinline__ float from_float(float v, float) { return v; }
+
+// Two FP32 values, for the paired instructions.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 // The larger, NaN if one is: of a word's values at once.
 __device__ __forceinline__ uint32_t max_words(uint32_t a, uint32_t b, __half) {
@@ -90,11 +129,7 @@ __device__ __forceinline__ uint32_t lowest_word() {  // -infinity
     return sizeof(T) == 4 ? 0xFF800000u : std::is_same<T, __half>::value ? 0xFC00FC00u : 0xFF80FF80u;
 }
 
-__device__ __forceinline__ float exp_fast(float x) {  // x <= 0
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * kLog2e));
-    return y;
-}
+__device__ __forceinline__ float exp_fast(float x) { return exp2_fast(x * kLog2e); }
 
 // Whole numbers in the order of the values, NaN above all, -0 equal to 0; none is 0.
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -129,7 +164,11 @@ __device__ __forceinline__ Sums add(const Sums& a, const Sums& b) {
     return r;
 }
 
+template <typename T>
 struct ScoreShared {
+    T batch_top[kKept][kScoreThreads];  // the largest logit of a thread's batch
+    int batches;
+    uint32_t batch[kScoreThreads];      // those that reach the cut: thread | batch << 16
     Sums part[kScoreWarps];
     Sums sums;                      // of the block
     uint32_t group_key[kGroups];
@@ -158,7 +197,8 @@ template <typename T>
 __global__ void __launch_bounds__(kScoreThreads, kScoreBlocksPerSm)
     score_kernel(ScoreArgs a, int blocks) {
     constexpr int kPer = 16 / sizeof(T), kWord = 4 / sizeof(T);
-    __shared__ ScoreShared sh;
+    using Shared = ScoreShared<T>;
+    __shared__ Shared sh;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int64_t row = blockIdx.x / blocks;
     const int rank = (int)(blockIdx.x % blocks);
@@ -182,28 +222,13 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocksPerSm)
         token = a.wide ? static_cast<const int64_t*>(a.tokens)[row]
                        : static_cast<const int32_t*>(a.tokens)[row];
         if (token >= 0 && token < n) token_logit = to_float(x[token]);
-        sh.listed = sh.found = 0;
-    } else if (tid == 0) {
-        sh.listed = sh.found = 0;
     }
+    if (tid == 0) sh.listed = sh.found = sh.batches = 0;
 
     Sums own{-INFINITY, 0.f, 0.f, 0u};
     const bool some = tid < loose || tid < count;
-    if (tid < loose) {
-        const float v = to_float(x[loose_at]);
-        if (!(v < INFINITY))
-            own.worst = key_of(v);
-        else if (v > -INFINITY)
-            own = {v, 1.f, 0.f, 0u};
-    }
-    for (int j = tid; j < count; j += kBatch * kScoreThreads) {
-        uint4 v[kBatch];
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int at = j + b * kScoreThreads;
-            v[b] = make_uint4(lowest_word<T>(), lowest_word<T>(), lowest_word<T>(), lowest_word<T>());
-            if (at < count) v[b] = __ldg(piece + at);
-        }
+    float s = 0.f, t = 0.f;
+    const auto take = [&](const uint4 (&v)[kBatch], int batch) {
         uint32_t top = v[0].x;
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
@@ -215,37 +240,73 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocksPerSm)
         float f[kWord];
         word_values(top, f, T());
         const float higher = kWord == 2 ? max_nan(f[0], f[kWord - 1]) : f[0];
+        if (batch < kKept) sh.batch_top[batch][tid] = from_float(higher, T());
         if (!(higher <= own.m)) {  // a new maximum, or no number
             if (higher < INFINITY) {
-                const float d = own.m - higher;  // -infinity at first, with s = t = 0
-                const float e = exp_fast(d);
-                own.t = e > 0.f ? e * (own.t + own.s * d) : 0.f;
-                own.s *= e;
+                const float d = own.m == -INFINITY ? 0.f : fmaxf((own.m - higher) * kLog2e, -200.f);
+                const float e = exp2_fast(d);  // e' = e 2^d, y' = y + d
+                t = e * (t + s * d);
+                s *= e;
                 own.m = higher;
             } else {
                 own.worst = max(own.worst, key_of(higher));
             }
         }
-        float s = 0.f, t = 0.f;
+        uint64_t s2 = 0, t2 = 0;  // pairs of +0
+        const float base = own.m == -INFINITY ? 0.f : -own.m;
+        const uint64_t l2 = pair(kLog2e, kLog2e), m2 = pair(base, base);
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
             const uint32_t w[4] = {v[b].x, v[b].y, v[b].z, v[b].w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                word_values(w[i], f, T());
-#pragma unroll
-                for (int k = 0; k < kWord; ++k) {
-                    // at least -100, where e is 0: so a masked logit adds 0 and not 0 * infinity,
-                    // and so does one under a maximum of -infinity
-                    const float d = fmaxf(f[k] - own.m, -100.f);
-                    const float e = exp_fast(d);
-                    s += e;
-                    t = fmaf(e, d, t);
+            for (int i = 0; i < 4; i += 2 / kWord) {
+                float g[2];
+                if (kWord == 2) {
+                    word_values(w[i], f, T());
+                    g[0] = f[0], g[1] = f[kWord - 1];
+                } else {
+                    g[0] = __uint_as_float(w[i]), g[1] = __uint_as_float(w[i + 2 / kWord - 1]);
                 }
+                float y0, y1;
+                unpair(mul2(add2(pair(g[0], g[1]), m2), l2), y0, y1);
+                // at least -150, where e is 0: so a masked logit adds 0 and not 0 * infinity
+                y0 = fmaxf(y0, -150.f), y1 = fmaxf(y1, -150.f);
+                const uint64_t e2 = pair(exp2_fast(y0), exp2_fast(y1));
+                s2 = add2(s2, e2);
+                t2 = fma2(e2, pair(y0, y1), t2);
             }
         }
-        own.s += s;
-        own.t += t;
+        float lo, hi;
+        unpair(s2, lo, hi);
+        s += lo + hi;
+        unpair(t2, lo, hi);
+        t += lo + hi;
+    };
+    int j = tid, batch = 0;
+    for (; j + (kBatch - 1) * kScoreThreads < count; j += kBatch * kScoreThreads, ++batch) {
+        uint4 v[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) v[b] = __ldg(piece + j + b * kScoreThreads);
+        take(v, batch);
+    }
+    if (j < count) {
+        uint4 v[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int at = j + b * kScoreThreads;
+            v[b] = make_uint4(lowest_word<T>(), lowest_word<T>(), lowest_word<T>(), lowest_word<T>());
+            if (at < count) v[b] = __ldg(piece + at);
+        }
+        take(v, batch);
+    }
+    own.s = s;
+    own.t = t * kLn2;
+    if (tid < loose) {
+        const float v = to_float(x[loose_at]);
+        if (!(v < INFINITY))
+            own.worst = max(own.worst, key_of(v));
+        else if (v > -INFINITY)
+            own = add(own, Sums{v, 1.f, 0.f, 0u});
     }
     const uint32_t own_key = some ? max(key_of(own.m), own.worst) : 0u;
 
@@ -285,7 +346,7 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocksPerSm)
         const uint32_t cut = sh.cut;
         if (own_key != 0u && own_key >= cut) sh.list[atomicAdd(&sh.listed, 1)] = (uint16_t)tid;
         __syncthreads();
-        // the listed threads' logits with a key of at least `least`
+        // the listed threads' batches with a maximum of at least `least`, then their logits
         const auto collect = [&](uint32_t least) {
             const auto offer = [&](float v, int index) {
                 const uint32_t k = key_of(v);
@@ -293,10 +354,8 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocksPerSm)
                 const int at = atomicAdd(&sh.found, 1);
                 if (at < kCandidates) sh.candidate[at] = rank_of(k, index);
             };
-            const int listed = sh.listed, turns = (count + kScoreThreads - 1) / kScoreThreads;
-            for (int u = tid; u < listed * turns; u += kScoreThreads) {
-                const int at = u / listed * kScoreThreads + sh.list[u % listed];
-                if (at >= count) continue;
+            const auto offer_piece = [&](int at) {
+                if (at >= count) return;
                 const uint4 v = __ldg(piece + at);
                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
                 const int index = head + (first + at) * kPer;
@@ -307,8 +366,32 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocksPerSm)
 #pragma unroll
                     for (int k = 0; k < kWord; ++k) offer(f[k], index + i * kWord + k);
                 }
+            };
+            constexpr int kTurn = kBatch * kScoreThreads;
+            const int listed = sh.listed, turns = (count + kTurn - 1) / kTurn;
+            for (int u = tid; u < listed * turns; u += kScoreThreads) {
+                const int who = sh.list[u % listed], turn = u / listed;
+                if (turn < kKept) {
+                    if (turn * kTurn + who >= count ||
+                        key_of(to_float(sh.batch_top[turn][who])) < least)
+                        continue;
+                    const int at = atomicAdd(&sh.batches, 1);
+                    if (at < kScoreThreads) {
+                        sh.batch[at] = (uint32_t)who | (uint32_t)turn << 16;
+                        continue;
+                    }
+                }
+                // not kept, or too many for the list: here and now
+                for (int b = 0; b < kBatch; ++b) offer_piece(turn * kTurn + b * kScoreThreads + who);
             }
             if (tid < loose) offer(to_float(x[loose_at]), loose_at);
+            __syncthreads();
+            const int batches = min(sh.batches, kScoreThreads);
+            for (int u = tid; u < batches * kBatch; u += kScoreThreads) {
+                const uint32_t what = sh.batch[u / kBatch];
+                offer_piece((int)(what >> 16) * kTurn + u % kBatch * kScoreThreads +
+                            (int)(what & 0xFFFFu));
+            }
             __syncthreads();
             return sh.found;
         };
@@ -323,7 +406,7 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocksPerSm)
         int found = collect(cut);
         if (found > kCandidates) {
             __syncthreads();
-            if (tid == 0) sh.found = 0;
+            if (tid == 0) sh.found = sh.batches = 0;
             __syncthreads();
             found = cut == 0xFFFFFFFFu ? 0 : collect(cut + 1);
             for (int base = 0; found < a.top && base < part; base += kScoreThreads) {
@@ -382,7 +465,7 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocksPerSm)
         if (rank == 0) {
             const uint32_t here = smem_u32(&sh);
             for (int r = 1; r < blocks; ++r) {
-                const uint32_t there = map_to_cta(here, r) + (uint32_t)offsetof(ScoreShared, sums);
+                const uint32_t there = map_to_cta(here, r) + (uint32_t)offsetof(Shared, sums);
                 const Sums o{__uint_as_float(ld_cluster_u32(there)),
                              __uint_as_float(ld_cluster_u32(there + 4)),
                              __uint_as_float(ld_cluster_u32(there + 8)), ld_cluster_u32(there + 12)};
@@ -394,9 +477,9 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocksPerSm)
                 uint64_t mine = 0;
                 if (r < blocks) {
                     const uint32_t there = map_to_cta(here, r);
-                    const int held = (int)ld_cluster_u32(there + (uint32_t)offsetof(ScoreShared, bests));
+                    const int held = (int)ld_cluster_u32(there + (uint32_t)offsetof(Shared, bests));
                     if (k < held)
-                        mine = ld_cluster_u64(there + (uint32_t)offsetof(ScoreShared, best) + 8 * k);
+                        mine = ld_cluster_u64(there + (uint32_t)offsetof(Shared, best) + 8 * k);
                 }
                 sh.candidate[tid] = mine;  // 0: none, below all
                 __syncthreads();

@@ -159,10 +159,12 @@ constexpr int kTile = 16;                       // positions of a warp in a step
 constexpr int kStep = kTile * kAttendWarps;     // positions of a step
 constexpr float kLn2 = 0.6931471805599453f;
 
-// What a block leaves for the join: the item that begins in it and is ended
-// by the `count` blocks after it (count 0: none).
+// What is left for the join: an item that begins in block `first` and is ended
+// by the `count` blocks after it (count 0: none).  The place of an item's joint
+// is its own number where there are no more items than blocks, so that few
+// items need few join blocks, else its first block's.
 struct Joint {
-    int row, item, count, unused;
+    int row, item, count, first;
 };
 
 struct AttendArgs {
@@ -172,7 +174,8 @@ struct AttendArgs {
     float* lse;
     float* partial;     // [blocks][2][heads of an item][padded dim]
     float2* partial_ml; // [blocks][2][heads of an item]
-    Joint* joints;      // [blocks]
+    Joint* joints;      // [min(blocks, items in all)]
+    int by_item;        // whether joints are placed by their items
     int q_heads, group;
     int items;          // of a row: kv_heads * blocks of heads
     int head_blocks;    // per key-value head
@@ -353,10 +356,13 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
         while (at + (int64_t)n * a.items <= lo) at += (int64_t)n * a.items, n = steps_of(a.length(++r));
         begin = {r, (int)((lo - at) / n), (int)((lo - at) % n), n, a.length(r)};
     }
-    if (tid == 0) a.joints[blockIdx.x] = {0, 0, 0, 0};
+    if (!a.by_item && tid == 0) a.joints[blockIdx.x] = {0, 0, 0, 0};
     // rows without a position
     for (int r = blockIdx.x; r < a.c.batch; r += gridDim.x) {
         if (a.length(r) != 0) continue;
+        if (a.by_item)
+            for (int i = tid; i < a.items; i += kAttendThreads)
+                a.joints[r * a.items + i] = {0, 0, 0, 0};
         for (int h = warp; h < a.q_heads; h += kAttendWarps) {
             for (int x = lane * 8; x < dim; x += 256)
                 *reinterpret_cast<uint4*>(a.out + r * a.out_row + h * a.out_head + x) =
@@ -605,12 +611,16 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
                     if (x == 0) a.partial_ml[slot] = make_float2(m, l);
                 }
             }
-            if (!ends && side == 1 && tid == 0) {
-                const int64_t last = step + (here.steps - 1 - here.tile);  // the item's last step
-                int64_t owner = last * blocks / total;
-                while (cut(total, owner + 1, blocks) <= last) ++owner;
-                while (cut(total, owner, blocks) > last) --owner;
-                a.joints[blockIdx.x] = {here.row, here.item, (int)(owner - blockIdx.x), 0};
+            if (side == 1 && tid == 0 && (!ends || a.by_item)) {
+                int64_t owner = blockIdx.x;
+                if (!ends) {
+                    const int64_t last = step + (here.steps - 1 - here.tile);  // the item's last step
+                    owner = last * blocks / total;
+                    while (cut(total, owner + 1, blocks) <= last) ++owner;
+                    while (cut(total, owner, blocks) > last) --owner;
+                }
+                a.joints[a.by_item ? here.row * a.items + here.item : blockIdx.x] = {
+                    here.row, here.item, (int)(owner - blockIdx.x), (int)blockIdx.x};
             }
             __syncthreads();
             fresh = true;
@@ -622,8 +632,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
     copy_wait<0>();
 }
 
-// Adds up an item's parts: block (x, y) has head y of the item that begins in
-// block x of attend_kernel.  A row split over the whole GPU has some sixty
+// Adds up an item's parts: block (x, y) has head y of joint x.  A row split over the whole GPU has some sixty
 // parts a head: a thread group's first eight are read before the weights are
 // settled, and no part waits for another.  (One part at a time with running
 // maxima in between took 13 us of a 131071-position call.)
@@ -641,7 +650,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs a, int he
     if (joint.count == 0 || h >= a.heads_of(joint.item)) return;
     // part i: the first block's second slot, then the first slots of the blocks after it
     const auto slot = [&](int i) {
-        return ((int64_t)(blockIdx.x + i) * 2 + (i == 0)) * heads_padded + h;
+        return ((int64_t)(joint.first + i) * 2 + (i == 0)) * heads_padded + h;
     };
     constexpr int kAhead = 8;
     float4 u[kAhead];
@@ -742,7 +751,7 @@ Workspace plan_workspace(int64_t dim, int64_t group, const DeviceCtx& ctx) {
 }
 
 template <typename T, int DP, int NT, bool kTilePage>
-cudaError_t attend(const AttendArgs& a, cudaStream_t stream, const DeviceCtx& ctx) {
+cudaError_t attend(AttendArgs a, cudaStream_t stream, const DeviceCtx& ctx) {
     using S = AttendShape<DP, NT>;
     static std::atomic<bool> ready[64];
     int dev = 0;
@@ -759,6 +768,7 @@ cudaError_t attend(const AttendArgs& a, cudaStream_t stream, const DeviceCtx& ct
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     const unsigned blocks = (unsigned)attend_blocks(DP, NT, ctx);
+    a.by_item = (int64_t)a.c.batch * a.items <= blocks;
     cfg.gridDim = dim3(blocks);
     cfg.blockDim = dim3(kAttendThreads);
     cfg.dynamicSmemBytes = S::kSmem;
@@ -767,7 +777,7 @@ cudaError_t attend(const AttendArgs& a, cudaStream_t stream, const DeviceCtx& ct
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, attend_kernel<T, DP, NT, kTilePage>, a);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(blocks, (unsigned)a.block_heads);
+    cfg.gridDim = dim3(a.by_item ? (unsigned)(a.c.batch * a.items) : blocks, (unsigned)a.block_heads);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, join_kernel<T, DP>, a, 8 * NT);
