@@ -35,12 +35,12 @@ namespace {
 
 constexpr int kScoreThreads = 256;
 constexpr int kScoreWarps = kScoreThreads / 32;
-constexpr int kScoreBlocksPerSm = 5;
+constexpr int kScoreBlocksPerSm = 4;
 constexpr int kGroups = kScoreThreads / 4;  // of threads, for the first cut of the alternatives
-constexpr int kBatch = 4;                   // 16-byte pieces a thread has in flight
+constexpr int kBatch = 8;                   // 16-byte pieces a thread has in flight
 constexpr int kCandidates = 1024;
 constexpr int kMaxCluster = 8;
-constexpr int kKept = 32;                   // batches of a thread whose maxima are kept
+constexpr int kKept = 16;                   // batches of a thread whose maxima are kept
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -172,7 +172,7 @@ struct ScoreShared {
     Sums part[kScoreWarps];
     Sums sums;                      // of the block
     uint32_t group_key[kGroups];
-    uint32_t cut;
+    uint32_t cut, higher;
     int listed, found;
     uint16_t list[kScoreThreads];   // threads whose maximum reaches the cut
     uint64_t best[W4A16_MAX_TOP];   // the block's alternatives, in order
@@ -341,12 +341,11 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocksPerSm)
             for (int i = 0; i < kGroups; ++i)
                 before += sh.group_key[i] > mine || (sh.group_key[i] == mine && i < tid);
             if (before == a.top - 1) sh.cut = mine;
+            if (before == kGroups * 3 / 4) sh.higher = mine;  // as many groups are above it
         }
         __syncthreads();
         const uint32_t cut = sh.cut;
-        if (own_key != 0u && own_key >= cut) sh.list[atomicAdd(&sh.listed, 1)] = (uint16_t)tid;
-        __syncthreads();
-        // the listed threads' batches with a maximum of at least `least`, then their logits
+        // the batches with a maximum of at least `least`, then their logits
         const auto collect = [&](uint32_t least) {
             const auto offer = [&](float v, int index) {
                 const uint32_t k = key_of(v);
@@ -368,6 +367,9 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocksPerSm)
                 }
             };
             constexpr int kTurn = kBatch * kScoreThreads;
+            if (own_key != 0u && own_key >= least)
+                sh.list[atomicAdd(&sh.listed, 1)] = (uint16_t)tid;
+            __syncthreads();
             const int listed = sh.listed, turns = (count + kTurn - 1) / kTurn;
             for (int u = tid; u < listed * turns; u += kScoreThreads) {
                 const int who = sh.list[u % listed], turn = u / listed;
@@ -403,11 +405,16 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocksPerSm)
                    : e < before_pieces + in_pieces ? head + first * kPer + e - before_pieces
                                                    : head + pieces * kPer + e - before_pieces - in_pieces;
         };
-        int found = collect(cut);
+        // where most groups reach the cut, they do so at its value: a mask's
+        bool above = sh.higher >= cut;
+        int found = above ? 0 : collect(cut);
         if (found > kCandidates) {
+            above = true;
             __syncthreads();
-            if (tid == 0) sh.found = sh.batches = 0;
+            if (tid == 0) sh.listed = sh.found = sh.batches = 0;
             __syncthreads();
+        }
+        if (above) {
             found = cut == 0xFFFFFFFFu ? 0 : collect(cut + 1);
             for (int base = 0; found < a.top && base < part; base += kScoreThreads) {
                 const int index = index_of(min(base + tid, part - 1));
