@@ -433,7 +433,8 @@ typedef struct w4a16_query_shape {
  *              length 0.
  *   workspace  w4a16_paged_attention_workspace(cache, q_heads) bytes, 16-byte
  *              aligned, of any content; not read after the call's work is
- *              done, and not to be shared by calls that may run at once.
+ *              done, and not to be shared by calls that may run at once.  Where
+ *              that is 0 bytes, any aligned pointer other than NULL.
  * Positions whose page number is outside [0, pages) are left out, as if
  * masked.  The result does not depend on how the work was split beyond the
  * order of its FP32 sums; two calls on the same inputs give the same bits.
@@ -446,8 +447,8 @@ int w4a16_paged_attention(const void *q, const void *k_pool, const void *v_pool,
                           void *workspace, const w4a16_cache_shape *cache,
                           const w4a16_query_shape *query, void *stream);
 
-/* Bytes of workspace of w4a16_paged_attention on the current device (-1 on
- * a bad shape or device). */
+/* Bytes of workspace of w4a16_paged_attention on the current device, 0 for
+ * tables of few positions that need none (-1 on a bad shape or device). */
 int64_t w4a16_paged_attention_workspace(const w4a16_cache_shape *cache, int64_t q_heads);
 
 /*

@@ -39,7 +39,7 @@ constexpr int kScoreBlocksPerSm = 4;
 constexpr int kGroups = kScoreThreads / 4;  // of threads, for the first cut of the alternatives
 constexpr int kBatch = 8;                   // 16-byte pieces a thread has in flight
 constexpr int kCandidates = 1024;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 4;
 constexpr int kKept = 16;                   // batches of a thread whose maxima are kept
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -516,11 +516,14 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocksPerSm)
     }
 }
 
-// Blocks to a row: one where the rows alone fill the SMs, else up to eight (a
-// portable cluster), as many as keep a piece of the row for every thread.
+// Blocks to a row: one where the rows are more than half the SMs, else up to
+// four, as many as keep a piece of the row for every thread.  What a block does
+// after its pass costs more than a shorter pass saves: one row of 128256 takes
+// 9.0, 8.1 and 8.8 us by 2, 4 and 8 blocks, 64 rows 9.5 us by 2 and 16 us by 8,
+// 153 rows 15.5 us by 1 and 22 us by 4.
 int score_blocks(int64_t rows, int64_t vocabulary, int size, const DeviceCtx& ctx) {
     int blocks = 1;
-    while (blocks < kMaxCluster && rows * blocks * 2 <= 8 * ctx.num_sms &&
+    while (blocks < kMaxCluster && rows * blocks * 2 <= ctx.num_sms &&
            vocabulary * size / 16 >= (int64_t)blocks * 2 * kScoreThreads)
         blocks *= 2;
     return blocks;

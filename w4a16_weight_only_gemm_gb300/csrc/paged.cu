@@ -176,6 +176,7 @@ struct AttendArgs {
     float2* partial_ml; // [blocks][2][heads of an item]
     Joint* joints;      // [min(blocks, items in all)]
     int by_item;        // whether joints are placed by their items
+    int whole;          // whether a block takes one item, all of it: nothing to join
     int q_heads, group;
     int items;          // of a row: kv_heads * blocks of heads
     int head_blocks;    // per key-value head
@@ -326,41 +327,48 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
     grid_launch_dependents();
 
     // The line: its length, and where this block's part begins.
-    const int per = (a.c.batch + kAttendThreads - 1) / kAttendThreads;
-    const int r0 = min(tid * per, a.c.batch), r1 = min(r0 + per, a.c.batch);
-    int64_t mine = 0;
-    for (int r = r0; r < r1; ++r) mine += steps_of(a.length(r));
-    int64_t upto = mine;
+    int64_t total = 0, blocks = 0, lo = 0, hi = 0;
+    if (a.whole) {
+        const int row = blockIdx.x / a.items, n = steps_of(a.length(row));
+        if (tid == 0) begin = {row, (int)blockIdx.x % a.items, 0, n, a.length(row)};
+        hi = n;
+    } else {
+        const int per = (a.c.batch + kAttendThreads - 1) / kAttendThreads;
+        const int r0 = min(tid * per, a.c.batch), r1 = min(r0 + per, a.c.batch);
+        int64_t mine = 0;
+        for (int r = r0; r < r1; ++r) mine += steps_of(a.length(r));
+        int64_t upto = mine;
 #pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-        const int64_t o = __shfl_up_sync(~0u, upto, d);
-        if (lane >= d) upto += o;
-    }
-    if (lane == 31) scan[warp] = upto;
-    __syncthreads();
-    int64_t total = 0;
+        for (int d = 1; d < 32; d *= 2) {
+            const int64_t o = __shfl_up_sync(~0u, upto, d);
+            if (lane >= d) upto += o;
+        }
+        if (lane == 31) scan[warp] = upto;
+        __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kAttendWarps; ++w) {
-        if (w < warp) upto += scan[w];
-        total += scan[w];
+        for (int w = 0; w < kAttendWarps; ++w) {
+            if (w < warp) upto += scan[w];
+            total += scan[w];
+        }
+        total *= a.items;
+        blocks = min((int64_t)gridDim.x, total);
+        if (blockIdx.x < blocks) {
+            lo = cut(total, blockIdx.x, blocks);
+            hi = cut(total, blockIdx.x + 1, blocks);
+        }
+        if (lo < hi && (upto - mine) * a.items <= lo && lo < upto * a.items) {
+            int r = r0;
+            int64_t at = (upto - mine) * a.items;
+            int n = steps_of(a.length(r));
+            while (at + (int64_t)n * a.items <= lo) at += (int64_t)n * a.items, n = steps_of(a.length(++r));
+            begin = {r, (int)((lo - at) / n), (int)((lo - at) % n), n, a.length(r)};
+        }
     }
-    total *= a.items;
-    const int64_t blocks = min((int64_t)gridDim.x, total);
-    const bool idle = blockIdx.x >= blocks;
-    const int64_t lo = idle ? total : cut(total, blockIdx.x, blocks);
-    const int64_t hi = idle ? total : cut(total, blockIdx.x + 1, blocks);
-    if (!idle && (upto - mine) * a.items <= lo && lo < upto * a.items) {
-        int r = r0;
-        int64_t at = (upto - mine) * a.items;
-        int n = steps_of(a.length(r));
-        while (at + (int64_t)n * a.items <= lo) at += (int64_t)n * a.items, n = steps_of(a.length(++r));
-        begin = {r, (int)((lo - at) / n), (int)((lo - at) % n), n, a.length(r)};
-    }
-    if (!a.by_item && tid == 0) a.joints[blockIdx.x] = {0, 0, 0, 0};
+    if (!a.by_item && !a.whole && tid == 0) a.joints[blockIdx.x] = {0, 0, 0, 0};
     // rows without a position
     for (int r = blockIdx.x; r < a.c.batch; r += gridDim.x) {
         if (a.length(r) != 0) continue;
-        if (a.by_item)
+        if (a.by_item && !a.whole)
             for (int i = tid; i < a.items; i += kAttendThreads)
                 a.joints[r * a.items + i] = {0, 0, 0, 0};
         for (int h = warp; h < a.q_heads; h += kAttendWarps) {
@@ -370,7 +378,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
             if (a.lse && lane == 0) a.lse[(int64_t)r * a.q_heads + h] = -INFINITY;
         }
     }
-    if (idle) return;
+    if (lo == hi) return;
     __syncthreads();
 
     Place ahead = begin, here = begin;
@@ -611,7 +619,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
                     if (x == 0) a.partial_ml[slot] = make_float2(m, l);
                 }
             }
-            if (side == 1 && tid == 0 && (!ends || a.by_item)) {
+            if (side == 1 && tid == 0 && (!ends || a.by_item) && !a.whole) {
                 int64_t owner = blockIdx.x;
                 if (!ends) {
                     const int64_t last = step + (here.steps - 1 - here.tile);  // the item's last step
@@ -735,6 +743,15 @@ int attend_blocks(int64_t dim, int tiles, const DeviceCtx& ctx) {
     return std::min(kMaxParts, ctx.num_sms * per_sm[dim <= 64 ? 0 : dim <= 128 ? 1 : 2][tiles - 1]);
 }
 
+// A block takes one item, all of it, where every item finds a block and none is
+// longer than 8 steps: the second launch and its workspace cost more than the
+// steps side by side save.
+bool whole_items(const w4a16_cache_shape& c, int64_t group, const DeviceCtx& ctx) {
+    const HeadPlan heads = plan_heads(group);
+    return c.table_width * c.page_size <= 8 * kStep &&
+           c.batch * c.kv_heads * heads.blocks <= attend_blocks(c.head_dim, heads.tiles, ctx);
+}
+
 // The workspace: partial outputs, their maxima and sums, the joints.
 struct Workspace {
     int64_t partial, ml, joints, bytes;
@@ -769,14 +786,14 @@ cudaError_t attend(AttendArgs a, cudaStream_t stream, const DeviceCtx& ctx) {
     cudaLaunchConfig_t cfg = {};
     const unsigned blocks = (unsigned)attend_blocks(DP, NT, ctx);
     a.by_item = (int64_t)a.c.batch * a.items <= blocks;
-    cfg.gridDim = dim3(blocks);
+    cfg.gridDim = dim3(a.whole ? (unsigned)(a.c.batch * a.items) : blocks);
     cfg.blockDim = dim3(kAttendThreads);
     cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, attend_kernel<T, DP, NT, kTilePage>, a);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || a.whole) return e;
     cfg.gridDim = dim3(a.by_item ? (unsigned)(a.c.batch * a.items) : blocks, (unsigned)a.block_heads);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
@@ -837,7 +854,8 @@ cudaError_t launch_paged_append(const void* k, const void* v, void* k_pool, void
 
 int64_t paged_attention_workspace(const w4a16_cache_shape& cache, int64_t q_heads,
                                   const DeviceCtx& ctx) {
-    return plan_workspace(cache.head_dim, q_heads / cache.kv_heads, ctx).bytes;
+    const int64_t group = q_heads / cache.kv_heads;
+    return whole_items(cache, group, ctx) ? 0 : plan_workspace(cache.head_dim, group, ctx).bytes;
 }
 
 cudaError_t launch_paged_attention(const void* q, const void* k_pool, const void* v_pool,
@@ -859,6 +877,7 @@ cudaError_t launch_paged_attention(const void* q, const void* k_pool, const void
     a.head_blocks = heads.blocks;
     a.block_heads = heads.heads;
     a.items = (int)cache.kv_heads * heads.blocks;
+    a.whole = whole_items(cache, a.group, ctx);
     const Workspace w = plan_workspace(cache.head_dim, a.group, ctx);
     char* base = static_cast<char*>(workspace);
     a.partial = reinterpret_cast<float*>(base + w.partial);

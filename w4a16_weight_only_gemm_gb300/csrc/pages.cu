@@ -182,13 +182,18 @@ Space split_space(void* workspace, int64_t rows, int64_t pages, int64_t count) {
     return s;
 }
 
-// Gives every in-range row of the list its first request's number.
-__device__ void claim_rows(const Space& s, const int32_t* listed, int64_t count, int64_t rows,
+// Gives every in-range row of the list its first request's number.  `claim` has
+// a place a row: s.claim, or shared memory where one CTA works on few rows (a
+// round trip to L2 less for each of the steps that depend on one another).
+constexpr int kSharedRows = 4096;
+__device__ void claim_rows(int32_t* claim, const int32_t* listed, int64_t count, int64_t rows,
                            uint32_t ctas, int64_t thread, int64_t threads) {
-    for (int64_t r = thread; r < rows; r += threads) s.claim[r] = 0x7FFFFFFF;
+    for (int64_t r = thread; r < rows; r += threads) claim[r] = 0x7FFFFFFF;
     books_sync(ctas);
-    for (int64_t i = thread; i < count; i += threads)
-        if (listed[i] >= 0 && listed[i] < rows) atomicMin(&s.claim[listed[i]], (int)i);
+    for (int64_t i = thread; i < count; i += threads) {
+        const int32_t r = listed[i];
+        if (r >= 0 && r < rows) atomicMin(&claim[r], (int)i);
+    }
 }
 
 // One CTA: runs want(i) -> pages wanted (-1: refused) over the list in order and
@@ -231,9 +236,11 @@ __global__ void __launch_bounds__(kBookThreads)
     extend_kernel(Books b, const int32_t* listed, const int32_t* counts, int64_t count,
                   int32_t* done, Space s) {
     __shared__ ScanShared sh;
+    __shared__ int32_t shared_claim[kSharedRows];
     const uint32_t ctas = cluster_size(), rank = cluster_cta_rank();
     const int64_t threads = (int64_t)ctas * kBookThreads;
     const int64_t thread = (int64_t)rank * kBookThreads + threadIdx.x;
+    int32_t* const claim = ctas == 1 && b.rows <= kSharedRows ? shared_claim : s.claim;
     grid_dependency_wait();
     grid_launch_dependents();
     const int64_t n_free = sweep_pages(
@@ -242,14 +249,14 @@ __global__ void __launch_bounds__(kBookThreads)
             if (member) s.free[k] = (int32_t)p;
         });
     copy_books(b, thread, threads);
-    claim_rows(s, listed, count, b.rows, ctas, thread, threads);
+    claim_rows(claim, listed, count, b.rows, ctas, thread, threads);
     books_sync(ctas);
     if (rank == 0)
         serve_in_order(
             count, n_free,
             [&](int64_t i) -> int64_t {
                 const int64_t r = listed[i], more = counts[i];
-                if (r < 0 || r >= b.rows || s.claim[r] != i || more < 0) return -1;
+                if (r < 0 || r >= b.rows || claim[r] != i || more < 0) return -1;
                 const int64_t n = max(b.lengths_out[r], 0);
                 if (n + more > b.width * b.page_size) return -1;
                 return pages_of(n + more, b.page_size) - pages_of(n, b.page_size);
@@ -274,38 +281,55 @@ __global__ void __launch_bounds__(kBookThreads)
     }
 }
 
+// What request i of a fork reads of the books.
+struct ForkRequest {
+    int64_t from = -1, to = -1;
+    int32_t length = 0, child_length = -1, last = -1;  // last: the parent's partly filled page
+
+    __device__ void read(const Books& b, const int32_t* parents, const int32_t* children, int64_t i) {
+        from = parents[i], to = children[i];
+        if (from < 0 || from >= b.rows || to < 0 || to >= b.rows) return;
+        child_length = b.lengths_in[to];
+        length = (int32_t)min((int64_t)max(b.lengths_in[from], 0), b.width * b.page_size);
+        if (length % b.page_size)
+            last = b.tables_in[from * b.in_stride + length / b.page_size];
+    }
+};
+
 // What forking decides; the tables and the pages follow in fork_apply_kernel.
 __global__ void __launch_bounds__(kBookThreads)
     fork_plan_kernel(Books b, const int32_t* parents, const int32_t* children, int64_t count,
                      int32_t* done, Space s) {
     __shared__ ScanShared sh;
+    __shared__ int32_t shared_claim[kSharedRows];
     const uint32_t ctas = cluster_size(), rank = cluster_cta_rank();
     const int64_t threads = (int64_t)ctas * kBookThreads;
     const int64_t thread = (int64_t)rank * kBookThreads + threadIdx.x;
+    int32_t* const claim = ctas == 1 && b.rows <= kSharedRows ? shared_claim : s.claim;
     grid_dependency_wait();
     grid_launch_dependents();
+    ForkRequest early;  // of request threadIdx.x: three reads in a row, on their way with the sweep's
+    if (rank == 0 && threadIdx.x < count) early.read(b, parents, children, threadIdx.x);
     const int64_t n_free = sweep_pages(
         b.refs_in, b.pages, sh, rank, ctas, [](int32_t r) { return r <= 0; },
         [&](int64_t p, int k, bool member) {
             if (member && k < count) s.free[k] = (int32_t)p;  // one page a child at most
             if (b.refs_in != b.refs_out) b.refs_out[p] = b.refs_in[p];
         });
-    claim_rows(s, children, count, b.rows, ctas, thread, threads);
+    claim_rows(claim, children, count, b.rows, ctas, thread, threads);
     books_sync(ctas);
     if (rank == 0)
         serve_in_order(
             count, n_free,
             [&](int64_t i) -> int64_t {
-                const int64_t from = parents[i], to = children[i];
+                ForkRequest q = early;
+                if (i >= kBookThreads) q.read(b, parents, children, i);
                 s.from[i] = s.to[i] = -1;
-                if (from < 0 || from >= b.rows || to < 0 || to >= b.rows) return -1;
-                if (s.claim[to] != i || b.lengths_in[to] != 0) return -1;
-                const int64_t n = min((int64_t)max(b.lengths_in[from], 0), b.width * b.page_size);
-                s.length[i] = (int32_t)n;
-                if (n % b.page_size == 0) return 0;
-                const int32_t last = b.tables_in[from * b.in_stride + n / b.page_size];
-                if (last < 0 || last >= b.pages) return -1;
-                s.from[i] = last;
+                s.length[i] = q.length;
+                if (q.child_length != 0 || claim[q.to] != i) return -1;
+                if (q.length % b.page_size == 0) return 0;
+                if (q.last < 0 || q.last >= b.pages) return -1;
+                s.from[i] = q.last;
                 return 1;
             },
             [&](int64_t i, int64_t first, int64_t wanted) {
@@ -317,6 +341,8 @@ __global__ void __launch_bounds__(kBookThreads)
                 }
             });
     if (rank == 0 && threadIdx.x == 0) *s.next = 0;
+    if (claim != s.claim)
+        for (int64_t r = thread; r < b.rows; r += threads) s.claim[r] = claim[r];
 }
 
 // Page copies, in pieces of 16 KB.  Pieces are handed out as blocks become
@@ -487,10 +513,11 @@ __global__ void __launch_bounds__(kCopyThreads)
         copy_piece(pool, u, [&](int64_t i) { return from[i]; }, [&](int64_t i) { return to[i]; });
 }
 
-// The cluster of a books kernel: one CTA up to a sweep of pages, else eight.
+// The cluster of a books kernel: one CTA for up to a sweep of pages and as many
+// page numbers in rows to read or copy, else eight.
 template <typename... P, typename... A>
-cudaError_t launch_books(void (*kernel)(P...), int64_t pages, cudaStream_t stream, A... args) {
-    const unsigned ctas = pages <= kBookWarps * kPagesPerWarp ? 1 : 8;
+cudaError_t launch_books(void (*kernel)(P...), int64_t numbers, cudaStream_t stream, A... args) {
+    const unsigned ctas = numbers <= kBookWarps * kPagesPerWarp ? 1 : 8;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kBookThreads);
@@ -526,6 +553,11 @@ Books books_of(const PageBooks& b) {
             b.shape.out_stride, b.shape.page_size};
 }
 
+// Page numbers that a books kernel copies from one table to another.
+int64_t copied(const PageBooks& b) {
+    return b.tables_in == b.tables_out ? 0 : b.shape.rows * b.shape.width;
+}
+
 Pool pool_of(void* pool, const w4a16_pool_shape& s, int64_t pages) {
     return {static_cast<char*>(pool), s.planes, s.plane_stride, s.page_stride, s.page_bytes, pages};
 }
@@ -540,13 +572,15 @@ int64_t pages_workspace(const w4a16_books_shape& b, int64_t count) {
 
 cudaError_t launch_pages_free(const PageBooks& b, const int32_t* listed, int64_t count,
                               cudaStream_t stream) {
-    return launch_books(free_kernel, b.shape.pages, stream, books_of(b), listed, count);
+    // a warp goes through a listed row, three round trips to L2 each: eight CTAs from a few rows on
+    const int64_t rows = count <= 2 * kBookWarps ? 0 : (int64_t)1 << 40;
+    return launch_books(free_kernel, std::max({b.shape.pages, copied(b), rows}), stream, books_of(b), listed, count);
 }
 
 cudaError_t launch_pages_extend(const PageBooks& b, const int32_t* listed, const int32_t* counts,
                                 int64_t count, int32_t* done, void* workspace,
                                 cudaStream_t stream) {
-    return launch_books(extend_kernel, b.shape.pages, stream, books_of(b), listed, counts, count,
+    return launch_books(extend_kernel, std::max(b.shape.pages, copied(b)), stream, books_of(b), listed, counts, count,
                         done, split_space(workspace, b.shape.rows, b.shape.pages, count));
 }
 

@@ -174,7 +174,8 @@ def paged_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
     os = _heads(out, "out", dtype, shape)
     lse = _empty(q, (rows, q_heads), torch.float32, stream) if return_lse else None
     if rows:
-        workspace = _empty(q, _attention_workspace(cache, q_heads, dev), torch.uint8, stream)
+        size = _attention_workspace(cache, q_heads, dev)
+        workspace = _empty(q, size, torch.uint8, stream) if size else out  # 0: not looked at
         _run(dev, stream, "w4a16_paged_attention", q.data_ptr(), k_pool.data_ptr(),
              v_pool.data_ptr(), tables.data_ptr(), lengths.data_ptr(), out.data_ptr(),
              lse.data_ptr() if return_lse else None, workspace.data_ptr(), cache,
