@@ -88,6 +88,33 @@ def test_heads_and_sizes(w4lib, kv_heads, group, dim, dtype):
     check(*make(ODD, kv_heads, group, dim, 16, dtype, seed=dim + group))
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("kv_heads, group, dim", [(8, 4, 128), (4, 7, 128), (1, 1, 64), (2, 8, 64),
+                                                  (2, 16, 128), (3, 5, 96), (1, 12, 256),
+                                                  (2, 2, 256), (1, 71, 64), (5, 3, 8)])
+def test_tables_much_wider_than_the_rows(w4lib, kv_heads, group, dim, dtype):
+    """Room for 64000 positions, so rows are cut into parts wherever they end."""
+    check(*make(ODD + [1500, 70], kv_heads, group, dim, 16, dtype, seed=dim, width=4000))
+
+
+@pytest.mark.parametrize("page", [1, 13, 24, 32])
+@pytest.mark.parametrize("rows", [1, 2, 7, 29, 60])
+def test_rows_and_widths(w4lib, rows, page):
+    """Tables on both sides of every change in how the work is split."""
+    for positions in (64, 500, 1030, 2100, 4200):
+        lengths = [positions * (i + 1) // rows - i % 3 for i in range(rows)]
+        q, k, v, tables, n = make(lengths, 2, 4, 64, page, torch.float16, seed=rows)
+        narrow = check(q, k, v, tables, n)
+        wide = torch.cat([tables, torch.full((rows, 70000 // page), -1, dtype=torch.int32,
+                                             device="cuda")], 1)
+        other = w4.paged_attention(q, k, v, wide, n)
+        # split elsewhere: sums in another order, so a rounding of the output apart at most
+        assert ((narrow.double() - other.double()).abs()
+                <= 2 * UNIT[q.dtype] * narrow.double().abs() + 1e-4).all()
+    lengths[0] = 0
+    check(*make(lengths, 2, 4, 64, page, torch.float16, seed=rows))
+
+
 @pytest.mark.parametrize("layout", ["slots", "heads", "both"])
 @pytest.mark.parametrize("page", [1, 3, 8, 16, 24, 32, 48, 64, 128, 256])
 def test_pages_and_layouts(w4lib, page, layout):

@@ -158,6 +158,7 @@ constexpr int kAttendThreads = 32 * kAttendWarps;
 constexpr int kTile = 16;                       // positions of a warp in a step
 constexpr int kStep = kTile * kAttendWarps;     // positions of a step
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kMaxCluster = 8;                  // blocks to an item, without the line
 
 // What is left for the join: an item that begins in block `first` and is ended
 // by the `count` blocks after it (count 0: none).  The place of an item's joint
@@ -176,7 +177,7 @@ struct AttendArgs {
     float2* partial_ml; // [blocks][2][heads of an item]
     Joint* joints;      // [min(blocks, items in all)]
     int by_item;        // whether joints are placed by their items
-    int whole;          // whether a block takes one item, all of it: nothing to join
+    int cluster;        // blocks to an item, a cluster, where tables are short; 0: the line is cut
     int q_heads, group;
     int items;          // of a row: kv_heads * blocks of heads
     int head_blocks;    // per key-value head
@@ -306,6 +307,31 @@ __device__ __forceinline__ void advance(const AttendArgs& a, Place& p) {
     }
 }
 
+// Four values of a head's output, of sum `l` under the maximum `m` of binary exponents.
+template <typename T>
+__device__ __forceinline__ void write_out(const AttendArgs& a, int row, int head, int x,
+                                          const float4& v, float m, float l) {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (x < a.c.head_dim)
+        *reinterpret_cast<uint2*>(a.out + row * a.out_row + head * a.out_head + x) =
+            make_uint2(pack2<T>(v.x * inv, v.y * inv), pack2<T>(v.z * inv, v.w * inv));
+    if (x == 0 && a.lse)
+        a.lse[(int64_t)row * a.q_heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                 : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
 // The part [lo, hi) of the line that block `index` of `blocks` takes.
 __device__ __forceinline__ int64_t cut(int64_t total, int64_t index, int64_t blocks) {
     return total * index / blocks;
@@ -319,7 +345,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
     extern __shared__ __align__(16) unsigned char ring[];
     __shared__ int64_t scan[kAttendWarps];
     __shared__ Place begin;
-    __shared__ float2 warp_ml[kAttendWarps][kHeads];
+    __shared__ float2 warp_ml[kAttendWarps][kHeads], block_ml[kHeads];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
     const int dim = a.c.head_dim;
 
@@ -328,10 +354,13 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
 
     // The line: its length, and where this block's part begins.
     int64_t total = 0, blocks = 0, lo = 0, hi = 0;
-    if (a.whole) {
-        const int row = blockIdx.x / a.items, n = steps_of(a.length(row));
-        if (tid == 0) begin = {row, (int)blockIdx.x % a.items, 0, n, a.length(row)};
-        hi = n;
+    if (a.cluster) {
+        const int item = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster;
+        const int row = item / a.items, length = a.length(row), n = steps_of(length);
+        lo = cut(n, rank, a.cluster);
+        hi = cut(n, rank + 1, a.cluster);
+        if (tid == 0) begin = {row, item % a.items, (int)lo, n, length};
+        if (tid < kHeads) block_ml[tid] = make_float2(-INFINITY, 0.f);
     } else {
         const int per = (a.c.batch + kAttendThreads - 1) / kAttendThreads;
         const int r0 = min(tid * per, a.c.batch), r1 = min(r0 + per, a.c.batch);
@@ -364,11 +393,11 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
             begin = {r, (int)((lo - at) / n), (int)((lo - at) % n), n, a.length(r)};
         }
     }
-    if (!a.by_item && !a.whole && tid == 0) a.joints[blockIdx.x] = {0, 0, 0, 0};
+    if (!a.by_item && !a.cluster && tid == 0) a.joints[blockIdx.x] = {0, 0, 0, 0};
     // rows without a position
     for (int r = blockIdx.x; r < a.c.batch; r += gridDim.x) {
         if (a.length(r) != 0) continue;
-        if (a.by_item && !a.whole)
+        if (a.by_item && !a.cluster)
             for (int i = tid; i < a.items; i += kAttendThreads)
                 a.joints[r * a.items + i] = {0, 0, 0, 0};
         for (int h = warp; h < a.q_heads; h += kAttendWarps) {
@@ -378,8 +407,8 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
             if (a.lse && lane == 0) a.lse[(int64_t)r * a.q_heads + h] = -INFINITY;
         }
     }
-    if (lo == hi) return;
     __syncthreads();
+    if (lo == hi && (a.cluster <= 1 || begin.steps == 0)) return;
 
     Place ahead = begin, here = begin;
     const uint32_t warp_ring = smem_u32(ring) + warp * S::kTileBytes;
@@ -461,7 +490,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
         warp_ring + S::kHalf + ((lane >> 4) * 8 + lane % 8) * S::kRowBytes;
     const uint32_t v_xor = ((lane >> 3 & 1) ^ lane % 8) << 4;
 
-    load_page();
+    if (left > 0) load_page();
 #pragma unroll 1
     for (int s = 0; s < S::kStages; ++s) issue(s);
 
@@ -586,7 +615,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
                 }
             }
             __syncthreads();
-            const bool whole = ends && first_tile == 0;
+            const bool whole = ends && first_tile == 0 && a.cluster <= 1;
             const int heads = a.heads_of(here.item), side = first_tile == 0 ? 1 : 0;
             const float* parts = reinterpret_cast<const float*>(ring + stage * S::kStageBytes);
             for (int i = tid; i < heads * (DP / 4); i += kAttendThreads) {
@@ -605,21 +634,19 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
                     v.x += e * u.x, v.y += e * u.y, v.z += e * u.z, v.w += e * u.w;
                 }
                 if (whole) {
-                    const int head = a.first_head(here.item) + h;
-                    const float inv = l == 0.f ? 0.f : 1.f / l;
-                    if (x < dim)
-                        *reinterpret_cast<uint2*>(a.out + here.row * a.out_row + head * a.out_head + x) =
-                            make_uint2(pack2<T>(v.x * inv, v.y * inv), pack2<T>(v.z * inv, v.w * inv));
-                    if (x == 0 && a.lse)
-                        a.lse[(int64_t)here.row * a.q_heads + head] =
-                            l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+                    write_out<T>(a, here.row, a.first_head(here.item) + h, x, v, m, l);
+                } else if (a.cluster) {
+                    // at the ring's start, which only this thread still reads there, if any does
+                    *reinterpret_cast<float4*>(reinterpret_cast<float*>(ring) + h * DP +
+                                               (x ^ 8 * (h / 2 % 4))) = v;
+                    if (x == 0) block_ml[h] = make_float2(m, l);
                 } else {
                     const int64_t slot = ((int64_t)blockIdx.x * 2 + side) * kHeads + h;
                     *reinterpret_cast<float4*>(a.partial + slot * DP + x) = v;
                     if (x == 0) a.partial_ml[slot] = make_float2(m, l);
                 }
             }
-            if (side == 1 && tid == 0 && (!ends || a.by_item) && !a.whole) {
+            if (side == 1 && tid == 0 && (!ends || a.by_item) && !a.cluster) {
                 int64_t owner = blockIdx.x;
                 if (!ends) {
                     const int64_t last = step + (here.steps - 1 - here.tile);  // the item's last step
@@ -638,6 +665,42 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
         stage = stage + 1 == S::kStages ? 0 : stage + 1;
     }
     copy_wait<0>();
+
+    if (a.cluster > 1) {
+        // Each block adds up a part of the item's output, read from all of them.
+        cluster_sync_all();
+        const int heads = a.heads_of(begin.item);
+        const uint32_t my_ml = smem_u32(block_ml), my_out = smem_u32(ring);
+        for (int i = (int)cluster_cta_rank() * kAttendThreads + tid; i < heads * (DP / 4);
+             i += a.cluster * kAttendThreads) {
+            const int h = i / (DP / 4), x = i % (DP / 4) * 4;
+            const uint32_t offset = (h * DP + (x ^ 8 * (h / 2 % 4))) * 4;
+            float2 ml[kMaxCluster];
+            float4 u[kMaxCluster];
+            float m = -INFINITY, l = 0.f;
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r) {
+                ml[r] = make_float2(-INFINITY, 0.f);
+                u[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (r < a.cluster) {
+                    ml[r] = ld_cluster_f2(map_to_cta(my_ml + h * 8, r));
+                    u[r] = ld_cluster_f4(map_to_cta(my_out + offset, r));
+                    m = fmaxf(m, ml[r].x);
+                }
+            }
+            const float base = m == -INFINITY ? 0.f : m;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r) {
+                if (ml[r].x == -INFINITY) continue;  // no step, and nothing written at its ring's start
+                const float e = exp2_fast(ml[r].x - base);
+                l += e * ml[r].y;
+                v.x += e * u[r].x, v.y += e * u[r].y, v.z += e * u[r].z, v.w += e * u[r].w;
+            }
+            write_out<T>(a, begin.row, a.first_head(begin.item) + h, x, v, m, l);
+        }
+        cluster_sync_all();  // the others have read this block's part
+    }
 }
 
 // Adds up an item's parts: block (x, y) has head y of joint x.  A row split over the whole GPU has some sixty
@@ -712,13 +775,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs a, int he
         const float4 u = part[i][x];
         v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int head = a.first_head(joint.item) + h;
-    if (4 * x < a.c.head_dim)
-        *reinterpret_cast<uint2*>(a.out + joint.row * a.out_row + head * a.out_head + 4 * x) =
-            make_uint2(pack2<T>(v.x * inv, v.y * inv), pack2<T>(v.z * inv, v.w * inv));
-    if (x == 0 && a.lse)
-        a.lse[(int64_t)joint.row * a.q_heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    write_out<T>(a, joint.row, a.first_head(joint.item) + h, 4 * x, v, m, l);
 }
 
 // Query heads of an item and their tiles of 8: one tile up to 8 heads to a
@@ -743,13 +800,23 @@ int attend_blocks(int64_t dim, int tiles, const DeviceCtx& ctx) {
     return std::min(kMaxParts, ctx.num_sms * per_sm[dim <= 64 ? 0 : dim <= 128 ? 1 : 2][tiles - 1]);
 }
 
-// A block takes one item, all of it, where every item finds a block and none is
-// longer than 8 steps: the second launch and its workspace cost more than the
-// steps side by side save.
-bool whole_items(const w4a16_cache_shape& c, int64_t group, const DeviceCtx& ctx) {
+// Blocks to an item where tables are short, a cluster that joins its parts in
+// shared memory: no second launch and no workspace.  The largest power of two
+// that finds a place on the SMs at once and has a step each (clusters of 7
+// leave places empty: 64 items of 8 steps 10.9 us, by clusters of 4 7.4).  0,
+// and the line is cut instead, where that leaves a block too many steps, as a
+// row may be that much longer than the others: 16 where the blocks fill the
+// places (448 items of 16 steps 38 us, the line 48), else 8 (one row of 8 items,
+// 128 steps 15.9 us, the line 10.6; 64 items of 64 steps at most, spread evenly,
+// 21.6 us, the line 19.8; 8 items of 8 steps 4.8 us, the line 7.1).
+int item_cluster(const w4a16_cache_shape& c, int64_t group, const DeviceCtx& ctx) {
     const HeadPlan heads = plan_heads(group);
-    return c.table_width * c.page_size <= 8 * kStep &&
-           c.batch * c.kv_heads * heads.blocks <= attend_blocks(c.head_dim, heads.tiles, ctx);
+    const int64_t items = c.batch * c.kv_heads * heads.blocks;
+    const int64_t places = attend_blocks(c.head_dim, heads.tiles, ctx);
+    const int64_t steps = (c.table_width * c.page_size + kStep - 1) / kStep;
+    int64_t n = 1;
+    while (n < kMaxCluster && items * n * 2 <= places && n < steps) n *= 2;
+    return items <= places && steps <= n * (4 * items * n >= 3 * places ? 16 : 8) ? (int)n : 0;
 }
 
 // The workspace: partial outputs, their maxima and sums, the joints.
@@ -780,20 +847,24 @@ cudaError_t attend(AttendArgs a, cudaStream_t stream, const DeviceCtx& ctx) {
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) ready[dev].store(true, std::memory_order_release);
     }
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)a.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     const unsigned blocks = (unsigned)attend_blocks(DP, NT, ctx);
     a.by_item = (int64_t)a.c.batch * a.items <= blocks;
-    cfg.gridDim = dim3(a.whole ? (unsigned)(a.c.batch * a.items) : blocks);
+    cfg.gridDim = dim3(a.cluster ? (unsigned)(a.c.batch * a.items * a.cluster) : blocks);
     cfg.blockDim = dim3(kAttendThreads);
     cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = a.cluster > 1 ? 2 : 1;
     e = cudaLaunchKernelEx(&cfg, attend_kernel<T, DP, NT, kTilePage>, a);
-    if (e != cudaSuccess || a.whole) return e;
+    if (e != cudaSuccess || a.cluster) return e;
+    cfg.numAttrs = 1;
     cfg.gridDim = dim3(a.by_item ? (unsigned)(a.c.batch * a.items) : blocks, (unsigned)a.block_heads);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
@@ -855,7 +926,7 @@ cudaError_t launch_paged_append(const void* k, const void* v, void* k_pool, void
 int64_t paged_attention_workspace(const w4a16_cache_shape& cache, int64_t q_heads,
                                   const DeviceCtx& ctx) {
     const int64_t group = q_heads / cache.kv_heads;
-    return whole_items(cache, group, ctx) ? 0 : plan_workspace(cache.head_dim, group, ctx).bytes;
+    return item_cluster(cache, group, ctx) ? 0 : plan_workspace(cache.head_dim, group, ctx).bytes;
 }
 
 cudaError_t launch_paged_attention(const void* q, const void* k_pool, const void* v_pool,
@@ -877,7 +948,7 @@ cudaError_t launch_paged_attention(const void* q, const void* k_pool, const void
     a.head_blocks = heads.blocks;
     a.block_heads = heads.heads;
     a.items = (int)cache.kv_heads * heads.blocks;
-    a.whole = whole_items(cache, a.group, ctx);
+    a.cluster = item_cluster(cache, a.group, ctx);
     const Workspace w = plan_workspace(cache.head_dim, a.group, ctx);
     char* base = static_cast<char*>(workspace);
     a.partial = reinterpret_cast<float*>(base + w.partial);
