@@ -1,0 +1,71 @@
+"""The serving operators together: the example's best-of-n decoding against a
+dense forward pass of the same decoder that keeps every key and value.
+
+The dense pass shares the example's layers, so both round the same
+activations to fp16 at the same places; they differ by the attention's own
+rounding (2^-11 of its output) and what later layers make of it, a few units of
+2^-11 of a logit of order 1 each.  A summed log probability over `steps` tokens
+is off by at most steps * 2 * 8 * 2^-11 * max|logit|."""
+from __future__ import annotations
+
+import os
+import sys
+
+import pytest
+import torch
+
+import w4a16_weight_only_gemm_gb300 as w4
+
+sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                                "examples"))
+import paged_decode  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+def dense_logits(model, tokens):
+    """Logits at every position of one sequence, attention in FP32 over all of it."""
+    n = len(tokens)
+    group = model.q_heads // model.kv_heads
+
+    def attend(layer, q, k, v):
+        k, v = (t.float().repeat_interleave(group, 1) for t in (k, v))
+        x = torch.einsum("ihd,jhd->hij", q.float(), k) * model.head_dim ** -0.5
+        later = torch.ones(n, n, device="cuda").triu(1).bool()
+        p = torch.softmax(x.masked_fill(later, -torch.inf), -1)
+        return torch.einsum("hij,jhd->ihd", p, v).half()
+
+    return model.forward(paged_decode.ints(tokens), paged_decode.ints(list(range(n))), attend)
+
+
+@pytest.mark.parametrize("page_size, n, steps", [(16, 4, 12), (1, 2, 5), (13, 3, 20)])
+def test_best_of_n(w4lib, page_size, n, steps):
+    model = paged_decode.Decoder()
+    prompts = [[(7 * i + j * j) % 1024 for j in range(m)] for i, m in enumerate((37, 1, 64, 16))]
+    cache = w4.PagedCache(len(model.layers), len(prompts) * n, 2000 // page_size, model.kv_heads,
+                          model.head_dim, page_size=page_size, max_length=128)
+    answers, rows = paged_decode.best_of(model, cache, prompts, n, steps, seed=n)
+    for prompt, (tokens, score) in zip(prompts, answers):
+        logits = dense_logits(model, prompt + tokens[:-1])[len(prompt) - 1:].float()
+        want = torch.log_softmax(logits.double(), 1)[range(steps), tokens].sum().item()
+        assert abs(score - want) <= steps * 2 * 8 * 2.0 ** -11 * logits.abs().max().item()
+    # the kept rows alone hold pages, each its own, drawn together from 0 on
+    assert [r for r, m in enumerate(cache.lengths.tolist()) if m] == rows
+    assert cache.lengths[rows].tolist() == [len(p) + steps - 1 for p in prompts]
+    pages = sum(-(-(len(p) + steps - 1) // page_size) for p in prompts)
+    assert sorted(p for p in cache.tables.flatten().tolist() if p >= 0) == list(range(pages))
+    assert cache.refs.tolist() == [1] * pages + [0] * (cache.refs.numel() - pages)
+
+
+def test_too_few_pages(w4lib):
+    model = paged_decode.Decoder(layers=1)
+    cache = w4.PagedCache(1, 4, 3, model.kv_heads, model.head_dim, max_length=64)
+    with pytest.raises(RuntimeError, match="prompts"):
+        paged_decode.best_of(model, cache, [[1] * 60], 4, 3)
+    with pytest.raises(RuntimeError, match="branches"):
+        paged_decode.best_of(model, cache, [[1] * 20], 4, 3)
+
+
+def test_the_example_runs(w4lib, capsys):
+    paged_decode.main()
+    assert "pages held" in capsys.readouterr().out

@@ -389,6 +389,14 @@ class PagedCache:
     def _all(self):
         return self.refs, self.tables, self.lengths
 
+    def keys(self, layer: int) -> torch.Tensor:
+        """A layer's key pool [pages, page_size, kv_heads, head_dim]."""
+        return self.pool[2 * layer]
+
+    def values(self, layer: int) -> torch.Tensor:
+        """A layer's value pool [pages, page_size, kv_heads, head_dim]."""
+        return self.pool[2 * layer + 1]
+
     def extend(self, rows: torch.Tensor, counts: torch.Tensor, stream=None) -> torch.Tensor:
         """Room for counts[i] more positions in rows[i]; returns done (pages_extend)."""
         return pages_extend(*self._all(), rows, counts, self.page_size, out=self._all(),
@@ -399,7 +407,7 @@ class PagedCache:
                stream=None) -> None:
         """New tokens of every row (or of the listed ones) of one layer (paged_append)."""
         tables = self.tables if rows is None else self.tables.index_select(0, rows)
-        paged_append(k, v, self.pool[2 * layer], self.pool[2 * layer + 1], tables, starts, offsets,
+        paged_append(k, v, self.keys(layer), self.values(layer), tables, starts, offsets,
                      stream=stream)
 
     def attend(self, layer: int, q: torch.Tensor, rows: torch.Tensor | None = None,
@@ -408,7 +416,7 @@ class PagedCache:
         tables, lengths = self.tables, self.lengths
         if rows is not None:
             tables, lengths = tables.index_select(0, rows), lengths.index_select(0, rows)
-        return paged_attention(q, self.pool[2 * layer], self.pool[2 * layer + 1], tables, lengths,
+        return paged_attention(q, self.keys(layer), self.values(layer), tables, lengths,
                                scale=scale, out=out, stream=stream)
 
     def fork(self, parents: torch.Tensor, children: torch.Tensor, stream=None) -> torch.Tensor:
