@@ -410,7 +410,8 @@ int w4a16_paged_append(const void *k, const void *v, void *k_pool, void *v_pool,
                        void *stream);
 
 /* The queries and outputs of w4a16_paged_attention: q_heads a multiple of
- * kv_heads (at most 1024); strides in elements, multiples of 8. */
+ * kv_heads (at most 1024), batch * table_width * page_size * q_heads at most
+ * 2^43; strides in elements, multiples of 8. */
 typedef struct w4a16_query_shape {
     int64_t q_heads;
     int64_t q_row_stride, q_head_stride, out_row_stride, out_head_stride;

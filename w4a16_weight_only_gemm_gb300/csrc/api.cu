@@ -73,6 +73,12 @@ bool good_cache(const w4a16_cache_shape& c) {
            (c.batch == 1 || (c.table_stride >= 0 && c.table_stride <= (int64_t)1 << 40));
 }
 
+// Whether the attention's steps (64 positions of at most q_heads items) can be counted: at most
+// 2^43 positions over a grid of a hundred blocks or more leaves a block less than 2^31.
+bool good_steps(const w4a16_cache_shape& c, int64_t q_heads) {
+    return c.batch * c.table_width * c.page_size <= ((int64_t)1 << 43) / q_heads;
+}
+
 bool good_books(const w4a16_books_shape& b) {
     return b.pages >= 1 && b.pages < (int64_t)1 << 31 && b.rows >= 1 && b.rows <= (int64_t)1 << 24 &&
            b.width >= 1 && b.width <= (int64_t)1 << 24 && b.rows * b.width <= (int64_t)1 << 40 &&
@@ -382,7 +388,7 @@ int w4a16_paged_append(const void* k, const void* v, void* k_pool, void* v_pool,
 
 int64_t w4a16_paged_attention_workspace(const w4a16_cache_shape* cache, int64_t q_heads) {
     if (!cache || !good_cache(*cache) || q_heads < 1 || q_heads > 1024 ||
-        q_heads % cache->kv_heads != 0)
+        q_heads % cache->kv_heads != 0 || !good_steps(*cache, q_heads))
         return -1;
     DeviceCtx ctx;
     if (device_ctx(&ctx)) return -1;
@@ -396,7 +402,8 @@ int w4a16_paged_attention(const void* q, const void* k_pool, const void* v_pool,
     if (!q || !k_pool || !v_pool || !tables || !lengths || !out || !workspace || !cache || !query)
         return W4A16_ERR_NULL;
     if (!good_cache(*cache) || query->q_heads < 1 || query->q_heads > 1024 ||
-        query->q_heads % cache->kv_heads != 0 || !(query->scale == query->scale))
+        query->q_heads % cache->kv_heads != 0 || !good_steps(*cache, query->q_heads) ||
+        !(query->scale == query->scale))
         return W4A16_ERR_SHAPE;
     if (!good_stride(cache->batch, query->q_row_stride) ||
         !good_stride(query->q_heads, query->q_head_stride) ||

@@ -158,6 +158,7 @@ constexpr int kAttendThreads = 32 * kAttendWarps;
 constexpr int kTile = 16;                       // positions of a warp in a step
 constexpr int kStep = kTile * kAttendWarps;     // positions of a step
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 8.f;                   // a weight is at most 2^8
 constexpr int kMaxCluster = 8;                  // blocks to an item, without the line
 
 // What is left for the join: an item that begins in block `first` and is ended
@@ -188,6 +189,9 @@ struct AttendArgs {
 
     __device__ int length(int row) const {
         return min(max(lengths[row], 0), c.width * c.page_size.value);
+    }
+    __device__ int64_t head_offset(int item) const {
+        return (int64_t)(item / head_blocks) * c.head_stride;
     }
     __device__ int first_head(int item) const {
         return item / head_blocks * group + item % head_blocks * block_heads;
@@ -290,6 +294,7 @@ struct AttendShape {
 // A place on the line of steps.
 struct Place {
     int row, item, tile, steps, length;
+    int64_t head;  // of the item's keys and values in their pools
 };
 
 __device__ __forceinline__ int steps_of(int length) { return (length + kStep - 1) / kStep; }
@@ -297,8 +302,9 @@ __device__ __forceinline__ int steps_of(int length) { return (length + kStep - 1
 __device__ __forceinline__ void advance(const AttendArgs& a, Place& p) {
     if (++p.tile < p.steps) return;
     p.tile = 0;
-    if (++p.item < a.items) return;
-    p.item = 0;
+    p.item = p.item + 1 == a.items ? 0 : p.item + 1;
+    p.head = a.head_offset(p.item);
+    if (p.item) return;
     p.steps = 0;
     while (++p.row < a.c.batch) {
         p.length = a.length(p.row);
@@ -359,7 +365,8 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
         const int row = item / a.items, length = a.length(row), n = steps_of(length);
         lo = cut(n, rank, a.cluster);
         hi = cut(n, rank + 1, a.cluster);
-        if (tid == 0) begin = {row, item % a.items, (int)lo, n, length};
+        if (tid == 0)
+            begin = {row, item % a.items, (int)lo, n, length, a.head_offset(item % a.items)};
         if (tid < kHeads) block_ml[tid] = make_float2(-INFINITY, 0.f);
     } else {
         const int per = (a.c.batch + kAttendThreads - 1) / kAttendThreads;
@@ -390,7 +397,8 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
             int64_t at = (upto - mine) * a.items;
             int n = steps_of(a.length(r));
             while (at + (int64_t)n * a.items <= lo) at += (int64_t)n * a.items, n = steps_of(a.length(++r));
-            begin = {r, (int)((lo - at) / n), (int)((lo - at) % n), n, a.length(r)};
+                const int item = (int)((lo - at) / n);
+            begin = {r, item, (int)((lo - at) % n), n, a.length(r), a.head_offset(item)};
         }
     }
     if (!a.by_item && !a.cluster && tid == 0) a.joints[blockIdx.x] = {0, 0, 0, 0};
@@ -413,7 +421,8 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
     Place ahead = begin, here = begin;
     const uint32_t warp_ring = smem_u32(ring) + warp * S::kTileBytes;
     uint32_t flags = 0;      // two bits a tile in flight: whether positions g and g + 8 count
-    int64_t left = hi - lo;  // steps to issue
+    const int count = (int)(hi - lo);
+    int left = count;        // steps to issue
     int next_page = -1;      // of the tile to issue next: the warp's, or of position `lane`
 
     const auto load_page = [&]() {
@@ -430,7 +439,6 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
         if (left > 0) {
             --left;
             const int first = ahead.tile * kStep + warp * kTile;
-            const int64_t head = (int64_t)(ahead.item / a.head_blocks) * a.c.head_stride;
             const bool there = (uint32_t)next_page < (uint32_t)a.c.pages;
             const uint32_t dst = warp_ring + stage * S::kStageBytes + row0 * S::kRowBytes;
             // the swizzle of row r: K's pieces meet 4 to a row in a read, V's 8 to a row
@@ -444,7 +452,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
             if (kTilePage) {
                 const int slot = a.c.page_size.remainder(first);
                 const int64_t at =
-                    next_page * a.c.page_stride + (slot + row0) * a.c.slot_stride + head + 8 * piece;
+                    next_page * a.c.page_stride + (slot + row0) * a.c.slot_stride + ahead.head + 8 * piece;
                 const int n = there ? ahead.length - first : 0;  // positions that count
                 const uint16_t *k = a.k_pool + at, *v = a.v_pool + at;
                 const int64_t next = kRows * a.c.slot_stride;
@@ -466,7 +474,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
                 const int p = first + lane % kTile;
                 const int64_t at = there ? next_page * a.c.page_stride +
                                                a.c.page_size.remainder(p) * a.c.slot_stride +
-                                               head
+                                               ahead.head
                                          : -1;
                 flags |= (uint32_t)(__shfl_sync(~0u, at, g) >= 0) |
                          (uint32_t)(__shfl_sync(~0u, at, g + 8) >= 0) << 1;
@@ -499,7 +507,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
     bool fresh = true;
     int first_tile = 0, stage = 0;
 #pragma unroll 1
-    for (int64_t step = lo; step < hi; ++step) {
+    for (int step = 0; step < count; ++step) {
         if (fresh) {
             fresh = false;
             first_tile = here.tile;
@@ -544,33 +552,52 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
 #pragma unroll
             for (int x = 0; x < 4; ++x) c[n][x] += c2[n][x];
         const uint32_t bits = flags >> (2 * (S::kStages - 1));
-        uint32_t p_hi[NT][2], p_lo[NT][2];
+        // binary exponents under the maximum so far; masked positions -infinity
+        bool low = true;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            float keep[2];
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {  // heads 2t and 2t + 1
-                const float s0 = bits & 1 ? c[n][x] * a.scale_log2 : -INFINITY;
-                const float s1 = bits & 2 ? c[n][x + 2] * a.scale_log2 : -INFINITY;
-                float m = fmaxf(s0, s1);
-                m = fmaxf(m, __shfl_xor_sync(~0u, m, 4));
-                m = fmaxf(m, __shfl_xor_sync(~0u, m, 8));
-                m = fmaxf(m, __shfl_xor_sync(~0u, m, 16));
-                m = fmaxf(m, top[n][x]);
-                const float base = m == -INFINITY ? 0.f : m;  // nothing yet: every weight is 0
-                keep[x] = exp2_fast(top[n][x] - base);
-                top[n][x] = m;
-                c[n][x] = exp2_fast(s0 - base);
-                c[n][x + 2] = exp2_fast(s1 - base);
-                sum[n][x] = sum[n][x] * keep[x] + (c[n][x] + c[n][x + 2]);
+            for (int x = 0; x < 4; ++x) {
+                const float y = fmaf(c[n][x], a.scale_log2, -top[n][x & 1]);
+                c2[n][x] = bits >> (x >> 1) & 1 ? y : -INFINITY;
+                low = low && c2[n][x] <= kSlack;
             }
-            if (__any_sync(~0u, keep[0] != 1.f || keep[1] != 1.f)) {
+        if (!__all_sync(~0u, low)) {
+            // A new maximum.  One up to 2^8 above the old is let be: sums under it lose
+            // nothing, and after a row's first tiles this is rarely entered.
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float keep[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {  // heads 2t and 2t + 1
+                    const float s0 = bits & 1 ? c[n][x] * a.scale_log2 : -INFINITY;
+                    const float s1 = bits & 2 ? c[n][x + 2] * a.scale_log2 : -INFINITY;
+                    float m = fmaxf(s0, s1);
+                    m = fmaxf(m, __shfl_xor_sync(~0u, m, 4));
+                    m = fmaxf(m, __shfl_xor_sync(~0u, m, 8));
+                    m = fmaxf(m, __shfl_xor_sync(~0u, m, 16));
+                    m = fmaxf(m, top[n][x]);
+                    const float base = m == -INFINITY ? 0.f : m;  // nothing yet: every weight is 0
+                    keep[x] = exp2_fast(top[n][x] - base);
+                    top[n][x] = m;
+                    sum[n][x] *= keep[x];
+                    c2[n][x] = s0 - base;
+                    c2[n][x + 2] = s1 - base;
+                }
 #pragma unroll
                 for (int i = 0; i < DP / 16; ++i) {
                     o[n][i][0] *= keep[0], o[n][i][1] *= keep[1];
                     o[n][i][2] *= keep[0], o[n][i][3] *= keep[1];
                 }
             }
+        }
+        uint32_t p_hi[NT][2], p_lo[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) c[n][x] = exp2_fast(c2[n][x]);
+            sum[n][0] += c[n][0] + c[n][2];
+            sum[n][1] += c[n][1] + c[n][3];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {  // positions g and g + 8
                 const uint32_t hi16 = pack2<T>(c[n][2 * r], c[n][2 * r + 1]);
@@ -592,7 +619,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
         __syncwarp();  // the tile is read: its slot may be filled again
 
         const bool ends = here.tile == here.steps - 1;
-        if (ends || step == hi - 1) {
+        if (ends || step == count - 1) {
             // The warps' parts meet in the slots of the tiles just read.
             // (dims 16i + g and 16i + g + 8 of heads 2t, 2t + 1; swizzled by the head)
             float* mine_out = reinterpret_cast<float*>(ring + stage * S::kStageBytes +
@@ -649,7 +676,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
             if (side == 1 && tid == 0 && (!ends || a.by_item) && !a.cluster) {
                 int64_t owner = blockIdx.x;
                 if (!ends) {
-                    const int64_t last = step + (here.steps - 1 - here.tile);  // the item's last step
+                    const int64_t last = lo + step + (here.steps - 1 - here.tile);  // the item's last step
                     owner = last * blocks / total;
                     while (cut(total, owner + 1, blocks) <= last) ++owner;
                     while (cut(total, owner, blocks) > last) --owner;
