@@ -288,7 +288,9 @@ struct AttendShape {
     // 192 KB of ring an SM: as many blocks as registers allow
     static constexpr int kBlocksPerSm = DP == 64 ? (NT == 1 ? 4 : 3) : DP == 128 ? (NT == 1 ? 3 : 2) : 1;
     static constexpr int kStages = 192 * 1024 / kBlocksPerSm / kStageBytes;
-    static constexpr int kSmem = kStages * kStageBytes;
+    // behind the ring, the queries of as many items
+    static constexpr int kQueryBytes = 8 * NT * kRowBytes;
+    static constexpr int kSmem = kStages * (kStageBytes + kQueryBytes);
 };
 
 // A place on the line of steps.
@@ -434,10 +436,30 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
     constexpr int kPieces = DP / 8, kRows = 32 / kPieces;
     const int piece = lane % kPieces, row0 = lane / kPieces;
     const bool in_dim = piece * 8 < dim;
+    // The queries of an item come with its first tile: every warp copies all of them to the same
+    // place, and each waits for its own copies only.  (Read from memory at the item's start they
+    // held up its first tile.)
+    const uint32_t queries = smem_u32(ring) + S::kStages * S::kStageBytes;
+    int ahead_item = 0, here_item = 0;  // places of the items being issued and taken
+    bool ahead_fresh = true;
+    const auto issue_queries = [&]() {
+        const int heads = a.heads_of(ahead.item);
+        const uint16_t* src = a.q + ahead.row * a.q_row +
+                              (int64_t)a.first_head(ahead.item) * a.q_head + 8 * piece;
+        const uint32_t dst = queries + ahead_item * S::kQueryBytes + row0 * S::kRowBytes;
+#pragma unroll
+        for (int r = 0; r < kHeads; r += kRows) {
+            const int h = row0 + r;
+            const bool in = h < heads && in_dim;
+            copy16(dst + r * S::kRowBytes + ((piece ^ ((h & 1) << 2 | (h >> 1 & 3))) << 4),
+                   in ? src + h * a.q_head : a.q, in);
+        }
+    };
     const auto issue = [&](int stage) {
         flags <<= 2;
         if (left > 0) {
             --left;
+            if (ahead_fresh) issue_queries();
             const int first = ahead.tile * kStep + warp * kTile;
             const bool there = (uint32_t)next_page < (uint32_t)a.c.pages;
             const uint32_t dst = warp_ring + stage * S::kStageBytes + row0 * S::kRowBytes;
@@ -487,6 +509,8 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
                 }
             }
             advance(a, ahead);
+            ahead_fresh = ahead.tile == 0;
+            if (ahead_fresh) ahead_item = ahead_item + 1 == S::kStages ? 0 : ahead_item + 1;
             if (left > 0) load_page();
         }
         copy_commit();
@@ -508,19 +532,17 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
     int first_tile = 0, stage = 0;
 #pragma unroll 1
     for (int step = 0; step < count; ++step) {
+        copy_wait<S::kStages - 1>();
+        __syncwarp();
         if (fresh) {
             fresh = false;
             first_tile = here.tile;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const int h = 8 * n + g;
-                const bool in = h < a.heads_of(here.item);
-                const uint16_t* src =
-                    a.q + here.row * a.q_row + (a.first_head(here.item) + (in ? h : 0)) * a.q_head + 8 * t;
 #pragma unroll
                 for (int j = 0; j < DP / 32; ++j)
-                    q[n][j] = in && 32 * j + 8 * t < dim ? *reinterpret_cast<const uint4*>(src + 32 * j)
-                                                         : make_uint4(0, 0, 0, 0);
+                    q[n][j] = lds128(queries + here_item * S::kQueryBytes +
+                                     (8 * n + g) * S::kRowBytes + (k_xor ^ (64 * j)));
                 top[n][0] = top[n][1] = -INFINITY;
                 sum[n][0] = sum[n][1] = 0.f;
 #pragma unroll
@@ -528,9 +550,8 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
 #pragma unroll
                     for (int x = 0; x < 4; ++x) o[n][i][x] = 0.f;
             }
+            here_item = here_item + 1 == S::kStages ? 0 : here_item + 1;
         }
-        copy_wait<S::kStages - 1>();
-        __syncwarp();
         const uint32_t at = stage * S::kStageBytes;
         float c[NT][4], c2[NT][4];  // two chains
 #pragma unroll
