@@ -472,10 +472,15 @@ typedef struct w4a16_pool_shape {
     int64_t planes, plane_stride, page_stride, page_bytes;
 } w4a16_pool_shape;
 
-/* Bytes of workspace of w4a16_pages_extend, _fork and _compact for `count`
- * requests (0 for compact); 16-byte aligned, of any content, as the
- * attention's. */
+/* Bytes of workspace of w4a16_pages_extend for `count` requests, and of
+ * w4a16_pages_fork and w4a16_pages_compact, where small pools need none (0)
+ * if every `out` tensor is apart from its `in` tensor (apart = 1).  16-byte
+ * aligned, of any content, as the attention's; -1 on a bad shape. */
 int64_t w4a16_pages_workspace(const w4a16_books_shape *books, int64_t count);
+int64_t w4a16_pages_fork_workspace(const w4a16_books_shape *books, const w4a16_pool_shape *shape,
+                                   int64_t count, int32_t apart);
+int64_t w4a16_pages_compact_workspace(const w4a16_books_shape *books,
+                                      const w4a16_pool_shape *shape, int32_t apart);
 
 /*
  * w4a16_pages_free -- gives back every page of the `count` rows listed: one

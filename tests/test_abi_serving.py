@@ -149,3 +149,15 @@ def test_logprobs_arguments(lib):
         assert call(**bad) == 2
     assert call(FAKE + 1, *[FAKE] * 5) == 3
     assert call(FAKE + 2, *[FAKE] * 5, type=2) == 3
+
+
+def test_pages_workspaces(lib):
+    """Small pools need none where the books are written apart; else both ask for some."""
+    fork, compact = lib.w4a16_pages_fork_workspace, lib.w4a16_pages_compact_workspace
+    assert fork(books(), pool(), 2, 1) == 0 and compact(books(), pool(), 1) == 0
+    assert fork(books(), pool(), 2, 0) > 0 and compact(books(), pool(), 0) > 0
+    large = books(pages=100000)
+    assert fork(large, pool(), 2, 1) > 0 and compact(large, pool(), 1) > 0
+    assert fork(books(pages=0), pool(), 2, 1) == -1 and fork(books(), pool(size=8), 2, 1) == -1
+    assert fork(books(), pool(), -1, 1) == -1 and fork(None, pool(), 2, 1) == -1
+    assert compact(books(), None, 1) == -1

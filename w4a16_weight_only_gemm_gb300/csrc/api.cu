@@ -424,6 +424,20 @@ int64_t w4a16_pages_workspace(const w4a16_books_shape* books, int64_t count) {
     return books && good_books(*books) && good_count(count) ? pages_workspace(*books, count) : -1;
 }
 
+int64_t w4a16_pages_fork_workspace(const w4a16_books_shape* books, const w4a16_pool_shape* shape,
+                                   int64_t count, int32_t apart) {
+    return books && shape && good_books(*books) && good_pool(*shape) && good_count(count)
+               ? pages_fork_workspace(*books, *shape, count, apart != 0)
+               : -1;
+}
+
+int64_t w4a16_pages_compact_workspace(const w4a16_books_shape* books,
+                                      const w4a16_pool_shape* shape, int32_t apart) {
+    return books && shape && good_books(*books) && good_pool(*shape)
+               ? pages_compact_workspace(*books, *shape, apart != 0)
+               : -1;
+}
+
 int w4a16_pages_free(const int32_t* refs_in, const int32_t* tables_in, const int32_t* lengths_in,
                      const int32_t* listed, int64_t count, int32_t* refs_out, int32_t* tables_out,
                      int32_t* lengths_out, const w4a16_books_shape* books, void* stream) {

@@ -107,6 +107,10 @@ struct PageBooks {
     w4a16_books_shape shape;
 };
 int64_t pages_workspace(const w4a16_books_shape& books, int64_t count);
+int64_t pages_fork_workspace(const w4a16_books_shape& books, const w4a16_pool_shape& shape,
+                             int64_t count, bool apart);
+int64_t pages_compact_workspace(const w4a16_books_shape& books, const w4a16_pool_shape& shape,
+                                bool apart);
 cudaError_t launch_pages_free(const PageBooks& books, const int32_t* listed, int64_t count,
                               cudaStream_t stream);
 cudaError_t launch_pages_extend(const PageBooks& books, const int32_t* listed,

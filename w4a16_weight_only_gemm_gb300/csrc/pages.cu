@@ -475,15 +475,16 @@ __global__ void __launch_bounds__(kBookThreads)
     }
 }
 
-__global__ void __launch_bounds__(kCopyThreads)
-    compact_apply_kernel(Books b, const int32_t* used, Space s, Pool pool) {
-    grid_dependency_wait();
+// The books of a compaction: pair i moves page high(copies - 1 - i) to page hole(i); place(p) is
+// the place of a moving page p in `high`, anything for another page.
+template <typename High, typename Hole, typename Place>
+__device__ void compact_books(const Books& b, int64_t n, int64_t copies, High high, Hole hole,
+                              Place place) {
     const int64_t thread = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x;
     const int64_t threads = (int64_t)gridDim.x * kCopyThreads;
-    const int64_t copies = *s.copies, n = used[0];
     // a pair's two counts belong to one thread, so `out` may be `in`
     for (int64_t i = thread; i < copies; i += threads) {
-        const int32_t src = s.high[copies - 1 - i], dst = s.free[i];
+        const int32_t src = high(copies - 1 - i), dst = hole(i);
         const int32_t held = b.refs_in[src];
         b.refs_out[dst] = held;
         b.refs_out[src] = 0;
@@ -496,13 +497,167 @@ __global__ void __launch_bounds__(kCopyThreads)
             int32_t p = b.tables_in[r * b.in_stride + j];
             // a number n or above that no count holds is left as it is
             if (p >= n && p < b.pages) {
-                const int32_t k = s.place[p];
-                if (k >= 0 && k < copies && s.high[k] == p) p = s.free[copies - 1 - k];
+                const int32_t k = place(p);
+                if (k >= 0 && k < copies && high(k) == p) p = hole(copies - 1 - k);
             }
             b.tables_out[r * b.out_stride + j] = p;
         }
+}
+
+__global__ void __launch_bounds__(kCopyThreads)
+    compact_apply_kernel(Books b, const int32_t* used, Space s, Pool pool) {
+    grid_dependency_wait();
+    const int64_t copies = *s.copies;
+    compact_books(b, used[0], copies, [&](int64_t k) { return s.high[k]; },
+                  [&](int64_t i) { return s.free[i]; }, [&](int64_t p) { return s.place[p]; });
     copy_pages(pool, copies, s.next, [&](int64_t i) { return s.high[copies - 1 - i]; },
                [&](int64_t i) { return s.free[i]; });
+}
+
+// ---------------------------------------------------------------------------
+// One launch for small pools.  Every block reads the counts of all pages and
+// comes to the same lists, in shared memory; so nothing has to wait for a plan,
+// and there is no workspace.  Only where the books are written apart from the
+// ones read (another block may still be reading), and where the copies are few
+// enough to be shared out beforehand.
+// ---------------------------------------------------------------------------
+constexpr int kAloneWarps = kCopyThreads / 32;
+constexpr int kAlonePages = kAloneWarps * kPagesPerWarp;  // a sweep of one block
+constexpr int kAloneRows = 16384, kAloneCount = kCopyThreads;
+constexpr int64_t kAloneBytes = (int64_t)128 << 20;  // of copies
+
+// sweep_pages by one block on its own, for up to kAlonePages pages.
+template <typename In, typename Visit>
+__device__ __forceinline__ int sweep_alone(const int32_t* refs, int64_t pages, int (&total)[kAloneWarps],
+                                           In in, Visit visit) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    uint32_t mask[kPagesPerLane];
+    int count = 0;
+#pragma unroll
+    for (int k = 0; k < kPagesPerLane; ++k) {
+        const int p = warp * kPagesPerWarp + 32 * k + lane;
+        mask[k] = __ballot_sync(~0u, p < pages && in(refs[p < pages ? p : 0]));
+        count += __popc(mask[k]);
+    }
+    if (lane == 0) total[warp] = count;
+    __syncthreads();
+    int at = 0, sum = 0;
+#pragma unroll
+    for (int w = 0; w < kAloneWarps; ++w) {
+        if (w < warp) at += total[w];
+        sum += total[w];
+    }
+#pragma unroll
+    for (int k = 0; k < kPagesPerLane; ++k) {
+        const int p = warp * kPagesPerWarp + 32 * k + lane;
+        if (p < pages) visit(p, at + __popc(mask[k] & ((1u << lane) - 1)), (mask[k] >> lane) & 1u, sum);
+        at += __popc(mask[k]);
+    }
+    return sum;
+}
+
+__global__ void __launch_bounds__(kCopyThreads)
+    compact_alone_kernel(Books b, int32_t* used, Pool pool) {
+    __shared__ uint16_t hole[kAlonePages / 2], high[kAlonePages / 2], place[kAlonePages];
+    __shared__ int total[kAloneWarps], moves;
+    if (threadIdx.x == 0) moves = 0;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int n = sweep_alone(
+        b.refs_in, b.pages, total, [](int32_t r) { return r > 0; },
+        [&](int p, int k, bool member, int n) {
+            if (p < n && !member) hole[p - k] = (uint16_t)p;
+            if (p >= n && member) {
+                high[n - 1 - k] = (uint16_t)p;
+                place[p] = (uint16_t)(n - 1 - k);
+            }
+            if (p == n - 1) moves = p + 1 - k - (member ? 1 : 0);
+        });
+    __syncthreads();
+    const int copies = moves;
+    if (blockIdx.x == 0 && threadIdx.x == 0) used[0] = n;
+    compact_books(b, n, copies, [&](int64_t k) { return (int32_t)high[k]; },
+                  [&](int64_t i) { return (int32_t)hole[i]; },
+                  [&](int64_t p) { return (int32_t)place[p]; });
+    const int64_t units = copies * pool.planes * pool.pieces();
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x)
+        copy_piece(pool, u, [&](int64_t i) { return (int64_t)high[copies - 1 - i]; },
+                   [&](int64_t i) { return (int64_t)hole[i]; });
+}
+
+__global__ void __launch_bounds__(kCopyThreads)
+    fork_alone_kernel(Books b, const int32_t* parents, const int32_t* children, int64_t count,
+                      int32_t* done, Pool pool) {
+    __shared__ int total[kAloneWarps], wanted_total[kAloneWarps];
+    __shared__ uint16_t free[kAloneCount];
+    __shared__ int32_t child[kAloneCount], parent[kAloneCount], length[kAloneCount];
+    __shared__ int32_t from[kAloneCount], to[kAloneCount];
+    __shared__ uint32_t forked[kAloneRows / 32];  // a bit a row
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    for (int i = tid; i < kAloneRows / 32; i += kCopyThreads) forked[i] = 0;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    ForkRequest q;  // of request tid
+    if (tid < count) q.read(b, parents, children, tid);
+    child[tid] = q.to >= 0 && q.to < b.rows ? (int32_t)q.to : -1;
+    const int n_free = sweep_alone(
+        b.refs_in, b.pages, total, [](int32_t r) { return r <= 0; },
+        [&](int p, int k, bool member, int) {
+            if (member && k < kAloneCount) free[k] = (uint16_t)p;
+        });
+    int want = -1;
+    if (q.child_length == 0) {
+        want = q.length % b.page_size == 0 ? 0 : q.last >= 0 && q.last < b.pages ? 1 : -1;
+        for (int j = 0; j < tid; ++j)
+            if (child[j] == child[tid]) want = -1;  // listed before
+    }
+    const uint32_t mask = __ballot_sync(~0u, want > 0);
+    if (lane == 0) wanted_total[warp] = __popc(mask);
+    __syncthreads();
+    int upto = __popc(mask & ((2u << lane) - 1));  // pages wanted up to this request
+#pragma unroll
+    for (int w = 0; w < kAloneWarps; ++w)
+        if (w < warp) upto += wanted_total[w];
+    const bool granted = want >= 0 && upto <= n_free;
+    from[tid] = granted && want > 0 ? q.last : -1;
+    to[tid] = granted && want > 0 ? free[upto - 1] : -1;
+    parent[tid] = granted ? (int32_t)q.from : -1;
+    length[tid] = q.length;
+    if (granted) atomicOr(&forked[q.to / 32], 1u << (q.to % 32));
+    if (blockIdx.x == 0 && tid < count) done[tid] = granted;
+    __syncthreads();
+
+    // the first block has the counts; the rows go round
+    if (blockIdx.x == 0) {
+        for (int p = tid; p < b.pages; p += kCopyThreads) b.refs_out[p] = b.refs_in[p];
+        __syncthreads();
+        if (to[tid] >= 0) b.refs_out[to[tid]] = 1;
+    }
+    const int warps = gridDim.x * kAloneWarps, my_warp = blockIdx.x * kAloneWarps + warp;
+    for (int r = my_warp; r < b.rows; r += warps) {
+        if (forked[r / 32] >> (r % 32) & 1) continue;
+        for (int64_t j = lane; j < b.width; j += 32)
+            b.tables_out[r * b.out_stride + j] = b.tables_in[r * b.in_stride + j];
+        if (lane == 0) b.lengths_out[r] = b.lengths_in[r];
+    }
+    const int first = blockIdx.x == 0 ? warp : my_warp, stride = blockIdx.x == 0 ? kAloneWarps : warps;
+    for (int i = first; i < count; i += stride) {
+        if (parent[i] < 0) continue;
+        const int64_t full = length[i] / b.page_size;
+        const bool mine = i % warps == my_warp;
+        for (int64_t j = lane; j < b.width; j += 32) {
+            const int32_t p = j < full    ? b.tables_in[parent[i] * b.in_stride + j]
+                              : j == full ? to[i]
+                                          : -1;
+            if (blockIdx.x == 0 && j < full && p >= 0 && p < b.pages) atomicAdd(&b.refs_out[p], 1);
+            if (mine) b.tables_out[child[i] * b.out_stride + j] = p;
+        }
+        if (mine && lane == 0) b.lengths_out[child[i]] = length[i];
+    }
+    const int64_t units = count * pool.planes * pool.pieces();
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x)
+        copy_piece(pool, u, [&](int64_t i) { return (int64_t)from[i]; },
+                   [&](int64_t i) { return (int64_t)to[i]; });
 }
 
 __global__ void __launch_bounds__(kCopyThreads)
@@ -564,7 +719,35 @@ Pool pool_of(void* pool, const w4a16_pool_shape& s, int64_t pages) {
 
 unsigned copy_ctas(const DeviceCtx& ctx) { return (unsigned)(kCopyBlocksPerSm * ctx.num_sms); }
 
+// Whether a fork or compaction of at most `copies` pages goes in one launch.
+bool alone(const w4a16_books_shape& b, const w4a16_pool_shape& pool, int64_t copies, bool apart) {
+    return apart && b.pages <= kAlonePages && b.rows <= kAloneRows && b.rows * b.width <= 1 << 20 &&
+           copies * pool.planes <= kAloneBytes / pool.page_bytes;
+}
+bool fork_alone(const w4a16_books_shape& b, const w4a16_pool_shape& pool, int64_t count, bool apart) {
+    return count <= kAloneCount && count * b.width <= 1 << 14 && alone(b, pool, count, apart);
+}
+bool compact_alone(const w4a16_books_shape& b, const w4a16_pool_shape& pool, bool apart) {
+    return alone(b, pool, b.pages / 2, apart);
+}
+
+// Blocks for at most `copies` copies to share out.
+unsigned alone_ctas(const w4a16_pool_shape& pool, int64_t copies, const DeviceCtx& ctx) {
+    const int64_t units = copies * pool.planes * ((pool.page_bytes + kPiece - 1) / kPiece);
+    return (unsigned)std::max<int64_t>(1, std::min<int64_t>(units, copy_ctas(ctx)));
+}
+
 }  // namespace
+
+int64_t pages_fork_workspace(const w4a16_books_shape& b, const w4a16_pool_shape& pool,
+                             int64_t count, bool apart) {
+    return fork_alone(b, pool, count, apart) ? 0 : pages_workspace(b, count);
+}
+
+int64_t pages_compact_workspace(const w4a16_books_shape& b, const w4a16_pool_shape& pool,
+                                bool apart) {
+    return compact_alone(b, pool, apart) ? 0 : pages_workspace(b, 0);
+}
 
 int64_t pages_workspace(const w4a16_books_shape& b, int64_t count) {
     return 4 * (4 + b.rows + 4 * count + 3 * b.pages);
@@ -574,20 +757,27 @@ cudaError_t launch_pages_free(const PageBooks& b, const int32_t* listed, int64_t
                               cudaStream_t stream) {
     // a warp goes through a listed row, three round trips to L2 each: eight CTAs from a few rows on
     const int64_t rows = count <= 2 * kBookWarps ? 0 : (int64_t)1 << 40;
-    return launch_books(free_kernel, std::max({b.shape.pages, copied(b), rows}), stream, books_of(b), listed, count);
+    return launch_books(free_kernel, std::max({b.shape.pages, copied(b), rows}), stream, books_of(b),
+                        listed, count);
 }
 
 cudaError_t launch_pages_extend(const PageBooks& b, const int32_t* listed, const int32_t* counts,
                                 int64_t count, int32_t* done, void* workspace,
                                 cudaStream_t stream) {
-    return launch_books(extend_kernel, std::max(b.shape.pages, copied(b)), stream, books_of(b), listed, counts, count,
-                        done, split_space(workspace, b.shape.rows, b.shape.pages, count));
+    return launch_books(extend_kernel, std::max(b.shape.pages, copied(b)), stream, books_of(b),
+                        listed, counts, count, done,
+                        split_space(workspace, b.shape.rows, b.shape.pages, count));
 }
 
 cudaError_t launch_pages_fork(void* pool, const PageBooks& b, const int32_t* parents,
                               const int32_t* children, int64_t count, int32_t* done,
                               void* workspace, const w4a16_pool_shape& shape, cudaStream_t stream,
                               const DeviceCtx& ctx) {
+    if (fork_alone(b.shape, shape, count,
+                   b.refs_in != b.refs_out && b.tables_in != b.tables_out &&
+                       b.lengths_in != b.lengths_out))
+        return launch_apply(fork_alone_kernel, alone_ctas(shape, count, ctx), stream, books_of(b),
+                            parents, children, count, done, pool_of(pool, shape, b.shape.pages));
     const Space s = split_space(workspace, b.shape.rows, b.shape.pages, count);
     cudaError_t e = launch_books(fork_plan_kernel, b.shape.pages, stream, books_of(b), parents,
                                  children, count, done, s);
@@ -599,6 +789,9 @@ cudaError_t launch_pages_fork(void* pool, const PageBooks& b, const int32_t* par
 cudaError_t launch_pages_compact(void* pool, const PageBooks& b, int32_t* used, void* workspace,
                                  const w4a16_pool_shape& shape, cudaStream_t stream,
                                  const DeviceCtx& ctx) {
+    if (compact_alone(b.shape, shape, b.refs_in != b.refs_out && b.tables_in != b.tables_out))
+        return launch_apply(compact_alone_kernel, alone_ctas(shape, b.shape.pages / 2, ctx), stream,
+                            books_of(b), used, pool_of(pool, shape, b.shape.pages));
     const Space s = split_space(workspace, b.shape.rows, b.shape.pages, 0);
     cudaError_t e = launch_books(compact_plan_kernel, b.shape.pages, stream, books_of(b), used, s);
     if (e != cudaSuccess) return e;

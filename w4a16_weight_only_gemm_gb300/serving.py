@@ -245,10 +245,10 @@ def _pool_shape(pool: torch.Tensor, pages: int | None) -> bytes:
 
 
 @functools.lru_cache(maxsize=1024)
-def _pages_workspace(books: bytes, count: int) -> int:
-    n = _native.lib().w4a16_pages_workspace(books, count)
+def _pages_workspace(name: str, *shape) -> int:
+    n = getattr(_native.lib(), name)(*shape)
     if n < 0:
-        _native.check(2, "w4a16_pages_workspace")
+        _native.check(2, name)
     return n
 
 
@@ -276,7 +276,8 @@ def pages_extend(refs: torch.Tensor, tables: torch.Tensor, lengths: torch.Tensor
     dev, ins, outs, to, shape = _books(refs, tables, lengths, out, page_size, stream, rows=rows,
                                        counts=counts)
     done = _empty(refs, count, torch.int32, stream)
-    space = _empty(refs, _pages_workspace(shape, count), torch.uint8, stream)
+    space = _empty(refs, _pages_workspace("w4a16_pages_workspace", shape, count), torch.uint8,
+                   stream)
     _run(dev, stream, "w4a16_pages_extend", *ins, rows.data_ptr(), counts.data_ptr(), count, *to,
          done.data_ptr(), space.data_ptr(), shape)
     return *outs, done
@@ -296,7 +297,9 @@ def pages_fork(pool: torch.Tensor, refs: torch.Tensor, tables: torch.Tensor,
     dev, ins, outs, to, shape = _books(refs, tables, lengths, out, page_size, stream, pool=pool,
                                        parents=parents, children=children)
     done = _empty(refs, count, torch.int32, stream)
-    space = _empty(refs, _pages_workspace(shape, count), torch.uint8, stream)
+    apart = out is None or not any(i == o for i, o in zip(ins, to))
+    size = _pages_workspace("w4a16_pages_fork_workspace", shape, planes, count, apart)
+    space = _empty(refs, size, torch.uint8, stream) if size else pool  # 0: not looked at
     _run(dev, stream, "w4a16_pages_fork", pool.data_ptr(), *ins, parents.data_ptr(),
          children.data_ptr(), count, *to, done.data_ptr(), space.data_ptr(), shape, planes)
     return *outs, done
@@ -310,7 +313,9 @@ def pages_compact(pool: torch.Tensor, refs: torch.Tensor, tables: torch.Tensor, 
     planes = _pool_shape(pool, refs.shape[0])
     dev, ins, outs, to, shape = _books(refs, tables, None, out, 1, stream, pool=pool)
     used = _empty(refs, 1, torch.int32, stream)
-    space = _empty(refs, _pages_workspace(shape, 0), torch.uint8, stream)
+    apart = out is None or not any(i == o for i, o in zip(ins, to))
+    size = _pages_workspace("w4a16_pages_compact_workspace", shape, planes, apart)
+    space = _empty(refs, size, torch.uint8, stream) if size else pool  # 0: not looked at
     _run(dev, stream, "w4a16_pages_compact", pool.data_ptr(), *ins, *to, used.data_ptr(),
          space.data_ptr(), shape, planes)
     return *outs, used
