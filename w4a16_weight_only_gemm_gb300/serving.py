@@ -29,10 +29,16 @@ _POOL_SHAPE = struct.Struct("4q").pack
 # was wrong is looked for only when something was.
 
 
+@functools.lru_cache(maxsize=1)
+def _one_device() -> bool:
+    return torch.cuda.device_count() == 1
+
+
 def _run(dev: int, stream, name: str, *args) -> None:
     """Calls the library's entry point on device `dev` and the given or current stream."""
     fn = getattr(_native.lib(), name)
-    if stream is None and _raw_stream is not None and dev == torch.cuda.current_device():
+    if (stream is None and _raw_stream is not None
+            and (_one_device() or dev == torch.cuda.current_device())):
         rc = fn(*args, _raw_stream(dev))
     else:
         device = torch.device("cuda", dev)
@@ -157,12 +163,14 @@ def paged_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
     length 0), and with return_lse also the logarithm of each head's sum of
     exponentials, fp32 [rows, q_heads] (-inf for a row of length 0)."""
     cache = _cache_shape(k_pool, v_pool, tables)
-    shape, dtype = q.shape, k_pool.dtype
-    if len(shape) != 3:
-        raise ValueError(f"q must be [rows, q_heads, head_dim], got {list(shape)}")
-    rows, q_heads, dim = tables.shape[0], shape[1], k_pool.shape[3]
-    qs = _heads(q, "q", dtype, (rows, q_heads, dim))
-    _row(lengths, rows, "lengths")
+    shape, dtype, strides = q.shape, k_pool.dtype, q.stride()
+    rows, dim = tables.shape[0], k_pool.shape[3]
+    if (len(shape) != 3 or shape[0] != rows or shape[2] != dim or strides[2] != 1
+            or q.dtype is not dtype):
+        _heads(q, "q", dtype, (rows, shape[1] if len(shape) == 3 else "q_heads", dim))
+    q_heads = shape[1]
+    if lengths.dtype is not torch.int32 or lengths.shape != (rows,) or lengths.stride(0) != 1:
+        _row(lengths, rows, "lengths")
     dev = q.get_device()
     if (dev < 0 or k_pool.get_device() != dev or v_pool.get_device() != dev
             or tables.get_device() != dev or lengths.get_device() != dev
@@ -171,7 +179,9 @@ def paged_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
         _device(stream, q=q, k_pool=k_pool, v_pool=v_pool, tables=tables, lengths=lengths, out=out)
     if out is None:
         out = _empty(q, shape, dtype, stream)
-    os = _heads(out, "out", dtype, shape)
+        row, head = q_heads * dim, dim
+    else:
+        row, head, _ = _heads(out, "out", dtype, shape)
     lse = _empty(q, (rows, q_heads), torch.float32, stream) if return_lse else None
     if rows:
         size = _attention_workspace(cache, q_heads, dev)
@@ -179,15 +189,13 @@ def paged_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
         _run(dev, stream, "w4a16_paged_attention", q.data_ptr(), k_pool.data_ptr(),
              v_pool.data_ptr(), tables.data_ptr(), lengths.data_ptr(), out.data_ptr(),
              lse.data_ptr() if return_lse else None, workspace.data_ptr(), cache,
-             _QUERY_SHAPE(q_heads, qs[0], qs[1], os[0], os[1],
+             _QUERY_SHAPE(q_heads, strides[0], strides[1], row, head,
                           dim ** -0.5 if scale is None else scale))
     return (out, lse) if return_lse else out
 
 
 def _like(t: torch.Tensor, stream) -> torch.Tensor:
-    """A new tensor of t's shape and type, dense in its last dimension as t is."""
-    if stream is None:
-        return torch.empty_like(t)
+    """torch.empty_like on a stream (dense in its last dimension as t is)."""
     with torch.cuda.stream(stream):
         return torch.empty_like(t)
 
@@ -207,7 +215,8 @@ def _books(refs, tables, lengths, out, page_size: int, stream, **others):
     dev = refs.get_device()
     same = dev >= 0 and (stream is None or stream.device.index == dev)
     if out is None:
-        outs = [_like(t, stream) for t in ins] if dev >= 0 else ins
+        outs = ins if dev < 0 else [torch.empty_like(t) for t in ins] if stream is None \
+            else [_like(t, stream) for t in ins]
     else:
         outs = list(out)
         if len(outs) != len(ins):
