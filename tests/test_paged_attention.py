@@ -165,6 +165,23 @@ def test_equal_scores_average(w4lib):
     check(q, k, v, tables, lengths)
 
 
+@pytest.mark.parametrize("width", [None, 30000])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_many_small_weights_beside_a_large_one(w4lib, dtype, width):
+    """A position that draws nearly all attention, and a hundred thousand others whose
+    weights, each 1.5 * 2^-24 of it, are a hundredth of the sum."""
+    n = 100_000
+    q, k, v, tables, lengths = make([n], 1, 2, 64, 16, dtype, seed=12, garbage=0.0, width=width)
+    q.zero_()
+    q[:, :, 0] = 1.0
+    k.zero_()
+    v.fill_(1.0)
+    page = int(tables[0, 0])
+    k[page, 3, 0, 0] = math.log(2.0 ** 24 / 1.5)
+    v[page, 3] = 0.0
+    check(q, k, v, tables, lengths, scale=1.0)
+
+
 @pytest.mark.parametrize("rising", [True, False])
 def test_ordered_scores(w4lib, rising):
     """The maximum found last, or first."""

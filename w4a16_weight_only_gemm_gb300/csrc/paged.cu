@@ -158,7 +158,9 @@ constexpr int kAttendThreads = 32 * kAttendWarps;
 constexpr int kTile = 16;                       // positions of a warp in a step
 constexpr int kStep = kTile * kAttendWarps;     // positions of a step
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kSlack = 8.f;                   // a weight is at most 2^8
+// Weights are held times 2^12 (2^15 at most): FP16 has nothing between 0 and 2^-24, and many small
+// weights in a warp's part would each be rounded to one or the other beside a weight of 1.
+constexpr float kHeadroom = 12.f, kMostWeight = 15.f;
 constexpr int kMaxCluster = 8;                  // blocks to an item, without the line
 
 // What is left for the join: an item that begins in block `first` and is ended
@@ -573,7 +575,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
 #pragma unroll
             for (int x = 0; x < 4; ++x) c[n][x] += c2[n][x];
         const uint32_t bits = flags >> (2 * (S::kStages - 1));
-        // binary exponents under the maximum so far; masked positions -infinity
+        // binary exponents over `top`, the maximum so far less the headroom; masked: -infinity
         bool low = true;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -581,11 +583,11 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
             for (int x = 0; x < 4; ++x) {
                 const float y = fmaf(c[n][x], a.scale_log2, -top[n][x & 1]);
                 c2[n][x] = bits >> (x >> 1) & 1 ? y : -INFINITY;
-                low = low && c2[n][x] <= kSlack;
+                low = low && c2[n][x] <= kMostWeight;
             }
         if (!__all_sync(~0u, low)) {
-            // A new maximum.  One up to 2^8 above the old is let be: sums under it lose
-            // nothing, and after a row's first tiles this is rarely entered.
+            // A new maximum.  One up to 2^3 above the old is let be, so after a row's first
+            // tiles this is rarely entered.
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float keep[2];
@@ -597,7 +599,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
                     m = fmaxf(m, __shfl_xor_sync(~0u, m, 4));
                     m = fmaxf(m, __shfl_xor_sync(~0u, m, 8));
                     m = fmaxf(m, __shfl_xor_sync(~0u, m, 16));
-                    m = fmaxf(m, top[n][x]);
+                    m = fmaxf(m - kHeadroom, top[n][x]);
                     const float base = m == -INFINITY ? 0.f : m;  // nothing yet: every weight is 0
                     keep[x] = exp2_fast(top[n][x] - base);
                     top[n][x] = m;
