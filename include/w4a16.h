@@ -9,7 +9,10 @@
  * round-to-nearest quantizer that produces the packed weights ("LLM
  * quantization from IEEE 754 to GPTQ/AWQ/GGUF" tutorial, qaqbuyan.com
  * article 126, chapter "量化的数学基石" §2 formula and §3
- * per_group_symmetric_quantize / per_group_symmetric_dequantize).
+ * per_group_symmetric_quantize / per_group_symmetric_dequantize).  Around the
+ * linear layers it has the operators that a decoding program needs between
+ * them: a paged key-value cache, the attention of a new token over it, the
+ * care of its pages, and the scores of sampled tokens.
  *
  * Conventions for every entry point
  *  - Pointers are DEVICE pointers owned by the caller (for example a torch

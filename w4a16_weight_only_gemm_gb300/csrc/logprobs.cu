@@ -18,9 +18,12 @@
 // (masks leave fewer than k logits, so the cut is the mask's value), those
 // above the cut are kept and the lowest indices at it added in order.
 //
-// Bound by HBM for many rows.  A row is a block's, or, for few rows, a
-// cluster's, whose first block joins the others' sums and alternatives through
-// shared memory: no workspace, one launch.
+// A row is a block's, or, for few rows, a cluster's, whose first block joins
+// the others' sums and alternatives through shared memory: no workspace, one
+// launch.  Bound by HBM for many rows, short of it by what a block does after
+// its pass: on one GB300 (6790 GB/s copied) 2047 rows of 128256 take 90 us in
+// fp16 (5820 GB/s), 1023 in fp32 80 us (6560 GB/s).  One row takes 8.2 us, all
+// of it latency: a launch, a pass, seven barriers.
 #include <cuda_bf16.h>
 
 #include <stddef.h>

