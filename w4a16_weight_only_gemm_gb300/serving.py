@@ -200,25 +200,30 @@ def _like(t: torch.Tensor, stream) -> torch.Tensor:
         return torch.empty_like(t)
 
 
-def _books(refs, tables, lengths, out, page_size: int, stream, **others):
+def _books(refs, tables, lengths, out, page_size: int, stream, names: tuple, *others):
     """The books' device, their addresses, their outputs (new ones, or `out`), the outputs'
-    addresses and the packed shape; the tensors in `others` share the device.  lengths may be
+    addresses and the packed shape; `others` (of those names) share the device.  lengths may be
     None: neither read nor written."""
-    pages, (rows, width), strides = refs.shape[0], tables.shape, tables.stride()
-    _row(refs, pages, "refs")
+    pages, (rows, width), strides, dev = refs.shape[0], tables.shape, tables.stride(), refs.get_device()
+    if refs.dtype is not torch.int32 or refs.stride() != (1,):
+        _row(refs, pages, "refs")
     if tables.dtype is not torch.int32 or strides[1] != 1:
         _ints(tables, "tables", (None, None))
+    same = dev >= 0 and tables.get_device() == dev and (stream is None or stream.device.index == dev)
     ins = (refs, tables)
     if lengths is not None:
         _row(lengths, rows, "lengths")
+        same = same and lengths.get_device() == dev
         ins = (refs, tables, lengths)
-    dev = refs.get_device()
-    same = dev >= 0 and (stream is None or stream.device.index == dev)
+    for t in others:
+        same = same and t.get_device() == dev
     if out is None:
-        outs = ins if dev < 0 else [torch.empty_like(t) for t in ins] if stream is None \
-            else [_like(t, stream) for t in ins]
+        outs = ins
+        if same:
+            outs = tuple(map(torch.empty_like, ins)) if stream is None \
+                else tuple(_like(t, stream) for t in ins)
     else:
-        outs = list(out)
+        outs = tuple(out)
         if len(outs) != len(ins):
             raise ValueError(f"out must be {len(ins)} tensors")
         for t, o in zip(ins, outs):
@@ -226,16 +231,12 @@ def _books(refs, tables, lengths, out, page_size: int, stream, **others):
             if o.data_ptr() == t.data_ptr() and o.stride() != t.stride():
                 raise ValueError("an out tensor that is its input must have its strides")
             same = same and o.get_device() == dev
-    for t in ins[1:]:
-        same = same and t.get_device() == dev
-    for t in others.values():
-        same = same and t.get_device() == dev
+    row = outs[1].stride(0) if rows > 1 else width
     if not same:
-        _device(stream, refs=refs, tables=tables, lengths=lengths, **others,
+        _device(stream, refs=refs, tables=tables, lengths=lengths, **dict(zip(names, others)),
                 **{f"out[{i}]": o for i, o in enumerate(outs)})
     return (dev, [t.data_ptr() for t in ins], outs, [t.data_ptr() for t in outs],
-            _BOOKS_SHAPE(pages, rows, width, strides[0], outs[1].stride(0) if rows > 1 else width,
-                         page_size))
+            _BOOKS_SHAPE(pages, rows, width, strides[0], row, page_size))
 
 
 def _pool_shape(pool: torch.Tensor, pages: int | None) -> bytes:
@@ -246,10 +247,13 @@ def _pool_shape(pool: torch.Tensor, pages: int | None) -> bytes:
     if pages is not None and shape[1] != pages:
         raise ValueError(f"pool has {shape[1]} pages, the books {pages}")
     page = size
-    for i in range(len(shape) - 1, 1, -1):
-        if strides[i] * size != page and shape[i] > 1:
-            raise ValueError("pool must be dense within a page")
-        page *= shape[i]
+    if shape[1] > 1 and pool.is_contiguous():
+        page *= strides[1]
+    else:
+        for i in range(len(shape) - 1, 1, -1):
+            if strides[i] * size != page and shape[i] > 1:
+                raise ValueError("pool must be dense within a page")
+            page *= shape[i]
     return _POOL_SHAPE(shape[0], strides[0] * size, strides[1] * size, page)
 
 
@@ -268,9 +272,9 @@ def pages_free(refs: torch.Tensor, tables: torch.Tensor, lengths: torch.Tensor,
     (refs, tables, lengths), new tensors or `out` (which may be the inputs)."""
     count = rows.shape[0]
     _row(rows, count, "rows")
-    dev, ins, outs, to, shape = _books(refs, tables, lengths, out, 1, stream, rows=rows)
+    dev, ins, outs, to, shape = _books(refs, tables, lengths, out, 1, stream, ("rows",), rows)
     _run(dev, stream, "w4a16_pages_free", *ins, rows.data_ptr(), count, *to, shape)
-    return tuple(outs)
+    return outs
 
 
 def pages_extend(refs: torch.Tensor, tables: torch.Tensor, lengths: torch.Tensor,
@@ -282,8 +286,8 @@ def pages_extend(refs: torch.Tensor, tables: torch.Tensor, lengths: torch.Tensor
     count = rows.shape[0]
     _row(rows, count, "rows")
     _row(counts, count, "counts")
-    dev, ins, outs, to, shape = _books(refs, tables, lengths, out, page_size, stream, rows=rows,
-                                       counts=counts)
+    dev, ins, outs, to, shape = _books(refs, tables, lengths, out, page_size, stream,
+                                       ("rows", "counts"), rows, counts)
     done = _empty(refs, count, torch.int32, stream)
     space = _empty(refs, _pages_workspace("w4a16_pages_workspace", shape, count), torch.uint8,
                    stream)
@@ -303,8 +307,8 @@ def pages_fork(pool: torch.Tensor, refs: torch.Tensor, tables: torch.Tensor,
     planes, count = _pool_shape(pool, refs.shape[0]), parents.shape[0]
     _row(parents, count, "parents")
     _row(children, count, "children")
-    dev, ins, outs, to, shape = _books(refs, tables, lengths, out, page_size, stream, pool=pool,
-                                       parents=parents, children=children)
+    dev, ins, outs, to, shape = _books(refs, tables, lengths, out, page_size, stream,
+                                       ("pool", "parents", "children"), pool, parents, children)
     done = _empty(refs, count, torch.int32, stream)
     apart = out is None or not any(i == o for i, o in zip(ins, to))
     size = _pages_workspace("w4a16_pages_fork_workspace", shape, planes, count, apart)
@@ -320,7 +324,7 @@ def pages_compact(pool: torch.Tensor, refs: torch.Tensor, tables: torch.Tensor, 
     in ascending order, to the free ones below, in every plane of pool
     [planes, pages, ...].  Returns (refs, tables, used) with used = [n]."""
     planes = _pool_shape(pool, refs.shape[0])
-    dev, ins, outs, to, shape = _books(refs, tables, None, out, 1, stream, pool=pool)
+    dev, ins, outs, to, shape = _books(refs, tables, None, out, 1, stream, ("pool",), pool)
     used = _empty(refs, 1, torch.int32, stream)
     apart = out is None or not any(i == o for i, o in zip(ins, to))
     size = _pages_workspace("w4a16_pages_compact_workspace", shape, planes, apart)
