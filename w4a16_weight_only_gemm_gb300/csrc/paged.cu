@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
             int64_t at = (upto - mine) * a.items;
             int n = steps_of(a.length(r));
             while (at + (int64_t)n * a.items <= lo) at += (int64_t)n * a.items, n = steps_of(a.length(++r));
-                const int item = (int)((lo - at) / n);
+            const int item = (int)((lo - at) / n);
             begin = {r, item, (int)((lo - at) % n), n, a.length(r), a.head_offset(item)};
         }
     }
