@@ -3,7 +3,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
-#include <atomic>
+#include <mutex>
 #include <type_traits>
 
 #include "common.cuh"
@@ -156,9 +156,9 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
 // On one GB300 (6790 GB/s copied), 8 key-value heads of 128 and 4 query heads
 // to each: one row of 131071 positions 85.7 us (6260 GB/s), 128 rows of up to
 // 8191 314 us (6780 GB/s), one row of 512 4.8 us.  16 rows of up to 4093 with 4
-// key-value heads 19.1 us (3740 GB/s): a launch and three reads that depend on
-// one another (length, page, keys) before the first tile, two ends of items in
-// a block, and the second launch, about 9 us in all.
+// key-value heads 17.7 us (4030 GB/s): a launch and three reads that depend on
+// one another (length, page, keys) before the first tile, the longest rows'
+// blocks after the others are done, and the join, about 7 us in all.
 // ---------------------------------------------------------------------------
 constexpr int kAttendWarps = 4;
 constexpr int kAttendThreads = 32 * kAttendWarps;
@@ -168,7 +168,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 // Weights are held times 2^12 (2^15 at most): FP16 has nothing between 0 and 2^-24, and many small
 // weights in a warp's part would each be rounded to one or the other beside a weight of 1.
 constexpr float kHeadroom = 12.f, kMostWeight = 15.f;
-constexpr int kMaxCluster = 8;                  // blocks to an item, without the line
+constexpr int kMaxCluster = 8;                  // blocks to an item, without the line,
+constexpr int kFewSteps = 8, kMostSteps = 32;   // and the most steps of such a block
 
 // What is left for the join: an item that begins in block `first` and is ended
 // by the `count` blocks after it (count 0: none).  The place of an item's joint
@@ -907,23 +908,78 @@ int attend_blocks(int64_t dim, int tiles, const DeviceCtx& ctx) {
     return std::min(kMaxParts, ctx.num_sms * per_sm[dim <= 64 ? 0 : dim <= 128 ? 1 : 2][tiles - 1]);
 }
 
+// Clusters of 1 .. 8 blocks of an attention kernel that the device has room for at once.
+struct Room {
+    cudaError_t error = cudaSuccess;
+    int clusters[kMaxCluster + 1] = {};
+};
+
+template <typename T, int DP, int NT, bool kTilePage>
+const Room& room_of(int device) {
+    static std::once_flag once[64];
+    static Room room[64];
+    const auto kernel = attend_kernel<T, DP, NT, kTilePage>;
+    std::call_once(once[device], [&]() {
+        Room& r = room[device];
+        r.error = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       AttendShape<DP, NT>::kSmem);
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        cudaLaunchConfig_t cfg = {};
+        cfg.blockDim = dim3(kAttendThreads);
+        cfg.dynamicSmemBytes = AttendShape<DP, NT>::kSmem;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        for (int n = 1; n <= kMaxCluster && r.error == cudaSuccess; ++n) {
+            cfg.gridDim = dim3((unsigned)n);
+            attr.val.clusterDim.x = (unsigned)n;
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            r.error = cudaOccupancyMaxActiveClusters(&r.clusters[n], kernel, &cfg);
+        }
+    });
+    return room[device];
+}
+
+// The room of the kernel that a cache's geometry takes.
+template <typename T, int DP, int NT>
+const Room& room_of(bool tile_page, int device) {
+    return tile_page ? room_of<T, DP, NT, true>(device) : room_of<T, DP, NT, false>(device);
+}
+template <typename T>
+const Room& room_of(int dim, int tiles, bool tile_page, int device) {
+    if (dim <= 64)
+        return tiles == 1 ? room_of<T, 64, 1>(tile_page, device) : room_of<T, 64, 2>(tile_page, device);
+    if (dim <= 128)
+        return tiles == 1 ? room_of<T, 128, 1>(tile_page, device) : room_of<T, 128, 2>(tile_page, device);
+    return tiles == 1 ? room_of<T, 256, 1>(tile_page, device) : room_of<T, 256, 2>(tile_page, device);
+}
+
 // Blocks to an item where tables are short, a cluster that joins its parts in
-// shared memory: no second launch and no workspace.  The largest power of two
-// that finds a place on the SMs at once and has a step each (clusters of 7
-// leave places empty: 64 items of 8 steps 10.9 us, by clusters of 4 7.4).  0,
-// and the line is cut instead, where that leaves a block too many steps, as a
-// row may be that much longer than the others: 16 where the blocks fill the
-// places (448 items of 16 steps 38 us, the line 48), else 8 (one row of 8 items,
-// 128 steps 15.9 us, the line 10.6; 64 items of 64 steps at most, spread evenly,
-// 21.6 us, the line 19.8; 8 items of 8 steps 4.8 us, the line 7.1).
-int item_cluster(const w4a16_cache_shape& c, int64_t group, const DeviceCtx& ctx) {
+// shared memory: no second launch and no workspace.  As many as the device has
+// room for at once (a cluster stays within a part of the GPU, so 8 fit less
+// often than 6: 64 items of 8 steps by clusters of 7 take 10.9 us, by 6 7.1),
+// and a step each.  0, and the line is cut instead, where that leaves a block
+// too many steps, as a row may be that much longer than the others (such a step
+// takes 0.7 us): 32 where the blocks fill half the places or more, else 8.
+// Clusters / the line, 8 key-value heads: 56 rows of 2048 72 / 81 us, of 1 to
+// 2048 43 / 48, 14 rows of 1 to 4096 26.8 / 27.7, 8 rows of 1 to 4096 17.7 / 19.4,
+// of 512 7.0 / 9.3, one row of 512 4.8 / 7.1, one of 8192 15.9 / 10.2.
+int item_cluster(const w4a16_cache_shape& c, int64_t group, const DeviceCtx& ctx, cudaError_t* error) {
     const HeadPlan heads = plan_heads(group);
     const int64_t items = c.batch * c.kv_heads * heads.blocks;
     const int64_t places = attend_blocks(c.head_dim, heads.tiles, ctx);
     const int64_t steps = (c.table_width * c.page_size + kStep - 1) / kStep;
-    int64_t n = 1;
-    while (n < kMaxCluster && items * n * 2 <= places && n < steps) n *= 2;
-    return items <= places && steps <= n * (4 * items * n >= 3 * places ? 16 : 8) ? (int)n : 0;
+    if (items > places || steps > kMaxCluster * kMostSteps) return 0;
+    int device = 0;
+    if ((*error = cudaGetDevice(&device)) != cudaSuccess) return 0;
+    const bool tile_page = c.page_size % kTile == 0;
+    const Room& room = c.type == W4A16_BF16
+                           ? room_of<__nv_bfloat16>((int)c.head_dim, heads.tiles, tile_page, device)
+                           : room_of<__half>((int)c.head_dim, heads.tiles, tile_page, device);
+    if ((*error = room.error) != cudaSuccess) return 0;
+    int n = (int)std::min<int64_t>(kMaxCluster, steps);
+    while (n > 0 && items > room.clusters[n]) --n;
+    return steps <= n * (2 * items * n >= places ? kMostSteps : kFewSteps) ? n : 0;
 }
 
 // The workspace: partial outputs, their maxima and sums, the joints.
@@ -944,16 +1000,10 @@ Workspace plan_workspace(int64_t dim, int64_t group, const DeviceCtx& ctx) {
 template <typename T, int DP, int NT, bool kTilePage>
 cudaError_t attend(AttendArgs a, cudaStream_t stream, const DeviceCtx& ctx) {
     using S = AttendShape<DP, NT>;
-    static std::atomic<bool> ready[64];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
     if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(attend_kernel<T, DP, NT, kTilePage>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-        if (e != cudaSuccess) return e;
-        if (dev >= 0 && dev < 64) ready[dev].store(true, std::memory_order_release);
-    }
+    if ((e = room_of<T, DP, NT, kTilePage>(device).error) != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1044,7 +1094,10 @@ cudaError_t launch_paged_append(const void* k, const void* v, void* k_pool, void
 int64_t paged_attention_workspace(const w4a16_cache_shape& cache, int64_t q_heads,
                                   const DeviceCtx& ctx) {
     const int64_t group = q_heads / cache.kv_heads;
-    return item_cluster(cache, group, ctx) ? 0 : plan_workspace(cache.head_dim, group, ctx).bytes;
+    cudaError_t e = cudaSuccess;
+    const int cluster = item_cluster(cache, group, ctx, &e);
+    if (e != cudaSuccess) return -1;
+    return cluster ? 0 : plan_workspace(cache.head_dim, group, ctx).bytes;
 }
 
 cudaError_t launch_paged_attention(const void* q, const void* k_pool, const void* v_pool,
@@ -1066,7 +1119,9 @@ cudaError_t launch_paged_attention(const void* q, const void* k_pool, const void
     a.head_blocks = heads.blocks;
     a.block_heads = heads.heads;
     a.items = (int)cache.kv_heads * heads.blocks;
-    a.cluster = item_cluster(cache, a.group, ctx);
+    cudaError_t e = cudaSuccess;
+    a.cluster = item_cluster(cache, a.group, ctx, &e);
+    if (e != cudaSuccess) return e;
     const Workspace w = plan_workspace(cache.head_dim, a.group, ctx);
     char* base = static_cast<char*>(workspace);
     a.partial = reinterpret_cast<float*>(base + w.partial);
