@@ -36,10 +36,8 @@
 namespace w4a16 {
 namespace {
 
-constexpr int kScoreThreads = 256;
-constexpr int kScoreWarps = kScoreThreads / 32;
-constexpr int kScoreBlocksPerSm = 4;
-constexpr int kGroups = kScoreThreads / 4;  // of threads, for the first cut of the alternatives
+constexpr int kSmThreads = 1024;            // of blocks side by side on an SM
+constexpr int kGroups = 64;                 // of threads, for the first cut of the alternatives
 constexpr int kBatch = 8;                   // 16-byte pieces a thread has in flight
 constexpr int kCandidates = 1024;
 constexpr int kAheadBytes = 32768;          // of a row to come, asked into L2
@@ -168,22 +166,22 @@ __device__ __forceinline__ Sums add(const Sums& a, const Sums& b) {
     return r;
 }
 
-template <typename T>
+template <typename T, int kThreads>
 struct ScoreShared {
-    T batch_top[kKept][kScoreThreads];  // the largest logit of a thread's batch
+    T batch_top[kKept][kThreads];       // the largest logit of a thread's batch
     int batches;
-    uint32_t batch[kScoreThreads];      // those that reach the cut: thread | batch << 16
-    Sums part[kScoreWarps];
+    uint32_t batch[kThreads];      // those that reach the cut: thread | batch << 16
+    Sums part[kThreads / 32];
     Sums sums;                      // of the block
     uint32_t group_key[kGroups];
     uint32_t cut, higher;
     int listed, found;
-    uint16_t list[kScoreThreads];   // threads whose maximum reaches the cut
+    uint16_t list[kThreads];   // threads whose maximum reaches the cut
     uint64_t best[W4A16_MAX_TOP];   // the block's alternatives, in order
     int bests;
     uint64_t candidate[kCandidates];
-    uint64_t warp_best[kScoreWarps];
-    int equal[kScoreWarps];
+    uint64_t warp_best[kThreads / 32];
+    int equal[kThreads / 32];
 };
 
 __device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t addr) {
@@ -197,11 +195,12 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
     return v;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kScoreThreads, kScoreBlocksPerSm)
+template <typename T, int kThreads>
+__global__ void __launch_bounds__(kThreads, kSmThreads / kThreads)
     score_kernel(ScoreArgs a, int blocks, int64_t ahead) {
     constexpr int kPer = 16 / sizeof(T), kWord = 4 / sizeof(T);
-    using Shared = ScoreShared<T>;
+    constexpr int kWarps = kThreads / 32, kGroupThreads = kThreads / kGroups;
+    using Shared = ScoreShared<T, kThreads>;
     __shared__ Shared sh;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int64_t row = blockIdx.x / blocks;
@@ -287,17 +286,17 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocksPerSm)
         t += lo + hi;
     };
     int j = tid, batch = 0;
-    for (; j + (kBatch - 1) * kScoreThreads < count; j += kBatch * kScoreThreads, ++batch) {
+    for (; j + (kBatch - 1) * kThreads < count; j += kBatch * kThreads, ++batch) {
         uint4 v[kBatch];
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) v[b] = __ldg(piece + j + b * kScoreThreads);
+        for (int b = 0; b < kBatch; ++b) v[b] = __ldg(piece + j + b * kThreads);
         take(v, batch);
     }
     if (j < count) {
         uint4 v[kBatch];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-            const int at = j + b * kScoreThreads;
+            const int at = j + b * kThreads;
             v[b] = make_uint4(lowest_word<T>(), lowest_word<T>(), lowest_word<T>(), lowest_word<T>());
             if (at < count) v[b] = __ldg(piece + at);
         }
@@ -320,10 +319,10 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocksPerSm)
     }
     const uint32_t own_key = some ? max(key_of(own.m), own.worst) : 0u;
 
-    // The block's sums, and the maxima of its groups of four threads.
+    // The block's sums, and the maxima of its groups of two or four threads.
     uint32_t key = max(own_key, __shfl_xor_sync(~0u, own_key, 1));
-    key = max(key, __shfl_xor_sync(~0u, key, 2));
-    if (lane % 4 == 0) sh.group_key[tid / 4] = key;
+    if (kGroupThreads == 4) key = max(key, __shfl_xor_sync(~0u, key, 2));
+    if (lane % kGroupThreads == 0) sh.group_key[tid / kGroupThreads] = key;
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) {
         const Sums o{__shfl_xor_sync(~0u, own.m, d), __shfl_xor_sync(~0u, own.s, d),
@@ -332,10 +331,10 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocksPerSm)
     }
     if (lane == 0) sh.part[warp] = own;
     __syncthreads();
-    if (warp == kScoreWarps - 1) {
-        Sums p = lane < kScoreWarps ? sh.part[lane] : Sums{-INFINITY, 0.f, 0.f, 0u};
+    if (warp == kWarps - 1) {
+        Sums p = lane < kWarps ? sh.part[lane] : Sums{-INFINITY, 0.f, 0.f, 0u};
 #pragma unroll
-        for (int d = kScoreWarps / 2; d > 0; d /= 2) {
+        for (int d = kWarps / 2; d > 0; d /= 2) {
             const Sums o{__shfl_xor_sync(~0u, p.m, d), __shfl_xor_sync(~0u, p.s, d),
                          __shfl_xor_sync(~0u, p.t, d), __shfl_xor_sync(~0u, p.worst, d)};
             p = add(p, o);
@@ -376,32 +375,32 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocksPerSm)
                     for (int k = 0; k < kWord; ++k) offer(f[k], index + i * kWord + k);
                 }
             };
-            constexpr int kTurn = kBatch * kScoreThreads;
+            constexpr int kTurn = kBatch * kThreads;
             if (own_key != 0u && own_key >= least)
                 sh.list[atomicAdd(&sh.listed, 1)] = (uint16_t)tid;
             __syncthreads();
             const int listed = sh.listed, turns = (count + kTurn - 1) / kTurn;
-            for (int u = tid; u < listed * turns; u += kScoreThreads) {
+            for (int u = tid; u < listed * turns; u += kThreads) {
                 const int who = sh.list[u % listed], turn = u / listed;
                 if (turn < kKept) {
                     if (turn * kTurn + who >= count ||
                         key_of(to_float(sh.batch_top[turn][who])) < least)
                         continue;
                     const int at = atomicAdd(&sh.batches, 1);
-                    if (at < kScoreThreads) {
+                    if (at < kThreads) {
                         sh.batch[at] = (uint32_t)who | (uint32_t)turn << 16;
                         continue;
                     }
                 }
                 // not kept, or too many for the list: here and now
-                for (int b = 0; b < kBatch; ++b) offer_piece(turn * kTurn + b * kScoreThreads + who);
+                for (int b = 0; b < kBatch; ++b) offer_piece(turn * kTurn + b * kThreads + who);
             }
             if (tid < loose) offer(to_float(x[loose_at]), loose_at);
             __syncthreads();
-            const int batches = min(sh.batches, kScoreThreads);
-            for (int u = tid; u < batches * kBatch; u += kScoreThreads) {
+            const int batches = min(sh.batches, kThreads);
+            for (int u = tid; u < batches * kBatch; u += kThreads) {
                 const uint32_t what = sh.batch[u / kBatch];
-                offer_piece((int)(what >> 16) * kTurn + u % kBatch * kScoreThreads +
+                offer_piece((int)(what >> 16) * kTurn + u % kBatch * kThreads +
                             (int)(what & 0xFFFFu));
             }
             __syncthreads();
@@ -426,14 +425,14 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocksPerSm)
         }
         if (above) {
             found = cut == 0xFFFFFFFFu ? 0 : collect(cut + 1);
-            for (int base = 0; found < a.top && base < part; base += kScoreThreads) {
+            for (int base = 0; found < a.top && base < part; base += kThreads) {
                 const int index = index_of(min(base + tid, part - 1));
                 const bool equal = base + tid < part && key_of(to_float(x[index])) == cut;
                 const uint32_t mask = __ballot_sync(~0u, equal);
                 if (lane == 0) sh.equal[warp] = __popc(mask);
                 __syncthreads();
                 int at = found + __popc(mask & ((1u << lane) - 1));
-                for (int w = 0; w < kScoreWarps; ++w) {
+                for (int w = 0; w < kWarps; ++w) {
                     if (w < warp) at += sh.equal[w];
                     found += sh.equal[w];
                 }
@@ -443,7 +442,7 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocksPerSm)
             }
         }
         if (found <= kCandidates) {
-            for (int i = tid; i < found; i += kScoreThreads) {
+            for (int i = tid; i < found; i += kThreads) {
                 const uint64_t mine = sh.candidate[i];
                 int before = 0;
                 for (int j = 0; j < found; ++j) before += sh.candidate[j] > mine;
@@ -456,7 +455,7 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocksPerSm)
             uint64_t last = ~0ull;
             for (int k = 0; k < a.top; ++k) {
                 uint64_t next = 0;
-                for (int e = tid; e < part; e += kScoreThreads) {
+                for (int e = tid; e < part; e += kThreads) {
                     const int index = index_of(e);
                     const uint64_t r = rank_of(key_of(to_float(x[index])), index);
                     if (r < last) next = max(next, r);
@@ -465,7 +464,7 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocksPerSm)
                 for (int d = 16; d > 0; d /= 2) next = max(next, __shfl_xor_sync(~0u, next, d));
                 if (lane == 0) sh.warp_best[warp] = next;
                 __syncthreads();
-                for (int w = 0; w < kScoreWarps; ++w) next = max(next, sh.warp_best[w]);
+                for (int w = 0; w < kWarps; ++w) next = max(next, sh.warp_best[w]);
                 last = next;
                 if (tid == 0) sh.best[k] = next;
                 __syncthreads();
@@ -534,17 +533,16 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocksPerSm)
 int score_blocks(int64_t rows, int64_t vocabulary, int size, const DeviceCtx& ctx) {
     int blocks = 1;
     while (blocks < kMaxCluster && rows * blocks * 2 <= ctx.num_sms &&
-           vocabulary * size / 16 >= (int64_t)blocks * 2 * kScoreThreads)
+           vocabulary * size / 16 >= (int64_t)blocks * 2 * 256)
         blocks *= 2;
     return blocks;
 }
 
-template <typename T>
-cudaError_t score(const ScoreArgs& a, cudaStream_t stream, const DeviceCtx& ctx) {
-    const int blocks = score_blocks(a.rows, a.vocabulary, sizeof(T), ctx);
+template <typename T, int kThreads>
+cudaError_t score(const ScoreArgs& a, int blocks, cudaStream_t stream, const DeviceCtx& ctx) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.rows * blocks));
-    cfg.blockDim = dim3(kScoreThreads);
+    cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -555,8 +553,19 @@ cudaError_t score(const ScoreArgs& a, cudaStream_t stream, const DeviceCtx& ctx)
     cfg.attrs = attr;
     cfg.numAttrs = blocks > 1 ? 2 : 1;
     // rows to a wave of blocks; clusters have one wave
-    const int64_t ahead = blocks > 1 ? a.rows : (int64_t)kScoreBlocksPerSm * ctx.num_sms;
-    return cudaLaunchKernelEx(&cfg, score_kernel<T>, a, blocks, ahead);
+    const int64_t ahead = blocks > 1 ? a.rows : (int64_t)(kSmThreads / kThreads) * ctx.num_sms;
+    return cudaLaunchKernelEx(&cfg, score_kernel<T, kThreads>, a, blocks, ahead);
+}
+
+// Rows of less than two batches of pieces for 256 threads go by blocks of 128: what a block does
+// after its pass then runs beside seven others' (2047 rows of 32000 fp16 logits 30.5 us, by 256
+// threads 35.8; of 128256, top 20, 95 and 91).
+template <typename T>
+cudaError_t score(const ScoreArgs& a, cudaStream_t stream, const DeviceCtx& ctx) {
+    const int blocks = score_blocks(a.rows, a.vocabulary, sizeof(T), ctx);
+    return blocks == 1 && a.vocabulary * (int64_t)sizeof(T) / 16 < 2 * kBatch * 256
+               ? score<T, 128>(a, blocks, stream, ctx)
+               : score<T, 256>(a, blocks, stream, ctx);
 }
 
 }  // namespace
