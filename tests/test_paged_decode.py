@@ -69,3 +69,81 @@ def test_too_few_pages(w4lib):
 def test_the_example_runs(w4lib, capsys):
     paged_decode.main()
     assert "pages held" in capsys.readouterr().out
+
+
+def test_a_decode_step_in_a_graph(w4lib):
+    """Room, append and attention of a step captured once and replayed, as eager calls leave
+    the cache and their outputs; also all of it on a stream of its own."""
+    def fresh():
+        cache = w4.PagedCache(2, 5, 40, 2, 64, page_size=8, max_length=64)
+        g = torch.Generator(device="cuda").manual_seed(1)
+        cache.pool.normal_(generator=g)
+        cache.extend(paged_decode.ints([0, 1, 3]), paged_decode.ints([7, 8, 30]))
+        return cache
+
+    g = torch.Generator(device="cuda").manual_seed(2)
+    steps = [torch.randn(3, 5, 2, 64, generator=g, device="cuda").half() for _ in range(4)]
+    rows = torch.arange(5, dtype=torch.int32, device="cuda")
+
+    def step(cache, x, stream=None):
+        starts = cache.lengths.clone()
+        done = cache.extend(rows, (starts > 0).int(), stream=stream)
+        outs = []
+        for layer in range(2):
+            cache.append(layer, x[0], x[1], starts, stream=stream)
+            q = x[2].repeat_interleave(4, 1).contiguous()
+            outs.append(cache.attend(layer, q, stream=stream))
+        return (done, *outs)
+
+    eager = fresh()
+    want = [[t.clone() for t in step(eager, x)] for x in steps]
+    captured = fresh()
+    x = steps[0].clone()
+    books = [t.clone() for t in (captured.refs, captured.tables, captured.lengths)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step(captured, x)
+    for t, b in zip((captured.refs, captured.tables, captured.lengths), books):
+        assert torch.equal(t, b)               # a capture runs nothing
+    for now, values in zip(steps, want):
+        x.copy_(now)
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(outs, values))
+    aside = fresh()
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    for now, values in zip(steps, want):
+        with torch.cuda.stream(stream):
+            got = step(aside, now, stream)
+        stream.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, values))
+    for cache in (captured, aside):
+        for t, b in zip((cache.refs, cache.tables, cache.lengths, cache.pool),
+                        (eager.refs, eager.tables, eager.lengths, eager.pool)):
+            assert torch.equal(t, b)
+
+
+def test_listed_rows_on_another_stream(w4lib):
+    """The listed rows' tables and lengths are taken on the call's stream, not on the current
+    one, which is busy with something else."""
+    cache = w4.PagedCache(1, 6, 30, 2, 64, page_size=16, max_length=64)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    cache.pool.normal_(generator=g)
+    cache.extend(paged_decode.ints([0, 2, 5]), paged_decode.ints([40, 20, 9]))
+    rows = paged_decode.ints([5, 0])
+    q = torch.randn(2, 8, 64, generator=g, device="cuda").half()
+    k, v = (torch.randn(2, 2, 64, generator=g, device="cuda").half() for _ in range(2))
+    starts = paged_decode.ints([8, 39])
+    want = cache.pool.clone()
+    for i, (r, p) in enumerate(((5, 8), (0, 39))):
+        page = int(cache.tables[r, p // 16])
+        want[0, page, p % 16], want[1, page, p % 16] = k[i], v[i]
+    x = w4.paged_attention(q, want[0], want[1], cache.tables[[5, 0]], cache.lengths[[5, 0]])
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)             # some 50 ms on the current stream
+    cache.append(0, k, v, starts, rows=rows, stream=stream)
+    out = cache.attend(0, q, rows=rows, stream=stream)
+    stream.synchronize()
+    with torch.cuda.stream(stream):
+        assert torch.equal(out, x) and torch.equal(cache.pool, want)

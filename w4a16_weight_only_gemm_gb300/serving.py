@@ -383,6 +383,14 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0, str
     return logprobs, entropies, ids, likeliest
 
 
+def _pick(t: torch.Tensor, rows: torch.Tensor, stream) -> torch.Tensor:
+    """The listed rows of t, taken on the stream the call runs on."""
+    if stream is None:
+        return t.index_select(0, rows)
+    with torch.cuda.stream(stream):
+        return t.index_select(0, rows)
+
+
 class PagedCache:
     """The keys and values of a decoder's layers for `rows` sequences, in pages
     that sequences take, share and give back.
@@ -424,7 +432,7 @@ class PagedCache:
                offsets: torch.Tensor | None = None, rows: torch.Tensor | None = None,
                stream=None) -> None:
         """New tokens of every row (or of the listed ones) of one layer (paged_append)."""
-        tables = self.tables if rows is None else self.tables.index_select(0, rows)
+        tables = self.tables if rows is None else _pick(self.tables, rows, stream)
         paged_append(k, v, self.keys(layer), self.values(layer), tables, starts, offsets,
                      stream=stream)
 
@@ -433,7 +441,7 @@ class PagedCache:
         """Attention of one new token of every row (or of the listed ones) (paged_attention)."""
         tables, lengths = self.tables, self.lengths
         if rows is not None:
-            tables, lengths = tables.index_select(0, rows), lengths.index_select(0, rows)
+            tables, lengths = _pick(tables, rows, stream), _pick(lengths, rows, stream)
         return paged_attention(q, self.keys(layer), self.values(layer), tables, lengths,
                                scale=scale, out=out, stream=stream)
 
