@@ -136,6 +136,31 @@ def test_fork(w4lib, pages, rows, width, ps, in_place):
     assert torch.equal(pool, want)
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+def test_fork_long_lists_with_requests_that_are_refused(w4lib, in_place):
+    """More requests than a block has threads; every third past the first thousand names a row
+    that is not there, behind requests of the same thread that were granted."""
+    rows, ps = 2600, 4
+    b = [1] * 3 + [0] * 3000, [[0, 1, 2, -1]] + [[-1] * 4 for _ in range(rows - 1)], \
+        [11] + [0] * (rows - 1)
+    children = list(range(1, 2500))
+    parents = [0] * len(children)
+    for i in range(1024, len(children), 3):
+        if i % 2:
+            parents[i] = rows + i
+        else:
+            children[i] = -1 - i
+    pool = fill(2, 3003, (8,), torch.float16)
+    want = pool.clone()
+    ins, out = books(b, in_place)
+    got = w4.pages_fork(pool, *ins, ints(parents), ints(children), ps, out=out)
+    *books_want, copies = ref.fork(*b, parents, children, ps)
+    same(got, books_want)
+    for a, z in copies:
+        want[:, z] = want[:, a]
+    assert torch.equal(pool, want)
+
+
 def test_fork_exhausts_and_chains(w4lib):
     """Too few pages for all; a child that is also listed as an (empty) parent."""
     b = [1, 1, 0, 0], [[0, 1, -1]] + [[-1] * 3 for _ in range(5)], [6, 0, 0, 0, 0, 0]

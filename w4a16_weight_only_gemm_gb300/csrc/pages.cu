@@ -326,8 +326,11 @@ __global__ void __launch_bounds__(kBookThreads)
         serve_in_order(
             count, n_free,
             [&](int64_t i) -> int64_t {
-                ForkRequest q = early;
-                if (i >= kBookThreads) q.read(b, parents, children, i);
+                ForkRequest q;  // a new one: reading leaves what it does not find as it was
+                if (i < kBookThreads)
+                    q = early;
+                else
+                    q.read(b, parents, children, i);
                 s.from[i] = s.to[i] = -1;
                 s.length[i] = q.length;
                 if (q.child_length != 0 || claim[q.to] != i) return -1;
