@@ -9,6 +9,7 @@ terms, by (1 + H + ln n) times as much."""
 from __future__ import annotations
 
 import math
+import random
 
 import pytest
 import torch
@@ -168,6 +169,29 @@ def test_past_32_bit_offsets(w4lib):
     want = ref.scores(x[-1:], tokens[-1:], 2)
     assert got[2][-1].tolist() == [128255, 5] and got[2][0].tolist() == [0, 1]
     assert abs(got[0][-1].item() - want[0].item()) < 1e-4
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_random_rows(w4lib, seed):
+    rng = random.Random(seed)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    n = rng.choice((3, 9, 513, 2047, 4096, 16384, 32767, 32768, 70001, 131072, 300001))
+    rows = min(rng.choice((1, 2, 19, 38, 76, 77, 151, 160, 305)),
+               max(1, (100_000 if n <= 4096 else 3_000_000) // n))
+    dtype, shift = rng.choice(TYPES), rng.randrange(0, 9)
+    wide = torch.randn(rows, n + shift + rng.randrange(0, 5), generator=g, device="cuda")
+    wide *= rng.choice((0.01, 1.0, 4.0, 30.0))
+    kind = seed % 5
+    if kind == 1:
+        wide = (wide * 0.3).round()
+    elif kind == 2:
+        wide[:, rng.randrange(0, 12):] = -math.inf
+    elif kind == 3:
+        wide[torch.rand(wide.shape, generator=g, device="cuda") < 0.7] = -math.inf
+    elif kind == 4:
+        wide[torch.rand(wide.shape, generator=g, device="cuda") < 0.9] = torch.finfo(dtype).min
+    tokens = torch.randint(-1, n + 1, (rows,), generator=g, device="cuda")
+    check(wide.to(dtype)[:, shift:shift + n], tokens, rng.randrange(0, min(n, 32) + 1))
 
 
 def test_refusals(w4lib):

@@ -326,6 +326,54 @@ def test_append_nothing_and_many(w4lib):
     assert torch.equal(v_pool[pages].flatten(0, 1)[:9000], v)
 
 
+@pytest.mark.parametrize("seed", range(30))
+def test_random_caches(w4lib, seed):
+    rng = random.Random(seed)
+    kv_heads, group = rng.choice((1, 2, 3, 8)), rng.choice((1, 2, 5, 7, 8, 9, 16, 17, 33))
+    dim = rng.choice((8, 40, 64, 72, 96, 128, 136, 200, 256))
+    page = rng.choice((1, 2, 5, 16, 17, 32, 48, 64, 100, 128))
+    rows = rng.choice((1, 2, 3, 9, 40, 130))
+    longest = rng.choice((1, 17, 100, 300, 1500 if rows < 10 else 200))
+    lengths = [rng.choice((0, rng.randint(0, longest), longest)) for _ in range(rows)]
+    need = max(1, max(-(-n // page) for n in lengths))
+    case = make(lengths, kv_heads, group, dim, page, rng.choice((torch.float16, torch.bfloat16)),
+                rng.choice(("slots", "heads", "both")), seed=seed,
+                width=rng.choice((None, need + rng.randint(0, 50), need + 70000 // page)),
+                garbage=rng.choice((math.nan, math.inf, 0.0)))
+    if rng.random() < 0.2:
+        case[3][rng.randrange(rows), 0] = rng.choice((-1, case[1].shape[0], 2 ** 31 - 1))
+    check(*case, scale=rng.choice((None, None, 0.3, -0.1)))
+
+
+@pytest.mark.parametrize("seed", range(20))
+def test_append_to_many_rows(w4lib, seed):
+    """Rows by the thousand, most without a token, tokens before the first row and past the last."""
+    rng = random.Random(seed)
+    rows, page = rng.choice((1, 2, 31, 32, 33, 1000, 1025, 3000)), rng.choice((1, 7, 16))
+    counts = [rng.choice((0, 0, 1, rng.randint(0, 9))) for _ in range(rows)]
+    counts[rng.randrange(rows)] += rng.choice((0, 500))
+    starts = [rng.randint(0, 2 * page) for _ in range(rows)]
+    _, k_pool, v_pool, tables, _ = make([s + n for s, n in zip(starts, counts)], 2, 1, 24, page,
+                                        torch.float16, rng.choice(("slots", "heads")), seed=seed,
+                                        garbage=2.0)
+    first, past = rng.choice((0, 3)), rng.choice((0, 5))
+    offsets = [first]
+    for n in counts:
+        offsets.append(offsets[-1] + n)
+    k, v = (torch.randn(offsets[-1] + past, 2, 24, device="cuda").half() for _ in range(2))
+    at = [(b, s + i) for b, (s, n) in enumerate(zip(starts, counts)) for i in range(n)]
+    want = [k_pool.clone(), v_pool.clone()]
+    if at:
+        row, position = (torch.tensor(x, device="cuda") for x in zip(*at))
+        pages = tables[row, position // page].long()
+        for pool, new in zip(want, (k, v)):
+            pool[pages, position % page] = new[first:offsets[-1]]
+    w4.paged_append(k, v, k_pool, v_pool, tables,
+                    torch.tensor(starts, dtype=torch.int32, device="cuda"),
+                    torch.tensor(offsets, dtype=torch.int32, device="cuda"))
+    assert torch.equal(k_pool, want[0]) and torch.equal(v_pool, want[1])
+
+
 def test_refusals(w4lib):
     q, k, v, tables, lengths = make([20, 5], 2, 2, 64, 16, torch.float16, garbage=0.0)
     good = (q, k, v, tables, lengths)

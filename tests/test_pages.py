@@ -249,6 +249,45 @@ def test_copy_past_32_bit_offsets(w4lib):
     assert (pool[:, 1, -5:] == 3).all() and (pool[:, 1, :-5] == 0).all()
 
 
+@pytest.mark.parametrize("seed", range(60))
+def test_random_books(w4lib, seed):
+    """Sizes on both sides of every change in how the work is done, lists with rows out of
+    range and twice, in place and apart."""
+    rng = random.Random(seed)
+    pages = rng.choice((1, 2, 31, 33, 511, 513, 4095, 4096, 4097, 16384, 16385, 40000))
+    rows = rng.choice((1, 7, 100, 257, 1023, 1025, 4096, 4097))
+    width, ps = rng.choice((2, 3, 9, 33, 70)), rng.choice((1, 3, 16))
+    b = make(pages, rows, width, ps, rng.randrange(0, pages + 1), seed=seed)
+    ins, out = books(b, rng.random() < 0.4, wide=rng.random() < 0.5)
+    n = rng.choice((0, 1, 5, 255, 256, 257, 1024, 1025, 3000))
+    listed = [rng.randrange(-1, rows + 1) for _ in range(n)]
+    empty = [r for r, m in enumerate(b[2]) if m == 0] or [0]
+    children = [rng.choice(empty) if rng.random() < 0.8 else rng.randrange(-1, rows + 1)
+                for _ in range(n)]
+    counts = [rng.choice((-1, 0, 1, 2, ps, 3 * ps, width * ps)) for _ in range(n)]
+    pool = fill(2, pages, (8,), torch.float16, seed=seed)
+    moved, copies = pool.clone(), []
+    what = seed % 4
+    if what == 0:
+        got, want = w4.pages_free(*ins, ints(listed), out=out), ref.free(*b, listed)
+    elif what == 1:
+        got = w4.pages_extend(*ins, ints(listed), ints(counts), ps, out=out)
+        want = ref.extend(*b, listed, counts, ps)
+    elif what == 2:
+        got = w4.pages_fork(pool, *ins, ints(listed), ints(children), ps, out=out)
+        *want, copies = ref.fork(*b, listed, children, ps)
+    else:
+        got = w4.pages_compact(pool, *ins[:2], out=out[:2] if out else None)
+        *want, copies = ref.compact(*b[:2])
+    same(got, want)
+    if copies:
+        sources, targets = (torch.tensor(t, device="cuda") for t in zip(*copies))
+        moved[:, targets] = moved[:, sources]
+    assert torch.equal(pool, moved)
+    if out is None:
+        same(ins, b)
+
+
 def test_life_of_a_cache(w4lib):
     """Random lives of rows through PagedCache, its books checked at every step."""
     rng = random.Random(6)
