@@ -440,7 +440,9 @@ typedef struct w4a16_query_shape {
  *              done, and not to be shared by calls that may run at once.  Where
  *              that is 0 bytes, any aligned pointer other than NULL.
  * Positions whose page number is outside [0, pages) are left out, as if
- * masked.  The result does not depend on how the work was split beyond the
+ * masked, and so are those whose score is -infinity; a head that has no other
+ * position gets what a row of length 0 gets.  A head with a score that is NaN
+ * or +infinity gets NaN, in out and in lse.  The result does not depend on how the work was split beyond the
  * order of its FP32 sums; two calls on the same inputs give the same bits.
  * Errors: NULL -> W4A16_ERR_NULL; sizes outside the ranges above ->
  * W4A16_ERR_SHAPE; q, out, a pool or the workspace not 16-byte aligned ->

@@ -379,7 +379,8 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
         hi = cut(n, rank + 1, a.cluster);
         if (tid == 0)
             begin = {row, item % a.items, (int)lo, n, length, a.head_offset(item % a.items)};
-        if (tid < kHeads) block_ml[tid] = make_float2(-INFINITY, 0.f);
+        // a sum below 0: no step, and nothing written at this block's ring's start
+        if (tid < kHeads) block_ml[tid] = make_float2(-INFINITY, -1.f);
     } else {
         const int per = (a.c.batch + kAttendThreads - 1) / kAttendThreads;
         const int r0 = min(tid * per, a.c.batch), r1 = min(r0 + per, a.c.batch);
@@ -750,7 +751,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int r = 0; r < kMaxCluster; ++r) {
-                if (ml[r].x == -INFINITY) continue;  // no step, and nothing written at its ring's start
+                if (ml[r].y < 0.f) continue;  // no step; a maximum of -infinity may have a sum of NaN
                 const float e = exp2_fast(ml[r].x - base);
                 l += e * ml[r].y;
                 v.x += e * u[r].x, v.y += e * u[r].y, v.z += e * u[r].z, v.w += e * u[r].w;
