@@ -442,8 +442,12 @@ typedef struct w4a16_query_shape {
  * Positions whose page number is outside [0, pages) are left out, as if
  * masked, and so are those whose score is -infinity; a head that has no other
  * position gets what a row of length 0 gets.  A head with a score that is NaN
- * or +infinity gets NaN, in out and in lse.  The result does not depend on how the work was split beyond the
- * order of its FP32 sums; two calls on the same inputs give the same bits.
+ * or +infinity gets NaN, in out and in lse.  A value of +-infinity gives the
+ * infinity in its dimension of out, NaN beside a NaN or the opposite one, and
+ * also where its weight is below 2^-36 (fp16) or 2^-126 (bf16) of the head's
+ * largest, which may count as 0.  The result does not depend on how the work
+ * was split beyond the order of its FP32 sums; two calls on the same inputs
+ * give the same bits.
  * Errors: NULL -> W4A16_ERR_NULL; sizes outside the ranges above ->
  * W4A16_ERR_SHAPE; q, out, a pool or the workspace not 16-byte aligned ->
  * W4A16_ERR_ALIGN.

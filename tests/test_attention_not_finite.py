@@ -96,3 +96,31 @@ def test_all_keys_of_a_head(case, value):
     q = case[0].clone()
     q[:, :KV * GROUP, 3] = q[:, :KV * GROUP, 3].abs() + 0.5    # all scores +infinity or -infinity
     check(case, (q, k, case[2]))
+
+
+@pytest.mark.parametrize("values", [[math.inf], [-math.inf], [math.nan], [math.inf, math.inf],
+                                    [math.inf, -math.inf], [math.inf, math.nan]], ids=str)
+def test_values(case, values):
+    """Infinite and missing values in held places: weights are above 0, so an infinity shows
+    as it is, beside an opposite one or a NaN as NaN, in its own dimension alone."""
+    v, tables = case[2].clone(), case[3]
+    for row in (0, 1, 2, 4, 7):
+        n = LENGTHS[row]
+        for i, value in enumerate(values[:n]):
+            for p in (n - 1 - i, i * (n // 3)):    # side by side, and steps apart
+                page, slot = spot(tables, row, p)
+                v[page, slot, 1, 9 + p % 5] = value
+                v[page, slot, 0, 63] = value
+    check(case, (*case[:2], v))
+
+
+def test_values_of_equal_weight(w4lib, dtype):
+    """Weights that 16 bits hold exactly, so that nothing is left over for a second part."""
+    case = make(LENGTHS, KV, GROUP, DIM, PAGE, dtype, seed=22)
+    case[0].zero_()
+    v, tables = case[2].clone(), case[3]
+    for row in (0, 1, 2, 4):
+        page, slot = spot(tables, row, LENGTHS[row] - 1)
+        v[page, slot, 0, :32] = math.inf
+        v[page, slot, 0, 32:] = -math.inf
+    check(case, (*case[:2], v))

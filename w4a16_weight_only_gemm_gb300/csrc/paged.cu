@@ -151,7 +151,10 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
 // lanes' 16-byte reads and V's for the matrix loads.
 // P is split in two 16-bit parts, its value and what rounding that left over,
 // so that the probabilities keep 22 (fp16) or 16 (bf16) bits: the MMAs are
-// far from the bound, and the output is then rounded only once.
+// far from the bound, and the output is then rounded only once.  The first part
+// is rounded down and the second never 0 beside it, so both have the sign of
+// the weight: an infinite value meets no zero and no opposite sign, which would
+// turn it into NaN.
 //
 // On one GB300 (6790 GB/s copied), 8 key-value heads of 128 and 4 query heads
 // to each: one row of 131071 positions 85.7 us (6260 GB/s), 128 rows of up to
@@ -222,6 +225,16 @@ template <>
 __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
+}
+// The same, rounded towards zero.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2_down(float lo, float hi) {
+    uint32_t r;
+    if constexpr (std::is_same<T, __half>::value)
+        asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 template <typename T>
 __device__ __forceinline__ float2 unpack2(uint32_t v);
@@ -360,6 +373,8 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
     attend_kernel(AttendArgs a) {
     using S = AttendShape<DP, NT>;
     constexpr int kHeads = 8 * NT;
+    // the least a part of a weight can be: FP16's smallest number, BF16's smallest normal one
+    constexpr float kLeast = std::is_same<T, __half>::value ? 0x1p-24f : 0x1p-126f;
     extern __shared__ __align__(16) unsigned char ring[];
     __shared__ int64_t scan[kAttendWarps];
     __shared__ Place begin;
@@ -632,10 +647,13 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<DP, NT>::kBlocksPe
             sum[n][1] += c[n][1] + c[n][3];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {  // positions g and g + 8
-                const uint32_t hi16 = pack2<T>(c[n][2 * r], c[n][2 * r + 1]);
+                const float p0 = c[n][2 * r], p1 = c[n][2 * r + 1];
+                const uint32_t hi16 = pack2_down<T>(p0, p1);
                 const float2 back = unpack2<T>(hi16);
                 p_hi[n][r] = transpose8x8(hi16);
-                p_lo[n][r] = transpose8x8(pack2<T>(c[n][2 * r] - back.x, c[n][2 * r + 1] - back.y));
+                // a weight below kLeast has no first part and stays what it is
+                p_lo[n][r] = transpose8x8(pack2<T>(fmaxf(p0 - back.x, fminf(p0, kLeast)),
+                                                   fmaxf(p1 - back.y, fminf(p1, kLeast))));
             }
         }
 #pragma unroll
