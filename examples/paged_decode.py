@@ -97,18 +97,19 @@ def prefill(model: Decoder, cache: w4.PagedCache, prompts: list[list[int]], rows
     return model.forward(tokens, positions, attend)[offsets[1:].long() - 1]
 
 
-def decode(model: Decoder, cache: w4.PagedCache, tokens: torch.Tensor) -> torch.Tensor:
-    """One token of every row of the cache; the next token's logits.  A row of length 0 (or
-    one that found no page) takes no part: its logits say nothing."""
+def decode(model: Decoder, cache: w4.PagedCache, tokens: torch.Tensor):
+    """One token of every row of the cache; the next token's logits, and PagedCache.extend's
+    answer.  A row of length 0 takes no part, and one whose answer is 0 found no page for its
+    token (or was listed after such a row): their logits say nothing."""
     rows = torch.arange(cache.tables.shape[0], dtype=torch.int32, device="cuda")
     starts = cache.lengths.clone()
-    cache.extend(rows, (starts > 0).int())
+    done = cache.extend(rows, (starts > 0).int())
 
     def attend(layer, q, k, v):
         cache.append(layer, k, v, starts)
         return cache.attend(layer, q)
 
-    return model.forward(tokens, starts, attend)
+    return model.forward(tokens, starts, attend), done
 
 
 def best_of(model: Decoder, cache: w4.PagedCache, prompts: list[list[int]], n: int, steps: int,
@@ -126,14 +127,18 @@ def best_of(model: Decoder, cache: w4.PagedCache, prompts: list[list[int]], n: i
     logits = logits.repeat_interleave(n, 0)
     total = torch.zeros(count * n, device="cuda")
     sampled = []
+    placed = torch.ones(count * n, dtype=torch.int32, device="cuda")
     for step in range(steps):
         if step:
-            logits = decode(model, cache, sampled[-1])
+            logits, done = decode(model, cache, sampled[-1])
+            placed &= done                     # looked at once, after the last step
         noise = torch.rand(logits.shape, generator=g, device="cuda").clamp_min(1e-9)
         tokens = (logits.float() - torch.log(-torch.log(noise))).argmax(1)
         logprobs, _, _, _ = w4.token_logprobs(logits, tokens, top=4)
         total += logprobs
         sampled.append(tokens)
+    if not placed.all():
+        raise RuntimeError("the cache ran out of free pages while decoding")
     best = total.view(count, n).argmax(1) + torch.arange(count, device="cuda") * n
     kept = best.tolist()
     cache.free(ints([r for r in range(count * n) if r not in kept]))

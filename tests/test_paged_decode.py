@@ -147,3 +147,15 @@ def test_listed_rows_on_another_stream(w4lib):
     stream.synchronize()
     with torch.cuda.stream(stream):
         assert torch.equal(out, x) and torch.equal(cache.pool, want)
+
+
+def test_too_few_pages_while_decoding(w4lib):
+    """A prompt of 20 and a branch fit in 4 pages of 16; the 13th step of the two does not."""
+    model = paged_decode.Decoder(layers=1)
+
+    def cache():
+        return w4.PagedCache(1, 2, 4, model.kv_heads, model.head_dim, max_length=64)
+
+    assert paged_decode.best_of(model, cache(), [[1] * 20], 2, 12)[1]
+    with pytest.raises(RuntimeError, match="decoding"):
+        paged_decode.best_of(model, cache(), [[1] * 20], 2, 16)
