@@ -417,3 +417,28 @@ def test_no_rows(w4lib):
     out, lse = w4.paged_attention(q[:0], k, v, tables[:0], lengths[:0], return_lse=True)
     assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
     w4.paged_append(q[:0, :2], q[:0, :2], k, v, tables[:0], lengths[:0])
+
+
+@pytest.mark.parametrize("page, width", [(14322, 149943), (8176, 262657)])
+def test_lengths_up_to_the_last_31_bit_position(w4lib, page, width):
+    """A table for 2^31 - 2 and for 2^31 - 16 positions, all on one page but the last.  Head 0
+    weighs all alike: sums of whole numbers below 2^24 a warp, so what is off is the join of at
+    most 1024 parts (2^-14) and the output's rounding.  Head 1 sees the last position alone."""
+    total = page * width
+    assert 2 ** 31 - 64 < total < 2 ** 31
+    q = torch.zeros(1, 2, 8, dtype=torch.float16)
+    q[0, 1] = 1.0
+    k = torch.zeros(2, page, 1, 8, dtype=torch.float16)
+    k[1, -1] = 6.0                              # a score of 48 = 2 ln 2^31 and more
+    v = (torch.arange(page) % 8)[None, :, None, None].expand(2, -1, 1, 8).half().contiguous()
+    v[1, -1] = 100.0
+    tables = torch.zeros(1, width, dtype=torch.int32)
+    tables[0, -1] = 1
+    mean = ((v[0, :, 0, 0].double().sum() * width + 100 - v[0, -1, 0, 0]) / total).item()
+    for length in (total, 2 ** 31 - 1):
+        out, lse = w4.paged_attention(q.cuda(), k.cuda(), v.cuda(), tables.cuda(),
+                                      torch.tensor([length], dtype=torch.int32).cuda(),
+                                      scale=1.0, return_lse=True)
+        assert ((out[0, 0].cpu().double() - mean).abs() <= mean * (2.0 ** -11 + 2.0 ** -13)).all()
+        assert abs(lse[0, 0].item() - math.log(total)) <= 2.0 ** -13
+        assert (out[0, 1] == 100).all() and abs(lse[0, 1].item() - 48) <= 2.0 ** -12

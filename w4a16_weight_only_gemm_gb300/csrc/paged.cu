@@ -322,7 +322,10 @@ struct Place {
     int64_t head;  // of the item's keys and values in their pools
 };
 
-__device__ __forceinline__ int steps_of(int length) { return (length + kStep - 1) / kStep; }
+// (unsigned: lengths go up to 2^31 - 1)
+__device__ __forceinline__ int steps_of(int length) {
+    return (int)(((uint32_t)length + kStep - 1) / kStep);
+}
 
 __device__ __forceinline__ void advance(const AttendArgs& a, Place& p) {
     if (++p.tile < p.steps) return;
