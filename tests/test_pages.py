@@ -374,3 +374,69 @@ def test_refusals(w4lib):
         w4.pages_compact(fill(2, 8, (7,), torch.float16), refs, tables)     # 14-byte pages
     with pytest.raises(ValueError):
         w4.pages_copy(pool, one, ints([1, 2]))
+
+
+# (values of a page, planes): one piece of 16 KB and several, the last one partly filled; 52 and
+# 53 planes are on both sides of 128 MB of copies by 32 pages of 80016 bytes.
+POOLS = [(8, 3), (1000, 3), (8192, 2), (8200, 2), (16384, 5), (40008, 1), (40008, 52), (40008, 53)]
+
+
+def gapped(planes, pages, values, seed):
+    """A pool with foreign planes around it and gaps between its pages, and all of its memory."""
+    wide = fill(planes + 2, pages, (values + 8,), torch.float16, seed=seed)
+    return wide[1:-1, :, :values], wide
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("gaps", [False, True])
+@pytest.mark.parametrize("values, planes", POOLS)
+def test_compact_moves_whole_pages(w4lib, values, planes, gaps, in_place):
+    b = make(64, 12, 9, 16, 40, seed=values)
+    pool, wide = gapped(planes, 64, values, planes)
+    if not gaps:
+        pool = wide = pool.contiguous()
+    want = wide.clone()
+    inner = want[1:-1, :, :values] if gaps else want
+    ins, out = books(b, in_place)
+    got = w4.pages_compact(pool, *ins[:2], out=out[:2] if out else None)
+    *books_want, copies = ref.compact(*b[:2])
+    assert len(copies) > 3
+    same(got, books_want)
+    for a, z in copies:
+        inner[:, z] = inner[:, a]
+    assert torch.equal(wide, want)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("gaps", [False, True])
+@pytest.mark.parametrize("values, planes", POOLS)
+def test_fork_copies_whole_pages(w4lib, values, planes, gaps, in_place):
+    """32 branches, some of parents that end on a page's edge and copy nothing, and too few free
+    pages for the last ones."""
+    ps, parents_of = 16, [5, 16, 40, 33, 0, 64, 1, 20]
+    tables, refs = [], [0] * 64
+    for i, n in enumerate(parents_of):
+        row = [(i * 7 + j * 11) % 64 for j in range(-(-n // ps))]
+        for p in row:
+            refs[p] += 1
+        tables.append(row + [-1] * (5 - len(row)))
+    free = [p for p in range(64) if refs[p] == 0]
+    for p in free[18:]:
+        refs[p] = 1                                # held by rows elsewhere
+    tables += [[-1] * 5 for _ in range(32)]
+    b = refs, tables, parents_of + [0] * 32
+    parents, children = [i * 3 % 8 for i in range(32)], list(range(8, 40))
+    random.Random(values).shuffle(children)
+    pool, wide = gapped(planes, 64, values, planes)
+    if not gaps:
+        pool = wide = pool.contiguous()
+    want = wide.clone()
+    inner = want[1:-1, :, :values] if gaps else want
+    ins, out = books(b, in_place)
+    got = w4.pages_fork(pool, *ins, ints(parents), ints(children), ps, out=out)
+    *books_want, copies = ref.fork(*b, parents, children, ps)
+    assert len(copies) == 18 and 0 in books_want[3]
+    same(got, books_want)
+    for a, z in copies:
+        inner[:, z] = inner[:, a]
+    assert torch.equal(wide, want)
