@@ -492,6 +492,18 @@ int64_t w4a16_pages_compact_workspace(const w4a16_books_shape *books,
                                       const w4a16_pool_shape *shape, int32_t apart);
 
 /*
+ * w4a16_pages_rows -- the listed rows of the books, for calls on some rows:
+ * tables_out [count, width], dense, and lengths_out [count], if it is not
+ * NULL, get those of row listed[i]; of a row outside [0, rows) they get -1 and
+ * 0, so that such a row has no position and takes no token.  pages, page_size
+ * and out_stride of the books are checked only.  Neither output overlaps an
+ * input.
+ */
+int w4a16_pages_rows(const int32_t *tables_in, const int32_t *lengths_in, const int32_t *listed,
+                     int64_t count, int32_t *tables_out, int32_t *lengths_out,
+                     const w4a16_books_shape *books, void *stream);
+
+/*
  * w4a16_pages_free -- gives back every page of the `count` rows listed: one
  * holder fewer for each, the row's page numbers -1 and its length 0.  A row
  * listed twice is given back once; one outside [0, rows) is passed over.

@@ -161,3 +161,15 @@ def test_pages_workspaces(lib):
     assert fork(books(pages=0), pool(), 2, 1) == -1 and fork(books(), pool(size=8), 2, 1) == -1
     assert fork(books(), pool(), -1, 1) == -1 and fork(None, pool(), 2, 1) == -1
     assert compact(books(), None, 1) == -1
+
+
+def test_listed_rows_arguments(lib):
+    def call(p, b=books(), count=2):
+        return lib.w4a16_pages_rows(*p[:3], count, *p[3:], b, None)
+
+    for i in (0, 1, 2, 3):                       # a NULL lengths_out asks for none
+        assert call([None if j == i else FAKE for j in range(5)]) == 1
+    assert call([FAKE] * 5, None) == 1
+    assert call([FAKE] * 5, count=-1) == 2 and call([FAKE] * 5, count=(1 << 24) + 1) == 2
+    for bad in (dict(rows=0), dict(width=0), dict(in_stride=-1), dict(out_stride=2)):
+        assert call([FAKE] * 5, books(**bad)) == 2

@@ -440,3 +440,53 @@ def test_fork_copies_whole_pages(w4lib, values, planes, gaps, in_place):
     for a, z in copies:
         inner[:, z] = inner[:, a]
     assert torch.equal(wide, want)
+
+
+@pytest.mark.parametrize("aside", [False, True])
+@pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
+def test_listed_rows_out_of_range(w4lib, dtype, aside):
+    """A PagedCache passes them over: no token of theirs is written, and their attention is that
+    of an empty row; the rows beside them are served."""
+    cache = w4.PagedCache(1, 3, 12, 2, 64, page_size=16, max_length=64)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    cache.pool.normal_(generator=g)
+    cache.extend(ints([0, 2]), ints([20, 33]))
+    listed = torch.tensor([-1, 2, 3, 0, 2 ** 31 - 1, -2 ** 31], dtype=dtype, device="cuda")
+    starts, offsets = ints([0, 30, 0, 18, 5, 3]), ints([0, 4, 7, 9, 11, 12, 20])
+    k, v = (torch.randn(20, 2, 64, generator=g, device="cuda").half() for _ in range(2))
+    q = torch.randn(6, 8, 64, generator=g, device="cuda").half()
+    want = cache.pool.clone()
+    for row, start, first, count in ((2, 30, 4, 3), (0, 18, 9, 2)):
+        for i in range(count):
+            page = int(cache.tables[row, (start + i) // 16])
+            want[0, page, (start + i) % 16] = k[first + i]
+            want[1, page, (start + i) % 16] = v[first + i]
+    x = w4.paged_attention(q[[1, 3]], want[0], want[1], cache.tables[[2, 0]], cache.lengths[[2, 0]])
+    stream = torch.cuda.Stream() if aside else None
+    torch.cuda.synchronize()
+    cache.append(0, k, v, starts, offsets, rows=listed, stream=stream)
+    out = cache.attend(0, q, rows=listed, stream=stream)
+    torch.cuda.synchronize()
+    assert torch.equal(cache.pool, want)
+    assert torch.equal(out[[1, 3]], x) and (out[[0, 2, 4, 5]] == 0).all()
+    assert starts.tolist() == [0, 30, 0, 18, 5, 3]
+
+
+@pytest.mark.parametrize("width", [1, 3, 1023, 1025, 5000])
+def test_listed_rows_of_wide_tables(w4lib, width):
+    """More rows and columns than one piece, from a slice of a wider table."""
+    g = torch.Generator(device="cuda").manual_seed(width)
+    cache = w4.PagedCache(1, 70, 4 * width, 1, 8, page_size=1, max_length=width)
+    wide = torch.randint(0, 4 * width, (70, width + 3), generator=g, device="cuda").int()
+    cache.tables = wide[:, 1:width + 1]
+    cache.lengths.random_(0, width + 1, generator=g)
+    cache.pool.normal_(generator=g)
+    listed = torch.randint(-3, 73, (300,), generator=g, device="cuda").int()
+    q = torch.randn(300, 2, 8, generator=g, device="cuda").half()
+    out = cache.attend(0, q, rows=listed)
+    inside = (listed >= 0) & (listed < 70)
+    at = listed[inside].long()
+    want = w4.paged_attention(q[inside], cache.keys(0), cache.values(0),
+                              cache.tables[at].contiguous(), cache.lengths[at])
+    assert torch.allclose(out[inside].float(), want.float(), rtol=2.0 ** -9, atol=2.0 ** -12)
+    assert (out[~inside] == 0).all()

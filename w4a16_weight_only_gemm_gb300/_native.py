@@ -48,6 +48,7 @@ SIGNATURES = {
     "w4a16_pages_workspace": (_I64, [_S, _I64]),
     "w4a16_pages_fork_workspace": (_I64, [_S, _S, _I64, _I32]),
     "w4a16_pages_compact_workspace": (_I64, [_S, _S, _I32]),
+    "w4a16_pages_rows": (ctypes.c_int, [_P] * 3 + [_I64] + [_P] * 2 + [_S, _P]),
     "w4a16_pages_free": (ctypes.c_int, [_P] * 4 + [_I64] + [_P] * 3 + [_S, _P]),
     "w4a16_pages_extend": (ctypes.c_int, [_P] * 5 + [_I64] + [_P] * 5 + [_S, _P]),
     "w4a16_pages_fork": (ctypes.c_int, [_P] * 6 + [_I64] + [_P] * 5 + [_S, _S, _P]),

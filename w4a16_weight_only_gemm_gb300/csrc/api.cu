@@ -438,6 +438,19 @@ int64_t w4a16_pages_compact_workspace(const w4a16_books_shape* books,
                : -1;
 }
 
+int w4a16_pages_rows(const int32_t* tables_in, const int32_t* lengths_in, const int32_t* listed,
+                     int64_t count, int32_t* tables_out, int32_t* lengths_out,
+                     const w4a16_books_shape* books, void* stream) {
+    if (!books || (count && (!tables_in || !listed || !tables_out || (lengths_out && !lengths_in))))
+        return W4A16_ERR_NULL;
+    if (!good_books(*books) || !good_count(count)) return W4A16_ERR_SHAPE;
+    DeviceCtx ctx;
+    if (int rc = device_ctx(&ctx)) return rc;
+    return from_cuda(launch_pages_rows(
+        {nullptr, tables_in, lengths_in, nullptr, tables_out, lengths_out, *books}, listed, count,
+        static_cast<cudaStream_t>(stream)));
+}
+
 int w4a16_pages_free(const int32_t* refs_in, const int32_t* tables_in, const int32_t* lengths_in,
                      const int32_t* listed, int64_t count, int32_t* refs_out, int32_t* tables_out,
                      int32_t* lengths_out, const w4a16_books_shape* books, void* stream) {

@@ -111,6 +111,8 @@ int64_t pages_fork_workspace(const w4a16_books_shape& books, const w4a16_pool_sh
                              int64_t count, bool apart);
 int64_t pages_compact_workspace(const w4a16_books_shape& books, const w4a16_pool_shape& shape,
                                 bool apart);
+cudaError_t launch_pages_rows(const PageBooks& books, const int32_t* listed, int64_t count,
+                              cudaStream_t stream);
 cudaError_t launch_pages_free(const PageBooks& books, const int32_t* listed, int64_t count,
                               cudaStream_t stream);
 cudaError_t launch_pages_extend(const PageBooks& books, const int32_t* listed,

@@ -675,6 +675,23 @@ __global__ void __launch_bounds__(kCopyThreads)
         copy_piece(pool, u, [&](int64_t i) { return from[i]; }, [&](int64_t i) { return to[i]; });
 }
 
+// The listed rows' page numbers and lengths; those of a row out of range are none and 0.
+constexpr int kRowPiece = 4 * kCopyThreads;
+__global__ void __launch_bounds__(kCopyThreads)
+    rows_kernel(Books b, const int32_t* listed, int64_t count) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int64_t pieces = (b.width + kRowPiece - 1) / kRowPiece;
+    for (int64_t u = blockIdx.x; u < count * pieces; u += gridDim.x) {
+        const int64_t i = u / pieces, first = u % pieces * kRowPiece, r = listed[i];
+        const bool there = r >= 0 && r < b.rows;
+        for (int64_t j = first + threadIdx.x; j < min(first + kRowPiece, b.width); j += kCopyThreads)
+            b.tables_out[i * b.width + j] = there ? b.tables_in[r * b.in_stride + j] : -1;
+        if (first == 0 && threadIdx.x == 0 && b.lengths_out)
+            b.lengths_out[i] = there ? b.lengths_in[r] : 0;
+    }
+}
+
 // The cluster of a books kernel: one CTA for up to a sweep of pages and as many
 // page numbers in rows to read or copy, else eight.
 template <typename... P, typename... A>
@@ -758,6 +775,14 @@ int64_t pages_compact_workspace(const w4a16_books_shape& b, const w4a16_pool_sha
 
 int64_t pages_workspace(const w4a16_books_shape& b, int64_t count) {
     return 4 * (4 + b.rows + 4 * count + 3 * b.pages);
+}
+
+cudaError_t launch_pages_rows(const PageBooks& b, const int32_t* listed, int64_t count,
+                              cudaStream_t stream) {
+    if (count == 0) return cudaSuccess;
+    const int64_t units = count * ((b.shape.width + kRowPiece - 1) / kRowPiece);
+    return launch_apply(rows_kernel, (unsigned)std::min<int64_t>(units, 1 << 20), stream, books_of(b),
+                        listed, count);
 }
 
 cudaError_t launch_pages_free(const PageBooks& b, const int32_t* listed, int64_t count,

@@ -383,12 +383,27 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0, str
     return logprobs, entropies, ids, likeliest
 
 
-def _pick(t: torch.Tensor, rows: torch.Tensor, stream) -> torch.Tensor:
-    """The listed rows of t, taken on the stream the call runs on."""
-    if stream is None:
-        return t.index_select(0, rows)
-    with torch.cuda.stream(stream):
-        return t.index_select(0, rows)
+def _listed(tables: torch.Tensor, lengths: torch.Tensor | None, rows: torch.Tensor, stream):
+    """The listed rows' tables and lengths (None for None), taken on the stream the call runs on;
+    a row out of range has no pages and length 0."""
+    (n, width), count, dev = tables.shape, rows.shape[0], tables.get_device()
+    if rows.dtype is torch.int64:
+        with torch.cuda.stream(stream):
+            rows = rows.clamp(-1, n).int()
+    _row(rows, count, "rows")
+    _ints(tables, "tables", (n, width))
+    if lengths is not None:
+        _row(lengths, n, "lengths")
+    if (dev < 0 or rows.get_device() != dev or lengths is not None and lengths.get_device() != dev
+            or stream is not None and stream.device.index != dev):
+        _device(stream, tables=tables, lengths=lengths, rows=rows)
+    new_tables = _empty(tables, (count, width), torch.int32, stream)
+    new_lengths = None if lengths is None else _empty(tables, count, torch.int32, stream)
+    _run(dev, stream, "w4a16_pages_rows", tables.data_ptr(),
+         None if lengths is None else lengths.data_ptr(), rows.data_ptr(), count,
+         new_tables.data_ptr(), None if lengths is None else new_lengths.data_ptr(),
+         _BOOKS_SHAPE(1, n, width, tables.stride(0), width, 1))
+    return new_tables, new_lengths
 
 
 class PagedCache:
@@ -399,7 +414,8 @@ class PagedCache:
     in plane 2l and its values in plane 2l + 1; one page number means the same
     page of every plane.  refs, tables and lengths are the books the pages_*
     functions keep, updated in place, so the methods may be captured in a CUDA
-    graph."""
+    graph.  A listed row that is out of range is passed over by every method: its
+    tokens go nowhere, its attention is that of a row of length 0."""
 
     def __init__(self, layers: int, rows: int, pages: int, kv_heads: int, head_dim: int,
                  page_size: int = 16, max_length: int | None = None,
@@ -432,7 +448,7 @@ class PagedCache:
                offsets: torch.Tensor | None = None, rows: torch.Tensor | None = None,
                stream=None) -> None:
         """New tokens of every row (or of the listed ones) of one layer (paged_append)."""
-        tables = self.tables if rows is None else _pick(self.tables, rows, stream)
+        tables = self.tables if rows is None else _listed(self.tables, None, rows, stream)[0]
         paged_append(k, v, self.keys(layer), self.values(layer), tables, starts, offsets,
                      stream=stream)
 
@@ -441,7 +457,7 @@ class PagedCache:
         """Attention of one new token of every row (or of the listed ones) (paged_attention)."""
         tables, lengths = self.tables, self.lengths
         if rows is not None:
-            tables, lengths = _pick(tables, rows, stream), _pick(lengths, rows, stream)
+            tables, lengths = _listed(tables, lengths, rows, stream)
         return paged_attention(q, self.keys(layer), self.values(layer), tables, lengths,
                                scale=scale, out=out, stream=stream)
 
