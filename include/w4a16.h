@@ -445,9 +445,10 @@ typedef struct w4a16_query_shape {
  * or +infinity gets NaN, in out and in lse.  A value of +-infinity gives the
  * infinity in its dimension of out, NaN beside a NaN or the opposite one, and
  * also where its weight is below 2^-36 (fp16) or 2^-126 (bf16) of the head's
- * largest, which may count as 0.  The result does not depend on how the work
- * was split beyond the order of its FP32 sums; two calls on the same inputs
- * give the same bits.
+ * largest, which may count as 0.  How the work is split, which goes by the
+ * sizes and the device, changes the order of the FP32 sums and the maximum that
+ * the weights are held against: they keep 22 bits in fp16 and 16 in bf16.  Two
+ * calls on the same inputs and sizes give the same bits.
  * Errors: NULL -> W4A16_ERR_NULL; sizes outside the ranges above ->
  * W4A16_ERR_SHAPE; q, out, a pool or the workspace not 16-byte aligned ->
  * W4A16_ERR_ALIGN.
@@ -465,8 +466,8 @@ int64_t w4a16_paged_attention_workspace(const w4a16_cache_shape *cache, int64_t 
  * The books of a cache's pages: how many rows hold each page (`refs`, <= 0 is
  * free), each row's page numbers (`tables`, -1 past its pages) and each row's
  * positions (`lengths`).  Row r of length n holds ceil(n / page_size) pages.
- *   pages 1 .. 2^31 - 1; rows 1 .. 2^24; width 1 .. 2^24, rows * width <
- *   2^40; strides in elements.  Every call reads the `in` books and writes
+ *   pages 1 .. 2^31 - 1; rows 1 .. 2^24; width 1 .. 2^24, rows * width at
+ *   most 2^40, width * page_size < 2^31; strides in elements.  Every call reads the `in` books and writes
  *   the `out` ones whole; each `out` tensor is its `in` tensor (with the same
  *   stride) or overlaps none.
  */

@@ -68,7 +68,8 @@ bool good_cache(const w4a16_cache_shape& c) {
            c.kv_heads >= 1 && c.kv_heads <= 1024 && c.head_dim >= 8 && c.head_dim <= 256 &&
            c.head_dim % 8 == 0 && (c.type == W4A16_F16 || c.type == W4A16_BF16) &&
            good_stride(c.pages, c.page_stride) && good_stride(c.page_size, c.slot_stride) &&
-           good_stride(c.kv_heads, c.head_stride) && c.batch >= 1 && c.batch <= 65535 && c.table_width >= 1 && c.table_width <= (int64_t)1 << 24 &&
+           good_stride(c.kv_heads, c.head_stride) && c.batch >= 1 && c.batch <= 65535 &&
+           c.table_width >= 1 && c.table_width <= (int64_t)1 << 24 &&
            c.table_width * c.page_size < (int64_t)1 << 31 &&
            (c.batch == 1 || (c.table_stride >= 0 && c.table_stride <= (int64_t)1 << 40));
 }

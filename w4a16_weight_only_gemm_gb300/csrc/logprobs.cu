@@ -23,7 +23,8 @@
 // launch.  Bound by HBM for many rows, short of it by what a block does after
 // its pass: on one GB300 (6790 GB/s copied) 2047 rows of 128256 take 88 us in
 // fp16 (5985 GB/s), 1023 in fp32 80 us (6560 GB/s).  One row takes 8.2 us, all
-// of it latency: a launch, a pass, seven barriers.
+// of it latency: a launch, a pass, six barriers of a block with alternatives
+// (two without), two of the cluster and three in its first block.
 #include <cuda_bf16.h>
 
 #include <stddef.h>

@@ -157,11 +157,12 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
 // turn it into NaN.
 //
 // On one GB300 (6790 GB/s copied), 8 key-value heads of 128 and 4 query heads
-// to each: one row of 131071 positions 85.7 us (6260 GB/s), 128 rows of up to
-// 8191 314 us (6780 GB/s), one row of 512 4.8 us.  16 rows of up to 4093 with 4
+// to each: one row of 131071 positions 86.1 us (6240 GB/s), 128 rows of up to
+// 8191 318 us (6700 GB/s), one row of 512 4.8 us.  16 rows of up to 4093 with 4
 // key-value heads 17.7 us (4030 GB/s): a launch and three reads that depend on
 // one another (length, page, keys) before the first tile, the longest rows'
-// blocks after the others are done, and the join, about 7 us in all.
+// blocks after the others are done, and the join, about 7 us in all.  32 rows of
+// 4096 take 90 us by pages of 16 to 128, 91 by pages of 8, 13 and 24, 89 by 1.
 // ---------------------------------------------------------------------------
 constexpr int kAttendWarps = 4;
 constexpr int kAttendThreads = 32 * kAttendWarps;
@@ -309,7 +310,8 @@ struct AttendShape {
     static constexpr int kTileBytes = 2 * kHalf;        // and values
     static constexpr int kStageBytes = kTileBytes * kAttendWarps;
     // 192 KB of ring an SM: as many blocks as registers allow
-    static constexpr int kBlocksPerSm = DP == 64 ? (NT == 1 ? 4 : 3) : DP == 128 ? (NT == 1 ? 3 : 2) : 1;
+    static constexpr int kBlocksPerSm =
+        DP == 64 ? (NT == 1 ? 4 : 3) : DP == 128 ? (NT == 1 ? 3 : 2) : 1;
     static constexpr int kStages = 192 * 1024 / kBlocksPerSm / kStageBytes;
     // behind the ring, the queries of as many items
     static constexpr int kQueryBytes = 8 * NT * kRowBytes;
@@ -833,8 +835,8 @@ __global__ void __launch_bounds__(kFewThreads) join_few_kernel(AttendArgs a, int
 }
 
 // The same where an item has many parts: block (x, y) has head y of joint x.  A
-// row split over the whole GPU has some sixty parts a head: a thread group's first eight are read before the weights are
-// settled, and no part waits for another.  (One part at a time with running
+// row split over the whole GPU has some sixty parts a head: a thread group's first
+// eight are read before the weights are settled, and no part waits for another.  (One part at a time with running
 // maxima in between took 13 us of a 131071-position call.)
 constexpr int kJoinThreads = 256;
 constexpr int kMaxParts = 1024;  // blocks of attend_kernel: num_sms * kBlocksPerSm at most
@@ -983,9 +985,11 @@ const Room& room_of(int dim, int tiles, bool tile_page, int device) {
 // and a step each.  0, and the line is cut instead, where that leaves a block
 // too many steps, as a row may be that much longer than the others (such a step
 // takes 0.7 us): 32 where the blocks fill half the places or more, else 8.
-// Clusters / the line, 8 key-value heads: 56 rows of 2048 72 / 81 us, of 1 to
-// 2048 43 / 48, 14 rows of 1 to 4096 26.8 / 27.7, 8 rows of 1 to 4096 17.7 / 19.4,
-// of 512 7.0 / 9.3, one row of 512 4.8 / 7.1, one of 8192 15.9 / 10.2.
+// Clusters / the line, 8 key-value heads: 56 rows of 2048 73 / 81 us, from short
+// ones to 2048 44 / 48, 14 rows to 4096 27.7 / 27.9, 8 rows to 4096 17.7 / 19.3,
+// of 512 7.0 / 9.2, one row of 512 4.8 / 6.8, one of 8192 15.9 / 10.9.
+// What counts is the room of the tables: the lengths are on the device.  So one row
+// of 512 takes the line where its table has room for more than 4096 positions.
 int item_cluster(const w4a16_cache_shape& c, int64_t group, const DeviceCtx& ctx, cudaError_t* error) {
     const HeadPlan heads = plan_heads(group);
     const int64_t items = c.batch * c.kv_heads * heads.blocks;
@@ -1046,8 +1050,9 @@ cudaError_t attend(AttendArgs a, cudaStream_t stream, const DeviceCtx& ctx) {
     cfg.numAttrs = 1;
     cfg.dynamicSmemBytes = 0;
     const int64_t items = (int64_t)a.c.batch * a.items;
-    // Few joints, so several parts an item: 64 items of 7 heads 19.2 us, 20.0 by the other form.
-    // Many joints, mostly of two parts: 512 items of 4 heads 50.8 us, 53.3 by this form.
+    // Few joints, so several parts an item: 64 items of 7 heads (16 rows to 4093, 4 key-value
+    // heads, wide tables) 19.2 us, 20.0 by the other form.  Many joints, mostly of two parts: 512
+    // items of 4 heads (64 rows of 1024, 8 key-value heads) 51 us, 53.3 by this form.
     if (items * a.block_heads <= blocks) {
         cfg.gridDim = dim3((unsigned)items, (unsigned)a.block_heads);
         cfg.blockDim = dim3(kJoinThreads);
