@@ -355,8 +355,9 @@ int w4a16_gemm_ex_plan(int64_t M, int64_t N, int64_t K, int32_t group, int32_t z
 
 /* ------------------------------------------------------------------------
  * Serving operators: the paged key-value cache between the quantized linear
- * layers, the attention of a new token over it, the care of its pages, and
- * the scores of sampled tokens.
+ * layers, rotary positions, the attention of a new token or of chunks of them
+ * over the cache, the care of its pages, the adjustment of logits and the
+ * scores of sampled tokens.
  *
  * The conventions above hold, with these differences.  Tensors may be
  * strided where a stride is an argument (in elements, or in bytes where the
@@ -461,6 +462,106 @@ int w4a16_paged_attention(const void *q, const void *k_pool, const void *v_pool,
 /* Bytes of workspace of w4a16_paged_attention on the current device, 0 for
  * tables of few positions that need none (-1 on a bad shape or device). */
 int64_t w4a16_paged_attention_workspace(const w4a16_cache_shape *cache, int64_t q_heads);
+
+/*
+ * A rotation: the first `dims` of a head's dimensions are turned in pairs,
+ * (2 i, 2 i + 1) where interleaved = 1, (i, i + dims / 2) where it is 0; the
+ * others stay as they are.  At position p the pair (a, b) becomes
+ *   magnitude * (a cos(p w[i]) - b sin(p w[i])),  magnitude * (a sin(p w[i]) + b cos(p w[i])).
+ * The rates come as `turns` [dims / 2] uint64: w[i] / (2 pi) * 2^64, modulo
+ * 2^64.  The angle is reduced exactly, so far positions lose nothing; sums are
+ * FP32, rounded once.
+ *   dims 2 .. head_dim, even.
+ */
+typedef struct w4a16_rotary_shape {
+    int64_t dims, interleaved;
+    double magnitude;
+} w4a16_rotary_shape;
+
+/* Heads [tokens, heads, head_dim] that are read and heads of the same sizes
+ * that are written: tokens 0 .. 2^31, heads 1 .. 1024, head_dim 8 .. 256, a
+ * multiple of 8; strides in elements, multiples of 8. */
+typedef struct w4a16_heads_shape {
+    int64_t tokens, heads, head_dim, type;
+    int64_t token_stride, head_stride, out_token_stride, out_head_stride;
+} w4a16_heads_shape;
+
+/*
+ * w4a16_rotate -- rotary positions: out[t] is x[t] rotated to positions[t].
+ *   x, out     heads of `type` (W4A16_F16, _BF16, _F32), 16-byte aligned; out
+ *              is x (with the same strides) or overlaps none of it.
+ *   positions  [tokens] int32, of either sign: a rotation to -p undoes one to
+ *              p, and is its gradient.
+ * Errors: NULL -> W4A16_ERR_NULL; sizes outside the ranges above, a magnitude
+ * that is not finite -> W4A16_ERR_SHAPE; x or out not 16-byte aligned ->
+ * W4A16_ERR_ALIGN.
+ */
+int w4a16_rotate(const void *x, const int32_t *positions, const uint64_t *turns, void *out,
+                 const w4a16_rotary_shape *rotary, const w4a16_heads_shape *heads, void *stream);
+
+/*
+ * w4a16_paged_append_rotary -- w4a16_paged_append with the keys rotated to
+ * their positions in the cache, and queries of the same tokens rotated to
+ * theirs.
+ *   q, out     [tokens, heads, head_dim] of the cache's type, described by
+ *              `queries` (whose head_dim and type are the cache's); out is q
+ *              (with the same strides) or overlaps none of it.  Both NULL: keys
+ *              and values only (of `queries`, tokens alone is looked at).
+ * A token whose position has no page has its queries rotated all the same; the
+ * queries of one that no row claims become zeros.
+ * Errors: as w4a16_paged_append and w4a16_rotate.
+ */
+int w4a16_paged_append_rotary(const void *k, const void *v, const uint64_t *turns, void *k_pool,
+                              void *v_pool, const int32_t *tables, const int32_t *starts,
+                              const int32_t *offsets, const void *q, void *out,
+                              const w4a16_cache_shape *cache, const w4a16_rotary_shape *rotary,
+                              const w4a16_heads_shape *queries, int64_t k_token_stride,
+                              int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                              void *stream);
+
+/*
+ * w4a16_paged_chunk_attention -- attention of each row's last tokens over a
+ * paged cache: row b's tokens offsets[b] <= t < offsets[b + 1] are its last
+ * positions, token t at position lengths[b] - offsets[b + 1] + t, and each sees
+ * the positions up to its own:
+ *   out[t, h] = sum_p w[p] V[b, p, h / g],  w = softmax_p(scale * q[t, h] . K[b, p, h / g])
+ * over p <= that position, g = q_heads / kv_heads.  Scores, statistics and sums
+ * are held in FP32; weights enter the products with V in the cache's type.
+ *
+ *   q          [tokens, q_heads, head_dim] of the cache's type; the strides of
+ *              `query` for rows are those of tokens here.
+ *   lengths    [batch] int32, the new tokens among them, clamped as
+ *              w4a16_paged_attention does.
+ *   offsets    [batch + 1] int32, not descending, within 0 .. tokens.  A row
+ *              may have no tokens.
+ *   out        [tokens, q_heads, head_dim], written.  A token with a position
+ *              below 0 (a row with more tokens than positions) and one that no
+ *              row claims get zeros.
+ *   lse        NULL, or [tokens, q_heads] float, written: the natural logarithm
+ *              of sum_p exp(scale * q . K), -infinity for tokens as above.
+ *   workspace  w4a16_paged_chunk_workspace(cache, q_heads, tokens) bytes,
+ *              16-byte aligned, of any content; not to be shared by calls that
+ *              may run at once.
+ *   tokens     0 .. 2^24, tokens * q_heads at most 2^31; q_heads as for
+ *              w4a16_paged_attention.
+ * Positions without a valid page are left out, as if masked, and so are those
+ * whose score is -infinity; a head that has no other position gets zeros and
+ * -infinity.  A score that is NaN or +infinity gives NaN.  A value that is not
+ * finite makes its dimension of out not finite (an infinity may come out as
+ * NaN) for the tokens that see it, and for no other.  Two calls on the same
+ * inputs and sizes give the same bits.
+ * Errors: as w4a16_paged_attention.
+ */
+int w4a16_paged_chunk_attention(const void *q, const void *k_pool, const void *v_pool,
+                                const int32_t *tables, const int32_t *lengths,
+                                const int32_t *offsets, void *out, float *lse, void *workspace,
+                                const w4a16_cache_shape *cache, const w4a16_query_shape *query,
+                                int64_t tokens, void *stream);
+
+/* Bytes of workspace of w4a16_paged_chunk_attention on the current device (-1
+ * on a bad shape or device). */
+int64_t w4a16_paged_chunk_workspace(const w4a16_cache_shape *cache, int64_t q_heads,
+                                    int64_t tokens);
 
 /*
  * The books of a cache's pages: how many rows hold each page (`refs`, <= 0 is
@@ -593,6 +694,56 @@ int w4a16_token_logprobs(const void *logits, const void *tokens, float *logprob,
                          int32_t *top_ids, float *top_logprobs, int64_t rows, int64_t vocabulary,
                          int64_t row_stride, int32_t type, int32_t wide, int32_t top,
                          void *stream);
+
+/* Most biases a row of w4a16_adjust_logits. */
+#define W4A16_MAX_BIASES 1024
+
+/* The tensors of w4a16_adjust_logits; all but logits and out may be NULL. */
+typedef struct w4a16_adjust_tensors {
+    const void *logits, *tokens;
+    const int32_t *lengths, *prompts;
+    const float *repetition, *presence, *frequency;
+    const int32_t *bias_ids;
+    const float *biases;
+    const uint32_t *mask;
+    void *out;
+} w4a16_adjust_tensors;
+
+/* Its sizes: rows 1 .. 2^24, vocabulary 1 .. 2^30, type W4A16_F16, _BF16 or
+ * _F32; strides in elements of rows; wide = 1 where tokens are int64; width of
+ * the rows of tokens; biases of a row (0 .. 1024); and the penalties of every
+ * row where the tensor of that name is NULL. */
+typedef struct w4a16_adjust_shape {
+    int64_t rows, vocabulary, type, logits_stride, out_stride;
+    int64_t wide, width, token_stride, biases, bias_stride, mask_stride;
+    double repetition, presence, frequency;
+} w4a16_adjust_shape;
+
+/*
+ * w4a16_adjust_logits -- penalties, biases and masks on logits, in this order.
+ * Of row r the first lengths[r] of tokens[r] (all of them where lengths is NULL;
+ * clamped to 0 .. width) have been said, the first prompts[r] of those (none
+ * where prompts is NULL) by the prompt.  With c[j] the times that token j is
+ * among the others:
+ *   x[j] / repetition where x[j] > 0, else x[j] * repetition, if j was said at all;
+ *   - frequency * c[j], and - presence where c[j] > 0;
+ *   + every biases[r, i] with bias_ids[r, i] = j, in the order of the list;
+ *   -infinity where bit j % 32 of mask[r, j / 32] is 0.
+ * In FP32, rounded once; a logit that nothing applies to keeps its bits.
+ *
+ *   logits, out    [rows, vocabulary] of `type`, aligned to their element; out
+ *                  is logits (with the same stride) or overlaps none of it.
+ *   tokens         [rows, width] int32 or int64; one outside [0, vocabulary) is
+ *                  passed over, as is such a bias_ids entry ([rows, biases] int32,
+ *                  with biases [rows, biases] float, in rows of the same stride).
+ *   repetition, presence, frequency  [rows] float, or NULL.
+ *   mask           [rows, (vocabulary + 31) / 32] int32.
+ * Errors: logits or out NULL, or bias_ids without biases -> W4A16_ERR_NULL; sizes
+ * outside the ranges above -> W4A16_ERR_SHAPE; logits or out not aligned to
+ * their element -> W4A16_ERR_ALIGN.
+ */
+int w4a16_adjust_logits(const w4a16_adjust_tensors *tensors, const w4a16_adjust_shape *shape,
+                        void *stream);
 
 /*
  * w4a16_device_status -- synchronises the current device, returns in

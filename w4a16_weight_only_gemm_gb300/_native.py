@@ -45,6 +45,10 @@ SIGNATURES = {
     "w4a16_paged_append": (ctypes.c_int, [_P] * 7 + [_S] + [_I64] * 5 + [_P]),
     "w4a16_paged_attention": (ctypes.c_int, [_P] * 8 + [_S] * 2 + [_P]),
     "w4a16_paged_attention_workspace": (_I64, [_S, _I64]),
+    "w4a16_rotate": (ctypes.c_int, [_P] * 4 + [_S] * 2 + [_P]),
+    "w4a16_paged_append_rotary": (ctypes.c_int, [_P] * 10 + [_S] * 3 + [_I64] * 4 + [_P]),
+    "w4a16_paged_chunk_workspace": (_I64, [_S, _I64, _I64]),
+    "w4a16_paged_chunk_attention": (ctypes.c_int, [_P] * 9 + [_S] * 2 + [_I64, _P]),
     "w4a16_pages_workspace": (_I64, [_S, _I64]),
     "w4a16_pages_fork_workspace": (_I64, [_S, _S, _I64, _I32]),
     "w4a16_pages_compact_workspace": (_I64, [_S, _S, _I32]),
@@ -55,6 +59,7 @@ SIGNATURES = {
     "w4a16_pages_compact": (ctypes.c_int, [_P] * 7 + [_S, _S, _P]),
     "w4a16_pages_copy": (ctypes.c_int, [_P] * 3 + [_I64] * 2 + [_S, _P]),
     "w4a16_token_logprobs": (ctypes.c_int, [_P] * 6 + [_I64] * 3 + [_I32] * 3 + [_P]),
+    "w4a16_adjust_logits": (ctypes.c_int, [_S] * 2 + [_P]),
     "w4a16_device_status": (ctypes.c_int, [ctypes.POINTER(ctypes.c_int)]),
     "w4a16_set_wait_timeout_ns": (None, [_U64]),
     "w4a16_selftest_wait_timeout": (ctypes.c_int, [_U64, _P]),

@@ -80,6 +80,30 @@ bool good_steps(const w4a16_cache_shape& c, int64_t q_heads) {
     return c.batch * c.table_width * c.page_size <= ((int64_t)1 << 43) / q_heads;
 }
 
+bool good_heads(const w4a16_heads_shape& h) {
+    return h.heads >= 1 && h.heads <= 1024 && h.head_dim >= 8 && h.head_dim <= 256 &&
+           h.head_dim % 8 == 0 && good_stride(h.tokens, h.token_stride) &&
+           good_stride(h.heads, h.head_stride) && good_stride(h.tokens, h.out_token_stride) &&
+           good_stride(h.heads, h.out_head_stride);
+}
+
+bool good_rotary(const w4a16_rotary_shape& r, int64_t head_dim) {
+    return r.dims >= 2 && r.dims <= head_dim && r.dims % 2 == 0 &&
+           (r.interleaved == 0 || r.interleaved == 1) && r.magnitude - r.magnitude == 0;
+}
+
+// An output that is the input has its strides.
+bool good_in_place(const void* in, const void* out, const w4a16_heads_shape& h) {
+    return in != out || ((h.tokens == 1 || h.token_stride == h.out_token_stride) &&
+                         (h.heads == 1 || h.head_stride == h.out_head_stride));
+}
+
+bool good_chunk(const w4a16_cache_shape& c, int64_t q_heads, int64_t tokens) {
+    return good_cache(c) && q_heads >= 1 && q_heads <= 1024 && q_heads % c.kv_heads == 0 &&
+           good_steps(c, q_heads) && tokens >= 0 && tokens <= (int64_t)1 << 24 &&
+           tokens * q_heads <= (int64_t)1 << 31;
+}
+
 bool good_books(const w4a16_books_shape& b) {
     return b.pages >= 1 && b.pages < (int64_t)1 << 31 && b.rows >= 1 && b.rows <= (int64_t)1 << 24 &&
            b.width >= 1 && b.width <= (int64_t)1 << 24 && b.rows * b.width <= (int64_t)1 << 40 &&
@@ -421,6 +445,88 @@ int w4a16_paged_attention(const void* q, const void* k_pool, const void* v_pool,
                                             ctx));
 }
 
+int w4a16_rotate(const void* x, const int32_t* positions, const uint64_t* turns, void* out,
+                 const w4a16_rotary_shape* rotary, const w4a16_heads_shape* heads, void* stream) {
+    if (!rotary || !heads) return W4A16_ERR_NULL;
+    if (heads->tokens < 0 || heads->tokens > (int64_t)1 << 31 || heads->type < W4A16_F16 ||
+        heads->type > W4A16_F32 || !good_heads(*heads) || !good_rotary(*rotary, heads->head_dim) ||
+        !good_in_place(x, out, *heads))
+        return W4A16_ERR_SHAPE;
+    if (heads->tokens == 0) return W4A16_OK;
+    if (!x || !positions || !turns || !out) return W4A16_ERR_NULL;
+    if (!aligned16(x) || !aligned16(out)) return W4A16_ERR_ALIGN;
+    DeviceCtx ctx;
+    if (int rc = device_ctx(&ctx)) return rc;
+    return from_cuda(launch_rotate(x, positions, turns, out, *rotary, *heads,
+                                   static_cast<cudaStream_t>(stream), ctx));
+}
+
+int w4a16_paged_append_rotary(const void* k, const void* v, const uint64_t* turns, void* k_pool,
+                              void* v_pool, const int32_t* tables, const int32_t* starts,
+                              const int32_t* offsets, const void* q, void* out,
+                              const w4a16_cache_shape* cache, const w4a16_rotary_shape* rotary,
+                              const w4a16_heads_shape* queries, int64_t k_token_stride,
+                              int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                              void* stream) {
+    if (!cache || !rotary || !queries) return W4A16_ERR_NULL;
+    const int64_t tokens = queries->tokens;
+    if (!good_cache(*cache) || tokens < 0 || tokens > (int64_t)1 << 31 ||
+        (!offsets && tokens != cache->batch) || !good_rotary(*rotary, cache->head_dim))
+        return W4A16_ERR_SHAPE;
+    if (q && (!good_heads(*queries) || queries->head_dim != cache->head_dim ||
+              queries->type != cache->type || !good_in_place(q, out, *queries)))
+        return W4A16_ERR_SHAPE;
+    if (tokens == 0) return W4A16_OK;
+    if (!good_stride(tokens, k_token_stride) || !good_stride(cache->kv_heads, k_head_stride) ||
+        !good_stride(tokens, v_token_stride) || !good_stride(cache->kv_heads, v_head_stride))
+        return W4A16_ERR_SHAPE;
+    if (!k || !v || !turns || !k_pool || !v_pool || !tables || !starts || !q != !out)
+        return W4A16_ERR_NULL;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_pool) || !aligned16(v_pool) ||
+        !aligned16(q) || !aligned16(out))
+        return W4A16_ERR_ALIGN;
+    DeviceCtx ctx;
+    if (int rc = device_ctx(&ctx)) return rc;
+    return from_cuda(launch_paged_append_rotary(
+        k, v, turns, k_pool, v_pool, tables, starts, offsets, q, out, *cache, *rotary, *queries,
+        k_token_stride, k_head_stride, v_token_stride, v_head_stride,
+        static_cast<cudaStream_t>(stream), ctx));
+}
+
+int64_t w4a16_paged_chunk_workspace(const w4a16_cache_shape* cache, int64_t q_heads,
+                                    int64_t tokens) {
+    if (!cache || !good_chunk(*cache, q_heads, tokens)) return -1;
+    DeviceCtx ctx;
+    if (device_ctx(&ctx)) return -1;
+    return paged_chunk_workspace(*cache, q_heads, tokens, ctx);
+}
+
+int w4a16_paged_chunk_attention(const void* q, const void* k_pool, const void* v_pool,
+                                const int32_t* tables, const int32_t* lengths,
+                                const int32_t* offsets, void* out, float* lse, void* workspace,
+                                const w4a16_cache_shape* cache, const w4a16_query_shape* query,
+                                int64_t tokens, void* stream) {
+    if (!cache || !query) return W4A16_ERR_NULL;
+    if (!good_chunk(*cache, query->q_heads, tokens) || !(query->scale == query->scale))
+        return W4A16_ERR_SHAPE;
+    if (tokens == 0) return W4A16_OK;
+    if (!q || !k_pool || !v_pool || !tables || !lengths || !offsets || !out || !workspace)
+        return W4A16_ERR_NULL;
+    if (!good_stride(tokens, query->q_row_stride) ||
+        !good_stride(query->q_heads, query->q_head_stride) ||
+        !good_stride(tokens, query->out_row_stride) ||
+        !good_stride(query->q_heads, query->out_head_stride))
+        return W4A16_ERR_SHAPE;
+    if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out) ||
+        !aligned16(workspace))
+        return W4A16_ERR_ALIGN;
+    DeviceCtx ctx;
+    if (int rc = device_ctx(&ctx)) return rc;
+    return from_cuda(launch_paged_chunk_attention(q, k_pool, v_pool, tables, lengths, offsets, out,
+                                                  lse, workspace, *cache, *query, tokens,
+                                                  static_cast<cudaStream_t>(stream), ctx));
+}
+
 int64_t w4a16_pages_workspace(const w4a16_books_shape* books, int64_t count) {
     return books && good_books(*books) && good_count(count) ? pages_workspace(*books, count) : -1;
 }
@@ -545,6 +651,29 @@ int w4a16_token_logprobs(const void* logits, const void* tokens, float* logprob,
     return from_cuda(launch_token_logprobs(logits, tokens, logprob, entropy, top_ids, top_logprobs,
                                            rows, vocabulary, row_stride, type, wide, top,
                                            static_cast<cudaStream_t>(stream), ctx));
+}
+
+int w4a16_adjust_logits(const w4a16_adjust_tensors* tensors, const w4a16_adjust_shape* shape,
+                        void* stream) {
+    if (!tensors || !shape || !tensors->logits || !tensors->out ||
+        (tensors->bias_ids && shape->biases && !tensors->biases))
+        return W4A16_ERR_NULL;
+    const w4a16_adjust_shape& s = *shape;
+    const auto stride = [&](int64_t n) { return s.rows == 1 || (n >= 0 && n <= (int64_t)1 << 40); };
+    if (s.rows < 1 || s.rows > (int64_t)1 << 24 || s.vocabulary < 1 ||
+        s.vocabulary > (int64_t)1 << 30 || s.type < W4A16_F16 || s.type > W4A16_F32 ||
+        !stride(s.logits_stride) || !stride(s.out_stride) || !stride(s.token_stride) ||
+        !stride(s.bias_stride) || !stride(s.mask_stride) || (s.wide != 0 && s.wide != 1) ||
+        s.width < 0 || s.width >= (int64_t)1 << 31 || s.biases < 0 || s.biases > W4A16_MAX_BIASES ||
+        (tensors->logits == tensors->out && s.rows > 1 && s.logits_stride != s.out_stride))
+        return W4A16_ERR_SHAPE;
+    const uintptr_t size = s.type == W4A16_F32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(tensors->logits) % size ||
+        reinterpret_cast<uintptr_t>(tensors->out) % size)
+        return W4A16_ERR_ALIGN;
+    DeviceCtx ctx;
+    if (int rc = device_ctx(&ctx)) return rc;
+    return from_cuda(launch_adjust_logits(*tensors, s, static_cast<cudaStream_t>(stream), ctx));
 }
 
 int w4a16_device_status(int* status) {

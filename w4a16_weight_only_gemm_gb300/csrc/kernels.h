@@ -100,6 +100,25 @@ cudaError_t launch_paged_attention(const void* q, const void* k_pool, const void
                                    float* lse, void* workspace, const w4a16_cache_shape& cache,
                                    const w4a16_query_shape& query, cudaStream_t stream,
                                    const DeviceCtx& ctx);
+cudaError_t launch_rotate(const void* x, const int32_t* positions, const uint64_t* turns, void* out,
+                          const w4a16_rotary_shape& rotary, const w4a16_heads_shape& heads,
+                          cudaStream_t stream, const DeviceCtx& ctx);
+cudaError_t launch_paged_append_rotary(const void* k, const void* v, const uint64_t* turns,
+                                       void* k_pool, void* v_pool, const int32_t* tables,
+                                       const int32_t* starts, const int32_t* offsets, const void* q,
+                                       void* out, const w4a16_cache_shape& cache,
+                                       const w4a16_rotary_shape& rotary,
+                                       const w4a16_heads_shape& queries, int64_t k_token,
+                                       int64_t k_head, int64_t v_token, int64_t v_head,
+                                       cudaStream_t stream, const DeviceCtx& ctx);
+int64_t paged_chunk_workspace(const w4a16_cache_shape& cache, int64_t q_heads, int64_t tokens,
+                              const DeviceCtx& ctx);
+cudaError_t launch_paged_chunk_attention(const void* q, const void* k_pool, const void* v_pool,
+                                         const int32_t* tables, const int32_t* lengths,
+                                         const int32_t* offsets, void* out, float* lse,
+                                         void* workspace, const w4a16_cache_shape& cache,
+                                         const w4a16_query_shape& query, int64_t tokens,
+                                         cudaStream_t stream, const DeviceCtx& ctx);
 // The books that a page call reads and writes.
 struct PageBooks {
     const int32_t *refs_in, *tables_in, *lengths_in;
@@ -132,6 +151,9 @@ cudaError_t launch_token_logprobs(const void* logits, const void* tokens, float*
                                   float* entropy, int32_t* top_ids, float* top_logprobs,
                                   int64_t rows, int64_t vocabulary, int64_t row_stride, int type,
                                   int wide, int top, cudaStream_t stream, const DeviceCtx& ctx);
+cudaError_t launch_adjust_logits(const w4a16_adjust_tensors& tensors,
+                                 const w4a16_adjust_shape& shape, cudaStream_t stream,
+                                 const DeviceCtx& ctx);
 cudaError_t launch_selftest_wait(uint64_t timeout_ns, cudaStream_t stream, const DeviceCtx& ctx);
 
 }  // namespace w4a16

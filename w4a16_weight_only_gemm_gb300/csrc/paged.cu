@@ -8,41 +8,10 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "paged.cuh"
 
 namespace w4a16 {
 namespace {
-
-// x / divisor for 0 <= x < 2^31: with l = ceil(log2 divisor) and
-// m = floor(2^(31 + l) / divisor) + 1, m * divisor exceeds 2^(31 + l) by at most
-// divisor <= 2^l, so x * m / 2^(31 + l) is off by less than 1 / divisor.
-struct Divisor {
-    int value;
-    uint32_t mul, shift;
-
-    explicit Divisor(int64_t divisor = 1) : value((int)divisor) {
-        uint32_t l = 0;
-        while (((int64_t)1 << l) < divisor) ++l;
-        shift = 31 + l;
-        mul = (uint32_t)(((uint64_t)1 << shift) / (uint64_t)divisor + 1);
-    }
-    __device__ __forceinline__ int quotient(int x) const {
-        return (int)(((uint64_t)(uint32_t)x * mul) >> shift);
-    }
-    __device__ __forceinline__ int remainder(int x) const { return x - quotient(x) * value; }
-};
-
-// A cache's geometry; strides in elements (2 bytes).
-struct Cache {
-    int64_t pages, page_stride, slot_stride, head_stride, table_stride;
-    int kv_heads, head_dim, batch, width;
-    Divisor page_size;
-};
-
-Cache cache_of(const w4a16_cache_shape& c) {
-    return {c.pages,         c.page_stride,    c.slot_stride,    c.head_stride,
-            c.table_stride,  (int)c.kv_heads,  (int)c.head_dim,  (int)c.batch,
-            (int)c.table_width, Divisor(c.page_size)};
-}
 
 // ---------------------------------------------------------------------------
 // Append
@@ -66,20 +35,6 @@ struct AppendArgs {
     Divisor token_pieces, head_pieces;  // 16-byte pieces of a token's keys, of a head
 };
 
-// The row with offsets[b] <= token < offsets[b + 1], -1 if none; by a whole warp.
-__device__ int row_of(const AppendArgs& a, int64_t token) {
-    if (!a.offsets) return (int)token;
-    const int lane = threadIdx.x % 32;
-    int lo = 0, step = a.c.batch;  // rows before lo end at or before the token
-    do {
-        step = (step + 31) / 32;
-        const int last = lo + (lane + 1) * step - 1;  // of the lane's part
-        const bool before = last < a.c.batch && a.offsets[last + 1] <= token;
-        lo += __popc(__ballot_sync(~0u, before)) * step;
-    } while (step > 1 && lo < a.c.batch);
-    return lo < a.c.batch && a.offsets[lo] <= token && token < a.offsets[lo + 1] ? lo : -1;
-}
-
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
     __shared__ int64_t place[kAppendTokens];  // where a token's heads start in the pools, -1: nowhere
     grid_dependency_wait();
@@ -88,7 +43,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
     const int tokens = (int)min((int64_t)a.block_tokens, a.tokens - first);
     for (int i = threadIdx.x / 32; i < tokens; i += kAppendThreads / 32) {
         const int64_t t = first + i;
-        const int b = row_of(a, t);
+        const int b = row_of(a.offsets, a.c.batch, t);
         int64_t at = -1;
         if (b >= 0) {
             const int64_t p = (int64_t)a.starts[b] + t - (a.offsets ? a.offsets[b] : t);

@@ -1,6 +1,7 @@
 """Serving operators for torch tensors: the paged key-value cache between the
-quantized linear layers, the attention of a new token over it, the care of its
-pages, and the scores of sampled tokens.
+quantized linear layers, rotary positions, the attention of new tokens over the
+cache, the care of its pages, the adjustment of logits and the scores of sampled
+tokens.
 
 As in ``ops``, each function checks shapes and dtypes, allocates outputs with
 torch, and calls the library on the current CUDA stream (or on ``stream``).
@@ -15,14 +16,19 @@ import torch
 
 from . import _native
 from .ops import _call, _device_of, _raw_stream, _stream_ptr
+from .rotary import Rotary
 
 MAX_TOP = 32
+MAX_BIASES = 1024
 
 _TYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 _CACHE_SHAPE = struct.Struct("11q").pack
 _QUERY_SHAPE = struct.Struct("5qd").pack
 _BOOKS_SHAPE = struct.Struct("6q").pack
 _POOL_SHAPE = struct.Struct("4q").pack
+_HEADS_SHAPE = struct.Struct("8q").pack
+_ADJUST_TENSORS = struct.Struct("11Q").pack
+_ADJUST_SHAPE = struct.Struct("11q3d").pack
 
 # A decode step makes these calls once a layer, and their kernels take a few
 # microseconds: each check below is one pass over plain attributes, and what
@@ -192,6 +198,150 @@ def paged_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
              _QUERY_SHAPE(q_heads, strides[0], strides[1], row, head,
                           dim ** -0.5 if scale is None else scale))
     return (out, lse) if return_lse else out
+
+
+def rotate(x: torch.Tensor, positions: torch.Tensor, rotary: Rotary,
+           out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Heads x [tokens, heads, head_dim] (fp16, bf16 or fp32, any strides) rotated to
+    their tokens' positions (int32 [tokens], of either sign); `out` may be x.
+    A rotation to -positions undoes it, and is its gradient."""
+    shape, dtype = x.shape, x.dtype
+    if len(shape) != 3 or dtype not in _TYPES or not 1 <= rotary.dim <= shape[2]:
+        raise ValueError("x must be a float16, bfloat16 or float32 tensor [tokens, heads, "
+                         f"head_dim >= {rotary.dim}], got {dtype} {list(shape)}")
+    row, head, _ = _heads(x, "x", dtype, shape)
+    tokens, heads, dim = shape
+    _row(positions, tokens, "positions")
+    dev = x.get_device()
+    if (dev < 0 or positions.get_device() != dev or rotary.turns.get_device() != dev
+            or out is not None and out.get_device() != dev
+            or stream is not None and stream.device.index != dev):
+        _device(stream, x=x, positions=positions, rotary=rotary.turns, out=out)
+    if out is None:
+        out = _empty(x, shape, dtype, stream)
+        to_row, to_head = heads * dim, dim
+    else:
+        to_row, to_head, _ = _heads(out, "out", dtype, shape)
+    if tokens and heads:
+        _run(dev, stream, "w4a16_rotate", x.data_ptr(), positions.data_ptr(),
+             rotary.turns.data_ptr(), out.data_ptr(), rotary._shape,
+             _HEADS_SHAPE(tokens, heads, dim, _TYPES[dtype], row, head, to_row, to_head))
+    return out
+
+
+def paged_append_rotary(k: torch.Tensor, v: torch.Tensor, k_pool: torch.Tensor,
+                        v_pool: torch.Tensor, tables: torch.Tensor, starts: torch.Tensor,
+                        rotary: Rotary, offsets: torch.Tensor | None = None,
+                        q: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                        stream=None):
+    """paged_append with the keys rotated to their positions in the cache, and with
+    queries of the same tokens, q [tokens, q_heads, head_dim], rotated to theirs: returns
+    those (a new tensor, or `out`, which may be q), or None without q.  The queries of a
+    token that no row claims become zeros."""
+    cache = _cache_shape(k_pool, v_pool, tables)
+    rows, tokens, dtype, dim = tables.shape[0], k.shape[0], k_pool.dtype, k_pool.shape[3]
+    if rotary.dim > dim:
+        raise ValueError(f"the rotation has {rotary.dim} dimensions, a head {dim}")
+    heads = (tokens, k_pool.shape[2], dim)
+    ks, vs = _heads(k, "k", dtype, heads), _heads(v, "v", dtype, heads)
+    _row(starts, rows, "starts")
+    if offsets is not None:
+        _row(offsets, rows + 1, "offsets")
+    elif tokens != rows:
+        raise ValueError(f"without offsets there must be one token a row, got {tokens} for {rows}")
+    if q is None and out is not None:
+        raise ValueError("out without q")
+    if q is not None:
+        shape = (tokens, q.shape[1] if q.dim() == 3 else "q_heads", dim)
+        qs = _heads(q, "q", dtype, shape)
+    dev = k.get_device()
+    named = {"v": v, "k_pool": k_pool, "v_pool": v_pool, "tables": tables, "starts": starts,
+             "rotary": rotary.turns, "offsets": offsets, "q": q, "out": out}
+    if (dev < 0 or any(t is not None and t.get_device() != dev for t in named.values())
+            or stream is not None and stream.device.index != dev):
+        _device(stream, k=k, **named)
+    queries = _HEADS_SHAPE(tokens, 0, dim, 0, 0, 0, 0, 0)
+    if q is not None:
+        if out is None:
+            out = _empty(q, shape, dtype, stream)
+            to = shape[1] * dim, dim
+        else:
+            to = _heads(out, "out", dtype, shape)
+        if shape[1]:
+            queries = _HEADS_SHAPE(tokens, shape[1], dim, _TYPES[dtype], qs[0], qs[1], to[0], to[1])
+        else:
+            q = None
+    if rows and tokens:
+        _run(dev, stream, "w4a16_paged_append_rotary", k.data_ptr(), v.data_ptr(),
+             rotary.turns.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), tables.data_ptr(),
+             starts.data_ptr(), None if offsets is None else offsets.data_ptr(),
+             None if q is None else q.data_ptr(), None if q is None else out.data_ptr(), cache,
+             rotary._shape, queries, ks[0], ks[1], vs[0], vs[1])
+    elif q is not None and tokens:
+        _zero(out, stream)
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _chunk_workspace(cache: bytes, q_heads: int, tokens: int, dev: int) -> int:
+    with torch.cuda.device(dev):
+        n = _native.lib().w4a16_paged_chunk_workspace(cache, q_heads, tokens)
+    if n < 0:
+        _native.check(2, "w4a16_paged_chunk_workspace")
+    return n
+
+
+def paged_chunk_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
+                          tables: torch.Tensor, lengths: torch.Tensor, offsets: torch.Tensor,
+                          scale: float | None = None, out: torch.Tensor | None = None,
+                          return_lse: bool = False, stream=None):
+    """Attention of each row's last tokens over its pages, whose keys and values the cache
+    holds already; see paged_append for the cache.  Row b's tokens offsets[b] ..
+    offsets[b+1] - 1 (int32 [rows + 1]) of q [tokens, q_heads, head_dim] are the last of
+    its lengths[b] positions (int32 [rows]), and each sees the positions up to its own.
+    q_heads is a multiple of kv_heads; scale defaults to head_dim ** -0.5.  Returns
+    [tokens, q_heads, head_dim], zeros for tokens of no row or of a position below 0, and
+    with return_lse also the logarithm of each head's sum of exponentials, fp32
+    [tokens, q_heads] (-inf for such tokens)."""
+    cache = _cache_shape(k_pool, v_pool, tables)
+    shape, dtype = q.shape, k_pool.dtype
+    rows, dim = tables.shape[0], k_pool.shape[3]
+    tokens, q_heads = (shape[0], shape[1]) if len(shape) == 3 else ("tokens", "q_heads")
+    row, head, _ = _heads(q, "q", dtype, (tokens, q_heads, dim))
+    _row(lengths, rows, "lengths")
+    _row(offsets, rows + 1, "offsets")
+    dev = q.get_device()
+    if (dev < 0 or k_pool.get_device() != dev or v_pool.get_device() != dev
+            or tables.get_device() != dev or lengths.get_device() != dev
+            or offsets.get_device() != dev or out is not None and out.get_device() != dev
+            or stream is not None and stream.device.index != dev):
+        _device(stream, q=q, k_pool=k_pool, v_pool=v_pool, tables=tables, lengths=lengths,
+                offsets=offsets, out=out)
+    if out is None:
+        out = _empty(q, shape, dtype, stream)
+        to_row, to_head = q_heads * dim, dim
+    else:
+        to_row, to_head, _ = _heads(out, "out", dtype, shape)
+    lse = _empty(q, (tokens, q_heads), torch.float32, stream) if return_lse else None
+    if rows and tokens:
+        size = _chunk_workspace(cache, q_heads, tokens, dev)
+        workspace = _empty(q, size, torch.uint8, stream) if size else out  # 0: not looked at
+        _run(dev, stream, "w4a16_paged_chunk_attention", q.data_ptr(), k_pool.data_ptr(),
+             v_pool.data_ptr(), tables.data_ptr(), lengths.data_ptr(), offsets.data_ptr(),
+             out.data_ptr(), lse.data_ptr() if return_lse else None, workspace.data_ptr(), cache,
+             _QUERY_SHAPE(q_heads, row, head, to_row, to_head,
+                          dim ** -0.5 if scale is None else scale), tokens)
+    elif tokens:
+        _zero(out, stream)
+        if return_lse:
+            _zero(lse, stream, -float("inf"))
+    return (out, lse) if return_lse else out
+
+
+def _zero(t: torch.Tensor, stream, value: float = 0.0) -> None:
+    """Fills what no row of an empty batch claims."""
+    with torch.cuda.stream(stream):
+        t.fill_(value)
 
 
 def _like(t: torch.Tensor, stream) -> torch.Tensor:
@@ -383,6 +533,106 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0, str
     return logprobs, entropies, ids, likeliest
 
 
+def _penalty(value, rows: int, name: str):
+    """A penalty's tensor and number: one of every row (fp32 [rows]), or one number for all."""
+    if not isinstance(value, torch.Tensor):
+        return None, float(value)
+    if value.dtype is not torch.float32 or value.shape != (rows,) or not value.is_contiguous():
+        raise ValueError(f"{name} must be a number or a dense float32 tensor [{rows}], got "
+                         f"{value.dtype} {list(value.shape)}")
+    return value, 0.0
+
+
+def _rows_of(t: torch.Tensor, rows: int, name: str, dtypes: tuple) -> None:
+    """Refuses what is not [rows, any], dense in its last dimension, of one of the types."""
+    if (t.dtype not in dtypes or t.dim() != 2 or t.shape[0] != rows
+            or t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a {' or '.join(map(str, dtypes))} tensor [{rows}, any], "
+                         f"dense in its last dimension, got {t.dtype} {list(t.shape)}")
+
+
+def adjust_logits(logits: torch.Tensor, tokens: torch.Tensor | None = None,
+                  lengths: torch.Tensor | None = None, prompts: torch.Tensor | None = None,
+                  repetition=1.0, presence=0.0, frequency=0.0,
+                  bias_ids: torch.Tensor | None = None, biases: torch.Tensor | None = None,
+                  mask: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                  stream=None) -> torch.Tensor:
+    """Penalties, biases and masks on logits [rows, vocabulary] (fp16, bf16 or fp32, dense in
+    the last dimension), in this order; returns a new tensor, or `out`, which may be logits.
+
+    tokens (int32 or int64 [rows, width]) lists what each row has said: its first lengths[r]
+    (int32 [rows]; all when None), of which the first prompts[r] (int32 [rows]; none when None)
+    are the prompt's.  A logit x of a token said at all becomes x / repetition where x > 0 and
+    x * repetition elsewhere; frequency times its count in the generation is taken off, and
+    presence once if it is there.  The three are numbers or fp32 tensors [rows].  Then
+    biases[r, i] (fp32 [rows, n], n at most 1024) is added to the logit bias_ids[r, i] (int32),
+    and where bit j % 32 of mask[r, j / 32] (int32 [rows, ceil(vocabulary / 32)]) is 0 logit j
+    becomes -inf.  Tokens outside the vocabulary are passed over."""
+    kind = _TYPES.get(logits.dtype)
+    if kind is None or logits.dim() != 2:
+        raise ValueError("logits must be a float16, bfloat16 or float32 tensor "
+                         f"[rows, vocabulary], got {logits.dtype} {list(logits.shape)}")
+    rows, vocabulary = logits.shape
+    if vocabulary > 1 and logits.stride(1) != 1:
+        raise ValueError("logits must be dense in their last dimension")
+    width = token_stride = wide = 0
+    if tokens is not None:
+        _rows_of(tokens, rows, "tokens", (torch.int32, torch.int64))
+        width, token_stride, wide = tokens.shape[1], tokens.stride(0), tokens.dtype is torch.int64
+    elif lengths is not None or prompts is not None:
+        raise ValueError("lengths or prompts without tokens")
+    for name, t in (("lengths", lengths), ("prompts", prompts)):
+        if t is not None:
+            _row(t, rows, name)
+    scalars, rates = [], []
+    for name, value in (("repetition", repetition), ("presence", presence),
+                        ("frequency", frequency)):
+        t, number = _penalty(value, rows, name)
+        if t is None and name == "repetition" and not number > 0:
+            raise ValueError(f"repetition must be above 0, got {number}")
+        rates.append(t)
+        scalars.append(number)
+    count = bias_stride = 0
+    if (bias_ids is None) != (biases is None):
+        raise ValueError("bias_ids and biases go together")
+    if biases is not None:
+        _rows_of(bias_ids, rows, "bias_ids", (torch.int32,))
+        _rows_of(biases, rows, "biases", (torch.float32,))
+        count, bias_stride = biases.shape[1], biases.stride(0)
+        if bias_ids.shape[1] != count or rows > 1 and bias_ids.stride(0) != bias_stride:
+            raise ValueError("bias_ids and biases must have the same shape and strides")
+        if count > MAX_BIASES:
+            raise ValueError(f"at most {MAX_BIASES} biases a row, got {count}")
+    mask_stride = 0
+    if mask is not None:
+        _rows_of(mask, rows, "mask", (torch.int32,))
+        if mask.shape[1] != -(-vocabulary // 32):
+            raise ValueError(f"mask must have {-(-vocabulary // 32)} words a row, "
+                             f"got {mask.shape[1]}")
+        mask_stride = mask.stride(0)
+    if out is not None and (out.dtype is not logits.dtype or out.shape != logits.shape
+                            or vocabulary > 1 and out.stride(1) != 1):
+        raise ValueError(f"out must be {logits.dtype} {list(logits.shape)}, dense in its last "
+                         f"dimension, got {out.dtype} {list(out.shape)}")
+    dev = logits.get_device()
+    named = {"tokens": tokens, "lengths": lengths, "prompts": prompts, "repetition": rates[0],
+             "presence": rates[1], "frequency": rates[2], "bias_ids": bias_ids, "biases": biases,
+             "mask": mask, "out": out}
+    if (dev < 0 or any(t is not None and t.get_device() != dev for t in named.values())
+            or stream is not None and stream.device.index != dev):
+        _device(stream, logits=logits, **named)
+    if out is None:
+        out = _empty(logits, (rows, vocabulary), logits.dtype, stream)
+    if rows and vocabulary:
+        named["out"] = out
+        _run(dev, stream, "w4a16_adjust_logits",
+             _ADJUST_TENSORS(logits.data_ptr(),
+                             *(0 if t is None else t.data_ptr() for t in named.values())),
+             _ADJUST_SHAPE(rows, vocabulary, kind, logits.stride(0), out.stride(0), wide, width,
+                           token_stride, count, bias_stride, mask_stride, *scalars))
+    return out
+
+
 def _listed(tables: torch.Tensor, lengths: torch.Tensor | None, rows: torch.Tensor, stream):
     """The listed rows' tables and lengths (None for None), taken on the stream the call runs on;
     a row out of range has no pages and length 0."""
@@ -452,6 +702,16 @@ class PagedCache:
         paged_append(k, v, self.keys(layer), self.values(layer), tables, starts, offsets,
                      stream=stream)
 
+    def append_rotary(self, layer: int, k: torch.Tensor, v: torch.Tensor, starts: torch.Tensor,
+                      rotary: Rotary, offsets: torch.Tensor | None = None,
+                      q: torch.Tensor | None = None, rows: torch.Tensor | None = None,
+                      out: torch.Tensor | None = None, stream=None):
+        """New tokens of every row (or of the listed ones) of one layer, keys rotated to their
+        positions; returns the rotated queries (paged_append_rotary)."""
+        tables = self.tables if rows is None else _listed(self.tables, None, rows, stream)[0]
+        return paged_append_rotary(k, v, self.keys(layer), self.values(layer), tables, starts,
+                                   rotary, offsets, q=q, out=out, stream=stream)
+
     def attend(self, layer: int, q: torch.Tensor, rows: torch.Tensor | None = None,
                scale: float | None = None, out: torch.Tensor | None = None, stream=None):
         """Attention of one new token of every row (or of the listed ones) (paged_attention)."""
@@ -460,6 +720,17 @@ class PagedCache:
             tables, lengths = _listed(tables, lengths, rows, stream)
         return paged_attention(q, self.keys(layer), self.values(layer), tables, lengths,
                                scale=scale, out=out, stream=stream)
+
+    def attend_chunks(self, layer: int, q: torch.Tensor, offsets: torch.Tensor,
+                      rows: torch.Tensor | None = None, scale: float | None = None,
+                      out: torch.Tensor | None = None, stream=None):
+        """Attention of the last tokens of every row (or of the listed ones)
+        (paged_chunk_attention)."""
+        tables, lengths = self.tables, self.lengths
+        if rows is not None:
+            tables, lengths = _listed(tables, lengths, rows, stream)
+        return paged_chunk_attention(q, self.keys(layer), self.values(layer), tables, lengths,
+                                     offsets, scale=scale, out=out, stream=stream)
 
     def fork(self, parents: torch.Tensor, children: torch.Tensor, stream=None) -> torch.Tensor:
         """Row children[i] becomes a copy of row parents[i]; returns done (pages_fork)."""
