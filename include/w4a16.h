@@ -542,7 +542,7 @@ int w4a16_paged_append_rotary(const void *k, const void *v, const uint64_t *turn
  *   workspace  w4a16_paged_chunk_workspace(cache, q_heads, tokens) bytes,
  *              16-byte aligned, of any content; not to be shared by calls that
  *              may run at once.
- *   tokens     0 .. 2^24, tokens * q_heads at most 2^31; q_heads as for
+ *   tokens     0 .. 2^24, tokens * q_heads at most 2^30; q_heads as for
  *              w4a16_paged_attention.
  * Positions without a valid page are left out, as if masked, and so are those
  * whose score is -infinity; a head that has no other position gets zeros and

@@ -101,7 +101,7 @@ bool good_in_place(const void* in, const void* out, const w4a16_heads_shape& h) 
 bool good_chunk(const w4a16_cache_shape& c, int64_t q_heads, int64_t tokens) {
     return good_cache(c) && q_heads >= 1 && q_heads <= 1024 && q_heads % c.kv_heads == 0 &&
            good_steps(c, q_heads) && tokens >= 0 && tokens <= (int64_t)1 << 24 &&
-           tokens * q_heads <= (int64_t)1 << 31;
+           tokens * q_heads <= (int64_t)1 << 30;
 }
 
 bool good_books(const w4a16_books_shape& b) {

@@ -1,113 +1,1000 @@
-// chunk.cu -- attention of chunks of new tokens over the paged cache.
+// chunk.cu -- attention of chunks of new tokens over the paged cache, on the
+// tcgen05 tensor cores.
+//
+// A row's new tokens and the query heads that share a key-value head are one list
+// of queries, token by token, and 256 of those (128 with heads above 128) are the
+// rows of an item: two MMA tiles of 128 rows, whatever the number of heads to a
+// key-value head.  An item walks the positions that its last query sees in steps
+// of 128 (64): S = Q K^T, P = exp(S - max), O += P V, with S and O in tensor memory
+// and P written over S as the 16-bit left operand of the second product.
+//
+// Bound by the tensor cores: 4 dim FLOPs a query and position, where a step's 64 KB
+// of keys and values serve 256 queries.  The two tiles take turns, so that the
+// tensor cores work on one while the other's softmax runs:
+//   warps 0-3, 4-7   softmax of the first and second tile, a thread a query
+//   warps 8-11       copy queries, keys and values (cp.async, any page size),
+//                    zeros where a position has no page
+//   warp 12          one thread issues the MMAs
+//   warp 13          takes the next unit of work
+// The work is cut by a plan kernel, as only the device knows the lengths: items are
+// split into parts where that levels the load, and a join kernel adds those up.
+// Blocks take units from a counter, longest first within a row, the parts of one
+// item side by side: blocks at work at the same time read the same keys and values,
+// through L2.
 #include <cuda_bf16.h>
+
+#include <algorithm>
+#include <mutex>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
 #include "paged.cuh"
+#include "tcgen05.cuh"
 
 namespace w4a16 {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kQueryTile = 128;   // queries of an MMA
+constexpr int kSoftmaxWarps = 8, kCopyWarps = 4;
+constexpr int kMmaWarp = kSoftmaxWarps + kCopyWarps, kUnitWarp = kMmaWarp + 1;
+constexpr int kThreads = 32 * (kUnitWarp + 1);
+constexpr int kSlots = 4;         // of the ring: keys, values, keys, values
+constexpr int kUnits = 4;         // places for units' notes of values that are not finite
+constexpr int kPlanThreads = 1024;
+constexpr int kJoinThreads = 128;
+constexpr int kPartsPerSm = 4;    // of the workspace
+
+// Sizes by the padded head size: queries of an item, positions of a step.
+template <int DP>
+struct Shape {
+    static constexpr int kTiles = DP <= 128 ? 2 : 1;
+    static constexpr int kRows = kTiles * kQueryTile;
+    static constexpr int kStep = DP <= 128 ? 128 : 64;
+    static constexpr int kTileBytes = kQueryTile * DP * 2;
+    static constexpr int kSlotBytes = kStep * DP * 2;
+    static constexpr int kOffRing = kTiles * kTileBytes;
+    static constexpr int kOffRest = kOffRing + kSlots * kSlotBytes;
+    static constexpr int kSmem = 1024 + kOffRest + 16384;
+    static constexpr int kOutColumn = 256;                      // of tensor memory
+};
+constexpr int rows_of(int64_t dim) { return dim <= 128 ? 256 : 128; }
+constexpr int step_of(int64_t dim) { return dim <= 128 ? 128 : 64; }
+
+// What the plan leaves: `entries` units for each key-value head, `parts` of them parts of
+// `joints` items.
+struct Plan {
+    int entries, parts, joints;
+    unsigned next;  // unit to hand out
+};
+struct Entry {
+    int row, tile, first, steps;  // steps first .. first + steps - 1 of item `tile` of `row`
+    int part;                     // its place among the parts, -1: a whole item
+    int unused[3];
+};
+struct Joint {
+    int row, tile, part, count;
+};
+struct Slot {
+    int row, tile, steps, unused;
+};
 
 struct ChunkArgs {
     const uint16_t *q, *k_pool, *v_pool;
     const int32_t *tables, *lengths, *offsets;
     uint16_t* out;
     float* lse;
+    Plan* plan;
+    Entry* entries;
+    Joint* joints;
+    Slot* slots;
+    float* partial;      // [part][head][tile][dim / 4][query][4]
+    float2* partial_ml;  // [part][head][query of the item]
     int64_t tokens, q_row, q_head, out_row, out_head;
-    int q_heads, group;
-    float scale;
+    int64_t slot_count, most_parts;
+    int q_heads, sms;
+    float scale_log2;    // of the scale's magnitude; its sign:
+    int negative;
+    unsigned* status;
+    uint64_t timeout_ns;
     Cache c;
+    Divisor group;
+
+    __device__ int64_t offset(int b) const {
+        return min(max((int64_t)offsets[b], (int64_t)0), tokens);
+    }
+    __device__ int64_t length(int b) const {
+        return min(max((int64_t)lengths[b], (int64_t)0), (int64_t)c.width * c.page_size.value);
+    }
 };
 
-// A warp has one head of one token: 32 positions at a time, a lane's score each, then the lanes
-// take eight dimensions of V each.
-template <typename T>
-__global__ void __launch_bounds__(32 * kWarps) chunk_kernel(ChunkArgs a) {
-    __shared__ float query[kWarps][256];
+// ---------------------------------------------------------------------------
+// The plan
+//
+// Item j of row b takes slot offsets[b] group / rows + b + j (rows of an item): as
+// offsets do not descend, no two items share one, and an item's row is found by a
+// search.  Items of n steps are cut into ceil(n / u) parts, with the u out of
+// ceil(longest / 1), ceil(longest / 2), ... that makes the estimated time least: a unit
+// costs its steps and two more (three where it is a part), blocks are level to half
+// a unit, or, where all items are alike, take whole rounds.
+// ---------------------------------------------------------------------------
+constexpr int kUnitCost = 2, kCandidates = 256;
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a, int rows, int step) {
+    __shared__ int64_t sums[32];
+    __shared__ int mins[32], maxs[32];
+    __shared__ float best_cost[kCandidates];
+    __shared__ int chosen;
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     grid_dependency_wait();
     grid_launch_dependents();
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int64_t unit = (int64_t)blockIdx.x * kWarps + warp;
-    if (unit >= a.tokens * a.q_heads) return;
-    const int64_t t = unit / a.q_heads;
-    const int h = (int)(unit % a.q_heads), dim = a.c.head_dim;
-    const int b = row_of(a.offsets, a.c.batch, t);
-    int64_t limit = 0;  // positions that the token sees
-    if (b >= 0) {
-        const int64_t length = min(max((int64_t)a.lengths[b], (int64_t)0),
-                                   (int64_t)a.c.width * a.c.page_size.value);
-        limit = max(length - a.offsets[b + 1] + t + 1, (int64_t)0);
-    }
-    const T* q = reinterpret_cast<const T*>(a.q) + t * a.q_row + h * a.q_head;
-    for (int x = lane; x < dim; x += 32) query[warp][x] = (float)q[x];
-    __syncwarp();
-    const int64_t head = (int64_t)(h / a.group) * a.c.head_stride;
-    float m = -INFINITY, l = 0.f, o[8] = {};
-    for (int64_t first = 0; first < limit; first += 32) {
-        const int64_t p = first + lane;
-        int64_t at = -1;
-        if (p < limit) {
-            const int j = a.c.page_size.quotient((int)p);
-            const int64_t page = a.tables[b * a.c.table_stride + j];
-            if (page >= 0 && page < a.c.pages)
-                at = page * a.c.page_stride + (p - j * a.c.page_size.value) * a.c.slot_stride + head;
+    const int heads = a.c.kv_heads;
+    int64_t total = 0;
+    int longest = 0, shortest = INT32_MAX;
+    for (int64_t s = tid; s < a.slot_count; s += kPlanThreads) {
+        const auto key = [&](int b) { return a.offset(b) * a.group.value / rows + b; };
+        int lo = 0, hi = a.c.batch;  // key(lo) <= s < key(hi)
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (key(mid) <= s) lo = mid; else hi = mid;
         }
-        float s = -INFINITY;
-        if (at >= 0) {
-            s = 0.f;
-            const T* k = reinterpret_cast<const T*>(a.k_pool) + at;
-            for (int x = 0; x < dim; x += 8) {
-                const uint4 piece = *reinterpret_cast<const uint4*>(k + x);
-                const T* v = reinterpret_cast<const T*>(&piece);
+        const int64_t from = a.offset(lo), count = max(a.offset(lo + 1) - from, (int64_t)0);
+        const int64_t tile = s - key(lo);
+        int steps = 0;
+        if (tile >= 0 && tile * rows < count * a.group.value) {
+            const int64_t end = min(count, ((tile + 1) * rows + a.group.value - 1) / a.group.value);
+            const int64_t seen = a.length(lo) - count + end;  // positions of the item's last query
+            steps = seen > 0 ? (int)((seen + step - 1) / step) : 0;
+        }
+        a.slots[s] = {lo, (int)tile, steps, 0};
+        if (steps) {
+            total += steps;
+            longest = max(longest, steps);
+            shortest = min(shortest, steps);
+        }
+    }
 #pragma unroll
-                for (int y = 0; y < 8; ++y) s = fmaf((float)v[y], query[warp][x + y], s);
+    for (int d = 16; d > 0; d /= 2) {
+        total += __shfl_xor_sync(~0u, total, d);
+        longest = max(longest, __shfl_xor_sync(~0u, longest, d));
+        shortest = min(shortest, __shfl_xor_sync(~0u, shortest, d));
+    }
+    if (lane == 0) sums[warp] = total, maxs[warp] = longest, mins[warp] = shortest;
+    __syncthreads();
+    total = 0;
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+        total += sums[w];
+        longest = max(longest, maxs[w]);
+        shortest = min(shortest, mins[w]);
+    }
+    total *= heads;
+    int unit = max(longest, 1);
+    // (an item that is a small part of a block's share is not worth a cut)
+    if ((int64_t)longest * 6 * a.sms > total && a.most_parts > 0) {
+        if (tid < kCandidates) {
+            const int u = (longest + tid) / (tid + 1);
+            float cost = INFINITY;
+            if (tid == 0 || u >= 2) {
+                int64_t units = 0, parts = 0;
+                const float inverse = 1.f / (float)u;
+                for (int64_t s = 0; s < a.slot_count; ++s) {
+                    const int n = a.slots[s].steps;
+                    int k = (int)((float)n * inverse);  // ceil(n / u), or one more for very large n
+                    k += k * (int64_t)u < n;
+                    k += k * (int64_t)u < n;
+                    units += k;
+                    if (k > 1) parts += k;
+                }
+                units *= heads;
+                const float extra = parts ? kUnitCost + 1 : kUnitCost;
+                if (shortest == longest)
+                    cost = (float)((units + a.sms - 1) / a.sms) * ((float)u + extra);
+                else
+                    cost = ((float)total + extra * (float)units) / (float)a.sms + ((float)u + extra) / 2;
+                if (parts * heads > a.most_parts) cost = INFINITY;
             }
-            s *= a.scale;
+            best_cost[tid] = cost;
         }
-        float top = s;
+        __syncthreads();
+        if (tid == 0) {
+            int best = 0;
+            for (int i = 1; i < kCandidates; ++i)
+                if (best_cost[i] < best_cost[best]) best = i;
+            chosen = (longest + best) / (best + 1);
+        }
+        __syncthreads();
+        unit = chosen;
+    }
+    // Entries, from the last slot to the first.
+    int64_t base_units = 0, base_parts = 0;
+    int base_joints = 0;
+    for (int64_t first = 0; first < a.slot_count; first += kPlanThreads) {
+        const int64_t s = a.slot_count - 1 - first - tid;
+        Slot slot = {};
+        if (s >= 0) slot = a.slots[s];
+        const int k = slot.steps ? (slot.steps + unit - 1) / unit : 0;
+        // units in the low half, parts in the high one
+        int64_t both = k + ((int64_t)(k > 1 ? k : 0) << 32), upto = both;
+        int joint = k > 1, joint_upto = joint;
 #pragma unroll
-        for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-        top = fmaxf(top, m);
+        for (int d = 1; d < 32; d *= 2) {
+            const int64_t o = __shfl_up_sync(~0u, upto, d);
+            const int j = __shfl_up_sync(~0u, joint_upto, d);
+            if (lane >= d) upto += o, joint_upto += j;
+        }
+        __syncthreads();
+        if (lane == 31) sums[warp] = upto, maxs[warp] = joint_upto;
+        __syncthreads();
+        int64_t all = 0;
+        int all_joints = 0;
+        for (int w = 0; w < kPlanThreads / 32; ++w) {
+            if (w == warp) upto += all, joint_upto += all_joints;
+            all += sums[w];
+            all_joints += maxs[w];
+        }
+        const int64_t at = base_units + (uint32_t)(upto - both);
+        const int64_t part = base_parts + ((upto - both) >> 32);
+        if (k > 1) a.joints[base_joints + joint_upto - joint] = {slot.row, slot.tile, (int)part, k};
+        for (int i = 0; i < k; ++i) {
+            const int from = (int)((int64_t)slot.steps * i / k), to = (int)((int64_t)slot.steps * (i + 1) / k);
+            a.entries[at + i] = {slot.row, slot.tile, from, to - from, k > 1 ? (int)(part + i) : -1, {}};
+        }
+        base_units += (uint32_t)all;
+        base_parts += all >> 32;
+        base_joints += all_joints;
+    }
+    if (tid == 0) *a.plan = {(int)base_units, (int)base_parts, base_joints, 0};
+}
+
+// ---------------------------------------------------------------------------
+// Helpers
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(there ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if constexpr (std::is_same<T, __half>::value) {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    } else {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+}
+
+// D[tmem] (+)= A[tmem] * B[smem desc], 16-bit inputs, f32 accumulate.
+__device__ __forceinline__ void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                              uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// tcgen05.ld of 32 columns, and the wait for it (one statement: nothing may use r in between).
+__device__ __forceinline__ void tmem_load32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+        "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// V's tile as the right operand [positions x dims] with dims along the rows of shared memory
+// (MN-major, 128-byte swizzle): 64 dimensions are a 128-byte row, `block` bytes from one such
+// block of dimensions to the next, 1024 bytes from eight positions to the next eight.
+__device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t smem_addr, uint32_t block) {
+    return (uint64_t)((smem_addr >> 4) & 0x3FFFu) | ((uint64_t)(block >> 4) << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// ---------------------------------------------------------------------------
+// The attention
+// ---------------------------------------------------------------------------
+// A unit of work as every warp reads it.
+struct Unit {
+    int row, head, first, steps, part;  // steps < 0: no more units
+    int lin0, lins;        // queries of the item: first and count, in the row's list
+    int64_t token0;        // the row's first token
+    int64_t position0;     // its position (below 0 for a row with more tokens than positions)
+    int64_t length;        // positions of the row
+};
+
+// Values that are not finite, in steps that some of the item's queries do not see whole: the
+// first position of each dimension with NaN, +infinity and -infinity.  They enter the products
+// as zeros, so that queries before them are left alone.
+template <int DP>
+struct Odd {
+    int any;
+    int first[3][DP];
+};
+
+template <int DP>
+struct Rest {
+    uint64_t unit_full[2], unit_free[2], q_full, q_free;
+    uint64_t kv_full[kSlots], kv_free[kSlots], s_full[2], p_full[2], o_full[2], done;
+    uint32_t tmem;
+    uint32_t valid[4][4];  // of a step, a bit a position (step / 4 a word)
+    Unit unit[2];
+    Odd<DP> odd[kUnits];
+};
+
+// A group of copies on its way: where to report it, and whether its values are to be looked at.
+struct Group {
+    uint32_t bar;    // 0: none
+    uint32_t slot;   // of values to be looked at, 0: not
+    int position;
+    int unit;
+};
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ ChunkArgs a) {
+    using S = Shape<DP>;
+    static_assert(sizeof(Rest<DP>) <= 16384, "the rest of shared memory");
+    constexpr bool kHalf = std::is_same<T, __half>::value;
+    // Weights are held times 2^headroom: FP16 has nothing below 2^-24, and many small weights
+    // beside a large one would vanish.  A new maximum is let be up to 2^slack above the old.
+    constexpr float kHeadroom = kHalf ? 12.f : 0.f, kSlack = kHalf ? 3.f : 8.f;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
+    Rest<DP>& rest = *reinterpret_cast<Rest<DP>*>(smem + S::kOffRest);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const auto bar = [&](const uint64_t& b) { return smem_u32(&b); };
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(rest.unit_full[i]), 1);
+            mbar_init(bar(rest.unit_free[i]), 4 * S::kTiles + kCopyWarps + 1);
+            mbar_init(bar(rest.s_full[i]), 2);
+            mbar_init(bar(rest.p_full[i]), 4);
+            mbar_init(bar(rest.o_full[i]), 2);
+        }
+        mbar_init(bar(rest.q_full), kCopyWarps);
+        mbar_init(bar(rest.q_free), 1);
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(bar(rest.kv_full[i]), kCopyWarps);
+            mbar_init(bar(rest.kv_free[i]), 1);
+        }
+        mbar_init(bar(rest.done), 1);
+        fence_barrier_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(smem_u32(&rest.tmem), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&rest.tmem);
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int group = a.group.value;
+
+    // Waits for unit number n and reads it; false where there is none, or the wait gave up.
+    const auto next_unit = [&](uint32_t n, Unit& u) {
+        bool ok = mbar_wait(bar(rest.unit_full[n % 2]), n / 2 % 2, a.timeout_ns, a.status);
+        ok = __all_sync(~0u, ok);
+        u.steps = -1;
+        if (ok) u = rest.unit[n % 2];
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(bar(rest.unit_free[n % 2]));
+        return u.steps > 0;
+    };
+    // Steps that tile q of a unit takes part in.
+    const auto steps_of = [&](const Unit& u, int q) {
+        const int end = min(u.lins, (q + 1) * kQueryTile);
+        if (end <= q * kQueryTile) return 0;
+        const int64_t seen = u.position0 + a.group.quotient(u.lin0 + end - 1) + 1;
+        const int64_t steps = seen > 0 ? (seen + S::kStep - 1) / S::kStep : 0;
+        return (int)min(max(steps - u.first, (int64_t)0), (int64_t)u.steps);
+    };
+
+    if (warp == kUnitWarp) {
+        // =============================== units ================================
+        const unsigned total = (unsigned)a.plan->entries * (unsigned)a.c.kv_heads;
+        const unsigned entries = (unsigned)a.plan->entries;
+        for (uint32_t n = 0;; ++n) {
+            unsigned i = 0;
+            if (lane == 0) i = atomicAdd(&a.plan->next, 1u);
+            i = __shfl_sync(~0u, i, 0);
+            Unit u = {};
+            u.steps = -1;
+            if (i < total) {
+                const Entry e = a.entries[i % entries];
+                const int64_t from = a.offset(e.row), count = a.offset(e.row + 1) - from;
+                u.row = e.row;
+                u.head = (int)(i / entries);
+                u.first = e.first;
+                u.steps = e.steps;
+                u.part = e.part;
+                u.lin0 = e.tile * S::kRows;
+                u.lins = (int)min((int64_t)S::kRows, count * group - u.lin0);
+                u.token0 = from;
+                u.length = a.length(e.row);
+                u.position0 = u.length - count;
+            }
+            bool ok = n < 2 || mbar_wait(bar(rest.unit_free[n % 2]), (n / 2 - 1) % 2, a.timeout_ns,
+                                         a.status);
+            if (!__all_sync(~0u, ok)) break;
+            Odd<DP>& odd = rest.odd[n % kUnits];
+            for (int x = lane; x < 3 * DP; x += 32) (&odd.first[0][0])[x] = INT32_MAX;
+            if (lane == 0) {
+                odd.any = 0;
+                rest.unit[n % 2] = u;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(rest.unit_full[n % 2]));
+            if (u.steps < 0) break;
+        }
+    } else if (warp == kMmaWarp) {
+        // ================================ MMAs ================================
+        constexpr uint32_t kType = kHalf ? 0u : (1u << 7) | (1u << 10);
+        const uint32_t scores = umma_idesc_f16_f32(kQueryTile, S::kStep) | kType |
+                                (a.negative ? 1u << 13 : 0u);  // (minus the queries)
+        const uint32_t values = umma_idesc_f16_f32(kQueryTile, DP) | kType | (1u << 16);  // V: MN-major
+        uint32_t step = 0;  // of the block, for the ring's slots
+        uint32_t taken[2] = {0, 0};  // steps of each tile
+        Unit u;
+        bool ok = true;
+        for (uint32_t n = 0; ok && next_unit(n, u); ++n) {
+            if (lane == 0) {
+                const int steps[2] = {steps_of(u, 0), S::kTiles == 2 ? steps_of(u, 1) : 0};
+                const auto wait = [&](uint64_t& b, uint32_t phase) {
+                    if (ok) ok = mbar_wait(bar(b), phase & 1, a.timeout_ns, a.status);
+                    tc_fence_after_sync();
+                };
+                // Reports the MMAs issued so far, and passes on (by an arrival of this thread) what
+                // the copying warps wrote.
+                const auto finished = [&](uint64_t& b) {
+                    tc_commit(bar(b));
+                    mbar_arrive(bar(b));
+                };
+                const auto score = [&](int q, uint32_t slot) {
+                    const uint32_t qa = base + q * S::kTileBytes;
+                    const uint32_t ka = base + S::kOffRing + slot * S::kSlotBytes;
+#pragma unroll
+                    for (int j = 0; j < DP / 16; ++j)
+                        tc_mma_f16(tmem + q * 128,
+                                   umma_desc_sw128(qa + j / 4 * (kQueryTile * 128) + j % 4 * 32),
+                                   umma_desc_sw128(ka + j / 4 * (S::kStep * 128) + j % 4 * 32), scores,
+                                   j != 0);
+                    finished(rest.s_full[q]);
+                };
+                wait(rest.q_full, n);
+                wait(rest.kv_full[2 * step % kSlots], 2 * step / kSlots);
+                if (ok) {
+                    for (int q = 0; q < S::kTiles; ++q)
+                        if (steps[q] > 0) score(q, 2 * step % kSlots);
+                    tc_commit(bar(rest.kv_free[2 * step % kSlots]));
+                    if (u.steps == 1) tc_commit(bar(rest.q_free));
+                }
+                for (int i = 0; ok && i < u.steps; ++i, ++step) {
+                    const uint32_t v = 2 * step + 1, k = 2 * step + 2;
+                    wait(rest.kv_full[v % kSlots], v / kSlots);
+                    if (i + 1 < u.steps) wait(rest.kv_full[k % kSlots], k / kSlots);
+                    for (int q = 0; q < S::kTiles; ++q) {
+                        if (i >= steps[q]) continue;
+                        wait(rest.p_full[q], taken[q]++);
+                        if (!ok) break;
+                        const uint32_t va = base + S::kOffRing + v % kSlots * S::kSlotBytes;
+#pragma unroll
+                        for (int j = 0; j < S::kStep / 16; ++j)
+                            tc_mma_f16_ta(tmem + S::kOutColumn + q * DP, tmem + q * 128 + 8 * j,
+                                          umma_desc_mn_sw128(va + j * 2048, S::kStep * 128), values,
+                                          (i | j) != 0);
+                        if (i + 1 < steps[q])
+                            score(q, k % kSlots);
+                        else
+                            finished(rest.o_full[q]);
+                    }
+                    if (!ok) break;
+                    tc_commit(bar(rest.kv_free[v % kSlots]));
+                    if (i + 1 < u.steps) tc_commit(bar(rest.kv_free[k % kSlots]));
+                    if (i + 2 == u.steps) tc_commit(bar(rest.q_free));
+                }
+            }
+            ok = __shfl_sync(~0u, ok, 0);
+        }
+        if (lane == 0) {  // nothing in flight when the block ends
+            tc_commit(bar(rest.done));
+            mbar_wait(bar(rest.done), 0, drain_bound(a.timeout_ns), a.status);
+        }
+        __syncwarp();
+    } else if (warp >= kSoftmaxWarps) {
+        // =============================== copies ===============================
+        constexpr int kPieces = DP / 8;              // of a row, 16 bytes each
+        constexpr int kPasses = kPieces < 32 ? 1 : kPieces / 32;
+        constexpr int kRowsPass = kPieces < 32 ? 32 / kPieces : 1;
+        static_assert(kPasses == 1, "a pass of a warp is whole rows");
+        constexpr int kRowsWarp = S::kStep / kCopyWarps;
+        const int w = warp - kSoftmaxWarps, piece = lane % kPieces, row0 = lane / kPieces;
+        const bool in_dim = piece * 8 < a.c.head_dim;
+        // a piece's place in a tile of `rows` rows: blocks of 64 dimensions, swizzled by the row
+        const auto at = [&](int row, int rows) {
+            return (uint32_t)(piece / 8 * rows * 128 + row * 128 + ((piece % 8 ^ row % 8) << 4));
+        };
+        Group pending[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+        // The oldest group has landed: look through its values, if need be, and report it.
+        const auto report = [&](const Group& g) {
+            if (g.bar == 0) return;
+            if (g.slot) {
+                Odd<DP>& odd = rest.odd[g.unit % kUnits];
+                for (int r = row0; r < kRowsWarp; r += kRowsPass) {
+                    const int row = w * kRowsWarp + r;
+                    const uint32_t where = g.slot + at(row, S::kStep);
+                    uint4 v = lds128(where);
+                    uint32_t* words = reinterpret_cast<uint32_t*>(&v);
+                    constexpr uint32_t kExponent = kHalf ? 0x7C00u : 0x7F80u;
+                    bool bad = false;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        bad = bad || (words[x] & kExponent) == kExponent ||
+                              (words[x] & kExponent << 16) == kExponent << 16;
+                    if (!bad) continue;
+                    for (int x = 0; x < 8; ++x) {
+                        const uint32_t one = words[x / 2] >> (16 * (x % 2)) & 0xFFFFu;
+                        if ((one & kExponent) != kExponent) continue;
+                        const int kind = (one & (kExponent ^ 0x7FFFu)) ? 0 : one >> 15 ? 2 : 1;
+                        atomicMin(&odd.first[kind][piece * 8 + x], g.position + row);
+                        words[x / 2] &= x % 2 ? 0xFFFFu : 0xFFFF0000u;
+                    }
+                    odd.any = 1;
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(where), "r"(v.x),
+                                 "r"(v.y), "r"(v.z), "r"(v.w)
+                                 : "memory");
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(g.bar);
+        };
+        const auto issued = [&](const Group& g) {
+            copy_commit();
+            copy_wait<2>();
+            report(pending[0]);
+            pending[0] = pending[1];
+            pending[1] = g;
+        };
+        uint32_t step = 0;
+        Unit u;
+        bool ok = true;
+        const auto wait = [&](uint64_t& b, uint32_t phase) {
+            const bool got = mbar_wait(bar(b), phase & 1, a.timeout_ns, a.status);
+            ok = __all_sync(~0u, got);
+        };
+        for (uint32_t n = 0; ok && next_unit(n, u); ++n) {
+            const int64_t head = (int64_t)u.head * a.c.head_stride;
+            const int32_t* table = a.tables + u.row * a.c.table_stride;
+            const auto page_of = [&](int i) {  // of this lane's position in step i
+                const int64_t p = (int64_t)(u.first + i) * S::kStep + w * kRowsWarp + lane % kRowsWarp;
+                return p < u.length ? table[a.c.page_size.quotient((int)p)] : -1;
+            };
+            int next = page_of(0);
+            // positions that every query of the item sees
+            const int64_t all_see = u.position0 + a.group.quotient(u.lin0) + 1;
+            if (n > 0) wait(rest.q_free, n - 1);
+            if (!ok) break;
+            const uint16_t* q0 = a.q + u.token0 * a.q_row + (int64_t)u.head * group * a.q_head;
+            for (int r = w * (S::kRows / kCopyWarps) + row0; r < (w + 1) * (S::kRows / kCopyWarps);
+                 r += kRowsPass) {
+                const bool in = r < u.lins && in_dim;
+                const int token = a.group.quotient(u.lin0 + r), h = u.lin0 + r - token * group;
+                copy16(base + r / kQueryTile * S::kTileBytes + at(r % kQueryTile, kQueryTile),
+                       in ? q0 + token * a.q_row + h * a.q_head + 8 * piece : a.q, in);
+            }
+            issued({bar(rest.q_full), 0, 0, 0});
+            for (int i = 0; i < u.steps; ++i, ++step) {
+                const int position = (u.first + i) * S::kStep;
+                int64_t place = -1;
+                if ((uint32_t)next < (uint32_t)a.c.pages) {
+                    const int p = position + w * kRowsWarp + lane % kRowsWarp;
+                    place = next * a.c.page_stride + a.c.page_size.remainder(p) * a.c.slot_stride + head;
+                }
+                const uint32_t there = __ballot_sync(~0u, place >= 0);
+                if (i + 1 < u.steps) next = page_of(i + 1);
+#pragma unroll 1
+                for (int value = 0; value < 2; ++value) {
+                    const uint32_t g = 2 * step + value, slot = g % kSlots;
+                    if (g >= kSlots) wait(rest.kv_free[slot], g / kSlots - 1);
+                    if (!ok) break;
+                    if (!value && lane == 0)
+                        rest.valid[step % 4][w] =
+                            kRowsWarp == 32 ? there : there & ((1u << kRowsWarp % 32) - 1);
+                    const uint32_t to = base + S::kOffRing + slot * S::kSlotBytes;
+                    const uint16_t* pool = (value ? a.v_pool : a.k_pool) + 8 * piece;
+#pragma unroll
+                    for (int r = 0; r < kRowsWarp; r += kRowsPass) {
+                        const int64_t o = __shfl_sync(~0u, place, r + row0);
+                        const bool in = o >= 0 && in_dim;
+                        copy16(to + at(w * kRowsWarp + r + row0, S::kStep), in ? pool + o : a.k_pool, in);
+                    }
+                    const bool look = value && (int64_t)position + S::kStep > all_see;
+                    issued({bar(rest.kv_full[slot]), look ? to : 0u, position, (int)n});
+                }
+                if (!ok) break;
+            }
+            copy_wait<0>();
+            if (ok) {
+                report(pending[0]);
+                report(pending[1]);
+            }
+            pending[0].bar = pending[1].bar = 0;
+        }
+        copy_wait<0>();
+    } else if (warp < 4 * S::kTiles) {
+        // ============================== softmax ===============================
+        const int q = warp / 4, r = warp % 4 * 32 + lane;
+        const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
+        const uint32_t t_scores = tmem + lanes + q * 128;
+        const uint32_t t_out = tmem + lanes + S::kOutColumn + q * DP;
+        // What no unit writes: tokens of no row, or of positions below 0.
+        {
+            const int per = 32 * 4 * S::kTiles;
+            const int x = threadIdx.x;
+            const auto zero = [&](int64_t from, int64_t to) {  // tokens, by all the softmax threads
+                const int64_t work = (to - from) * a.q_heads;
+                for (int64_t i = x; i < work; i += per) {
+                    const int64_t t = from + i / a.q_heads;
+                    const int h = (int)(i % a.q_heads);
+                    uint16_t* o = a.out + t * a.out_row + h * a.out_head;
+                    for (int y = 0; y < a.c.head_dim; y += 8)
+                        *reinterpret_cast<uint4*>(o + y) = make_uint4(0, 0, 0, 0);
+                    if (a.lse) a.lse[t * a.q_heads + h] = -INFINITY;
+                }
+            };
+            for (int b = blockIdx.x; b < a.c.batch; b += gridDim.x) {
+                const int64_t from = a.offset(b), count = a.offset(b + 1) - from;
+                const int64_t below = count - a.length(b);
+                if (below > 0) zero(from, from + min(below, count));
+            }
+            const int64_t before = a.offset(0), behind = a.tokens - a.offset(a.c.batch);
+            for (int64_t t = blockIdx.x; t < before; t += gridDim.x) zero(t, t + 1);
+            for (int64_t t = blockIdx.x; t < behind; t += gridDim.x)
+                zero(a.tokens - 1 - t, a.tokens - t);
+        }
+        uint32_t taken = 0, units = 0, step0 = 0;  // steps and units of this tile, steps of the block
+        Unit u;
+        bool ok = true;
+        for (uint32_t n = 0; ok && next_unit(n, u); step0 += u.steps, ++n) {
+            const int steps = steps_of(u, q);
+            const int lin = u.lin0 + q * kQueryTile + r;
+            const bool in = q * kQueryTile + r < u.lins;
+            const int token = a.group.quotient(lin), h = u.head * group + lin - token * group;
+            // positions that the query sees; all, for a row that is not there
+            const int64_t limit = in ? max(u.position0 + token + 1, (int64_t)0) : INT32_MAX;
+            const int least = __reduce_min_sync(~0u, (int)limit);
+            float top = -INFINITY, sum = 0.f;
+#pragma unroll 1
+            for (int i = 0; i < steps; ++i) {
+                ok = mbar_wait(bar(rest.s_full[q]), taken & 1, a.timeout_ns, a.status);
+                ok = __all_sync(~0u, ok);
+                if (!ok) break;
+                ++taken;
+                tc_fence_after_sync();
+                const int position = (u.first + i) * S::kStep;
+                // a bit a position of the step that counts
+                uint32_t bits[S::kStep / 32];
+                bool whole = (int64_t)position + S::kStep <= least;
+#pragma unroll
+                for (int k = 0; k < S::kStep / 32; ++k) {
+                    const uint32_t* v = rest.valid[(step0 + i) % 4];
+                    bits[k] = S::kStep == 128 ? v[k] : v[2 * k] | v[2 * k + 1] << 16;
+                    whole = whole && bits[k] == ~0u;
+                }
+                if (!whole) {
+                    const int left = (int)min(max(limit - position, (int64_t)0), (int64_t)S::kStep);
+#pragma unroll
+                    for (int k = 0; k < S::kStep / 32; ++k)
+                        bits[k] &= left >= 32 * k + 32 ? ~0u : left <= 32 * k ? 0u : (1u << (left - 32 * k)) - 1;
+                }
+                float high = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < S::kStep / 32; ++k) {
+                    uint32_t s[32];
+                    tmem_load32(t_scores + 32 * k, s);
+                    if (whole) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) high = fmaxf(high, __uint_as_float(s[j]));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            high = fmaxf(high, bits[k] >> j & 1 ? __uint_as_float(s[j]) : -INFINITY);
+                    }
+                }
+                high = high == -INFINITY ? high : high * a.scale_log2;
+                if (__any_sync(~0u, high > top + kSlack)) {
+                    // (each query by its own: what the others see makes no difference to it)
+                    const float higher = high > top + kSlack ? high : top;
+                    const float keep = higher == top ? 1.f : exp2_fast(top - higher);
+                    top = higher;
+                    sum *= keep;
+                    if (i > 0) {
+                        // (the scores are there, so the MMAs before them are done)
+#pragma unroll 1
+                        for (int c = 0; c < DP; c += 32) {
+                            uint32_t o[32];
+                            tmem_load32(t_out + c, o);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * keep);
+                            tmem_st_32x32b_x32(t_out + c, o);
+                        }
+                    }
+                }
+                const float base_exp = (top == -INFINITY ? 0.f : top) - kHeadroom;
+#pragma unroll
+                for (int k = 0; k < S::kStep / 32; ++k) {
+                    uint32_t s[32], p[16];
+                    tmem_load32(t_scores + 32 * k, s);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        float x = fmaf(__uint_as_float(s[j]), a.scale_log2, -base_exp);
+                        float y = fmaf(__uint_as_float(s[j + 1]), a.scale_log2, -base_exp);
+                        if (!whole) {
+                            x = bits[k] >> j & 1 ? x : -INFINITY;
+                            y = bits[k] >> (j + 1) & 1 ? y : -INFINITY;
+                        }
+                        x = exp2_fast(x);
+                        y = exp2_fast(y);
+                        sum += x + y;
+                        p[j / 2] = pack2<T>(x, y);
+                    }
+                    tmem_st_32x32b_x16(t_scores + 16 * k, p);
+                }
+                tmem_st_wait();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(rest.p_full[q]));
+            }
+            if (!ok) break;
+            const bool whole = u.part < 0;
+            const int64_t part = whole ? 0 : (int64_t)u.part * a.c.kv_heads + u.head;
+            if (steps > 0) {
+                ok = mbar_wait(bar(rest.o_full[q]), units & 1, a.timeout_ns, a.status);
+                ok = __all_sync(~0u, ok);
+                if (!ok) break;
+                ++units;
+                tc_fence_after_sync();
+                const Odd<DP>& odd = rest.odd[n % kUnits];
+                const bool any = *reinterpret_cast<const volatile int*>(&odd.any) != 0;
+                const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+                const int64_t t = u.token0 + token;
+                uint16_t* to = a.out + t * a.out_row + h * a.out_head;
+                float* part_to = a.partial + ((part * S::kTiles + q) * (DP / 4) * kQueryTile + r) * 4;
+#pragma unroll 1
+                for (int c = 0; c < DP; c += 32) {
+                    uint32_t o[32];
+                    __syncwarp();
+                    tmem_load32(t_out + c, o);
+                    if (any) {
+                        for (int j = 0; j < 32; ++j) {
+                            float& x = reinterpret_cast<float&>(o[j]);
+                            if (odd.first[1][c + j] < limit) x += INFINITY;
+                            if (odd.first[2][c + j] < limit) x -= INFINITY;
+                            if (odd.first[0][c + j] < limit) x += NAN;
+                        }
+                    }
+                    if (!in) {
+                        // not a query
+                    } else if (whole) {
+                        // (a query that sees nothing has its zeros already)
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8) {
+                            if (c + j >= a.c.head_dim || limit == 0) continue;
+                            uint32_t v[4];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                v[x] = pack2<T>(__uint_as_float(o[j + 2 * x]) * inv,
+                                                __uint_as_float(o[j + 2 * x + 1]) * inv);
+                            *reinterpret_cast<uint4*>(to + c + j) = make_uint4(v[0], v[1], v[2], v[3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4)
+                            *reinterpret_cast<uint4*>(part_to + (int64_t)(c + j) * kQueryTile) =
+                                make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                    }
+                }
+            }
+            if (in && whole && limit > 0 && a.lse)
+                a.lse[(u.token0 + token) * a.q_heads + h] =
+                    sum == 0.f ? -INFINITY : (top - kHeadroom + log2f(sum)) * kLn2;
+            if (in && !whole)
+                a.partial_ml[part * S::kRows + q * kQueryTile + r] = make_float2(top - kHeadroom, sum);
+        }
+    } else {
+        // the second tile's warps where there is one: nothing to do
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------
+// The join
+// ---------------------------------------------------------------------------
+// Adds up items' parts; a block takes eight dimensions of a tile's 128 queries at a time.
+template <typename T, int DP>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(ChunkArgs a) {
+    using S = Shape<DP>;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int pieces = a.c.head_dim / 8, r = threadIdx.x;
+    const int64_t work = (int64_t)a.plan->joints * a.c.kv_heads * S::kTiles * pieces;
+    for (int64_t i = blockIdx.x; i < work; i += gridDim.x) {
+        const int piece = (int)(i % pieces), q = (int)(i / pieces % S::kTiles);
+        const int64_t item = i / pieces / S::kTiles;
+        const int head = (int)(item % a.c.kv_heads);
+        const Joint joint = a.joints[item / a.c.kv_heads];
+        const int64_t from = a.offset(joint.row), count = a.offset(joint.row + 1) - from;
+        const int lin = joint.tile * S::kRows + q * kQueryTile + r;
+        if (lin >= count * a.group.value) continue;
+        const int token = a.group.quotient(lin), h = head * a.group.value + lin - token * a.group.value;
+        if (a.length(joint.row) - count + token < 0) continue;  // zeros already
+        const auto part = [&](int p) { return (int64_t)(joint.part + p) * a.c.kv_heads + head; };
+        float top = -INFINITY;
+        for (int p = 0; p < joint.count; ++p)
+            top = fmaxf(top, a.partial_ml[part(p) * S::kRows + q * kQueryTile + r].x);
         const float base = top == -INFINITY ? 0.f : top;
-        const float keep = expf(m - base), w = expf(s - base);
-        m = top;
-        l = l * keep + w;
-#pragma unroll
-        for (int y = 0; y < 8; ++y) o[y] *= keep;
-        for (int i = 0; i < 32; ++i) {
-            const float weight = __shfl_sync(~0u, w, i);
-            const int64_t from = __shfl_sync(~0u, at, i);
-            if (from < 0 || 8 * lane >= dim) continue;
-            const uint4 piece =
-                *reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.v_pool) + from + 8 * lane);
-            const T* v = reinterpret_cast<const T*>(&piece);
-#pragma unroll
-            for (int y = 0; y < 8; ++y) o[y] = fmaf(weight, (float)v[y], o[y]);
+        float sum = 0.f, v[8] = {};
+#pragma unroll 4
+        for (int p = 0; p < joint.count; ++p) {
+            const float2 ml = a.partial_ml[part(p) * S::kRows + q * kQueryTile + r];
+            if (ml.y == 0.f) continue;  // no step, or nothing seen: no output was written, or zeros
+            const float e = exp2_fast(ml.x - base);
+            const float* from_part =
+                a.partial + (((part(p) * S::kTiles + q) * (DP / 4) + 2 * piece) * kQueryTile + r) * 4;
+            const float4 x = *reinterpret_cast<const float4*>(from_part);
+            const float4 y = *reinterpret_cast<const float4*>(from_part + 4 * kQueryTile);
+            sum += e * ml.y;
+            v[0] += e * x.x, v[1] += e * x.y, v[2] += e * x.z, v[3] += e * x.w;
+            v[4] += e * y.x, v[5] += e * y.y, v[6] += e * y.z, v[7] += e * y.w;
         }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const int64_t t = from + token;
+        *reinterpret_cast<uint4*>(a.out + t * a.out_row + h * a.out_head + 8 * piece) =
+            make_uint4(pack2<T>(v[0] * inv, v[1] * inv), pack2<T>(v[2] * inv, v[3] * inv),
+                       pack2<T>(v[4] * inv, v[5] * inv), pack2<T>(v[6] * inv, v[7] * inv));
+        if (a.lse && piece == 0)
+            a.lse[t * a.q_heads + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
     }
-#pragma unroll
-    for (int d = 16; d > 0; d /= 2) l += __shfl_xor_sync(~0u, l, d);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    if (8 * lane < dim) {
-        T* to = reinterpret_cast<T*>(a.out) + t * a.out_row + h * a.out_head + 8 * lane;
-#pragma unroll
-        for (int y = 0; y < 8; ++y) to[y] = (T)(o[y] * inv);
+}
+
+// ---------------------------------------------------------------------------
+// Launches
+// ---------------------------------------------------------------------------
+int padded_dim(int64_t dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
+
+struct Workspace {
+    int64_t slot_count, most_parts;
+    int64_t entries, joints, slots, partial, ml, bytes;
+};
+Workspace plan_workspace(const w4a16_cache_shape& c, int64_t q_heads, int64_t tokens,
+                         const DeviceCtx& ctx) {
+    const int64_t rows = rows_of(c.head_dim), dim = padded_dim(c.head_dim);
+    const int64_t group = q_heads / c.kv_heads;
+    Workspace w;
+    w.slot_count = tokens * group / rows + c.batch;
+    // parts of all heads; items are at most slots, and a part has two steps or more
+    const int64_t steps = (c.table_width * c.page_size + step_of(c.head_dim) - 1) / step_of(c.head_dim);
+    w.most_parts = steps < 2 ? 0
+                             : std::min((int64_t)kPartsPerSm * ctx.num_sms,
+                                        w.slot_count * c.kv_heads * steps);
+    const int64_t parts = w.most_parts / c.kv_heads;  // of one head
+    w.entries = 256;
+    w.joints = w.entries + (w.slot_count + parts) * (int64_t)sizeof(Entry);
+    w.slots = w.joints + (parts + 1) * (int64_t)sizeof(Joint);
+    w.ml = w.slots + w.slot_count * (int64_t)sizeof(Slot);
+    w.partial = (w.ml + w.most_parts * rows * 8 + 255) / 256 * 256;
+    w.bytes = w.partial + w.most_parts * rows * dim * 4;
+    return w;
+}
+
+template <typename T, int DP>
+cudaError_t attend(const ChunkArgs& a, cudaStream_t stream, const DeviceCtx& ctx) {
+    using S = Shape<DP>;
+    static std::once_flag once[64];
+    static cudaError_t set[64];
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    std::call_once(once[device], [&]() {
+        set[device] = cudaFuncSetAttribute(chunk_kernel<T, DP>,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    });
+    if (set[device] != cudaSuccess) return set[device];
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(kPlanThreads);
+    if ((e = cudaLaunchKernelEx(&cfg, plan_kernel, a, S::kRows, S::kStep)) != cudaSuccess) return e;
+    cfg.gridDim = dim3((unsigned)ctx.num_sms);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    if ((e = cudaLaunchKernelEx(&cfg, chunk_kernel<T, DP>, a)) != cudaSuccess) return e;
+    if (a.most_parts == 0) return cudaSuccess;
+    cfg.gridDim = dim3((unsigned)(8 * ctx.num_sms));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, join_kernel<T, DP>, a);
+}
+
+template <typename T>
+cudaError_t attend(const ChunkArgs& a, cudaStream_t stream, const DeviceCtx& ctx) {
+    switch (padded_dim(a.c.head_dim)) {
+        case 64: return attend<T, 64>(a, stream, ctx);
+        case 128: return attend<T, 128>(a, stream, ctx);
+        default: return attend<T, 256>(a, stream, ctx);
     }
-    if (a.lse && lane == 0) a.lse[t * a.q_heads + h] = l == 0.f ? -INFINITY : m + logf(l);
 }
 
 }  // namespace
 
-int64_t paged_chunk_workspace(const w4a16_cache_shape&, int64_t, int64_t, const DeviceCtx&) { return 0; }
+int64_t paged_chunk_workspace(const w4a16_cache_shape& cache, int64_t q_heads, int64_t tokens,
+                              const DeviceCtx& ctx) {
+    return plan_workspace(cache, q_heads, tokens, ctx).bytes;
+}
 
 cudaError_t launch_paged_chunk_attention(const void* q, const void* k_pool, const void* v_pool,
                                          const int32_t* tables, const int32_t* lengths,
-                                         const int32_t* offsets, void* out, float* lse, void*,
-                                         const w4a16_cache_shape& cache,
+                                         const int32_t* offsets, void* out, float* lse,
+                                         void* workspace, const w4a16_cache_shape& cache,
                                          const w4a16_query_shape& query, int64_t tokens,
-                                         cudaStream_t stream, const DeviceCtx&) {
+                                         cudaStream_t stream, const DeviceCtx& ctx) {
     ChunkArgs a;
     a.q = static_cast<const uint16_t*>(q);
     a.k_pool = static_cast<const uint16_t*>(k_pool);
@@ -117,26 +1004,31 @@ cudaError_t launch_paged_chunk_attention(const void* q, const void* k_pool, cons
     a.offsets = offsets;
     a.out = static_cast<uint16_t*>(out);
     a.lse = lse;
+    const Workspace w = plan_workspace(cache, query.q_heads, tokens, ctx);
+    char* base = static_cast<char*>(workspace);
+    a.plan = reinterpret_cast<Plan*>(base);
+    a.entries = reinterpret_cast<Entry*>(base + w.entries);
+    a.joints = reinterpret_cast<Joint*>(base + w.joints);
+    a.slots = reinterpret_cast<Slot*>(base + w.slots);
+    a.partial = reinterpret_cast<float*>(base + w.partial);
+    a.partial_ml = reinterpret_cast<float2*>(base + w.ml);
+    a.slot_count = w.slot_count;
+    a.most_parts = w.most_parts;
     a.tokens = tokens;
     a.q_row = query.q_row_stride;
     a.q_head = query.q_head_stride;
     a.out_row = query.out_row_stride;
     a.out_head = query.out_head_stride;
     a.q_heads = (int)query.q_heads;
-    a.group = (int)(query.q_heads / cache.kv_heads);
-    a.scale = (float)query.scale;
+    a.sms = ctx.num_sms;
+    a.scale_log2 = (float)((query.scale < 0 ? -query.scale : query.scale) * 1.4426950408889634);
+    a.negative = query.scale < 0;
+    a.status = ctx.status;
+    a.timeout_ns = ctx.timeout_ns;
     a.c = cache_of(cache);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((tokens * a.q_heads + kWarps - 1) / kWarps));
-    cfg.blockDim = dim3(32 * kWarps);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cache.type == W4A16_BF16 ? cudaLaunchKernelEx(&cfg, chunk_kernel<__nv_bfloat16>, a)
-                                    : cudaLaunchKernelEx(&cfg, chunk_kernel<__half>, a);
+    a.group = Divisor(query.q_heads / cache.kv_heads);
+    return cache.type == W4A16_BF16 ? attend<__nv_bfloat16>(a, stream, ctx)
+                                    : attend<__half>(a, stream, ctx);
 }
 
 }  // namespace w4a16
