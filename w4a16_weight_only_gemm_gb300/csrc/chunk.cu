@@ -16,6 +16,8 @@
 //                    zeros where a position has no page
 //   warp 12          one thread issues the MMAs
 //   warp 13          takes the next unit of work
+//   warps 14, 15     look for values that are not finite where some queries see a
+//                    step in part
 // The work is cut by a plan kernel, as only the device knows the lengths: items are
 // split into parts where that levels the load, and a join kernel adds those up.
 // Blocks take units from a counter, longest first within a row, the parts of one
@@ -24,6 +26,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 #include <type_traits>
 
@@ -39,7 +42,11 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kQueryTile = 128;   // queries of an MMA
 constexpr int kSoftmaxWarps = 8, kCopyWarps = 4;
 constexpr int kMmaWarp = kSoftmaxWarps + kCopyWarps, kUnitWarp = kMmaWarp + 1;
-constexpr int kThreads = 32 * (kUnitWarp + 1);
+constexpr int kLookWarp = kUnitWarp + 1, kLookWarps = 2;
+constexpr int kThreads = 32 * (kLookWarp + kLookWarps);
+// Registers of a thread: launched with 128, a softmax thread holds a row of scores.  The four
+// warpgroups' shares, 2 x 184 + 2 x 72, are what the block was launched with.
+constexpr int kSoftmaxRegisters = 184, kOtherRegisters = 72;
 constexpr int kSlots = 4;         // of the ring: keys, values, keys, values
 constexpr int kUnits = 4;         // places for units' notes of values that are not finite
 constexpr int kPlanThreads = 1024;
@@ -62,10 +69,10 @@ struct Shape {
 constexpr int rows_of(int64_t dim) { return dim <= 128 ? 256 : 128; }
 constexpr int step_of(int64_t dim) { return dim <= 128 ? 128 : 64; }
 
-// What the plan leaves: `entries` units for each key-value head, `parts` of them parts of
-// `joints` items.
+// What the plan leaves, for each key-value head: `whole` units that are items, then `parts` that
+// are parts of `joints` items.
 struct Plan {
-    int entries, parts, joints;
+    int whole, parts, joints;
     unsigned next;  // unit to hand out
 };
 struct Entry {
@@ -114,32 +121,60 @@ struct ChunkArgs {
 //
 // Item j of row b takes slot offsets[b] group / rows + b + j (rows of an item): as
 // offsets do not descend, no two items share one, and an item's row is found by a
-// search.  Items of n steps are cut into ceil(n / u) parts, with the u out of
-// ceil(longest / 1), ceil(longest / 2), ... that makes the estimated time least: a unit
-// costs its steps and two more (three where it is a part), blocks are level to half
-// a unit, or, where all items are alike, take whole rounds.
+// search.  Some of the items are handed out whole, first; the others, and any longer
+// than a block's share, are cut into ceil(n / u) parts of nearly equal length.  Tried are
+// 32 lengths u, with none whole or as many as make full rounds of the blocks; taken is
+// what makes the estimated time least: a unit costs its steps and two more (three where it
+// is a part), and blocks are level to half a unit.
 // ---------------------------------------------------------------------------
-constexpr int kUnitCost = 2, kCandidates = 256;
+constexpr int kUnitCost = 2, kStaged = 2048;
+
+template <typename V, typename F>
+__device__ __forceinline__ V block_reduce(V v, F f, V* space) {
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) v = f(v, __shfl_xor_sync(~0u, v, d));
+    __syncthreads();
+    if (threadIdx.x % 32 == 0) space[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = space[threadIdx.x % 32];
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) v = f(v, __shfl_xor_sync(~0u, v, d));
+    return v;
+}
+
+__device__ __forceinline__ int parts_of(int steps, int unit, float inverse) {
+    int k = (int)((float)steps * inverse);  // ceil(steps / unit), or one more for very many
+    k += (int64_t)k * unit < steps;
+    k += (int64_t)k * unit < steps;
+    return k;
+}
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a, int rows, int step) {
+    static_assert(kPlanThreads == 1024, "32 warps: one for each length tried");
     __shared__ int64_t sums[32];
-    __shared__ int mins[32], maxs[32];
-    __shared__ float best_cost[kCandidates];
-    __shared__ int chosen;
+    __shared__ int ints[32];
+    __shared__ int32_t staged[kStaged + 1];
+    __shared__ float costs[32];
+    __shared__ int units[32], keeps[32];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     grid_dependency_wait();
     grid_launch_dependents();
-    const int heads = a.c.kv_heads;
+    const int heads = a.c.kv_heads, batch = a.c.batch;
+    const bool short_batch = batch <= kStaged;
+    if (short_batch)
+        for (int b = tid; b <= batch; b += kPlanThreads) staged[b] = (int32_t)a.offset(b);
+    __syncthreads();
+    const auto offset = [&](int b) { return short_batch ? (int64_t)staged[b] : a.offset(b); };
+    const auto key = [&](int b) { return offset(b) * a.group.value / rows + b; };
     int64_t total = 0;
-    int longest = 0, shortest = INT32_MAX;
+    int longest = 0, items = 0;
     for (int64_t s = tid; s < a.slot_count; s += kPlanThreads) {
-        const auto key = [&](int b) { return a.offset(b) * a.group.value / rows + b; };
-        int lo = 0, hi = a.c.batch;  // key(lo) <= s < key(hi)
+        int lo = 0, hi = batch;  // key(lo) <= s < key(hi)
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
             if (key(mid) <= s) lo = mid; else hi = mid;
         }
-        const int64_t from = a.offset(lo), count = max(a.offset(lo + 1) - from, (int64_t)0);
+        const int64_t from = offset(lo), count = max(offset(lo + 1) - from, (int64_t)0);
         const int64_t tile = s - key(lo);
         int steps = 0;
         if (tile >= 0 && tile * rows < count * a.group.value) {
@@ -148,74 +183,82 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a, int row
             steps = seen > 0 ? (int)((seen + step - 1) / step) : 0;
         }
         a.slots[s] = {lo, (int)tile, steps, 0};
-        if (steps) {
-            total += steps;
-            longest = max(longest, steps);
-            shortest = min(shortest, steps);
-        }
+        total += steps;
+        items += steps > 0;
+        longest = max(longest, steps);
     }
-#pragma unroll
-    for (int d = 16; d > 0; d /= 2) {
-        total += __shfl_xor_sync(~0u, total, d);
-        longest = max(longest, __shfl_xor_sync(~0u, longest, d));
-        shortest = min(shortest, __shfl_xor_sync(~0u, shortest, d));
-    }
-    if (lane == 0) sums[warp] = total, maxs[warp] = longest, mins[warp] = shortest;
-    __syncthreads();
-    total = 0;
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
-        total += sums[w];
-        longest = max(longest, maxs[w]);
-        shortest = min(shortest, mins[w]);
-    }
-    total *= heads;
+    const auto add = [](auto x, auto y) { return x + y; };
+    total = block_reduce(total, add, sums) * heads;
+    const int64_t item_count = block_reduce((int64_t)items, add, sums) * heads;
+    longest = block_reduce(longest, [](int x, int y) { return max(x, y); }, ints);
+    // Slots are taken from the last to the first, so that a row's long items come first.  Cut are
+    // those from the `keep`-th on, and those longer than `cap`.
+    const int cap = (int)max(total / a.sms, (int64_t)1);
     int unit = max(longest, 1);
+    int64_t keep = a.slot_count;
     // (an item that is a small part of a block's share is not worth a cut)
-    if ((int64_t)longest * 6 * a.sms > total && a.most_parts > 0) {
-        if (tid < kCandidates) {
-            const int u = (longest + tid) / (tid + 1);
-            float cost = INFINITY;
-            if (tid == 0 || u >= 2) {
-                int64_t units = 0, parts = 0;
-                const float inverse = 1.f / (float)u;
-                for (int64_t s = 0; s < a.slot_count; ++s) {
-                    const int n = a.slots[s].steps;
-                    int k = (int)((float)n * inverse);  // ceil(n / u), or one more for very large n
-                    k += k * (int64_t)u < n;
-                    k += k * (int64_t)u < n;
-                    units += k;
-                    if (k > 1) parts += k;
-                }
-                units *= heads;
-                const float extra = parts ? kUnitCost + 1 : kUnitCost;
-                if (shortest == longest)
-                    cost = (float)((units + a.sms - 1) / a.sms) * ((float)u + extra);
-                else
-                    cost = ((float)total + extra * (float)units) / (float)a.sms + ((float)u + extra) / 2;
-                if (parts * heads > a.most_parts) cost = INFINITY;
+    if ((int64_t)longest * 8 * a.sms > total && a.most_parts > 0) {
+        // k = 1, 2, 3, ... 8, then some 2^(1/4) apart up to 512
+        const int k = warp < 8 ? warp + 1 : (int)(8.f * exp2f((float)(warp - 7) * 0.25f));
+        const int u = (longest + k - 1) / k;
+        const float inverse = 1.f / (float)u;
+        float best = INFINITY;
+        int64_t best_keep = 0;
+        for (int rounds = 0; rounds < 2; ++rounds) {
+            const int64_t kept = rounds ? item_count / a.sms * a.sms / heads : 0;
+            if (rounds && kept == 0) break;
+            int64_t whole = 0, whole_steps = 0, parts = 0;
+            for (int64_t r = lane; r < a.slot_count; r += 32) {
+                const int n = a.slots[a.slot_count - 1 - r].steps;
+                const int p = r >= kept || n > cap ? parts_of(n, u, inverse) : n > 0;
+                if (p > 1) parts += p;
+                if (p == 1) ++whole, whole_steps += n;
             }
-            best_cost[tid] = cost;
+#pragma unroll
+            for (int d = 16; d > 0; d /= 2) {
+                whole += __shfl_xor_sync(~0u, whole, d);
+                whole_steps += __shfl_xor_sync(~0u, whole_steps, d);
+                parts += __shfl_xor_sync(~0u, parts, d);
+            }
+            const float sms = (float)a.sms;
+            const float work = (float)total + (float)(kUnitCost * (whole + parts) * heads + parts * heads);
+            float cost = work / sms + (float)(u + kUnitCost) / 2;
+            if (whole) {  // rounds of whole items
+                const float mean = (float)whole_steps / (float)whole + kUnitCost;
+                cost = fmaxf(cost, (float)((whole * heads + a.sms - 1) / a.sms) * mean);
+            }
+            if (parts) cost += 2.f;  // the join
+            if (parts * heads <= a.most_parts && cost < best) best = cost, best_keep = kept;
         }
+        if (lane == 0) costs[warp] = best, units[warp] = u, keeps[warp] = (int)best_keep;
         __syncthreads();
-        if (tid == 0) {
-            int best = 0;
-            for (int i = 1; i < kCandidates; ++i)
-                if (best_cost[i] < best_cost[best]) best = i;
-            chosen = (longest + best) / (best + 1);
+        float least = costs[lane];
+        int which = lane;
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) {
+            const float o = __shfl_xor_sync(~0u, least, d);
+            const int w = __shfl_xor_sync(~0u, which, d);
+            if (o < least || (o == least && w < which)) least = o, which = w;
         }
-        __syncthreads();
-        unit = chosen;
+        if (least < INFINITY) unit = units[which], keep = keeps[which];
     }
-    // Entries, from the last slot to the first.
-    int64_t base_units = 0, base_parts = 0;
+    const auto cut = [&](int64_t r, int n) {
+        return n == 0 ? 0 : r >= keep || n > cap ? (n + unit - 1) / unit : 1;
+    };
+    // How many there are whole; then the entries.
+    int64_t whole = 0;
+    for (int64_t r = tid; r < a.slot_count; r += kPlanThreads)
+        whole += cut(r, a.slots[a.slot_count - 1 - r].steps) == 1;
+    whole = block_reduce(whole, add, sums);
+    int64_t base_whole = 0, base_parts = 0;
     int base_joints = 0;
     for (int64_t first = 0; first < a.slot_count; first += kPlanThreads) {
-        const int64_t s = a.slot_count - 1 - first - tid;
+        const int64_t r = first + tid;
         Slot slot = {};
-        if (s >= 0) slot = a.slots[s];
-        const int k = slot.steps ? (slot.steps + unit - 1) / unit : 0;
-        // units in the low half, parts in the high one
-        int64_t both = k + ((int64_t)(k > 1 ? k : 0) << 32), upto = both;
+        if (r < a.slot_count) slot = a.slots[a.slot_count - 1 - r];
+        const int k = cut(r, slot.steps);
+        // whole ones in the low half, parts in the high one
+        int64_t both = (k == 1) + ((int64_t)(k > 1 ? k : 0) << 32), upto = both;
         int joint = k > 1, joint_upto = joint;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
@@ -224,27 +267,33 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a, int row
             if (lane >= d) upto += o, joint_upto += j;
         }
         __syncthreads();
-        if (lane == 31) sums[warp] = upto, maxs[warp] = joint_upto;
+        if (lane == 31) sums[warp] = upto, ints[warp] = joint_upto;
         __syncthreads();
-        int64_t all = 0;
-        int all_joints = 0;
-        for (int w = 0; w < kPlanThreads / 32; ++w) {
-            if (w == warp) upto += all, joint_upto += all_joints;
-            all += sums[w];
-            all_joints += maxs[w];
+        int64_t all = sums[lane], before = lane < warp ? all : 0;
+        int all_joints = ints[lane], before_joints = lane < warp ? all_joints : 0;
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) {
+            all += __shfl_xor_sync(~0u, all, d);
+            before += __shfl_xor_sync(~0u, before, d);
+            all_joints += __shfl_xor_sync(~0u, all_joints, d);
+            before_joints += __shfl_xor_sync(~0u, before_joints, d);
         }
-        const int64_t at = base_units + (uint32_t)(upto - both);
-        const int64_t part = base_parts + ((upto - both) >> 32);
-        if (k > 1) a.joints[base_joints + joint_upto - joint] = {slot.row, slot.tile, (int)part, k};
-        for (int i = 0; i < k; ++i) {
-            const int from = (int)((int64_t)slot.steps * i / k), to = (int)((int64_t)slot.steps * (i + 1) / k);
-            a.entries[at + i] = {slot.row, slot.tile, from, to - from, k > 1 ? (int)(part + i) : -1, {}};
+        upto += before - both;
+        joint_upto += before_joints - joint;
+        if (k == 1) a.entries[base_whole + (uint32_t)upto] = {slot.row, slot.tile, 0, slot.steps, -1, {}};
+        if (k > 1) {
+            const int64_t part = base_parts + (upto >> 32);
+            a.joints[base_joints + joint_upto] = {slot.row, slot.tile, (int)part, k};
+            for (int i = 0; i < k; ++i) {
+                const int from = (int)((int64_t)slot.steps * i / k), to = (int)((int64_t)slot.steps * (i + 1) / k);
+                a.entries[whole + part + i] = {slot.row, slot.tile, from, to - from, (int)(part + i), {}};
+            }
         }
-        base_units += (uint32_t)all;
+        base_whole += (uint32_t)all;
         base_parts += all >> 32;
         base_joints += all_joints;
     }
-    if (tid == 0) *a.plan = {(int)base_units, (int)base_parts, base_joints, 0};
+    if (tid == 0) *a.plan = {(int)base_whole, (int)base_parts, base_joints, 0};
 }
 
 // ---------------------------------------------------------------------------
@@ -259,6 +308,10 @@ __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_gr
 template <int N>
 __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// An arrival once every copy of this thread so far has landed.
+__device__ __forceinline__ void copy_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -278,6 +331,13 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     }
 }
 
+__device__ __forceinline__ void registers_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegisters));
+}
+__device__ __forceinline__ void registers_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegisters));
+}
+
 // D[tmem] (+)= A[tmem] * B[smem desc], 16-bit inputs, f32 accumulate.
 __device__ __forceinline__ void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
                                               uint32_t idesc, uint32_t accumulate) {
@@ -289,22 +349,41 @@ __device__ __forceinline__ void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, 
         : "memory");
 }
 
-// tcgen05.ld of 32 columns, and the wait for it (one statement: nothing may use r in between).
-__device__ __forceinline__ void tmem_load32(uint32_t taddr, uint32_t (&r)[32]) {
+// tcgen05.ld, and the wait for it (one statement: nothing may use r in between).
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31 "
+        "}, [%32];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr)
         : "memory");
 }
-
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[64]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63 "
+        "}, [%64];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(taddr)
+        : "memory");
+}
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -348,9 +427,9 @@ struct Unit {
     int64_t length;        // positions of the row
 };
 
-// Values that are not finite, in steps that some of the item's queries do not see whole: the
-// first position of each dimension with NaN, +infinity and -infinity.  They enter the products
-// as zeros, so that queries before them are left alone.
+// Values that are not finite, in steps that some of the item's queries see in part: the first
+// position of each dimension with NaN, +infinity and -infinity.  They enter the products as
+// zeros, so that queries before them are left alone.
 template <int DP>
 struct Odd {
     int any;
@@ -360,19 +439,12 @@ struct Odd {
 template <int DP>
 struct Rest {
     uint64_t unit_full[2], unit_free[2], q_full, q_free;
-    uint64_t kv_full[kSlots], kv_free[kSlots], s_full[2], p_full[2], o_full[2], done;
+    uint64_t kv_full[kSlots], kv_free[kSlots], looked[kSlots];
+    uint64_t s_full[2], p_full[2][2], o_full[2], done;
     uint32_t tmem;
     uint32_t valid[4][4];  // of a step, a bit a position (step / 4 a word)
     Unit unit[2];
     Odd<DP> odd[kUnits];
-};
-
-// A group of copies on its way: where to report it, and whether its values are to be looked at.
-struct Group {
-    uint32_t bar;    // 0: none
-    uint32_t slot;   // of values to be looked at, 0: not
-    int position;
-    int unit;
 };
 
 template <typename T, int DP>
@@ -393,16 +465,19 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(rest.unit_full[i]), 1);
-            mbar_init(bar(rest.unit_free[i]), 4 * S::kTiles + kCopyWarps + 1);
+            mbar_init(bar(rest.unit_free[i]), 4 * S::kTiles + kCopyWarps + 1 + kLookWarps);
             mbar_init(bar(rest.s_full[i]), 2);
-            mbar_init(bar(rest.p_full[i]), 4);
+            mbar_init(bar(rest.p_full[i][0]), 4);
+            mbar_init(bar(rest.p_full[i][1]), 4);
             mbar_init(bar(rest.o_full[i]), 2);
         }
-        mbar_init(bar(rest.q_full), kCopyWarps);
+        mbar_init(bar(rest.q_full), 32 * kCopyWarps);
         mbar_init(bar(rest.q_free), 1);
         for (int i = 0; i < kSlots; ++i) {
-            mbar_init(bar(rest.kv_full[i]), kCopyWarps);
-            mbar_init(bar(rest.kv_free[i]), 1);
+            // every copying thread's copies, and an arrival of each warp for what it wrote itself
+            mbar_init(bar(rest.kv_full[i]), 33 * kCopyWarps);
+            mbar_init(bar(rest.kv_free[i]), i % 2 ? 1 + kLookWarps : 1);  // values: also the lookers'
+            mbar_init(bar(rest.looked[i]), kLookWarps);
         }
         mbar_init(bar(rest.done), 1);
         fence_barrier_init();
@@ -437,124 +512,204 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         const int64_t steps = seen > 0 ? (seen + S::kStep - 1) / S::kStep : 0;
         return (int)min(max(steps - u.first, (int64_t)0), (int64_t)u.steps);
     };
+    // The first step of a unit that some of its queries do not see whole.
+    const auto part_seen_from = [&](const Unit& u) {
+        const int64_t all = max(u.position0 + a.group.quotient(u.lin0) + 1, (int64_t)0);
+        return (int)min(max(all / S::kStep - u.first, (int64_t)0), (int64_t)u.steps);
+    };
 
-    if (warp == kUnitWarp) {
-        // =============================== units ================================
-        const unsigned total = (unsigned)a.plan->entries * (unsigned)a.c.kv_heads;
-        const unsigned entries = (unsigned)a.plan->entries;
-        for (uint32_t n = 0;; ++n) {
-            unsigned i = 0;
-            if (lane == 0) i = atomicAdd(&a.plan->next, 1u);
-            i = __shfl_sync(~0u, i, 0);
-            Unit u = {};
-            u.steps = -1;
-            if (i < total) {
-                const Entry e = a.entries[i % entries];
-                const int64_t from = a.offset(e.row), count = a.offset(e.row + 1) - from;
-                u.row = e.row;
-                u.head = (int)(i / entries);
-                u.first = e.first;
-                u.steps = e.steps;
-                u.part = e.part;
-                u.lin0 = e.tile * S::kRows;
-                u.lins = (int)min((int64_t)S::kRows, count * group - u.lin0);
-                u.token0 = from;
-                u.length = a.length(e.row);
-                u.position0 = u.length - count;
+    if (warp >= kMmaWarp) {
+        registers_down();
+        if (warp == kUnitWarp) {
+            // ============================== units ===============================
+            const unsigned whole = (unsigned)a.plan->whole, parts = (unsigned)a.plan->parts;
+            const unsigned heads = (unsigned)a.c.kv_heads;
+            for (uint32_t n = 0;; ++n) {
+                unsigned i = 0;
+                if (lane == 0) i = atomicAdd(&a.plan->next, 1u);
+                i = __shfl_sync(~0u, i, 0);
+                Unit u = {};
+                u.steps = -1;
+                if (i < (whole + parts) * heads) {
+                    unsigned e;
+                    if (i < whole * heads) {
+                        u.head = (int)(i / whole);
+                        e = i % whole;
+                    } else {
+                        u.head = (int)((i - whole * heads) / parts);
+                        e = whole + (i - whole * heads) % parts;
+                    }
+                    const Entry entry = a.entries[e];
+                    const int64_t from = a.offset(entry.row), count = a.offset(entry.row + 1) - from;
+                    u.row = entry.row;
+                    u.first = entry.first;
+                    u.steps = entry.steps;
+                    u.part = entry.part;
+                    u.lin0 = entry.tile * S::kRows;
+                    u.lins = (int)min((int64_t)S::kRows, count * group - u.lin0);
+                    u.token0 = from;
+                    u.length = a.length(entry.row);
+                    u.position0 = u.length - count;
+                }
+                const bool ok = n < 2 || mbar_wait(bar(rest.unit_free[n % 2]), (n / 2 - 1) % 2,
+                                                   a.timeout_ns, a.status);
+                if (!__all_sync(~0u, ok)) break;
+                Odd<DP>& odd = rest.odd[n % kUnits];
+                for (int x = lane; x < 3 * DP; x += 32) (&odd.first[0][0])[x] = INT32_MAX;
+                if (lane == 0) {
+                    odd.any = 0;
+                    rest.unit[n % 2] = u;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(rest.unit_full[n % 2]));
+                if (u.steps < 0) break;
             }
-            bool ok = n < 2 || mbar_wait(bar(rest.unit_free[n % 2]), (n / 2 - 1) % 2, a.timeout_ns,
-                                         a.status);
-            if (!__all_sync(~0u, ok)) break;
-            Odd<DP>& odd = rest.odd[n % kUnits];
-            for (int x = lane; x < 3 * DP; x += 32) (&odd.first[0][0])[x] = INT32_MAX;
-            if (lane == 0) {
-                odd.any = 0;
-                rest.unit[n % 2] = u;
+        } else if (warp == kMmaWarp) {
+            // =============================== MMAs ===============================
+            constexpr uint32_t kType = kHalf ? 0u : (1u << 7) | (1u << 10);
+            const uint32_t scores = umma_idesc_f16_f32(kQueryTile, S::kStep) | kType |
+                                    (a.negative ? 1u << 13 : 0u);  // (minus the queries)
+            const uint32_t values = umma_idesc_f16_f32(kQueryTile, DP) | kType | (1u << 16);  // V: MN-major
+            uint32_t step = 0;           // of the block, for the ring's slots
+            uint32_t taken[2] = {0, 0};  // steps of each tile
+            uint32_t looks[2] = {0, 0};  // at each slot of values
+            Unit u;
+            bool ok = true;
+            for (uint32_t n = 0; ok && next_unit(n, u); ++n) {
+                if (lane == 0) {
+                    const int steps[2] = {steps_of(u, 0), S::kTiles == 2 ? steps_of(u, 1) : 0};
+                    const int looked_from = part_seen_from(u);
+                    const auto wait = [&](uint64_t& b, uint32_t phase) {
+                        if (ok) ok = mbar_wait(bar(b), phase & 1, a.timeout_ns, a.status);
+                    };
+                    // Reports the MMAs issued so far, and passes on (by an arrival of this thread)
+                    // what the copying warps wrote.
+                    const auto finished = [&](uint64_t& b) {
+                        tc_commit(bar(b));
+                        mbar_arrive(bar(b));
+                    };
+                    const auto score = [&](int q, uint32_t slot) {
+                        const uint32_t qa = base + q * S::kTileBytes;
+                        const uint32_t ka = base + S::kOffRing + slot * S::kSlotBytes;
+#pragma unroll
+                        for (int j = 0; j < DP / 16; ++j)
+                            tc_mma_f16(tmem + q * 128,
+                                       umma_desc_sw128(qa + j / 4 * (kQueryTile * 128) + j % 4 * 32),
+                                       umma_desc_sw128(ka + j / 4 * (S::kStep * 128) + j % 4 * 32), scores,
+                                       j != 0);
+                        finished(rest.s_full[q]);
+                    };
+                    wait(rest.q_full, n);
+                    wait(rest.kv_full[2 * step % kSlots], 2 * step / kSlots);
+                    if (ok) {
+                        fence_proxy_async_smem();
+                        for (int q = 0; q < S::kTiles; ++q)
+                            if (steps[q] > 0) score(q, 2 * step % kSlots);
+                        tc_commit(bar(rest.kv_free[2 * step % kSlots]));
+                        if (u.steps == 1) tc_commit(bar(rest.q_free));
+                    }
+                    for (int i = 0; ok && i < u.steps; ++i, ++step) {
+                        const uint32_t v = 2 * step + 1, k = 2 * step + 2;
+                        if (i < looked_from)
+                            wait(rest.kv_full[v % kSlots], v / kSlots);
+                        else
+                            wait(rest.looked[v % kSlots], looks[v % kSlots / 2]++);
+                        if (i + 1 < u.steps) wait(rest.kv_full[k % kSlots], k / kSlots);
+                        fence_proxy_async_smem();
+                        for (int q = 0; q < S::kTiles; ++q) {
+                            if (i >= steps[q]) continue;
+                            const uint32_t va = base + S::kOffRing + v % kSlots * S::kSlotBytes;
+                            // the first half of the weights, while the second is still made
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                wait(rest.p_full[q][half], taken[q]);
+                                if (!ok) break;
+                                tc_fence_after_sync();
+#pragma unroll
+                                for (int j = half * S::kStep / 32; j < (half + 1) * S::kStep / 32; ++j)
+                                    tc_mma_f16_ta(tmem + S::kOutColumn + q * DP, tmem + q * 128 + 8 * j,
+                                                  umma_desc_mn_sw128(va + j * 2048, S::kStep * 128), values,
+                                                  (i | j) != 0);
+                            }
+                            if (!ok) break;
+                            ++taken[q];
+                            if (i + 1 < steps[q])
+                                score(q, k % kSlots);
+                            else
+                                finished(rest.o_full[q]);
+                        }
+                        if (!ok) break;
+                        tc_commit(bar(rest.kv_free[v % kSlots]));
+                        if (i + 1 < u.steps) tc_commit(bar(rest.kv_free[k % kSlots]));
+                        if (i + 2 == u.steps) tc_commit(bar(rest.q_free));
+                    }
+                }
+                ok = __shfl_sync(~0u, ok, 0);
+            }
+            if (lane == 0) {  // nothing in flight when the block ends
+                tc_commit(bar(rest.done));
+                mbar_wait(bar(rest.done), 0, drain_bound(a.timeout_ns), a.status);
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(rest.unit_full[n % 2]));
-            if (u.steps < 0) break;
-        }
-    } else if (warp == kMmaWarp) {
-        // ================================ MMAs ================================
-        constexpr uint32_t kType = kHalf ? 0u : (1u << 7) | (1u << 10);
-        const uint32_t scores = umma_idesc_f16_f32(kQueryTile, S::kStep) | kType |
-                                (a.negative ? 1u << 13 : 0u);  // (minus the queries)
-        const uint32_t values = umma_idesc_f16_f32(kQueryTile, DP) | kType | (1u << 16);  // V: MN-major
-        uint32_t step = 0;  // of the block, for the ring's slots
-        uint32_t taken[2] = {0, 0};  // steps of each tile
-        Unit u;
-        bool ok = true;
-        for (uint32_t n = 0; ok && next_unit(n, u); ++n) {
-            if (lane == 0) {
-                const int steps[2] = {steps_of(u, 0), S::kTiles == 2 ? steps_of(u, 1) : 0};
-                const auto wait = [&](uint64_t& b, uint32_t phase) {
-                    if (ok) ok = mbar_wait(bar(b), phase & 1, a.timeout_ns, a.status);
-                    tc_fence_after_sync();
-                };
-                // Reports the MMAs issued so far, and passes on (by an arrival of this thread) what
-                // the copying warps wrote.
-                const auto finished = [&](uint64_t& b) {
-                    tc_commit(bar(b));
-                    mbar_arrive(bar(b));
-                };
-                const auto score = [&](int q, uint32_t slot) {
-                    const uint32_t qa = base + q * S::kTileBytes;
-                    const uint32_t ka = base + S::kOffRing + slot * S::kSlotBytes;
-#pragma unroll
-                    for (int j = 0; j < DP / 16; ++j)
-                        tc_mma_f16(tmem + q * 128,
-                                   umma_desc_sw128(qa + j / 4 * (kQueryTile * 128) + j % 4 * 32),
-                                   umma_desc_sw128(ka + j / 4 * (S::kStep * 128) + j % 4 * 32), scores,
-                                   j != 0);
-                    finished(rest.s_full[q]);
-                };
-                wait(rest.q_full, n);
-                wait(rest.kv_full[2 * step % kSlots], 2 * step / kSlots);
-                if (ok) {
-                    for (int q = 0; q < S::kTiles; ++q)
-                        if (steps[q] > 0) score(q, 2 * step % kSlots);
-                    tc_commit(bar(rest.kv_free[2 * step % kSlots]));
-                    if (u.steps == 1) tc_commit(bar(rest.q_free));
-                }
-                for (int i = 0; ok && i < u.steps; ++i, ++step) {
-                    const uint32_t v = 2 * step + 1, k = 2 * step + 2;
-                    wait(rest.kv_full[v % kSlots], v / kSlots);
-                    if (i + 1 < u.steps) wait(rest.kv_full[k % kSlots], k / kSlots);
-                    for (int q = 0; q < S::kTiles; ++q) {
-                        if (i >= steps[q]) continue;
-                        wait(rest.p_full[q], taken[q]++);
-                        if (!ok) break;
-                        const uint32_t va = base + S::kOffRing + v % kSlots * S::kSlotBytes;
-#pragma unroll
-                        for (int j = 0; j < S::kStep / 16; ++j)
-                            tc_mma_f16_ta(tmem + S::kOutColumn + q * DP, tmem + q * 128 + 8 * j,
-                                          umma_desc_mn_sw128(va + j * 2048, S::kStep * 128), values,
-                                          (i | j) != 0);
-                        if (i + 1 < steps[q])
-                            score(q, k % kSlots);
-                        else
-                            finished(rest.o_full[q]);
-                    }
+        } else {
+            // ============================== looking =============================
+            constexpr uint32_t kExponent = kHalf ? 0x7C00u : 0x7F80u;
+            uint32_t step = 0;
+            Unit u;
+            bool ok = true;
+            for (uint32_t n = 0; ok && next_unit(n, u); ++n) {
+                Odd<DP>& odd = rest.odd[n % kUnits];
+                const int looked_from = part_seen_from(u);
+                for (int i = 0; i < u.steps; ++i, ++step) {
+                    // (every step's, so that the barriers' phases are followed one by one)
+                    const uint32_t v = 2 * step + 1, slot = v % kSlots;
+                    ok = mbar_wait(bar(rest.kv_full[slot]), v / kSlots & 1, a.timeout_ns, a.status);
+                    ok = __all_sync(~0u, ok);
                     if (!ok) break;
-                    tc_commit(bar(rest.kv_free[v % kSlots]));
-                    if (i + 1 < u.steps) tc_commit(bar(rest.kv_free[k % kSlots]));
-                    if (i + 2 == u.steps) tc_commit(bar(rest.q_free));
+                    if (i < looked_from) {
+                        if (lane == 0) mbar_arrive(bar(rest.kv_free[slot]));
+                        continue;
+                    }
+                    const uint32_t from = base + S::kOffRing + slot * S::kSlotBytes;
+#pragma unroll 4
+                    for (int x = (warp - kLookWarp) * 32 + lane; x < S::kSlotBytes / 16;
+                         x += 32 * kLookWarps) {
+                        uint4 piece = lds128(from + 16 * x);
+                        uint32_t* words = reinterpret_cast<uint32_t*>(&piece);
+                        bool bad = false;
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            bad = bad || (words[y] & kExponent) == kExponent ||
+                                  (words[y] & kExponent << 16) == kExponent << 16;
+                        if (!bad) continue;
+                        const int row = x / 8 % S::kStep, dim = (x / 8 / S::kStep * 8 + (x % 8 ^ row % 8)) * 8;
+                        for (int y = 0; y < 8; ++y) {
+                            const uint32_t one = words[y / 2] >> (16 * (y % 2)) & 0xFFFFu;
+                            if ((one & kExponent) != kExponent) continue;
+                            const int kind = (one & (kExponent ^ 0x7FFFu)) ? 0 : one >> 15 ? 2 : 1;
+                            atomicMin(&odd.first[kind][dim + y], (u.first + i) * S::kStep + row);
+                            words[y / 2] &= y % 2 ? 0xFFFFu : 0xFFFF0000u;
+                        }
+                        odd.any = 1;
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(from + 16 * x),
+                                     "r"(piece.x), "r"(piece.y), "r"(piece.z), "r"(piece.w)
+                                     : "memory");
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bar(rest.looked[slot]));
+                        mbar_arrive(bar(rest.kv_free[slot]));
+                    }
                 }
             }
-            ok = __shfl_sync(~0u, ok, 0);
         }
-        if (lane == 0) {  // nothing in flight when the block ends
-            tc_commit(bar(rest.done));
-            mbar_wait(bar(rest.done), 0, drain_bound(a.timeout_ns), a.status);
-        }
-        __syncwarp();
     } else if (warp >= kSoftmaxWarps) {
         // =============================== copies ===============================
+        registers_down();
         constexpr int kPieces = DP / 8;              // of a row, 16 bytes each
-        constexpr int kPasses = kPieces < 32 ? 1 : kPieces / 32;
         constexpr int kRowsPass = kPieces < 32 ? 32 / kPieces : 1;
-        static_assert(kPasses == 1, "a pass of a warp is whole rows");
+        static_assert(kPieces <= 32, "a pass of a warp is whole rows");
         constexpr int kRowsWarp = S::kStep / kCopyWarps;
         const int w = warp - kSoftmaxWarps, piece = lane % kPieces, row0 = lane / kPieces;
         const bool in_dim = piece * 8 < a.c.head_dim;
@@ -562,48 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         const auto at = [&](int row, int rows) {
             return (uint32_t)(piece / 8 * rows * 128 + row * 128 + ((piece % 8 ^ row % 8) << 4));
         };
-        Group pending[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-        // The oldest group has landed: look through its values, if need be, and report it.
-        const auto report = [&](const Group& g) {
-            if (g.bar == 0) return;
-            if (g.slot) {
-                Odd<DP>& odd = rest.odd[g.unit % kUnits];
-                for (int r = row0; r < kRowsWarp; r += kRowsPass) {
-                    const int row = w * kRowsWarp + r;
-                    const uint32_t where = g.slot + at(row, S::kStep);
-                    uint4 v = lds128(where);
-                    uint32_t* words = reinterpret_cast<uint32_t*>(&v);
-                    constexpr uint32_t kExponent = kHalf ? 0x7C00u : 0x7F80u;
-                    bool bad = false;
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        bad = bad || (words[x] & kExponent) == kExponent ||
-                              (words[x] & kExponent << 16) == kExponent << 16;
-                    if (!bad) continue;
-                    for (int x = 0; x < 8; ++x) {
-                        const uint32_t one = words[x / 2] >> (16 * (x % 2)) & 0xFFFFu;
-                        if ((one & kExponent) != kExponent) continue;
-                        const int kind = (one & (kExponent ^ 0x7FFFu)) ? 0 : one >> 15 ? 2 : 1;
-                        atomicMin(&odd.first[kind][piece * 8 + x], g.position + row);
-                        words[x / 2] &= x % 2 ? 0xFFFFu : 0xFFFF0000u;
-                    }
-                    odd.any = 1;
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(where), "r"(v.x),
-                                 "r"(v.y), "r"(v.z), "r"(v.w)
-                                 : "memory");
-                }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(g.bar);
-        };
-        const auto issued = [&](const Group& g) {
-            copy_commit();
-            copy_wait<2>();
-            report(pending[0]);
-            pending[0] = pending[1];
-            pending[1] = g;
-        };
+        const bool whole_pages = a.c.page_size.value % 16 == 0;
         uint32_t step = 0;
         Unit u;
         bool ok = true;
@@ -619,24 +733,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 return p < u.length ? table[a.c.page_size.quotient((int)p)] : -1;
             };
             int next = page_of(0);
-            // positions that every query of the item sees
-            const int64_t all_see = u.position0 + a.group.quotient(u.lin0) + 1;
-            if (n > 0) wait(rest.q_free, n - 1);
-            if (!ok) break;
-            const uint16_t* q0 = a.q + u.token0 * a.q_row + (int64_t)u.head * group * a.q_head;
-            for (int r = w * (S::kRows / kCopyWarps) + row0; r < (w + 1) * (S::kRows / kCopyWarps);
-                 r += kRowsPass) {
-                const bool in = r < u.lins && in_dim;
-                const int token = a.group.quotient(u.lin0 + r), h = u.lin0 + r - token * group;
-                copy16(base + r / kQueryTile * S::kTileBytes + at(r % kQueryTile, kQueryTile),
-                       in ? q0 + token * a.q_row + h * a.q_head + 8 * piece : a.q, in);
-            }
-            issued({bar(rest.q_full), 0, 0, 0});
             for (int i = 0; i < u.steps; ++i, ++step) {
-                const int position = (u.first + i) * S::kStep;
                 int64_t place = -1;
                 if ((uint32_t)next < (uint32_t)a.c.pages) {
-                    const int p = position + w * kRowsWarp + lane % kRowsWarp;
+                    const int p = (u.first + i) * S::kStep + w * kRowsWarp + lane % kRowsWarp;
                     place = next * a.c.page_stride + a.c.page_size.remainder(p) * a.c.slot_stride + head;
                 }
                 const uint32_t there = __ballot_sync(~0u, place >= 0);
@@ -651,27 +751,51 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                             kRowsWarp == 32 ? there : there & ((1u << kRowsWarp % 32) - 1);
                     const uint32_t to = base + S::kOffRing + slot * S::kSlotBytes;
                     const uint16_t* pool = (value ? a.v_pool : a.k_pool) + 8 * piece;
+                    if (whole_pages && there == ~0u) {
+                        // sixteen rows at a time lie in one page
+                        const int64_t next_rows = kRowsPass * a.c.slot_stride;
 #pragma unroll
-                    for (int r = 0; r < kRowsWarp; r += kRowsPass) {
-                        const int64_t o = __shfl_sync(~0u, place, r + row0);
-                        const bool in = o >= 0 && in_dim;
-                        copy16(to + at(w * kRowsWarp + r + row0, S::kStep), in ? pool + o : a.k_pool, in);
+                        for (int r = 0; r < kRowsWarp; r += 16) {
+                            const uint16_t* from =
+                                pool + __shfl_sync(~0u, place, r) + row0 * a.c.slot_stride;
+#pragma unroll
+                            for (int x = 0; x < 16; x += kRowsPass, from += next_rows)
+                                copy16(to + at(w * kRowsWarp + r + x + row0, S::kStep), from, in_dim);
+                        }
+                    } else {
+#pragma unroll 4
+                        for (int r = 0; r < kRowsWarp; r += kRowsPass) {
+                            const int64_t o = __shfl_sync(~0u, place, r + row0);
+                            const bool in = o >= 0 && in_dim;
+                            copy16(to + at(w * kRowsWarp + r + row0, S::kStep), in ? pool + o : a.k_pool,
+                                   in);
+                        }
                     }
-                    const bool look = value && (int64_t)position + S::kStep > all_see;
-                    issued({bar(rest.kv_full[slot]), look ? to : 0u, position, (int)n});
+                    copy_arrive(bar(rest.kv_full[slot]));
+                    if (lane == 0) mbar_arrive(bar(rest.kv_full[slot]));
+                    if (value || i) continue;
+                    // the queries, behind the first keys: theirs is the longer wait
+                    if (n > 0) wait(rest.q_free, n - 1);
+                    if (!ok) break;
+                    const uint16_t* q0 = a.q + u.token0 * a.q_row + (int64_t)u.head * group * a.q_head;
+#pragma unroll 4
+                    for (int r = w * (S::kRows / kCopyWarps) + row0; r < (w + 1) * (S::kRows / kCopyWarps);
+                         r += kRowsPass) {
+                        const bool in = r < u.lins && in_dim;
+                        const int token = a.group.quotient(u.lin0 + r), h = u.lin0 + r - token * group;
+                        copy16(base + r / kQueryTile * S::kTileBytes + at(r % kQueryTile, kQueryTile),
+                               in ? q0 + token * a.q_row + h * a.q_head + 8 * piece : a.q, in);
+                    }
+                    copy_arrive(bar(rest.q_full));
                 }
                 if (!ok) break;
             }
-            copy_wait<0>();
-            if (ok) {
-                report(pending[0]);
-                report(pending[1]);
-            }
-            pending[0].bar = pending[1].bar = 0;
         }
+        copy_commit();
         copy_wait<0>();
     } else if (warp < 4 * S::kTiles) {
         // ============================== softmax ===============================
+        registers_up();
         const int q = warp / 4, r = warp % 4 * 32 + lane;
         const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
         const uint32_t t_scores = tmem + lanes + q * 128;
@@ -704,6 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         uint32_t taken = 0, units = 0, step0 = 0;  // steps and units of this tile, steps of the block
         Unit u;
         bool ok = true;
+        const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
         for (uint32_t n = 0; ok && next_unit(n, u); step0 += u.steps, ++n) {
             const int steps = steps_of(u, q);
             const int lin = u.lin0 + q * kQueryTile + r;
@@ -712,7 +837,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             // positions that the query sees; all, for a row that is not there
             const int64_t limit = in ? max(u.position0 + token + 1, (int64_t)0) : INT32_MAX;
             const int least = __reduce_min_sync(~0u, (int)limit);
-            float top = -INFINITY, sum = 0.f;
+            float top = -INFINITY;
+            float2 sum2 = make_float2(0.f, 0.f);
 #pragma unroll 1
             for (int i = 0; i < steps; ++i) {
                 ok = mbar_wait(bar(rest.s_full[q]), taken & 1, a.timeout_ns, a.status);
@@ -720,81 +846,87 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 if (!ok) break;
                 ++taken;
                 tc_fence_after_sync();
-                const int position = (u.first + i) * S::kStep;
-                // a bit a position of the step that counts
-                uint32_t bits[S::kStep / 32];
-                bool whole = (int64_t)position + S::kStep <= least;
-#pragma unroll
-                for (int k = 0; k < S::kStep / 32; ++k) {
+                const int64_t position = (int64_t)(u.first + i) * S::kStep;
+                {
+                    // Scores that do not count become -infinity, in tensor memory.
                     const uint32_t* v = rest.valid[(step0 + i) % 4];
-                    bits[k] = S::kStep == 128 ? v[k] : v[2 * k] | v[2 * k + 1] << 16;
-                    whole = whole && bits[k] == ~0u;
-                }
-                if (!whole) {
-                    const int left = (int)min(max(limit - position, (int64_t)0), (int64_t)S::kStep);
+                    bool whole = position + S::kStep <= least;
 #pragma unroll
-                    for (int k = 0; k < S::kStep / 32; ++k)
-                        bits[k] &= left >= 32 * k + 32 ? ~0u : left <= 32 * k ? 0u : (1u << (left - 32 * k)) - 1;
-                }
-                float high = -INFINITY;
+                    for (int k = 0; k < 4; ++k)
+                        whole = whole && v[k] == (S::kStep == 128 ? ~0u : 0xFFFFu);
+                    if (!whole) {
+                        const int left = (int)min(max(limit - position, (int64_t)0), (int64_t)S::kStep);
+#pragma unroll 1
+                        for (int k = 0; k < S::kStep / 32; ++k) {
+                            uint32_t bits = S::kStep == 128 ? v[k] : v[2 * k] | v[2 * k + 1] << 16;
+                            bits &= left >= 32 * k + 32 ? ~0u
+                                    : left <= 32 * k    ? 0u
+                                                        : (1u << (left - 32 * k)) - 1;
+                            if (__all_sync(~0u, bits == ~0u)) continue;
+                            uint32_t s[32];
+                            tmem_load(t_scores + 32 * k, s);
 #pragma unroll
-                for (int k = 0; k < S::kStep / 32; ++k) {
-                    uint32_t s[32];
-                    tmem_load32(t_scores + 32 * k, s);
-                    if (whole) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) high = fmaxf(high, __uint_as_float(s[j]));
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            high = fmaxf(high, bits[k] >> j & 1 ? __uint_as_float(s[j]) : -INFINITY);
+                            for (int j = 0; j < 32; ++j)
+                                if (!(bits >> j & 1)) s[j] = 0xFF800000u;
+                            tmem_st_32x32b_x32(t_scores + 32 * k, s);
+                        }
+                        tmem_st_wait();
                     }
                 }
-                high = high == -INFINITY ? high : high * a.scale_log2;
-                if (__any_sync(~0u, high > top + kSlack)) {
+                uint32_t part[S::kStep / 64][64];
+#pragma unroll
+                for (int k = 0; k < S::kStep / 64; ++k) tmem_load(t_scores + 64 * k, part[k]);
+                const auto s = [&](int j) { return __uint_as_float(part[j / 64][j % 64]); };
+                float high[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int j = 0; j < S::kStep; j += 8)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        high[x] = fmaxf(fmaxf(high[x], s(j + 2 * x)), s(j + 2 * x + 1));
+                float highest = fmaxf(fmaxf(high[0], high[1]), fmaxf(high[2], high[3]));
+                highest = highest == -INFINITY ? highest : highest * a.scale_log2;
+                if (__any_sync(~0u, highest > top + kSlack)) {
                     // (each query by its own: what the others see makes no difference to it)
-                    const float higher = high > top + kSlack ? high : top;
+                    const float higher = highest > top + kSlack ? highest : top;
                     const float keep = higher == top ? 1.f : exp2_fast(top - higher);
                     top = higher;
-                    sum *= keep;
+                    sum2.x *= keep, sum2.y *= keep;
                     if (i > 0) {
                         // (the scores are there, so the MMAs before them are done)
 #pragma unroll 1
                         for (int c = 0; c < DP; c += 32) {
                             uint32_t o[32];
-                            tmem_load32(t_out + c, o);
+                            tmem_load(t_out + c, o);
 #pragma unroll
                             for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * keep);
                             tmem_st_32x32b_x32(t_out + c, o);
                         }
                     }
                 }
-                const float base_exp = (top == -INFINITY ? 0.f : top) - kHeadroom;
+                const float down = kHeadroom - (top == -INFINITY ? 0.f : top);
+                const float2 down2 = make_float2(down, down);
 #pragma unroll
                 for (int k = 0; k < S::kStep / 32; ++k) {
-                    uint32_t s[32], p[16];
-                    tmem_load32(t_scores + 32 * k, s);
+                    uint32_t p[16];
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
-                        float x = fmaf(__uint_as_float(s[j]), a.scale_log2, -base_exp);
-                        float y = fmaf(__uint_as_float(s[j + 1]), a.scale_log2, -base_exp);
-                        if (!whole) {
-                            x = bits[k] >> j & 1 ? x : -INFINITY;
-                            y = bits[k] >> (j + 1) & 1 ? y : -INFINITY;
-                        }
-                        x = exp2_fast(x);
-                        y = exp2_fast(y);
-                        sum += x + y;
-                        p[j / 2] = pack2<T>(x, y);
+                        const float2 x =
+                            __ffma2_rn(make_float2(s(32 * k + j), s(32 * k + j + 1)), scale2, down2);
+                        const float2 e = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+                        sum2 = __fadd2_rn(sum2, e);
+                        p[j / 2] = pack2<T>(e.x, e.y);
                     }
                     tmem_st_32x32b_x16(t_scores + 16 * k, p);
+                    if (k % (S::kStep / 64) == S::kStep / 64 - 1) {  // half of them
+                        tmem_st_wait();
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(rest.p_full[q][k / (S::kStep / 64)]));
+                    }
                 }
-                tmem_st_wait();
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(rest.p_full[q]));
             }
             if (!ok) break;
+            const float sum = sum2.x + sum2.y;
             const bool whole = u.part < 0;
             const int64_t part = whole ? 0 : (int64_t)u.part * a.c.kv_heads + u.head;
             if (steps > 0) {
@@ -813,13 +945,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 for (int c = 0; c < DP; c += 32) {
                     uint32_t o[32];
                     __syncwarp();
-                    tmem_load32(t_out + c, o);
+                    tmem_load(t_out + c, o);
                     if (any) {
+#pragma unroll
                         for (int j = 0; j < 32; ++j) {
-                            float& x = reinterpret_cast<float&>(o[j]);
+                            float x = __uint_as_float(o[j]);
                             if (odd.first[1][c + j] < limit) x += INFINITY;
                             if (odd.first[2][c + j] < limit) x -= INFINITY;
                             if (odd.first[0][c + j] < limit) x += NAN;
+                            o[j] = __float_as_uint(x);
                         }
                     }
                     if (!in) {
@@ -850,8 +984,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             if (in && !whole)
                 a.partial_ml[part * S::kRows + q * kQueryTile + r] = make_float2(top - kHeadroom, sum);
         }
-    } else {
-        // the second tile's warps where there is one: nothing to do
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -1021,7 +1153,8 @@ cudaError_t launch_paged_chunk_attention(const void* q, const void* k_pool, cons
     a.out_head = query.out_head_stride;
     a.q_heads = (int)query.q_heads;
     a.sms = ctx.num_sms;
-    a.scale_log2 = (float)((query.scale < 0 ? -query.scale : query.scale) * 1.4426950408889634);
+    // (not 0, which would make NaN of the -infinity of a position that does not count)
+    a.scale_log2 = std::max((float)(std::abs(query.scale) * 1.4426950408889634), 0x1p-126f);
     a.negative = query.scale < 0;
     a.status = ctx.status;
     a.timeout_ns = ctx.timeout_ns;
