@@ -320,6 +320,26 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
+// Transposes the 4x4 pieces of four neighbouring lanes: v[j] of lane i and v[i] of lane j change places.
+__device__ __forceinline__ void turn4(uint4 (&v)[4], int lane) {
+#pragma unroll
+    for (int d = 1; d < 4; d *= 2) {
+        const bool high = lane & d;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (j & d) continue;
+            // the low lane keeps v[j] and gives v[j + d], the high one the other way round
+            uint32_t* keep = reinterpret_cast<uint32_t*>(&v[j]);
+            uint32_t* give = reinterpret_cast<uint32_t*>(&v[j + d]);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const uint32_t got = __shfl_xor_sync(~0u, high ? keep[x] : give[x], d);
+                if (high) keep[x] = got; else give[x] = got;
+            }
+        }
+    }
+}
+
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     if constexpr (std::is_same<T, __half>::value) {
@@ -338,15 +358,56 @@ __device__ __forceinline__ void registers_down() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegisters));
 }
 
-// D[tmem] (+)= A[tmem] * B[smem desc], 16-bit inputs, f32 accumulate.
-__device__ __forceinline__ void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                              uint32_t idesc, uint32_t accumulate) {
+// The MMAs, by the one lane whose `leader` is set: predicated, so that the warp stays together and
+// the operands, which are alike in all lanes, in its uniform registers.  (Under a branch on the
+// lane, each operand was moved there anew: a step's 32 MMAs took 5300 cycles.)  A matrix in shared
+// memory is given by its descriptor's low word; the high word is that of the layouts below.
+constexpr uint32_t kDescHigh = (1024 >> 4) | (1u << 14) | (2u << 29);
+
+// D[tmem] (+)= A[smem] * B[smem]^T, 16-bit inputs, f32 accumulate.
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint32_t a, uint32_t b,
+                                       uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\t"
+        "setp.ne.b32 q, %0, 0;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "mov.b64 x, {%2, %4};\n\t"
+        "mov.b64 y, {%3, %4};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%1], x, y, %5, p;\n\t}" ::"r"(leader),
+        "r"(d), "r"(a), "r"(b), "r"(kDescHigh), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem].
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint32_t b,
+                                       uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\t"
+        "setp.ne.b32 q, %0, 0;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "mov.b64 y, {%3, %4};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], y, %5, p;\n\t}" ::"r"(leader),
+        "r"(d), "r"(a), "r"(b), "r"(kDescHigh), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_commit(uint32_t leader, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %0, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(
+            leader),
+        "r"(bar)
+        : "memory");
+}
+
+// Low words of descriptors, 128-byte swizzle.  Queries and keys: dimensions along the rows of
+// shared memory (K-major).  V as the right operand [positions x dims]: again dims along the rows,
+// which is MN-major: 64 of them are a row, `block` bytes from one such block to the next, 1024
+// bytes from eight positions to the next eight.
+__device__ __forceinline__ uint32_t desc_k_major(uint32_t smem_addr) { return smem_addr >> 4 | 1u << 16; }
+__device__ __forceinline__ uint32_t desc_mn_major(uint32_t smem_addr, uint32_t block) {
+    return smem_addr >> 4 | block >> 4 << 16;
 }
 
 // tcgen05.ld, and the wait for it (one statement: nothing may use r in between).
@@ -405,14 +466,6 @@ __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_
 }
 __device__ __forceinline__ void tmem_st_wait() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-// V's tile as the right operand [positions x dims] with dims along the rows of shared memory
-// (MN-major, 128-byte swizzle): 64 dimensions are a 128-byte row, `block` bytes from one such
-// block of dimensions to the next, 1024 bytes from eight positions to the next eight.
-__device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t smem_addr, uint32_t block) {
-    return (uint64_t)((smem_addr >> 4) & 0x3FFFu) | ((uint64_t)(block >> 4) << 16) |
-           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
 // ---------------------------------------------------------------------------
@@ -570,86 +623,83 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             const uint32_t scores = umma_idesc_f16_f32(kQueryTile, S::kStep) | kType |
                                     (a.negative ? 1u << 13 : 0u);  // (minus the queries)
             const uint32_t values = umma_idesc_f16_f32(kQueryTile, DP) | kType | (1u << 16);  // V: MN-major
-            uint32_t step = 0;           // of the block, for the ring's slots
+            const uint32_t leader = lane == 0;
+            const uint32_t q_desc = desc_k_major(base), k_desc = desc_k_major(base + S::kOffRing);
+            const uint32_t v_desc = desc_mn_major(base + S::kOffRing, S::kStep * 128);
+            uint32_t step = 0;         // of the block, for the ring's slots
             uint32_t taken[2] = {0, 0};  // steps of each tile
             uint32_t looks[2] = {0, 0};  // at each slot of values
             Unit u;
             bool ok = true;
+            const auto wait = [&](uint64_t& b, uint32_t phase) {
+                if (ok) ok = __all_sync(~0u, mbar_wait(bar(b), phase & 1, a.timeout_ns, a.status));
+            };
+            // Reports the MMAs issued so far, and passes on (by an arrival of this thread) what the
+            // copying warps wrote.
+            const auto finished = [&](uint64_t& b) {
+                mma_commit(leader, bar(b));
+                if (leader) mbar_arrive(bar(b));
+            };
+            const auto score = [&](int q, uint32_t slot) {
+                const uint32_t qa = q_desc + q * (S::kTileBytes >> 4);
+                const uint32_t ka = k_desc + slot * (S::kSlotBytes >> 4);
+#pragma unroll
+                for (int j = 0; j < DP / 16; ++j)
+                    mma_ss(leader, tmem + q * 128, qa + j / 4 * (kQueryTile * 8) + j % 4 * 2,
+                           ka + j / 4 * (S::kStep * 8) + j % 4 * 2, scores, j != 0);
+                finished(rest.s_full[q]);
+            };
             for (uint32_t n = 0; ok && next_unit(n, u); ++n) {
-                if (lane == 0) {
-                    const int steps[2] = {steps_of(u, 0), S::kTiles == 2 ? steps_of(u, 1) : 0};
-                    const int looked_from = part_seen_from(u);
-                    const auto wait = [&](uint64_t& b, uint32_t phase) {
-                        if (ok) ok = mbar_wait(bar(b), phase & 1, a.timeout_ns, a.status);
-                    };
-                    // Reports the MMAs issued so far, and passes on (by an arrival of this thread)
-                    // what the copying warps wrote.
-                    const auto finished = [&](uint64_t& b) {
-                        tc_commit(bar(b));
-                        mbar_arrive(bar(b));
-                    };
-                    const auto score = [&](int q, uint32_t slot) {
-                        const uint32_t qa = base + q * S::kTileBytes;
-                        const uint32_t ka = base + S::kOffRing + slot * S::kSlotBytes;
+                const int steps[2] = {steps_of(u, 0), S::kTiles == 2 ? steps_of(u, 1) : 0};
+                const int looked_from = part_seen_from(u);
+                wait(rest.q_full, n);
+                wait(rest.kv_full[2 * step % kSlots], 2 * step / kSlots);
+                if (!ok) break;
+                fence_proxy_async_smem();
 #pragma unroll
-                        for (int j = 0; j < DP / 16; ++j)
-                            tc_mma_f16(tmem + q * 128,
-                                       umma_desc_sw128(qa + j / 4 * (kQueryTile * 128) + j % 4 * 32),
-                                       umma_desc_sw128(ka + j / 4 * (S::kStep * 128) + j % 4 * 32), scores,
-                                       j != 0);
-                        finished(rest.s_full[q]);
-                    };
-                    wait(rest.q_full, n);
-                    wait(rest.kv_full[2 * step % kSlots], 2 * step / kSlots);
-                    if (ok) {
-                        fence_proxy_async_smem();
-                        for (int q = 0; q < S::kTiles; ++q)
-                            if (steps[q] > 0) score(q, 2 * step % kSlots);
-                        tc_commit(bar(rest.kv_free[2 * step % kSlots]));
-                        if (u.steps == 1) tc_commit(bar(rest.q_free));
-                    }
-                    for (int i = 0; ok && i < u.steps; ++i, ++step) {
-                        const uint32_t v = 2 * step + 1, k = 2 * step + 2;
-                        if (i < looked_from)
-                            wait(rest.kv_full[v % kSlots], v / kSlots);
-                        else
-                            wait(rest.looked[v % kSlots], looks[v % kSlots / 2]++);
-                        if (i + 1 < u.steps) wait(rest.kv_full[k % kSlots], k / kSlots);
-                        fence_proxy_async_smem();
-                        for (int q = 0; q < S::kTiles; ++q) {
-                            if (i >= steps[q]) continue;
-                            const uint32_t va = base + S::kOffRing + v % kSlots * S::kSlotBytes;
-                            // the first half of the weights, while the second is still made
+                for (int q = 0; q < S::kTiles; ++q)
+                    if (steps[q] > 0) score(q, 2 * step % kSlots);
+                mma_commit(leader, bar(rest.kv_free[2 * step % kSlots]));
+                if (u.steps == 1) mma_commit(leader, bar(rest.q_free));
+                for (int i = 0; i < u.steps; ++i, ++step) {
+                    const uint32_t v = 2 * step + 1, k = 2 * step + 2;
+                    if (i < looked_from)
+                        wait(rest.kv_full[v % kSlots], v / kSlots);
+                    else
+                        wait(rest.looked[v % kSlots], looks[v % kSlots / 2]++);
+                    if (i + 1 < u.steps) wait(rest.kv_full[k % kSlots], k / kSlots);
+                    fence_proxy_async_smem();
 #pragma unroll
-                            for (int half = 0; half < 2; ++half) {
-                                wait(rest.p_full[q][half], taken[q]);
-                                if (!ok) break;
-                                tc_fence_after_sync();
+                    for (int q = 0; q < S::kTiles; ++q) {
+                        if (i >= steps[q]) continue;
+                        const uint32_t va = v_desc + v % kSlots * (S::kSlotBytes >> 4);
+                        // the first half of the weights, while the second is still made
 #pragma unroll
-                                for (int j = half * S::kStep / 32; j < (half + 1) * S::kStep / 32; ++j)
-                                    tc_mma_f16_ta(tmem + S::kOutColumn + q * DP, tmem + q * 128 + 8 * j,
-                                                  umma_desc_mn_sw128(va + j * 2048, S::kStep * 128), values,
-                                                  (i | j) != 0);
-                            }
+                        for (int half = 0; half < 2; ++half) {
+                            wait(rest.p_full[q][half], taken[q]);
                             if (!ok) break;
-                            ++taken[q];
-                            if (i + 1 < steps[q])
-                                score(q, k % kSlots);
-                            else
-                                finished(rest.o_full[q]);
+                            tc_fence_after_sync();
+#pragma unroll
+                            for (int j = half * S::kStep / 32; j < (half + 1) * S::kStep / 32; ++j)
+                                mma_ts(leader, tmem + S::kOutColumn + q * DP, tmem + q * 128 + 8 * j,
+                                       va + j * (2048 >> 4), values, (i | j) != 0);
                         }
                         if (!ok) break;
-                        tc_commit(bar(rest.kv_free[v % kSlots]));
-                        if (i + 1 < u.steps) tc_commit(bar(rest.kv_free[k % kSlots]));
-                        if (i + 2 == u.steps) tc_commit(bar(rest.q_free));
+                        ++taken[q];
+                        if (i + 1 < steps[q])
+                            score(q, k % kSlots);
+                        else
+                            finished(rest.o_full[q]);
                     }
+                    if (!ok) break;
+                    mma_commit(leader, bar(rest.kv_free[v % kSlots]));
+                    if (i + 1 < u.steps) mma_commit(leader, bar(rest.kv_free[k % kSlots]));
+                    if (i + 2 == u.steps) mma_commit(leader, bar(rest.q_free));
                 }
-                ok = __shfl_sync(~0u, ok, 0);
             }
-            if (lane == 0) {  // nothing in flight when the block ends
-                tc_commit(bar(rest.done));
-                mbar_wait(bar(rest.done), 0, drain_bound(a.timeout_ns), a.status);
-            }
+            // nothing in flight when the block ends
+            mma_commit(leader, bar(rest.done));
+            mbar_wait(bar(rest.done), 0, drain_bound(a.timeout_ns), a.status);
             __syncwarp();
         } else {
             // ============================== looking =============================
@@ -671,29 +721,39 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                         continue;
                     }
                     const uint32_t from = base + S::kOffRing + slot * S::kSlotBytes;
-#pragma unroll 4
-                    for (int x = (warp - kLookWarp) * 32 + lane; x < S::kSlotBytes / 16;
-                         x += 32 * kLookWarps) {
-                        uint4 piece = lds128(from + 16 * x);
-                        uint32_t* words = reinterpret_cast<uint32_t*>(&piece);
-                        bool bad = false;
+                    // Eight pieces at a time, by the largest of the magnitudes' bits; any one that
+                    // is not finite is then looked for.
+                    constexpr int kAhead = 8, kEach = S::kSlotBytes / 16 / (32 * kLookWarps);
+#pragma unroll 1
+                    for (int first = 0; first < kEach; first += kAhead) {
+                        const uint32_t x0 = ((warp - kLookWarp) * kEach + first) * 32 + lane;
+                        uint4 piece[kAhead];
 #pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            bad = bad || (words[y] & kExponent) == kExponent ||
-                                  (words[y] & kExponent << 16) == kExponent << 16;
-                        if (!bad) continue;
-                        const int row = x / 8 % S::kStep, dim = (x / 8 / S::kStep * 8 + (x % 8 ^ row % 8)) * 8;
-                        for (int y = 0; y < 8; ++y) {
-                            const uint32_t one = words[y / 2] >> (16 * (y % 2)) & 0xFFFFu;
+                        for (int y = 0; y < kAhead; ++y) piece[y] = lds128(from + 16 * (x0 + 32 * y));
+                        uint32_t most = 0;
+#pragma unroll
+                        for (int y = 0; y < kAhead; ++y) {
+                            most = __vmaxu2(most, piece[y].x & 0x7FFF7FFFu);
+                            most = __vmaxu2(most, piece[y].y & 0x7FFF7FFFu);
+                            most = __vmaxu2(most, piece[y].z & 0x7FFF7FFFu);
+                            most = __vmaxu2(most, piece[y].w & 0x7FFF7FFFu);
+                        }
+                        if ((most & 0xFFFFu) < kExponent && most >> 16 < kExponent) continue;
+#pragma unroll 1
+                        for (int y = 0; y < 8 * kAhead; ++y) {
+                            const uint32_t x = x0 + 32 * (y / 8);
+                            // value y % 8 of piece x: its row, and its dimension behind the swizzle
+                            const uint32_t where = from + 16 * x + 2 * (y % 8);
+                            const int row = x / 8 % S::kStep;
+                            const int dim = (x / 8 / S::kStep * 8 + (x % 8 ^ row % 8)) * 8 + y % 8;
+                            uint16_t one;
+                            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(one) : "r"(where) : "memory");
                             if ((one & kExponent) != kExponent) continue;
                             const int kind = (one & (kExponent ^ 0x7FFFu)) ? 0 : one >> 15 ? 2 : 1;
-                            atomicMin(&odd.first[kind][dim + y], (u.first + i) * S::kStep + row);
-                            words[y / 2] &= y % 2 ? 0xFFFFu : 0xFFFF0000u;
+                            atomicMin(&odd.first[kind][dim], (u.first + i) * S::kStep + row);
+                            odd.any = 1;
+                            asm volatile("st.shared.u16 [%0], %1;" ::"r"(where), "h"((uint16_t)0) : "memory");
                         }
-                        odd.any = 1;
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(from + 16 * x),
-                                     "r"(piece.x), "r"(piece.y), "r"(piece.z), "r"(piece.w)
-                                     : "memory");
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -778,13 +838,20 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     if (n > 0) wait(rest.q_free, n - 1);
                     if (!ok) break;
                     const uint16_t* q0 = a.q + u.token0 * a.q_row + (int64_t)u.head * group * a.q_head;
-#pragma unroll 4
-                    for (int r = w * (S::kRows / kCopyWarps) + row0; r < (w + 1) * (S::kRows / kCopyWarps);
-                         r += kRowsPass) {
+                    int r = w * (S::kRows / kCopyWarps) + row0;
+                    int h = u.lin0 + r - a.group.quotient(u.lin0 + r) * group;
+                    const uint16_t* from =
+                        q0 + a.group.quotient(u.lin0 + r) * a.q_row + h * a.q_head + 8 * piece;
+                    const int64_t next_head = kRowsPass * a.q_head, next_token = a.q_row - group * a.q_head;
+#pragma unroll 8
+                    for (int x = 0; x < S::kRows / kCopyWarps; x += kRowsPass) {
                         const bool in = r < u.lins && in_dim;
-                        const int token = a.group.quotient(u.lin0 + r), h = u.lin0 + r - token * group;
                         copy16(base + r / kQueryTile * S::kTileBytes + at(r % kQueryTile, kQueryTile),
-                               in ? q0 + token * a.q_row + h * a.q_head + 8 * piece : a.q, in);
+                               in ? from : a.q, in);
+                        r += kRowsPass;
+                        h += kRowsPass;
+                        from += next_head;
+                        while (h >= group) h -= group, from += next_token;
                     }
                     copy_arrive(bar(rest.q_full));
                 }
@@ -847,36 +914,30 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 ++taken;
                 tc_fence_after_sync();
                 const int64_t position = (int64_t)(u.first + i) * S::kStep;
-                {
-                    // Scores that do not count become -infinity, in tensor memory.
-                    const uint32_t* v = rest.valid[(step0 + i) % 4];
-                    bool whole = position + S::kStep <= least;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        whole = whole && v[k] == (S::kStep == 128 ? ~0u : 0xFFFFu);
-                    if (!whole) {
-                        const int left = (int)min(max(limit - position, (int64_t)0), (int64_t)S::kStep);
-#pragma unroll 1
-                        for (int k = 0; k < S::kStep / 32; ++k) {
-                            uint32_t bits = S::kStep == 128 ? v[k] : v[2 * k] | v[2 * k + 1] << 16;
-                            bits &= left >= 32 * k + 32 ? ~0u
-                                    : left <= 32 * k    ? 0u
-                                                        : (1u << (left - 32 * k)) - 1;
-                            if (__all_sync(~0u, bits == ~0u)) continue;
-                            uint32_t s[32];
-                            tmem_load(t_scores + 32 * k, s);
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (!(bits >> j & 1)) s[j] = 0xFF800000u;
-                            tmem_st_32x32b_x32(t_scores + 32 * k, s);
-                        }
-                        tmem_st_wait();
-                    }
-                }
                 uint32_t part[S::kStep / 64][64];
 #pragma unroll
                 for (int k = 0; k < S::kStep / 64; ++k) tmem_load(t_scores + 64 * k, part[k]);
                 const auto s = [&](int j) { return __uint_as_float(part[j / 64][j % 64]); };
+                const uint32_t* v = rest.valid[(step0 + i) % 4];
+                bool whole = position + S::kStep <= least;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    whole = whole && v[k] == (S::kStep == 128 ? ~0u : 0xFFFFu);
+                if (!whole) {  // scores that do not count become -infinity
+                    const int left = (int)min(max(limit - position, (int64_t)0), (int64_t)S::kStep);
+#pragma unroll
+                    for (int k = 0; k < S::kStep / 32; ++k) {
+                        uint32_t bits = S::kStep == 128 ? v[k] : v[2 * k] | v[2 * k + 1] << 16;
+                        bits &= left >= 32 * k + 32 ? ~0u
+                                : left <= 32 * k    ? 0u
+                                                    : (1u << (left - 32 * k)) - 1;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            uint32_t& x = part[k / 2][k % 2 * 32 + j];
+                            x = bits >> j & 1 ? x : 0xFF800000u;
+                        }
+                    }
+                }
                 float high[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int j = 0; j < S::kStep; j += 8)
@@ -939,7 +1000,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 const bool any = *reinterpret_cast<const volatile int*>(&odd.any) != 0;
                 const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
                 const int64_t t = u.token0 + token;
-                uint16_t* to = a.out + t * a.out_row + h * a.out_head;
+                // (a query that sees nothing has its zeros already)
+                uint16_t* mine = in && limit > 0 ? a.out + t * a.out_row + h * a.out_head : nullptr;
                 float* part_to = a.partial + ((part * S::kTiles + q) * (DP / 4) * kQueryTile + r) * 4;
 #pragma unroll 1
                 for (int c = 0; c < DP; c += 32) {
@@ -956,21 +1018,27 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                             o[j] = __float_as_uint(x);
                         }
                     }
-                    if (!in) {
-                        // not a query
-                    } else if (whole) {
-                        // (a query that sees nothing has its zeros already)
+                    if (whole) {
+                        // Four neighbours turn their four pieces of 16 bytes each around, so that
+                        // every store has 64 bytes of a query in a row.  (One query a lane: twice
+                        // the sectors, and 4000 cycles for a unit's output.)
+                        uint4 v[4];
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8) {
-                            if (c + j >= a.c.head_dim || limit == 0) continue;
-                            uint32_t v[4];
+                        for (int j = 0; j < 4; ++j)
+                            v[j] = make_uint4(
+                                pack2<T>(__uint_as_float(o[8 * j]) * inv, __uint_as_float(o[8 * j + 1]) * inv),
+                                pack2<T>(__uint_as_float(o[8 * j + 2]) * inv, __uint_as_float(o[8 * j + 3]) * inv),
+                                pack2<T>(__uint_as_float(o[8 * j + 4]) * inv, __uint_as_float(o[8 * j + 5]) * inv),
+                                pack2<T>(__uint_as_float(o[8 * j + 6]) * inv, __uint_as_float(o[8 * j + 7]) * inv));
+                        turn4(v, lane);
 #pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                v[x] = pack2<T>(__uint_as_float(o[j + 2 * x]) * inv,
-                                                __uint_as_float(o[j + 2 * x + 1]) * inv);
-                            *reinterpret_cast<uint4*>(to + c + j) = make_uint4(v[0], v[1], v[2], v[3]);
+                        for (int j = 0; j < 4; ++j) {  // of query j of the four
+                            uint16_t* there = reinterpret_cast<uint16_t*>(
+                                __shfl_sync(~0u, reinterpret_cast<uint64_t>(mine), lane / 4 * 4 + j));
+                            if (there && c + lane % 4 * 8 < a.c.head_dim)
+                                *reinterpret_cast<uint4*>(there + c + lane % 4 * 8) = v[j];
                         }
-                    } else {
+                    } else if (in) {
 #pragma unroll
                         for (int j = 0; j < 32; j += 4)
                             *reinterpret_cast<uint4*>(part_to + (int64_t)(c + j) * kQueryTile) =
