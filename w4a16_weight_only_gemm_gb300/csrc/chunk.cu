@@ -358,46 +358,64 @@ __device__ __forceinline__ void registers_down() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegisters));
 }
 
-// The MMAs, by the one lane whose `leader` is set: predicated, so that the warp stays together and
-// the operands, which are alike in all lanes, in its uniform registers.  (Under a branch on the
-// lane, each operand was moved there anew: a step's 32 MMAs took 5300 cycles.)  A matrix in shared
-// memory is given by its descriptor's low word; the high word is that of the layouts below.
+// The MMAs.  The whole warp comes here together, with operands that are alike in all lanes, and
+// one lane, elected in the same statement, issues them: so they stay in uniform registers.  (Under
+// a branch on the lane, or by a predicate of the lane's, an MMA took some 100 cycles to issue.)  A
+// matrix in shared memory is given by its descriptor's low word; the high word is that of the
+// layouts below.
 constexpr uint32_t kDescHigh = (1024 >> 4) | (1u << 14) | (2u << 29);
 
-// D[tmem] (+)= A[smem] * B[smem]^T, 16-bit inputs, f32 accumulate.
-__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint32_t a, uint32_t b,
-                                       uint32_t idesc, uint32_t accumulate) {
+// D[tmem] (+)= A[smem] * B[smem]^T over 64 of K, K-major; 16-bit inputs, f32 accumulate.
+__device__ __forceinline__ void mma_ss_64(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                          uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\t"
-        "setp.ne.b32 q, %0, 0;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "mov.b64 x, {%2, %4};\n\t"
-        "mov.b64 y, {%3, %4};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%1], x, y, %5, p;\n\t}" ::"r"(leader),
-        "r"(d), "r"(a), "r"(b), "r"(kDescHigh), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\t.reg .b32 a, b;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 x, {%1, %3};\n\t"
+        "mov.b64 y, {%2, %3};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t"
+        "add.u32 a, %1, 2;\n\t"
+        "add.u32 b, %2, 2;\n\t"
+        "mov.b64 x, {a, %3};\n\t"
+        "mov.b64 y, {b, %3};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, 1;\n\t"
+        "add.u32 a, %1, 4;\n\t"
+        "add.u32 b, %2, 4;\n\t"
+        "mov.b64 x, {a, %3};\n\t"
+        "mov.b64 y, {b, %3};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, 1;\n\t"
+        "add.u32 a, %1, 6;\n\t"
+        "add.u32 b, %2, 6;\n\t"
+        "mov.b64 x, {a, %3};\n\t"
+        "mov.b64 y, {b, %3};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, 1;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(kDescHigh), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
-// D[tmem] (+)= A[tmem] * B[smem].
-__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint32_t b,
-                                       uint32_t idesc, uint32_t accumulate) {
+// D[tmem] (+)= A[tmem] * B[smem] over 32 of K, B MN-major.
+__device__ __forceinline__ void mma_ts_32(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                          uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\t"
-        "setp.ne.b32 q, %0, 0;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "mov.b64 y, {%3, %4};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], y, %5, p;\n\t}" ::"r"(leader),
-        "r"(d), "r"(a), "r"(b), "r"(kDescHigh), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\t.reg .b32 a, b;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 y, {%2, %3};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t"
+        "add.u32 a, %1, 8;\n\t"
+        "add.u32 b, %2, 128;\n\t"
+        "mov.b64 y, {b, %3};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %4, 1;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(kDescHigh), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
-__device__ __forceinline__ void mma_commit(uint32_t leader, uint32_t bar) {
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
     asm volatile(
         "{\n\t.reg .pred q;\n\t"
-        "setp.ne.b32 q, %0, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(
-            leader),
-        "r"(bar)
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
         : "memory");
 }
 
@@ -623,7 +641,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             const uint32_t scores = umma_idesc_f16_f32(kQueryTile, S::kStep) | kType |
                                     (a.negative ? 1u << 13 : 0u);  // (minus the queries)
             const uint32_t values = umma_idesc_f16_f32(kQueryTile, DP) | kType | (1u << 16);  // V: MN-major
-            const uint32_t leader = lane == 0;
             const uint32_t q_desc = desc_k_major(base), k_desc = desc_k_major(base + S::kOffRing);
             const uint32_t v_desc = desc_mn_major(base + S::kOffRing, S::kStep * 128);
             uint32_t step = 0;         // of the block, for the ring's slots
@@ -637,16 +654,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             // Reports the MMAs issued so far, and passes on (by an arrival of this thread) what the
             // copying warps wrote.
             const auto finished = [&](uint64_t& b) {
-                mma_commit(leader, bar(b));
-                if (leader) mbar_arrive(bar(b));
+                mma_commit(bar(b));
+                if (lane == 0) mbar_arrive(bar(b));
             };
             const auto score = [&](int q, uint32_t slot) {
                 const uint32_t qa = q_desc + q * (S::kTileBytes >> 4);
                 const uint32_t ka = k_desc + slot * (S::kSlotBytes >> 4);
 #pragma unroll
-                for (int j = 0; j < DP / 16; ++j)
-                    mma_ss(leader, tmem + q * 128, qa + j / 4 * (kQueryTile * 8) + j % 4 * 2,
-                           ka + j / 4 * (S::kStep * 8) + j % 4 * 2, scores, j != 0);
+                for (int j = 0; j < DP / 64; ++j)
+                    mma_ss_64(tmem + q * 128, qa + j * (kQueryTile * 8), ka + j * (S::kStep * 8), scores,
+                              j != 0);
                 finished(rest.s_full[q]);
             };
             for (uint32_t n = 0; ok && next_unit(n, u); ++n) {
@@ -659,8 +676,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
 #pragma unroll
                 for (int q = 0; q < S::kTiles; ++q)
                     if (steps[q] > 0) score(q, 2 * step % kSlots);
-                mma_commit(leader, bar(rest.kv_free[2 * step % kSlots]));
-                if (u.steps == 1) mma_commit(leader, bar(rest.q_free));
+                mma_commit(bar(rest.kv_free[2 * step % kSlots]));
+                if (u.steps == 1) mma_commit(bar(rest.q_free));
                 for (int i = 0; i < u.steps; ++i, ++step) {
                     const uint32_t v = 2 * step + 1, k = 2 * step + 2;
                     if (i < looked_from)
@@ -680,9 +697,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                             if (!ok) break;
                             tc_fence_after_sync();
 #pragma unroll
-                            for (int j = half * S::kStep / 32; j < (half + 1) * S::kStep / 32; ++j)
-                                mma_ts(leader, tmem + S::kOutColumn + q * DP, tmem + q * 128 + 8 * j,
-                                       va + j * (2048 >> 4), values, (i | j) != 0);
+                            for (int j = half * S::kStep / 64; j < (half + 1) * S::kStep / 64; ++j)
+                                mma_ts_32(tmem + S::kOutColumn + q * DP, tmem + q * 128 + 16 * j,
+                                          va + j * (4096 >> 4), values, (i | j) != 0);
                         }
                         if (!ok) break;
                         ++taken[q];
@@ -692,13 +709,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                             finished(rest.o_full[q]);
                     }
                     if (!ok) break;
-                    mma_commit(leader, bar(rest.kv_free[v % kSlots]));
-                    if (i + 1 < u.steps) mma_commit(leader, bar(rest.kv_free[k % kSlots]));
-                    if (i + 2 == u.steps) mma_commit(leader, bar(rest.q_free));
+                    mma_commit(bar(rest.kv_free[v % kSlots]));
+                    if (i + 1 < u.steps) mma_commit(bar(rest.kv_free[k % kSlots]));
+                    if (i + 2 == u.steps) mma_commit(bar(rest.q_free));
                 }
             }
             // nothing in flight when the block ends
-            mma_commit(leader, bar(rest.done));
+            mma_commit(bar(rest.done));
             mbar_wait(bar(rest.done), 0, drain_bound(a.timeout_ns), a.status);
             __syncwarp();
         } else {
