@@ -2,9 +2,9 @@
 // tcgen05 tensor cores.
 //
 // A row's new tokens and the query heads that share a key-value head are one list
-// of queries, token by token, and 256 of those (128 with heads above 128) are the
-// rows of an item: two MMA tiles of 128 rows, whatever the number of heads to a
-// key-value head.  An item walks the positions that its last query sees in steps
+// of queries, token by token.  As many whole tokens as make 128 queries at most are
+// the rows of an MMA tile, and two such tiles (one with heads above 128) an item: so
+// no number of heads to a key-value head wastes much.  An item walks the positions that its last query sees in steps
 // of 128 (64): S = Q K^T, P = exp(S - max), O += P V, with S and O in tensor memory
 // and P written over S as the 16-bit left operand of the second product.
 //
@@ -12,8 +12,9 @@
 // of keys and values serve 256 queries.  The two tiles take turns, so that the
 // tensor cores work on one while the other's softmax runs:
 //   warps 0-3, 4-7   softmax of the first and second tile, a thread a query
-//   warps 8-11       copy queries, keys and values (cp.async, any page size),
-//                    zeros where a position has no page
+//   warps 8-11       copy queries, keys and values: by tensor maps, a box for a
+//                    page's rows, or row by row (cp.async) with zeros where a
+//                    position has no page, and for pages of odd sizes
 //   warp 12          one thread issues the MMAs
 //   warp 13          takes the next unit of work
 //   warps 14, 15     look for values that are not finite where some queries see a
@@ -66,7 +67,10 @@ struct Shape {
     static constexpr int kSmem = 1024 + kOffRest + 16384;
     static constexpr int kOutColumn = 256;                      // of tensor memory
 };
-constexpr int rows_of(int64_t dim) { return dim <= 128 ? 256 : 128; }
+constexpr int tiles_of(int64_t dim) { return dim <= 128 ? 2 : 1; }
+constexpr int tile_rows_of(int64_t group) {
+    return (int)(group <= kQueryTile ? kQueryTile / group * group : kQueryTile);
+}
 constexpr int step_of(int64_t dim) { return dim <= 128 ? 128 : 64; }
 
 // What the plan leaves, for each key-value head: `whole` units that are items, then `parts` that
@@ -107,6 +111,10 @@ struct ChunkArgs {
     uint64_t timeout_ns;
     Cache c;
     Divisor group;
+    int tile_rows;       // queries of a tile: as many whole tokens as 128 rows hold
+    // Tensor maps serve: of the queries [tokens, heads, dim], of the pools [pages, heads, slots, dim]
+    // with boxes of box_rows slots.  0: they do not, and cp.async copies row by row.
+    int q_map, box_rows;
 
     __device__ int64_t offset(int b) const {
         return min(max((int64_t)offsets[b], (int64_t)0), tokens);
@@ -314,6 +322,26 @@ __device__ __forceinline__ void copy_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+// Tensor-map loads by one elected lane of a warp that is together (see the MMAs below).
+__device__ __forceinline__ void box_load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1,
+                                            int c2, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void box_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1,
+                                            int c2, int c3, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        : "memory");
+}
+
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -519,7 +547,9 @@ struct Rest {
 };
 
 template <typename T, int DP>
-__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ ChunkArgs a) {
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                 const __grid_constant__ CUtensorMap v_map, const __grid_constant__ ChunkArgs a) {
     using S = Shape<DP>;
     static_assert(sizeof(Rest<DP>) <= 16384, "the rest of shared memory");
     constexpr bool kHalf = std::is_same<T, __half>::value;
@@ -542,10 +572,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             mbar_init(bar(rest.p_full[i][1]), 4);
             mbar_init(bar(rest.o_full[i]), 2);
         }
-        mbar_init(bar(rest.q_full), 32 * kCopyWarps);
+        mbar_init(bar(rest.q_full), 33 * kCopyWarps);
         mbar_init(bar(rest.q_free), 1);
         for (int i = 0; i < kSlots; ++i) {
-            // every copying thread's copies, and an arrival of each warp for what it wrote itself
+            // every copying thread's copies, and an arrival of each warp for its boxes and its writes
             mbar_init(bar(rest.kv_full[i]), 33 * kCopyWarps);
             mbar_init(bar(rest.kv_free[i]), i % 2 ? 1 + kLookWarps : 1);  // values: also the lookers'
             mbar_init(bar(rest.looked[i]), kLookWarps);
@@ -577,8 +607,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     };
     // Steps that tile q of a unit takes part in.
     const auto steps_of = [&](const Unit& u, int q) {
-        const int end = min(u.lins, (q + 1) * kQueryTile);
-        if (end <= q * kQueryTile) return 0;
+        const int end = min(u.lins, (q + 1) * a.tile_rows);
+        if (end <= q * a.tile_rows) return 0;
         const int64_t seen = u.position0 + a.group.quotient(u.lin0 + end - 1) + 1;
         const int64_t steps = seen > 0 ? (seen + S::kStep - 1) / S::kStep : 0;
         return (int)min(max(steps - u.first, (int64_t)0), (int64_t)u.steps);
@@ -616,8 +646,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     u.first = entry.first;
                     u.steps = entry.steps;
                     u.part = entry.part;
-                    u.lin0 = entry.tile * S::kRows;
-                    u.lins = (int)min((int64_t)S::kRows, count * group - u.lin0);
+                    u.lin0 = entry.tile * S::kTiles * a.tile_rows;
+                    u.lins = (int)min((int64_t)S::kTiles * a.tile_rows, count * group - u.lin0);
                     u.token0 = from;
                     u.length = a.length(entry.row);
                     u.position0 = u.length - count;
@@ -794,7 +824,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         const auto at = [&](int row, int rows) {
             return (uint32_t)(piece / 8 * rows * 128 + row * 128 + ((piece % 8 ^ row % 8) << 4));
         };
-        const bool whole_pages = a.c.page_size.value % 16 == 0;
         uint32_t step = 0;
         Unit u;
         bool ok = true;
@@ -805,18 +834,19 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         for (uint32_t n = 0; ok && next_unit(n, u); ++n) {
             const int64_t head = (int64_t)u.head * a.c.head_stride;
             const int32_t* table = a.tables + u.row * a.c.table_stride;
-            const auto page_of = [&](int i) {  // of this lane's position in step i
-                const int64_t p = (int64_t)(u.first + i) * S::kStep + w * kRowsWarp + lane % kRowsWarp;
+            // this lane's position in step i, and its page
+            const auto position_of = [&](int i) {
+                return (int64_t)(u.first + i) * S::kStep + w * kRowsWarp + lane % kRowsWarp;
+            };
+            const auto page_of = [&](int i) {
+                const int64_t p = position_of(i);
                 return p < u.length ? table[a.c.page_size.quotient((int)p)] : -1;
             };
             int next = page_of(0);
             for (int i = 0; i < u.steps; ++i, ++step) {
-                int64_t place = -1;
-                if ((uint32_t)next < (uint32_t)a.c.pages) {
-                    const int p = (u.first + i) * S::kStep + w * kRowsWarp + lane % kRowsWarp;
-                    place = next * a.c.page_stride + a.c.page_size.remainder(p) * a.c.slot_stride + head;
-                }
-                const uint32_t there = __ballot_sync(~0u, place >= 0);
+                const int page = next, in_page = a.c.page_size.remainder((int)position_of(i));
+                const bool there = (uint32_t)page < (uint32_t)a.c.pages;
+                const uint32_t all = __ballot_sync(~0u, there);
                 if (i + 1 < u.steps) next = page_of(i + 1);
 #pragma unroll 1
                 for (int value = 0; value < 2; ++value) {
@@ -825,21 +855,24 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     if (!ok) break;
                     if (!value && lane == 0)
                         rest.valid[step % 4][w] =
-                            kRowsWarp == 32 ? there : there & ((1u << kRowsWarp % 32) - 1);
+                            kRowsWarp == 32 ? all : all & ((1u << kRowsWarp % 32) - 1);
                     const uint32_t to = base + S::kOffRing + slot * S::kSlotBytes;
-                    const uint16_t* pool = (value ? a.v_pool : a.k_pool) + 8 * piece;
-                    if (whole_pages && there == ~0u) {
-                        // sixteen rows at a time lie in one page
-                        const int64_t next_rows = kRowsPass * a.c.slot_stride;
+                    const uint32_t full = bar(rest.kv_full[slot]);
+                    if (a.box_rows && all == ~0u) {
+                        if (lane == 0) mbar_arrive_expect_tx(full, kRowsWarp * DP * 2);
+                        __syncwarp();
+                        fence_proxy_async_smem();  // (rows of the slot that were written one by one)
+                        for (int r = 0; r < kRowsWarp; r += a.box_rows) {
+                            const int in_box = __shfl_sync(~0u, in_page, r), of = __shfl_sync(~0u, page, r);
 #pragma unroll
-                        for (int r = 0; r < kRowsWarp; r += 16) {
-                            const uint16_t* from =
-                                pool + __shfl_sync(~0u, place, r) + row0 * a.c.slot_stride;
-#pragma unroll
-                            for (int x = 0; x < 16; x += kRowsPass, from += next_rows)
-                                copy16(to + at(w * kRowsWarp + r + x + row0, S::kStep), from, in_dim);
+                            for (int x = 0; x < DP / 64; ++x)
+                                box_load_4d(to + x * S::kStep * 128 + (w * kRowsWarp + r) * 128,
+                                            value ? &v_map : &k_map, 64 * x, in_box, u.head, of, full);
                         }
                     } else {
+                        const uint16_t* pool = (value ? a.v_pool : a.k_pool) + 8 * piece;
+                        const int64_t place =
+                            there ? page * a.c.page_stride + in_page * a.c.slot_stride + head : -1;
 #pragma unroll 4
                         for (int r = 0; r < kRowsWarp; r += kRowsPass) {
                             const int64_t o = __shfl_sync(~0u, place, r + row0);
@@ -847,36 +880,55 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                             copy16(to + at(w * kRowsWarp + r + row0, S::kStep), in ? pool + o : a.k_pool,
                                    in);
                         }
+                        if (lane == 0) mbar_arrive(full);
                     }
-                    copy_arrive(bar(rest.kv_full[slot]));
-                    if (lane == 0) mbar_arrive(bar(rest.kv_full[slot]));
+                    copy_arrive(full);
                     if (value || i) continue;
                     // the queries, behind the first keys: theirs is the longer wait
                     if (n > 0) wait(rest.q_free, n - 1);
                     if (!ok) break;
-                    const uint16_t* q0 = a.q + u.token0 * a.q_row + (int64_t)u.head * group * a.q_head;
-                    int r = w * (S::kRows / kCopyWarps) + row0;
-                    int h = u.lin0 + r - a.group.quotient(u.lin0 + r) * group;
-                    const uint16_t* from =
-                        q0 + a.group.quotient(u.lin0 + r) * a.q_row + h * a.q_head + 8 * piece;
-                    const int64_t next_head = kRowsPass * a.q_head, next_token = a.q_row - group * a.q_head;
-#pragma unroll 8
-                    for (int x = 0; x < S::kRows / kCopyWarps; x += kRowsPass) {
-                        const bool in = r < u.lins && in_dim;
-                        copy16(base + r / kQueryTile * S::kTileBytes + at(r % kQueryTile, kQueryTile),
-                               in ? from : a.q, in);
-                        r += kRowsPass;
-                        h += kRowsPass;
-                        from += next_head;
-                        while (h >= group) h -= group, from += next_token;
+                    const uint32_t queries = bar(rest.q_full);
+                    if (a.q_map) {
+                        const int tiles = u.lins > a.tile_rows ? 2 : 1;
+                        if (lane == 0) {
+                            if (w)
+                                mbar_arrive(queries);
+                            else
+                                mbar_arrive_expect_tx(queries, tiles * a.tile_rows * DP * 2);
+                        }
+                        __syncwarp();
+                        const int token = (int)u.token0 + a.group.quotient(u.lin0);
+                        const int tokens = a.group.quotient(a.tile_rows);
+                        for (int q = 0; w == 0 && q < tiles; ++q)
+#pragma unroll
+                            for (int x = 0; x < DP / 64; ++x)
+                                box_load_3d(base + q * S::kTileBytes + x * (kQueryTile * 128), &q_map, 64 * x,
+                                            u.head * group, token + q * tokens, queries);
+                    } else {
+                        const uint16_t* q0 = a.q + u.token0 * a.q_row + (int64_t)u.head * group * a.q_head;
+#pragma unroll 1
+                        for (int r = w * (S::kRows / kCopyWarps) + row0; r < (w + 1) * (S::kRows / kCopyWarps);
+                             r += kRowsPass) {
+                            const int row = r % kQueryTile, lin = r / kQueryTile * a.tile_rows + row;
+                            const bool in = row < a.tile_rows && lin < u.lins && in_dim;
+                            const int token = a.group.quotient(u.lin0 + lin);
+                            const int h = u.lin0 + lin - token * group;
+                            copy16(base + r / kQueryTile * S::kTileBytes + at(row, kQueryTile),
+                                   in ? q0 + token * a.q_row + h * a.q_head + 8 * piece : a.q, in);
+                        }
+                        if (lane == 0) mbar_arrive(queries);
                     }
-                    copy_arrive(bar(rest.q_full));
+                    copy_arrive(queries);
                 }
                 if (!ok) break;
             }
         }
         copy_commit();
         copy_wait<0>();
+        if (!ok) {  // a wait gave up: boxes on their way land before the block ends
+            const uint64_t since = global_timer_ns();
+            while (global_timer_ns() - since < kDrainFloorNs) {}
+        }
     } else if (warp < 4 * S::kTiles) {
         // ============================== softmax ===============================
         registers_up();
@@ -910,17 +962,22 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 zero(a.tokens - 1 - t, a.tokens - t);
         }
         uint32_t taken = 0, units = 0, step0 = 0;  // steps and units of this tile, steps of the block
-        Unit u;
         bool ok = true;
         const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
-        for (uint32_t n = 0; ok && next_unit(n, u); step0 += u.steps, ++n) {
+        for (uint32_t n = 0;; ++n) {
+            ok = mbar_wait(bar(rest.unit_full[n % 2]), n / 2 % 2, a.timeout_ns, a.status);
+            ok = __all_sync(~0u, ok);
+            // (stays where it is until the unit is done: the scores take most registers)
+            const Unit& u = rest.unit[n % 2];
+            if (!ok || u.steps < 0) break;
             const int steps = steps_of(u, q);
-            const int lin = u.lin0 + q * kQueryTile + r;
-            const bool in = q * kQueryTile + r < u.lins;
+            const int lin = u.lin0 + q * a.tile_rows + r;
+            const bool in = r < a.tile_rows && q * a.tile_rows + r < u.lins;
             const int token = a.group.quotient(lin), h = u.head * group + lin - token * group;
             // positions that the query sees; all, for a row that is not there
-            const int64_t limit = in ? max(u.position0 + token + 1, (int64_t)0) : INT32_MAX;
-            const int least = __reduce_min_sync(~0u, (int)limit);
+            const int limit = in ? (int)max(u.position0 + token + 1, (int64_t)0) : INT32_MAX;
+            const int least = __reduce_min_sync(~0u, limit);
+            const int first = u.first;
             float top = -INFINITY;
             float2 sum2 = make_float2(0.f, 0.f);
 #pragma unroll 1
@@ -930,18 +987,18 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 if (!ok) break;
                 ++taken;
                 tc_fence_after_sync();
-                const int64_t position = (int64_t)(u.first + i) * S::kStep;
+                const int position = (first + i) * S::kStep;
                 uint32_t part[S::kStep / 64][64];
 #pragma unroll
                 for (int k = 0; k < S::kStep / 64; ++k) tmem_load(t_scores + 64 * k, part[k]);
                 const auto s = [&](int j) { return __uint_as_float(part[j / 64][j % 64]); };
                 const uint32_t* v = rest.valid[(step0 + i) % 4];
-                bool whole = position + S::kStep <= least;
+                bool whole = least - position >= S::kStep;
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     whole = whole && v[k] == (S::kStep == 128 ? ~0u : 0xFFFFu);
                 if (!whole) {  // scores that do not count become -infinity
-                    const int left = (int)min(max(limit - position, (int64_t)0), (int64_t)S::kStep);
+                    const int left = min(max(limit - position, 0), S::kStep);
 #pragma unroll
                     for (int k = 0; k < S::kStep / 32; ++k) {
                         uint32_t bits = S::kStep == 128 ? v[k] : v[2 * k] | v[2 * k + 1] << 16;
@@ -1013,8 +1070,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 if (!ok) break;
                 ++units;
                 tc_fence_after_sync();
-                const Odd<DP>& odd = rest.odd[n % kUnits];
-                const bool any = *reinterpret_cast<const volatile int*>(&odd.any) != 0;
                 const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
                 const int64_t t = u.token0 + token;
                 // (a query that sees nothing has its zeros already)
@@ -1025,16 +1080,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     uint32_t o[32];
                     __syncwarp();
                     tmem_load(t_out + c, o);
-                    if (any) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            float x = __uint_as_float(o[j]);
-                            if (odd.first[1][c + j] < limit) x += INFINITY;
-                            if (odd.first[2][c + j] < limit) x -= INFINITY;
-                            if (odd.first[0][c + j] < limit) x += NAN;
-                            o[j] = __float_as_uint(x);
-                        }
-                    }
                     if (whole) {
                         // Four neighbours turn their four pieces of 16 bytes each around, so that
                         // every store has 64 bytes of a query in a row.  (One query a lane: twice
@@ -1063,11 +1108,34 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     }
                 }
             }
+            if (steps > 0 && *reinterpret_cast<const volatile int*>(&rest.odd[n % kUnits].any) != 0) {
+                // What was not finite is added to what was written, in the dimensions it is in.
+                __syncwarp();
+                const Odd<DP>& odd = rest.odd[n % kUnits];
+                for (int d = 0; in && limit > 0 && d < a.c.head_dim; ++d) {
+                    float x = 0.f;
+                    if (odd.first[1][d] < limit) x += INFINITY;
+                    if (odd.first[2][d] < limit) x -= INFINITY;
+                    if (odd.first[0][d] < limit) x += NAN;
+                    if (x == 0.f) continue;
+                    if (whole) {
+                        T* o = reinterpret_cast<T*>(a.out) + (u.token0 + token) * a.out_row +
+                               h * a.out_head + d;
+                        *o = (T)((float)*o + x);
+                    } else {
+                        a.partial[((part * S::kTiles + q) * (DP / 4) + d / 4) * (4 * kQueryTile) + 4 * r +
+                                  d % 4] += x;
+                    }
+                }
+            }
             if (in && whole && limit > 0 && a.lse)
                 a.lse[(u.token0 + token) * a.q_heads + h] =
                     sum == 0.f ? -INFINITY : (top - kHeadroom + log2f(sum)) * kLn2;
             if (in && !whole)
                 a.partial_ml[part * S::kRows + q * kQueryTile + r] = make_float2(top - kHeadroom, sum);
+            step0 += u.steps;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(rest.unit_free[n % 2]));
         }
     }
     tc_fence_before_sync();
@@ -1093,8 +1161,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(ChunkArgs a) {
         const int head = (int)(item % a.c.kv_heads);
         const Joint joint = a.joints[item / a.c.kv_heads];
         const int64_t from = a.offset(joint.row), count = a.offset(joint.row + 1) - from;
-        const int lin = joint.tile * S::kRows + q * kQueryTile + r;
-        if (lin >= count * a.group.value) continue;
+        const int lin = (joint.tile * S::kTiles + q) * a.tile_rows + r;
+        if (r >= a.tile_rows || lin >= count * a.group.value) continue;
         const int token = a.group.quotient(lin), h = head * a.group.value + lin - token * a.group.value;
         if (a.length(joint.row) - count + token < 0) continue;  // zeros already
         const auto part = [&](int p) { return (int64_t)(joint.part + p) * a.c.kv_heads + head; };
@@ -1137,10 +1205,10 @@ struct Workspace {
 };
 Workspace plan_workspace(const w4a16_cache_shape& c, int64_t q_heads, int64_t tokens,
                          const DeviceCtx& ctx) {
-    const int64_t rows = rows_of(c.head_dim), dim = padded_dim(c.head_dim);
-    const int64_t group = q_heads / c.kv_heads;
+    const int64_t group = q_heads / c.kv_heads, dim = padded_dim(c.head_dim);
+    const int64_t rows = tiles_of(c.head_dim) * kQueryTile;
     Workspace w;
-    w.slot_count = tokens * group / rows + c.batch;
+    w.slot_count = tokens * group / (tiles_of(c.head_dim) * tile_rows_of(group)) + c.batch;
     // parts of all heads; items are at most slots, and a part has two steps or more
     const int64_t steps = (c.table_width * c.page_size + step_of(c.head_dim) - 1) / step_of(c.head_dim);
     w.most_parts = steps < 2 ? 0
@@ -1156,8 +1224,30 @@ Workspace plan_workspace(const w4a16_cache_shape& c, int64_t q_heads, int64_t to
     return w;
 }
 
+// Tensor maps of 128-byte rows, swizzled: sizes and byte strides from the second dimension on (a
+// dimension of size 1 gets a stride that will do).  False where the strides cannot be had.
+bool encode(CUtensorMap* map, bool half, const void* data, int rank, const int64_t* sizes,
+            const int64_t* strides, const uint32_t* box) {
+    const auto encoder = tensor_map_encoder();
+    if (!encoder) return false;
+    cuuint64_t dims[4], bytes[3];
+    cuuint32_t boxes[4], ones[4] = {1, 1, 1, 1};
+    for (int i = 0; i < rank; ++i) {
+        dims[i] = (cuuint64_t)sizes[i];
+        boxes[i] = box[i];
+        if (i) bytes[i - 1] = (cuuint64_t)(sizes[i] == 1 ? 16 : 2 * strides[i]);
+        if (i && (bytes[i - 1] == 0 || bytes[i - 1] >= (cuuint64_t)1 << 40)) return false;
+    }
+    return encoder(map, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                   (cuuint32_t)rank, const_cast<void*>(data), dims, bytes, boxes, ones,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename T, int DP>
-cudaError_t attend(const ChunkArgs& a, cudaStream_t stream, const DeviceCtx& ctx) {
+cudaError_t attend(ChunkArgs a, const w4a16_cache_shape& cache, cudaStream_t stream,
+                   const DeviceCtx& ctx) {
     using S = Shape<DP>;
     static std::once_flag once[64];
     static cudaError_t set[64];
@@ -1169,6 +1259,24 @@ cudaError_t attend(const ChunkArgs& a, cudaStream_t stream, const DeviceCtx& ctx
                                            cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     });
     if (set[device] != cudaSuccess) return set[device];
+    constexpr bool kHalf = std::is_same<T, __half>::value;
+    alignas(64) CUtensorMap maps[3] = {};
+    if (a.group.value <= kQueryTile) {
+        const int64_t sizes[3] = {a.c.head_dim, a.q_heads, a.tokens}, strides[3] = {1, a.q_head, a.q_row};
+        const uint32_t box[3] = {64, (uint32_t)a.group.value, (uint32_t)(a.tile_rows / a.group.value)};
+        a.q_map = encode(&maps[0], kHalf, a.q, 3, sizes, strides, box);
+    }
+    // boxes of 8 to 32 (16) rows: whole swizzled groups of eight, within a page and a warp's rows
+    uint32_t box_rows = S::kStep / kCopyWarps;
+    while (cache.page_size % box_rows) box_rows /= 2;
+    if (box_rows >= 8) {
+        const int64_t sizes[4] = {a.c.head_dim, cache.page_size, a.c.kv_heads, a.c.pages};
+        const int64_t strides[4] = {1, a.c.slot_stride, a.c.head_stride, a.c.page_stride};
+        const uint32_t box[4] = {64, box_rows, 1, 1};
+        if (encode(&maps[1], kHalf, a.k_pool, 4, sizes, strides, box) &&
+            encode(&maps[2], kHalf, a.v_pool, 4, sizes, strides, box))
+            a.box_rows = (int)box_rows;
+    }
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1178,11 +1286,12 @@ cudaError_t attend(const ChunkArgs& a, cudaStream_t stream, const DeviceCtx& ctx
     cfg.numAttrs = 1;
     cfg.gridDim = dim3(1);
     cfg.blockDim = dim3(kPlanThreads);
-    if ((e = cudaLaunchKernelEx(&cfg, plan_kernel, a, S::kRows, S::kStep)) != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, plan_kernel, a, S::kTiles * a.tile_rows, S::kStep)) != cudaSuccess) return e;
     cfg.gridDim = dim3((unsigned)ctx.num_sms);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = S::kSmem;
-    if ((e = cudaLaunchKernelEx(&cfg, chunk_kernel<T, DP>, a)) != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, chunk_kernel<T, DP>, maps[0], maps[1], maps[2], a)) != cudaSuccess)
+        return e;
     if (a.most_parts == 0) return cudaSuccess;
     cfg.gridDim = dim3((unsigned)(8 * ctx.num_sms));
     cfg.blockDim = dim3(kJoinThreads);
@@ -1191,11 +1300,12 @@ cudaError_t attend(const ChunkArgs& a, cudaStream_t stream, const DeviceCtx& ctx
 }
 
 template <typename T>
-cudaError_t attend(const ChunkArgs& a, cudaStream_t stream, const DeviceCtx& ctx) {
+cudaError_t attend(const ChunkArgs& a, const w4a16_cache_shape& cache, cudaStream_t stream,
+                   const DeviceCtx& ctx) {
     switch (padded_dim(a.c.head_dim)) {
-        case 64: return attend<T, 64>(a, stream, ctx);
-        case 128: return attend<T, 128>(a, stream, ctx);
-        default: return attend<T, 256>(a, stream, ctx);
+        case 64: return attend<T, 64>(a, cache, stream, ctx);
+        case 128: return attend<T, 128>(a, cache, stream, ctx);
+        default: return attend<T, 256>(a, cache, stream, ctx);
     }
 }
 
@@ -1245,8 +1355,10 @@ cudaError_t launch_paged_chunk_attention(const void* q, const void* k_pool, cons
     a.timeout_ns = ctx.timeout_ns;
     a.c = cache_of(cache);
     a.group = Divisor(query.q_heads / cache.kv_heads);
-    return cache.type == W4A16_BF16 ? attend<__nv_bfloat16>(a, stream, ctx)
-                                    : attend<__half>(a, stream, ctx);
+    a.tile_rows = tile_rows_of(a.group.value);
+    a.q_map = a.box_rows = 0;
+    return cache.type == W4A16_BF16 ? attend<__nv_bfloat16>(a, cache, stream, ctx)
+                                    : attend<__half>(a, cache, stream, ctx);
 }
 
 }  // namespace w4a16
