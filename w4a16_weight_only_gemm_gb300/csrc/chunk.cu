@@ -157,7 +157,7 @@ __device__ __forceinline__ int parts_of(int steps, int unit, float inverse) {
     return k;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a, int rows, int step) {
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a, Divisor rows, int step_bits) {
     static_assert(kPlanThreads == 1024, "32 warps: one for each length tried");
     __shared__ int64_t sums[32];
     __shared__ int ints[32];
@@ -173,7 +173,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a, int row
         for (int b = tid; b <= batch; b += kPlanThreads) staged[b] = (int32_t)a.offset(b);
     __syncthreads();
     const auto offset = [&](int b) { return short_batch ? (int64_t)staged[b] : a.offset(b); };
-    const auto key = [&](int b) { return offset(b) * a.group.value / rows + b; };
+    // (tokens * group is below 2^31)
+    const auto key = [&](int b) { return (int64_t)rows.quotient((int)offset(b) * a.group.value) + b; };
     int64_t total = 0;
     int longest = 0, items = 0;
     for (int64_t s = tid; s < a.slot_count; s += kPlanThreads) {
@@ -185,10 +186,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a, int row
         const int64_t from = offset(lo), count = max(offset(lo + 1) - from, (int64_t)0);
         const int64_t tile = s - key(lo);
         int steps = 0;
-        if (tile >= 0 && tile * rows < count * a.group.value) {
-            const int64_t end = min(count, ((tile + 1) * rows + a.group.value - 1) / a.group.value);
+        if (tile >= 0 && tile * rows.value < count * a.group.value) {
+            const int64_t end =
+                min(count, (int64_t)a.group.quotient((int)((tile + 1) * rows.value) + a.group.value - 1));
             const int64_t seen = a.length(lo) - count + end;  // positions of the item's last query
-            steps = seen > 0 ? (int)((seen + step - 1) / step) : 0;
+            steps = seen > 0 ? (int)((seen + (1 << step_bits) - 1) >> step_bits) : 0;
         }
         a.slots[s] = {lo, (int)tile, steps, 0};
         total += steps;
@@ -201,7 +203,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a, int row
     longest = block_reduce(longest, [](int x, int y) { return max(x, y); }, ints);
     // Slots are taken from the last to the first, so that a row's long items come first.  Cut are
     // those from the `keep`-th on, and those longer than `cap`.
-    const int cap = (int)max(total / a.sms, (int64_t)1);
+    const int cap = (int)fmaxf((float)total / (float)a.sms, 1.f);
+    // slots of as many items as make full rounds of the blocks
+    const int64_t full_rounds =
+        (int64_t)(floorf((float)item_count / (float)a.sms) * (float)a.sms / (float)heads);
     int unit = max(longest, 1);
     int64_t keep = a.slot_count;
     // (an item that is a small part of a block's share is not worth a cut)
@@ -213,7 +218,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a, int row
         float best = INFINITY;
         int64_t best_keep = 0;
         for (int rounds = 0; rounds < 2; ++rounds) {
-            const int64_t kept = rounds ? item_count / a.sms * a.sms / heads : 0;
+            const int64_t kept = rounds ? full_rounds : 0;
             if (rounds && kept == 0) break;
             int64_t whole = 0, whole_steps = 0, parts = 0;
             for (int64_t r = lane; r < a.slot_count; r += 32) {
@@ -233,7 +238,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a, int row
             float cost = work / sms + (float)(u + kUnitCost) / 2;
             if (whole) {  // rounds of whole items
                 const float mean = (float)whole_steps / (float)whole + kUnitCost;
-                cost = fmaxf(cost, (float)((whole * heads + a.sms - 1) / a.sms) * mean);
+                cost = fmaxf(cost, ceilf((float)(whole * heads) / sms) * mean);
             }
             if (parts) cost += 2.f;  // the join
             if (parts * heads <= a.most_parts && cost < best) best = cost, best_keep = kept;
@@ -292,9 +297,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a, int row
         if (k > 1) {
             const int64_t part = base_parts + (upto >> 32);
             a.joints[base_joints + joint_upto] = {slot.row, slot.tile, (int)part, k};
-            for (int i = 0; i < k; ++i) {
-                const int from = (int)((int64_t)slot.steps * i / k), to = (int)((int64_t)slot.steps * (i + 1) / k);
-                a.entries[whole + part + i] = {slot.row, slot.tile, from, to - from, (int)(part + i), {}};
+            // lengths differ by a step at most
+            const int each = slot.steps / k, more = slot.steps - each * k;
+            for (int i = 0, at = 0; i < k; ++i) {
+                const int n = each + (i < more);
+                a.entries[whole + part + i] = {slot.row, slot.tile, at, n, (int)(part + i), {}};
+                at += n;
             }
         }
         base_whole += (uint32_t)all;
@@ -322,6 +330,20 @@ __device__ __forceinline__ void copy_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+// A whole warp's wait, in little code: there are two dozen of them, and code that is run once a
+// unit comes from L2 each time.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t phase, uint64_t timeout_ns,
+                                          unsigned* status) {
+    if (__all_sync(~0u, mbar_try_wait(bar, phase & 1))) return true;
+    const uint64_t since = global_timer_ns();
+#pragma unroll 1
+    do {
+        if (__all_sync(~0u, mbar_try_wait(bar, phase & 1))) return true;
+    } while (__any_sync(~0u, global_timer_ns() - since < timeout_ns));
+    atomicOr(status, kDevTimeout);
+    return false;
+}
+
 // Tensor-map loads by one elected lane of a warp that is together (see the MMAs below).
 __device__ __forceinline__ void box_load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1,
                                             int c2, uint32_t bar) {
@@ -340,6 +362,12 @@ __device__ __forceinline__ void box_load_4d(uint32_t dst, const CUtensorMap* map
         "[%0], [%1, {%2, %3, %4, %5}], [%6];\n\t}" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
         : "memory");
+}
+
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float m;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
+    return m;
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -456,14 +484,13 @@ __device__ __forceinline__ uint32_t desc_mn_major(uint32_t smem_addr, uint32_t b
     return smem_addr >> 4 | block >> 4 << 16;
 }
 
-// tcgen05.ld, and the wait for it (one statement: nothing may use r in between).
+// tcgen05.ld; its registers are to be used behind tmem_ld_wait and tmem_loaded only.
 __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
         "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
         "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31 "
-        "}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
+        "}, [%32];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
           "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
@@ -478,8 +505,7 @@ __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[64]) {
         "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
         "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
         "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63 "
-        "}, [%64];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
+        "}, [%64];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
           "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
@@ -491,6 +517,14 @@ __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[64]) {
         : "r"(taddr)
         : "memory");
 }
+// The wait for all loads so far.  What they loaded goes through `loaded` behind it, so that nothing
+// uses it before.
+template <int N>
+__device__ __forceinline__ void tmem_loaded(uint32_t (&r)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -597,8 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // Waits for unit number n and reads it; false where there is none, or the wait gave up.
     const auto next_unit = [&](uint32_t n, Unit& u) {
-        bool ok = mbar_wait(bar(rest.unit_full[n % 2]), n / 2 % 2, a.timeout_ns, a.status);
-        ok = __all_sync(~0u, ok);
+        const bool ok = warp_wait(bar(rest.unit_full[n % 2]), n / 2, a.timeout_ns, a.status);
         u.steps = -1;
         if (ok) u = rest.unit[n % 2];
         __syncwarp();
@@ -652,9 +685,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     u.length = a.length(entry.row);
                     u.position0 = u.length - count;
                 }
-                const bool ok = n < 2 || mbar_wait(bar(rest.unit_free[n % 2]), (n / 2 - 1) % 2,
-                                                   a.timeout_ns, a.status);
-                if (!__all_sync(~0u, ok)) break;
+                if (n >= 2 && !warp_wait(bar(rest.unit_free[n % 2]), n / 2 - 1, a.timeout_ns, a.status))
+                    break;
                 Odd<DP>& odd = rest.odd[n % kUnits];
                 for (int x = lane; x < 3 * DP; x += 32) (&odd.first[0][0])[x] = INT32_MAX;
                 if (lane == 0) {
@@ -679,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Unit u;
             bool ok = true;
             const auto wait = [&](uint64_t& b, uint32_t phase) {
-                if (ok) ok = __all_sync(~0u, mbar_wait(bar(b), phase & 1, a.timeout_ns, a.status));
+                if (ok) ok = warp_wait(bar(b), phase, a.timeout_ns, a.status);
             };
             // Reports the MMAs issued so far, and passes on (by an arrival of this thread) what the
             // copying warps wrote.
@@ -746,8 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // nothing in flight when the block ends
             mma_commit(bar(rest.done));
-            mbar_wait(bar(rest.done), 0, drain_bound(a.timeout_ns), a.status);
-            __syncwarp();
+            warp_wait(bar(rest.done), 0, drain_bound(a.timeout_ns), a.status);
         } else {
             // ============================== looking =============================
             constexpr uint32_t kExponent = kHalf ? 0x7C00u : 0x7F80u;
@@ -760,8 +791,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < u.steps; ++i, ++step) {
                     // (every step's, so that the barriers' phases are followed one by one)
                     const uint32_t v = 2 * step + 1, slot = v % kSlots;
-                    ok = mbar_wait(bar(rest.kv_full[slot]), v / kSlots & 1, a.timeout_ns, a.status);
-                    ok = __all_sync(~0u, ok);
+                    ok = warp_wait(bar(rest.kv_full[slot]), v / kSlots, a.timeout_ns, a.status);
                     if (!ok) break;
                     if (i < looked_from) {
                         if (lane == 0) mbar_arrive(bar(rest.kv_free[slot]));
@@ -828,8 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Unit u;
         bool ok = true;
         const auto wait = [&](uint64_t& b, uint32_t phase) {
-            const bool got = mbar_wait(bar(b), phase & 1, a.timeout_ns, a.status);
-            ok = __all_sync(~0u, got);
+            ok = warp_wait(bar(b), phase, a.timeout_ns, a.status);
         };
         for (uint32_t n = 0; ok && next_unit(n, u); ++n) {
             const int64_t head = (int64_t)u.head * a.c.head_stride;
@@ -941,15 +970,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int per = 32 * 4 * S::kTiles;
             const int x = threadIdx.x;
             const auto zero = [&](int64_t from, int64_t to) {  // tokens, by all the softmax threads
-                const int64_t work = (to - from) * a.q_heads;
-                for (int64_t i = x; i < work; i += per) {
-                    const int64_t t = from + i / a.q_heads;
-                    const int h = (int)(i % a.q_heads);
-                    uint16_t* o = a.out + t * a.out_row + h * a.out_head;
-                    for (int y = 0; y < a.c.head_dim; y += 8)
-                        *reinterpret_cast<uint4*>(o + y) = make_uint4(0, 0, 0, 0);
-                    if (a.lse) a.lse[t * a.q_heads + h] = -INFINITY;
-                }
+                for (int64_t t = from; t < to; ++t)
+                    for (int h = x; h < a.q_heads; h += per) {
+                        uint16_t* o = a.out + t * a.out_row + h * a.out_head;
+#pragma unroll 1
+                        for (int y = 0; y < a.c.head_dim; y += 8)
+                            *reinterpret_cast<uint4*>(o + y) = make_uint4(0, 0, 0, 0);
+                        if (a.lse) a.lse[t * a.q_heads + h] = -INFINITY;
+                    }
             };
             for (int b = blockIdx.x; b < a.c.batch; b += gridDim.x) {
                 const int64_t from = a.offset(b), count = a.offset(b + 1) - from;
@@ -965,8 +993,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
         for (uint32_t n = 0;; ++n) {
-            ok = mbar_wait(bar(rest.unit_full[n % 2]), n / 2 % 2, a.timeout_ns, a.status);
-            ok = __all_sync(~0u, ok);
+            ok = warp_wait(bar(rest.unit_full[n % 2]), n / 2, a.timeout_ns, a.status);
             // (stays where it is until the unit is done: the scores take most registers)
             const Unit& u = rest.unit[n % 2];
             if (!ok || u.steps < 0) break;
@@ -979,11 +1006,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int least = __reduce_min_sync(~0u, limit);
             const int first = u.first;
             float top = -INFINITY;
-            float2 sum2 = make_float2(0.f, 0.f);
+            float2 sum2 = make_float2(0.f, 0.f), more2 = sum2;
 #pragma unroll 1
             for (int i = 0; i < steps; ++i) {
-                ok = mbar_wait(bar(rest.s_full[q]), taken & 1, a.timeout_ns, a.status);
-                ok = __all_sync(~0u, ok);
+                ok = warp_wait(bar(rest.s_full[q]), taken, a.timeout_ns, a.status);
                 if (!ok) break;
                 ++taken;
                 tc_fence_after_sync();
@@ -991,6 +1017,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t part[S::kStep / 64][64];
 #pragma unroll
                 for (int k = 0; k < S::kStep / 64; ++k) tmem_load(t_scores + 64 * k, part[k]);
+                tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < S::kStep / 64; ++k) tmem_loaded(part[k]);
                 const auto s = [&](int j) { return __uint_as_float(part[j / 64][j % 64]); };
                 const uint32_t* v = rest.valid[(step0 + i) % 4];
                 bool whole = least - position >= S::kStep;
@@ -1017,21 +1046,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < S::kStep; j += 8)
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
-                        high[x] = fmaxf(fmaxf(high[x], s(j + 2 * x)), s(j + 2 * x + 1));
-                float highest = fmaxf(fmaxf(high[0], high[1]), fmaxf(high[2], high[3]));
+                        high[x] = max3(high[x], s(j + 2 * x), s(j + 2 * x + 1));
+                float highest = fmaxf(max3(high[0], high[1], high[2]), high[3]);
                 highest = highest == -INFINITY ? highest : highest * a.scale_log2;
                 if (__any_sync(~0u, highest > top + kSlack)) {
                     // (each query by its own: what the others see makes no difference to it)
                     const float higher = highest > top + kSlack ? highest : top;
                     const float keep = higher == top ? 1.f : exp2_fast(top - higher);
                     top = higher;
-                    sum2.x *= keep, sum2.y *= keep;
+                    sum2.x *= keep, sum2.y *= keep, more2.x *= keep, more2.y *= keep;
                     if (i > 0) {
                         // (the scores are there, so the MMAs before them are done)
 #pragma unroll 1
                         for (int c = 0; c < DP; c += 32) {
                             uint32_t o[32];
                             tmem_load(t_out + c, o);
+                            tmem_ld_wait();
+                            tmem_loaded(o);
 #pragma unroll
                             for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * keep);
                             tmem_st_32x32b_x32(t_out + c, o);
@@ -1048,7 +1079,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float2 x =
                             __ffma2_rn(make_float2(s(32 * k + j), s(32 * k + j + 1)), scale2, down2);
                         const float2 e = make_float2(exp2_fast(x.x), exp2_fast(x.y));
-                        sum2 = __fadd2_rn(sum2, e);
+                        float2& to = j % 4 ? more2 : sum2;
+                        to = __fadd2_rn(to, e);
                         p[j / 2] = pack2<T>(e.x, e.y);
                     }
                     tmem_st_32x32b_x16(t_scores + 16 * k, p);
@@ -1061,12 +1093,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (!ok) break;
-            const float sum = sum2.x + sum2.y;
+            const float sum = (sum2.x + sum2.y) + (more2.x + more2.y);
             const bool whole = u.part < 0;
             const int64_t part = whole ? 0 : (int64_t)u.part * a.c.kv_heads + u.head;
             if (steps > 0) {
-                ok = mbar_wait(bar(rest.o_full[q]), units & 1, a.timeout_ns, a.status);
-                ok = __all_sync(~0u, ok);
+                ok = warp_wait(bar(rest.o_full[q]), units, a.timeout_ns, a.status);
                 if (!ok) break;
                 ++units;
                 tc_fence_after_sync();
@@ -1075,34 +1106,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // (a query that sees nothing has its zeros already)
                 uint16_t* mine = in && limit > 0 ? a.out + t * a.out_row + h * a.out_head : nullptr;
                 float* part_to = a.partial + ((part * S::kTiles + q) * (DP / 4) * kQueryTile + r) * 4;
+                uint16_t* there[4];  // of the four neighbours' queries
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    there[j] = reinterpret_cast<uint16_t*>(
+                        __shfl_sync(~0u, reinterpret_cast<uint64_t>(mine), lane / 4 * 4 + j));
 #pragma unroll 1
-                for (int c = 0; c < DP; c += 32) {
-                    uint32_t o[32];
+                for (int c = 0; c < DP; c += 64) {
+                    uint32_t o[64];
                     __syncwarp();
                     tmem_load(t_out + c, o);
+                    tmem_ld_wait();
+                    tmem_loaded(o);
                     if (whole) {
                         // Four neighbours turn their four pieces of 16 bytes each around, so that
                         // every store has 64 bytes of a query in a row.  (One query a lane: twice
                         // the sectors, and 4000 cycles for a unit's output.)
-                        uint4 v[4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            v[j] = make_uint4(
-                                pack2<T>(__uint_as_float(o[8 * j]) * inv, __uint_as_float(o[8 * j + 1]) * inv),
-                                pack2<T>(__uint_as_float(o[8 * j + 2]) * inv, __uint_as_float(o[8 * j + 3]) * inv),
-                                pack2<T>(__uint_as_float(o[8 * j + 4]) * inv, __uint_as_float(o[8 * j + 5]) * inv),
-                                pack2<T>(__uint_as_float(o[8 * j + 6]) * inv, __uint_as_float(o[8 * j + 7]) * inv));
-                        turn4(v, lane);
+                        for (int k = 0; k < 64; k += 32) {
+                            uint4 v[4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {  // of query j of the four
-                            uint16_t* there = reinterpret_cast<uint16_t*>(
-                                __shfl_sync(~0u, reinterpret_cast<uint64_t>(mine), lane / 4 * 4 + j));
-                            if (there && c + lane % 4 * 8 < a.c.head_dim)
-                                *reinterpret_cast<uint4*>(there + c + lane % 4 * 8) = v[j];
+                            for (int j = 0; j < 4; ++j) {
+                                const auto two = [&](int x) {
+                                    return pack2<T>(__uint_as_float(o[k + 8 * j + x]) * inv,
+                                                    __uint_as_float(o[k + 8 * j + x + 1]) * inv);
+                                };
+                                v[j] = make_uint4(two(0), two(2), two(4), two(6));
+                            }
+                            turn4(v, lane);
+                            const int x = c + k + lane % 4 * 8;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                if (there[j] && x < a.c.head_dim) *reinterpret_cast<uint4*>(there[j] + x) = v[j];
                         }
                     } else if (in) {
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4)
+                        for (int j = 0; j < 64; j += 4)
                             *reinterpret_cast<uint4*>(part_to + (int64_t)(c + j) * kQueryTile) =
                                 make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
                     }
@@ -1154,12 +1193,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(ChunkArgs a) {
     grid_dependency_wait();
     grid_launch_dependents();
     const int pieces = a.c.head_dim / 8, r = threadIdx.x;
-    const int64_t work = (int64_t)a.plan->joints * a.c.kv_heads * S::kTiles * pieces;
-    for (int64_t i = blockIdx.x; i < work; i += gridDim.x) {
-        const int piece = (int)(i % pieces), q = (int)(i / pieces % S::kTiles);
-        const int64_t item = i / pieces / S::kTiles;
-        const int head = (int)(item % a.c.kv_heads);
-        const Joint joint = a.joints[item / a.c.kv_heads];
+    const int work = a.plan->joints * a.c.kv_heads * S::kTiles * pieces;
+    for (int i = blockIdx.x; i < work; i += gridDim.x) {
+        const int piece = i % pieces, tile = i / pieces, q = tile % S::kTiles, item = tile / S::kTiles;
+        const int which = item / a.c.kv_heads, head = item - which * a.c.kv_heads;
+        const Joint joint = a.joints[which];
         const int64_t from = a.offset(joint.row), count = a.offset(joint.row + 1) - from;
         const int lin = (joint.tile * S::kTiles + q) * a.tile_rows + r;
         if (r >= a.tile_rows || lin >= count * a.group.value) continue;
@@ -1286,7 +1324,8 @@ cudaError_t attend(ChunkArgs a, const w4a16_cache_shape& cache, cudaStream_t str
     cfg.numAttrs = 1;
     cfg.gridDim = dim3(1);
     cfg.blockDim = dim3(kPlanThreads);
-    if ((e = cudaLaunchKernelEx(&cfg, plan_kernel, a, S::kTiles * a.tile_rows, S::kStep)) != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, plan_kernel, a, Divisor(S::kTiles * a.tile_rows),
+                                S::kStep == 128 ? 7 : 6)) != cudaSuccess) return e;
     cfg.gridDim = dim3((unsigned)ctx.num_sms);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = S::kSmem;
