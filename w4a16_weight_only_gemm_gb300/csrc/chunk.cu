@@ -77,18 +77,26 @@ constexpr int step_of(int64_t dim) { return dim <= 128 ? 128 : 64; }
 // are parts of `joints` items.
 struct Plan {
     int whole, parts, joints;
-    unsigned next;  // unit to hand out
+    unsigned next;  // unit to hand out after each block's first
+};
+// An item: its row, the row's first token and its position (below 0 for a row with more tokens than
+// positions), the row's length, and its queries, first and count, in the row's list.
+struct Item {
+    int row, token0, position0, length, lin0, lins;
 };
 struct Entry {
-    int row, tile, first, steps;  // steps first .. first + steps - 1 of item `tile` of `row`
-    int part;                     // its place among the parts, -1: a whole item
+    Item item;
+    int first, steps;  // steps first .. first + steps - 1
+    int part;          // its place among the parts, -1: a whole item
     int unused[3];
 };
 struct Joint {
-    int row, tile, part, count;
+    Item item;
+    int part, count;
 };
 struct Slot {
-    int row, tile, steps, unused;
+    Item item;
+    int steps, unused;
 };
 
 struct ChunkArgs {
@@ -137,19 +145,6 @@ struct ChunkArgs {
 // ---------------------------------------------------------------------------
 constexpr int kUnitCost = 2, kStaged = 2048;
 
-template <typename V, typename F>
-__device__ __forceinline__ V block_reduce(V v, F f, V* space) {
-#pragma unroll
-    for (int d = 16; d > 0; d /= 2) v = f(v, __shfl_xor_sync(~0u, v, d));
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) space[threadIdx.x / 32] = v;
-    __syncthreads();
-    v = space[threadIdx.x % 32];
-#pragma unroll
-    for (int d = 16; d > 0; d /= 2) v = f(v, __shfl_xor_sync(~0u, v, d));
-    return v;
-}
-
 __device__ __forceinline__ int parts_of(int steps, int unit, float inverse) {
     int k = (int)((float)steps * inverse);  // ceil(steps / unit), or one more for very many
     k += (int64_t)k * unit < steps;
@@ -157,75 +152,93 @@ __device__ __forceinline__ int parts_of(int steps, int unit, float inverse) {
     return k;
 }
 
+// (Loops are not unrolled: it runs once, and its time is mostly that of fetching its code.)
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a, Divisor rows, int step_bits) {
     static_assert(kPlanThreads == 1024, "32 warps: one for each length tried");
     __shared__ int64_t sums[32];
-    __shared__ int ints[32];
+    __shared__ int longests[32], ints[32];
     __shared__ int32_t staged[kStaged + 1];
     __shared__ float costs[32];
     __shared__ int units[32], keeps[32];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     grid_dependency_wait();
     grid_launch_dependents();
-    const int heads = a.c.kv_heads, batch = a.c.batch;
+    const int heads = a.c.kv_heads, batch = a.c.batch, group = a.group.value;
+    const int slots = (int)a.slot_count;
     const bool short_batch = batch <= kStaged;
     if (short_batch)
+#pragma unroll 1
         for (int b = tid; b <= batch; b += kPlanThreads) staged[b] = (int32_t)a.offset(b);
     __syncthreads();
-    const auto offset = [&](int b) { return short_batch ? (int64_t)staged[b] : a.offset(b); };
+    const auto offset = [&](int b) { return short_batch ? staged[b] : (int)a.offset(b); };
     // (tokens * group is below 2^31)
-    const auto key = [&](int b) { return (int64_t)rows.quotient((int)offset(b) * a.group.value) + b; };
+    const auto key = [&](int b) { return rows.quotient(offset(b) * group) + b; };
     int64_t total = 0;
     int longest = 0, items = 0;
-    for (int64_t s = tid; s < a.slot_count; s += kPlanThreads) {
+#pragma unroll 1
+    for (int s = tid; s < slots; s += kPlanThreads) {
         int lo = 0, hi = batch;  // key(lo) <= s < key(hi)
+#pragma unroll 1
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
             if (key(mid) <= s) lo = mid; else hi = mid;
         }
-        const int64_t from = offset(lo), count = max(offset(lo + 1) - from, (int64_t)0);
-        const int64_t tile = s - key(lo);
-        int steps = 0;
-        if (tile >= 0 && tile * rows.value < count * a.group.value) {
-            const int64_t end =
-                min(count, (int64_t)a.group.quotient((int)((tile + 1) * rows.value) + a.group.value - 1));
-            const int64_t seen = a.length(lo) - count + end;  // positions of the item's last query
-            steps = seen > 0 ? (int)((seen + (1 << step_bits) - 1) >> step_bits) : 0;
+        const int from = offset(lo), count = max(offset(lo + 1) - from, 0), length = (int)a.length(lo);
+        const int tile = s - key(lo), lins = count * group;
+        Slot slot = {{lo, from, length - count, length, 0, 0}, 0, 0};
+        if (tile >= 0 && (int64_t)tile * rows.value < lins) {
+            slot.item.lin0 = tile * rows.value;
+            slot.item.lins = min(rows.value, lins - slot.item.lin0);
+            // positions of the item's last query
+            const int last = a.group.quotient(slot.item.lin0 + slot.item.lins - 1);
+            const int64_t seen = (int64_t)slot.item.position0 + last + 1;
+            slot.steps = seen > 0 ? (int)((seen + (1 << step_bits) - 1) >> step_bits) : 0;
         }
-        a.slots[s] = {lo, (int)tile, steps, 0};
-        total += steps;
-        items += steps > 0;
-        longest = max(longest, steps);
+        a.slots[s] = slot;
+        total += slot.steps;
+        items += slot.steps > 0;
+        longest = max(longest, slot.steps);
     }
-    const auto add = [](auto x, auto y) { return x + y; };
-    total = block_reduce(total, add, sums) * heads;
-    const int64_t item_count = block_reduce((int64_t)items, add, sums) * heads;
-    longest = block_reduce(longest, [](int x, int y) { return max(x, y); }, ints);
+#pragma unroll 1
+    for (int level = 0; level < 2; ++level) {  // over the warp, then over the warps
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) {
+            total += __shfl_xor_sync(~0u, total, d);
+            items += __shfl_xor_sync(~0u, items, d);
+            longest = max(longest, __shfl_xor_sync(~0u, longest, d));
+        }
+        if (level) break;
+        if (lane == 0) sums[warp] = total, ints[warp] = items, longests[warp] = longest;
+        __syncthreads();
+        total = sums[lane], items = ints[lane], longest = longests[lane];
+    }
+    total *= heads;
     // Slots are taken from the last to the first, so that a row's long items come first.  Cut are
     // those from the `keep`-th on, and those longer than `cap`.
-    const int cap = (int)fmaxf((float)total / (float)a.sms, 1.f);
-    // slots of as many items as make full rounds of the blocks
-    const int64_t full_rounds =
-        (int64_t)(floorf((float)item_count / (float)a.sms) * (float)a.sms / (float)heads);
-    int unit = max(longest, 1);
-    int64_t keep = a.slot_count;
+    const float sms = (float)a.sms, share = (float)total / sms;
+    const int cap = (int)fmaxf(share, 1.f);
+    int unit = max(longest, 1), keep = slots;
     // (an item that is a small part of a block's share is not worth a cut)
-    if ((int64_t)longest * 8 * a.sms > total && a.most_parts > 0) {
+    if ((float)longest * 8.f > share && a.most_parts > 0) {
+        // as many as make full rounds of the blocks
+        const int full_rounds = (int)(floorf((float)items * (float)heads / sms) * sms / (float)heads);
         // k = 1, 2, 3, ... 8, then some 2^(1/4) apart up to 512
         const int k = warp < 8 ? warp + 1 : (int)(8.f * exp2f((float)(warp - 7) * 0.25f));
         const int u = (longest + k - 1) / k;
         const float inverse = 1.f / (float)u;
         float best = INFINITY;
-        int64_t best_keep = 0;
-        for (int rounds = 0; rounds < 2; ++rounds) {
-            const int64_t kept = rounds ? full_rounds : 0;
-            if (rounds && kept == 0) break;
-            int64_t whole = 0, whole_steps = 0, parts = 0;
-            for (int64_t r = lane; r < a.slot_count; r += 32) {
-                const int n = a.slots[a.slot_count - 1 - r].steps;
+        int best_keep = 0;
+#pragma unroll 1
+        for (int round = 0; round < (full_rounds ? 2 : 1); ++round) {
+            const int kept = round ? full_rounds : 0;
+            float whole = 0.f, whole_steps = 0.f;
+            int parts = 0;
+#pragma unroll 1
+            for (int r = lane; r < slots; r += 32) {
+                const int n = a.slots[slots - 1 - r].steps;
                 const int p = r >= kept || n > cap ? parts_of(n, u, inverse) : n > 0;
                 if (p > 1) parts += p;
-                if (p == 1) ++whole, whole_steps += n;
+                if (p == 1) whole += 1.f, whole_steps += (float)n;
             }
 #pragma unroll
             for (int d = 16; d > 0; d /= 2) {
@@ -233,17 +246,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a, Divisor
                 whole_steps += __shfl_xor_sync(~0u, whole_steps, d);
                 parts += __shfl_xor_sync(~0u, parts, d);
             }
-            const float sms = (float)a.sms;
-            const float work = (float)total + (float)(kUnitCost * (whole + parts) * heads + parts * heads);
+            const float all_parts = (float)parts * (float)heads, all_whole = whole * (float)heads;
+            const float work = (float)total + kUnitCost * all_whole + (kUnitCost + 1) * all_parts;
             float cost = work / sms + (float)(u + kUnitCost) / 2;
-            if (whole) {  // rounds of whole items
-                const float mean = (float)whole_steps / (float)whole + kUnitCost;
-                cost = fmaxf(cost, ceilf((float)(whole * heads) / sms) * mean);
-            }
+            if (whole > 0.f)  // rounds of whole items
+                cost = fmaxf(cost, ceilf(all_whole / sms) * (whole_steps / whole + kUnitCost));
             if (parts) cost += 2.f;  // the join
-            if (parts * heads <= a.most_parts && cost < best) best = cost, best_keep = kept;
+            if ((int64_t)parts * heads <= a.most_parts && cost < best) best = cost, best_keep = kept;
         }
-        if (lane == 0) costs[warp] = best, units[warp] = u, keeps[warp] = (int)best_keep;
+        if (lane == 0) costs[warp] = best, units[warp] = u, keeps[warp] = best_keep;
         __syncthreads();
         float least = costs[lane];
         int which = lane;
@@ -255,61 +266,53 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a, Divisor
         }
         if (least < INFINITY) unit = units[which], keep = keeps[which];
     }
-    const auto cut = [&](int64_t r, int n) {
-        return n == 0 ? 0 : r >= keep || n > cap ? (n + unit - 1) / unit : 1;
-    };
-    // How many there are whole; then the entries.
-    int64_t whole = 0;
-    for (int64_t r = tid; r < a.slot_count; r += kPlanThreads)
-        whole += cut(r, a.slots[a.slot_count - 1 - r].steps) == 1;
-    whole = block_reduce(whole, add, sums);
-    int64_t base_whole = 0, base_parts = 0;
-    int base_joints = 0;
-    for (int64_t first = 0; first < a.slot_count; first += kPlanThreads) {
-        const int64_t r = first + tid;
+    // The entries: whole ones from the table's start, parts from place `slots` on.
+    int base_whole = 0, base_parts = 0, base_joints = 0;
+#pragma unroll 1
+    for (int first = 0; first < slots; first += kPlanThreads) {
+        const int r = first + tid;
         Slot slot = {};
-        if (r < a.slot_count) slot = a.slots[a.slot_count - 1 - r];
-        const int k = cut(r, slot.steps);
-        // whole ones in the low half, parts in the high one
-        int64_t both = (k == 1) + ((int64_t)(k > 1 ? k : 0) << 32), upto = both;
-        int joint = k > 1, joint_upto = joint;
+        if (r < slots) slot = a.slots[slots - 1 - r];
+        const int n = slot.steps;
+        const int k = n == 0 ? 0 : r >= keep || n > cap ? (n + unit - 1) / unit : 1;
+        // before this slot: whole ones, joints (16 bits each: 1024 slots at most), parts
+        const int own = (k == 1) | (k > 1) << 16, own_parts = k > 1 ? k : 0;
+        int upto = own, upto_parts = own_parts;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
-            const int64_t o = __shfl_up_sync(~0u, upto, d);
-            const int j = __shfl_up_sync(~0u, joint_upto, d);
-            if (lane >= d) upto += o, joint_upto += j;
+            const int o = __shfl_up_sync(~0u, upto, d), p = __shfl_up_sync(~0u, upto_parts, d);
+            if (lane >= d) upto += o, upto_parts += p;
         }
         __syncthreads();
-        if (lane == 31) sums[warp] = upto, ints[warp] = joint_upto;
+        if (lane == 31) ints[warp] = upto, longests[warp] = upto_parts;
         __syncthreads();
-        int64_t all = sums[lane], before = lane < warp ? all : 0;
-        int all_joints = ints[lane], before_joints = lane < warp ? all_joints : 0;
+        int all = ints[lane], before = lane < warp ? all : 0;
+        int all_parts = longests[lane], before_parts = lane < warp ? all_parts : 0;
 #pragma unroll
         for (int d = 16; d > 0; d /= 2) {
             all += __shfl_xor_sync(~0u, all, d);
             before += __shfl_xor_sync(~0u, before, d);
-            all_joints += __shfl_xor_sync(~0u, all_joints, d);
-            before_joints += __shfl_xor_sync(~0u, before_joints, d);
+            all_parts += __shfl_xor_sync(~0u, all_parts, d);
+            before_parts += __shfl_xor_sync(~0u, before_parts, d);
         }
-        upto += before - both;
-        joint_upto += before_joints - joint;
-        if (k == 1) a.entries[base_whole + (uint32_t)upto] = {slot.row, slot.tile, 0, slot.steps, -1, {}};
-        if (k > 1) {
-            const int64_t part = base_parts + (upto >> 32);
-            a.joints[base_joints + joint_upto] = {slot.row, slot.tile, (int)part, k};
-            // lengths differ by a step at most
-            const int each = slot.steps / k, more = slot.steps - each * k;
-            for (int i = 0, at = 0; i < k; ++i) {
-                const int n = each + (i < more);
-                a.entries[whole + part + i] = {slot.row, slot.tile, at, n, (int)(part + i), {}};
-                at += n;
-            }
+        upto += before - own;
+        upto_parts += before_parts - own_parts;
+        const int part = base_parts + upto_parts;
+        if (k > 1) a.joints[base_joints + (upto >> 16)] = {slot.item, part, k};
+        // (lengths of parts differ by a step at most)
+        const int each = k > 1 ? n / k : n, more = n - each * k;
+#pragma unroll 1
+        for (int i = 0, at = 0; i < k; ++i) {
+            const int steps = each + (i < more);
+            a.entries[k > 1 ? slots + part + i : base_whole + (upto & 0xFFFF)] = {
+                slot.item, at, steps, k > 1 ? part + i : -1, {}};
+            at += steps;
         }
-        base_whole += (uint32_t)all;
-        base_parts += all >> 32;
-        base_joints += all_joints;
+        base_whole += all & 0xFFFF;
+        base_parts += all_parts;
+        base_joints += all >> 16;
     }
-    if (tid == 0) *a.plan = {(int)base_whole, (int)base_parts, base_joints, 0};
+    if (tid == 0) *a.plan = {base_whole, base_parts, base_joints, 0};
 }
 
 // ---------------------------------------------------------------------------
@@ -553,11 +556,8 @@ __device__ __forceinline__ void tmem_st_wait() {
 // ---------------------------------------------------------------------------
 // A unit of work as every warp reads it.
 struct Unit {
-    int row, head, first, steps, part;  // steps < 0: no more units
-    int lin0, lins;        // queries of the item: first and count, in the row's list
-    int64_t token0;        // the row's first token
-    int64_t position0;     // its position (below 0 for a row with more tokens than positions)
-    int64_t length;        // positions of the row
+    Item item;
+    int head, first, steps, part;  // steps < 0: no more units
 };
 
 // Values that are not finite, in steps that some of the item's queries see in part: the first
@@ -594,7 +594,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
     Rest<DP>& rest = *reinterpret_cast<Rest<DP>*>(smem + S::kOffRest);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    // (by a shuffle, so that a warp is known to take one way together: its addresses and loop counts
+    // stay in uniform registers, which the MMAs want; without it 1 row of 2048 after 129023 takes
+    // 2.80 ms for 2.56)
+    const int warp = __shfl_sync(~0u, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const auto bar = [&](const uint64_t& b) { return smem_u32(&b); };
 
     if (threadIdx.x == 0) {
@@ -624,7 +627,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&rest.tmem);
+    // All 512 columns are this block's, so that they begin at address 0, a constant in what follows.
+    constexpr uint32_t tmem = 0;
+    const bool fits = *reinterpret_cast<volatile uint32_t*>(&rest.tmem) == tmem;
     grid_dependency_wait();
     grid_launch_dependents();
     const int group = a.group.value;
@@ -634,56 +639,52 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool ok = warp_wait(bar(rest.unit_full[n % 2]), n / 2, a.timeout_ns, a.status);
         u.steps = -1;
         if (ok) u = rest.unit[n % 2];
+        u.steps = __shfl_sync(~0u, u.steps, 0), u.first = __shfl_sync(~0u, u.first, 0);
+        u.item.lin0 = __shfl_sync(~0u, u.item.lin0, 0), u.item.lins = __shfl_sync(~0u, u.item.lins, 0);
+        u.item.position0 = __shfl_sync(~0u, u.item.position0, 0), u.head = __shfl_sync(~0u, u.head, 0);
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(bar(rest.unit_free[n % 2]));
         return u.steps > 0;
     };
     // Steps that tile q of a unit takes part in.
     const auto steps_of = [&](const Unit& u, int q) {
-        const int end = min(u.lins, (q + 1) * a.tile_rows);
+        const int end = min(u.item.lins, (q + 1) * a.tile_rows);
         if (end <= q * a.tile_rows) return 0;
-        const int64_t seen = u.position0 + a.group.quotient(u.lin0 + end - 1) + 1;
+        const int64_t seen = (int64_t)u.item.position0 + a.group.quotient(u.item.lin0 + end - 1) + 1;
         const int64_t steps = seen > 0 ? (seen + S::kStep - 1) / S::kStep : 0;
         return (int)min(max(steps - u.first, (int64_t)0), (int64_t)u.steps);
     };
     // The first step of a unit that some of its queries do not see whole.
     const auto part_seen_from = [&](const Unit& u) {
-        const int64_t all = max(u.position0 + a.group.quotient(u.lin0) + 1, (int64_t)0);
+        const int64_t all = max((int64_t)u.item.position0 + a.group.quotient(u.item.lin0) + 1, (int64_t)0);
         return (int)min(max(all / S::kStep - u.first, (int64_t)0), (int64_t)u.steps);
     };
 
-    if (warp >= kMmaWarp) {
+    if (!fits) {
+        if (threadIdx.x == 0) atomicOr(a.status, kDevBadLaunch);
+    } else if (warp >= kMmaWarp) {
         registers_down();
         if (warp == kUnitWarp) {
             // ============================== units ===============================
             const unsigned whole = (unsigned)a.plan->whole, parts = (unsigned)a.plan->parts;
             const unsigned heads = (unsigned)a.c.kv_heads;
             for (uint32_t n = 0;; ++n) {
-                unsigned i = 0;
-                if (lane == 0) i = atomicAdd(&a.plan->next, 1u);
-                i = __shfl_sync(~0u, i, 0);
+                unsigned i = blockIdx.x;
+                if (n) {
+                    if (lane == 0) i = gridDim.x + atomicAdd(&a.plan->next, 1u);
+                    i = __shfl_sync(~0u, i, 0);
+                }
                 Unit u = {};
                 u.steps = -1;
                 if (i < (whole + parts) * heads) {
-                    unsigned e;
-                    if (i < whole * heads) {
-                        u.head = (int)(i / whole);
-                        e = i % whole;
-                    } else {
-                        u.head = (int)((i - whole * heads) / parts);
-                        e = whole + (i - whole * heads) % parts;
-                    }
-                    const Entry entry = a.entries[e];
-                    const int64_t from = a.offset(entry.row), count = a.offset(entry.row + 1) - from;
-                    u.row = entry.row;
+                    const bool part = i >= whole * heads;
+                    const unsigned j = part ? i - whole * heads : i, of = part ? parts : whole;
+                    u.head = (int)(j / of);
+                    const Entry entry = a.entries[(part ? a.slot_count : 0) + j % of];
+                    u.item = entry.item;
                     u.first = entry.first;
                     u.steps = entry.steps;
                     u.part = entry.part;
-                    u.lin0 = entry.tile * S::kTiles * a.tile_rows;
-                    u.lins = (int)min((int64_t)S::kTiles * a.tile_rows, count * group - u.lin0);
-                    u.token0 = from;
-                    u.length = a.length(entry.row);
-                    u.position0 = u.length - count;
                 }
                 if (n >= 2 && !warp_wait(bar(rest.unit_free[n % 2]), n / 2 - 1, a.timeout_ns, a.status))
                     break;
@@ -705,74 +706,77 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t values = umma_idesc_f16_f32(kQueryTile, DP) | kType | (1u << 16);  // V: MN-major
             const uint32_t q_desc = desc_k_major(base), k_desc = desc_k_major(base + S::kOffRing);
             const uint32_t v_desc = desc_mn_major(base + S::kOffRing, S::kStep * 128);
-            uint32_t step = 0;         // of the block, for the ring's slots
-            uint32_t taken[2] = {0, 0};  // steps of each tile
-            uint32_t looks[2] = {0, 0};  // at each slot of values
+            uint32_t step = 0;         // of the block, whose keys come next: for the ring's slots
+            uint32_t taken = 0;        // steps of each tile, modulo 2: a bit each
+            uint32_t looks = 0;        // looks at each slot of values, modulo 2
             Unit u;
             bool ok = true;
             const auto wait = [&](uint64_t& b, uint32_t phase) {
                 if (ok) ok = warp_wait(bar(b), phase, a.timeout_ns, a.status);
             };
-            // Reports the MMAs issued so far, and passes on (by an arrival of this thread) what the
-            // copying warps wrote.
-            const auto finished = [&](uint64_t& b) {
-                mma_commit(bar(b));
-                if (lane == 0) mbar_arrive(bar(b));
-            };
-            const auto score = [&](int q, uint32_t slot) {
-                const uint32_t qa = q_desc + q * (S::kTileBytes >> 4);
-                const uint32_t ka = k_desc + slot * (S::kSlotBytes >> 4);
-#pragma unroll
-                for (int j = 0; j < DP / 64; ++j)
-                    mma_ss_64(tmem + q * 128, qa + j * (kQueryTile * 8), ka + j * (S::kStep * 8), scores,
-                              j != 0);
-                finished(rest.s_full[q]);
-            };
+            // Keys of step i of a unit, against the queries of every tile that takes part; then the
+            // values of the step before, as each tile's weights come.  (One loop for all of it: the
+            // code of this warp, unrolled over tiles, was a third of the kernel's.)
             for (uint32_t n = 0; ok && next_unit(n, u); ++n) {
-                const int steps[2] = {steps_of(u, 0), S::kTiles == 2 ? steps_of(u, 1) : 0};
+                const int steps0 = steps_of(u, 0), steps1 = S::kTiles == 2 ? steps_of(u, 1) : 0;
                 const int looked_from = part_seen_from(u);
                 wait(rest.q_full, n);
-                wait(rest.kv_full[2 * step % kSlots], 2 * step / kSlots);
-                if (!ok) break;
-                fence_proxy_async_smem();
-#pragma unroll
-                for (int q = 0; q < S::kTiles; ++q)
-                    if (steps[q] > 0) score(q, 2 * step % kSlots);
-                mma_commit(bar(rest.kv_free[2 * step % kSlots]));
-                if (u.steps == 1) mma_commit(bar(rest.q_free));
-                for (int i = 0; i < u.steps; ++i, ++step) {
-                    const uint32_t v = 2 * step + 1, k = 2 * step + 2;
-                    if (i < looked_from)
+#pragma unroll 1
+                for (int i = -1; ok && i < u.steps; ++i) {
+                    const uint32_t v = 2 * step - 1, k = 2 * step;  // of steps i and i + 1
+                    if (i >= looked_from) {
+                        wait(rest.looked[v % kSlots], looks >> (v % kSlots / 2));
+                        looks ^= 1u << (v % kSlots / 2);
+                    } else if (i >= 0) {
                         wait(rest.kv_full[v % kSlots], v / kSlots);
-                    else
-                        wait(rest.looked[v % kSlots], looks[v % kSlots / 2]++);
+                    }
                     if (i + 1 < u.steps) wait(rest.kv_full[k % kSlots], k / kSlots);
                     fence_proxy_async_smem();
 #pragma unroll
                     for (int q = 0; q < S::kTiles; ++q) {
-                        if (i >= steps[q]) continue;
-                        const uint32_t va = v_desc + v % kSlots * (S::kSlotBytes >> 4);
-                        // the first half of the weights, while the second is still made
+                        const int steps = q ? steps1 : steps0;
+                        if (i >= steps) continue;
+                        if (i >= 0) {
+                            // the first half of the weights, while the second is still made
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            wait(rest.p_full[q][half], taken[q]);
+                            for (int half = 0; half < 2; ++half) {
+                                wait(rest.p_full[q][half], taken >> q);
+                                if (!ok) break;
+                                tc_fence_after_sync();
+                                const uint32_t va = v_desc + v % kSlots * (S::kSlotBytes >> 4) +
+                                                    half * (S::kStep / 2 * 128 >> 4);
+                                const uint32_t pa = tmem + q * 128 + half * (S::kStep / 4);
+#pragma unroll
+                                for (int j = 0; j < S::kStep / 64; ++j)
+                                    mma_ts_32(tmem + S::kOutColumn + q * DP, pa + 16 * j, va + j * (4096 >> 4),
+                                              values, (i | half | j) != 0);
+                            }
                             if (!ok) break;
-                            tc_fence_after_sync();
-#pragma unroll
-                            for (int j = half * S::kStep / 64; j < (half + 1) * S::kStep / 64; ++j)
-                                mma_ts_32(tmem + S::kOutColumn + q * DP, tmem + q * 128 + 16 * j,
-                                          va + j * (4096 >> 4), values, (i | j) != 0);
+                            taken ^= 1u << q;
                         }
-                        if (!ok) break;
-                        ++taken[q];
-                        if (i + 1 < steps[q])
-                            score(q, k % kSlots);
-                        else
-                            finished(rest.o_full[q]);
+                        const bool more = i + 1 < steps;
+                        if (more) {
+                            const uint32_t qa = q_desc + q * (S::kTileBytes >> 4);
+                            const uint32_t ka = k_desc + k % kSlots * (S::kSlotBytes >> 4);
+#pragma unroll
+                            for (int j = 0; j < DP / 64; ++j)
+                                mma_ss_64(tmem + q * 128, qa + j * (kQueryTile * 8), ka + j * (S::kStep * 8),
+                                          scores, j != 0);
+                        }
+                        if (more || i >= 0) {
+                            // reports the MMAs issued so far, and passes on (by an arrival of this
+                            // thread) what the copying warps wrote
+                            const uint32_t to = more ? bar(rest.s_full[q]) : bar(rest.o_full[q]);
+                            mma_commit(to);
+                            if (lane == 0) mbar_arrive(to);
+                        }
                     }
                     if (!ok) break;
-                    mma_commit(bar(rest.kv_free[v % kSlots]));
-                    if (i + 1 < u.steps) mma_commit(bar(rest.kv_free[k % kSlots]));
+                    if (i >= 0) mma_commit(bar(rest.kv_free[v % kSlots]));
+                    if (i + 1 < u.steps) {
+                        mma_commit(bar(rest.kv_free[k % kSlots]));
+                        ++step;
+                    }
                     if (i + 2 == u.steps) mma_commit(bar(rest.q_free));
                 }
             }
@@ -862,14 +866,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         for (uint32_t n = 0; ok && next_unit(n, u); ++n) {
             const int64_t head = (int64_t)u.head * a.c.head_stride;
-            const int32_t* table = a.tables + u.row * a.c.table_stride;
+            const int32_t* table = a.tables + u.item.row * a.c.table_stride;
             // this lane's position in step i, and its page
             const auto position_of = [&](int i) {
                 return (int64_t)(u.first + i) * S::kStep + w * kRowsWarp + lane % kRowsWarp;
             };
             const auto page_of = [&](int i) {
                 const int64_t p = position_of(i);
-                return p < u.length ? table[a.c.page_size.quotient((int)p)] : -1;
+                return p < u.item.length ? table[a.c.page_size.quotient((int)p)] : -1;
             };
             int next = page_of(0);
             for (int i = 0; i < u.steps; ++i, ++step) {
@@ -918,7 +922,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     const uint32_t queries = bar(rest.q_full);
                     if (a.q_map) {
-                        const int tiles = u.lins > a.tile_rows ? 2 : 1;
+                        const int tiles = u.item.lins > a.tile_rows ? 2 : 1;
                         if (lane == 0) {
                             if (w)
                                 mbar_arrive(queries);
@@ -926,7 +930,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 mbar_arrive_expect_tx(queries, tiles * a.tile_rows * DP * 2);
                         }
                         __syncwarp();
-                        const int token = (int)u.token0 + a.group.quotient(u.lin0);
+                        const int token = (int)(int64_t)u.item.token0 + a.group.quotient(u.item.lin0);
                         const int tokens = a.group.quotient(a.tile_rows);
                         for (int q = 0; w == 0 && q < tiles; ++q)
 #pragma unroll
@@ -934,14 +938,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 box_load_3d(base + q * S::kTileBytes + x * (kQueryTile * 128), &q_map, 64 * x,
                                             u.head * group, token + q * tokens, queries);
                     } else {
-                        const uint16_t* q0 = a.q + u.token0 * a.q_row + (int64_t)u.head * group * a.q_head;
+                        const uint16_t* q0 = a.q + (int64_t)u.item.token0 * a.q_row + (int64_t)u.head * group * a.q_head;
 #pragma unroll 1
                         for (int r = w * (S::kRows / kCopyWarps) + row0; r < (w + 1) * (S::kRows / kCopyWarps);
                              r += kRowsPass) {
                             const int row = r % kQueryTile, lin = r / kQueryTile * a.tile_rows + row;
-                            const bool in = row < a.tile_rows && lin < u.lins && in_dim;
-                            const int token = a.group.quotient(u.lin0 + lin);
-                            const int h = u.lin0 + lin - token * group;
+                            const bool in = row < a.tile_rows && lin < u.item.lins && in_dim;
+                            const int token = a.group.quotient(u.item.lin0 + lin);
+                            const int h = u.item.lin0 + lin - token * group;
                             copy16(base + r / kQueryTile * S::kTileBytes + at(row, kQueryTile),
                                    in ? q0 + token * a.q_row + h * a.q_head + 8 * piece : a.q, in);
                         }
@@ -966,28 +970,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t t_scores = tmem + lanes + q * 128;
         const uint32_t t_out = tmem + lanes + S::kOutColumn + q * DP;
         // What no unit writes: tokens of no row, or of positions below 0.
-        {
-            const int per = 32 * 4 * S::kTiles;
-            const int x = threadIdx.x;
-            const auto zero = [&](int64_t from, int64_t to) {  // tokens, by all the softmax threads
-                for (int64_t t = from; t < to; ++t)
-                    for (int h = x; h < a.q_heads; h += per) {
-                        uint16_t* o = a.out + t * a.out_row + h * a.out_head;
+        // (a row's are a block's; those before the first row and behind the last are dealt out)
 #pragma unroll 1
-                        for (int y = 0; y < a.c.head_dim; y += 8)
-                            *reinterpret_cast<uint4*>(o + y) = make_uint4(0, 0, 0, 0);
-                        if (a.lse) a.lse[t * a.q_heads + h] = -INFINITY;
-                    }
-            };
-            for (int b = blockIdx.x; b < a.c.batch; b += gridDim.x) {
-                const int64_t from = a.offset(b), count = a.offset(b + 1) - from;
-                const int64_t below = count - a.length(b);
-                if (below > 0) zero(from, from + min(below, count));
+        for (int64_t b = blockIdx.x;; b += gridDim.x) {
+            const bool row = b < a.c.batch;
+            const int64_t from = a.offset(row ? (int)b : 0), to = a.offset(row ? (int)b + 1 : a.c.batch);
+            // of a row: the tokens below position 0; else all but those from `from` up to `to`
+            const int64_t count = row ? min(max(to - from - a.length((int)b), (int64_t)0), to - from)
+                                      : a.tokens - max(to - from, (int64_t)0);
+#pragma unroll 1
+            for (int64_t i = row ? 0 : blockIdx.x; i < count; i += row ? 1 : gridDim.x) {
+                const int64_t t = row ? from + i : i < from ? i : i + to - from;
+#pragma unroll 1
+                for (int x = threadIdx.x; x < a.q_heads; x += 128 * S::kTiles) {
+                    uint16_t* o = a.out + t * a.out_row + x * a.out_head;
+#pragma unroll 1
+                    for (int y = 0; y < a.c.head_dim; y += 8)
+                        *reinterpret_cast<uint4*>(o + y) = make_uint4(0, 0, 0, 0);
+                    if (a.lse) a.lse[t * a.q_heads + x] = -INFINITY;
+                }
             }
-            const int64_t before = a.offset(0), behind = a.tokens - a.offset(a.c.batch);
-            for (int64_t t = blockIdx.x; t < before; t += gridDim.x) zero(t, t + 1);
-            for (int64_t t = blockIdx.x; t < behind; t += gridDim.x)
-                zero(a.tokens - 1 - t, a.tokens - t);
+            if (!row) break;
         }
         uint32_t taken = 0, units = 0, step0 = 0;  // steps and units of this tile, steps of the block
         bool ok = true;
@@ -997,12 +1000,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             // (stays where it is until the unit is done: the scores take most registers)
             const Unit& u = rest.unit[n % 2];
             if (!ok || u.steps < 0) break;
-            const int steps = steps_of(u, q);
-            const int lin = u.lin0 + q * a.tile_rows + r;
-            const bool in = r < a.tile_rows && q * a.tile_rows + r < u.lins;
+            const int steps = __shfl_sync(~0u, steps_of(u, q), 0);
+            const int lin = u.item.lin0 + q * a.tile_rows + r;
+            const bool in = r < a.tile_rows && q * a.tile_rows + r < u.item.lins;
             const int token = a.group.quotient(lin), h = u.head * group + lin - token * group;
             // positions that the query sees; all, for a row that is not there
-            const int limit = in ? (int)max(u.position0 + token + 1, (int64_t)0) : INT32_MAX;
+            const int limit = in ? max(u.item.position0 + token + 1, 0) : INT32_MAX;
             const int least = __reduce_min_sync(~0u, limit);
             const int first = u.first;
             float top = -INFINITY;
@@ -1102,7 +1105,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++units;
                 tc_fence_after_sync();
                 const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
-                const int64_t t = u.token0 + token;
+                const int64_t t = (int64_t)u.item.token0 + token;
                 // (a query that sees nothing has its zeros already)
                 uint16_t* mine = in && limit > 0 ? a.out + t * a.out_row + h * a.out_head : nullptr;
                 float* part_to = a.partial + ((part * S::kTiles + q) * (DP / 4) * kQueryTile + r) * 4;
@@ -1112,37 +1115,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                     there[j] = reinterpret_cast<uint16_t*>(
                         __shfl_sync(~0u, reinterpret_cast<uint64_t>(mine), lane / 4 * 4 + j));
 #pragma unroll 1
-                for (int c = 0; c < DP; c += 64) {
-                    uint32_t o[64];
+                for (int c = 0; c < DP; c += 32) {
+                    uint32_t o[32];
                     __syncwarp();
                     tmem_load(t_out + c, o);
                     tmem_ld_wait();
                     tmem_loaded(o);
                     if (whole) {
                         // Four neighbours turn their four pieces of 16 bytes each around, so that
-                        // every store has 64 bytes of a query in a row.  (One query a lane: twice
-                        // the sectors, and 4000 cycles for a unit's output.)
+                        // every store has 64 bytes of a query in a row: half the sectors.
+                        uint4 v[4];
 #pragma unroll
-                        for (int k = 0; k < 64; k += 32) {
-                            uint4 v[4];
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const auto two = [&](int x) {
-                                    return pack2<T>(__uint_as_float(o[k + 8 * j + x]) * inv,
-                                                    __uint_as_float(o[k + 8 * j + x + 1]) * inv);
-                                };
-                                v[j] = make_uint4(two(0), two(2), two(4), two(6));
-                            }
-                            turn4(v, lane);
-                            const int x = c + k + lane % 4 * 8;
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                if (there[j] && x < a.c.head_dim) *reinterpret_cast<uint4*>(there[j] + x) = v[j];
+                        for (int j = 0; j < 4; ++j) {
+                            const auto two = [&](int x) {
+                                return pack2<T>(__uint_as_float(o[8 * j + x]) * inv,
+                                                __uint_as_float(o[8 * j + x + 1]) * inv);
+                            };
+                            v[j] = make_uint4(two(0), two(2), two(4), two(6));
                         }
-                    } else if (in) {
+                        turn4(v, lane);
+                        const int x = c + lane % 4 * 8;
 #pragma unroll
-                        for (int j = 0; j < 64; j += 4)
-                            *reinterpret_cast<uint4*>(part_to + (int64_t)(c + j) * kQueryTile) =
+                        for (int j = 0; j < 4; ++j)
+                            if (there[j] && x < a.c.head_dim) *reinterpret_cast<uint4*>(there[j] + x) = v[j];
+                    } else if (in) {
+                        float* to = part_to + (int64_t)c * kQueryTile;
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4)
+                            *reinterpret_cast<uint4*>(to + j * kQueryTile) =
                                 make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
                     }
                 }
@@ -1158,7 +1158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (odd.first[0][d] < limit) x += NAN;
                     if (x == 0.f) continue;
                     if (whole) {
-                        T* o = reinterpret_cast<T*>(a.out) + (u.token0 + token) * a.out_row +
+                        T* o = reinterpret_cast<T*>(a.out) + ((int64_t)u.item.token0 + token) * a.out_row +
                                h * a.out_head + d;
                         *o = (T)((float)*o + x);
                     } else {
@@ -1168,7 +1168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (in && whole && limit > 0 && a.lse)
-                a.lse[(u.token0 + token) * a.q_heads + h] =
+                a.lse[((int64_t)u.item.token0 + token) * a.q_heads + h] =
                     sum == 0.f ? -INFINITY : (top - kHeadroom + log2f(sum)) * kLn2;
             if (in && !whole)
                 a.partial_ml[part * S::kRows + q * kQueryTile + r] = make_float2(top - kHeadroom, sum);
@@ -1180,7 +1180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+    if (warp == kMmaWarp) tmem_dealloc(*reinterpret_cast<volatile uint32_t*>(&rest.tmem), 512);
 }
 
 // ---------------------------------------------------------------------------
@@ -1198,11 +1198,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(ChunkArgs a) {
         const int piece = i % pieces, tile = i / pieces, q = tile % S::kTiles, item = tile / S::kTiles;
         const int which = item / a.c.kv_heads, head = item - which * a.c.kv_heads;
         const Joint joint = a.joints[which];
-        const int64_t from = a.offset(joint.row), count = a.offset(joint.row + 1) - from;
-        const int lin = (joint.tile * S::kTiles + q) * a.tile_rows + r;
-        if (r >= a.tile_rows || lin >= count * a.group.value) continue;
+        const int of_item = q * a.tile_rows + r;
+        if (r >= a.tile_rows || of_item >= joint.item.lins) continue;
+        const int lin = joint.item.lin0 + of_item;
         const int token = a.group.quotient(lin), h = head * a.group.value + lin - token * a.group.value;
-        if (a.length(joint.row) - count + token < 0) continue;  // zeros already
+        if (joint.item.position0 + token < 0) continue;  // zeros already
         const auto part = [&](int p) { return (int64_t)(joint.part + p) * a.c.kv_heads + head; };
         float top = -INFINITY;
         for (int p = 0; p < joint.count; ++p)
@@ -1223,7 +1223,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(ChunkArgs a) {
             v[4] += e * y.x, v[5] += e * y.y, v[6] += e * y.z, v[7] += e * y.w;
         }
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int64_t t = from + token;
+        const int64_t t = joint.item.token0 + token;
         *reinterpret_cast<uint4*>(a.out + t * a.out_row + h * a.out_head + 8 * piece) =
             make_uint4(pack2<T>(v[0] * inv, v[1] * inv), pack2<T>(v[2] * inv, v[3] * inv),
                        pack2<T>(v[4] * inv, v[5] * inv), pack2<T>(v[6] * inv, v[7] * inv));
