@@ -19,6 +19,8 @@
 //   warp 13          takes the next unit of work
 //   warps 14, 15     look for values that are not finite where some queries see a
 //                    step in part
+// An item of one tile has both softmax groups all the same: they take its steps in turn, and
+// what the second has is added to the first's at the end.
 // The work is cut by a plan kernel, as only the device knows the lengths: items are
 // split into parts where that levels the load, and a join kernel adds those up.
 // Blocks take units from a counter, longest first within a row, the parts of one
@@ -573,10 +575,11 @@ template <int DP>
 struct Rest {
     uint64_t unit_full[2], unit_free[2], q_full, q_free;
     uint64_t kv_full[kSlots], kv_free[kSlots], looked[kSlots];
-    uint64_t s_full[2], p_full[2][2], o_full[2], done;
+    uint64_t s_full[2], p_full[2][2], o_full[2], other_full, other_free, done;
     uint32_t tmem;
     uint32_t valid[4][4];  // of a step, a bit a position (step / 4 a word)
     Unit unit[2];
+    float2 other[kQueryTile];  // maxima and sums of the second group's steps of the first tile
     Odd<DP> odd[kUnits];
 };
 
@@ -617,6 +620,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bar(rest.kv_free[i]), i % 2 ? 1 + kLookWarps : 1);  // values: also the lookers'
             mbar_init(bar(rest.looked[i]), kLookWarps);
         }
+        mbar_init(bar(rest.other_full), 4);
+        mbar_init(bar(rest.other_free), 4);
         mbar_init(bar(rest.done), 1);
         fence_barrier_init();
     }
@@ -654,6 +659,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t steps = seen > 0 ? (seen + S::kStep - 1) / S::kStep : 0;
         return (int)min(max(steps - u.first, (int64_t)0), (int64_t)u.steps);
     };
+    // Whether the two softmax groups share the one tile of a unit.
+    const auto one_tile = [&](const Unit& u) { return S::kTiles == 2 && u.item.lins <= a.tile_rows; };
     // The first step of a unit that some of its queries do not see whole.
     const auto part_seen_from = [&](const Unit& u) {
         const int64_t all = max((int64_t)u.item.position0 + a.group.quotient(u.item.lin0) + 1, (int64_t)0);
@@ -706,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t values = umma_idesc_f16_f32(kQueryTile, DP) | kType | (1u << 16);  // V: MN-major
             const uint32_t q_desc = desc_k_major(base), k_desc = desc_k_major(base + S::kOffRing);
             const uint32_t v_desc = desc_mn_major(base + S::kOffRing, S::kStep * 128);
-            uint32_t step = 0;         // of the block, whose keys come next: for the ring's slots
+            uint32_t step = 0;         // the unit's first of the block, for the ring's slots
             uint32_t taken = 0;        // steps of each tile, modulo 2: a bit each
             uint32_t looks = 0;        // looks at each slot of values, modulo 2
             Unit u;
@@ -714,28 +721,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             const auto wait = [&](uint64_t& b, uint32_t phase) {
                 if (ok) ok = warp_wait(bar(b), phase, a.timeout_ns, a.status);
             };
-            // Keys of step i of a unit, against the queries of every tile that takes part; then the
-            // values of the step before, as each tile's weights come.  (One loop for all of it: the
-            // code of this warp, unrolled over tiles, was a third of the kernel's.)
+            // The values of step i, as each tile's weights come, then the keys of the next step of that
+            // tile.  (One loop for all of it: this code, unrolled over starts and ends too, was a
+            // third of the kernel's.)
             for (uint32_t n = 0; ok && next_unit(n, u); ++n) {
-                const int steps0 = steps_of(u, 0), steps1 = S::kTiles == 2 ? steps_of(u, 1) : 0;
+                const bool shared = one_tile(u);
+                const int ahead = shared ? 2 : 1;
+                const int steps0 = steps_of(u, 0);
+                const int steps1 = shared ? steps0 : S::kTiles == 2 ? steps_of(u, 1) : 0;
                 const int looked_from = part_seen_from(u);
                 wait(rest.q_full, n);
 #pragma unroll 1
-                for (int i = -1; ok && i < u.steps; ++i) {
-                    const uint32_t v = 2 * step - 1, k = 2 * step;  // of steps i and i + 1
+                for (int i = -ahead; ok && i < u.steps; ++i) {
+                    const int next = i + ahead;
+                    const uint32_t v = 2 * (step + i) + 1, k = 2 * (step + next);
                     if (i >= looked_from) {
                         wait(rest.looked[v % kSlots], looks >> (v % kSlots / 2));
                         looks ^= 1u << (v % kSlots / 2);
                     } else if (i >= 0) {
                         wait(rest.kv_full[v % kSlots], v / kSlots);
                     }
-                    if (i + 1 < u.steps) wait(rest.kv_full[k % kSlots], k / kSlots);
+                    if (next < u.steps) wait(rest.kv_full[k % kSlots], k / kSlots);
                     fence_proxy_async_smem();
 #pragma unroll
                     for (int q = 0; q < S::kTiles; ++q) {
                         const int steps = q ? steps1 : steps0;
-                        if (i >= steps) continue;
+                        if (i >= steps || (shared && (i & 1) != q)) continue;
                         if (i >= 0) {
                             // the first half of the weights, while the second is still made
 #pragma unroll
@@ -749,14 +760,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                                 for (int j = 0; j < S::kStep / 64; ++j)
                                     mma_ts_32(tmem + S::kOutColumn + q * DP, pa + 16 * j, va + j * (4096 >> 4),
-                                              values, (i | half | j) != 0);
+                                              values, i >= ahead || (half | j) != 0);
                             }
                             if (!ok) break;
                             taken ^= 1u << q;
                         }
-                        const bool more = i + 1 < steps;
+                        const bool more = next < steps;
                         if (more) {
-                            const uint32_t qa = q_desc + q * (S::kTileBytes >> 4);
+                            const uint32_t qa = q_desc + (shared ? 0 : q * (S::kTileBytes >> 4));
                             const uint32_t ka = k_desc + k % kSlots * (S::kSlotBytes >> 4);
 #pragma unroll
                             for (int j = 0; j < DP / 64; ++j)
@@ -773,12 +784,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (!ok) break;
                     if (i >= 0) mma_commit(bar(rest.kv_free[v % kSlots]));
-                    if (i + 1 < u.steps) {
-                        mma_commit(bar(rest.kv_free[k % kSlots]));
-                        ++step;
-                    }
-                    if (i + 2 == u.steps) mma_commit(bar(rest.q_free));
+                    if (next < u.steps) mma_commit(bar(rest.kv_free[k % kSlots]));
+                    if (next + 1 == u.steps) mma_commit(bar(rest.q_free));
                 }
+                step += u.steps;
             }
             // nothing in flight when the block ends
             mma_commit(bar(rest.done));
@@ -875,19 +884,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int64_t p = position_of(i);
                 return p < u.item.length ? table[a.c.page_size.quotient((int)p)] : -1;
             };
-            int next = page_of(0);
-            for (int i = 0; i < u.steps; ++i, ++step) {
-                const int page = next, in_page = a.c.page_size.remainder((int)position_of(i));
-                const bool there = (uint32_t)page < (uint32_t)a.c.pages;
-                const uint32_t all = __ballot_sync(~0u, there);
+            // Keys and values in turn; where two groups share a tile, the keys a step further ahead.
+            const int lag = one_tile(u) ? 1 : 0;
+            int next = page_of(0), behind = -1;  // pages of the step to come, and of the one before
+            for (int i = 0; i < u.steps + lag; ++i) {
+                const int now = next;
                 if (i + 1 < u.steps) next = page_of(i + 1);
 #pragma unroll 1
                 for (int value = 0; value < 2; ++value) {
-                    const uint32_t g = 2 * step + value, slot = g % kSlots;
+                    const int of = value ? i - lag : i;  // the step
+                    if (of < 0 || of >= u.steps) continue;
+                    const int page = value && lag ? behind : now;
+                    const int in_page = a.c.page_size.remainder((int)position_of(of));
+                    const bool there = (uint32_t)page < (uint32_t)a.c.pages;
+                    const uint32_t all = __ballot_sync(~0u, there);
+                    const uint32_t g = 2 * (step + of) + value, slot = g % kSlots;
                     if (g >= kSlots) wait(rest.kv_free[slot], g / kSlots - 1);
                     if (!ok) break;
                     if (!value && lane == 0)
-                        rest.valid[step % 4][w] =
+                        rest.valid[(step + of) % 4][w] =
                             kRowsWarp == 32 ? all : all & ((1u << kRowsWarp % 32) - 1);
                     const uint32_t to = base + S::kOffRing + slot * S::kSlotBytes;
                     const uint32_t full = bar(rest.kv_full[slot]);
@@ -896,11 +911,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         __syncwarp();
                         fence_proxy_async_smem();  // (rows of the slot that were written one by one)
                         for (int r = 0; r < kRowsWarp; r += a.box_rows) {
-                            const int in_box = __shfl_sync(~0u, in_page, r), of = __shfl_sync(~0u, page, r);
+                            const int in_box = __shfl_sync(~0u, in_page, r), box = __shfl_sync(~0u, page, r);
 #pragma unroll
                             for (int x = 0; x < DP / 64; ++x)
                                 box_load_4d(to + x * S::kStep * 128 + (w * kRowsWarp + r) * 128,
-                                            value ? &v_map : &k_map, 64 * x, in_box, u.head, of, full);
+                                            value ? &v_map : &k_map, 64 * x, in_box, u.head, box, full);
                         }
                     } else {
                         const uint16_t* pool = (value ? a.v_pool : a.k_pool) + 8 * piece;
@@ -954,7 +969,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     copy_arrive(queries);
                 }
                 if (!ok) break;
+                behind = now;
             }
+            step += u.steps;
         }
         copy_commit();
         copy_wait<0>();
@@ -992,7 +1009,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!row) break;
         }
-        uint32_t taken = 0, units = 0, step0 = 0;  // steps and units of this tile, steps of the block
+        // steps and units of this group, joined units, steps of the block
+        uint32_t taken = 0, units = 0, joins = 0, step0 = 0;
         bool ok = true;
         const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
         for (uint32_t n = 0;; ++n) {
@@ -1000,14 +1018,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             // (stays where it is until the unit is done: the scores take most registers)
             const Unit& u = rest.unit[n % 2];
             if (!ok || u.steps < 0) break;
-            const int steps = __shfl_sync(~0u, steps_of(u, q), 0);
-            const int lin = u.item.lin0 + q * a.tile_rows + r;
-            const bool in = r < a.tile_rows && q * a.tile_rows + r < u.item.lins;
+            // steps first, first + stride, ... of the unit are this group's
+            const bool shared = one_tile(u);
+            const int tile = shared ? 0 : q, stride = shared ? 2 : 1;
+            int steps = __shfl_sync(~0u, steps_of(u, tile), 0);
+            const bool joined = shared && steps > 1;
+            if (shared) steps = (steps + 1 - q) / 2;
+            const int lin = u.item.lin0 + tile * a.tile_rows + r;
+            const bool in = r < a.tile_rows && tile * a.tile_rows + r < u.item.lins;
             const int token = a.group.quotient(lin), h = u.head * group + lin - token * group;
             // positions that the query sees; all, for a row that is not there
             const int limit = in ? max(u.item.position0 + token + 1, 0) : INT32_MAX;
             const int least = __reduce_min_sync(~0u, limit);
-            const int first = u.first;
+            const int first = u.first + (shared ? q : 0);
             float top = -INFINITY;
             float2 sum2 = make_float2(0.f, 0.f), more2 = sum2;
 #pragma unroll 1
@@ -1016,7 +1039,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 ++taken;
                 tc_fence_after_sync();
-                const int position = (first + i) * S::kStep;
+                const int position = (first + i * stride) * S::kStep;
                 uint32_t part[S::kStep / 64][64];
 #pragma unroll
                 for (int k = 0; k < S::kStep / 64; ++k) tmem_load(t_scores + 64 * k, part[k]);
@@ -1024,7 +1047,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int k = 0; k < S::kStep / 64; ++k) tmem_loaded(part[k]);
                 const auto s = [&](int j) { return __uint_as_float(part[j / 64][j % 64]); };
-                const uint32_t* v = rest.valid[(step0 + i) % 4];
+                const uint32_t* v = rest.valid[(step0 + (shared ? q : 0) + i * stride) % 4];
                 bool whole = least - position >= S::kStep;
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
@@ -1096,7 +1119,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (!ok) break;
-            const float sum = (sum2.x + sum2.y) + (more2.x + more2.y);
+            float sum = (sum2.x + sum2.y) + (more2.x + more2.y);
             const bool whole = u.part < 0;
             const int64_t part = whole ? 0 : (int64_t)u.part * a.c.kv_heads + u.head;
             if (steps > 0) {
@@ -1104,11 +1127,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 ++units;
                 tc_fence_after_sync();
+            }
+            if (shared && q == 1) {
+                // The second group's part is the first's to write; its output must stay until then.
+                if (joined) {
+                    rest.other[r] = make_float2(top, sum);
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(rest.other_full));
+                    ok = warp_wait(bar(rest.other_free), joins, a.timeout_ns, a.status);
+                    if (!ok) break;
+                    ++joins;
+                }
+            } else if (steps > 0) {
+                float keep = 1.f, add = 0.f;  // of this group's part, of the other's
+                if (joined) {
+                    ok = warp_wait(bar(rest.other_full), joins, a.timeout_ns, a.status);
+                    if (!ok) break;
+                    ++joins;
+                    tc_fence_after_sync();
+                    const float2 other = rest.other[r];
+                    const float higher = fmaxf(top, other.x), base_exp = higher == -INFINITY ? 0.f : higher;
+                    keep = exp2_fast(top - base_exp);
+                    add = exp2_fast(other.x - base_exp);
+                    sum = keep * sum + add * other.y;
+                    top = higher;
+                }
                 const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
                 const int64_t t = (int64_t)u.item.token0 + token;
                 // (a query that sees nothing has its zeros already)
                 uint16_t* mine = in && limit > 0 ? a.out + t * a.out_row + h * a.out_head : nullptr;
-                float* part_to = a.partial + ((part * S::kTiles + q) * (DP / 4) * kQueryTile + r) * 4;
+                float* part_to = a.partial + ((part * S::kTiles + tile) * (DP / 4) * kQueryTile + r) * 4;
                 uint16_t* there[4];  // of the four neighbours' queries
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -1119,6 +1168,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t o[32];
                     __syncwarp();
                     tmem_load(t_out + c, o);
+                    if (joined) {
+                        uint32_t other[32];
+                        tmem_load(t_out + DP + c, other);
+                        tmem_ld_wait();
+                        tmem_loaded(o);
+                        tmem_loaded(other);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            o[j] = __float_as_uint(keep * __uint_as_float(o[j]) +
+                                                   add * __uint_as_float(other[j]));
+                    }
                     tmem_ld_wait();
                     tmem_loaded(o);
                     if (whole) {
@@ -1146,8 +1206,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
                     }
                 }
+                if (joined) {
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(rest.other_free));
+                }
             }
-            if (steps > 0 && *reinterpret_cast<const volatile int*>(&rest.odd[n % kUnits].any) != 0) {
+            const bool writes = !(shared && q == 1);
+            if (steps > 0 && writes && *reinterpret_cast<const volatile int*>(&rest.odd[n % kUnits].any) != 0) {
                 // What was not finite is added to what was written, in the dimensions it is in.
                 __syncwarp();
                 const Odd<DP>& odd = rest.odd[n % kUnits];
@@ -1162,16 +1228,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                                h * a.out_head + d;
                         *o = (T)((float)*o + x);
                     } else {
-                        a.partial[((part * S::kTiles + q) * (DP / 4) + d / 4) * (4 * kQueryTile) + 4 * r +
+                        a.partial[((part * S::kTiles + tile) * (DP / 4) + d / 4) * (4 * kQueryTile) + 4 * r +
                                   d % 4] += x;
                     }
                 }
             }
-            if (in && whole && limit > 0 && a.lse)
+            if (in && writes && whole && limit > 0 && a.lse)
                 a.lse[((int64_t)u.item.token0 + token) * a.q_heads + h] =
                     sum == 0.f ? -INFINITY : (top - kHeadroom + log2f(sum)) * kLn2;
-            if (in && !whole)
-                a.partial_ml[part * S::kRows + q * kQueryTile + r] = make_float2(top - kHeadroom, sum);
+            if (in && writes && !whole)
+                a.partial_ml[part * S::kRows + tile * kQueryTile + r] = make_float2(top - kHeadroom, sum);
             step0 += u.steps;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(rest.unit_free[n % 2]));
