@@ -142,10 +142,10 @@ struct ChunkArgs {
 // search.  Some of the items are handed out whole, first; the others, and any longer
 // than a block's share, are cut into ceil(n / u) parts of nearly equal length.  Tried are
 // 32 lengths u, with none whole or as many as make full rounds of the blocks; taken is
-// what makes the estimated time least: a unit costs its steps and two more (three where it
-// is a part), and blocks are level to half a unit.
+// what makes the estimated time least: a unit costs its steps and three more (four where it
+// is a part), and blocks are level to half a unit, or take rounds of parts that are alike.
 // ---------------------------------------------------------------------------
-constexpr int kUnitCost = 2, kStaged = 2048;
+constexpr int kUnitCost = 3, kStaged = 2048;
 
 __device__ __forceinline__ int parts_of(int steps, int unit, float inverse) {
     int k = (int)((float)steps * inverse);  // ceil(steps / unit), or one more for very many
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a, Divisor
     // (tokens * group is below 2^31)
     const auto key = [&](int b) { return rows.quotient(offset(b) * group) + b; };
     int64_t total = 0;
-    int longest = 0, items = 0;
+    int longest = 0, shortest = INT32_MAX, items = 0;
 #pragma unroll 1
     for (int s = tid; s < slots; s += kPlanThreads) {
         int lo = 0, hi = batch;  // key(lo) <= s < key(hi)
@@ -200,6 +200,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a, Divisor
         total += slot.steps;
         items += slot.steps > 0;
         longest = max(longest, slot.steps);
+        if (slot.steps) shortest = min(shortest, slot.steps);
     }
 #pragma unroll 1
     for (int level = 0; level < 2; ++level) {  // over the warp, then over the warps
@@ -208,11 +209,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a, Divisor
             total += __shfl_xor_sync(~0u, total, d);
             items += __shfl_xor_sync(~0u, items, d);
             longest = max(longest, __shfl_xor_sync(~0u, longest, d));
+            shortest = min(shortest, __shfl_xor_sync(~0u, shortest, d));
         }
         if (level) break;
-        if (lane == 0) sums[warp] = total, ints[warp] = items, longests[warp] = longest;
+        if (lane == 0) {
+            sums[warp] = total, ints[warp] = items;
+            longests[warp] = longest, units[warp] = shortest;
+        }
         __syncthreads();
-        total = sums[lane], items = ints[lane], longest = longests[lane];
+        total = sums[lane], items = ints[lane], longest = longests[lane], shortest = units[lane];
     }
     total *= heads;
     // Slots are taken from the last to the first, so that a row's long items come first.  Cut are
@@ -251,6 +256,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a, Divisor
             const float all_parts = (float)parts * (float)heads, all_whole = whole * (float)heads;
             const float work = (float)total + kUnitCost * all_whole + (kUnitCost + 1) * all_parts;
             float cost = work / sms + (float)(u + kUnitCost) / 2;
+            // (parts all alike: rounds of them)
+            if (whole == 0.f && shortest * 5 >= longest * 4)
+                cost = fminf(cost, ceilf(all_parts / sms) * (float)(u + kUnitCost + 1));
             if (whole > 0.f)  // rounds of whole items
                 cost = fmaxf(cost, ceilf(all_whole / sms) * (whole_steps / whole + kUnitCost));
             if (parts) cost += 2.f;  // the join
