@@ -711,7 +711,7 @@ typedef struct w4a16_adjust_tensors {
 
 /* Its sizes: rows 1 .. 2^24, vocabulary 1 .. 2^30, type W4A16_F16, _BF16 or
  * _F32; strides in elements of rows; wide = 1 where tokens are int64; width of
- * the rows of tokens; biases of a row (0 .. 1024); and the penalties of every
+ * the rows of tokens, below 2^30; biases of a row (0 .. 1024); and the penalties of every
  * row where the tensor of that name is NULL. */
 typedef struct w4a16_adjust_shape {
     int64_t rows, vocabulary, type, logits_stride, out_stride;

@@ -127,7 +127,7 @@ def test_adjust_arguments(lib):
     assert call(tensors(bias_ids=FAKE)) == 1
     for bad in (dict(rows=0), dict(rows=(1 << 24) + 1), dict(vocabulary=0),
                 dict(vocabulary=(1 << 30) + 1), dict(type=3), dict(type=-1), dict(stride=-1),
-                dict(out=-1), dict(wide=2), dict(width=-1), dict(width=1 << 31), dict(tokens=-1),
+                dict(out=-1), dict(wide=2), dict(width=-1), dict(width=1 << 30), dict(tokens=-1),
                 dict(biases=-1), dict(biases=1025), dict(bias=-4), dict(mask=-4)):
         assert call(s=sizes(**bad)) == 2
     assert call(tensors(out=FAKE), sizes(out=104)) == 2          # the input's place, another stride

@@ -5,14 +5,15 @@
 //   y = x, or where the prompt or the generation has the token x / r (x > 0), x r (else)
 //   y = y - f c - p [c > 0] + bias,   -infinity where the mask's bit is 0.
 //
-// A copy of the logits, bound by HBM, but for the few tokens that a row has
-// said.  Those a block finds without a table in memory: it takes a slice of one
-// row's vocabulary, holds a word of counts for each token of it in shared
-// memory, and reads the whole history, which the row's other blocks find in L2
-// (8191 tokens are 32 KB, as many bytes as 16384 logits of 16 bits).  Counts are
-// integers, so the order of the atomics changes nothing.  A piece of 16 bytes
-// without a token that was said moves as it is, one that the mask has none of
-// is not read, and in place only what changes is touched.
+// A copy of the logits under the mask, bound by HBM, and then the few tokens that a
+// row has said or has biases for, one by one.  Those a block finds without a table
+// in memory: it takes a slice of one row's vocabulary, holds a word of counts for
+// each token of it in shared memory, and reads the whole history, which the row's
+// other blocks find in L2 (8191 tokens are 32 KB, as many bytes as a slice of 16384
+// logits of 16 bits); a sweep over the words then lists the tokens that were said.
+// Counts are integers and a token's logit is its own, so the order of the atomics
+// changes nothing.  A piece of 16 bytes that the mask has none of is not read, and in
+// place only what changes is touched.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -24,11 +25,22 @@
 namespace w4a16 {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kMostSlice = 16384;
+constexpr int kThreads = 256;
+constexpr int kBlocksPerSm = 8;
+constexpr int kAhead = 1;            // pieces of a thread on their way
+constexpr int kWordBytes = 16384;    // of a slice's words at most
+constexpr int kListed = 4096;        // words swept at a time, as many as the list has places for
 constexpr int kMostBiases = W4A16_MAX_BIASES;
-constexpr int kBiasesEach = (kMostBiases + kThreads - 1) / kThreads;
-constexpr uint32_t kPrompt = 1u << 31;  // of a token's word; the rest counts its generation
+
+// A token's word: whether a bias is listed for it, whether the prompt has it, and in the other bits
+// how often the generation has it.  Of 16 bits where histories are short enough, else of 32.
+template <typename W>
+struct Word {
+    static constexpr int kBits = 8 * sizeof(W);
+    static constexpr uint32_t kBiased = 1u << (kBits - 1), kPrompt = 1u << (kBits - 2),
+                              kCount = kPrompt - 1;
+    static constexpr int kSlice = kWordBytes / sizeof(W);
+};
 
 struct AdjustArgs {
     w4a16_adjust_tensors t;
@@ -45,12 +57,13 @@ __device__ __forceinline__ T from_float(float v) {
     return (T)v;
 }
 
+template <typename W>
 struct Penalties {
     float repetition, presence, frequency;
 
     __device__ __forceinline__ float apply(float x, uint32_t word) const {
-        if (word) x = x > 0.f ? x / repetition : x * repetition;
-        const uint32_t count = word & ~kPrompt;
+        if (word & ~Word<W>::kBiased) x = x > 0.f ? x / repetition : x * repetition;
+        const uint32_t count = word & Word<W>::kCount;
         if (count) x = x - frequency * (float)count - presence;
         return x;
     }
@@ -67,12 +80,16 @@ __device__ __forceinline__ bool allowed(const uint32_t* mask, int64_t j) {
 }
 
 // V: logits of a piece, 16 bytes where the rows of logits and out lie alike to that boundary, else 1.
-template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) adjust_kernel(AdjustArgs a) {
-    extern __shared__ __align__(16) uint32_t words[];  // of the slice's tokens
+template <typename T, int V, typename W>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) adjust_kernel(AdjustArgs a) {
+    extern __shared__ __align__(16) uint32_t space[];  // words of the slice's tokens, then the list
+    W* words = reinterpret_cast<W*>(space);
     __shared__ int32_t bias_ids[kMostBiases];
+    __shared__ int listed;  // tokens on the list
+    __shared__ int twice;   // whether some token has two biases
+    uint16_t* list = reinterpret_cast<uint16_t*>(words + a.slice);
     const int64_t row = blockIdx.x / a.slices;
-    const int64_t vocabulary = a.s.vocabulary;
+    const int vocabulary = (int)a.s.vocabulary;
     grid_dependency_wait();
     grid_launch_dependents();
     const T* x = static_cast<const T*>(a.t.logits) + row * a.s.logits_stride;
@@ -80,115 +97,166 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(AdjustArgs a) {
     const uint32_t* mask = a.t.mask ? a.t.mask + row * a.s.mask_stride : nullptr;
     // The slice begins where a piece does: `shift` values before the row's first one are passed over.
     const int shift = (int)(reinterpret_cast<uintptr_t>(x) / sizeof(T) % V);
-    const int64_t begin = (int64_t)(blockIdx.x % a.slices) * a.slice - shift;
-    const int64_t from = max(begin, (int64_t)0), to = min(begin + a.slice, vocabulary);
+    const int begin = (int)(blockIdx.x % a.slices) * a.slice - shift;
+    const int from = max(begin, 0), to = (int)min((int64_t)begin + a.slice, (int64_t)vocabulary);
     if (from >= to) return;
-    for (int i = threadIdx.x * 4; i < a.slice; i += kThreads * 4)
-        *reinterpret_cast<uint4*>(words + i) = make_uint4(0, 0, 0, 0);
-    const Penalties p = {a.t.repetition ? a.t.repetition[row] : (float)a.s.repetition,
-                         a.t.presence ? a.t.presence[row] : (float)a.s.presence,
-                         a.t.frequency ? a.t.frequency[row] : (float)a.s.frequency};
+    const uint32_t span = (uint32_t)(to - from), skip = (uint32_t)(from - begin);
+
+    const int length = a.t.tokens ? (int)(a.t.lengths ? min(max((int64_t)a.t.lengths[row], (int64_t)0), a.s.width)
+                                                      : a.s.width)
+                                  : 0;
+    const int prompt = a.t.prompts ? a.t.prompts[row] : 0;
     const int biases = a.t.bias_ids ? (int)a.s.biases : 0;
     for (int i = threadIdx.x; i < biases; i += kThreads)
         bias_ids[i] = a.t.bias_ids[row * a.s.bias_stride + i];
+    for (int i = threadIdx.x; i < a.slice * (int)sizeof(W) / 16; i += kThreads)
+        reinterpret_cast<uint4*>(space)[i] = make_uint4(0, 0, 0, 0);
+    if (threadIdx.x == 0) listed = twice = 0;
     __syncthreads();
-    if (a.t.tokens) {
-        const int64_t length = a.t.lengths ? min(max((int64_t)a.t.lengths[row], (int64_t)0), a.s.width)
-                                           : a.s.width;
-        const int64_t prompt = a.t.prompts ? a.t.prompts[row] : 0;
-        const auto note = [&](int64_t i, int64_t token) {
-            if (token < from || token >= to) return;
-            uint32_t* w = words + (token - begin);
-            if (i < prompt)
-                atomicOr(w, kPrompt);
-            else
-                atomicAdd(w, 1u);
-        };
-        if (a.s.wide) {
-            const int64_t* tokens = static_cast<const int64_t*>(a.t.tokens) + row * a.s.token_stride;
+
+    // The history.  (Predicated, and nothing waits for it: with branches, or with the old word
+    // returned to see who is first, this took longer than all the rest.)
+    const uint32_t word0 = smem_u32(words) + skip * sizeof(W);
+    const auto note = [&](int i, int32_t token) {
+        const uint32_t at = (uint32_t)token - (uint32_t)from;
+        const uint32_t by = sizeof(W) == 2 ? 16 * ((at + skip) & 1) : 0;  // its place in 32 bits
+        asm volatile(
+            "{\n\t.reg .pred p, q, r;\n\t"
+            "setp.lt.s32 r, %3, %4;\n\t"
+            "setp.lt.and.u32 p, %1, %2, r;\n\t"
+            "setp.lt.and.u32 q, %1, %2, !r;\n\t"
+            "@p red.shared.or.b32 [%0], %5;\n\t"
+            "@q red.shared.add.u32 [%0], %6;\n\t}" ::"r"((word0 + at * (uint32_t)sizeof(W)) & ~3u),
+            "r"(at), "r"(span), "r"(i), "r"(prompt), "r"(Word<W>::kPrompt << by), "r"(1u << by)
+            : "memory");
+    };
+    if (a.s.wide) {
+        const int64_t* tokens = static_cast<const int64_t*>(a.t.tokens) + row * a.s.token_stride;
 #pragma unroll 4
-            for (int64_t i = threadIdx.x; i < length; i += kThreads) note(i, tokens[i]);
-        } else {
-            const int32_t* tokens = static_cast<const int32_t*>(a.t.tokens) + row * a.s.token_stride;
-#pragma unroll 4
-            for (int64_t i = threadIdx.x; i < length; i += kThreads) note(i, tokens[i]);
+        for (int i = threadIdx.x; i < length; i += kThreads) {
+            const int64_t token = tokens[i];
+            note(i, token >= 0 && token < vocabulary ? (int32_t)token : -1);
+        }
+    } else if (length) {
+        const int32_t* tokens = static_cast<const int32_t*>(a.t.tokens) + row * a.s.token_stride;
+        const int whole = reinterpret_cast<uintptr_t>(tokens) % 16 == 0 ? length / 4 * 4 : 0;
+#pragma unroll 2
+        for (int i = threadIdx.x * 4; i < whole; i += kThreads * 4) {
+            const int4 four = *reinterpret_cast<const int4*>(tokens + i);
+            note(i, four.x);
+            note(i + 1, four.y);
+            note(i + 2, four.z);
+            note(i + 3, four.w);
+        }
+        for (int i = whole + threadIdx.x; i < length; i += kThreads) note(i, tokens[i]);
+    }
+    // Tokens that a bias is listed for are marked: they are their biases' business.
+    for (int i = threadIdx.x; i < biases; i += kThreads) {
+        const uint32_t at = (uint32_t)bias_ids[i] - (uint32_t)from;
+        if (at >= span) continue;
+        const uint32_t by = sizeof(W) == 2 ? 16 * ((at + skip) & 1) : 0;
+        const uint32_t old = atomicOr(space + (at + skip) * sizeof(W) / 4, Word<W>::kBiased << by);
+        if (old & Word<W>::kBiased << by) twice = 1;
+    }
+
+    // The copy, under the mask.
+    constexpr uint32_t kAll = (1u << V) - 1;
+    const T masked = from_float<T>(-INFINITY);
+    for (int first = 0; first < a.slice; first += kAhead * kThreads * V) {
+        uint32_t bits[kAhead];  // the mask's for each piece; kAll + 1: no whole piece
+        Piece<T, V> v[kAhead];
+#pragma unroll
+        for (int n = 0; n < kAhead; ++n) {
+            const int i = first + (n * kThreads + threadIdx.x) * V, j = begin + i;
+            bits[n] = kAll + 1;
+            if (i >= a.slice || j < 0 || j + V > to) continue;
+            bits[n] = kAll;
+            if (!mask) continue;
+            // the V bits from token j on, which may lie in two words
+            const int word = j >> 5, last = (j + V - 1) >> 5;
+            const uint32_t low = mask[word], high = last > word ? mask[last] : 0;
+            bits[n] = __funnelshift_r(low, high, j & 31) & kAll;
+        }
+#pragma unroll
+        for (int n = 0; n < kAhead; ++n) {
+            const int i = first + (n * kThreads + threadIdx.x) * V;
+            if (bits[n] && bits[n] <= kAll && !(a.in_place && bits[n] == kAll))
+                v[n] = *reinterpret_cast<const Piece<T, V>*>(x + begin + i);
+        }
+#pragma unroll
+        for (int n = 0; n < kAhead; ++n) {
+            const int i = first + (n * kThreads + threadIdx.x) * V, j = begin + i;
+            if (bits[n] <= kAll) {
+                if (bits[n] != kAll) {
+#pragma unroll
+                    for (int k = 0; k < V; ++k)
+                        if (!(bits[n] >> k & 1)) v[n].x[k] = masked;
+                } else if (a.in_place) {
+                    continue;
+                }
+                *reinterpret_cast<Piece<T, V>*>(out + j) = v[n];
+            } else if (i < a.slice && j + V > 0 && j < to) {  // the row's ends
+                for (int k = 0; k < V; ++k)
+                    if (j + k >= 0 && j + k < to && !(a.in_place && allowed(mask, j + k)))
+                        out[j + k] = allowed(mask, j + k) ? x[j + k] : masked;
+            }
         }
     }
+    const Penalties<W> p = {a.t.repetition ? a.t.repetition[row] : (float)a.s.repetition,
+                            a.t.presence ? a.t.presence[row] : (float)a.s.presence,
+                            a.t.frequency ? a.t.frequency[row] : (float)a.s.frequency};
     __syncthreads();
-    // Biased tokens: what they become is computed before the pass (in place it writes over their
-    // logits) and written after it.  A token listed twice is its first listing's, with the biases
-    // added in the order of the list.
-    float biased[kBiasesEach];
-    int mine = 0;
-#pragma unroll
-    for (int k = 0; k < kBiasesEach; ++k) {
-        const int i = threadIdx.x + k * kThreads;
-        const int64_t id = i < biases ? bias_ids[i] : -1;
-        if (id < from || id >= to || !allowed(mask, id)) continue;
-        const float* value = a.t.biases + row * a.s.bias_stride;
+
+    // Biased tokens.  One with several biases is its first listing's, with the biases added in the
+    // order of the list.
+    const float* value = a.t.biases + row * a.s.bias_stride;
+    for (int i = threadIdx.x; i < biases; i += kThreads) {
+        const int id = bias_ids[i];
+        if ((uint32_t)id - (uint32_t)from >= span || !allowed(mask, id)) continue;
         float y = p.apply(to_float(x[id]), words[id - begin]) + value[i];
-        bool earlier = false;
-        for (int j = 0; j < biases; ++j)
+        bool later = false;
+        for (int j = 0; twice && j < biases; ++j)
             if (bias_ids[j] == id && j != i) {
-                earlier = earlier || j < i;
+                later = later || j < i;
                 y += value[j];
             }
-        if (!earlier) mine |= 1 << k;
-        biased[k] = y;
+        // (in place a later listing's thread may read what the first has written, and is dropped)
+        if (!later) out[id] = from_float<T>(y);
     }
-    if (biases) __syncthreads();
-    const T masked = from_float<T>(-INFINITY);
-    for (int i = threadIdx.x * V; i < a.slice; i += kThreads * V) {
-        const int64_t j = begin + i;
-        if (j + V <= 0 || j >= vocabulary) continue;
-        const bool whole = j >= 0 && j + V <= vocabulary;
-        uint32_t w[V], any = 0;
+    // Said tokens: those of kListed words at a time are listed, a bit a word, and then taken one by
+    // one, so that all threads have their share of what has to be fetched.
+    if (!length) return;
+    constexpr int kEach = 16 / sizeof(W);  // words of a 16-byte read
+    for (int first = 0; first < a.slice; first += kListed) {
+        uint32_t set = 0;
 #pragma unroll
-        for (int k = 0; k < V; ++k) any |= w[k] = words[i + k];
-        if (whole) {
-            uint32_t bits = ~0u;
-            if (mask) {
-                // the V bits from token j on, which may lie in two words
-                bits = mask[j >> 5];
-                const int64_t last = j + V - 1;
-                bits = __funnelshift_r(bits, (last >> 5) > (j >> 5) ? mask[last >> 5] : 0, j & 31);
-            }
-            bits &= (1u << V) - 1;
-            const bool full = bits == (1u << V) - 1;
-            if (a.in_place && full && !any) continue;
-            Piece<T, V> v;
-            if (bits) v = *reinterpret_cast<const Piece<T, V>*>(x + j);
-            if (any) {
+        for (int n = 0; n < kListed / (kThreads * kEach); ++n) {
+            const int i = first + (n * kThreads + threadIdx.x) * kEach;
+            if (i >= a.slice) continue;
+            const uint4 read = *reinterpret_cast<const uint4*>(words + i);
+            const W* w = reinterpret_cast<const W*>(&read);
 #pragma unroll
-                for (int k = 0; k < V; ++k)
-                    if (w[k]) v.x[k] = from_float<T>(p.apply(to_float(v.x[k]), w[k]));
-            }
-            if (!full) {
-#pragma unroll
-                for (int k = 0; k < V; ++k)
-                    if (!(bits >> k & 1)) v.x[k] = masked;
-            }
-            *reinterpret_cast<Piece<T, V>*>(out + j) = v;
-        } else {
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                if (j + k < 0 || j + k >= vocabulary) continue;
-                const bool in = allowed(mask, j + k);
-                if (a.in_place && in && !w[k]) continue;
-                T y = x[j + k];
-                if (w[k]) y = from_float<T>(p.apply(to_float(y), w[k]));
-                out[j + k] = in ? y : masked;
-            }
+            for (int k = 0; k < kEach; ++k)
+                set |= (uint32_t)(w[k] != 0 && w[k] < Word<W>::kBiased) << (n * kEach + k);
         }
+        int at = set ? atomicAdd(&listed, __popc(set)) : 0;
+        for (; set; set &= set - 1) {
+            const int bit = __ffs(set) - 1;
+            list[at++] = (uint16_t)(first + (bit / kEach * kThreads + threadIdx.x) * kEach + bit % kEach);
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < listed; i += kThreads) {
+            const int id = begin + list[i];
+            if (allowed(mask, id)) out[id] = from_float<T>(p.apply(to_float(x[id]), words[list[i]]));
+        }
+        if (first + kListed >= a.slice) break;
+        __syncthreads();
+        if (threadIdx.x == 0) listed = 0;
+        __syncthreads();
     }
-    if (!biases) return;
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kBiasesEach; ++k)
-        if (mine >> k & 1) out[bias_ids[threadIdx.x + k * kThreads]] = from_float<T>(biased[k]);
 }
 
-template <typename T, int V>
+template <typename T, int V, typename W>
 cudaError_t launch(AdjustArgs a, cudaStream_t stream, const DeviceCtx& ctx) {
     static std::once_flag once[64];
     static cudaError_t set[64];
@@ -196,13 +264,14 @@ cudaError_t launch(AdjustArgs a, cudaStream_t stream, const DeviceCtx& ctx) {
     cudaError_t e = cudaGetDevice(&device);
     if (e != cudaSuccess) return e;
     std::call_once(once[device], [&]() {
-        set[device] = cudaFuncSetAttribute(adjust_kernel<T, V>,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kMostSlice);
+        set[device] =
+            cudaFuncSetAttribute(adjust_kernel<T, V, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kWordBytes + 2 * kListed);
     });
     if (set[device] != cudaSuccess) return set[device];
-    // a slice of 16384 tokens, less where that leaves fewer than four blocks an SM
+    // as large a slice as there are words for, less where that leaves fewer than four blocks an SM
     const int64_t padded = a.s.vocabulary + V - 1;  // a row may begin inside a piece
-    int64_t slice = std::min<int64_t>(kMostSlice, padded * a.s.rows / (4 * ctx.num_sms));
+    int64_t slice = std::min<int64_t>(Word<W>::kSlice, padded * a.s.rows / (4 * ctx.num_sms));
     slice = std::max<int64_t>(1024, slice / 1024 * 1024);
     a.slice = (int)slice;
     a.slices = (int)((padded + slice - 1) / slice);
@@ -213,11 +282,17 @@ cudaError_t launch(AdjustArgs a, cudaStream_t stream, const DeviceCtx& ctx) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.s.rows * a.slices));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = 4 * slice;
+    cfg.dynamicSmemBytes = slice * sizeof(W) + 2 * std::min<int64_t>(slice, kListed);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, adjust_kernel<T, V>, a);
+    return cudaLaunchKernelEx(&cfg, adjust_kernel<T, V, W>, a);
+}
+
+template <typename T, int V>
+cudaError_t launch(const AdjustArgs& a, cudaStream_t stream, const DeviceCtx& ctx) {
+    return a.s.width <= (int64_t)Word<uint16_t>::kCount ? launch<T, V, uint16_t>(a, stream, ctx)
+                                                        : launch<T, V, uint32_t>(a, stream, ctx);
 }
 
 template <typename T>
@@ -230,7 +305,6 @@ cudaError_t launch(const AdjustArgs& a, cudaStream_t stream, const DeviceCtx& ct
         return launch<T, V>(a, stream, ctx);
     return launch<T, 1>(a, stream, ctx);
 }
-
 }  // namespace
 
 cudaError_t launch_adjust_logits(const w4a16_adjust_tensors& tensors,

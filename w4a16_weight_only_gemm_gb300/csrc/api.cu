@@ -664,7 +664,7 @@ int w4a16_adjust_logits(const w4a16_adjust_tensors* tensors, const w4a16_adjust_
         s.vocabulary > (int64_t)1 << 30 || s.type < W4A16_F16 || s.type > W4A16_F32 ||
         !stride(s.logits_stride) || !stride(s.out_stride) || !stride(s.token_stride) ||
         !stride(s.bias_stride) || !stride(s.mask_stride) || (s.wide != 0 && s.wide != 1) ||
-        s.width < 0 || s.width >= (int64_t)1 << 31 || s.biases < 0 || s.biases > W4A16_MAX_BIASES ||
+        s.width < 0 || s.width >= (int64_t)1 << 30 || s.biases < 0 || s.biases > W4A16_MAX_BIASES ||
         (tensors->logits == tensors->out && s.rows > 1 && s.logits_stride != s.out_stride))
         return W4A16_ERR_SHAPE;
     const uintptr_t size = s.type == W4A16_F32 ? 4 : 2;

@@ -9,10 +9,12 @@
 // An angle in FP32 would be off by 2^-8 radians at position 131071.
 //
 // Bound by HBM: 3 FLOPs a value.  A block takes a few tokens, finds their
-// positions (and places in the cache), fills a table of their cosines and
-// sines, which all heads share, and then works through units of 2 V values,
-// the two halves of V pairs: 16-byte pieces where a head has a multiple of 8
-// pairs.  Values of dimensions that are not rotated, and V's heads, are copied.
+// positions (and places in the cache) and fills a table of their cosines and
+// sines.  Its threads are dealt out over tokens, over every so manieth head, and
+// over units of 2 V values of a head, the two halves of V pairs: 16-byte pieces
+// where a head has a multiple of 8 pairs.  So a thread has its pairs' cosines and
+// sines in registers and steps from head to head by an addition.  Values of
+// dimensions that are not rotated, and V's heads, are copied.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -25,10 +27,10 @@
 namespace w4a16 {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;    // of a block at most
 constexpr int kMostTokens = 16;  // of a block
 constexpr int kMostPairs = 128;
-constexpr int kUnroll = 2;       // units of a thread in flight
+constexpr int kUnroll = 2;       // heads of a thread in flight
 
 struct RotaryArgs {
     const void *q, *k, *v;
@@ -40,10 +42,9 @@ struct RotaryArgs {
     int q_heads, kv_heads, dim, pairs, interleaved;
     float magnitude;
     Cache c;
-    int block_tokens;
-    // units: of a token, of its rotated heads, and of one head that is rotated or copied
-    int rotated_units;
-    Divisor token_units, head_units, copy_units;
+    int units;                        // of a head
+    int block_tokens, block_heads;    // tokens of a block, and heads that it takes at a time
+    Divisor token_threads, head_units;
 };
 
 template <typename T>
@@ -61,9 +62,95 @@ struct alignas(sizeof(T) * V < 16 ? sizeof(T) * V : 16) Piece {
     T x[V];
 };
 
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float2 v) {
+    if constexpr (std::is_same<T, __half>::value) {
+        const __half2 h = __float22half2_rn(v);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __nv_bfloat162 h = __float22bfloat162_rn(v);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t v) {
+    if constexpr (std::is_same<T, __half>::value)
+        return __half22float2(*reinterpret_cast<const __half2*>(&v));
+    else
+        return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
+}
+
+// The turned pieces.  16-bit values are taken in twos (a conversion at a time runs on a pipe of a
+// quarter of the rate).
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a) {
+__device__ __forceinline__ void turn(Piece<T, V>& lo, Piece<T, V>& hi, const float2 (&cs)[V],
+                                     bool interleaved) {
+    if constexpr (sizeof(T) == 2 && V >= 2) {
+        uint32_t* a = reinterpret_cast<uint32_t*>(&lo);
+        uint32_t* b = reinterpret_cast<uint32_t*>(&hi);
+        if (interleaved) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                uint32_t& w = j < V / 2 ? a[j] : b[j - V / 2];
+                const float2 v = unpack2<T>(w), z = cs[j];
+                w = pack2<T>(make_float2(v.x * z.x - v.y * z.y, v.x * z.y + v.y * z.x));
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) {
+                const float2 x = unpack2<T>(a[j]), y = unpack2<T>(b[j]), z = cs[2 * j], n = cs[2 * j + 1];
+                a[j] = pack2<T>(make_float2(x.x * z.x - y.x * z.y, x.y * n.x - y.y * n.y));
+                b[j] = pack2<T>(make_float2(x.x * z.y + y.x * z.x, x.y * n.y + y.y * n.x));
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float2 z = cs[j];
+            // the pair's places in the two pieces
+            T& x = !interleaved ? lo.x[j] : 2 * j < V ? lo.x[2 * j % V] : hi.x[2 * j % V];
+            T& y = !interleaved ? hi.x[j] : 2 * j + 1 < V ? lo.x[(2 * j + 1) % V] : hi.x[(2 * j + 1) % V];
+            const float p = to_float(x), q = to_float(y);
+            x = from_float<T>(p * z.x - q * z.y);
+            y = from_float<T>(p * z.y + q * z.x);
+        }
+    }
+}
+
+// One unit of heads first, first + every, ... below `heads`, from `from` to `to` (of head 0, with
+// their strides); turned by cs where `turned`, else copied.  x0, x1: where its pieces begin (x1 < 0:
+// there is no second one).
+template <typename T, int V>
+__device__ __forceinline__ void move_heads(const T* from, int64_t from_head, T* to, int64_t to_head,
+                                           int first, int heads, int every, int x0, int x1, bool turned,
+                                           bool interleaved, bool zero, const float2 (&cs)[V]) {
     using P = Piece<T, V>;
+    for (int h = first; h < heads; h += kUnroll * every) {
+        P lo[kUnroll], hi[kUnroll];
+#pragma unroll
+        for (int n = 0; n < kUnroll; ++n) {
+            if (h + n * every >= heads) break;
+            const T* at = from + (h + n * every) * from_head;
+            lo[n] = *reinterpret_cast<const P*>(at + x0);
+            if (x1 >= 0) hi[n] = *reinterpret_cast<const P*>(at + x1);
+        }
+#pragma unroll
+        for (int n = 0; n < kUnroll; ++n) {
+            if (h + n * every >= heads) break;
+            if (turned) turn<T, V>(lo[n], hi[n], cs, interleaved);
+            if (zero) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) lo[n].x[j] = hi[n].x[j] = from_float<T>(0.f);
+            }
+            T* at = to + (h + n * every) * to_head;
+            *reinterpret_cast<P*>(at + x0) = lo[n];
+            if (x1 >= 0) *reinterpret_cast<P*>(at + x1) = hi[n];
+        }
+    }
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads, 4) rotary_kernel(RotaryArgs a) {
     __shared__ int64_t place[kMostTokens];     // where a token's heads start in the pools, -1: nowhere
     __shared__ int64_t position[kMostTokens];
     __shared__ int claimed[kMostTokens];
@@ -71,14 +158,14 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a) {
     grid_dependency_wait();
     grid_launch_dependents();
     const int64_t first = (int64_t)blockIdx.x * a.block_tokens;
-    const int tokens = (int)min((int64_t)a.block_tokens, a.tokens - first);
+    const int tokens = (int)min((int64_t)a.block_tokens, a.tokens - first), threads = blockDim.x;
     if (a.positions) {
         if (threadIdx.x < tokens) {
             position[threadIdx.x] = a.positions[first + threadIdx.x];
             claimed[threadIdx.x] = 1;
         }
     } else {
-        for (int i = threadIdx.x / 32; i < tokens; i += kThreads / 32) {
+        for (int i = threadIdx.x / 32; i < tokens; i += threads / 32) {
             const int64_t t = first + i;
             const int b = row_of(a.offsets, a.c.batch, t);
             int64_t at = -1, p = 0;
@@ -95,7 +182,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a) {
         }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < tokens * a.pairs; i += kThreads) {
+    for (int i = threadIdx.x; i < tokens * a.pairs; i += threads) {
         const int t = i / a.pairs, j = i - t * a.pairs;
         const int64_t turn = (int64_t)((uint64_t)position[t] * a.turns[j]);  // of 2^64
         float s, c;
@@ -103,103 +190,48 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a) {
         table[t * kMostPairs + j] = make_float2(c * a.magnitude, s * a.magnitude);
     }
     __syncthreads();
-    const int units = tokens * a.token_units.value;
-    for (int u = threadIdx.x; u < units; u += kUnroll * kThreads) {
-        P lo[kUnroll], hi[kUnroll];
-        T *to[kUnroll], *to_hi[kUnroll];
-        const float2* turn[kUnroll];
-        bool zero[kUnroll];
+    const int i = a.token_threads.quotient((int)threadIdx.x);
+    if (i >= tokens) return;
+    const int in_token = threadIdx.x - i * a.token_threads.value;
+    const int h = a.head_units.quotient(in_token), u = in_token - h * a.units;
+    const int64_t t = first + i;
+    const bool turned = u * V < a.pairs;
+    float2 cs[V];
 #pragma unroll
-        for (int n = 0; n < kUnroll; ++n) {
-            const int w = u + n * kThreads;
-            to[n] = to_hi[n] = nullptr;
-            turn[n] = nullptr;
-            zero[n] = false;
-            if (w >= units) continue;
-            const int i = a.token_units.quotient(w);
-            int y = w - i * a.token_units.value;
-            const bool copied = y >= a.rotated_units;
-            if (copied) y -= a.rotated_units;
-            const Divisor& per = copied ? a.copy_units : a.head_units;
-            int h = per.quotient(y);
-            y -= h * per.value;
-            // the unit's two pieces begin at x0 and x1 of the head
-            int x0, x1;
-            if (!copied && y * V < a.pairs) {
-                turn[n] = table + i * kMostPairs + y * V;
-                x0 = a.interleaved ? 2 * V * y : V * y;
-                x1 = a.interleaved ? x0 + V : x0 + a.pairs;
-            } else {
-                x0 = (copied ? 0 : 2 * a.pairs) + 2 * V * (copied ? y : y - a.pairs / V);
-                x1 = x0 + V;
-            }
-            const T* from;
-            if (!copied && h < a.q_heads) {
-                from = static_cast<const T*>(a.q) + (first + i) * a.q_token + h * a.q_head;
-                to[n] = static_cast<T*>(a.out) + (first + i) * a.out_token + h * a.out_head;
-                zero[n] = !claimed[i];
-            } else {
-                if (place[i] < 0) continue;
-                if (!copied) h -= a.q_heads;
-                from = copied ? static_cast<const T*>(a.v) + (first + i) * a.v_token + h * a.v_head
-                              : static_cast<const T*>(a.k) + (first + i) * a.k_token + h * a.k_head;
-                to[n] = static_cast<T*>(copied ? a.v_pool : a.k_pool) + place[i] + h * a.c.head_stride;
-            }
-            if (x1 < a.dim) to_hi[n] = to[n] + x1;
-            to[n] += x0;
-            lo[n] = *reinterpret_cast<const P*>(from + x0);
-            if (to_hi[n]) hi[n] = *reinterpret_cast<const P*>(from + x1);
-        }
-#pragma unroll
-        for (int n = 0; n < kUnroll; ++n) {
-            if (!to[n]) continue;
-            if (turn[n]) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    // the pair's places in the two pieces, in either layout
-                    const float2 z = turn[n][j];
-                    if (a.interleaved) {
-                        T& x = 2 * j < V ? lo[n].x[2 * j % V] : hi[n].x[2 * j % V];
-                        T& y = 2 * j + 1 < V ? lo[n].x[(2 * j + 1) % V] : hi[n].x[(2 * j + 1) % V];
-                        const float p = to_float(x), q = to_float(y);
-                        x = from_float<T>(p * z.x - q * z.y);
-                        y = from_float<T>(p * z.y + q * z.x);
-                    } else {
-                        const float p = to_float(lo[n].x[j]), q = to_float(hi[n].x[j]);
-                        lo[n].x[j] = from_float<T>(p * z.x - q * z.y);
-                        hi[n].x[j] = from_float<T>(p * z.y + q * z.x);
-                    }
-                }
-            }
-            if (zero[n]) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) lo[n].x[j] = hi[n].x[j] = from_float<T>(0.f);
-            }
-            *reinterpret_cast<P*>(to[n]) = lo[n];
-            if (to_hi[n]) *reinterpret_cast<P*>(to_hi[n]) = hi[n];
-        }
-    }
+    for (int j = 0; j < V; ++j) cs[j] = turned ? table[i * kMostPairs + u * V + j] : make_float2(0.f, 0.f);
+    // a copied unit is 2 V values in a row; V's heads are copied throughout
+    const int copied = 2 * V * u, copied_hi = copied + V < a.dim ? copied + V : -1;
+    const int x0 = turned && !a.interleaved ? V * u : copied;
+    const int x1 = turned && !a.interleaved ? V * u + a.pairs : copied_hi;
+    move_heads<T, V>(static_cast<const T*>(a.q) + t * a.q_token, a.q_head,
+                     static_cast<T*>(a.out) + t * a.out_token, a.out_head, h, a.q_heads, a.block_heads, x0,
+                     x1, turned, a.interleaved, !claimed[i], cs);
+    if (a.kv_heads == 0 || place[i] < 0) return;
+    move_heads<T, V>(static_cast<const T*>(a.k) + t * a.k_token, a.k_head,
+                     static_cast<T*>(a.k_pool) + place[i], a.c.head_stride, h, a.kv_heads, a.block_heads, x0,
+                     x1, turned, a.interleaved, false, cs);
+    move_heads<T, V>(static_cast<const T*>(a.v) + t * a.v_token, a.v_head,
+                     static_cast<T*>(a.v_pool) + place[i], a.c.head_stride, h, a.kv_heads, a.block_heads,
+                     copied, copied_hi, false, false, false, cs);
 }
 
 template <typename T, int V>
 cudaError_t launch(RotaryArgs a, cudaStream_t stream, const DeviceCtx& ctx) {
-    const int head = a.pairs / V + (a.dim - 2 * a.pairs + 2 * V - 1) / (2 * V);
-    const int copied = (a.dim + 2 * V - 1) / (2 * V);
-    a.rotated_units = (a.q_heads + a.kv_heads) * head;
-    const int units = a.rotated_units + (a.v ? a.kv_heads : 0) * copied;
-    a.head_units = Divisor(head);
-    a.copy_units = Divisor(copied);
-    a.token_units = Divisor(units);
-    // up to 16 tokens a block and four units a thread, while that leaves four blocks an SM
-    const int64_t most = (int64_t)4 * kThreads / units;
-    a.block_tokens = (int)std::max<int64_t>(
-        1, std::min({(int64_t)kMostTokens, a.tokens / (4 * ctx.num_sms), most}));
+    a.units = (a.dim + 2 * V - 1) / (2 * V);
+    // Tokens of a block: as many as leave a block two for each SM, and four threads for a unit's heads;
+    // the rest of the threads go over the heads.
+    const int64_t most = std::max(1, std::min(kMostTokens, kThreads / (4 * a.units)));
+    a.block_tokens = (int)std::max<int64_t>(1, std::min(most, a.tokens / (2 * ctx.num_sms)));
+    a.block_heads = std::max(1, std::min(std::max(a.q_heads, a.kv_heads),
+                                         kThreads / (a.units * a.block_tokens)));
+    a.token_threads = Divisor(a.units * a.block_heads);
+    a.head_units = Divisor(a.units);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((a.tokens + a.block_tokens - 1) / a.block_tokens));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3((unsigned)((a.units * a.block_heads * a.block_tokens + 31) / 32 * 32));
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
