@@ -21,8 +21,9 @@ from fractions import Fraction
 
 import torch
 
-# 1 / (2 pi), to more digits than 2^64 needs
-_TURN = Fraction("0.159154943091895335768883763372514362034459645740456448747667344058896797634")
+# 2^192 / (2 pi)
+_TURN = int(Fraction("0.159154943091895335768883763372514362034459645740456448747667344058896797634")
+            * 2 ** 192)
 _SCALINGS = (None, "linear", "base", "ramp")
 _SHAPE = struct.Struct("2qd").pack
 
@@ -46,6 +47,12 @@ def _rates(dim, base, scaling, factor, original, low, high) -> list[float]:
         keep = [min(1.0, max(0.0, (t - low) / (high - low))) for t in turns]
         return [r * k + r / factor * (1.0 - k) for r, k in zip(rates, keep)]
     return rates
+
+
+def _turn(rate: float) -> int:
+    """rate / (2 pi) as a fraction of a turn times 2^64, rounded."""
+    n, d = rate.as_integer_ratio()
+    return ((n * _TURN // d >> 127) + 1 >> 1) % 2 ** 64
 
 
 class Rotary:
@@ -75,7 +82,9 @@ class Rotary:
             raise ValueError(f"magnitude must be finite, got {magnitude}")
         self.dim, self.interleaved, self.magnitude = dim, bool(interleaved), float(magnitude)
         self.rates = rates
-        turns = [round(Fraction(r) * _TURN * 2 ** 64) % 2 ** 64 for r in rates]
+        turns = [_turn(r) for r in rates]
         self.turns = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns],
                                   dtype=torch.int64, device=device)
         self._shape = _SHAPE(dim, self.interleaved, self.magnitude)
+        # (read at every call)
+        self._device, self._pointer = self.turns.get_device(), self.turns.data_ptr()

@@ -213,7 +213,7 @@ def rotate(x: torch.Tensor, positions: torch.Tensor, rotary: Rotary,
     tokens, heads, dim = shape
     _row(positions, tokens, "positions")
     dev = x.get_device()
-    if (dev < 0 or positions.get_device() != dev or rotary.turns.get_device() != dev
+    if (dev < 0 or positions.get_device() != dev or rotary._device != dev
             or out is not None and out.get_device() != dev
             or stream is not None and stream.device.index != dev):
         _device(stream, x=x, positions=positions, rotary=rotary.turns, out=out)
@@ -224,7 +224,7 @@ def rotate(x: torch.Tensor, positions: torch.Tensor, rotary: Rotary,
         to_row, to_head, _ = _heads(out, "out", dtype, shape)
     if tokens and heads:
         _run(dev, stream, "w4a16_rotate", x.data_ptr(), positions.data_ptr(),
-             rotary.turns.data_ptr(), out.data_ptr(), rotary._shape,
+             rotary._pointer, out.data_ptr(), rotary._shape,
              _HEADS_SHAPE(tokens, heads, dim, _TYPES[dtype], row, head, to_row, to_head))
     return out
 
@@ -239,46 +239,52 @@ def paged_append_rotary(k: torch.Tensor, v: torch.Tensor, k_pool: torch.Tensor,
     those (a new tensor, or `out`, which may be q), or None without q.  The queries of a
     token that no row claims become zeros."""
     cache = _cache_shape(k_pool, v_pool, tables)
-    rows, tokens, dtype, dim = tables.shape[0], k.shape[0], k_pool.dtype, k_pool.shape[3]
+    rows, tokens, dtype = tables.shape[0], k.shape[0], k_pool.dtype
+    _, _, kv_heads, dim = k_pool.shape
     if rotary.dim > dim:
         raise ValueError(f"the rotation has {rotary.dim} dimensions, a head {dim}")
-    heads = (tokens, k_pool.shape[2], dim)
+    heads = (tokens, kv_heads, dim)
     ks, vs = _heads(k, "k", dtype, heads), _heads(v, "v", dtype, heads)
     _row(starts, rows, "starts")
+    dev = k.get_device()
+    same = (dev >= 0 and v.get_device() == dev and k_pool.get_device() == dev
+            and v_pool.get_device() == dev and tables.get_device() == dev
+            and starts.get_device() == dev and rotary._device == dev
+            and (stream is None or stream.device.index == dev))
+    at = None
     if offsets is not None:
         _row(offsets, rows + 1, "offsets")
+        same, at = same and offsets.get_device() == dev, offsets.data_ptr()
     elif tokens != rows:
         raise ValueError(f"without offsets there must be one token a row, got {tokens} for {rows}")
-    if q is None and out is not None:
-        raise ValueError("out without q")
-    if q is not None:
-        shape = (tokens, q.shape[1] if q.dim() == 3 else "q_heads", dim)
-        qs = _heads(q, "q", dtype, shape)
-    dev = k.get_device()
-    named = {"v": v, "k_pool": k_pool, "v_pool": v_pool, "tables": tables, "starts": starts,
-             "rotary": rotary.turns, "offsets": offsets, "q": q, "out": out}
-    if (dev < 0 or any(t is not None and t.get_device() != dev for t in named.values())
-            or stream is not None and stream.device.index != dev):
-        _device(stream, k=k, **named)
-    queries = _HEADS_SHAPE(tokens, 0, dim, 0, 0, 0, 0, 0)
-    if q is not None:
+    if q is None:
+        if out is not None:
+            raise ValueError("out without q")
+    else:
+        q_heads = q.shape[1] if q.dim() == 3 else "q_heads"
+        qs = _heads(q, "q", dtype, (tokens, q_heads, dim))
+        same = same and q.get_device() == dev and (out is None or out.get_device() == dev)
+    if not same:
+        _device(stream, k=k, v=v, k_pool=k_pool, v_pool=v_pool, tables=tables, starts=starts,
+                rotary=rotary.turns, offsets=offsets, q=q, out=out)
+    q_at = out_at = None
+    if q is None:
+        queries = _HEADS_SHAPE(tokens, 0, dim, 0, 0, 0, 0, 0)
+    else:
         if out is None:
-            out = _empty(q, shape, dtype, stream)
-            to = shape[1] * dim, dim
+            out = _empty(q, (tokens, q_heads, dim), dtype, stream)
+            row, head = q_heads * dim, dim
         else:
-            to = _heads(out, "out", dtype, shape)
-        if shape[1]:
-            queries = _HEADS_SHAPE(tokens, shape[1], dim, _TYPES[dtype], qs[0], qs[1], to[0], to[1])
-        else:
-            q = None
+            row, head, _ = _heads(out, "out", dtype, (tokens, q_heads, dim))
+        queries = _HEADS_SHAPE(tokens, q_heads, dim, _TYPES[dtype], qs[0], qs[1], row, head)
+        if q_heads:
+            q_at, out_at = q.data_ptr(), out.data_ptr()
     if rows and tokens:
-        _run(dev, stream, "w4a16_paged_append_rotary", k.data_ptr(), v.data_ptr(),
-             rotary.turns.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), tables.data_ptr(),
-             starts.data_ptr(), None if offsets is None else offsets.data_ptr(),
-             None if q is None else q.data_ptr(), None if q is None else out.data_ptr(), cache,
-             rotary._shape, queries, ks[0], ks[1], vs[0], vs[1])
+        _run(dev, stream, "w4a16_paged_append_rotary", k.data_ptr(), v.data_ptr(), rotary._pointer,
+             k_pool.data_ptr(), v_pool.data_ptr(), tables.data_ptr(), starts.data_ptr(), at, q_at,
+             out_at, cache, rotary._shape, queries, ks[0], ks[1], vs[0], vs[1])
     elif q is not None and tokens:
-        _zero(out, stream)
+        _fill(out, stream, 0.0)
     return out
 
 
@@ -332,13 +338,13 @@ def paged_chunk_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.T
              _QUERY_SHAPE(q_heads, row, head, to_row, to_head,
                           dim ** -0.5 if scale is None else scale), tokens)
     elif tokens:
-        _zero(out, stream)
+        _fill(out, stream, 0.0)
         if return_lse:
-            _zero(lse, stream, -float("inf"))
+            _fill(lse, stream, -float("inf"))
     return (out, lse) if return_lse else out
 
 
-def _zero(t: torch.Tensor, stream, value: float = 0.0) -> None:
+def _fill(t: torch.Tensor, stream, value: float) -> None:
     """Fills what no row of an empty batch claims."""
     with torch.cuda.stream(stream):
         t.fill_(value)
@@ -533,22 +539,25 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0, str
     return logprobs, entropies, ids, likeliest
 
 
-def _penalty(value, rows: int, name: str):
-    """A penalty's tensor and number: one of every row (fp32 [rows]), or one number for all."""
-    if not isinstance(value, torch.Tensor):
-        return None, float(value)
+def _penalty(value: torch.Tensor, rows: int, name: str) -> int:
+    """The address of a penalty that is one of every row."""
     if value.dtype is not torch.float32 or value.shape != (rows,) or not value.is_contiguous():
         raise ValueError(f"{name} must be a number or a dense float32 tensor [{rows}], got "
                          f"{value.dtype} {list(value.shape)}")
-    return value, 0.0
+    return value.data_ptr()
 
 
-def _rows_of(t: torch.Tensor, rows: int, name: str, dtypes: tuple) -> None:
-    """Refuses what is not [rows, any], dense in its last dimension, of one of the types."""
-    if (t.dtype not in dtypes or t.dim() != 2 or t.shape[0] != rows
-            or t.shape[1] > 1 and t.stride(1) != 1):
+def _rows_of(t: torch.Tensor, rows: int, name: str, *dtypes) -> tuple:
+    """The width and row stride of what is [rows, any], dense in its last dimension, of one of the
+    types."""
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or t.dtype not in dtypes:
         raise ValueError(f"{name} must be a {' or '.join(map(str, dtypes))} tensor [{rows}, any], "
-                         f"dense in its last dimension, got {t.dtype} {list(t.shape)}")
+                         f"got {t.dtype} {list(shape)}")
+    strides = t.stride()
+    if strides[1] != 1 and shape[1] > 1:
+        raise ValueError(f"{name} must be dense in its last dimension")
+    return shape[1], strides[0]
 
 
 def adjust_logits(logits: torch.Tensor, tokens: torch.Tensor | None = None,
@@ -568,68 +577,83 @@ def adjust_logits(logits: torch.Tensor, tokens: torch.Tensor | None = None,
     biases[r, i] (fp32 [rows, n], n at most 1024) is added to the logit bias_ids[r, i] (int32),
     and where bit j % 32 of mask[r, j / 32] (int32 [rows, ceil(vocabulary / 32)]) is 0 logit j
     becomes -inf.  Tokens outside the vocabulary are passed over."""
-    kind = _TYPES.get(logits.dtype)
-    if kind is None or logits.dim() != 2:
+    dtype, shape, strides = logits.dtype, logits.shape, logits.stride()
+    kind = _TYPES.get(dtype)
+    if kind is None or len(shape) != 2:
         raise ValueError("logits must be a float16, bfloat16 or float32 tensor "
-                         f"[rows, vocabulary], got {logits.dtype} {list(logits.shape)}")
-    rows, vocabulary = logits.shape
-    if vocabulary > 1 and logits.stride(1) != 1:
+                         f"[rows, vocabulary], got {dtype} {list(shape)}")
+    rows, vocabulary = shape
+    if strides[1] != 1 and vocabulary > 1:
         raise ValueError("logits must be dense in their last dimension")
-    width = token_stride = wide = 0
+    dev = logits.get_device()
+    same = dev >= 0 and (stream is None or stream.device.index == dev)
+    width = token_stride = wide = said = known = prompted = 0
     if tokens is not None:
-        _rows_of(tokens, rows, "tokens", (torch.int32, torch.int64))
-        width, token_stride, wide = tokens.shape[1], tokens.stride(0), tokens.dtype is torch.int64
+        width, token_stride = _rows_of(tokens, rows, "tokens", torch.int32, torch.int64)
+        wide, said = tokens.dtype is torch.int64, tokens.data_ptr()
+        same = same and tokens.get_device() == dev
+        if lengths is not None:
+            _row(lengths, rows, "lengths")
+            known, same = lengths.data_ptr(), same and lengths.get_device() == dev
+        if prompts is not None:
+            _row(prompts, rows, "prompts")
+            prompted, same = prompts.data_ptr(), same and prompts.get_device() == dev
     elif lengths is not None or prompts is not None:
         raise ValueError("lengths or prompts without tokens")
-    for name, t in (("lengths", lengths), ("prompts", prompts)):
-        if t is not None:
-            _row(t, rows, name)
-    scalars, rates = [], []
-    for name, value in (("repetition", repetition), ("presence", presence),
-                        ("frequency", frequency)):
-        t, number = _penalty(value, rows, name)
-        if t is None and name == "repetition" and not number > 0:
-            raise ValueError(f"repetition must be above 0, got {number}")
-        rates.append(t)
-        scalars.append(number)
-    count = bias_stride = 0
-    if (bias_ids is None) != (biases is None):
-        raise ValueError("bias_ids and biases go together")
-    if biases is not None:
-        _rows_of(bias_ids, rows, "bias_ids", (torch.int32,))
-        _rows_of(biases, rows, "biases", (torch.float32,))
-        count, bias_stride = biases.shape[1], biases.stride(0)
-        if bias_ids.shape[1] != count or rows > 1 and bias_ids.stride(0) != bias_stride:
+    penalties = {"repetition": repetition, "presence": presence, "frequency": frequency}
+    each = [0, 0, 0]                            # addresses of those that rows have of their own
+    if isinstance(repetition, torch.Tensor):
+        same = same and repetition.get_device() == dev
+        each[0], repetition = _penalty(repetition, rows, "repetition"), 1.0
+    elif not repetition > 0:
+        raise ValueError(f"repetition must be above 0, got {repetition}")
+    if isinstance(presence, torch.Tensor):
+        same = same and presence.get_device() == dev
+        each[1], presence = _penalty(presence, rows, "presence"), 0.0
+    if isinstance(frequency, torch.Tensor):
+        same = same and frequency.get_device() == dev
+        each[2], frequency = _penalty(frequency, rows, "frequency"), 0.0
+    count = bias_stride = ids = values = 0
+    if bias_ids is not None and biases is not None:
+        count, bias_stride = _rows_of(biases, rows, "biases", torch.float32)
+        if _rows_of(bias_ids, rows, "bias_ids", torch.int32) != (count, bias_stride) and (
+                bias_ids.shape[1] != count or rows > 1):
             raise ValueError("bias_ids and biases must have the same shape and strides")
         if count > MAX_BIASES:
             raise ValueError(f"at most {MAX_BIASES} biases a row, got {count}")
-    mask_stride = 0
+        same = same and bias_ids.get_device() == dev and biases.get_device() == dev
+        if count:
+            ids, values = bias_ids.data_ptr(), biases.data_ptr()
+    elif bias_ids is not None or biases is not None:
+        raise ValueError("bias_ids and biases go together")
+    mask_stride = bits = 0
     if mask is not None:
-        _rows_of(mask, rows, "mask", (torch.int32,))
-        if mask.shape[1] != -(-vocabulary // 32):
-            raise ValueError(f"mask must have {-(-vocabulary // 32)} words a row, "
-                             f"got {mask.shape[1]}")
-        mask_stride = mask.stride(0)
-    if out is not None and (out.dtype is not logits.dtype or out.shape != logits.shape
-                            or vocabulary > 1 and out.stride(1) != 1):
-        raise ValueError(f"out must be {logits.dtype} {list(logits.shape)}, dense in its last "
-                         f"dimension, got {out.dtype} {list(out.shape)}")
-    dev = logits.get_device()
-    named = {"tokens": tokens, "lengths": lengths, "prompts": prompts, "repetition": rates[0],
-             "presence": rates[1], "frequency": rates[2], "bias_ids": bias_ids, "biases": biases,
-             "mask": mask, "out": out}
-    if (dev < 0 or any(t is not None and t.get_device() != dev for t in named.values())
-            or stream is not None and stream.device.index != dev):
-        _device(stream, logits=logits, **named)
+        words, mask_stride = _rows_of(mask, rows, "mask", torch.int32)
+        if words != -(-vocabulary // 32):
+            raise ValueError(f"mask must have {-(-vocabulary // 32)} words a row, got {words}")
+        bits, same = mask.data_ptr(), same and mask.get_device() == dev
+    if out is not None:
+        if out.dtype is not dtype or out.shape != shape or vocabulary > 1 and out.stride(1) != 1:
+            raise ValueError(f"out must be {dtype} {list(shape)}, dense in its last dimension, got "
+                             f"{out.dtype} {list(out.shape)}")
+        same = same and out.get_device() == dev
+    if not same:
+        given = {"tokens": tokens, "lengths": lengths, "prompts": prompts, "bias_ids": bias_ids,
+                 "biases": biases, "mask": mask, "out": out,
+                 **{n: t for n, t in penalties.items() if isinstance(t, torch.Tensor)}}
+        _device(stream, logits=logits, **given)
     if out is None:
-        out = _empty(logits, (rows, vocabulary), logits.dtype, stream)
+        out = _empty(logits, shape, dtype, stream)
+        out_stride = vocabulary
+    else:
+        out_stride = out.stride(0)
     if rows and vocabulary:
-        named["out"] = out
         _run(dev, stream, "w4a16_adjust_logits",
-             _ADJUST_TENSORS(logits.data_ptr(),
-                             *(0 if t is None else t.data_ptr() for t in named.values())),
-             _ADJUST_SHAPE(rows, vocabulary, kind, logits.stride(0), out.stride(0), wide, width,
-                           token_stride, count, bias_stride, mask_stride, *scalars))
+             _ADJUST_TENSORS(logits.data_ptr(), said, known, prompted, *each, ids, values, bits,
+                             out.data_ptr()),
+             _ADJUST_SHAPE(rows, vocabulary, kind, strides[0], out_stride, wide, width,
+                           token_stride, count, bias_stride, mask_stride, repetition, presence,
+                           frequency))
     return out
 
 
