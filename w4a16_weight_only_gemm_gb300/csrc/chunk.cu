@@ -147,11 +147,11 @@ struct ChunkArgs {
 // ---------------------------------------------------------------------------
 constexpr int kUnitCost = 3, kStaged = 2048;
 
+// ceil(steps / unit), or one more for very many (steps are at most 2^25).
 __device__ __forceinline__ int parts_of(int steps, int unit, float inverse) {
-    int k = (int)((float)steps * inverse);  // ceil(steps / unit), or one more for very many
-    k += (int64_t)k * unit < steps;
-    k += (int64_t)k * unit < steps;
-    return k;
+    int k = (int)((float)steps * inverse);
+    k += k * unit < steps;
+    return k + (k * unit < steps);
 }
 
 // (Loops are not unrolled: it runs once, and its time is mostly that of fetching its code.)
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a, Divisor
     static_assert(kPlanThreads == 1024, "32 warps: one for each length tried");
     __shared__ int64_t sums[32];
     __shared__ int longests[32], ints[32];
-    __shared__ int32_t staged[kStaged + 1];
+    __shared__ int32_t staged[kStaged + 1], staged_steps[kStaged];
     __shared__ float costs[32];
     __shared__ int units[32], keeps[32];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -197,6 +197,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a, Divisor
             slot.steps = seen > 0 ? (int)((seen + (1 << step_bits) - 1) >> step_bits) : 0;
         }
         a.slots[s] = slot;
+        if (s < kStaged) staged_steps[s] = slot.steps;
         total += slot.steps;
         items += slot.steps > 0;
         longest = max(longest, slot.steps);
@@ -238,15 +239,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a, Divisor
 #pragma unroll 1
         for (int round = 0; round < (full_rounds ? 2 : 1); ++round) {
             const int kept = round ? full_rounds : 0;
-            float whole = 0.f, whole_steps = 0.f;
-            int parts = 0;
+            int wholes = 0, parts = 0;
+            float whole_steps = 0.f;
 #pragma unroll 1
             for (int r = lane; r < slots; r += 32) {
-                const int n = a.slots[slots - 1 - r].steps;
-                const int p = r >= kept || n > cap ? parts_of(n, u, inverse) : n > 0;
-                if (p > 1) parts += p;
-                if (p == 1) whole += 1.f, whole_steps += (float)n;
+                const int s = slots - 1 - r, n = s < kStaged ? staged_steps[s] : a.slots[s].steps;
+                int p = n > 0;
+                if (r >= kept || n > cap) p = parts_of(n, u, inverse);
+                parts += p > 1 ? p : 0;
+                wholes += p == 1;
+                whole_steps += p == 1 ? (float)n : 0.f;
             }
+            float whole = (float)wholes;
 #pragma unroll
             for (int d = 16; d > 0; d /= 2) {
                 whole += __shfl_xor_sync(~0u, whole, d);
@@ -751,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (next < u.steps) wait(rest.kv_full[k % kSlots], k / kSlots);
                     fence_proxy_async_smem();
-#pragma unroll
+#pragma unroll 1
                     for (int q = 0; q < S::kTiles; ++q) {
                         const int steps = q ? steps1 : steps0;
                         if (i >= steps || (shared && (i & 1) != q)) continue;
