@@ -226,8 +226,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a, Divisor
     const float sms = (float)a.sms, share = (float)total / sms;
     const int cap = (int)fmaxf(share, 1.f);
     int unit = max(longest, 1), keep = slots;
-    // (an item that is a small part of a block's share is not worth a cut)
-    if ((float)longest * 8.f > share && a.most_parts > 0) {
+    // (an item that is a sixth of a block's share or less is not worth a cut, nor the search for one)
+    if ((float)longest * 6.f > share && a.most_parts > 0) {
         // as many as make full rounds of the blocks
         const int full_rounds = (int)(floorf((float)items * (float)heads / sms) * sms / (float)heads);
         // k = 1, 2, 3, ... 8, then some 2^(1/4) apart up to 512
