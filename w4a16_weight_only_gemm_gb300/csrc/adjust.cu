@@ -9,8 +9,8 @@
 // row has said or has biases for, one by one.  Those a block finds without a table
 // in memory: it takes a slice of one row's vocabulary, holds a word of counts for
 // each token of it in shared memory, and reads the whole history, which the row's
-// other blocks find in L2 (8191 tokens are 32 KB, as many bytes as a slice of 16384
-// logits of 16 bits); a sweep over the words then lists the tokens that were said.
+// other blocks find in L2 (4096 tokens are 16 KB, as many bytes as a slice of 8192
+// logits of 16 bits).
 // Counts are integers and a token's logit is its own, so the order of the atomics
 // changes nothing.  A piece of 16 bytes that the mask has none of is not read, and in
 // place only what changes is touched.
@@ -18,6 +18,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -29,7 +30,8 @@ constexpr int kThreads = 256;
 constexpr int kBlocksPerSm = 8;
 constexpr int kAhead = 1;            // pieces of a thread on their way
 constexpr int kWordBytes = 16384;    // of a slice's words at most
-constexpr int kListed = 4096;        // words swept at a time, as many as the list has places for
+constexpr int kListed = 4096;        // places of the list; words swept at a time
+constexpr int kOwn = kListed / kThreads;  // of them a thread's, for what it finds itself
 constexpr int kMostBiases = W4A16_MAX_BIASES;
 
 // A token's word: whether a bias is listed for it, whether the prompt has it, and in the other bits
@@ -114,41 +116,64 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) adjust_kernel(AdjustAr
     if (threadIdx.x == 0) listed = twice = 0;
     __syncthreads();
 
-    // The history.  (Predicated, and nothing waits for it: with branches, or with the old word
-    // returned to see who is first, this took longer than all the rest.)
-    const uint32_t word0 = smem_u32(words) + skip * sizeof(W);
-    const auto note = [&](int i, int32_t token) {
-        const uint32_t at = (uint32_t)token - (uint32_t)from;
-        const uint32_t by = sizeof(W) == 2 ? 16 * ((at + skip) & 1) : 0;  // its place in 32 bits
-        asm volatile(
-            "{\n\t.reg .pred p, q, r;\n\t"
-            "setp.lt.s32 r, %3, %4;\n\t"
-            "setp.lt.and.u32 p, %1, %2, r;\n\t"
-            "setp.lt.and.u32 q, %1, %2, !r;\n\t"
-            "@p red.shared.or.b32 [%0], %5;\n\t"
-            "@q red.shared.add.u32 [%0], %6;\n\t}" ::"r"((word0 + at * (uint32_t)sizeof(W)) & ~3u),
-            "r"(at), "r"(span), "r"(i), "r"(prompt), "r"(Word<W>::kPrompt << by), "r"(1u << by)
-            : "memory");
+    // The history: first what the prompt has, then what the generation has.  Each thread also writes
+    // down what it finds in the slice, which is little.  (Predicated, and nothing waits for it: with
+    // branches, or with the old word returned to see who is first, this took longer than all the rest.
+    // A number before the row's first token counts in a word that stands for none.)
+    const uint32_t word0 = smem_u32(words), own0 = smem_u32(list) + 2 * threadIdx.x;
+    const uint32_t size = (uint32_t)(to - begin);
+    int found = 0;
+    const auto note = [&](auto said, int32_t token) {
+        constexpr bool kSaid = decltype(said)::value;  // by the prompt
+        const uint32_t at = (uint32_t)token - (uint32_t)begin;
+        const uint32_t address = sizeof(W) == 2 ? word0 + (2 * at & ~3u) : word0 + 4 * at;
+        const uint32_t unit = kSaid ? Word<W>::kPrompt : 1u;
+        const uint32_t value = sizeof(W) == 2 && (at & 1) ? unit << 16 : unit;
+        const bool in = at < size;
+        if constexpr (kSaid)
+            asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p red.shared.or.b32 [%0], %1;\n\t}"
+                         ::"r"(address), "r"(value), "r"((uint32_t)in) : "memory");
+        else
+            asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p red.shared.add.u32 [%0], %1;\n\t}"
+                         ::"r"(address), "r"(value), "r"((uint32_t)in) : "memory");
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p st.shared.u16 [%0], %1;\n\t}"
+                     ::"r"(own0 + found * (2 * kThreads)), "h"((uint16_t)at), "r"((uint32_t)(in && found < kOwn))
+                     : "memory");
+        found += in;
     };
-    if (a.s.wide) {
-        const int64_t* tokens = static_cast<const int64_t*>(a.t.tokens) + row * a.s.token_stride;
-#pragma unroll 4
-        for (int i = threadIdx.x; i < length; i += kThreads) {
-            const int64_t token = tokens[i];
-            note(i, token >= 0 && token < vocabulary ? (int32_t)token : -1);
-        }
-    } else if (length) {
-        const int32_t* tokens = static_cast<const int32_t*>(a.t.tokens) + row * a.s.token_stride;
-        const int whole = reinterpret_cast<uintptr_t>(tokens) % 16 == 0 ? length / 4 * 4 : 0;
+    // tokens first .. last - 1 of the row
+    const auto read = [&](auto said, int first, int last) {
+        if (a.s.wide) {
+            const int64_t* tokens = static_cast<const int64_t*>(a.t.tokens) + row * a.s.token_stride;
 #pragma unroll 2
-        for (int i = threadIdx.x * 4; i < whole; i += kThreads * 4) {
-            const int4 four = *reinterpret_cast<const int4*>(tokens + i);
-            note(i, four.x);
-            note(i + 1, four.y);
-            note(i + 2, four.z);
-            note(i + 3, four.w);
+            for (int i = first + threadIdx.x; i < last; i += kThreads) {
+                const int64_t token = tokens[i];
+                note(said, token >= 0 && token < vocabulary ? (int32_t)token : INT32_MIN);
+            }
+            return;
         }
-        for (int i = whole + threadIdx.x; i < length; i += kThreads) note(i, tokens[i]);
+        const int32_t* tokens = static_cast<const int32_t*>(a.t.tokens) + row * a.s.token_stride;
+        // fours that begin at a 16-byte boundary, and single ones before and behind them
+        const int shift = (int)(reinterpret_cast<uintptr_t>(tokens) / 4 % 4);
+        const int begin4 = min((first + shift + 3) / 4 * 4 - shift, last);
+        const int end4 = max((last + shift) / 4 * 4 - shift, begin4);
+#pragma unroll 2
+        for (int i = begin4 + threadIdx.x * 4; i < end4; i += kThreads * 4) {
+            const int4 four = *reinterpret_cast<const int4*>(tokens + i);
+            note(said, four.x);
+            note(said, four.y);
+            note(said, four.z);
+            note(said, four.w);
+        }
+        const int singles = begin4 - first + last - end4;
+        if (threadIdx.x < singles) {
+            const int i = first + threadIdx.x;
+            note(said, tokens[i < begin4 ? i : i - begin4 + end4]);
+        }
+    };
+    if (length) {
+        read(std::true_type(), 0, min(max(prompt, 0), length));
+        read(std::false_type(), min(max(prompt, 0), length), length);
     }
     // Tokens that a bias is listed for are marked: they are their biases' business.
     for (int i = threadIdx.x; i < biases; i += kThreads) {
@@ -205,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) adjust_kernel(AdjustAr
     const Penalties<W> p = {a.t.repetition ? a.t.repetition[row] : (float)a.s.repetition,
                             a.t.presence ? a.t.presence[row] : (float)a.s.presence,
                             a.t.frequency ? a.t.frequency[row] : (float)a.s.frequency};
-    __syncthreads();
+    const bool own = !__syncthreads_or(found > kOwn) && !a.in_place;
 
     // Biased tokens.  One with several biases is its first listing's, with the biases added in the
     // order of the list.
@@ -223,9 +248,21 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) adjust_kernel(AdjustAr
         // (in place a later listing's thread may read what the first has written, and is dropped)
         if (!later) out[id] = from_float<T>(y);
     }
-    // Said tokens: those of kListed words at a time are listed, a bit a word, and then taken one by
-    // one, so that all threads have their share of what has to be fetched.
+    // Said tokens: each thread's own, where all had places for what they found.  One that several
+    // threads found is written by each of them, alike.
+    if (own) {
+        for (int n = 0; n < found; ++n) {
+            const int at = list[n * kThreads + threadIdx.x], id = begin + at;
+            const uint32_t word = words[at];
+            if (id >= 0 && word < Word<W>::kBiased && allowed(mask, id))
+                out[id] = from_float<T>(p.apply(to_float(x[id]), word));
+        }
+        return;
+    }
+    // Else (and in place, where a logit is to be read once) those of kListed words at a time are listed,
+    // a bit a word, and then taken one by one, so that all threads have their share.
     if (!length) return;
+    __syncthreads();
     constexpr int kEach = 16 / sizeof(W);  // words of a 16-byte read
     for (int first = 0; first < a.slice; first += kListed) {
         uint32_t set = 0;
@@ -247,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) adjust_kernel(AdjustAr
         __syncthreads();
         for (int i = threadIdx.x; i < listed; i += kThreads) {
             const int id = begin + list[i];
-            if (allowed(mask, id)) out[id] = from_float<T>(p.apply(to_float(x[id]), words[list[i]]));
+            if (id >= 0 && allowed(mask, id)) out[id] = from_float<T>(p.apply(to_float(x[id]), words[list[i]]));
         }
         if (first + kListed >= a.slice) break;
         __syncthreads();
@@ -282,7 +319,7 @@ cudaError_t launch(AdjustArgs a, cudaStream_t stream, const DeviceCtx& ctx) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.s.rows * a.slices));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = slice * sizeof(W) + 2 * std::min<int64_t>(slice, kListed);
+    cfg.dynamicSmemBytes = slice * sizeof(W) + 2 * kListed;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
