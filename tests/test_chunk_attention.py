@@ -113,23 +113,31 @@ def test_garbage_where_no_row_is(w4lib, garbage):
     check(*make(ROWS, 2, 4, 128, 32, torch.float16, garbage=garbage))
 
 
+# a row of two tiles and one of one; the first among many others, so that no item is cut; rows of
+# one tile, whose steps two groups of warps share
+SPOILT = {"cut": [(40, 150), (100, 100)], "whole": [(40, 150)] + [(0, 260)] * 90,
+          "one tile": [(40, 20), (700, 9)]}
+
+
 @gpu
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("rows", SPOILT)
 @pytest.mark.parametrize("garbage", [math.nan, math.inf, -math.inf])
-def test_garbage_that_only_later_tokens_see(w4lib, garbage, dim, dtype):
+def test_garbage_that_only_later_tokens_see(w4lib, garbage, rows, dim, dtype):
     """A key or a value that is not finite spoils the tokens that see it, and no other."""
-    args = make([(40, 150), (100, 100)], 2, 4, dim, 16, dtype, garbage=0.0, seed=3)
+    rows = SPOILT[rows]
+    args = make(rows, 2, 4, dim, 16, dtype, garbage=0.0, seed=3)
     q, k, v, tables, lengths, offsets = args
-    plain = w4.paged_chunk_attention(*args)
-    for pool, at in ((k, 90), (v, 90), (v, 130)):
+    plain, held, new = w4.paged_chunk_attention(*args), *rows[0]
+    for pool, at in ((k, held + new // 3), (v, held + new // 3), (v, held + new - 2)):
         spoilt = pool.clone()
         page, slot = int(tables[0, at // 16]), at % 16
         spoilt[page, slot, 1, 3] = garbage
         pools = (spoilt, v) if pool is k else (k, spoilt)
         out, lse = w4.paged_chunk_attention(q, *pools, tables, lengths, offsets, return_lse=True)
-        seeing = torch.zeros(250, 8, dtype=torch.bool, device="cuda")
-        seeing[at - 40:150, 4:] = True
+        seeing = torch.zeros(q.shape[:2], dtype=torch.bool, device="cuda")
+        seeing[at - held:new, 4:] = True
         assert torch.equal(out[~seeing], plain[~seeing])
         if pool is v:                            # one dimension of V, of all tokens that see it
             assert not torch.isfinite(out[seeing][:, 3]).any()
@@ -258,6 +266,37 @@ def test_strided_query_and_output(w4lib):
     tables[:, :rest[2].shape[1]] = rest[2]
     rest[2] = tables[:, :rest[2].shape[1]]
     assert torch.equal(w4.paged_chunk_attention(q, *rest), plain)
+
+
+@gpu
+@pytest.mark.parametrize("page", [16, 13])
+def test_heads_and_pages_of_stride_zero(w4lib, page):
+    """Key-value heads that are one head seen several times, and a table of one page repeated."""
+    q, k, v, tables, lengths, offsets = make([(100, 40), (3, 200)], 1, 8, 64, page, torch.float16,
+                                             seed=14, garbage=0.0)
+    four = [t.expand(-1, -1, 4, -1) for t in (k, v)]
+    assert four[0].stride(2) == 0
+    # (two heads to each of four: other tiles than eight to one, so other sums, each within the bound)
+    check(q, *four, tables, lengths, offsets)
+    same = tables.clone()
+    same[:] = tables[0, 0]
+    check(q, k, v, same, lengths, offsets)
+
+
+@gpu
+def test_offsets_that_make_no_sense(w4lib):
+    """Descending, below 0 and past the tokens: whatever comes out, nothing else is touched and the
+    next call is right."""
+    args = make([(100, 40), (3, 200), (0, 30)], 2, 4, 64, 16, torch.float16, seed=15, garbage=0.0)
+    plain = w4.paged_chunk_attention(*args)
+    wide = torch.full((272, 9, 64), 7.0, device="cuda").half()
+    for bad in ([0, 240, 40, 270], [-5, 40, 10 ** 9, 270], [270, 0, 0, 0], [2 ** 31 - 1] * 4,
+                [-2 ** 31] * 4, [0, 0, 0, 2 ** 31 - 1]):
+        w4.paged_chunk_attention(*args[:5], ints(bad), out=wide[1:271, :8])
+        torch.cuda.synchronize()
+        assert w4.device_status() == 0
+        assert (wide[0] == 7).all() and (wide[271] == 7).all() and (wide[:, 8] == 7).all()
+    assert torch.equal(w4.paged_chunk_attention(*args), plain)
 
 
 @gpu

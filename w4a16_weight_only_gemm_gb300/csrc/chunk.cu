@@ -53,7 +53,7 @@ constexpr int kSoftmaxRegisters = 184, kOtherRegisters = 72;
 constexpr int kSlots = 4;         // of the ring: keys, values, keys, values
 constexpr int kUnits = 4;         // places for units' notes of values that are not finite
 constexpr int kPlanThreads = 1024;
-constexpr int kJoinThreads = 128;
+constexpr int kJoinThreads = 128, kJoinAhead = 4;  // parts on their way
 constexpr int kPartsPerSm = 4;    // of the workspace
 
 // Sizes by the padded head size: queries of an item, positions of a step.
@@ -1281,24 +1281,37 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(ChunkArgs a) {
         const int lin = joint.item.lin0 + of_item;
         const int token = a.group.quotient(lin), h = head * a.group.value + lin - token * a.group.value;
         if (joint.item.position0 + token < 0) continue;  // zeros already
-        const auto part = [&](int p) { return (int64_t)(joint.part + p) * a.c.kv_heads + head; };
-        float top = -INFINITY;
-        for (int p = 0; p < joint.count; ++p)
-            top = fmaxf(top, a.partial_ml[part(p) * S::kRows + q * kQueryTile + r].x);
-        const float base = top == -INFINITY ? 0.f : top;
-        float sum = 0.f, v[8] = {};
-#pragma unroll 4
-        for (int p = 0; p < joint.count; ++p) {
-            const float2 ml = a.partial_ml[part(p) * S::kRows + q * kQueryTile + r];
-            if (ml.y == 0.f) continue;  // no step, or nothing seen: no output was written, or zeros
-            const float e = exp2_fast(ml.x - base);
-            const float* from_part =
-                a.partial + (((part(p) * S::kTiles + q) * (DP / 4) + 2 * piece) * kQueryTile + r) * 4;
-            const float4 x = *reinterpret_cast<const float4*>(from_part);
-            const float4 y = *reinterpret_cast<const float4*>(from_part + 4 * kQueryTile);
-            sum += e * ml.y;
-            v[0] += e * x.x, v[1] += e * x.y, v[2] += e * x.z, v[3] += e * x.w;
-            v[4] += e * y.x, v[5] += e * y.y, v[6] += e * y.z, v[7] += e * y.w;
+        float top = -INFINITY, sum = 0.f, v[8] = {};
+#pragma unroll 1
+        for (int first = 0; first < joint.count; first += kJoinAhead) {
+            float2 ml[kJoinAhead];
+            float4 x[kJoinAhead], y[kJoinAhead];
+            float higher = top;
+#pragma unroll
+            for (int n = 0; n < kJoinAhead; ++n) {
+                ml[n] = make_float2(-INFINITY, 0.f);
+                if (first + n >= joint.count) continue;
+                const int64_t part = (int64_t)(joint.part + first + n) * a.c.kv_heads + head;
+                const float* from =
+                    a.partial + (((part * S::kTiles + q) * (DP / 4) + 2 * piece) * kQueryTile + r) * 4;
+                ml[n] = a.partial_ml[part * S::kRows + q * kQueryTile + r];
+                x[n] = *reinterpret_cast<const float4*>(from);
+                y[n] = *reinterpret_cast<const float4*>(from + 4 * kQueryTile);
+                higher = fmaxf(higher, ml[n].x);
+            }
+            const float base = higher == -INFINITY ? 0.f : higher, keep = exp2_fast(top - base);
+            top = higher;
+            sum *= keep;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] *= keep;
+#pragma unroll
+            for (int n = 0; n < kJoinAhead; ++n) {
+                if (ml[n].y == 0.f) continue;  // no step, or nothing seen: what lies there is no output
+                const float e = exp2_fast(ml[n].x - base);
+                sum += e * ml[n].y;
+                v[0] += e * x[n].x, v[1] += e * x[n].y, v[2] += e * x[n].z, v[3] += e * x[n].w;
+                v[4] += e * y[n].x, v[5] += e * y[n].y, v[6] += e * y[n].z, v[7] += e * y[n].w;
+            }
         }
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const int64_t t = joint.item.token0 + token;
@@ -1410,7 +1423,7 @@ cudaError_t attend(ChunkArgs a, const w4a16_cache_shape& cache, cudaStream_t str
     if ((e = cudaLaunchKernelEx(&cfg, chunk_kernel<T, DP>, maps[0], maps[1], maps[2], a)) != cudaSuccess)
         return e;
     if (a.most_parts == 0) return cudaSuccess;
-    cfg.gridDim = dim3((unsigned)(8 * ctx.num_sms));
+    cfg.gridDim = dim3((unsigned)(16 * ctx.num_sms));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, join_kernel<T, DP>, a);
