@@ -23,9 +23,8 @@
 // what the second has is added to the first's at the end.
 // The work is cut by a plan kernel, as only the device knows the lengths: items are
 // split into parts where that levels the load, and a join kernel adds those up.
-// Blocks take units from a counter, longest first within a row, the parts of one
-// item side by side: blocks at work at the same time read the same keys and values,
-// through L2.
+// Blocks take units from a counter, the longest first, an item's heads and parts side by
+// side: blocks at work at the same time read the same keys and values, through L2.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -51,6 +50,7 @@ constexpr int kThreads = 32 * (kLookWarp + kLookWarps);
 // warpgroups' shares, 2 x 184 + 2 x 72, are what the block was launched with.
 constexpr int kSoftmaxRegisters = 184, kOtherRegisters = 72;
 constexpr int kSlots = 4;         // of the ring: keys, values, keys, values
+constexpr int kWanted = 4;        // steps of a unit left to copy when the next one is asked for
 constexpr int kUnits = 4;         // places for units' notes of values that are not finite
 constexpr int kPlanThreads = 1024;
 constexpr int kJoinThreads = 128, kJoinAhead = 4;  // parts on their way
@@ -139,13 +139,17 @@ struct ChunkArgs {
 //
 // Item j of row b takes slot offsets[b] group / rows + b + j (rows of an item): as
 // offsets do not descend, no two items share one, and an item's row is found by a
-// search.  Some of the items are handed out whole, first; the others, and any longer
-// than a block's share, are cut into ceil(n / u) parts of nearly equal length.  Tried are
-// 32 lengths u, with none whole or as many as make full rounds of the blocks; taken is
-// what makes the estimated time least: a unit costs its steps and three more (four where it
-// is a part), and blocks are level to half a unit, or take rounds of parts that are alike.
+// search.  Some of the items are handed out whole, first and by their length, the longest
+// before the others; the rest, and any longer than a block's share, are cut into
+// ceil(n / u) parts of nearly equal length.  Tried are 32 lengths u, with none whole or as
+// many as make full rounds of the blocks; taken is what makes the estimated time least: a
+// unit costs its steps and three more (four where it is a part), and the blocks end within
+// half of one of the last units, those that the blocks take last being the shortest; or
+// they take rounds of units that are alike.  (48 rows, 8 of them with chunks of up to 509
+// tokens and positions from few to 8191: with items in the order of their rows the last
+// block ended 207 us after the start, the mean one after 138.)
 // ---------------------------------------------------------------------------
-constexpr int kUnitCost = 3, kStaged = 2048;
+constexpr int kUnitCost = 3, kStaged = 2048, kLengths = 64;
 
 // ceil(steps / unit), or one more for very many (steps are at most 2^25).
 __device__ __forceinline__ int parts_of(int steps, int unit, float inverse) {
@@ -162,12 +166,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a, Divisor
     __shared__ int32_t staged[kStaged + 1], staged_steps[kStaged];
     __shared__ float costs[32];
     __shared__ int units[32], keeps[32];
+    __shared__ int of_length[kLengths];  // items by their length, then where those go
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     grid_dependency_wait();
     grid_launch_dependents();
     const int heads = a.c.kv_heads, batch = a.c.batch, group = a.group.value;
     const int slots = (int)a.slot_count;
     const bool short_batch = batch <= kStaged;
+    if (tid < kLengths) of_length[tid] = 0;
     if (short_batch)
 #pragma unroll 1
         for (int b = tid; b <= batch; b += kPlanThreads) staged[b] = (int32_t)a.offset(b);
@@ -221,51 +227,75 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a, Divisor
         total = sums[lane], items = ints[lane], longest = longests[lane], shortest = units[lane];
     }
     total *= heads;
-    // Slots are taken from the last to the first, so that a row's long items come first.  Cut are
-    // those from the `keep`-th on, and those longer than `cap`.
+    // Slots are gone through from the last to the first.  Cut are those from the `keep`-th on, and
+    // those longer than `cap`.
     const float sms = (float)a.sms, share = (float)total / sms;
     const int cap = (int)fmaxf(share, 1.f);
+    const float by_length = (float)(kLengths - 1) / (float)max(longest, 1);
+    const auto steps_of_slot = [&](int s) { return s < kStaged ? staged_steps[s] : a.slots[s].steps; };
     int unit = max(longest, 1), keep = slots;
     // (an item that is a sixth of a block's share or less is not worth a cut, nor the search for one)
     if ((float)longest * 6.f > share && a.most_parts > 0) {
+        // The longest of the last units, where none is cut: as many of the shortest items as there
+        // are blocks.
+        int last = longest;
+        const bool many = (float)items * (float)heads > sms;
+        if (many) {
+#pragma unroll 1
+            for (int s = tid; s < slots; s += kPlanThreads) {
+                const int n = steps_of_slot(s);
+                if (n) atomicAdd(&of_length[(int)((float)n * by_length)], heads);
+            }
+            __syncthreads();
+            static_assert(kLengths == 64, "two lengths a lane");
+            const int x = of_length[2 * lane], y = of_length[2 * lane + 1];
+            int upto = x + y;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const int o = __shfl_up_sync(~0u, upto, d);
+                if (lane >= d) upto += o;
+            }
+            const int enough = __ballot_sync(~0u, upto >= a.sms);
+            const int at = enough ? 2 * (__ffs(enough) - 1) + 2 : kLengths;
+            last = min(longest, (int)((float)at / by_length) + 1);
+        }
         // as many as make full rounds of the blocks
         const int full_rounds = (int)(floorf((float)items * (float)heads / sms) * sms / (float)heads);
         // k = 1, 2, 3, ... 8, then some 2^(1/4) apart up to 512
         const int k = warp < 8 ? warp + 1 : (int)(8.f * exp2f((float)(warp - 7) * 0.25f));
         const int u = (longest + k - 1) / k;
         const float inverse = 1.f / (float)u;
+        const bool alike = shortest * 5 >= longest * 4;
         float best = INFINITY;
         int best_keep = 0;
 #pragma unroll 1
         for (int round = 0; round < (full_rounds ? 2 : 1); ++round) {
             const int kept = round ? full_rounds : 0;
-            int wholes = 0, parts = 0;
-            float whole_steps = 0.f;
+            int whole = 0, parts = 0;
 #pragma unroll 1
             for (int r = lane; r < slots; r += 32) {
-                const int s = slots - 1 - r, n = s < kStaged ? staged_steps[s] : a.slots[s].steps;
+                const int n = steps_of_slot(slots - 1 - r);
                 int p = n > 0;
                 if (r >= kept || n > cap) p = parts_of(n, u, inverse);
                 parts += p > 1 ? p : 0;
-                wholes += p == 1;
-                whole_steps += p == 1 ? (float)n : 0.f;
+                whole += p == 1;
             }
-            float whole = (float)wholes;
 #pragma unroll
             for (int d = 16; d > 0; d /= 2) {
                 whole += __shfl_xor_sync(~0u, whole, d);
-                whole_steps += __shfl_xor_sync(~0u, whole_steps, d);
                 parts += __shfl_xor_sync(~0u, parts, d);
             }
-            const float all_parts = (float)parts * (float)heads, all_whole = whole * (float)heads;
+            const float all_parts = (float)parts * (float)heads, all_whole = (float)whole * (float)heads;
             const float work = (float)total + kUnitCost * all_whole + (kUnitCost + 1) * all_parts;
-            float cost = work / sms + (float)(u + kUnitCost) / 2;
-            // (parts all alike: rounds of them)
-            if (whole == 0.f && shortest * 5 >= longest * 4)
+            const float end = (float)(all_parts >= sms ? min(u, last) : last);
+            float cost = work / sms + (end + kUnitCost) / 2;
+            if (all_parts + all_whole <= sms)  // all at once
+                cost = (float)((parts ? u : longest) + kUnitCost + (parts > 0));
+            if (alike && whole == 0)
                 cost = fminf(cost, ceilf(all_parts / sms) * (float)(u + kUnitCost + 1));
-            if (whole > 0.f)  // rounds of whole items
-                cost = fmaxf(cost, ceilf(all_whole / sms) * (whole_steps / whole + kUnitCost));
-            if (parts) cost += 2.f;  // the join
+            if (alike && parts == 0)
+                cost = ceilf(all_whole / sms) * (float)(longest + kUnitCost);
+            if (parts) cost += 1.f;  // the join
             if ((int64_t)parts * heads <= a.most_parts && cost < best) best = cost, best_keep = kept;
         }
         if (lane == 0) costs[warp] = best, units[warp] = u, keeps[warp] = best_keep;
@@ -279,6 +309,29 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a, Divisor
             if (o < least || (o == least && w < which)) least = o, which = w;
         }
         if (least < INFINITY) unit = units[which], keep = keeps[which];
+        if (tid < kLengths) of_length[tid] = 0;
+    }
+    const auto parts_of_slot = [&](int r, int n) {
+        return n == 0 ? 0 : r >= keep || n > cap ? (n + unit - 1) / unit : 1;
+    };
+    // Whole items by their length: how many there are, then where the longest of them begin.
+    __syncthreads();
+#pragma unroll 1
+    for (int r = tid; r < slots; r += kPlanThreads) {
+        const int n = steps_of_slot(slots - 1 - r);
+        if (parts_of_slot(r, n) == 1) atomicAdd(&of_length[(int)((float)n * by_length)], 1);
+    }
+    __syncthreads();
+    if (warp == 0) {
+        const int x = of_length[2 * lane], y = of_length[2 * lane + 1];
+        int from = x + y;  // of these lengths and longer ones
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int o = __shfl_down_sync(~0u, from, d);
+            if (lane + d < 32) from += o;
+        }
+        of_length[2 * lane] = from - x;
+        of_length[2 * lane + 1] = from - x - y;
     }
     // The entries: whole ones from the table's start, parts from place `slots` on.
     int base_whole = 0, base_parts = 0, base_joints = 0;
@@ -288,7 +341,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a, Divisor
         Slot slot = {};
         if (r < slots) slot = a.slots[slots - 1 - r];
         const int n = slot.steps;
-        const int k = n == 0 ? 0 : r >= keep || n > cap ? (n + unit - 1) / unit : 1;
+        const int k = parts_of_slot(r, n);
         // before this slot: whole ones, joints (16 bits each: 1024 slots at most), parts
         const int own = (k == 1) | (k > 1) << 16, own_parts = k > 1 ? k : 0;
         int upto = own, upto_parts = own_parts;
@@ -318,7 +371,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a, Divisor
 #pragma unroll 1
         for (int i = 0, at = 0; i < k; ++i) {
             const int steps = each + (i < more);
-            a.entries[k > 1 ? slots + part + i : base_whole + (upto & 0xFFFF)] = {
+            a.entries[k > 1 ? slots + part + i : atomicAdd(&of_length[(int)((float)n * by_length)], 1)] = {
                 slot.item, at, steps, k > 1 ? part + i : -1, {}};
             at += steps;
         }
@@ -585,7 +638,7 @@ struct Odd {
 
 template <int DP>
 struct Rest {
-    uint64_t unit_full[2], unit_free[2], q_full, q_free;
+    uint64_t unit_full[2], unit_free[2], unit_wanted, q_full, q_free;
     uint64_t kv_full[kSlots], kv_free[kSlots], looked[kSlots];
     uint64_t s_full[2], p_full[2][2], o_full[2], other_full, other_free, done;
     uint32_t tmem;
@@ -624,6 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bar(rest.p_full[i][1]), 4);
             mbar_init(bar(rest.o_full[i]), 2);
         }
+        mbar_init(bar(rest.unit_wanted), 1);
         mbar_init(bar(rest.q_full), 33 * kCopyWarps);
         mbar_init(bar(rest.q_free), 1);
         for (int i = 0; i < kSlots; ++i) {
@@ -690,6 +744,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (uint32_t n = 0;; ++n) {
                 unsigned i = blockIdx.x;
                 if (n) {
+                    // (not before the last unit's end is near: blocks that took theirs two ahead were
+                    // as good as dealt out from the start)
+                    if (!warp_wait(bar(rest.unit_wanted), n - 1, a.timeout_ns, a.status)) break;
                     if (lane == 0) i = gridDim.x + atomicAdd(&a.plan->next, 1u);
                     i = __shfl_sync(~0u, i, 0);
                 }
@@ -697,9 +754,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 u.steps = -1;
                 if (i < (whole + parts) * heads) {
                     const bool part = i >= whole * heads;
-                    const unsigned j = part ? i - whole * heads : i, of = part ? parts : whole;
-                    u.head = (int)(j / of);
-                    const Entry entry = a.entries[(part ? a.slot_count : 0) + j % of];
+                    const unsigned j = part ? i - whole * heads : i;
+                    u.head = (int)(j % heads);
+                    const Entry entry = a.entries[(part ? a.slot_count : 0) + j / heads];
                     u.item = entry.item;
                     u.first = entry.first;
                     u.steps = entry.steps;
@@ -902,6 +959,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < u.steps + lag; ++i) {
                 const int now = next;
                 if (i + 1 < u.steps) next = page_of(i + 1);
+                if (w == 0 && lane == 0 && i == max(u.steps - kWanted, 0)) mbar_arrive(bar(rest.unit_wanted));
 #pragma unroll 1
                 for (int value = 0; value < 2; ++value) {
                     const int of = value ? i - lag : i;  // the step
