@@ -480,7 +480,8 @@ typedef struct w4a16_rotary_shape {
 
 /* Heads [tokens, heads, head_dim] that are read and heads of the same sizes
  * that are written: tokens 0 .. 2^31, heads 1 .. 1024, head_dim 8 .. 256, a
- * multiple of 8; strides in elements, multiples of 8. */
+ * multiple of 8; strides in elements, multiples of 8; no two heads that are
+ * written share a value (W4A16_ERR_SHAPE). */
 typedef struct w4a16_heads_shape {
     int64_t tokens, heads, head_dim, type;
     int64_t token_stride, head_stride, out_token_stride, out_head_stride;
@@ -534,9 +535,9 @@ int w4a16_paged_append_rotary(const void *k, const void *v, const uint64_t *turn
  *              w4a16_paged_attention does.
  *   offsets    [batch + 1] int32, not descending, within 0 .. tokens.  A row
  *              may have no tokens.
- *   out        [tokens, q_heads, head_dim], written.  A token with a position
- *              below 0 (a row with more tokens than positions) and one that no
- *              row claims get zeros.
+ *   out        [tokens, q_heads, head_dim], written; no two heads share a value
+ *              (W4A16_ERR_SHAPE).  A token with a position below 0 (a row with
+ *              more tokens than positions) and one that no row claims get zeros.
  *   lse        NULL, or [tokens, q_heads] float, written: the natural logarithm
  *              of sum_p exp(scale * q . K), -infinity for tokens as above.
  *   workspace  w4a16_paged_chunk_workspace(cache, q_heads, tokens) bytes,
@@ -548,7 +549,8 @@ int w4a16_paged_append_rotary(const void *k, const void *v, const uint64_t *turn
  * whose score is -infinity; a head that has no other position gets zeros and
  * -infinity.  A score that is NaN or +infinity gives NaN.  A value that is not
  * finite makes its dimension of out not finite (an infinity may come out as
- * NaN) for the tokens that see it, and for no other.  Two calls on the same
+ * NaN) for the tokens that see it, and for no other; at a position left out for
+ * its score alone it may do so or not.  Two calls on the same
  * inputs and sizes give the same bits.
  * Errors: as w4a16_paged_attention.
  */
@@ -732,7 +734,8 @@ typedef struct w4a16_adjust_shape {
  * In FP32, rounded once; a logit that nothing applies to keeps its bits.
  *
  *   logits, out    [rows, vocabulary] of `type`, aligned to their element; out
- *                  is logits (with the same stride) or overlaps none of it.
+ *                  is logits (with the same stride) or overlaps none of it, and its
+ *                  rows overlap one another nowhere.
  *   tokens         [rows, width] int32 or int64; one outside [0, vocabulary) is
  *                  passed over, as is such a bias_ids entry ([rows, biases] int32,
  *                  with biases [rows, biases] float, in rows of the same stride).

@@ -133,3 +133,35 @@ def test_adjust_arguments(lib):
     assert call(tensors(out=FAKE), sizes(out=104)) == 2          # the input's place, another stride
     assert call(tensors(logits=FAKE + 1)) == 3 and call(tensors(out=FAKE + 1)) == 3
     assert call(tensors(logits=FAKE + 2), sizes(type=2)) == 3
+
+
+# Strides of 5 tokens of 8 heads of 64 (tokens, heads) in which heads share values, and ones in
+# which none do.
+SHARED = [(0, 64), (512, 0), (0, 0), (512, 56), (504, 64), (448, 64), (64, 312), (56, 320), (64, 0)]
+APART = [(512, 64), (520, 64), (1024, 128), (64, 320), (72, 352)]
+
+
+def test_outputs_that_share_values_are_refused(lib):
+    for row, head in SHARED:
+        h = heads(o_row=row, o_head=head)
+        assert lib.w4a16_rotate(*(FAKE,) * 3, FAKE + 16, rotary(), h, None) == 2
+        assert lib.w4a16_paged_append_rotary(*(FAKE,) * 7, FAKE, FAKE, FAKE + 16, cache(), rotary(),
+                                             h, 128, 64, 128, 64, None) == 2
+        assert lib.w4a16_paged_chunk_attention(*[FAKE] * 7, None, FAKE, cache(),
+                                               query(o_row=row, o_head=head), 5, None) == 2
+    for out in (0, 1, 99):
+        assert lib.w4a16_adjust_logits(tensors(), sizes(out=out), None) == 2
+
+
+def test_outputs_that_share_no_value_are_taken(lib):
+    # (told by the check behind the strides', of the alignment)
+    for row, head in APART + [(0, 64)]:
+        tokens = 5 if row else 1
+        h = heads(tokens=tokens, o_row=row, o_head=head)
+        assert lib.w4a16_rotate(*(FAKE,) * 3, MISALIGNED, rotary(), h, None) == 3
+        assert lib.w4a16_paged_append_rotary(*(FAKE,) * 7, FAKE, FAKE, MISALIGNED, cache(), rotary(),
+                                             h, 128, 64, 128, 64, None) == 3
+        assert lib.w4a16_paged_chunk_attention(*[FAKE] * 6, MISALIGNED, None, FAKE, cache(),
+                                               query(o_row=row, o_head=head), tokens, None) == 3
+    assert lib.w4a16_adjust_logits(tensors(out=FAKE + 1), sizes(out=100), None) == 3
+    assert lib.w4a16_adjust_logits(tensors(out=FAKE + 1), sizes(rows=1, out=0), None) == 3

@@ -80,11 +80,21 @@ bool good_steps(const w4a16_cache_shape& c, int64_t q_heads) {
     return c.batch * c.table_width * c.page_size <= ((int64_t)1 << 43) / q_heads;
 }
 
+// Strides of heads [tokens, heads, dim] that are written: as good_stride's, and no two heads share
+// a value, in either order of the two dimensions.
+bool good_out(int64_t tokens, int64_t token, int64_t heads, int64_t head, int64_t dim) {
+    if (!good_stride(tokens, token) || !good_stride(heads, head)) return false;
+    if (tokens <= 1) return heads <= 1 || head >= dim;
+    if (heads <= 1) return token >= dim;
+    return (head >= dim && token >= head * (heads - 1) + dim) ||
+           (token >= dim && head >= token * (tokens - 1) + dim);
+}
+
 bool good_heads(const w4a16_heads_shape& h) {
     return h.heads >= 1 && h.heads <= 1024 && h.head_dim >= 8 && h.head_dim <= 256 &&
            h.head_dim % 8 == 0 && good_stride(h.tokens, h.token_stride) &&
-           good_stride(h.heads, h.head_stride) && good_stride(h.tokens, h.out_token_stride) &&
-           good_stride(h.heads, h.out_head_stride);
+           good_stride(h.heads, h.head_stride) &&
+           good_out(h.tokens, h.out_token_stride, h.heads, h.out_head_stride, h.head_dim);
 }
 
 bool good_rotary(const w4a16_rotary_shape& r, int64_t head_dim) {
@@ -514,8 +524,7 @@ int w4a16_paged_chunk_attention(const void* q, const void* k_pool, const void* v
         return W4A16_ERR_NULL;
     if (!good_stride(tokens, query->q_row_stride) ||
         !good_stride(query->q_heads, query->q_head_stride) ||
-        !good_stride(tokens, query->out_row_stride) ||
-        !good_stride(query->q_heads, query->out_head_stride))
+        !good_out(tokens, query->out_row_stride, query->q_heads, query->out_head_stride, cache->head_dim))
         return W4A16_ERR_SHAPE;
     if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out) ||
         !aligned16(workspace))
@@ -665,6 +674,7 @@ int w4a16_adjust_logits(const w4a16_adjust_tensors* tensors, const w4a16_adjust_
         !stride(s.logits_stride) || !stride(s.out_stride) || !stride(s.token_stride) ||
         !stride(s.bias_stride) || !stride(s.mask_stride) || (s.wide != 0 && s.wide != 1) ||
         s.width < 0 || s.width >= (int64_t)1 << 30 || s.biases < 0 || s.biases > W4A16_MAX_BIASES ||
+        (s.rows > 1 && s.out_stride < s.vocabulary) ||  // rows that share values
         (tensors->logits == tensors->out && s.rows > 1 && s.logits_stride != s.out_stride))
         return W4A16_ERR_SHAPE;
     const uintptr_t size = s.type == W4A16_F32 ? 4 : 2;
