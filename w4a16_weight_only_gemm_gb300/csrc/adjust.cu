@@ -14,6 +14,15 @@
 // Counts are integers and a token's logit is its own, so the order of the atomics
 // changes nothing.  A piece of 16 bytes that the mask has none of is not read, and in
 // place only what changes is touched.
+//
+// Measured: 512 rows of 128256 bf16 logits under masks, histories of up to 8191 (4103 on
+// average), 80 us: 43 for the copy, the rest for the histories (41 would be all bytes once at
+// 6790 GB/s); instructions bound it, issue slots are 79 % full.  64 rows of fp32, histories of
+// up to 4093, 18 us (9.8).  One row 4.0 us, which is latency.  The same with
+//   slices of 16384, 512 threads       79, 21.4, 3.9 us: half as many reads of the histories, but
+//                                      too few blocks for 64 rows
+//   what is found by a bit a token, and from a list of the block's  90, 18, 4.0
+//   logits staged in shared memory while the history is read        90, 23, 4.2
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -30,8 +39,13 @@ constexpr int kThreads = 256;
 constexpr int kBlocksPerSm = 8;
 constexpr int kAhead = 1;            // pieces of a thread on their way
 constexpr int kWordBytes = 16384;    // of a slice's words at most
-constexpr int kListed = 4096;        // places of the list; words swept at a time
-constexpr int kOwn = kListed / kThreads;  // of them a thread's, for what it finds itself
+constexpr int kTogether = 3;         // said tokens of a thread on their way
+// Places of the list for what a thread finds itself: with 6, one block in several ran out (99 us for
+// 512 rows with 4, 89 with 6, 83 with 10); with 16 the list takes from L1 what it gives (90).
+constexpr int kOwn = 10;
+constexpr int kListed = kOwn * kThreads;
+constexpr int kEach = 4, kSwept = kEach * kThreads;  // words of a thread and of a block, swept at a time
+static_assert(kSwept <= kListed && 1024 % kSwept == 0, "a list of them, and slices are multiples of 1024");
 constexpr int kMostBiases = W4A16_MAX_BIASES;
 
 // A token's word: whether a bias is listed for it, whether the prompt has it, and in the other bits
@@ -49,6 +63,7 @@ struct AdjustArgs {
     w4a16_adjust_shape s;
     int slice, slices;
     bool in_place;
+    float repetition, presence, frequency;  // (converted by the host: FP64 units are few)
 };
 
 __device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
@@ -76,6 +91,24 @@ struct alignas(sizeof(T) * V) Piece {
     T x[V];
 };
 
+// The values whose bit is 0 become -infinity; two of 16 bits at a time.
+template <typename T, int V>
+__device__ __forceinline__ void blank(Piece<T, V>& v, uint32_t bits) {
+    if constexpr (sizeof(T) == 2 && V >= 2) {
+        constexpr uint32_t kMasked = std::is_same<T, __half>::value ? 0xFC00FC00u : 0xFF80FF80u;
+        uint32_t* two = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+        for (int k = 0; k < V / 2; ++k, bits >>= 2) {
+            const uint32_t keep = ((bits | bits << 15) & 0x00010001u) * 0xFFFFu;
+            two[k] = (two[k] & keep) | (kMasked & ~keep);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+            if (!(bits >> k & 1)) v.x[k] = from_float<T>(-INFINITY);
+    }
+}
+
 // Whether the row's mask allows token j (all of them without a mask).
 __device__ __forceinline__ bool allowed(const uint32_t* mask, int64_t j) {
     return !mask || (mask[j >> 5] >> (j & 31) & 1);
@@ -84,12 +117,13 @@ __device__ __forceinline__ bool allowed(const uint32_t* mask, int64_t j) {
 // V: logits of a piece, 16 bytes where the rows of logits and out lie alike to that boundary, else 1.
 template <typename T, int V, typename W>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) adjust_kernel(AdjustArgs a) {
-    extern __shared__ __align__(16) uint32_t space[];  // words of the slice's tokens, then the list
+    // words of the slice's tokens, the list, the biases' tokens
+    extern __shared__ __align__(16) uint32_t space[];
     W* words = reinterpret_cast<W*>(space);
-    __shared__ int32_t bias_ids[kMostBiases];
     __shared__ int listed;  // tokens on the list
     __shared__ int twice;   // whether some token has two biases
     uint16_t* list = reinterpret_cast<uint16_t*>(words + a.slice);
+    int32_t* bias_ids = reinterpret_cast<int32_t*>(list + kListed);
     const int64_t row = blockIdx.x / a.slices;
     const int vocabulary = (int)a.s.vocabulary;
     grid_dependency_wait();
@@ -121,25 +155,27 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) adjust_kernel(AdjustAr
     // branches, or with the old word returned to see who is first, this took longer than all the rest.
     // A number before the row's first token counts in a word that stands for none.)
     const uint32_t word0 = smem_u32(words), own0 = smem_u32(list) + 2 * threadIdx.x;
-    const uint32_t size = (uint32_t)(to - begin);
-    int found = 0;
+    const uint32_t own_end = own0 + kOwn * (2 * kThreads), size = (uint32_t)(to - begin);
+    uint32_t next = own0;  // where the thread's next find goes
     const auto note = [&](auto said, int32_t token) {
         constexpr bool kSaid = decltype(said)::value;  // by the prompt
         const uint32_t at = (uint32_t)token - (uint32_t)begin;
         const uint32_t address = sizeof(W) == 2 ? word0 + (2 * at & ~3u) : word0 + 4 * at;
         const uint32_t unit = kSaid ? Word<W>::kPrompt : 1u;
         const uint32_t value = sizeof(W) == 2 && (at & 1) ? unit << 16 : unit;
-        const bool in = at < size;
-        if constexpr (kSaid)
-            asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p red.shared.or.b32 [%0], %1;\n\t}"
-                         ::"r"(address), "r"(value), "r"((uint32_t)in) : "memory");
-        else
-            asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p red.shared.add.u32 [%0], %1;\n\t}"
-                         ::"r"(address), "r"(value), "r"((uint32_t)in) : "memory");
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p st.shared.u16 [%0], %1;\n\t}"
-                     ::"r"(own0 + found * (2 * kThreads)), "h"((uint16_t)at), "r"((uint32_t)(in && found < kOwn))
-                     : "memory");
-        found += in;
+#define NOTE(OPERATION)                                          \
+    asm volatile(                                                \
+        "{\n\t.reg .pred p, q;\n\t"                              \
+        "setp.lt.u32 p, %1, %2;\n\t"                             \
+        "@p red.shared." OPERATION " [%3], %4;\n\t"              \
+        "setp.lt.and.u32 q, %0, %5, p;\n\t"                      \
+        "@q st.shared.u16 [%0], %1;\n\t"                         \
+        "@p add.u32 %0, %0, %6;\n\t}"                            \
+        : "+r"(next)                                             \
+        : "r"(at), "r"(size), "r"(address), "r"(value), "r"(own_end), "n"(2 * kThreads) \
+        : "memory")
+        if constexpr (kSaid) NOTE("or.b32"); else NOTE("add.u32");
+#undef NOTE
     };
     // tokens first .. last - 1 of the row
     const auto read = [&](auto said, int first, int last) {
@@ -213,9 +249,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) adjust_kernel(AdjustAr
             const int i = first + (n * kThreads + threadIdx.x) * V, j = begin + i;
             if (bits[n] <= kAll) {
                 if (bits[n] != kAll) {
-#pragma unroll
-                    for (int k = 0; k < V; ++k)
-                        if (!(bits[n] >> k & 1)) v[n].x[k] = masked;
+                    blank<T, V>(v[n], bits[n]);
                 } else if (a.in_place) {
                     continue;
                 }
@@ -227,10 +261,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) adjust_kernel(AdjustAr
             }
         }
     }
-    const Penalties<W> p = {a.t.repetition ? a.t.repetition[row] : (float)a.s.repetition,
-                            a.t.presence ? a.t.presence[row] : (float)a.s.presence,
-                            a.t.frequency ? a.t.frequency[row] : (float)a.s.frequency};
-    const bool own = !__syncthreads_or(found > kOwn) && !a.in_place;
+    const Penalties<W> p = {a.t.repetition ? a.t.repetition[row] : a.repetition,
+                            a.t.presence ? a.t.presence[row] : a.presence,
+                            a.t.frequency ? a.t.frequency[row] : a.frequency};
+    const int found = (int)((next - own0) / (2 * kThreads));
+    const bool own = !__syncthreads_or(found > kOwn);
 
     // Biased tokens.  One with several biases is its first listing's, with the biases added in the
     // order of the list.
@@ -249,47 +284,53 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) adjust_kernel(AdjustAr
         if (!later) out[id] = from_float<T>(y);
     }
     // Said tokens: each thread's own, where all had places for what they found.  One that several
-    // threads found is written by each of them, alike.
+    // threads found is written by each of them, alike; in place it is the first's to mark its word.
     if (own) {
-        for (int n = 0; n < found; ++n) {
-            const int at = list[n * kThreads + threadIdx.x], id = begin + at;
-            const uint32_t word = words[at];
-            if (id >= 0 && word < Word<W>::kBiased && allowed(mask, id))
-                out[id] = from_float<T>(p.apply(to_float(x[id]), word));
+#pragma unroll 1
+        for (int first = 0; first < found; first += kTogether) {
+            int at[kTogether];
+            T was[kTogether];
+            uint32_t bits[kTogether];
+#pragma unroll
+            for (int n = 0; n < kTogether; ++n) {
+                at[n] = -1;
+                if (first + n >= found) continue;
+                const int there = list[(first + n) * kThreads + threadIdx.x], id = begin + there;
+                const uint32_t mark = Word<W>::kBiased << (sizeof(W) == 2 ? 16 * (there & 1) : 0);
+                if (id < 0 || words[there] >= Word<W>::kBiased ||
+                    (a.in_place && atomicOr(space + there * sizeof(W) / 4, mark) & mark)) continue;
+                at[n] = there;
+                was[n] = x[id];
+                bits[n] = mask ? mask[id >> 5] : ~0u;
+            }
+#pragma unroll
+            for (int n = 0; n < kTogether; ++n) {
+                const int id = begin + at[n];
+                if (at[n] >= 0 && bits[n] >> (id & 31) & 1)
+                    out[id] = from_float<T>(p.apply(to_float(was[n]), words[at[n]]));
+            }
         }
         return;
     }
-    // Else (and in place, where a logit is to be read once) those of kListed words at a time are listed,
-    // a bit a word, and then taken one by one, so that all threads have their share.
-    if (!length) return;
-    __syncthreads();
-    constexpr int kEach = 16 / sizeof(W);  // words of a 16-byte read
-    for (int first = 0; first < a.slice; first += kListed) {
-        uint32_t set = 0;
-#pragma unroll
-        for (int n = 0; n < kListed / (kThreads * kEach); ++n) {
-            const int i = first + (n * kThreads + threadIdx.x) * kEach;
-            if (i >= a.slice) continue;
-            const uint4 read = *reinterpret_cast<const uint4*>(words + i);
-            const W* w = reinterpret_cast<const W*>(&read);
-#pragma unroll
-            for (int k = 0; k < kEach; ++k)
-                set |= (uint32_t)(w[k] != 0 && w[k] < Word<W>::kBiased) << (n * kEach + k);
-        }
-        int at = set ? atomicAdd(&listed, __popc(set)) : 0;
-        for (; set; set &= set - 1) {
-            const int bit = __ffs(set) - 1;
-            list[at++] = (uint16_t)(first + (bit / kEach * kThreads + threadIdx.x) * kEach + bit % kEach);
-        }
-        __syncthreads();
-        for (int i = threadIdx.x; i < listed; i += kThreads) {
-            const int id = begin + list[i];
-            if (id >= 0 && allowed(mask, id)) out[id] = from_float<T>(p.apply(to_float(x[id]), words[list[i]]));
-        }
-        if (first + kListed >= a.slice) break;
+    // Else those of kSwept words at a time are listed, and then taken one by one, so that all threads
+    // have their share.
+#pragma unroll 1
+    for (int first = 0; first < a.slice; first += kSwept) {
         __syncthreads();
         if (threadIdx.x == 0) listed = 0;
         __syncthreads();
+        const int i = first + threadIdx.x * kEach;
+        uint32_t set = 0;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k)
+            if (words[i + k] != 0 && words[i + k] < Word<W>::kBiased) set |= 1u << k;
+        int at = set ? atomicAdd(&listed, __popc(set)) : 0;
+        for (; set; set &= set - 1) list[at++] = (uint16_t)(i + __ffs(set) - 1);
+        __syncthreads();
+        for (int n = threadIdx.x; n < listed; n += kThreads) {
+            const int id = begin + list[n];
+            if (id >= 0 && allowed(mask, id)) out[id] = from_float<T>(p.apply(to_float(x[id]), words[list[n]]));
+        }
     }
 }
 
@@ -303,7 +344,7 @@ cudaError_t launch(AdjustArgs a, cudaStream_t stream, const DeviceCtx& ctx) {
     std::call_once(once[device], [&]() {
         set[device] =
             cudaFuncSetAttribute(adjust_kernel<T, V, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kWordBytes + 2 * kListed);
+                                 kWordBytes + 2 * kListed + 4 * kMostBiases);
     });
     if (set[device] != cudaSuccess) return set[device];
     // as large a slice as there are words for, less where that leaves fewer than four blocks an SM
@@ -319,7 +360,7 @@ cudaError_t launch(AdjustArgs a, cudaStream_t stream, const DeviceCtx& ctx) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.s.rows * a.slices));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = slice * sizeof(W) + 2 * kListed;
+    cfg.dynamicSmemBytes = slice * sizeof(W) + 2 * kListed + (a.t.bias_ids ? 4 * a.s.biases : 0);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -351,6 +392,9 @@ cudaError_t launch_adjust_logits(const w4a16_adjust_tensors& tensors,
     a.t = tensors;
     a.s = shape;
     a.in_place = tensors.logits == tensors.out;
+    a.repetition = (float)shape.repetition;
+    a.presence = (float)shape.presence;
+    a.frequency = (float)shape.frequency;
     if (shape.rows == 1) a.s.logits_stride = a.s.out_stride = 0;
     if (shape.type == W4A16_BF16) return launch<__nv_bfloat16>(a, stream, ctx);
     return shape.type == W4A16_F16 ? launch<__half>(a, stream, ctx) : launch<float>(a, stream, ctx);
