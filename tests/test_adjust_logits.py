@@ -194,6 +194,16 @@ def test_a_token_said_very_often(w4lib):
 
 
 @gpu
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("width", [60, 900, 9000, 20000])
+def test_in_place_with_tokens_said_again(w4lib, width, wide):
+    """Few and many finds of a thread, words of 16 and of 32 bits."""
+    x, s = make(3, 9001, width, torch.float32, 20, True, seed=width, wide=wide)
+    want = check(x, s)
+    assert torch.equal(w4.adjust_logits(x, **s, out=x), want)
+
+
+@gpu
 def test_streams_graphs_and_repeats(w4lib):
     x, s = make(8, 20011, 500, torch.bfloat16, 30, True, seed=8)
     want = w4.adjust_logits(x, **s)
