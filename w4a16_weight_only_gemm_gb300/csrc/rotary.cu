@@ -15,6 +15,13 @@
 // where a head has a multiple of 8 pairs.  So a thread has its pairs' cosines and
 // sines in registers and steps from head to head by an addition.  Values of
 // dimensions that are not rotated, and V's heads, are copied.
+//
+// Measured: 16381 tokens of 40 heads of 128, 64 dimensions of each, bf16, 54 us,
+// 6.2 TB/s (0.91 of a plain copy); 32749 tokens of 8 + 8 heads into the pages and
+// of 32 heads of queries, 123 us, 6.6 TB/s (0.97).  One token 2.4 us, 16 tokens
+// into the pages 3.9: launches and dependent reads.  Threads without pairs of
+// their own, which read the table for each head, took 82 and 209 us; six blocks an
+// SM and more heads in flight were slower.
 #include <cuda_bf16.h>
 
 #include <algorithm>
