@@ -63,7 +63,8 @@ class Rotary:
 
     `rates` holds the numbers used, `turns` (int64 [dim / 2], on the device) each
     as a fraction of a turn times 2^64, so that a position's angle is reduced by
-    an integer product alone."""
+    an integer product alone.  What describes a rotation is read-only; it may be
+    copied and pickled like any object that holds a tensor."""
 
     def __init__(self, dim: int, base: float = 10000.0, interleaved: bool = False,
                  scaling: str | None = None, factor: float = 1.0, original: int | None = None,
@@ -80,11 +81,25 @@ class Rotary:
             raise ValueError(f"rates must be {dim // 2} finite numbers")
         if not math.isfinite(magnitude):
             raise ValueError(f"magnitude must be finite, got {magnitude}")
-        self.dim, self.interleaved, self.magnitude = dim, bool(interleaved), float(magnitude)
-        self.rates = rates
+        self._dim, self._interleaved, self._magnitude = dim, bool(interleaved), float(magnitude)
+        self._rates = tuple(rates)
         turns = [_turn(r) for r in rates]
-        self.turns = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns],
-                                  dtype=torch.int64, device=device)
-        self._shape = _SHAPE(dim, self.interleaved, self.magnitude)
-        # (read at every call)
-        self._device, self._pointer = self.turns.get_device(), self.turns.data_ptr()
+        self._turns = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns],
+                                   dtype=torch.int64, device=device)
+        self._shape = _SHAPE(dim, self._interleaved, self._magnitude)
+
+    dim = property(lambda self: self._dim)
+    interleaved = property(lambda self: self._interleaved)
+    magnitude = property(lambda self: self._magnitude)
+    rates = property(lambda self: list(self._rates))
+    turns = property(lambda self: self._turns)
+
+    def _held(self) -> tuple[int, int]:
+        """The device and the address of `turns` as they are now: a copy of this object has
+        memory of its own, and torch may give a tensor another."""
+        turns = self._turns
+        if turns.dtype is not torch.int64 or turns.shape != (self._dim // 2,) or (
+                not turns.is_contiguous()):
+            raise ValueError(f"the rotation's turns must be a dense int64 tensor "
+                             f"[{self._dim // 2}], got {turns.dtype} {list(turns.shape)}")
+        return turns.get_device(), turns.data_ptr()

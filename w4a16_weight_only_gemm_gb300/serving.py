@@ -213,7 +213,8 @@ def rotate(x: torch.Tensor, positions: torch.Tensor, rotary: Rotary,
     tokens, heads, dim = shape
     _row(positions, tokens, "positions")
     dev = x.get_device()
-    if (dev < 0 or positions.get_device() != dev or rotary._device != dev
+    on, turns = rotary._held()
+    if (dev < 0 or positions.get_device() != dev or on != dev
             or out is not None and out.get_device() != dev
             or stream is not None and stream.device.index != dev):
         _device(stream, x=x, positions=positions, rotary=rotary.turns, out=out)
@@ -224,7 +225,7 @@ def rotate(x: torch.Tensor, positions: torch.Tensor, rotary: Rotary,
         to_row, to_head, _ = _heads(out, "out", dtype, shape)
     if tokens and heads:
         _run(dev, stream, "w4a16_rotate", x.data_ptr(), positions.data_ptr(),
-             rotary._pointer, out.data_ptr(), rotary._shape,
+             turns, out.data_ptr(), rotary._shape,
              _HEADS_SHAPE(tokens, heads, dim, _TYPES[dtype], row, head, to_row, to_head))
     return out
 
@@ -247,9 +248,10 @@ def paged_append_rotary(k: torch.Tensor, v: torch.Tensor, k_pool: torch.Tensor,
     ks, vs = _heads(k, "k", dtype, heads), _heads(v, "v", dtype, heads)
     _row(starts, rows, "starts")
     dev = k.get_device()
+    on, turns = rotary._held()
     same = (dev >= 0 and v.get_device() == dev and k_pool.get_device() == dev
             and v_pool.get_device() == dev and tables.get_device() == dev
-            and starts.get_device() == dev and rotary._device == dev
+            and starts.get_device() == dev and on == dev
             and (stream is None or stream.device.index == dev))
     at = None
     if offsets is not None:
@@ -280,7 +282,7 @@ def paged_append_rotary(k: torch.Tensor, v: torch.Tensor, k_pool: torch.Tensor,
         if q_heads:
             q_at, out_at = q.data_ptr(), out.data_ptr()
     if rows and tokens:
-        _run(dev, stream, "w4a16_paged_append_rotary", k.data_ptr(), v.data_ptr(), rotary._pointer,
+        _run(dev, stream, "w4a16_paged_append_rotary", k.data_ptr(), v.data_ptr(), turns,
              k_pool.data_ptr(), v_pool.data_ptr(), tables.data_ptr(), starts.data_ptr(), at, q_at,
              out_at, cache, rotary._shape, queries, ks[0], ks[1], vs[0], vs[1])
     elif q is not None and tokens:
