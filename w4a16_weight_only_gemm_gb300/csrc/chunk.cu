@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a, Divisor
     static_assert(kPlanThreads == 1024, "32 warps: one for each length tried");
     __shared__ int64_t sums[32];
     __shared__ int longests[32], ints[32];
+    __shared__ int shortests[32];  // (of their own: nothing waits for all to have read them)
     __shared__ int32_t staged[kStaged + 1], staged_steps[kStaged];
     __shared__ float costs[32];
     __shared__ int units[32], keeps[32];
@@ -229,10 +230,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a, Divisor
         if (level) break;
         if (lane == 0) {
             sums[warp] = total, ints[warp] = items;
-            longests[warp] = longest, units[warp] = shortest;
+            longests[warp] = longest, shortests[warp] = shortest;
         }
         __syncthreads();
-        total = sums[lane], items = ints[lane], longest = longests[lane], shortest = units[lane];
+        total = sums[lane], items = ints[lane], longest = longests[lane];
+        shortest = shortests[lane];
     }
     total *= heads;
     // Slots are gone through from the last to the first.  Cut are those from the `keep`-th on, and
