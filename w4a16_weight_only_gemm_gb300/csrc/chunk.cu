@@ -1066,28 +1066,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
         const uint32_t t_scores = tmem + lanes + q * 128;
         const uint32_t t_out = tmem + lanes + S::kOutColumn + q * DP;
-        // What no unit writes: tokens of no row, or of positions below 0.
-        // (a row's are a block's; those before the first row and behind the last are dealt out)
+        // What no unit writes, dealt out over all blocks; of a row, a slot's tokens at a time.  (Rows
+        // left to a block each, a thread a head, took 3.0 ms for 8192 tokens without a position beside
+        // 64 after 636, and the block's other warps waited through all of it; this takes 61 us, of
+        // which the 64 MB of zeros are 16.)
+        const int pieces = a.c.head_dim / 8;
+        const auto zero = [&](int64_t t, int h, int piece) {
+            *reinterpret_cast<uint4*>(a.out + t * a.out_row + h * a.out_head + 8 * piece) =
+                make_uint4(0, 0, 0, 0);
+            if (a.lse && piece == 0) a.lse[t * a.q_heads + h] = -INFINITY;
+        };
+        // queries of positions below 0
 #pragma unroll 1
-        for (int64_t b = blockIdx.x;; b += gridDim.x) {
-            const bool row = b < a.c.batch;
-            const int64_t from = a.offset(row ? (int)b : 0), to = a.offset(row ? (int)b + 1 : a.c.batch);
-            // of a row: the tokens below position 0; else all but those from `from` up to `to`
-            const int64_t count = row ? min(max(to - from - a.length((int)b), (int64_t)0), to - from)
-                                      : a.tokens - max(to - from, (int64_t)0);
+        for (int64_t s0 = blockIdx.x; s0 < a.slot_count; s0 += 32 * (int64_t)gridDim.x) {
+            const int64_t s = s0 + (int64_t)lane * gridDim.x;
+            bool some = false;
+            if (s < a.slot_count) {
+                const Item& item = a.slots[s].item;
+                some = item.lins > 0 && item.position0 + a.group.quotient(item.lin0) < 0;
+            }
+            uint32_t all = __ballot_sync(~0u, some);
 #pragma unroll 1
-            for (int64_t i = row ? 0 : blockIdx.x; i < count; i += row ? 1 : gridDim.x) {
-                const int64_t t = row ? from + i : i < from ? i : i + to - from;
+            for (; all; all &= all - 1) {
+                const Item item = a.slots[s0 + (int64_t)(__ffs(all) - 1) * gridDim.x].item;
+                const int below = (int)min((int64_t)item.lins, -(int64_t)item.position0 * group - item.lin0);
 #pragma unroll 1
-                for (int x = threadIdx.x; x < a.q_heads; x += 128 * S::kTiles) {
-                    uint16_t* o = a.out + t * a.out_row + x * a.out_head;
-#pragma unroll 1
-                    for (int y = 0; y < a.c.head_dim; y += 8)
-                        *reinterpret_cast<uint4*>(o + y) = make_uint4(0, 0, 0, 0);
-                    if (a.lse) a.lse[t * a.q_heads + x] = -INFINITY;
+                for (int i = threadIdx.x; i < below * a.c.kv_heads * pieces; i += 128 * S::kTiles) {
+                    const int query = i / pieces, lin = item.lin0 + query / a.c.kv_heads;
+                    const int token = a.group.quotient(lin);
+                    zero((int64_t)item.token0 + token, query % a.c.kv_heads * group + lin - token * group,
+                         i % pieces);
                 }
             }
-            if (!row) break;
+        }
+        // tokens before the first row and behind the last
+        {
+            const int64_t from = a.offset(0), to = a.offset(a.c.batch);
+            const int64_t held = max(to - from, (int64_t)0);
+#pragma unroll 1
+            for (int64_t i = blockIdx.x; i < a.tokens - held; i += gridDim.x)
+#pragma unroll 1
+                for (int x = threadIdx.x; x < a.q_heads * pieces; x += 128 * S::kTiles)
+                    zero(i < from ? i : i + to - from, x / pieces, x % pieces);
         }
         // steps and units of this group, joined units, steps of the block
         uint32_t taken = 0, units = 0, joins = 0, step0 = 0;
