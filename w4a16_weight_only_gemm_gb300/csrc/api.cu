@@ -86,8 +86,12 @@ bool good_out(int64_t tokens, int64_t token, int64_t heads, int64_t head, int64_
     if (!good_stride(tokens, token) || !good_stride(heads, head)) return false;
     if (tokens <= 1) return heads <= 1 || head >= dim;
     if (heads <= 1) return token >= dim;
-    return (head >= dim && token >= head * (heads - 1) + dim) ||
-           (token >= dim && head >= token * (tokens - 1) + dim);
+    // a stride that is as long as n others of `inner` and a head's values (divided, as a product of
+    // 2^31 tokens' strides may pass 64 bits)
+    const auto spans = [&](int64_t outer, int64_t inner, int64_t n) {
+        return inner >= dim && outer >= dim && (outer - dim) / inner >= n;
+    };
+    return spans(token, head, heads - 1) || spans(head, token, tokens - 1);
 }
 
 bool good_heads(const w4a16_heads_shape& h) {
