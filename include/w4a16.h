@@ -491,8 +491,9 @@ typedef struct w4a16_heads_shape {
  * w4a16_rotate -- rotary positions: out[t] is x[t] rotated to positions[t].
  *   x, out     heads of `type` (W4A16_F16, _BF16, _F32), 16-byte aligned; out
  *              is x (with the same strides) or overlaps none of it.
- *   positions  [tokens] int32, of either sign: a rotation to -p undoes one to
- *              p, and is its gradient.
+ *   positions  [tokens] int32, of either sign: a rotation to -p is the gradient of
+ *              one to p, and after it gives the values times the magnitude's
+ *              square (so it undoes a rotation of magnitude 1).
  * Errors: NULL -> W4A16_ERR_NULL; sizes outside the ranges above, a magnitude
  * that is not finite -> W4A16_ERR_SHAPE; x or out not 16-byte aligned ->
  * W4A16_ERR_ALIGN.
@@ -536,8 +537,9 @@ int w4a16_paged_append_rotary(const void *k, const void *v, const uint64_t *turn
  *   offsets    [batch + 1] int32, not descending, within 0 .. tokens.  A row
  *              may have no tokens.
  *   out        [tokens, q_heads, head_dim], written; no two heads share a value
- *              (W4A16_ERR_SHAPE).  A token with a position below 0 (a row with
- *              more tokens than positions) and one that no row claims get zeros.
+ *              (W4A16_ERR_SHAPE) and out overlaps no input.  A token with a position
+ *              below 0 (a row with more tokens than positions) and one that no row
+ *              claims get zeros.
  *   lse        NULL, or [tokens, q_heads] float, written: the natural logarithm
  *              of sum_p exp(scale * q . K), -infinity for tokens as above.
  *   workspace  w4a16_paged_chunk_workspace(cache, q_heads, tokens) bytes,
@@ -552,6 +554,10 @@ int w4a16_paged_append_rotary(const void *k, const void *v, const uint64_t *turn
  * NaN) for the tokens that see it, and for no other; at a position left out for
  * its score alone it may do so or not.  Two calls on the same
  * inputs and sizes give the same bits.
+ * A weight keeps 11 bits in fp16 and 8 in bf16, and what divides is the sum of
+ * the weights before that rounding: out is off by up to 2^-11 (2^-8) of the
+ * weighted average of |V|, its own rounding aside.  w4a16_paged_attention keeps
+ * 22 (16) bits for single tokens.
  * Errors: as w4a16_paged_attention.
  */
 int w4a16_paged_chunk_attention(const void *q, const void *k_pool, const void *v_pool,

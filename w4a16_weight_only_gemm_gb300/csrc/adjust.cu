@@ -17,12 +17,15 @@
 //
 // Measured: 512 rows of 128256 bf16 logits under masks, histories of up to 8191 (4103 on
 // average), 80 us: 43 for the copy, the rest for the histories (41 would be all bytes once at
-// 6790 GB/s); instructions bound it, issue slots are 79 % full.  64 rows of fp32, histories of
+// 6790 GB/s); instructions bound it, issue slots are 77 % full.  64 rows of fp32, histories of
 // up to 4093, 18 us (9.8).  One row 4.0 us, which is latency.  The same with
 //   slices of 16384, 512 threads       79, 21.4, 3.9 us: half as many reads of the histories, but
 //                                      too few blocks for 64 rows
 //   what is found by a bit a token, and from a list of the block's  90, 18, 4.0
 //   logits staged in shared memory while the history is read        90, 23, 4.2
+// Other calls, the same inputs again each time: the 512 rows in place 75 us, with int64 tokens 98
+// (a load of 8 bytes each); 64 rows of bf16 with histories of up to 16383 tokens 23, 30000 33, 16
+// rows of 100000 41, one 24.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -41,7 +44,9 @@ constexpr int kAhead = 1;            // pieces of a thread on their way
 constexpr int kWordBytes = 16384;    // of a slice's words at most
 constexpr int kTogether = 3;         // said tokens of a thread on their way
 // Places of the list for what a thread finds itself: with 6, one block in several ran out (99 us for
-// 512 rows with 4, 89 with 6, 83 with 10); with 16 the list takes from L1 what it gives (90).
+// 512 rows with 4, 89 with 6, 83 with 10); with 16 the list takes from L1 what it gives (90, and 86
+// now that 10 take 78).  A block that runs out sweeps its words: where all of a row's history lies in one
+// slice, 512 rows take 72 us for 78, 64 rows of fp32 16.1 for 13.4 (the same inputs again each time).
 constexpr int kOwn = 10;
 constexpr int kListed = kOwn * kThreads;
 constexpr int kEach = 4, kSwept = kEach * kThreads;  // words of a thread and of a block, swept at a time

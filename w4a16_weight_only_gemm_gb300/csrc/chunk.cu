@@ -27,10 +27,17 @@
 // side: blocks at work at the same time read the same keys and values, through L2.
 //
 // Weights are rounded to 16 bits once, for the product with V (two 16-bit parts would make it
-// two products); the sums that divide it are of the weights before that.
+// two products): off by up to 2^-11 (fp16) or 2^-8 (bf16) of themselves.  The sums that divide it
+// are of the weights before that.  So an average of equal values is not always that value: weights
+// that are alike all round alike, as those of 1244 positions with scores of 4.94 behind 256 of 0, over
+// which equal bf16 values came out up to 0.6 % off, their own rounding in it (fp16 0.05 %).  Summing
+// the rounded weights too, to divide by, gave the value itself, and took 187 us for 162 (prompts),
+// 160 for 153.5 (a mixed step), 2.84 to 2.95 ms for 2.61 to 2.67 (2048 after 129023) and with heads of
+// 64 397 for 317 (2048 after 16384).  It is not done: the error is the bound that each weight's
+// rounding has by itself.
 //
 // Measured (8 key-value heads of 128, 4 query heads to each): one row of 2048 tokens after
-// 129023, bf16, 2.56 to 2.69 ms, 1620 to 1700 TFLOP/s where the power allows it; 23 prompts of up to
+// 129023, bf16, 2.56 to 2.87 ms, 1520 to 1700 TFLOP/s, as the power allows; 23 prompts of up to
 // 1531 tokens, fp16, 161 us, 970 TFLOP/s, the rest being the ends of units, 2 to 3 us
 // each, 15.7 of them a block; 5 tokens after 700, 15 us: the plan 6, the attention and the join.
 #include <cuda_bf16.h>
@@ -153,9 +160,10 @@ struct ChunkArgs {
 // many as make full rounds of the blocks; taken is what makes the estimated time least: a
 // unit costs its steps and three more (four where it is a part), and the blocks end within
 // half of one of the last units, those that the blocks take last being the shortest; or
-// they take rounds of units that are alike.  (48 rows, 8 of them with chunks of up to 509
-// tokens and positions from few to 8191: with items in the order of their rows the last
-// block ended 207 us after the start, the mean one after 138.)
+// they take rounds of units that are alike.  (Whole ones are counted in slots, from the last;
+// slots that no item took count among them, so that a last round may lack a few.  48 rows, 8
+// of them with chunks of up to 509 tokens and positions from few to 8191: with items in the
+// order of their rows the last block ended 207 us after the start, the mean one after 138.)
 // ---------------------------------------------------------------------------
 constexpr int kUnitCost = 3, kStaged = 2048, kLengths = 64;
 
@@ -244,7 +252,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a, Divisor
     const float by_length = (float)(kLengths - 1) / (float)max(longest, 1);
     const auto steps_of_slot = [&](int s) { return s < kStaged ? staged_steps[s] : a.slots[s].steps; };
     int unit = max(longest, 1), keep = slots;
-    // (an item that is a sixth of a block's share or less is not worth a cut, nor the search for one)
+    // (An item that is a sixth of a block's share or less is not worth a cut, nor the search for one.
+    // With an eighth, 128 rows of a token after 500 took 66.7 us for 62.5, after 4000 340.8 for 336.5;
+    // 30 ragged ones of up to 400 new tokens 211.7 for 216.5.)
     if ((float)longest * 6.f > share && a.most_parts > 0) {
         // The longest of the last units, where none is cut: as many of the shortest items as there
         // are blocks.
@@ -658,6 +668,7 @@ struct Rest {
     Odd<DP> odd[kUnits];
 };
 
+// (With DP = 256 a softmax thread spills 4 bytes, of 20 that it loads again.)
 template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,

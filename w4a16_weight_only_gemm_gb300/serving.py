@@ -203,8 +203,9 @@ def paged_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
 def rotate(x: torch.Tensor, positions: torch.Tensor, rotary: Rotary,
            out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Heads x [tokens, heads, head_dim] (fp16, bf16 or fp32, any strides) rotated to
-    their tokens' positions (int32 [tokens], of either sign); `out` may be x.
-    A rotation to -positions undoes it, and is its gradient."""
+    their tokens' positions (int32 [tokens], of either sign); `out` may be x, and else
+    overlaps none of it.  A rotation to -positions is the gradient; it undoes the rotation
+    but for the square of its magnitude."""
     shape, dtype = x.shape, x.dtype
     if len(shape) != 3 or dtype not in _TYPES or not 1 <= rotary.dim <= shape[2]:
         raise ValueError("x must be a float16, bfloat16 or float32 tensor [tokens, heads, "
@@ -237,8 +238,8 @@ def paged_append_rotary(k: torch.Tensor, v: torch.Tensor, k_pool: torch.Tensor,
                         stream=None):
     """paged_append with the keys rotated to their positions in the cache, and with
     queries of the same tokens, q [tokens, q_heads, head_dim], rotated to theirs: returns
-    those (a new tensor, or `out`, which may be q), or None without q.  The queries of a
-    token that no row claims become zeros."""
+    those (a new tensor, or `out`, which may be q and else overlaps no input), or None
+    without q.  The queries of a token that no row claims become zeros."""
     cache = _cache_shape(k_pool, v_pool, tables)
     rows, tokens, dtype = tables.shape[0], k.shape[0], k_pool.dtype
     _, _, kv_heads, dim = k_pool.shape
@@ -308,9 +309,11 @@ def paged_chunk_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.T
     offsets[b+1] - 1 (int32 [rows + 1]) of q [tokens, q_heads, head_dim] are the last of
     its lengths[b] positions (int32 [rows]), and each sees the positions up to its own.
     q_heads is a multiple of kv_heads; scale defaults to head_dim ** -0.5.  Returns
-    [tokens, q_heads, head_dim], zeros for tokens of no row or of a position below 0, and
-    with return_lse also the logarithm of each head's sum of exponentials, fp32
-    [tokens, q_heads] (-inf for such tokens)."""
+    [tokens, q_heads, head_dim] (or `out`, which overlaps no input), zeros for tokens of no
+    row or of a position below 0, and with return_lse also the logarithm of each head's sum
+    of exponentials, fp32 [tokens, q_heads] (-inf for such tokens).  Weights enter the
+    product with the values in the cache's type (paged_attention, for one new token a row,
+    keeps twice their bits)."""
     cache = _cache_shape(k_pool, v_pool, tables)
     shape, dtype = q.shape, k_pool.dtype
     rows, dim = tables.shape[0], k_pool.shape[3]
@@ -569,7 +572,8 @@ def adjust_logits(logits: torch.Tensor, tokens: torch.Tensor | None = None,
                   mask: torch.Tensor | None = None, out: torch.Tensor | None = None,
                   stream=None) -> torch.Tensor:
     """Penalties, biases and masks on logits [rows, vocabulary] (fp16, bf16 or fp32, dense in
-    the last dimension), in this order; returns a new tensor, or `out`, which may be logits.
+    the last dimension), in this order; returns a new tensor, or `out`, which may be logits and
+    else overlaps none of them.
 
     tokens (int32 or int64 [rows, width]) lists what each row has said: its first lengths[r]
     (int32 [rows]; all when None), of which the first prompts[r] (int32 [rows]; none when None)
